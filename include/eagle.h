@@ -22,6 +22,9 @@
  *   eagle_tree_attention                  stage 5 (one layer per call)
  *   eagle_verify                          stage 6
  *   eagle_kv_compact                      stage 6b
+ * The same cycle over a KV cache of 8-bit codes (eagle_kvq_*) and with 4-bit
+ * LM-head weights (eagle_lmhead_quant), and the log-probabilities of a cycle's
+ * tokens (eagle_token_logprobs), are further down.
  *
  * Conventions for every call:
  *   - Pointers named in the signatures are device pointers owned by the
@@ -341,6 +344,162 @@ int eagle_verify(const eagle_tree_cfg* cfg, void* ws, size_t ws_bytes, int mode,
  */
 int eagle_kv_compact(const eagle_kv_cfg* kv, void* kv_cache, const int32_t* prefix_len, const int32_t* accept_len,
                      const int32_t* accepted_slots, int slots_stride, int32_t* new_len, void* ws, void* stream);
+
+/* ------------------------------------------------------ 8-bit KV cache --- */
+/*
+ * A KV cache held in 8 bits: every element is an e4m3 code (one sign, four
+ * exponent and three fraction bits, largest value 448) and the elements of
+ * `block` consecutive positions of one (sequence, layer, K|V, head) share one
+ * fp32 scale; the value is code * scale. None of this is on the pages: the
+ * stages are those of the 16-bit cache (stage 5 reads it, stage 6b moves the
+ * accepted path), at half the bytes.
+ *
+ * Code (b, layer, kv, pos, h, e), kv = 0 for K and 1 for V, is the byte at
+ *   b*seq_stride + layer*layer_stride + kv*kv_stride + pos*pos_stride + h*head_dim + e
+ * and its scale the fp32 element at
+ *   b*scale_seq_stride + layer*scale_layer_stride + kv*scale_kv_stride
+ *     + (pos / block)*scale_block_stride + h.
+ * Code strides are multiples of 16 and pos_stride >= n_kv_heads * head_dim;
+ * scale_block_stride >= n_kv_heads. head_dim is 128, `block` 16, 32, 64 or
+ * 128; q, k, v and the attention output are bf16 (dtype EAGLE_BF16). Tree slot
+ * j of sequence b is stored at position prefix_len[b] + j, as in the 16-bit cache.
+ *
+ * eagle_kvq_store writes scales that are powers of two, which makes moving a
+ * code to a larger scale exact but for values that become subnormal; the
+ * readers take any positive finite scale.
+ */
+typedef struct {
+    int batch, n_q_heads, n_kv_heads, head_dim;
+    int layers;  /* layers moved by eagle_kvq_compact */
+    int max_len; /* positions available per (sequence, layer, K|V) region */
+    int block;   /* positions that share a scale */
+    int dtype;   /* eagle_dtype of q, k, v and the attention output */
+    int64_t seq_stride, layer_stride, kv_stride, pos_stride;                               /* codes, bytes */
+    int64_t scale_seq_stride, scale_layer_stride, scale_kv_stride, scale_block_stride;    /* scales, elements */
+} eagle_kvq_cfg;
+
+/*
+ * Write K and V rows of one layer into the cache: the tokens of a prompt, of a
+ * draft tree (its slots, before eagle_kvq_tree_attention) or of a decode step.
+ *   T          the most tokens of any sequence in this call (>= 1).
+ *   k, v       bf16 rows of n_kv_heads * head_dim elements; row r starts at
+ *              r * row_stride elements (row_stride >= n_kv_heads * head_dim, a
+ *              multiple of 8; bases 16-byte aligned).
+ *   row_start  [B] int32 in, or NULL: the row of the sequence's first token
+ *              (packed sequences); NULL = b * T.
+ *   start      [B] int32 in: the position of the sequence's first token.
+ *   count      [B] int32 in, or NULL (= T each): tokens of the sequence, 0..T.
+ * Token j of sequence b goes to position start[b] + j. For every block that
+ * gets a token: with amax the largest |x| of its new tokens and s0 the
+ * smallest power of two (at least 2^-126) with amax <= 448 s0, the scale
+ * becomes s = s0 when the block holds no earlier position of the sequence
+ * (start[b] at or before its first position), else s = max(old scale, s0).
+ * New codes are x / s, and codes of the block's earlier positions, when s has
+ * grown, code * (old scale / s), both rounded to the nearest e4m3 value (ties
+ * to even, saturating). Positions from start[b] + count[b] on keep their codes.
+ *   ws         any eagle workspace whose status word receives device faults,
+ *              or NULL: status 3 for a sequence with count outside 0..T, a
+ *              negative row_start or positions outside 0..max_len (it is left
+ *              untouched), status 1 for a NaN or infinity in k or v.
+ */
+int eagle_kvq_store(const eagle_kvq_cfg* kv, int layer, int T, const void* k, const void* v, int64_t row_stride,
+                    const int32_t* row_start, const int32_t* start, const int32_t* count, void* codes, float* scales,
+                    void* ws, void* stream);
+
+/* Scratch bytes for eagle_kvq_tree_attention with this geometry and T slots (0: invalid or unsupported). */
+size_t eagle_kvq_attention_workspace_bytes(const eagle_kvq_cfg* kv, int T);
+
+/*
+ * Stage 5 over the 8-bit cache: eagle_tree_attention's definition with K and V
+ * the values code * scale. Sums, row maxima and the softmax are fp32; K takes
+ * part exactly and q within 2^-18 of its row's largest element; the softmax
+ * weights are rounded to fp16 (relative 2^-11) for the product with V. Output
+ * bf16, rounded to nearest even.
+ *   q, out   [B, T, Hq, 128] bf16, contiguous, 16-byte aligned; T = 1..256.
+ *   mask     [B, T, W] as eagle_build_tree writes it, or NULL: slot i sees the
+ *            slots 0..i (a chain; with T = 1 the plain decode step).
+ *   n_tree   [B], or NULL: T slots each.
+ * Requires prefix_len[b] + T <= max_len, as eagle_tree_attention (status 3 and
+ * zero rows otherwise). A row that sees no key is zero. Any number of query
+ * heads per KV head.
+ */
+int eagle_kvq_tree_attention(const eagle_kvq_cfg* kv, int T, const void* q, const void* codes, const float* scales,
+                             int layer, const int32_t* prefix_len, const uint32_t* mask, const int32_t* n_tree,
+                             void* out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Stage 6b over the 8-bit cache: eagle_kv_compact's definition. For every
+ * layer in [0, kv->layers), K and V, head h and j = 1..a_b with
+ * s_j = accepted_slots[b, j] > j, position L_b + j takes the row of position
+ * L_b + s_j (all sources read first). The scale of a destination block becomes
+ * the largest of its own and those of the rows that move into it; where it
+ * grows, the codes of the block's positions up to L_b + a_b are moved to it,
+ * and a moved row's codes go from its source block's scale to it: code *
+ * (old / new), rounded to the nearest e4m3 value. new_len[b] = L_b + a_b + 1.
+ * Faults and `ws` as eagle_kv_compact.
+ */
+int eagle_kvq_compact(const eagle_kvq_cfg* kv, void* codes, float* scales, const int32_t* prefix_len,
+                      const int32_t* accept_len, const int32_t* accepted_slots, int slots_stride, int32_t* new_len,
+                      void* ws, void* stream);
+
+/* ------------------------------------------------------ 4-bit LM head --- */
+/*
+ * eagle_lmhead with 4-bit weights [notes EAGLE 方法: the draft model reuses the
+ * target model's LM head, which every draft step reads whole].
+ *   group    32, 64 or 128: entries of a weight row that share a scale.
+ *   hidden   [B*k, H] bf16 in, H a multiple of 128.
+ *   codes    [V, H/2] in: byte i of a row holds entry 2i in its low and entry
+ *            2i + 1 in its high four bits, code c = 0..15.
+ *   scales   [V, H/group] bf16 in: weight[v, h] = (c - 8) * scales[v, h / group].
+ *   draft_logits [B*k, V] out in cfg->logit_dtype: the sums of hidden * weight,
+ *            fp32 (products of a group on the tensor cores, exact operands;
+ *            groups scaled and added in fp32), rounded once.
+ * Reads the weight once per 16 rows of hidden (once per 8 when the rows of 16
+ * do not fit in shared memory: H > 5120): meant for the few rows of a
+ * small batch, where reading the weight is the cost; V a multiple of 8.
+ */
+int eagle_lmhead_quant(const eagle_tree_cfg* cfg, void* ws, size_t ws_bytes, int hidden_dim, int group,
+                       const void* hidden, const void* codes, const void* scales, void* draft_logits, void* stream);
+
+/*
+ * The 4-bit form of an LM head's bf16 weight [V, H], H a multiple of `group`
+ * and of 8: per group scale = amax / 7 rounded to bf16, code c = 8 +
+ * round(weight / scale) (ties to even, kept in 1..15); a group of zeros has
+ * scale 0 and codes 8. Non-finite weights are outside the contract (no access
+ * depends on a value).
+ */
+int eagle_lmhead_quant_pack(int vocab, int hidden_dim, int group, const void* weight, void* codes, void* scales,
+                            void* stream);
+
+/* ------------------------------------------------ log-probabilities --- */
+/*
+ * What a server answers with beside a token: its log-probability, its rank,
+ * the distribution's entropy and the most likely alternatives (not on the
+ * pages; the rows are those eagle_verify reads).
+ *   n_seq, per_seq   tokens [n_seq, per_seq]; entry (b, j) reads row
+ *                    slots[b, j] (row j when slots is NULL) of logits
+ *                    [n_seq, rows_per_seq, V], in cfg->logit_dtype. After
+ *                    eagle_verify: tokens = out_tokens, slots =
+ *                    accepted_slots, per_seq = D + 1, rows_per_seq = T.
+ *   temperature      > 0, finite: probabilities are softmax(row / temperature).
+ *   n_alt            alternatives per entry, 0..16.
+ *   logprob  fp32 out: ln p[token].   rank  int32 out, or NULL: entries of the
+ *            row above the token (larger logit, or equal and lower id).
+ *   entropy  fp32 out, or NULL: -sum p ln p (natural logarithm).
+ *   alt_ids, alt_logprobs [n_seq, per_seq, n_alt] out: the largest logits,
+ *            best first, equal logits by lower id (NULL when n_alt is 0;
+ *            -1 / -inf past the row's V entries).
+ * An entry with a negative token or slot is padding: logprob, entropy and
+ * alt_logprobs NaN, rank and alt_ids -1, no row read. A token >= V or a slot
+ * >= rows_per_seq raises status 3 and gives padding values. Logits of -inf
+ * have probability 0; a row with a NaN, a +inf or no finite logit raises
+ * status 1. Of `cfg` only vocab and logit_dtype matter here, of `ws` the
+ * status word.
+ */
+int eagle_token_logprobs(const eagle_tree_cfg* cfg, void* ws, size_t ws_bytes, int n_seq, int per_seq,
+                         int rows_per_seq, const void* logits, float temperature, const int32_t* slots,
+                         const int32_t* tokens, int n_alt, float* logprob, int32_t* rank, float* entropy,
+                         int32_t* alt_ids, float* alt_logprobs, void* stream);
 
 /* ------------------------------------------------- vocabulary shards --- */
 /*

@@ -92,6 +92,33 @@ int resolve_kv(const eagle_kv_cfg* kv, KvDims* k) {
     return EAGLE_OK;
 }
 
+int resolve_kvq(const eagle_kvq_cfg* kv, KvqDims* k) {
+    if (kv == nullptr) return EAGLE_ERR_INVALID_ARG;
+    if (kv->batch < 1 || kv->n_q_heads < 1 || kv->n_kv_heads < 1 || kv->head_dim < 1 || kv->layers < 0 ||
+        kv->max_len < 1 || kv->n_q_heads % kv->n_kv_heads != 0)
+        return EAGLE_ERR_INVALID_ARG;
+    if (kv->dtype != EAGLE_F32 && kv->dtype != EAGLE_BF16) return EAGLE_ERR_INVALID_ARG;
+    if (kv->block != 16 && kv->block != 32 && kv->block != 64 && kv->block != 128) return EAGLE_ERR_INVALID_ARG;
+    if (kv->seq_stride < 0 || kv->layer_stride < 0 || kv->kv_stride < 0 || kv->scale_seq_stride < 0 ||
+        kv->scale_layer_stride < 0 || kv->scale_kv_stride < 0)
+        return EAGLE_ERR_INVALID_ARG;
+    if (kv->pos_stride < static_cast<int64_t>(kv->n_kv_heads) * kv->head_dim ||
+        kv->scale_block_stride < kv->n_kv_heads)
+        return EAGLE_ERR_INVALID_ARG;
+    if (kv->head_dim != kKvqHeadDim || kv->dtype != EAGLE_BF16 || kv->batch > 65535 || kv->n_kv_heads > 65535)
+        return EAGLE_ERR_UNSUPPORTED;
+    if (kv->seq_stride % 16 || kv->layer_stride % 16 || kv->kv_stride % 16 || kv->pos_stride % 16)
+        return EAGLE_ERR_UNSUPPORTED;
+    // limits of a tensor map's strides and of 32-bit position arithmetic
+    if (kv->seq_stride >= (int64_t{1} << 40) || kv->pos_stride >= (int64_t{1} << 40) || kv->max_len > (1 << 30))
+        return EAGLE_ERR_UNSUPPORTED;
+    *k = KvqDims{kv->batch,        kv->n_q_heads,  kv->n_kv_heads,       kv->layers,
+                 kv->max_len,      kv->block,      kv->seq_stride,       kv->layer_stride,
+                 kv->kv_stride,    kv->pos_stride, kv->scale_seq_stride, kv->scale_layer_stride,
+                 kv->scale_kv_stride, kv->scale_block_stride};
+    return EAGLE_OK;
+}
+
 // The CUDA error of the calling thread's last failed call (0 = none).
 thread_local int g_last_cuda_error = 0;
 
@@ -411,6 +438,108 @@ int eagle_kv_compact(const eagle_kv_cfg* kv, void* kv_cache, const int32_t* pref
     if (k.layers * 2 > 65535) return EAGLE_ERR_UNSUPPORTED;
     return launch_result(launch_kv_compact(k, kv_cache, prefix_len, accept_len, accepted_slots, slots_stride, new_len,
                                            static_cast<int*>(ws), static_cast<cudaStream_t>(stream)));
+}
+
+int eagle_kvq_store(const eagle_kvq_cfg* kv, int layer, int T, const void* k, const void* v, int64_t row_stride,
+                    const int32_t* row_start, const int32_t* start, const int32_t* count, void* codes, float* scales,
+                    void* ws, void* stream) {
+    EAGLE_CALL(stream, ws);
+    KvqDims d;
+    int rc = resolve_kvq(kv, &d);
+    if (rc != EAGLE_OK) return rc;
+    if (layer < 0 || T < 1 || !k || !v || !start || !codes || !scales ||
+        row_stride < static_cast<int64_t>(d.Hkv) * kKvqHeadDim)
+        return EAGLE_ERR_INVALID_ARG;
+    if (row_stride % 8 != 0 || !aligned16(k) || !aligned16(v) || !aligned16(codes)) return EAGLE_ERR_UNSUPPORTED;
+    return launch_result(launch_kvq_store(d, layer, T, k, v, row_stride, row_start, start, count, codes, scales,
+                                          static_cast<int*>(ws), static_cast<cudaStream_t>(stream)));
+}
+
+int eagle_kvq_compact(const eagle_kvq_cfg* kv, void* codes, float* scales, const int32_t* prefix_len,
+                      const int32_t* accept_len, const int32_t* accepted_slots, int slots_stride, int32_t* new_len,
+                      void* ws, void* stream) {
+    EAGLE_CALL(stream, ws);
+    KvqDims d;
+    int rc = resolve_kvq(kv, &d);
+    if (rc != EAGLE_OK) return rc;
+    if (!codes || !scales || !prefix_len || !accept_len || !accepted_slots || !new_len || slots_stride < 1)
+        return EAGLE_ERR_INVALID_ARG;
+    if (!aligned16(codes)) return EAGLE_ERR_UNSUPPORTED;
+    if (d.layers == 0) return EAGLE_OK;
+    if (d.layers * 2 > 65535) return EAGLE_ERR_UNSUPPORTED;
+    return launch_result(launch_kvq_compact(d, codes, scales, prefix_len, accept_len, accepted_slots, slots_stride,
+                                            new_len, static_cast<int*>(ws), static_cast<cudaStream_t>(stream)));
+}
+
+size_t eagle_kvq_attention_workspace_bytes(const eagle_kvq_cfg* kv, int T) {
+    KvqDims d;
+    if (resolve_kvq(kv, &d) != EAGLE_OK || T < 1 || T > kMaxSlots) return 0;
+    return kvq_attention_ws_bytes(d, T);
+}
+
+int eagle_kvq_tree_attention(const eagle_kvq_cfg* kv, int T, const void* q, const void* codes, const float* scales,
+                             int layer, const int32_t* prefix_len, const uint32_t* mask, const int32_t* n_tree,
+                             void* out, void* ws, size_t ws_bytes, void* stream) {
+    EAGLE_CALL(stream, ws);
+    KvqDims d;
+    int rc = resolve_kvq(kv, &d);
+    if (rc != EAGLE_OK) return rc;
+    if (T < 1 || T > kMaxSlots || layer < 0) return EAGLE_ERR_INVALID_ARG;
+    if (!q || !codes || !scales || !prefix_len || !out) return EAGLE_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(codes) || !aligned16(out)) return EAGLE_ERR_UNSUPPORTED;
+    if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || ws_bytes < kvq_attention_ws_bytes(d, T))
+        return EAGLE_ERR_WORKSPACE;
+    return launch_result(launch_kvq_attention(d, T, q, codes, scales, layer, prefix_len, mask, n_tree, out, ws,
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+int eagle_lmhead_quant(const eagle_tree_cfg* cfg, void* ws, size_t ws_bytes, int hidden_dim, int group,
+                       const void* hidden, const void* codes, const void* scales, void* draft_logits, void* stream) {
+    EAGLE_CALL(stream, ws);
+    TreeDims d;
+    TreeWs w;
+    int rc = resolve(cfg, &d);
+    if (rc == EAGLE_OK) rc = bind_ws(d, ws, ws_bytes, &w);
+    if (rc != EAGLE_OK) return rc;
+    if (!hidden || !codes || !scales || !draft_logits || hidden_dim < 1 ||
+        (group != 32 && group != 64 && group != 128))
+        return EAGLE_ERR_INVALID_ARG;
+    if (hidden_dim % 128 != 0 || hidden_dim > kLmQuantMaxHidden || d.V % 8 != 0 || !aligned16(hidden) ||
+        !aligned16(codes) || !aligned16(scales) || !aligned16(draft_logits))
+        return EAGLE_ERR_UNSUPPORTED;
+    return launch_result(launch_lmhead_quant(d.B * d.k, d.V, hidden_dim, group, hidden, codes, scales, d.dtype,
+                                             draft_logits, w.status, static_cast<cudaStream_t>(stream)));
+}
+
+int eagle_lmhead_quant_pack(int vocab, int hidden_dim, int group, const void* weight, void* codes, void* scales,
+                            void* stream) {
+    EAGLE_CALL(stream, nullptr);
+    if (vocab < 1 || hidden_dim < 1 || !weight || !codes || !scales || (group != 32 && group != 64 && group != 128))
+        return EAGLE_ERR_INVALID_ARG;
+    if (hidden_dim % group != 0 || !aligned16(weight) || !aligned16(codes) || !aligned16(scales))
+        return EAGLE_ERR_UNSUPPORTED;
+    return launch_result(launch_lmhead_quant_pack(vocab, hidden_dim, group, weight, codes, scales,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
+int eagle_token_logprobs(const eagle_tree_cfg* cfg, void* ws, size_t ws_bytes, int n_seq, int per_seq,
+                         int rows_per_seq, const void* logits, float temperature, const int32_t* slots,
+                         const int32_t* tokens, int n_alt, float* logprob, int32_t* rank, float* entropy,
+                         int32_t* alt_ids, float* alt_logprobs, void* stream) {
+    EAGLE_CALL(stream, ws);
+    TreeDims d;
+    TreeWs w;
+    int rc = resolve(cfg, &d);
+    if (rc == EAGLE_OK) rc = bind_ws(d, ws, ws_bytes, &w);
+    if (rc != EAGLE_OK) return rc;
+    if (n_seq < 1 || per_seq < 1 || rows_per_seq < 1 || n_alt < 0 || n_alt > kMaxTopK || !logits || !tokens ||
+        !logprob || (n_alt > 0 && (!alt_ids || !alt_logprobs)) || !(temperature > 0.0f) || !std::isfinite(temperature))
+        return EAGLE_ERR_INVALID_ARG;
+    if (slots == nullptr && per_seq > rows_per_seq) return EAGLE_ERR_INVALID_ARG;
+    if (!aligned16(logits) || static_cast<int64_t>(n_seq) * per_seq > (1 << 24)) return EAGLE_ERR_UNSUPPORTED;
+    const LogprobArgs a{n_seq * per_seq, per_seq, rows_per_seq, d.V,     n_alt,        temperature, logits, slots,
+                        tokens,          logprob, entropy,      alt_logprobs, rank, alt_ids,     w.status};
+    return launch_result(launch_token_logprobs(a, d.dtype, static_cast<cudaStream_t>(stream)));
 }
 
 int eagle_status_fetch(void* ws, int* device_status, void* stream) {

@@ -1,0 +1,426 @@
+// LM head with 4-bit weights and group scales (sm_103a): logits [M, V] =
+// hidden [M, H] (bf16) x weight [V, H]^T, weight[v, h] = (c - 8) * scale of
+// (v, h / group). ["EAGLE" notes, EAGLE 方法: the draft model reuses the target
+// model's LM head]; the 4-bit form is not on the pages.
+//
+// With the few rows of a small batch the weight's bytes are the cost (V*H/2,
+// a quarter of the 16-bit head's), 4 M flops a byte. Per byte there is little
+// time: two products per code and row, so the codes are taken from registers:
+//   - mma.sync m16n8k16 with the weight as A (16 vocabulary rows) and the
+//     hidden rows as B (8 per MMA). tcgen05 would need the weight as bf16 in
+//     shared or tensor memory: four times its bytes written and read again
+//     on chip, more than shared memory's bandwidth at HBM's pace.
+//   - a code becomes bf16 in two instructions per pair: (w >> s & 0x000f000f)
+//     | 0x43004300 is 128 + c, minus 136 is c - 8, both exact. The products of a
+//     group are summed by the tensor core in fp32 and multiplied by the
+//     group's scale in fp32: no rounding of a weight at all.
+//   - the hidden dimension is summed over in an order in which a lane holds
+//     32 neighbouring entries of a weight row (one 16-byte load of codes per
+//     128 entries) and the hidden rows are laid out in shared memory in that
+//     order once per CTA.
+// One persistent CTA per SM takes an equal, contiguous range of the
+// vocabulary in tiles of 64 rows; its eight MMA warps split the hidden
+// dimension (warp w: the 128-wide slices w, w + 8, ...), so that each works
+// alone, streaming its slices of one tile after the other through its own
+// ring of TMA tiles; two more warps add the eight partial sums of a finished
+// tile and write the logits while the next tile streams.
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "attn_common.cuh"
+#include "eagle_internal.cuh"
+#include "eagle_ws.h"
+#include "tc_ptx.cuh"
+
+namespace eagle {
+namespace {
+
+constexpr int kMmaWarps = 8;
+constexpr int kAddWarps = 2;
+constexpr int kThreads = (kMmaWarps + kAddWarps) * 32;
+constexpr int kSlice = 128;                // hidden entries of a slice
+constexpr int kSliceBytes = kSlice / 2;    // codes of one row's slice
+constexpr int kMaxStages = 4;
+constexpr int kSms = 152;
+constexpr int kMaxSmem = 227 * 1024 - 1024;  // dynamic, beside the barriers
+
+struct QuantParams {
+    int M, V, H, n_slice;
+    int rows;        // hidden rows of a pass (blockIdx.y takes rows [y * rows, ...))
+    int stages;
+    int hid_stride;  // bytes of a hidden row in shared memory
+    const __nv_bfloat16* hidden;
+    const __nv_bfloat16* scales;
+    void* out;
+    int* status;
+};
+
+__device__ __forceinline__ void mma_bf16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Codes at bits S and 16 + S of w as bf16 pairs c - 8.
+template <int S>
+__device__ __forceinline__ uint32_t pair(uint32_t w) {
+    const uint32_t x = ((w >> S) & 0x000f000fu) | 0x43004300u;  // 128 + c
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), __float2bfloat162_rn(136.0f));
+    return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// First hidden entry (within a slice) of the eight that lane t of a quad
+// takes in step pair q (0..3): neighbouring words of the lane's codes, for a
+// group that spans the slice; quarters of the slice for the smaller groups.
+template <int GROUP>
+__device__ __forceinline__ int entry0(int q, int t) {
+    return GROUP == 128 ? t * 32 + q * 8 : GROUP == 64 ? (q >> 1) * 64 + t * 16 + (q & 1) * 8 : q * 32 + t * 8;
+}
+
+// RT: vocabulary rows of a tile; NT: n-tiles of eight hidden rows.
+template <int RT, int NT, int GROUP, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    lmhead_quant_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm16, QuantParams p) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    __shared__ uint64_t bar_full[kMmaWarps][kMaxStages], bar_red_full[2], bar_red_empty[2];
+    constexpr int MT = RT / 16;
+    constexpr int kStage = RT * kSliceBytes;
+    constexpr int NG = kSlice / GROUP;  // groups of a slice
+    constexpr int RS = 8 * NT;          // columns of a partial row
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int m0 = blockIdx.y * p.rows;
+    const int rows = min(p.rows, p.M - m0);
+    // tile partial sums: [buffer][warp][row][RS]
+    float* red = reinterpret_cast<float*>(smem);
+    unsigned char* ring = smem + 2 * kMmaWarps * RT * RS * 4 + warp * p.stages * kStage;  // MMA warps
+    unsigned char* hid = smem + 2 * kMmaWarps * RT * RS * 4 + kMmaWarps * p.stages * kStage;
+    // this CTA's vocabulary rows, in units of 16
+    const int units = (p.V + 15) / 16;
+    const int u0 = static_cast<int>(static_cast<long>(units) * blockIdx.x / gridDim.x);
+    const int u1 = static_cast<int>(static_cast<long>(units) * (blockIdx.x + 1) / gridDim.x);
+    const int v0 = u0 * 16, v1 = u1 * 16;
+    const int n_tiles = (v1 - v0 + RT - 1) / RT;
+    if (threadIdx.x == 0) {
+        for (int w = 0; w < kMmaWarps; ++w)
+            for (int s = 0; s < p.stages; ++s) mbar_init(&bar_full[w][s], 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bar_red_full[s], kMmaWarps);
+            mbar_init(&bar_red_empty[s], kAddWarps);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const int my_slices = warp < kMmaWarps ? (p.n_slice - warp + kMmaWarps - 1) / kMmaWarps : 0;
+    const int total = my_slices * n_tiles;  // stages this warp consumes
+    int filled = 0, f_tile = 0, f_slice = warp;
+    auto fill = [&]() {
+        if (filled >= total) return;
+        if (lane == 0) {
+            const int s = filled % p.stages;
+            uint64_t* bar = &bar_full[warp][s];
+            const int v = v0 + f_tile * RT;
+            const int mts = min(MT, (v1 - v) / 16);  // a last tile of fewer rows: 16 at a time
+            mbar_arrive_expect_tx(bar, mts * 16 * kSliceBytes);
+            if (mts == MT)
+                tma_load_2d(ring + s * kStage, &tm, f_slice * kSliceBytes, v, bar);
+            else
+                for (int i = 0; i < mts; ++i)
+                    tma_load_2d(ring + s * kStage + i * 16 * kSliceBytes, &tm16, f_slice * kSliceBytes, v + 16 * i, bar);
+        }
+        ++filled;
+        f_slice += kMmaWarps;
+        if (f_slice >= p.n_slice) {
+            f_slice = warp;
+            ++f_tile;
+        }
+    };
+    if (warp < kMmaWarps)
+        for (int s = 0; s < p.stages; ++s) fill();
+    // hidden rows into shared memory: 16-byte pieces of eight entries in MMA order
+    // (0 4, 1 5, 2 6, 3 7), piece (slice, q, t) of a row at (slice * 16 + 4 q + t) * 16
+    for (int i = threadIdx.x; i < rows * p.n_slice * 16; i += kThreads) {
+        const int m = i / (p.n_slice * 16), c = i - m * p.n_slice * 16;
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p.hidden + static_cast<size_t>(m0 + m) * p.H +
+                                                             (c >> 4) * kSlice + entry0<GROUP>((c >> 2) & 3, c & 3)));
+        *reinterpret_cast<uint4*>(hid + m * p.hid_stride + c * 16) =
+            make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632), __byte_perm(u.y, u.w, 0x5410),
+                       __byte_perm(u.y, u.w, 0x7632));
+    }
+    __syncthreads();
+
+    if (warp < kMmaWarps) {
+        bool ok = true;
+        int used = 0;
+        for (int tile = 0; tile < n_tiles; ++tile) {
+            const int v = v0 + tile * RT;
+            const int mts = min(MT, (v1 - v) / 16);
+            float sum[MT][NT][4];
+#pragma unroll
+            for (int a = 0; a < MT; ++a)
+#pragma unroll
+                for (int b = 0; b < NT; ++b) sum[a][b][0] = sum[a][b][1] = sum[a][b][2] = sum[a][b][3] = 0.0f;
+            for (int slice = warp; slice < p.n_slice; slice += kMmaWarps) {
+                const int st = used % p.stages;
+                // scales of rows g, g + 8 of every m-tile (a row past the vocabulary reads the last one's)
+                float sc[MT][2][NG];
+#pragma unroll
+                for (int a = 0; a < MT; ++a)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const __nv_bfloat16* src =
+                            p.scales + static_cast<size_t>(min(v + a * 16 + g + 8 * e, p.V - 1)) * (p.n_slice * NG) + slice * NG;
+#pragma unroll
+                        for (int q = 0; q < NG; ++q) sc[a][e][q] = __bfloat162float(__ldg(src + q));
+                    }
+                if (ok && !__all_sync(0xffffffffu, mbar_wait_sleep(&bar_full[warp][st], (used / p.stages) & 1))) {
+                    ok = false;
+                    if (lane == 0) raise_status(p.status, kDevTimeout);
+                    for (int f = used + 1; f < filled; ++f)  // copies land before shared memory goes away
+                        mbar_wait_sleep(&bar_full[warp][f % p.stages], (f / p.stages) & 1);
+                }
+                ++used;
+                if (!ok) continue;
+                const unsigned char* src = ring + st * kStage;
+                uint32_t w[MT][2][4];
+#pragma unroll
+                for (int a = 0; a < MT; ++a)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const unsigned char* row = src + (a * 16 + g + 8 * e) * kSliceBytes;
+                        if (GROUP == 128) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(row + t * 16);
+                            w[a][e][0] = x.x, w[a][e][1] = x.y, w[a][e][2] = x.z, w[a][e][3] = x.w;
+                        } else if (GROUP == 64) {
+                            const uint2 x = *reinterpret_cast<const uint2*>(row + t * 8);
+                            const uint2 y = *reinterpret_cast<const uint2*>(row + 32 + t * 8);
+                            w[a][e][0] = x.x, w[a][e][1] = x.y, w[a][e][2] = y.x, w[a][e][3] = y.y;
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) w[a][e][q] = *reinterpret_cast<const uint32_t*>(row + q * 16 + t * 4);
+                        }
+                    }
+                __syncwarp();  // every lane has read the stage
+                fill();
+                float acc[MT][NT][4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (q % (4 / NG) == 0) {
+#pragma unroll
+                        for (int a = 0; a < MT; ++a)
+#pragma unroll
+                            for (int b = 0; b < NT; ++b) acc[a][b][0] = acc[a][b][1] = acc[a][b][2] = acc[a][b][3] = 0.0f;
+                    }
+                    uint4 hb[NT];
+#pragma unroll
+                    for (int b = 0; b < NT; ++b) {
+                        const int m = b * 8 + g;
+                        hb[b] = m < rows ? *reinterpret_cast<const uint4*>(hid + m * p.hid_stride + (slice * 16 + q * 4 + t) * 16)
+                                         : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int a = 0; a < MT; ++a) {
+                        const uint32_t lo = w[a][0][q], hi = w[a][1][q];
+                        const uint32_t a0 = pair<0>(lo), a1 = pair<0>(hi), a2 = pair<4>(lo), a3 = pair<4>(hi);
+                        const uint32_t a4 = pair<8>(lo), a5 = pair<8>(hi), a6 = pair<12>(lo), a7 = pair<12>(hi);
+#pragma unroll
+                        for (int b = 0; b < NT; ++b) {
+                            mma_bf16_16816(acc[a][b], a0, a1, a2, a3, hb[b].x, hb[b].y);
+                            mma_bf16_16816(acc[a][b], a4, a5, a6, a7, hb[b].z, hb[b].w);
+                        }
+                    }
+                    if (q % (4 / NG) == 4 / NG - 1) {
+                        const int gi = q / (4 / NG);
+#pragma unroll
+                        for (int a = 0; a < MT; ++a)
+#pragma unroll
+                            for (int b = 0; b < NT; ++b)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) sum[a][b][e] = fmaf(acc[a][b][e], sc[a][e >> 1][gi], sum[a][b][e]);
+                    }
+                }
+            }
+            // the tile's partial sums to the adding warps
+            const int buf = tile & 1;
+            if (ok && tile >= 2 && !__all_sync(0xffffffffu, mbar_wait_sleep(&bar_red_empty[buf], ((tile >> 1) - 1) & 1))) {
+                ok = false;
+                if (lane == 0) raise_status(p.status, kDevTimeout);
+                for (int f = used; f < filled; ++f) mbar_wait_sleep(&bar_full[warp][f % p.stages], (f / p.stages) & 1);
+            }
+            float* dst = red + (buf * kMmaWarps + warp) * RT * RS;
+            if (ok) {
+#pragma unroll
+                for (int a = 0; a < MT; ++a) {
+                    if (a >= mts) break;
+#pragma unroll
+                    for (int b = 0; b < NT; ++b)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<float2*>(dst + (a * 16 + g + 8 * e) * RS + b * 8 + 2 * t) =
+                                make_float2(sum[a][b][2 * e], sum[a][b][2 * e + 1]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_red_full[buf]);
+        }
+    } else {
+        const int at = threadIdx.x - kMmaWarps * 32;
+        bool ok = true;
+        for (int tile = 0; ok && tile < n_tiles; ++tile) {
+            const int buf = tile & 1;
+            const int v = v0 + tile * RT;
+            const int nv = min(RT, min(v1, p.V) - v);  // rows of the tile inside the vocabulary (a multiple of 8)
+            if (!__all_sync(0xffffffffu, mbar_wait_sleep(&bar_red_full[buf], (tile >> 1) & 1))) {
+                if (lane == 0) raise_status(p.status, kDevTimeout);
+                break;
+            }
+            const float* src = red + buf * kMmaWarps * RT * RS;
+            for (int i = at; i < rows * (RT / 2); i += kAddWarps * 32) {  // two vocabulary rows each
+                const int m = i / (RT / 2), r = (i - m * (RT / 2)) * 2;
+                if (r >= nv) continue;
+                float x = 0.0f, y = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kMmaWarps; ++w) {
+                    x += src[(w * RT + r) * RS + m];
+                    y += src[(w * RT + r + 1) * RS + m];
+                }
+                const size_t o = static_cast<size_t>(m0 + m) * p.V + v + r;
+                if (BF16) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + o) = pack_bf16(x, y);
+                else *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o) = make_float2(x, y);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_red_empty[buf]);
+        }
+    }
+}
+
+// A 2-D map of the codes: (bytes of a row, row), boxes of one slice x `rows` rows.
+bool make_map(CUtensorMap* m, const void* codes, int V, int H, int rows) {
+    auto fn = tensor_map_encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(H / 2), static_cast<cuuint64_t>(V)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(H / 2)};
+    const cuuint32_t box[2] = {kSliceBytes, static_cast<cuuint32_t>(rows)};
+    const cuuint32_t estride[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, estride,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Shared memory of a pass of `rows` hidden rows with RT-row tiles and `stages` per ring.
+int smem_bytes(int rows, int H, int RT, int NT, int stages) {
+    return 2 * kMmaWarps * RT * 8 * NT * 4 + kMmaWarps * stages * RT * kSliceBytes + rows * (2 * H + 64) + 128;
+}
+
+template <int RT, int NT, int GROUP, bool BF16>
+cudaError_t launch(const QuantParams& p, const void* codes, int smem, cudaStream_t stream) {
+    CUtensorMap tm, tm16;
+    if (!make_map(&tm, codes, p.V, p.H, RT) || !make_map(&tm16, codes, p.V, p.H, 16)) return cudaErrorInvalidValue;
+    auto kernel = lmhead_quant_kernel<RT, NT, GROUP, BF16>;
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), smem);
+    if (e != cudaSuccess) return e;
+    const int units = (p.V + 15) / 16;
+    return launch_pdl(kernel, dim3(std::min(kSms, units), (p.M + p.rows - 1) / p.rows), dim3(kThreads),
+                      static_cast<size_t>(smem), stream, tm, tm16, p);
+}
+
+template <int RT, int NT>
+cudaError_t launch_group(const QuantParams& p, int group, bool bf16, const void* codes, int smem, cudaStream_t s) {
+    if (group == 128) return bf16 ? launch<RT, NT, 128, true>(p, codes, smem, s) : launch<RT, NT, 128, false>(p, codes, smem, s);
+    if (group == 64) return bf16 ? launch<RT, NT, 64, true>(p, codes, smem, s) : launch<RT, NT, 64, false>(p, codes, smem, s);
+    return bf16 ? launch<RT, NT, 32, true>(p, codes, smem, s) : launch<RT, NT, 32, false>(p, codes, smem, s);
+}
+
+// ------------------------------------------------------------------- pack ---
+
+// One lane per eight entries; group / 8 neighbouring lanes share a scale.
+__global__ void __launch_bounds__(256) lmhead_quant_pack_kernel(long pieces, int group, const uint4* __restrict__ weight,
+                                                                uint32_t* __restrict__ codes,
+                                                                __nv_bfloat16* __restrict__ scales) {
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const int lanes = group / 8;
+    // pieces is a multiple of lanes (<= 16), so a group's lanes are in range together
+    for (long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; i - (threadIdx.x & 31) < pieces; i += 256l * gridDim.x) {
+        const bool in = i < pieces;
+        const uint4 u = in ? weight[i] : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        float x[8], am = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] = __uint_as_float((e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16));
+            am = fmaxf(am, fabsf(x[e]));
+        }
+        for (int o = 1; o < lanes; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+        const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(am, 7.0f));
+        const float s = __bfloat162float(sb);
+        uint32_t c = 0u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float q = s > 0.0f ? rintf(__fdiv_rn(x[e], s)) : 0.0f;
+            c |= (static_cast<uint32_t>(8 + static_cast<int>(fminf(fmaxf(q, -7.0f), 7.0f))) & 15u) << (4 * e);
+        }
+        if (in) {
+            codes[i] = c;
+            if (i % lanes == 0) scales[i / lanes] = sb;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_lmhead_quant(int M, int V, int H, int group, const void* hidden, const void* codes,
+                                const void* scales, int out_dtype, void* out, int* status, cudaStream_t stream) {
+    QuantParams p{};
+    p.M = M;
+    p.V = V;
+    p.H = H;
+    p.n_slice = H / kSlice;
+    p.hid_stride = 2 * H + 64;  // rows 64 bytes apart modulo 128: no bank conflicts between neighbouring rows
+    p.hidden = static_cast<const __nv_bfloat16*>(hidden);
+    p.scales = static_cast<const __nv_bfloat16*>(scales);
+    p.out = out;
+    p.status = status;
+    // Up to 16 hidden rows per pass, 8 when 16 (or all, if fewer) do not fit beside two stages
+    // of the ring; tiles of 64 vocabulary rows, 32 when 64 do not fit.
+    const bool bf16 = out_dtype == 1;
+    auto run = [&](int rows, int RT, int NT, auto fn, cudaError_t* e) -> bool {
+        int st = kMaxStages;
+        while (st >= 2 && smem_bytes(rows, H, RT, NT, st) > kMaxSmem) --st;
+        if (st < 2) return false;
+        p.rows = rows;
+        p.stages = st;
+        *e = fn(p, group, bf16, codes, smem_bytes(rows, H, RT, NT, st), stream);
+        return true;
+    };
+    cudaError_t e = cudaErrorInvalidValue;
+    if (M > 8) {
+        const int rows = std::min(M, 16);
+        if (run(rows, 64, 2, launch_group<64, 2>, &e) || run(rows, 32, 2, launch_group<32, 2>, &e)) return e;
+    }
+    const int rows = std::min(M, 8);
+    if (run(rows, 64, 1, launch_group<64, 1>, &e) || run(rows, 32, 1, launch_group<32, 1>, &e)) return e;
+    return e;
+}
+
+cudaError_t launch_lmhead_quant_pack(int V, int H, int group, const void* weight, void* codes, void* scales,
+                                     cudaStream_t stream) {
+    const long pieces = static_cast<long>(V) * H / 8;
+    const unsigned grid = static_cast<unsigned>(std::min<long>((pieces + 255) / 256, 152 * 16));
+    return launch_pdl(lmhead_quant_pack_kernel, dim3(grid), dim3(256), 0, stream, pieces, group,
+                      static_cast<const uint4*>(weight), static_cast<uint32_t*>(codes),
+                      static_cast<__nv_bfloat16*>(scales));
+}
+
+}  // namespace eagle

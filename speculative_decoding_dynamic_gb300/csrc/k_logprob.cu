@@ -1,0 +1,447 @@
+// Log-probabilities of given tokens with rank, entropy and top alternatives
+// (sm_103a): eagle_token_logprobs. Not on the pages; the rows are the target
+// rows of stage 6.
+//
+// With c = log2(e) / T, the row's maximum M and y = (x - M) c:
+//   S = sum 2^y, E = sum y 2^y
+//   ln p[t] = (x_t - M) / T - ln S,  entropy = ln S - ln2 E / S
+// S and E are kept together in one pass, like an online softmax: when the
+// running maximum rises by d / c, S <- 2^-d S and E <- 2^-d (E - d S). The
+// difference is taken before the product (one packed addition more than a
+// multiply-add of the scaled maximum) so that it is exact next to logits of any
+// size. The rank counts entries above the token's logit, read before the pass.
+// Logits are clamped to -2^100 for the sums only (2^y is 0 there, and y 2^y must
+// not be -inf * 0).
+//
+// Bound by HBM: a row is read once, 16 bytes per lane and load, four loads in
+// flight per thread; about six instructions per element beside
+// the one exponential (packed fp32 pairs for the multiply-adds and sums, packed
+// bf16 for clamps, maxima and compares; the compare is skipped for groups
+// whose maximum is below the token's logit). A row is split over a cluster of
+// 1..8 CTAs when there are few rows. The alternatives need no second pass
+// over the row: the k-th largest of the threads' maxima bounds the k-th
+// largest entry from below, and only the groups (four vectors of a thread)
+// whose maximum reaches it are read again, from L2.
+
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "eagle_internal.cuh"
+#include "eagle_ws.h"
+
+namespace eagle {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kVecs = 4;                             // 16-byte vectors of a group
+constexpr int kChunkBytes = kThreads * kVecs * 16;   // 16 KB
+constexpr int kKeys = 512;                           // candidate keys held at once
+constexpr float kFloor = -0x1p100f;  // a value of both types
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Part {  // one CTA's share of a row
+    float m, s, e;
+    int above;
+};
+struct Shared {
+    uint32_t wtop[kWarps][kMaxTopK];
+    unsigned long long keys[kKeys];
+    unsigned long long red[kWarps];
+    uint64_t ctop[kMaxTopK];
+    Part wpart[kWarps];
+    float wmax[kWarps];
+    int nkeys;
+    uint32_t tau;
+    // filled by every CTA of the cluster in the leader's copy
+    uint64_t rtop[kMaxChunks * kMaxTopK];
+    Part rpart[kMaxChunks];
+    float rmax[kMaxChunks];
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ __nv_bfloat162 bf2(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+__device__ __forceinline__ uint32_t u32(__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+
+template <int DT>
+__device__ __forceinline__ float vec_max(const uint4& u) {
+    if (DT == 1) {
+        const __nv_bfloat162 m = __hmax2(__hmax2(bf2(u.x), bf2(u.y)), __hmax2(bf2(u.z), bf2(u.w)));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+}
+template <int DT>
+__device__ __forceinline__ float element(const uint4& u, int e) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if (DT == 1) return __uint_as_float((e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16));
+    return __uint_as_float(w[e]);
+}
+template <int DT>
+__device__ __forceinline__ uint4 neg_inf() {
+    const uint32_t w = DT == 1 ? 0xff80ff80u : 0xff800000u;
+    return make_uint4(w, w, w, w);
+}
+
+// Entries of a vector above x: larger, or (or_equal) equal.
+template <int DT>
+__device__ __forceinline__ int count_above(const uint4& u, float x, bool or_equal) {
+    if (DT == 1) {
+        const __nv_bfloat162 t = __float2bfloat162_rn(x);  // x is a bf16 value
+        __nv_bfloat162 n;
+        if (or_equal) n = __hadd2(__hadd2(__hge2(bf2(u.x), t), __hge2(bf2(u.y), t)), __hadd2(__hge2(bf2(u.z), t), __hge2(bf2(u.w), t)));
+        else n = __hadd2(__hadd2(__hgt2(bf2(u.x), t), __hgt2(bf2(u.y), t)), __hadd2(__hgt2(bf2(u.z), t), __hgt2(bf2(u.w), t)));
+        return static_cast<int>(__low2float(n) + __high2float(n));
+    }
+    const float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+    int n = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) n += or_equal ? v[e] >= x : v[e] > x;
+    return n;
+}
+
+// a <- a and b over the larger maximum.
+__device__ __forceinline__ void join(Part& a, const Part& b, float c) {
+    const float M = fmaxf(a.m, b.m);
+    const float da = a.m == -INFINITY ? 0.0f : (a.m - M) * c, db = b.m == -INFINITY ? 0.0f : (b.m - M) * c;
+    const float fa = a.m == -INFINITY ? 0.0f : ex2_approx(da), fb = b.m == -INFINITY ? 0.0f : ex2_approx(db);
+    // a factor of 0 comes with a difference that may be infinite
+    a.e = (fa > 0.0f ? fa * fmaf(da, a.s, a.e) : 0.0f * a.s) + (fb > 0.0f ? fb * fmaf(db, b.s, b.e) : 0.0f * b.s);
+    a.s = fa * a.s + fb * b.s;
+    a.m = M;
+    a.above += b.above;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs a, int cpr, int seg, float c) {
+    extern __shared__ __align__(16) unsigned char gmax_raw[];  // [chunk][thread] group maxima (ordered bits)
+    __shared__ Shared sm;
+    constexpr int ES = DT == 1 ? 2 : 4;
+    constexpr int EPV = 16 / ES;
+    constexpr int CE = kChunkBytes / ES;  // elements of a chunk
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int entry = blockIdx.x / cpr, rank = blockIdx.x % cpr;  // a cluster is cpr neighbouring CTAs
+    const int k = a.n_alt;
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const int b = entry / a.per_seq, j = entry - b * a.per_seq;
+    const int slot = a.slots ? a.slots[entry] : j;
+    const int tok = a.tokens[entry];
+    if (slot < 0 || tok < 0 || slot >= a.rows_per_seq || tok >= a.V) {  // uniform over the cluster
+        if (rank == 0) {
+            if (tid == 0) {
+                if (slot >= a.rows_per_seq || tok >= a.V) raise_status(a.status, kDevBadIndex);
+                a.logprob[entry] = NAN;
+                if (a.entropy) a.entropy[entry] = NAN;
+                if (a.rank) a.rank[entry] = -1;
+            }
+            if (tid < k) {
+                a.alt_ids[static_cast<size_t>(entry) * k + tid] = -1;
+                a.alt_logprobs[static_cast<size_t>(entry) * k + tid] = NAN;
+            }
+        }
+        return;
+    }
+    const char* row = static_cast<const char*>(a.logits) +
+                      (static_cast<size_t>(b) * a.rows_per_seq + slot) * static_cast<size_t>(a.V) * ES;
+    const int first = rank * seg;                       // this CTA's elements [first, first + n)
+    const int n = max(0, min(seg, a.V - first));
+    const int nch = (n + CE - 1) / CE;
+    const uint4* vec = reinterpret_cast<const uint4*>(row + static_cast<size_t>(first) * ES);
+    const int nvec = n / EPV;
+    const float xt = DT == 1 ? __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(row) + tok)) << 16)
+                             : __ldg(reinterpret_cast<const float*>(row) + tok);
+    if (tid == 0) {
+        sm.nkeys = 0;
+        sm.tau = 0u;
+    }
+    if (tid < kMaxTopK) sm.ctop[tid] = 0ull;
+
+    // ---- the pass ----
+    Part my{-INFINITY, 0.0f, 0.0f, 0};
+    float top = -INFINITY;  // this thread's largest element
+    for (int ch = 0; ch < nch; ++ch) {
+        uint4 u[kVecs];
+#pragma unroll
+        for (int q = 0; q < kVecs; ++q) {
+            const int v = (ch * kVecs + q) * kThreads + tid;
+            u[q] = v < nvec ? __ldg(vec + v) : neg_inf<DT>();
+        }
+        const float gm = fmaxf(fmaxf(vec_max<DT>(u[0]), vec_max<DT>(u[1])), fmaxf(vec_max<DT>(u[2]), vec_max<DT>(u[3])));
+        top = fmaxf(top, gm);
+        const bool any = ch * kVecs * kThreads + tid < nvec;
+        if (k > 0) {  // bf16 values are decided by the top half of their ordered bits
+            if (DT == 1) reinterpret_cast<uint16_t*>(gmax_raw)[ch * kThreads + tid] = any ? f2o(gm) >> 16 : 0;
+            else reinterpret_cast<uint32_t*>(gmax_raw)[ch * kThreads + tid] = any ? f2o(gm) : 0u;
+        }
+        if (!any) continue;
+        if (gm >= xt) {
+#pragma unroll
+            for (int q = 0; q < kVecs; ++q) {
+                const int v = (ch * kVecs + q) * kThreads + tid;
+                const int id = first + v * EPV;
+                if (v >= nvec) break;  // fill
+                if (id + EPV <= tok || id > tok) {
+                    my.above += count_above<DT>(u[q], xt, id < tok);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < EPV; ++e) {
+                        const float x = element<DT>(u[q], e);
+                        my.above += x > xt || (x == xt && id + e < tok);
+                    }
+                }
+            }
+        }
+        if (fmaxf(gm, kFloor) > my.m) {
+            const Part up{fmaxf(gm, kFloor), 0.0f, 0.0f, 0};
+            join(my, up, c);
+        }
+        const uint64_t c2 = f2_pack(c, c), m2 = f2_pack(-my.m, -my.m);
+        uint64_t s2 = 0ull, e2 = 0ull;
+#pragma unroll
+        for (int q = 0; q < kVecs; ++q) {
+            const uint32_t w[4] = {u[q].x, u[q].y, u[q].z, u[q].w};
+#pragma unroll
+            for (int i = 0; i < EPV / 2; ++i) {
+                uint64_t x2;
+                if (DT == 1) {
+                    // vectors past the end are -inf: clamped like any other, they add 2^-huge = 0
+                    const uint32_t x = u32(__hmax2_nan(bf2(w[i]), __float2bfloat162_rn(kFloor)));
+                    x2 = f2_pack(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+                } else {
+                    x2 = f2_pack(max_nan(__uint_as_float(w[2 * i]), kFloor), max_nan(__uint_as_float(w[2 * i + 1]), kFloor));
+                }
+                const uint64_t y = f2_mul(f2_add(x2, m2), c2);
+                const uint64_t p = f2_pack(ex2_approx(f2_lo(y)), ex2_approx(f2_hi(y)));
+                s2 = f2_add(s2, p);
+                e2 = f2_fma(y, p, e2);
+            }
+        }
+        my.s += f2_lo(s2) + f2_hi(s2);
+        my.e += f2_lo(e2) + f2_hi(e2);
+    }
+    // ---- this CTA's sums ----
+    float wmx = top;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Part x;
+        x.m = __shfl_xor_sync(0xffffffffu, my.m, o);
+        x.s = __shfl_xor_sync(0xffffffffu, my.s, o);
+        x.e = __shfl_xor_sync(0xffffffffu, my.e, o);
+        x.above = __shfl_xor_sync(0xffffffffu, my.above, o);
+        wmx = fmaxf(wmx, __shfl_xor_sync(0xffffffffu, wmx, o));
+        join(my, x, c);
+    }
+    if (lane == 0) {
+        sm.wpart[warp] = my;
+        sm.wmax[warp] = wmx;
+    }
+    if (k > 0) {
+        // tau: the k-th largest of the threads' maxima (0: fewer threads hold elements)
+        uint32_t v = tid < nvec ? f2o(top) : 0u;
+#pragma unroll
+        for (int size = 2; size <= 32; size <<= 1)  // descending bitonic sort over the warp
+#pragma unroll
+            for (int s = size >> 1; s > 0; s >>= 1) {
+                const uint32_t o = __shfl_xor_sync(0xffffffffu, v, s);
+                v = (((lane & s) == 0) == ((lane & size) == 0)) ? max(o, v) : min(o, v);
+            }
+        if (lane < kMaxTopK) sm.wtop[warp][lane] = lane < k ? v : 0u;
+        __syncthreads();
+        if (tid < kWarps * kMaxTopK) {
+            const uint32_t x = (&sm.wtop[0][0])[tid];
+            if (x != 0u) {
+                int r = 0;
+                for (int i = 0; i < kWarps * kMaxTopK; ++i) {
+                    const uint32_t o = (&sm.wtop[0][0])[i];
+                    r += o > x || (o == x && i < tid);
+                }
+                if (r == k - 1) sm.tau = x;
+            }
+        }
+        __syncthreads();
+        const uint32_t tau = sm.tau;
+        // every element >= tau of the groups that reach it
+        auto hot = [&](int ch) -> bool {
+            const uint32_t g = DT == 1 ? static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(gmax_raw)[ch * kThreads + tid]) << 16
+                                       : reinterpret_cast<const uint32_t*>(gmax_raw)[ch * kThreads + tid];
+            return g != 0u && g >= (DT == 1 ? tau & 0xffff0000u : tau);
+        };
+        for (int ch = 0; ch < nch; ++ch) {
+            if (!hot(ch)) continue;
+            for (int q = 0; q < kVecs; ++q) {
+                const int v = (ch * kVecs + q) * kThreads + tid;
+                if (v >= nvec) break;
+                const uint4 u = __ldg(vec + v);
+#pragma unroll
+                for (int e = 0; e < EPV; ++e) {
+                    const float x = element<DT>(u, e);
+                    if (x == x && f2o(x) >= tau) {
+                        const int at = atomicAdd(&sm.nkeys, 1);
+                        if (at < kKeys) sm.keys[at] = make_key(x, static_cast<uint32_t>(first + v * EPV + e));
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        const int nk = sm.nkeys;
+        if (nk <= kKeys) {
+            for (int i = tid; i < nk; i += kThreads) {
+                const unsigned long long key = sm.keys[i];
+                int r = 0;
+                for (int o = 0; o < nk; ++o) r += sm.keys[o] > key;
+                if (r < k) sm.ctop[r] = key;
+            }
+        } else {  // many equal values at the top: k rounds, each the largest key below the last
+            uint64_t prev = ~0ull;
+            for (int r = 0; r < k; ++r) {
+                uint64_t best = 0;
+                for (int ch = 0; ch < nch; ++ch) {
+                    if (!hot(ch)) continue;
+                    for (int q = 0; q < kVecs; ++q) {
+                        const int v = (ch * kVecs + q) * kThreads + tid;
+                        if (v >= nvec) break;
+                        const uint4 u = __ldg(vec + v);
+#pragma unroll
+                        for (int e = 0; e < EPV; ++e) {
+                            const float x = element<DT>(u, e);
+                            const uint64_t key = x == x ? make_key(x, static_cast<uint32_t>(first + v * EPV + e)) : 0ull;
+                            if (key < prev && key > best) best = key;
+                        }
+                    }
+                }
+                best = warp_max_u64(best);
+                __syncthreads();
+                if (lane == 0) sm.red[warp] = best;
+                __syncthreads();
+                for (int i = 0; i < kWarps; ++i) best = sm.red[i] > best ? sm.red[i] : best;
+                if (tid == 0) sm.ctop[r] = best;
+                prev = best;
+                if (best == 0ull) break;  // uniform
+            }
+        }
+    }
+    __syncthreads();
+    // ---- the row's results in the cluster's leader ----
+    cg::cluster_group cluster = cg::this_cluster();
+    Shared* lead = cpr > 1 ? cluster.map_shared_rank(&sm, 0) : &sm;
+    if (tid < kMaxTopK) lead->rtop[rank * kMaxTopK + tid] = sm.ctop[tid];
+    if (tid == 0) {
+        Part p = sm.wpart[0];
+        float m = sm.wmax[0];
+        for (int i = 1; i < kWarps; ++i) {
+            join(p, sm.wpart[i], c);
+            m = fmaxf(m, sm.wmax[i]);
+        }
+        lead->rpart[rank] = p;
+        lead->rmax[rank] = m;
+    }
+    if (cpr > 1) {
+        cluster.sync();
+        if (rank != 0) return;
+    } else {
+        __syncthreads();
+    }
+    Part p = sm.rpart[0];
+    float m = sm.rmax[0];
+    for (int i = 1; i < cpr; ++i) {
+        join(p, sm.rpart[i], c);
+        m = fmaxf(m, sm.rmax[i]);
+    }
+    if (m <= kFloor && m > -INFINITY) {
+        // A row with nothing above the floor (a mask of the type's lowest value everywhere):
+        // the clamp hides its differences, so the leader sums it again as it is.
+        float s = 0.0f, e = 0.0f;
+        for (int v = tid; v < a.V / EPV; v += kThreads) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(row) + v);
+#pragma unroll
+            for (int i = 0; i < EPV; ++i) {
+                const float y = (element<DT>(u, i) - m) * c, w = ex2_approx(y);
+                s += w;
+                e += w > 0.0f ? y * w : 0.0f * w;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+            e += __shfl_xor_sync(0xffffffffu, e, o);
+        }
+        __syncthreads();
+        if (lane == 0) sm.wpart[warp] = Part{0.0f, s, e, 0};
+        __syncthreads();
+        p.s = p.e = 0.0f;
+        for (int i = 0; i < kWarps; ++i) {
+            p.s += sm.wpart[i].s;
+            p.e += sm.wpart[i].e;
+        }
+    }
+    const float ln2 = 0.693147180559945309417f, lns = logf(p.s);
+    auto ln_p = [&](float x) -> float { return (x - m) / a.temperature - lns; };
+    const bool bad = !(p.s > 0.0f) || !isfinite(p.s) || m == -INFINITY;
+    if (tid == 0) {
+        if (bad) raise_status(a.status, kDevNonFinite);
+        a.logprob[entry] = bad ? NAN : ln_p(xt);
+        if (a.entropy) a.entropy[entry] = bad ? NAN : lns - ln2 * (p.e / p.s);
+        if (a.rank) a.rank[entry] = p.above;
+    }
+    if (tid < cpr * kMaxTopK && k > 0) {
+        const uint64_t key = sm.rtop[tid];
+        int r = 0;
+        if (key != 0ull)
+            for (int i = 0; i < cpr * kMaxTopK; ++i) r += sm.rtop[i] > key;
+        if (key != 0ull && r < k) {
+            a.alt_ids[static_cast<size_t>(entry) * k + r] = static_cast<int32_t>(key_id(key));
+            a.alt_logprobs[static_cast<size_t>(entry) * k + r] = bad ? NAN : ln_p(key_val(key));
+        }
+    }
+    if (tid < k && tid >= a.V) {  // alternatives past the row's entries
+        a.alt_ids[static_cast<size_t>(entry) * k + tid] = -1;
+        a.alt_logprobs[static_cast<size_t>(entry) * k + tid] = -INFINITY;
+    }
+}
+
+template <int DT>
+cudaError_t launch(const LogprobArgs& a, cudaStream_t stream) {
+    constexpr int ES = DT == 1 ? 2 : 4;
+    // CTAs per row: enough to fill the machine (four CTAs per SM) with the
+    // entries there are, at least one chunk each
+    const int max_cpr = std::max(1, std::min<int>(kMaxChunks, static_cast<int>(static_cast<long>(a.V) * ES / kChunkBytes)));
+    int cpr = 1;
+    while (cpr * 2 <= max_cpr && static_cast<long>(a.n) * cpr < 152 * 4) cpr *= 2;
+    const int seg = row_seg_elems(a.V, ES, cpr);
+    const int nch = (seg * ES + kChunkBytes - 1) / kChunkBytes;
+    const int smem = a.n_alt > 0 ? nch * kThreads * (DT == 1 ? 2 : 4) : 0;
+    auto kernel = token_logprobs_kernel<DT>;
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.n) * cpr);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cpr;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    count_launch();
+    return cudaLaunchKernelEx(&cfg, kernel, a, cpr, seg, kLog2e / a.temperature);
+}
+
+}  // namespace
+
+cudaError_t launch_token_logprobs(const LogprobArgs& a, int dtype, cudaStream_t stream) {
+    return dtype == 1 ? launch<1>(a, stream) : launch<0>(a, stream);
+}
+
+}  // namespace eagle

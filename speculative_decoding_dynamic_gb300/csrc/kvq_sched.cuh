@@ -1,0 +1,219 @@
+// Work split of the attention over the 8-bit cache, shared by its two kernels
+// (k_kvq_decode.cu, k_kvq_attn.cu) and their merge. Not part of the public ABI.
+//
+// An item is one (sequence, KV head, row block) with all of the sequence's
+// keys in steps of `step` keys. The items of all sequences, laid end to end,
+// are one line of cost units: `ov` units for an item's start and end, then
+// one per step. Worker w takes the units [w chunk, (w+1) chunk), whatever the
+// lengths are, so ragged batches, single sequences and long contexts all fill
+// the machine; an item that a boundary cuts is finished from its pieces'
+// partial results (O, max, sum) by the merge kernel. A worker holds at most
+// two pieces of cut items: of the one it continues (slot 2w) and of the one
+// it begins (slot 2w + 1). The lengths are device data: every worker derives
+// the same line from them by itself.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "attn_common.cuh"
+#include "eagle_internal.cuh"
+#include "eagle_ws.h"
+
+namespace eagle {
+
+struct KvqSched {
+    const int32_t *prefix_len, *n_tree;  // n_tree may be NULL: T each
+    int B, T, max_len;
+    int per_seq;  // items of a sequence
+    int step, ov, workers, min_chunk;
+};
+
+struct KvqSeq {
+    int L, n, nkeys, nt, len;  // nkeys = nt = len = 0: lengths out of range
+};
+
+__device__ __forceinline__ KvqSeq kvq_seq(const KvqSched& s, int b) {
+    KvqSeq q;
+    q.L = __ldg(&s.prefix_len[b]);
+    q.n = s.n_tree ? __ldg(&s.n_tree[b]) : s.T;
+    const bool bad = q.L < 0 || q.L > s.max_len - s.T || q.n < 1 || q.n > s.T;
+    q.nkeys = bad ? 0 : q.L + q.n;
+    q.nt = (q.nkeys + s.step - 1) / s.step;
+    q.len = bad ? 0 : q.nt + s.ov;
+    return q;
+}
+
+// Total length of the line (whole warp).
+__device__ __forceinline__ long long kvq_total(const KvqSched& s) {
+    const int lane = threadIdx.x & 31;
+    long long t = 0;
+    for (int b = lane; b < s.B; b += 32) t += kvq_seq(s, b).len;
+    return static_cast<long long>(warp_sum_u64(static_cast<uint64_t>(t))) * s.per_seq;
+}
+
+__device__ __forceinline__ long long kvq_chunk(const KvqSched& s, long long total) {
+    const long long c = (total + s.workers - 1) / s.workers;
+    return c < s.min_chunk ? s.min_chunk : c;
+}
+
+// The sequence that holds unit pos < total, and the line's length before it (whole warp).
+__device__ __forceinline__ int kvq_find(const KvqSched& s, long long pos, long long* base) {
+    const int lane = threadIdx.x & 31;
+    long long before = 0;
+    for (int b0 = 0; b0 < s.B; b0 += 32) {
+        const int b = b0 + lane;
+        const long long own = b < s.B ? static_cast<long long>(kvq_seq(s, b).len) * s.per_seq : 0;
+        long long inc = own;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const uint64_t o = shfl_u64(static_cast<uint64_t>(inc), lane >= m ? lane - m : lane);
+            if (lane >= m) inc += static_cast<long long>(o);
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, before + inc > pos);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            *base = before + static_cast<long long>(shfl_u64(static_cast<uint64_t>(inc - own), l));
+            return b0 + l;
+        }
+        before += static_cast<long long>(shfl_u64(static_cast<uint64_t>(inc), 31));
+    }
+    *base = before;
+    return s.B;  // not reached for pos < total
+}
+
+// One piece: steps [t0, t1) of item `sub` of sequence b.
+struct KvqPiece {
+    int b, sub, L, n, nkeys, nt, t0, t1;
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
+    __device__ __forceinline__ int slot(int worker) const { return 2 * worker + (t0 == 0 ? 1 : 0); }
+};
+
+// A worker's pieces in order. init by a whole warp; next by any thread.
+struct KvqCursor {
+    long long pos, end, base;
+    int b;
+    KvqSeq q;
+    __device__ __forceinline__ void init(const KvqSched& s, int worker) {
+        const long long total = kvq_total(s), chunk = kvq_chunk(s, total);
+        pos = min(total, worker * chunk);
+        end = min(total, (worker + 1) * chunk);
+        base = 0;
+        b = 0;
+        if (pos < end) {
+            b = kvq_find(s, pos, &base);
+            q = kvq_seq(s, b);
+        }
+    }
+    __device__ __forceinline__ bool next(const KvqSched& s, KvqPiece& p) {
+        while (pos < end) {
+            const long long seq_end = base + static_cast<long long>(q.len) * s.per_seq;
+            if (pos >= seq_end) {  // the next sequence with keys (one exists: pos < end <= total)
+                base = seq_end;
+                do q = kvq_seq(s, ++b);
+                while (q.len == 0);
+                continue;
+            }
+            const int sub = static_cast<int>((pos - base) / q.len);
+            const long long g0 = base + static_cast<long long>(sub) * q.len;
+            const int from = static_cast<int>(pos - g0);
+            const int to = static_cast<int>(min(static_cast<long long>(q.len), end - g0));
+            pos = g0 + q.len;
+            p.b = b;
+            p.sub = sub;
+            p.L = q.L;
+            p.n = q.n;
+            p.nkeys = q.nkeys;
+            p.nt = q.nt;
+            p.t0 = max(0, from - s.ov);
+            p.t1 = max(0, to - s.ov);
+            if (p.t1 > p.t0) return true;
+        }
+        return false;
+    }
+};
+
+// Partial results of cut items: O [slot][row][128] (in units where O / sum is
+// the output), and (max in the log2 domain, sum) [slot][row][2].
+struct KvqPartials {
+    float* o;
+    float* ml;
+    int rows;  // rows of a piece
+};
+
+struct KvqMergeParams {
+    KvqSched s;
+    KvqPartials part;
+    int G, T, Hq, n_rb;
+    __nv_bfloat16* out;
+};
+cudaError_t launch_kvq_merge(const KvqMergeParams& p, cudaStream_t stream);
+
+// Zero rows of the sequences whose lengths are out of range (status 3), dealt
+// over the workers: `n` threads of a worker, this one the i-th.
+__device__ __forceinline__ void kvq_zero_bad(const KvqSched& s, int Hq, __nv_bfloat16* out, int* status, int worker,
+                                             int i, int n) {
+    for (int b = worker; b < s.B; b += s.workers) {
+        if (kvq_seq(s, b).len != 0) continue;
+        if (i == 0) raise_status(status, kDevBadIndex);
+        uint4* o = reinterpret_cast<uint4*>(out + static_cast<size_t>(b) * s.T * Hq * kKvqHeadDim);
+        const int nv = s.T * Hq * kKvqHeadDim / 8;
+        for (int e = i; e < nv; e += n) o[e] = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+// Two e4m3 codes (low and high byte of c) as a pair of fp16: exact.
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t c) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(c)));
+    return d;
+}
+// Two floats to a pair of fp16 (a in the low half), nearest even.
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    return d;
+}
+// 2^(e) for the power of two that brings a row's largest |q| into [2^to, 2^(to+1)): exponent field of the scale
+__device__ __forceinline__ float pow2_to(float amax, int to) {
+    const int e = static_cast<int>(__float_as_uint(amax) >> 23);  // biased; 0 for zero and subnormals
+    const int f = to + 254 - e;                                   // biased exponent of the scale
+    return __uint_as_float(static_cast<uint32_t>(max(1, min(f, 253))) << 23);
+}
+
+// A 4-D map of codes: (128 bytes of a head, head, position, sequence), 128-byte swizzle.
+inline bool make_map_codes(CUtensorMap* m, const void* base, const KvqDims& kv, int keys) {
+    auto fn = tensor_map_encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {kKvqHeadDim, static_cast<cuuint64_t>(kv.Hkv), static_cast<cuuint64_t>(kv.max_len),
+                                static_cast<cuuint64_t>(kv.B)};
+    // a single sequence's stride is never used: any valid one
+    const cuuint64_t strides[3] = {kKvqHeadDim, static_cast<cuuint64_t>(kv.pos_stride),
+                                   static_cast<cuuint64_t>(kv.B > 1 ? kv.seq_stride : kv.pos_stride)};
+    const cuuint32_t box[4] = {kKvqHeadDim, 1, static_cast<cuuint32_t>(keys), 1};
+    const cuuint32_t estride[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estride,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Few query rows per KV head: k_kvq_decode.cu.
+constexpr int kKvqDecodeRows = 16;
+constexpr int kKvqSms = 152;
+struct KvqAttnParams {
+    KvqSched s;
+    KvqPartials part;
+    int Hq, Hkv, G, n_rb, W;
+    int blk_shift;  // log2 of the positions of a scale block
+    int64_t s_seq, s_blk;
+    const float *k_scale, *v_scale;  // of this layer
+    const __nv_bfloat16* q;
+    const uint32_t* mask;  // may be NULL: slot i sees the slots 0..i
+    __nv_bfloat16* out;
+    int* status;
+    float scale_log2;  // log2(e) / sqrt(128)
+};
+cudaError_t launch_kvq_decode(const KvqDims& kv, const KvqAttnParams& p, const void* kbase, const void* vbase,
+                              cudaStream_t stream);
+KvqSched kvq_decode_sched(int B, int T, int max_len, int Hkv);
+
+}  // namespace eagle

@@ -67,11 +67,34 @@ class KvCfg(ctypes.Structure):
                 ("kv_stride", ctypes.c_int64), ("pos_stride", ctypes.c_int64)]
 
 
+class KvqCfg(ctypes.Structure):
+    """eagle_kvq_cfg (strides of codes in bytes, of scales in elements)."""
+    _fields_ = [("batch", ctypes.c_int), ("n_q_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("layers", ctypes.c_int), ("max_len", ctypes.c_int),
+                ("block", ctypes.c_int), ("dtype", ctypes.c_int), ("seq_stride", ctypes.c_int64),
+                ("layer_stride", ctypes.c_int64), ("kv_stride", ctypes.c_int64), ("pos_stride", ctypes.c_int64),
+                ("scale_seq_stride", ctypes.c_int64), ("scale_layer_stride", ctypes.c_int64),
+                ("scale_kv_stride", ctypes.c_int64), ("scale_block_stride", ctypes.c_int64)]
+
+    @property
+    def n_blocks(self) -> int:
+        return -(-self.max_len // self.block)
+
+    def extent(self, layers: int) -> tuple[int, int]:
+        """Bytes of codes and elements of scales that `layers` layers of the cache span."""
+        row = self.n_kv_heads * self.head_dim
+        return ((self.batch - 1) * self.seq_stride + (layers - 1) * self.layer_stride + self.kv_stride +
+                (self.max_len - 1) * self.pos_stride + row,
+                (self.batch - 1) * self.scale_seq_stride + (layers - 1) * self.scale_layer_stride +
+                self.scale_kv_stride + (self.n_blocks - 1) * self.scale_block_stride + self.n_kv_heads)
+
+
 _p = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
 _TP = ctypes.POINTER(TreeCfg)
 _KP = ctypes.POINTER(KvCfg)
+_QP = ctypes.POINTER(KvqCfg)
 
 _lib.eagle_workspace_bytes.argtypes = [_TP]
 _lib.eagle_workspace_bytes.restype = _sz
@@ -101,6 +124,15 @@ _lib.eagle_status_fetch.argtypes = [_p, ctypes.POINTER(ctypes.c_int), _p]
 _lib.eagle_tree_export.argtypes = [_TP, _p, _sz, _p, _p, _p, _p, _p, _p, _p, _p]
 _lib.eagle_verify_export.argtypes = [_TP, _p, _sz, _p, _p, _p, _p]
 _lib.eagle_test_sampling.argtypes = [_p, _p, _i, _p, _p, _p]
+_i64 = ctypes.c_int64
+_lib.eagle_kvq_store.argtypes = [_QP, _i, _i, _p, _p, _i64, _p, _p, _p, _p, _p, _p, _p]
+_lib.eagle_kvq_compact.argtypes = [_QP, _p, _p, _p, _p, _p, _i, _p, _p, _p]
+_lib.eagle_kvq_attention_workspace_bytes.argtypes = [_QP, _i]
+_lib.eagle_kvq_attention_workspace_bytes.restype = _sz
+_lib.eagle_kvq_tree_attention.argtypes = [_QP, _i, _p, _p, _p, _i, _p, _p, _p, _p, _p, _sz, _p]
+_lib.eagle_lmhead_quant.argtypes = [_TP, _p, _sz, _i, _i, _p, _p, _p, _p, _p]
+_lib.eagle_lmhead_quant_pack.argtypes = [_i, _i, _i, _p, _p, _p, _p]
+_lib.eagle_token_logprobs.argtypes = [_TP, _p, _sz, _i, _i, _i, _p, ctypes.c_float, _p, _p, _i, _p, _p, _p, _p, _p, _p]
 _lib.eagle_kernel_launches.restype = ctypes.c_uint64
 _lib.eagle_last_cuda_error.argtypes = [ctypes.POINTER(ctypes.c_char_p)]
 _lib.eagle_last_cuda_error.restype = _i
@@ -131,6 +163,28 @@ def _check(fn: str, rc: int) -> None:
 
 def _ws(ws) -> tuple[int, int]:
     return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _need(fn: str, name: str, t, dtypes, n: int) -> None:
+    """A tensor argument of `fn`: contiguous, on the current device, of one of `dtypes`, with at least n elements
+    (None and raw addresses pass: the library checks what it can of those)."""
+    if t is None or isinstance(t, int):
+        return
+    if t.dtype not in dtypes:
+        raise ValueError(f"{fn}: {name} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{fn}: {name} is on {t.device}, not on the current CUDA device")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} is not contiguous")
+    if t.numel() < n:
+        raise ValueError(f"{fn}: {name} has {t.numel()} elements, needs {n}")
+
+
+_I32 = (torch.int32,)
+_W32 = (torch.int32, torch.uint32)
+_F32 = (torch.float32,)
+_BF16 = (torch.bfloat16,)
+_CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
 def eagle_workspace_bytes(cfg: TreeCfg) -> int:
@@ -261,6 +315,121 @@ def eagle_kv_compact(kv, kv_cache, prefix_len, accept_len, accepted_slots, slots
     _check("eagle_kv_compact", _lib.eagle_kv_compact(ctypes.byref(kv), _ptr(kv_cache), _ptr(prefix_len),
                                                      _ptr(accept_len), _ptr(accepted_slots), slots_stride,
                                                      _ptr(new_len), _ptr(ws), _stream(stream)))
+
+
+def kvq_contiguous(batch, n_q_heads, n_kv_heads, head_dim, layers, max_len, block) -> KvqCfg:
+    """The 8-bit cache with codes [batch, layers, 2, max_len, n_kv_heads, head_dim] and scales
+    [batch, layers, 2, ceil(max_len / block), n_kv_heads], both contiguous."""
+    row, nb = n_kv_heads * head_dim, -(-max_len // block)
+    return KvqCfg(batch, n_q_heads, n_kv_heads, head_dim, layers, max_len, block, EAGLE_BF16,
+                  layers * 2 * max_len * row, 2 * max_len * row, max_len * row, row,
+                  layers * 2 * nb * n_kv_heads, 2 * nb * n_kv_heads, nb * n_kv_heads, n_kv_heads)
+
+
+def alloc_kvq(kv: KvqCfg, device="cuda") -> tuple[torch.Tensor, torch.Tensor]:
+    """Zeroed codes and scales of a contiguous 8-bit cache."""
+    shape = (kv.batch, kv.layers, 2)
+    return (torch.zeros(*shape, kv.max_len, kv.n_kv_heads, kv.head_dim, dtype=torch.uint8, device=device),
+            torch.zeros(*shape, kv.n_blocks, kv.n_kv_heads, dtype=torch.float32, device=device))
+
+
+def _need_kvq(fn: str, kv: KvqCfg, layers: int, codes, scales) -> None:
+    c, s = kv.extent(layers)
+    _need(fn, "codes", codes, _CODES, c)
+    _need(fn, "scales", scales, _F32, s)
+
+
+def eagle_kvq_store(kv, layer, T, k, v, row_stride, row_start, start, count, codes, scales, ws=None, stream=None):
+    fn = "eagle_kvq_store"
+    B = kv.batch
+    # dense rows: the last one reaches its heads' end (packed rows: the caller's row_start says how far)
+    rows = 0 if row_start is not None else (B * T - 1) * row_stride + kv.n_kv_heads * kv.head_dim
+    for name, t in (("k", k), ("v", v)):
+        if not isinstance(t, int) and t is not None and not t.is_contiguous():
+            t = t.as_strided((t.untyped_storage().nbytes() // t.element_size() - t.storage_offset(),), (1,))
+        _need(fn, name, t, _BF16, rows)
+    for name, t in (("row_start", row_start), ("start", start), ("count", count)):
+        _need(fn, name, t, _I32, B)
+    _need_kvq(fn, kv, layer + 1, codes, scales)
+    _check(fn, _lib.eagle_kvq_store(ctypes.byref(kv), layer, T, _ptr(k), _ptr(v), row_stride, _ptr(row_start),
+                                    _ptr(start), _ptr(count), _ptr(codes), _ptr(scales), _ptr(ws), _stream(stream)))
+
+
+def eagle_kvq_compact(kv, codes, scales, prefix_len, accept_len, accepted_slots, slots_stride, new_len, ws=None,
+                      stream=None):
+    fn = "eagle_kvq_compact"
+    B = kv.batch
+    for name, t in (("prefix_len", prefix_len), ("accept_len", accept_len), ("new_len", new_len)):
+        _need(fn, name, t, _I32, B)
+    _need(fn, "accepted_slots", accepted_slots, _I32, B * slots_stride)
+    if kv.layers > 0:
+        _need_kvq(fn, kv, kv.layers, codes, scales)
+    _check(fn, _lib.eagle_kvq_compact(ctypes.byref(kv), _ptr(codes), _ptr(scales), _ptr(prefix_len),
+                                      _ptr(accept_len), _ptr(accepted_slots), slots_stride, _ptr(new_len), _ptr(ws),
+                                      _stream(stream)))
+
+
+def eagle_kvq_attention_workspace_bytes(kv: KvqCfg, T: int) -> int:
+    return int(_lib.eagle_kvq_attention_workspace_bytes(ctypes.byref(kv), T))
+
+
+def eagle_kvq_tree_attention(kv, T, q, codes, scales, layer, prefix_len, mask, n_tree, out, ws, stream=None):
+    """Tree attention over the 8-bit cache; mask None: slot i sees slots 0..i (T = 1: a decode step)."""
+    fn = "eagle_kvq_tree_attention"
+    B = kv.batch
+    n = B * T * kv.n_q_heads * kv.head_dim
+    _need(fn, "q", q, _BF16, n)
+    _need(fn, "out", out, _BF16, n)
+    _need(fn, "prefix_len", prefix_len, _I32, B)
+    _need(fn, "n_tree", n_tree, _I32, B)
+    _need(fn, "mask", mask, _W32, B * T * ((T + 31) // 32))
+    _need_kvq(fn, kv, layer + 1, codes, scales)
+    _check(fn, _lib.eagle_kvq_tree_attention(ctypes.byref(kv), T, _ptr(q), _ptr(codes), _ptr(scales), layer,
+                                             _ptr(prefix_len), _ptr(mask), _ptr(n_tree), _ptr(out), *_ws(ws),
+                                             _stream(stream)))
+
+
+def _logit_dtypes(cfg):
+    return _BF16 if cfg.logit_dtype == EAGLE_BF16 else _F32
+
+
+def eagle_lmhead_quant(cfg, ws, hidden_dim, group, hidden, codes, scales, draft_logits, stream=None):
+    """LM-head logits from 4-bit weights with group scales (eagle_lmhead_quant_pack)."""
+    fn = "eagle_lmhead_quant"
+    M = cfg.batch * cfg.top_k
+    _need(fn, "hidden", hidden, _BF16, M * hidden_dim)
+    _need(fn, "codes", codes, (torch.uint8,), cfg.vocab * hidden_dim // 2)
+    _need(fn, "scales", scales, _BF16, cfg.vocab * hidden_dim // max(1, group))
+    _need(fn, "draft_logits", draft_logits, _logit_dtypes(cfg), M * cfg.vocab)
+    _check(fn, _lib.eagle_lmhead_quant(ctypes.byref(cfg), *_ws(ws), hidden_dim, group, _ptr(hidden), _ptr(codes),
+                                       _ptr(scales), _ptr(draft_logits), _stream(stream)))
+
+
+def eagle_lmhead_quant_pack(vocab, hidden_dim, group, weight, codes, scales, stream=None):
+    fn = "eagle_lmhead_quant_pack"
+    _need(fn, "weight", weight, _BF16, vocab * hidden_dim)
+    _need(fn, "codes", codes, (torch.uint8,), vocab * hidden_dim // 2)
+    _need(fn, "scales", scales, _BF16, vocab * hidden_dim // max(1, group))
+    _check(fn, _lib.eagle_lmhead_quant_pack(vocab, hidden_dim, group, _ptr(weight), _ptr(codes), _ptr(scales),
+                                            _stream(stream)))
+
+
+def eagle_token_logprobs(cfg, ws, n_seq, per_seq, rows_per_seq, logits, temperature, slots, tokens, n_alt, logprob,
+                         rank=None, entropy=None, alt_ids=None, alt_logprobs=None, stream=None):
+    """Log-probability, rank, entropy and top alternatives of given tokens (slots None: entry j reads row j)."""
+    fn = "eagle_token_logprobs"
+    n = n_seq * per_seq
+    _need(fn, "logits", logits, _logit_dtypes(cfg), n_seq * rows_per_seq * cfg.vocab)
+    for name, t in (("slots", slots), ("tokens", tokens), ("rank", rank)):
+        _need(fn, name, t, _I32, n)
+    for name, t in (("logprob", logprob), ("entropy", entropy)):
+        _need(fn, name, t, _F32, n)
+    _need(fn, "alt_ids", alt_ids, _I32, n * n_alt)
+    _need(fn, "alt_logprobs", alt_logprobs, _F32, n * n_alt)
+    _check(fn, _lib.eagle_token_logprobs(ctypes.byref(cfg), *_ws(ws), n_seq, per_seq, rows_per_seq, _ptr(logits),
+                                         float(temperature), _ptr(slots), _ptr(tokens), n_alt, _ptr(logprob),
+                                         _ptr(rank), _ptr(entropy), _ptr(alt_ids), _ptr(alt_logprobs),
+                                         _stream(stream)))
 
 
 def eagle_status_fetch(ws, stream=None) -> int:
