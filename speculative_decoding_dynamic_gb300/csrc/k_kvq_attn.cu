@@ -98,7 +98,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int worker = blockIdx.x;
-    pdl_launch_dependents();
     if (threadIdx.x == 0) {
         mbar_init(&bar_q, kSoftmaxThreads);
         for (int s = 0; s < kStages; ++s) {
@@ -121,6 +120,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     pdl_wait_prior();
+    pdl_launch_dependents();  // after the wait: the merge reads the lengths before its own
     KvqCursor cur;
     cur.init(p.s, worker);
     tc_fence_before();
@@ -293,18 +293,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const float* ks = p.k_scale + it.b * p.s_seq + hk;
             const float* vs = p.v_scale + it.b * p.s_seq + hk;
             const int last = (it.nkeys - 1) >> p.blk_shift;
-            float kc[2], vc[2], vm;  // of this thread's two 16-key groups; V's largest of the tile
+            // K's scales of this thread's two 16-key groups, V's of the tile's four: read a
+            // tile ahead and used only then (their latency is that of a miss)
+            float kc[2], vc[4];
             auto scales = [&](int j) {
-                float v4[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    v4[e] = __ldg(vs + min((j * kBN + 16 * e) >> p.blk_shift, last) * p.s_blk);
+                    vc[e] = __ldg(vs + min((j * kBN + 16 * e) >> p.blk_shift, last) * p.s_blk);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < 2; ++e)
                     kc[e] = __ldg(ks + min((j * kBN + 32 * h + 16 * e) >> p.blk_shift, last) * p.s_blk);
-                    vc[e] = h ? v4[2 + e] : v4[e];
-                }
-                vm = fmaxf(fmaxf(v4[0], v4[1]), fmaxf(v4[2], v4[3]));
             };
             scales(it.t0);
             float m_use = 0.0f, lh = 0.0f, sref = 0.0f;  // lh: this half's share of the row sum
@@ -313,7 +311,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 const int sb = t & 1;
                 const int key0 = j * kBN;
                 const uint32_t s_cols = tmem_s + sb * kBN;
-                const float k0 = kc[0] * fac, k1 = kc[1] * fac, v0 = vc[0], v1 = vc[1], vmax = vm;
+                const float k0 = kc[0] * fac, k1 = kc[1] * fac, v0 = h ? vc[2] : vc[0], v1 = h ? vc[3] : vc[1];
+                const float vmax = fmaxf(fmaxf(vc[0], vc[1]), fmaxf(vc[2], vc[3]));
                 if (j + 1 < it.t1) scales(j + 1);
                 // ---- V of this tile: 16 columns of two keys per thread, codes to fp16 ----
                 {

@@ -92,16 +92,24 @@ __global__ void __launch_bounds__(kStoreThreads) kvq_store_kernel(
     float* sp = scales + b * kv.s_seq + layer * kv.s_layer + which * kv.s_kv + blk * kv.s_blk + h;
     const bool merge = lo < p0;  // the block holds earlier positions
     const float s_old = live && merge ? *sp : 0.0f;
-    const int col = gt % 16;
+    // this thread's 16-byte column of rows gt / 16, gt / 16 + ROWS, ..
+    const int pos0 = lo + gt / 16, col = gt % 16;
+    const bool full = lo >= p0 && lo + BLK <= p0 + n;  // every position of the block is new
+    const uint4* in = reinterpret_cast<const uint4*>(src + (r0 + (pos0 - p0)) * row_stride + static_cast<int64_t>(h) * kD) + col;
+    const int64_t in_step = row_stride * ROWS / 8;
     uint4 x[8];
     uint32_t mx = 0u;  // packed largest |x| of two bf16 columns (a NaN is above infinity)
+    if (full && live) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i, in += in_step) x[i] = __ldcs(in);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i, in += in_step)
+            x[i] = live && static_cast<unsigned>(pos0 + i * ROWS - p0) < static_cast<unsigned>(n) ? __ldcs(in)
+                                                                                                   : make_uint4(0u, 0u, 0u, 0u);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int pos = lo + i * ROWS + gt / 16;
-        const bool in = live && pos >= p0 && pos < p0 + n;
-        x[i] = in ? __ldcs(reinterpret_cast<const uint4*>(src + (r0 + (pos - p0)) * row_stride +
-                                                          static_cast<int64_t>(h) * kD) + col)
-                  : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t m01 = __vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu);
         const uint32_t m23 = __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu);
         mx = __vmaxu2(mx, __vmaxu2(m01, m23));
@@ -122,38 +130,66 @@ __global__ void __launch_bounds__(kStoreThreads) kvq_store_kernel(
     float s = block_scale(__uint_as_float(am << 16));
     if (merge) s = fmaxf(s, s_old);
     if (gt == 0) *sp = s;
-    const bool exact = pow2(s);
-    const float inv = 1.0f / s;  // exact for a power of two (2^-126 .. 2^120)
+    const int64_t out_step = kv.pos_stride * ROWS / 8;
+    uint2* out = reinterpret_cast<uint2*>(dst + pos0 * kv.pos_stride) + col;
+    if (merge && s > s_old) {  // earlier tokens of the block, at the grown scale
+        const float ratio = __fdiv_rn(s_old, s);
+        uint2* w = out;
+        for (int i = 0; i < 8 && pos0 + i * ROWS < p0; ++i, w += out_step) {
+            const uint2 u = *w;
+            *w = make_uint2(rescale4(u.x, ratio), rescale4(u.y, ratio));
+        }
+    }
+    if (!pow2(s)) {  // an old scale from elsewhere: x / s as a division
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+            // x[i] by a select: an index that varies would put the array in local memory
+            uint4 u = x[0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int pos = lo + i * ROWS + gt / 16;
-        uint2* out = reinterpret_cast<uint2*>(dst + pos * kv.pos_stride) + col;
-        if (pos >= p0 && pos < p0 + n) {
-            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            for (int e = 1; e < 8; ++e)
+                if (i == e) u = x[e];
+            if (static_cast<unsigned>(pos0 + i * ROWS - p0) >= static_cast<unsigned>(n)) continue;
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
             uint32_t c[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float a = __uint_as_float(w[e] << 16), d = __uint_as_float(w[e] & 0xffff0000u);
-                c[e] = exact ? codes2(a * inv, d * inv) : codes2(__fdiv_rn(a, s), __fdiv_rn(d, s));
-            }
-            *out = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-        } else if (merge && pos < p0 && s > s_old) {  // earlier tokens of the block, at the grown scale
-            const float ratio = __fdiv_rn(s_old, s);
-            const uint2 w = *out;
-            *out = make_uint2(rescale4(w.x, ratio), rescale4(w.y, ratio));
+            for (int e = 0; e < 4; ++e)
+                c[e] = codes2(__fdiv_rn(__uint_as_float(w[e] << 16), s), __fdiv_rn(__uint_as_float(w[e] & 0xffff0000u), s));
+            out[i * out_step] = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
         }
+        return;
+    }
+    const float inv = 1.0f / s;  // exact for a power of two (2^-126 .. 2^120)
+    const uint64_t inv2 = f2_pack(inv, inv);
+#pragma unroll
+    for (int i = 0; i < 8; ++i, out += out_step) {
+        if (!full && static_cast<unsigned>(pos0 + i * ROWS - p0) >= static_cast<unsigned>(n)) continue;
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t c[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint64_t q = f2_mul(f2_pack(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u)), inv2);
+            c[e] = codes2(f2_lo(q), f2_hi(q));
+        }
+        *out = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
     }
 }
 
-constexpr int kMoveWarps = 4;
+constexpr int kMoveWarps = 2;
+constexpr int kMoveHeads = 4;          // heads of a warp, eight lanes each
 constexpr int kMaxAccept = kMaxDepth;  // a_b <= D <= 16 <= block: destinations span two blocks at most
 
-// One warp per (sequence, layer, K|V, head): a row of codes is 128 bytes, four
-// per lane. Every source row is in registers before the first store, and a
-// lane rewrites only bytes that it alone reads, so no barrier is needed. A
-// chain of dependent small loads (lengths, slots, rows and scales) and its
-// latency are the whole cost; the slots and the scales of all rows are loaded
-// by the lanes at once.
+// Sixteen codes moved to another scale.
+__device__ __forceinline__ uint4 rescale16(const uint4& u, float ratio) {
+    return make_uint4(rescale4(u.x, ratio), rescale4(u.y, ratio), rescale4(u.z, ratio), rescale4(u.w, ratio));
+}
+
+// One warp per (sequence, layer, K|V, four heads): a lane holds 16 bytes of a
+// row and every source row is in registers before the first store; a lane
+// rewrites only bytes that it alone reads, so no barrier is needed. The cost
+// is a chain of small loads (lengths and slots, then rows and scales) and
+// the number of warps that go through it: four heads per warp bring a batch
+// of 64 with 32 layers into one wave (one head per warp: 16.8 us; 4: see the
+// launch's note).
 __global__ void __launch_bounds__(kMoveWarps * 32) kvq_compact_kernel(
     KvqDims kv, unsigned char* __restrict__ codes, float* __restrict__ scales, const int32_t* __restrict__ prefix_len,
     const int32_t* __restrict__ accept_len, const int32_t* __restrict__ slots, int slots_stride,
@@ -161,14 +197,14 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kvq_compact_kernel(
     const int b = blockIdx.z;
     const int layer = blockIdx.y >> 1, which = blockIdx.y & 1;
     const int lane = threadIdx.x & 31;
-    const int h = blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
     pdl_launch_dependents();
     pdl_wait_prior();
     const int L = prefix_len[b], a = accept_len[b];
-    bool ok = a >= 0 && a <= kMaxAccept && a < slots_stride && L >= 0 && L < kv.max_len - a;
     // lane j holds row j: its slot, whether it moves
     int sj = lane;
-    if (ok && lane >= 1 && lane <= a) sj = slots[static_cast<int64_t>(b) * slots_stride + lane];
+    if (lane >= 1 && lane < min(slots_stride, kMaxAccept + 1)) sj = slots[static_cast<int64_t>(b) * slots_stride + lane];
+    if (lane > a) sj = lane;
+    bool ok = a >= 0 && a <= kMaxAccept && a < slots_stride && L >= 0 && L < kv.max_len - a;
     ok = ok && !__any_sync(0xffffffffu, lane >= 1 && lane <= a && (sj < lane || sj >= kv.max_len - L));
     const bool first = blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0;
     if (!ok) {
@@ -176,52 +212,65 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kvq_compact_kernel(
         return;
     }
     if (first) new_len[b] = L + a + 1;
-    if (h >= kv.Hkv) return;
     const unsigned moving = __ballot_sync(0xffffffffu, sj > lane);
     if (moving == 0u) return;
+    const int h = (blockIdx.x * kMoveWarps + (threadIdx.x >> 5)) * kMoveHeads + (lane >> 3);
+    const bool live = h < kv.Hkv;
+    const int q = lane & 7;
     unsigned char* col = codes + b * kv.seq_stride + layer * kv.layer_stride + which * kv.kv_stride +
-                         static_cast<int64_t>(h) * kD + lane * 4;
+                         static_cast<int64_t>(h) * kD + q * 16;
     float* sc = scales + b * kv.s_seq + layer * kv.s_layer + which * kv.s_kv + h;
-    uint32_t row[kMaxAccept];
+    uint4 row[kMaxAccept];
 #pragma unroll
     for (int j = 1; j <= kMaxAccept; ++j) {
         const int s = __shfl_sync(0xffffffffu, sj, j);
-        if (j <= a && s > j) row[j - 1] = *reinterpret_cast<const uint32_t*>(col + (L + s) * kv.pos_stride);
+        if (live && s > j) row[j - 1] = *reinterpret_cast<const uint4*>(col + (L + s) * kv.pos_stride);
     }
-    const bool mine = sj > lane;
-    const float s_src = mine ? sc[static_cast<int64_t>((L + sj) / kv.block) * kv.s_blk] : 0.0f;
+    // lane q of a head holds the scales of rows q + 1 and q + 9
     const int blk0 = (L + 1) / kv.block;
-    const int blk_of = (L + lane) / kv.block;  // block of this lane's destination
-    float s_new = 0.0f;  // the new scale of this lane's destination block
+    float had[2] = {0.0f, 0.0f}, s_src[2], s_new[2] = {0.0f, 0.0f};
+    int blk_of[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int j = q + 1 + 8 * e;
+        const int s = __shfl_sync(0xffffffffu, sj, j);
+        const bool moves = live && ((moving >> j) & 1u);
+        s_src[e] = moves ? sc[static_cast<int64_t>((L + s) / kv.block) * kv.s_blk] : 0.0f;
+        blk_of[e] = moves ? (L + j) / kv.block - blk0 : -1;
+        if (live && L + 1 + e * (kv.block - (L + 1) % kv.block) <= L + a)  // block blk0 + e holds a destination
+            had[e] = sc[static_cast<int64_t>(blk0 + e) * kv.s_blk];
+    }
+    float grown[2];  // the old scale over the new of the (up to two) destination blocks
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int blk = blk0 + i;
-        const unsigned into = __ballot_sync(0xffffffffu, mine && blk_of == blk);
-        if (into == 0u) continue;
-        const float had = sc[static_cast<int64_t>(blk) * kv.s_blk];
-        float s = mine && blk_of == blk ? s_src : 0.0f;
+        float s = fmaxf(blk_of[0] == i ? s_src[0] : 0.0f, blk_of[1] == i ? s_src[1] : 0.0f);
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, m));
-        s = fmaxf(s, had);
-        if (blk_of == blk) s_new = s;
-        if (s > had) {  // the block's scale grows: its other rows move to it
-            const float ratio = __fdiv_rn(had, s);
-            const int hi = min((blk + 1) * kv.block, L + a + 1);
-            for (int pos = blk * kv.block; pos < hi; ++pos) {
-                uint32_t* w = reinterpret_cast<uint32_t*>(col + pos * kv.pos_stride);
-                const int j = pos - L;
-                if (j < 1 || !((moving >> j) & 1u)) *w = rescale4(*w, ratio);
-            }
-            __syncwarp();
-            if (lane == 0) sc[static_cast<int64_t>(blk) * kv.s_blk] = s;
+        for (int m = 4; m > 0; m >>= 1) s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, m));
+        s = fmaxf(s, had[i]);
+        grown[i] = s > had[i] ? __fdiv_rn(had[i], s) : 1.0f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (blk_of[e] == i) s_new[e] = s;
+        if (q == 0 && s > had[i]) sc[static_cast<int64_t>(blk0 + i) * kv.s_blk] = s;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (!live || grown[i] == 1.0f) continue;  // uniform over a head's lanes
+        const int hi = min((blk0 + i + 1) * kv.block, L + a + 1);
+        for (int pos = (blk0 + i) * kv.block; pos < hi; ++pos) {  // the block's other rows move to its grown scale
+            const int j = pos - L;
+            if (j >= 1 && ((moving >> j) & 1u)) continue;
+            uint4* w = reinterpret_cast<uint4*>(col + pos * kv.pos_stride);
+            *w = rescale16(*w, grown[i]);
         }
     }
-    const float ratio = mine ? __fdiv_rn(s_src, s_new) : 1.0f;
+    const float ratio[2] = {blk_of[0] >= 0 ? __fdiv_rn(s_src[0], s_new[0]) : 1.0f,
+                            blk_of[1] >= 0 ? __fdiv_rn(s_src[1], s_new[1]) : 1.0f};
 #pragma unroll
     for (int j = 1; j <= kMaxAccept; ++j) {
-        const float r = __shfl_sync(0xffffffffu, ratio, j);
-        if ((moving >> j) & 1u)
-            *reinterpret_cast<uint32_t*>(col + (L + j) * kv.pos_stride) = r == 1.0f ? row[j - 1] : rescale4(row[j - 1], r);
+        const float r = __shfl_sync(0xffffffffu, ratio[(j - 1) >> 3], (lane & 24) + ((j - 1) & 7));
+        if (live && ((moving >> j) & 1u))
+            *reinterpret_cast<uint4*>(col + (L + j) * kv.pos_stride) = r == 1.0f ? row[j - 1] : rescale16(row[j - 1], r);
     }
 }
 
@@ -252,7 +301,8 @@ cudaError_t launch_kvq_store(const KvqDims& kv, int layer, int T, const void* k,
 cudaError_t launch_kvq_compact(const KvqDims& kv, void* codes, float* scales, const int32_t* prefix_len,
                                const int32_t* accept_len, const int32_t* slots, int slots_stride, int32_t* new_len,
                                int* status, cudaStream_t stream) {
-    const dim3 grid((kv.Hkv + kMoveWarps - 1) / kMoveWarps, kv.layers * 2, kv.B);
+    constexpr int per_cta = kMoveWarps * kMoveHeads;
+    const dim3 grid((kv.Hkv + per_cta - 1) / per_cta, kv.layers * 2, kv.B);
     return launch_pdl(kvq_compact_kernel, grid, dim3(kMoveWarps * 32), 0, stream, kv,
                       static_cast<unsigned char*>(codes), scales, prefix_len, accept_len, slots, slots_stride, new_len,
                       status);

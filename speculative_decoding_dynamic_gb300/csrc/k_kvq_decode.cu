@@ -71,8 +71,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         fence_mbar_init();
     }
     __syncwarp();
-    pdl_launch_dependents();
     pdl_wait_prior();
+    pdl_launch_dependents();  // after the wait: the merge reads the lengths before its own
     kvq_zero_bad(p.s, p.Hq, p.out, p.status, worker, lane, 32);
 
     KvqCursor cur, ahead;
@@ -320,86 +320,142 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 // ------------------------------------------------------------------ merge ---
 
 constexpr int kMergeWarps = 8;
+constexpr int kMergeAlone = 4;  // most pieces that one warp combines by itself
 
-// One CTA per (worker, group of rows): the worker that began a cut item
-// combines its pieces, O = sum_i 2^(m_i - M) O_i over sum_i 2^(m_i - M) l_i.
-// `wpr` warps share a row, each taking every wpr-th piece (many pieces and
-// few rows: a long context's decode); four columns per lane.
-__global__ void __launch_bounds__(kMergeWarps * 32) kvq_merge_kernel(KvqMergeParams p, int wpr) {
-    __shared__ float4 so[kMergeWarps][32];
-    __shared__ float sm[kMergeWarps], sl[kMergeWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int w = blockIdx.x;
-    pdl_launch_dependents();
-    pdl_wait_prior();
-    const long long total = kvq_total(p.s), chunk = kvq_chunk(p.s, total);
+// The cut item that worker w began: O = sum_i 2^(m_i - M) O_i over
+// sum_i 2^(m_i - M) l_i of its pieces i (worker w's in slot 2w + 1, w + i's in
+// slot 2 (w + i)).
+struct CutItem {
+    int np;  // pieces; 0: worker w began none that was cut
+    int b, sub, n;
+};
+
+__device__ __forceinline__ CutItem cut_item(const KvqSched& s, int w) {  // whole warp
+    CutItem c{0, 0, 0, 0};
+    const long long total = kvq_total(s), chunk = kvq_chunk(s, total);
     const long long end = (w + 1) * chunk;
-    if (w * chunk >= total || end >= total) return;  // the last worker's items end with it
+    if (w * chunk >= total || end >= total) return c;  // the last worker's items end with it
     long long base;
-    const int b = kvq_find(p.s, end - 1, &base);
-    const KvqSeq q = kvq_seq(p.s, b);
+    const int b = kvq_find(s, end - 1, &base);
+    const KvqSeq q = kvq_seq(s, b);
     const int sub = static_cast<int>((end - 1 - base) / q.len);
     const long long g0 = base + static_cast<long long>(sub) * q.len;
-    const long long t1 = end - g0 - p.s.ov, t0 = w * chunk - g0 - p.s.ov;
-    if (t1 <= 0 || t1 >= q.nt || t0 > 0) return;  // not cut, or begun by an earlier worker
-    const int np = static_cast<int>((g0 + p.s.ov + q.nt - 1) / chunk) - w + 1;
-    const int rpc = kMergeWarps / wpr;
-    const int r = blockIdx.y * rpc + warp / wpr;
-    const int hk = sub / p.n_rb, rb = sub - hk * p.n_rb;
-    const int row = rb * p.part.rows + r;  // row of the (sequence, KV head)
-    const bool mine = r < p.part.rows && row < p.G * p.T;
+    const long long t1 = end - g0 - s.ov, t0 = w * chunk - g0 - s.ov;
+    if (t1 <= 0 || t1 >= q.nt || t0 > 0) return c;  // not cut, or begun by an earlier worker
+    c.np = static_cast<int>((g0 + s.ov + q.nt - 1) / chunk) - w + 1;
+    c.b = b;
+    c.sub = sub;
+    c.n = q.n;
+    return c;
+}
+
+// Running combination of a row's pieces, four columns per lane.
+struct RowSum {
     float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (mine) {
-#pragma unroll 4
-        for (int i = warp % wpr; i < np; i += wpr) {
-            const size_t at = static_cast<size_t>(i == 0 ? 2 * w + 1 : 2 * (w + i)) * p.part.rows + r;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part.ml) + at);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part.o + at * kKvqHeadDim) + lane);
-            const float M = fmaxf(m, ml.x);  // -inf: the row saw nothing in the pieces so far (their O is 0)
-            const float a = m == -INFINITY ? 0.0f : ex2_approx(m - M), c = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - M);
-            m = M;
-            l = l * a + ml.y * c;
-            o = make_float4(o.x * a + x.x * c, o.y * a + x.y * c, o.z * a + x.z * c, o.w * a + x.w * c);
-        }
+    __device__ __forceinline__ void add(float pm, float pl, const float4& x) {
+        // a piece in which the row saw nothing: maximum -inf, O 0
+        const float M = fmaxf(m, pm);
+        const float a = m == -INFINITY ? 0.0f : ex2_approx(m - M), c = pm == -INFINITY ? 0.0f : ex2_approx(pm - M);
+        m = M;
+        l = l * a + pl * c;
+        o = make_float4(o.x * a + x.x * c, o.y * a + x.y * c, o.z * a + x.z * c, o.w * a + x.w * c);
     }
-    if (wpr > 1) {
-        so[warp][lane] = o;
-        if (lane == 0) {
-            sm[warp] = m;
-            sl[warp] = l;
-        }
-        __syncthreads();
-        if (warp % wpr != 0) return;
-        float M = m;
-        for (int i = 1; i < wpr; ++i) M = fmaxf(M, sm[warp + i]);
-        const float a = m == -INFINITY ? 0.0f : ex2_approx(m - M);
-        l *= a;
-        o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
-        for (int i = 1; i < wpr; ++i) {
-            if (sm[warp + i] == -INFINITY) continue;
-            const float c = ex2_approx(sm[warp + i] - M);
-            const float4 x = so[warp + i][lane];
-            l += sl[warp + i] * c;
-            o = make_float4(o.x + x.x * c, o.y + x.y * c, o.z + x.z * c, o.w + x.w * c);
-        }
-    }
-    if (!mine) return;
+};
+
+__device__ __forceinline__ void merge_store(const KvqMergeParams& p, const CutItem& c, int r, const RowSum& s, int lane) {
+    const int hk = c.sub / p.n_rb, row = (c.sub - hk * p.n_rb) * p.part.rows + r;
     const int slot = row / p.G;
-    const bool live = slot < q.n && l > 0.0f;
-    const float inv = live ? 1.0f / l : 0.0f;
+    if (slot >= p.T) return;  // past the (sequence, KV head)'s rows
+    const bool live = slot < c.n && s.l > 0.0f;
+    const float inv = live ? 1.0f / s.l : 0.0f;
     uint2* dst = reinterpret_cast<uint2*>(
-        p.out + ((static_cast<size_t>(b) * p.T + slot) * p.Hq + hk * p.G + (row - slot * p.G)) * kKvqHeadDim);
-    dst[lane] = live ? make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv)) : make_uint2(0u, 0u);
+        p.out + ((static_cast<size_t>(c.b) * p.T + slot) * p.Hq + static_cast<size_t>(hk) * p.G + (row - slot * p.G)) * kKvqHeadDim);
+    dst[lane] = live ? make_uint2(pack_bf16(s.o.x * inv, s.o.y * inv), pack_bf16(s.o.z * inv, s.o.w * inv))
+                     : make_uint2(0u, 0u);
+}
+
+// A CTA serves the items that eight neighbouring workers began (decode: few
+// rows) or one worker's (128 rows, blockIdx.y taking some of them). Which those are
+// comes from the lengths alone and is found while the attention kernel still
+// runs. With 128 rows a warp takes whole rows. Decode items of up to four pieces go
+// to one warp each; those of many (few long sequences) are shared by all
+// eight warps, row by row.
+__global__ void __launch_bounds__(kMergeWarps * 32) kvq_merge_kernel(KvqMergeParams p, int per_cta, int rows_per_cta) {
+    __shared__ CutItem items[kMergeWarps];
+    __shared__ float4 so[kMergeWarps][32];
+    __shared__ float2 sml[kMergeWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int w0 = blockIdx.x * per_cta;
+    if (warp < per_cta) {
+        const CutItem c = w0 + warp < p.s.workers ? cut_item(p.s, w0 + warp) : CutItem{0, 0, 0, 0};
+        if (lane == 0) items[warp] = c;
+    }
+    __syncthreads();
+    pdl_wait_prior();
+    pdl_launch_dependents();
+    const int r0 = blockIdx.y * rows_per_cta, r1 = min(p.part.rows, r0 + rows_per_cta);
+    const float2* ml = reinterpret_cast<const float2*>(p.part.ml);
+    const float4* po = reinterpret_cast<const float4*>(p.part.o);
+    auto slot_row = [&](int w, int i, int r) {
+        return static_cast<size_t>(i == 0 ? 2 * w + 1 : 2 * (w + i)) * p.part.rows + r;
+    };
+    const bool decode = per_cta > 1;
+    for (int e = 0; e < per_cta; ++e) {
+        const CutItem c = items[e];
+        if (c.np == 0 || (decode && (c.np > kMergeAlone || e != warp))) continue;
+        // decode: item e belongs to warp e; else its rows are dealt over the warps
+        for (int r = decode ? r0 : r0 + warp; r < r1; r += decode ? 1 : kMergeWarps) {
+            RowSum s;
+            for (int i0 = 0; i0 < c.np; i0 += kMergeAlone) {
+                float2 a[kMergeAlone];
+                float4 x[kMergeAlone];
+#pragma unroll
+                for (int i = 0; i < kMergeAlone; ++i) {
+                    if (i0 + i >= c.np) break;
+                    const size_t at = slot_row(w0 + e, i0 + i, r);
+                    a[i] = __ldcg(ml + at);
+                    x[i] = __ldcg(po + at * 32 + lane);
+                }
+#pragma unroll
+                for (int i = 0; i < kMergeAlone; ++i)
+                    if (i0 + i < c.np) s.add(a[i].x, a[i].y, x[i]);
+            }
+            merge_store(p, c, r, s, lane);
+        }
+    }
+    for (int e = 0; e < per_cta; ++e) {
+        const CutItem c = items[e];
+        if (!decode || c.np <= kMergeAlone) continue;  // uniform over the CTA
+        for (int r = r0; r < r1; ++r) {
+            RowSum s;
+#pragma unroll 4
+            for (int i = warp; i < c.np; i += kMergeWarps) {
+                const size_t at = slot_row(w0 + e, i, r);
+                const float2 a = __ldcg(ml + at);
+                const float4 x = __ldcg(po + at * 32 + lane);
+                s.add(a.x, a.y, x);
+            }
+            so[warp][lane] = s.o;
+            if (lane == 0) sml[warp] = make_float2(s.m, s.l);
+            __syncthreads();
+            if (warp == 0) {
+                for (int i = 1; i < kMergeWarps; ++i) s.add(sml[i].x, sml[i].y, so[i][lane]);
+                merge_store(p, c, r, s, lane);
+            }
+            __syncthreads();
+        }
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_kvq_merge(const KvqMergeParams& p, cudaStream_t stream) {
-    const int wpr = p.part.rows <= kKvqDecodeRows ? kMergeWarps : 1;
-    const int rpc = kMergeWarps / wpr;
-    return launch_pdl(kvq_merge_kernel, dim3(p.s.workers, (p.part.rows + rpc - 1) / rpc), dim3(kMergeWarps * 32), 0,
-                      stream, p, wpr);
+    const bool decode = p.part.rows <= kKvqDecodeRows;
+    const int per_cta = decode ? kMergeWarps : 1, rows_per_cta = decode ? p.part.rows : 32;
+    return launch_pdl(kvq_merge_kernel,
+                      dim3((p.s.workers + per_cta - 1) / per_cta, (p.part.rows + rows_per_cta - 1) / rows_per_cta),
+                      dim3(kMergeWarps * 32), 0, stream, p, per_cta, rows_per_cta);
 }
 
 KvqSched kvq_decode_sched(int B, int T, int max_len, int Hkv) {

@@ -51,7 +51,7 @@ constexpr int kMaxSmem = 227 * 1024 - 1024;  // dynamic, beside the barriers
 struct QuantParams {
     int M, V, H, n_slice;
     int rows;        // hidden rows of a pass (blockIdx.y takes rows [y * rows, ...))
-    int stages;
+    int stages, bufs;  // ring stages of an MMA warp; buffers of partial sums
     int hid_stride;  // bytes of a hidden row in shared memory
     const __nv_bfloat16* hidden;
     const __nv_bfloat16* scales;
@@ -84,6 +84,29 @@ __device__ __forceinline__ int entry0(int q, int t) {
     return GROUP == 128 ? t * 32 + q * 8 : GROUP == 64 ? (q >> 1) * 64 + t * 16 + (q & 1) * 8 : q * 32 + t * 8;
 }
 
+// A row's NG scales of a slice as one load.
+template <int NG>
+struct ScaleWord {
+    using type = unsigned short;
+};
+template <>
+struct ScaleWord<2> {
+    using type = uint32_t;
+};
+template <>
+struct ScaleWord<4> {
+    using type = uint2;
+};
+template <int NG>
+__device__ __forceinline__ float scale_of(const typename ScaleWord<NG>::type& w, int i) {
+    if constexpr (NG == 1) return __uint_as_float(static_cast<uint32_t>(w) << 16);
+    else if constexpr (NG == 2) return __uint_as_float(i ? (w & 0xffff0000u) : (w << 16));
+    else {
+        const uint32_t x = i < 2 ? w.x : w.y;
+        return __uint_as_float((i & 1) ? (x & 0xffff0000u) : (x << 16));
+    }
+}
+
 // RT: vocabulary rows of a tile; NT: n-tiles of eight hidden rows.
 template <int RT, int NT, int GROUP, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -95,15 +118,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int MT = RT / 16;
     constexpr int kStage = RT * kSliceBytes;
     constexpr int NG = kSlice / GROUP;  // groups of a slice
-    constexpr int RS = 8 * NT;          // columns of a partial row
+    using Scales = typename ScaleWord<NG>::type;
+    constexpr int CS = RT + 4;          // a column of partial sums, padded: no bank conflicts
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int m0 = blockIdx.y * p.rows;
     const int rows = min(p.rows, p.M - m0);
-    // tile partial sums: [buffer][warp][row][RS]
-    float* red = reinterpret_cast<float*>(smem);
-    unsigned char* ring = smem + 2 * kMmaWarps * RT * RS * 4 + warp * p.stages * kStage;  // MMA warps
-    unsigned char* hid = smem + 2 * kMmaWarps * RT * RS * 4 + kMmaWarps * p.stages * kStage;
+    // rings of the MMA warps; hidden rows; partial sums of a tile, [buffer][warp][hidden row][CS]
+    unsigned char* ring = smem + warp * p.stages * kStage;
+    unsigned char* hid = smem + kMmaWarps * p.stages * kStage;
+    float* red = reinterpret_cast<float*>(hid + p.rows * p.hid_stride);
     // this CTA's vocabulary rows, in units of 16
     const int units = (p.V + 15) / 16;
     const int u0 = static_cast<int>(static_cast<long>(units) * blockIdx.x / gridDim.x);
@@ -171,19 +195,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int a = 0; a < MT; ++a)
 #pragma unroll
                 for (int b = 0; b < NT; ++b) sum[a][b][0] = sum[a][b][1] = sum[a][b][2] = sum[a][b][3] = 0.0f;
+            // scales of rows g, g + 8 of every m-tile, a slice's NG together, read a slice ahead
+            const int last = (p.V - 1 - v - g) >> 3;  // rows past the vocabulary read its last one's
+            Scales next[2 * MT];
+            auto read_scales = [&](int slice) {
+                const __nv_bfloat16* src = p.scales + (static_cast<size_t>(v + g) * p.n_slice + slice) * NG;
+                const size_t step = static_cast<size_t>(8) * p.n_slice * NG;
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i) next[i] = __ldg(reinterpret_cast<const Scales*>(src + min(i, last) * step));
+            };
+            read_scales(min(warp, p.n_slice - 1));
             for (int slice = warp; slice < p.n_slice; slice += kMmaWarps) {
                 const int st = used % p.stages;
-                // scales of rows g, g + 8 of every m-tile (a row past the vocabulary reads the last one's)
-                float sc[MT][2][NG];
+                Scales sc[2 * MT];
 #pragma unroll
-                for (int a = 0; a < MT; ++a)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const __nv_bfloat16* src =
-                            p.scales + static_cast<size_t>(min(v + a * 16 + g + 8 * e, p.V - 1)) * (p.n_slice * NG) + slice * NG;
-#pragma unroll
-                        for (int q = 0; q < NG; ++q) sc[a][e][q] = __bfloat162float(__ldg(src + q));
-                    }
+                for (int i = 0; i < 2 * MT; ++i) sc[i] = next[i];
+                read_scales(min(slice + kMmaWarps, p.n_slice - 1));
                 if (ok && !__all_sync(0xffffffffu, mbar_wait_sleep(&bar_full[warp][st], (used / p.stages) & 1))) {
                     ok = false;
                     if (lane == 0) raise_status(p.status, kDevTimeout);
@@ -247,53 +274,54 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int b = 0; b < NT; ++b)
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) sum[a][b][e] = fmaf(acc[a][b][e], sc[a][e >> 1][gi], sum[a][b][e]);
+                                for (int e = 0; e < 4; ++e) sum[a][b][e] = fmaf(acc[a][b][e], scale_of<NG>(sc[2 * a + (e >> 1)], gi), sum[a][b][e]);
                     }
                 }
             }
             // the tile's partial sums to the adding warps
-            const int buf = tile & 1;
-            if (ok && tile >= 2 && !__all_sync(0xffffffffu, mbar_wait_sleep(&bar_red_empty[buf], ((tile >> 1) - 1) & 1))) {
+            const int buf = tile % p.bufs, turn = tile / p.bufs;
+            if (ok && turn > 0 && !__all_sync(0xffffffffu, mbar_wait_sleep(&bar_red_empty[buf], (turn - 1) & 1))) {
                 ok = false;
                 if (lane == 0) raise_status(p.status, kDevTimeout);
                 for (int f = used; f < filled; ++f) mbar_wait_sleep(&bar_full[warp][f % p.stages], (f / p.stages) & 1);
             }
-            float* dst = red + (buf * kMmaWarps + warp) * RT * RS;
+            float* dst = red + (buf * kMmaWarps + warp) * p.rows * CS + g;
             if (ok) {
 #pragma unroll
-                for (int a = 0; a < MT; ++a) {
-                    if (a >= mts) break;
+                for (int b = 0; b < NT; ++b)
 #pragma unroll
-                    for (int b = 0; b < NT; ++b)
+                    for (int x = 0; x < 2; ++x) {
+                        const int m = b * 8 + 2 * t + x;
+                        if (m >= rows) continue;
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            *reinterpret_cast<float2*>(dst + (a * 16 + g + 8 * e) * RS + b * 8 + 2 * t) =
-                                make_float2(sum[a][b][2 * e], sum[a][b][2 * e + 1]);
-                }
+                        for (int a = 0; a < MT; ++a)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) dst[m * CS + a * 16 + 8 * e] = sum[a][b][2 * e + x];
+                    }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_red_full[buf]);
         }
     } else {
         const int at = threadIdx.x - kMmaWarps * 32;
-        bool ok = true;
-        for (int tile = 0; ok && tile < n_tiles; ++tile) {
-            const int buf = tile & 1;
+        for (int tile = 0; tile < n_tiles; ++tile) {
+            const int buf = tile % p.bufs, turn = tile / p.bufs;
             const int v = v0 + tile * RT;
             const int nv = min(RT, min(v1, p.V) - v);  // rows of the tile inside the vocabulary (a multiple of 8)
-            if (!__all_sync(0xffffffffu, mbar_wait_sleep(&bar_red_full[buf], (tile >> 1) & 1))) {
+            if (!__all_sync(0xffffffffu, mbar_wait_sleep(&bar_red_full[buf], turn & 1))) {
                 if (lane == 0) raise_status(p.status, kDevTimeout);
                 break;
             }
-            const float* src = red + buf * kMmaWarps * RT * RS;
+            const float* src = red + buf * kMmaWarps * p.rows * CS;
             for (int i = at; i < rows * (RT / 2); i += kAddWarps * 32) {  // two vocabulary rows each
                 const int m = i / (RT / 2), r = (i - m * (RT / 2)) * 2;
                 if (r >= nv) continue;
                 float x = 0.0f, y = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kMmaWarps; ++w) {
-                    x += src[(w * RT + r) * RS + m];
-                    y += src[(w * RT + r + 1) * RS + m];
+                    const float2 s = *reinterpret_cast<const float2*>(src + (w * p.rows + m) * CS + r);
+                    x += s.x;
+                    y += s.y;
                 }
                 const size_t o = static_cast<size_t>(m0 + m) * p.V + v + r;
                 if (BF16) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + o) = pack_bf16(x, y);
@@ -318,9 +346,9 @@ bool make_map(CUtensorMap* m, const void* codes, int V, int H, int rows) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Shared memory of a pass of `rows` hidden rows with RT-row tiles and `stages` per ring.
-int smem_bytes(int rows, int H, int RT, int NT, int stages) {
-    return 2 * kMmaWarps * RT * 8 * NT * 4 + kMmaWarps * stages * RT * kSliceBytes + rows * (2 * H + 64) + 128;
+// Shared memory of a pass of `rows` hidden rows with RT-row tiles, `stages` per ring and `bufs` buffers of partial sums.
+int smem_bytes(int rows, int H, int RT, int stages, int bufs) {
+    return kMmaWarps * stages * RT * kSliceBytes + rows * (2 * H + 64) + bufs * kMmaWarps * rows * (RT + 4) * 4 + 128;
 }
 
 template <int RT, int NT, int GROUP, bool BF16>
@@ -393,24 +421,27 @@ cudaError_t launch_lmhead_quant(int M, int V, int H, int group, const void* hidd
     p.out = out;
     p.status = status;
     // Up to 16 hidden rows per pass, 8 when 16 (or all, if fewer) do not fit beside two stages
-    // of the ring; tiles of 64 vocabulary rows, 32 when 64 do not fit.
+    // of the rings; tiles of 64 vocabulary rows (a load of a hidden piece serves four MMAs), 32
+    // when 64 do not fit; a second buffer of partial sums and more stages where there is room.
     const bool bf16 = out_dtype == 1;
-    auto run = [&](int rows, int RT, int NT, auto fn, cudaError_t* e) -> bool {
-        int st = kMaxStages;
-        while (st >= 2 && smem_bytes(rows, H, RT, NT, st) > kMaxSmem) --st;
-        if (st < 2) return false;
+    auto run = [&](int rows, int RT, auto fn, cudaError_t* e) -> bool {
+        int st = 2, nb = 1;
+        if (smem_bytes(rows, H, RT, st, nb) > kMaxSmem) return false;
+        if (smem_bytes(rows, H, RT, st, 2) <= kMaxSmem) nb = 2;
+        while (st < kMaxStages && smem_bytes(rows, H, RT, st + 1, nb) <= kMaxSmem) ++st;
         p.rows = rows;
         p.stages = st;
-        *e = fn(p, group, bf16, codes, smem_bytes(rows, H, RT, NT, st), stream);
+        p.bufs = nb;
+        *e = fn(p, group, bf16, codes, smem_bytes(rows, H, RT, st, nb), stream);
         return true;
     };
     cudaError_t e = cudaErrorInvalidValue;
     if (M > 8) {
         const int rows = std::min(M, 16);
-        if (run(rows, 64, 2, launch_group<64, 2>, &e) || run(rows, 32, 2, launch_group<32, 2>, &e)) return e;
+        if (run(rows, 64, launch_group<64, 2>, &e) || run(rows, 32, launch_group<32, 2>, &e)) return e;
     }
     const int rows = std::min(M, 8);
-    if (run(rows, 64, 1, launch_group<64, 1>, &e) || run(rows, 32, 1, launch_group<32, 1>, &e)) return e;
+    if (run(rows, 64, launch_group<64, 1>, &e) || run(rows, 32, launch_group<32, 1>, &e)) return e;
     return e;
 }
 

@@ -47,7 +47,7 @@ struct Part {  // one CTA's share of a row
     int above;
 };
 struct Shared {
-    uint32_t wtop[kWarps][kMaxTopK];
+    alignas(16) uint32_t wtop[kWarps * kMaxTopK];
     unsigned long long keys[kKeys];
     unsigned long long red[kWarps];
     uint64_t ctop[kMaxTopK];
@@ -67,7 +67,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return d;
 }
 __device__ __forceinline__ __nv_bfloat162 bf2(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
-__device__ __forceinline__ uint32_t u32(__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
 template <int DT>
 __device__ __forceinline__ float vec_max(const uint4& u) {
@@ -89,21 +88,18 @@ __device__ __forceinline__ uint4 neg_inf() {
     return make_uint4(w, w, w, w);
 }
 
-// Entries of a vector above x: larger, or (or_equal) equal.
+// Entries of a vector above x.
 template <int DT>
-__device__ __forceinline__ int count_above(const uint4& u, float x, bool or_equal) {
+__device__ __forceinline__ int count_above(const uint4& u, float x) {
     if (DT == 1) {
-        const __nv_bfloat162 t = __float2bfloat162_rn(x);  // x is a bf16 value
-        __nv_bfloat162 n;
-        if (or_equal) n = __hadd2(__hadd2(__hge2(bf2(u.x), t), __hge2(bf2(u.y), t)), __hadd2(__hge2(bf2(u.z), t), __hge2(bf2(u.w), t)));
-        else n = __hadd2(__hadd2(__hgt2(bf2(u.x), t), __hgt2(bf2(u.y), t)), __hadd2(__hgt2(bf2(u.z), t), __hgt2(bf2(u.w), t)));
+        // x is a bf16 value, or the fp32 value below one: rounding it down to bf16 keeps the order of bf16 entries
+        const __nv_bfloat16 h = __float2bfloat16_rd(x);
+        const __nv_bfloat162 t = __halves2bfloat162(h, h);
+        const __nv_bfloat162 n =
+            __hadd2(__hadd2(__hgt2(bf2(u.x), t), __hgt2(bf2(u.y), t)), __hadd2(__hgt2(bf2(u.z), t), __hgt2(bf2(u.w), t)));
         return static_cast<int>(__low2float(n) + __high2float(n));
     }
-    const float v[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
-    int n = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) n += or_equal ? v[e] >= x : v[e] > x;
-    return n;
+    return (__uint_as_float(u.x) > x) + (__uint_as_float(u.y) > x) + (__uint_as_float(u.z) > x) + (__uint_as_float(u.w) > x);
 }
 
 // a <- a and b over the larger maximum.
@@ -157,6 +153,8 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
     const int nvec = n / EPV;
     const float xt = DT == 1 ? __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(row) + tok)) << 16)
                              : __ldg(reinterpret_cast<const float*>(row) + tok);
+    // x >= xt as x > xt_below, the next value down (both zeros are one value)
+    const float xt_below = xt == 0.0f ? __uint_as_float(0x80000001u) : o2f(f2o(xt) - 1u);
     if (tid == 0) {
         sm.nkeys = 0;
         sm.tau = 0u;
@@ -166,35 +164,42 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
     // ---- the pass ----
     Part my{-INFINITY, 0.0f, 0.0f, 0};
     float top = -INFINITY;  // this thread's largest element
-    for (int ch = 0; ch < nch; ++ch) {
+    const uint64_t c2 = f2_pack(c, c);
+    const int tokv = tok / EPV - first / EPV;  // the token's vector in this CTA's numbering (first is a multiple of EPV)
+    const uint4* in = vec + tid;
+    for (int ch = 0; ch < nch; ++ch, in += kVecs * kThreads) {
         uint4 u[kVecs];
+        const int v0 = ch * kVecs * kThreads + tid;
+        if ((ch + 1) * kVecs * kThreads <= nvec) {
 #pragma unroll
-        for (int q = 0; q < kVecs; ++q) {
-            const int v = (ch * kVecs + q) * kThreads + tid;
-            u[q] = v < nvec ? __ldg(vec + v) : neg_inf<DT>();
+            for (int q = 0; q < kVecs; ++q) u[q] = __ldg(in + q * kThreads);
+        } else {
+#pragma unroll
+            for (int q = 0; q < kVecs; ++q) u[q] = v0 + q * kThreads < nvec ? __ldg(in + q * kThreads) : neg_inf<DT>();
         }
         const float gm = fmaxf(fmaxf(vec_max<DT>(u[0]), vec_max<DT>(u[1])), fmaxf(vec_max<DT>(u[2]), vec_max<DT>(u[3])));
+        const bool any = v0 < nvec;
         top = fmaxf(top, gm);
-        const bool any = ch * kVecs * kThreads + tid < nvec;
         if (k > 0) {  // bf16 values are decided by the top half of their ordered bits
             if (DT == 1) reinterpret_cast<uint16_t*>(gmax_raw)[ch * kThreads + tid] = any ? f2o(gm) >> 16 : 0;
             else reinterpret_cast<uint32_t*>(gmax_raw)[ch * kThreads + tid] = any ? f2o(gm) : 0u;
         }
         if (!any) continue;
         if (gm >= xt) {
+            // vectors before the token's: larger or equal; after it: larger
 #pragma unroll
             for (int q = 0; q < kVecs; ++q) {
-                const int v = (ch * kVecs + q) * kThreads + tid;
-                const int id = first + v * EPV;
-                if (v >= nvec) break;  // fill
-                if (id + EPV <= tok || id > tok) {
-                    my.above += count_above<DT>(u[q], xt, id < tok);
-                } else {
+                const int v = v0 + q * kThreads;
+                if (v >= nvec) break;
+                if (v == tokv) {
 #pragma unroll
                     for (int e = 0; e < EPV; ++e) {
                         const float x = element<DT>(u[q], e);
-                        my.above += x > xt || (x == xt && id + e < tok);
+                        my.above += x > xt || (x == xt && first + v * EPV + e < tok);
                     }
+                } else {
+                    // nothing is below -inf: every entry before such a token is above it
+                    my.above += v < tokv && xt == -INFINITY ? EPV : count_above<DT>(u[q], v < tokv ? xt_below : xt);
                 }
             }
         }
@@ -202,29 +207,43 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
             const Part up{fmaxf(gm, kFloor), 0.0f, 0.0f, 0};
             join(my, up, c);
         }
-        const uint64_t c2 = f2_pack(c, c), m2 = f2_pack(-my.m, -my.m);
-        uint64_t s2 = 0ull, e2 = 0ull;
+        const uint64_t m2 = f2_pack(-my.m, -my.m);
+        // Sums of the group. Without the clamp first: y is then -inf for entries of -inf (or
+        // overflows), and y 2^y a NaN; only such a group is summed again with the clamp
+        // (vectors of a masked vocabulary, the row's last group).
+        float gs, ge;
+        auto sums = [&](bool clamp) {
+            uint64_t s2 = 0ull, e2 = 0ull;
 #pragma unroll
-        for (int q = 0; q < kVecs; ++q) {
-            const uint32_t w[4] = {u[q].x, u[q].y, u[q].z, u[q].w};
+            for (int q = 0; q < kVecs; ++q) {
+                const uint32_t w[4] = {u[q].x, u[q].y, u[q].z, u[q].w};
 #pragma unroll
-            for (int i = 0; i < EPV / 2; ++i) {
-                uint64_t x2;
-                if (DT == 1) {
-                    // vectors past the end are -inf: clamped like any other, they add 2^-huge = 0
-                    const uint32_t x = u32(__hmax2_nan(bf2(w[i]), __float2bfloat162_rn(kFloor)));
-                    x2 = f2_pack(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-                } else {
-                    x2 = f2_pack(max_nan(__uint_as_float(w[2 * i]), kFloor), max_nan(__uint_as_float(w[2 * i + 1]), kFloor));
+                for (int i = 0; i < EPV / 2; ++i) {
+                    float a, b;
+                    if (DT == 1) {
+                        a = __uint_as_float(w[i] << 16);
+                        b = __uint_as_float(w[i] & 0xffff0000u);
+                    } else {
+                        a = __uint_as_float(w[2 * i]);
+                        b = __uint_as_float(w[2 * i + 1]);
+                    }
+                    if (clamp) {
+                        a = max_nan(a, kFloor);
+                        b = max_nan(b, kFloor);
+                    }
+                    const uint64_t y = f2_mul(f2_add(f2_pack(a, b), m2), c2);
+                    const uint64_t p = f2_pack(ex2_approx(f2_lo(y)), ex2_approx(f2_hi(y)));
+                    s2 = f2_add(s2, p);
+                    e2 = f2_fma(y, p, e2);
                 }
-                const uint64_t y = f2_mul(f2_add(x2, m2), c2);
-                const uint64_t p = f2_pack(ex2_approx(f2_lo(y)), ex2_approx(f2_hi(y)));
-                s2 = f2_add(s2, p);
-                e2 = f2_fma(y, p, e2);
             }
-        }
-        my.s += f2_lo(s2) + f2_hi(s2);
-        my.e += f2_lo(e2) + f2_hi(e2);
+            gs = f2_lo(s2) + f2_hi(s2);
+            ge = f2_lo(e2) + f2_hi(e2);
+        };
+        sums(false);
+        if (ge != ge) sums(true);
+        my.s += gs;
+        my.e += ge;
     }
     // ---- this CTA's sums ----
     float wmx = top;
@@ -252,17 +271,19 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
                 const uint32_t o = __shfl_xor_sync(0xffffffffu, v, s);
                 v = (((lane & s) == 0) == ((lane & size) == 0)) ? max(o, v) : min(o, v);
             }
-        if (lane < kMaxTopK) sm.wtop[warp][lane] = lane < k ? v : 0u;
+        if (lane < k) sm.wtop[lane * kWarps + warp] = v;  // the warps' largest, then their second, ..
         __syncthreads();
-        if (tid < kWarps * kMaxTopK) {
-            const uint32_t x = (&sm.wtop[0][0])[tid];
+        if (tid < kWarps * k) {
+            const uint32_t x = sm.wtop[tid];
             if (x != 0u) {
-                int r = 0;
-                for (int i = 0; i < kWarps * kMaxTopK; ++i) {
-                    const uint32_t o = (&sm.wtop[0][0])[i];
-                    r += o > x || (o == x && i < tid);
+                int r = 0;  // values at or above x: tau is the largest x that k values reach
+                const uint4* w4 = reinterpret_cast<const uint4*>(sm.wtop);
+#pragma unroll 4
+                for (int i = 0; i < kWarps * k / 4; ++i) {
+                    const uint4 o = w4[i];
+                    r += (o.x >= x) + (o.y >= x) + (o.z >= x) + (o.w >= x);
                 }
-                if (r == k - 1) sm.tau = x;
+                if (r >= k) atomicMax(&sm.tau, x);
             }
         }
         __syncthreads();

@@ -165,25 +165,41 @@ def _ws(ws) -> tuple[int, int]:
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _need(fn: str, name: str, t, dtypes, n: int) -> None:
-    """A tensor argument of `fn`: contiguous, on the current device, of one of `dtypes`, with at least n elements
-    (None and raw addresses pass: the library checks what it can of those)."""
-    if t is None or isinstance(t, int):
+def _need(fn: str, name: str, t, dtypes, n: int, dev: int) -> None:
+    """A tensor argument of `fn`: contiguous, on device `dev` (the current one), of one of `dtypes`, with at least n
+    elements (None and raw addresses pass: the library checks what it can of those)."""
+    if t is None or type(t) is int:
+        return
+    if t.dtype in dtypes and t.get_device() == dev and t.is_contiguous() and t.numel() >= n:
         return
     if t.dtype not in dtypes:
         raise ValueError(f"{fn}: {name} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{fn}: {name} is on {t.device}, not on the current CUDA device")
     if not t.is_contiguous():
         raise ValueError(f"{fn}: {name} is not contiguous")
-    if t.numel() < n:
-        raise ValueError(f"{fn}: {name} has {t.numel()} elements, needs {n}")
+    raise ValueError(f"{fn}: {name} has {t.numel()} elements, needs {n}")
+
+
+def _device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+# the current stream's handle without a stream object around it: a third of a small call's time on the host
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, dev: int) -> int | None:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
 _I32 = (torch.int32,)
 _W32 = (torch.int32, torch.uint32)
 _F32 = (torch.float32,)
 _BF16 = (torch.bfloat16,)
+_U8 = (torch.uint8,)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
@@ -333,40 +349,41 @@ def alloc_kvq(kv: KvqCfg, device="cuda") -> tuple[torch.Tensor, torch.Tensor]:
             torch.zeros(*shape, kv.n_blocks, kv.n_kv_heads, dtype=torch.float32, device=device))
 
 
-def _need_kvq(fn: str, kv: KvqCfg, layers: int, codes, scales) -> None:
+def _need_kvq(fn: str, kv: KvqCfg, layers: int, codes, scales, dev: int) -> None:
     c, s = kv.extent(layers)
-    _need(fn, "codes", codes, _CODES, c)
-    _need(fn, "scales", scales, _F32, s)
+    _need(fn, "codes", codes, _CODES, c, dev)
+    _need(fn, "scales", scales, _F32, s, dev)
 
 
 def eagle_kvq_store(kv, layer, T, k, v, row_stride, row_start, start, count, codes, scales, ws=None, stream=None):
-    fn = "eagle_kvq_store"
-    B = kv.batch
+    fn, dev, B = "eagle_kvq_store", _device(), kv.batch
     # dense rows: the last one reaches its heads' end (packed rows: the caller's row_start says how far)
     rows = 0 if row_start is not None else (B * T - 1) * row_stride + kv.n_kv_heads * kv.head_dim
     for name, t in (("k", k), ("v", v)):
-        if not isinstance(t, int) and t is not None and not t.is_contiguous():
+        if isinstance(t, torch.Tensor) and not t.is_contiguous():  # a slice of fused rows: what lies behind its start
             t = t.as_strided((t.untyped_storage().nbytes() // t.element_size() - t.storage_offset(),), (1,))
-        _need(fn, name, t, _BF16, rows)
-    for name, t in (("row_start", row_start), ("start", start), ("count", count)):
-        _need(fn, name, t, _I32, B)
-    _need_kvq(fn, kv, layer + 1, codes, scales)
+        _need(fn, name, t, _BF16, rows, dev)
+    _need(fn, "row_start", row_start, _I32, B, dev)
+    _need(fn, "start", start, _I32, B, dev)
+    _need(fn, "count", count, _I32, B, dev)
+    _need_kvq(fn, kv, layer + 1, codes, scales, dev)
     _check(fn, _lib.eagle_kvq_store(ctypes.byref(kv), layer, T, _ptr(k), _ptr(v), row_stride, _ptr(row_start),
-                                    _ptr(start), _ptr(count), _ptr(codes), _ptr(scales), _ptr(ws), _stream(stream)))
+                                    _ptr(start), _ptr(count), _ptr(codes), _ptr(scales), _ptr(ws),
+                                    _stream_on(stream, dev)))
 
 
 def eagle_kvq_compact(kv, codes, scales, prefix_len, accept_len, accepted_slots, slots_stride, new_len, ws=None,
                       stream=None):
-    fn = "eagle_kvq_compact"
-    B = kv.batch
-    for name, t in (("prefix_len", prefix_len), ("accept_len", accept_len), ("new_len", new_len)):
-        _need(fn, name, t, _I32, B)
-    _need(fn, "accepted_slots", accepted_slots, _I32, B * slots_stride)
+    fn, dev, B = "eagle_kvq_compact", _device(), kv.batch
+    _need(fn, "prefix_len", prefix_len, _I32, B, dev)
+    _need(fn, "accept_len", accept_len, _I32, B, dev)
+    _need(fn, "new_len", new_len, _I32, B, dev)
+    _need(fn, "accepted_slots", accepted_slots, _I32, B * slots_stride, dev)
     if kv.layers > 0:
-        _need_kvq(fn, kv, kv.layers, codes, scales)
+        _need_kvq(fn, kv, kv.layers, codes, scales, dev)
     _check(fn, _lib.eagle_kvq_compact(ctypes.byref(kv), _ptr(codes), _ptr(scales), _ptr(prefix_len),
                                       _ptr(accept_len), _ptr(accepted_slots), slots_stride, _ptr(new_len), _ptr(ws),
-                                      _stream(stream)))
+                                      _stream_on(stream, dev)))
 
 
 def eagle_kvq_attention_workspace_bytes(kv: KvqCfg, T: int) -> int:
@@ -375,18 +392,17 @@ def eagle_kvq_attention_workspace_bytes(kv: KvqCfg, T: int) -> int:
 
 def eagle_kvq_tree_attention(kv, T, q, codes, scales, layer, prefix_len, mask, n_tree, out, ws, stream=None):
     """Tree attention over the 8-bit cache; mask None: slot i sees slots 0..i (T = 1: a decode step)."""
-    fn = "eagle_kvq_tree_attention"
-    B = kv.batch
+    fn, dev, B = "eagle_kvq_tree_attention", _device(), kv.batch
     n = B * T * kv.n_q_heads * kv.head_dim
-    _need(fn, "q", q, _BF16, n)
-    _need(fn, "out", out, _BF16, n)
-    _need(fn, "prefix_len", prefix_len, _I32, B)
-    _need(fn, "n_tree", n_tree, _I32, B)
-    _need(fn, "mask", mask, _W32, B * T * ((T + 31) // 32))
-    _need_kvq(fn, kv, layer + 1, codes, scales)
+    _need(fn, "q", q, _BF16, n, dev)
+    _need(fn, "out", out, _BF16, n, dev)
+    _need(fn, "prefix_len", prefix_len, _I32, B, dev)
+    _need(fn, "n_tree", n_tree, _I32, B, dev)
+    _need(fn, "mask", mask, _W32, B * T * ((T + 31) // 32), dev)
+    _need_kvq(fn, kv, layer + 1, codes, scales, dev)
     _check(fn, _lib.eagle_kvq_tree_attention(ctypes.byref(kv), T, _ptr(q), _ptr(codes), _ptr(scales), layer,
                                              _ptr(prefix_len), _ptr(mask), _ptr(n_tree), _ptr(out), *_ws(ws),
-                                             _stream(stream)))
+                                             _stream_on(stream, dev)))
 
 
 def _logit_dtypes(cfg):
@@ -395,41 +411,40 @@ def _logit_dtypes(cfg):
 
 def eagle_lmhead_quant(cfg, ws, hidden_dim, group, hidden, codes, scales, draft_logits, stream=None):
     """LM-head logits from 4-bit weights with group scales (eagle_lmhead_quant_pack)."""
-    fn = "eagle_lmhead_quant"
-    M = cfg.batch * cfg.top_k
-    _need(fn, "hidden", hidden, _BF16, M * hidden_dim)
-    _need(fn, "codes", codes, (torch.uint8,), cfg.vocab * hidden_dim // 2)
-    _need(fn, "scales", scales, _BF16, cfg.vocab * hidden_dim // max(1, group))
-    _need(fn, "draft_logits", draft_logits, _logit_dtypes(cfg), M * cfg.vocab)
+    fn, dev, M = "eagle_lmhead_quant", _device(), cfg.batch * cfg.top_k
+    _need(fn, "hidden", hidden, _BF16, M * hidden_dim, dev)
+    _need(fn, "codes", codes, _U8, cfg.vocab * hidden_dim // 2, dev)
+    _need(fn, "scales", scales, _BF16, cfg.vocab * hidden_dim // max(1, group), dev)
+    _need(fn, "draft_logits", draft_logits, _logit_dtypes(cfg), M * cfg.vocab, dev)
     _check(fn, _lib.eagle_lmhead_quant(ctypes.byref(cfg), *_ws(ws), hidden_dim, group, _ptr(hidden), _ptr(codes),
-                                       _ptr(scales), _ptr(draft_logits), _stream(stream)))
+                                       _ptr(scales), _ptr(draft_logits), _stream_on(stream, dev)))
 
 
 def eagle_lmhead_quant_pack(vocab, hidden_dim, group, weight, codes, scales, stream=None):
-    fn = "eagle_lmhead_quant_pack"
-    _need(fn, "weight", weight, _BF16, vocab * hidden_dim)
-    _need(fn, "codes", codes, (torch.uint8,), vocab * hidden_dim // 2)
-    _need(fn, "scales", scales, _BF16, vocab * hidden_dim // max(1, group))
+    fn, dev = "eagle_lmhead_quant_pack", _device()
+    _need(fn, "weight", weight, _BF16, vocab * hidden_dim, dev)
+    _need(fn, "codes", codes, _U8, vocab * hidden_dim // 2, dev)
+    _need(fn, "scales", scales, _BF16, vocab * hidden_dim // max(1, group), dev)
     _check(fn, _lib.eagle_lmhead_quant_pack(vocab, hidden_dim, group, _ptr(weight), _ptr(codes), _ptr(scales),
-                                            _stream(stream)))
+                                            _stream_on(stream, dev)))
 
 
 def eagle_token_logprobs(cfg, ws, n_seq, per_seq, rows_per_seq, logits, temperature, slots, tokens, n_alt, logprob,
                          rank=None, entropy=None, alt_ids=None, alt_logprobs=None, stream=None):
     """Log-probability, rank, entropy and top alternatives of given tokens (slots None: entry j reads row j)."""
-    fn = "eagle_token_logprobs"
-    n = n_seq * per_seq
-    _need(fn, "logits", logits, _logit_dtypes(cfg), n_seq * rows_per_seq * cfg.vocab)
-    for name, t in (("slots", slots), ("tokens", tokens), ("rank", rank)):
-        _need(fn, name, t, _I32, n)
-    for name, t in (("logprob", logprob), ("entropy", entropy)):
-        _need(fn, name, t, _F32, n)
-    _need(fn, "alt_ids", alt_ids, _I32, n * n_alt)
-    _need(fn, "alt_logprobs", alt_logprobs, _F32, n * n_alt)
+    fn, dev, n = "eagle_token_logprobs", _device(), n_seq * per_seq
+    _need(fn, "logits", logits, _logit_dtypes(cfg), n_seq * rows_per_seq * cfg.vocab, dev)
+    _need(fn, "slots", slots, _I32, n, dev)
+    _need(fn, "tokens", tokens, _I32, n, dev)
+    _need(fn, "logprob", logprob, _F32, n, dev)
+    _need(fn, "rank", rank, _I32, n, dev)
+    _need(fn, "entropy", entropy, _F32, n, dev)
+    _need(fn, "alt_ids", alt_ids, _I32, n * n_alt, dev)
+    _need(fn, "alt_logprobs", alt_logprobs, _F32, n * n_alt, dev)
     _check(fn, _lib.eagle_token_logprobs(ctypes.byref(cfg), *_ws(ws), n_seq, per_seq, rows_per_seq, _ptr(logits),
                                          float(temperature), _ptr(slots), _ptr(tokens), n_alt, _ptr(logprob),
                                          _ptr(rank), _ptr(entropy), _ptr(alt_ids), _ptr(alt_logprobs),
-                                         _stream(stream)))
+                                         _stream_on(stream, dev)))
 
 
 def eagle_status_fetch(ws, stream=None) -> int:
