@@ -3,59 +3,63 @@
 //
 // For sequence b and KV head hk the G = Hq/Hkv query heads of every tree slot
 // form G*T query rows (row r <-> slot r / G, head hk*G + r % G), in row blocks
-// of 128. A worker (one of two CTAs per SM) walks its pieces of (sequence,
-// head, row block) items (kvq_sched.cuh) in key tiles of 64; per tile t:
+// of 128. An item is a pair of row blocks with all keys; a worker (one CTA per
+// SM) walks its pieces of items (kvq_sched.cuh) in key tiles of 64. Per tile t
+// and row block g of the pair:
 //   S = q K^T        tcgen05.mma kind::f8f6f4 straight from the codes: a row
 //                    of q, scaled by a power of two to at most 256, is split
 //                    into two e4m3 operands q = hi + lo (eight significant
 //                    bits in all, those of bf16; elements below 2^-9 of the
 //                    row's largest lose some), two MMAs at twice the fp16
 //                    rate. K needs no conversion and its tile is half the size.
-//   P = softmax part eight warps, two threads per row (TMEM lane = row, 32 key
-//                    columns each): K's block scale and q's row scale, tree
-//                    mask, exponentials in the log2 domain against a reference
-//                    maximum, times V's block scale over a reference scale,
-//                    as fp16 pairs into tensor memory over the S buffer
+//   P = softmax part four warps, one thread per row (TMEM lane = row, 64 key
+//                    columns): K's block scale and q's row scale, tree mask,
+//                    exponentials in the log2 domain against a reference
+//                    maximum with V's block scale over a reference scale in
+//                    the exponent, as fp16 pairs into tensor memory over S
 //   O += P V         tcgen05.mma kind::f16, A = P from tensor memory, B = V as
-//                    fp16 in shared memory (MN-major), which the softmax warps
-//                    convert from the tile's codes (exact, one conversion per
-//                    two elements) before they wait for S. P in e4m3 would
-//                    spare that, at 2^-4 per weight instead of 2^-11.
+//                    fp16 in shared memory (MN-major), converted from the
+//                    tile's codes (exact, one conversion per two elements) by
+//                    four warps of their own, once for both row blocks. P in
+//                    e4m3 would spare that, at 2^-4 per weight instead of 2^-11.
 // The reference maximum (scale) is raised, and O and the row sum rescaled in
 // place, only when a tile's exceeds it by more than 2^8 (2^4), so the weights
-// stay below 2^12. S is double buffered, QK^T of tile t+1 runs while the
-// softmax works on tile t; the second CTA of the SM fills the tensor pipe
-// meanwhile. Codes arrive by TMA (128-byte swizzle) in rings of their own;
-// mbarriers order everything and every wait is bounded.
+// stay below 2^12. S is double buffered per row block: while one block's
+// softmax works, the tensor pipe serves the other and the next tile. q of the
+// next item is converted while the current one runs (double buffered). Codes
+// arrive by TMA (128-byte swizzle) in rings of their own; mbarriers order
+// everything and every wait is bounded.
+//
+// Bound by the tensor pipe: 2 x 64 x 128 x 128 multiply-adds per tile and row
+// block, about 630 cycles at the measured bf16 rate, against 256 for the
+// exponentials and about 300 of issue.
 
 #include "kvq_sched.cuh"
 
 #include <cmath>
-#include <mutex>
 
 namespace eagle {
 namespace {
 
 constexpr int kBM = 128;
 constexpr int kBN = 64;                  // keys per tile
+constexpr int kSub = kBN / 16;           // 16-key groups of a tile: each lies in one scale block
 constexpr int kHD = kKvqHeadDim;
-constexpr int kTileQ = kBM * kHD;        // 16 KB: one e4m3 part of q
+constexpr int kTileQ = kBM * kHD;        // 16 KB: one e4m3 part of a row block's q
 constexpr int kTile8 = kBN * kHD;        // 8 KB: a K or V tile of codes
 constexpr int kTileV = kBN * kHD * 2;    // 16 KB: V as fp16, two halves of 64 columns
 constexpr int kHalfV = kTileV / 2;
-constexpr int kStages = 2;               // code tiles in flight, K and V each
-constexpr int kSoftmaxWarps = 8;
-constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
-constexpr int kThreads = 64 + kSoftmaxThreads;  // warp 0 TMA, warp 1 MMA, warps 2..9 softmax
-constexpr int kCtasPerSm = 2;
-constexpr int kSmemQ = 0;                            // hi, lo
-constexpr int kSmemK = 2 * kTileQ;
-constexpr int kSmemV8 = kSmemK + kStages * kTile8;
-constexpr int kSmemV = kSmemV8 + kStages * kTile8;   // fp16 V of tile t at kSmemV + (t & 1) * kTileV
-constexpr int kSmemBytes = kSmemV + 2 * kTileV;      // 96 KB
-constexpr int kTmemCols = 256;  // S double buffer (2 x 64 columns; P over S), O (128)
-constexpr uint32_t kTmemO = 128;
-constexpr int kMaxW = kMaxSlots / 32;
+constexpr int kKStages = 3, kVStages = 2;  // code tiles in flight
+constexpr int kConvWarps = 4, kSoftmaxWarps = 8;
+constexpr int kWarpConv = 2, kWarpSoftmax = kWarpConv + kConvWarps;  // warp 0 TMA, warp 1 MMA
+constexpr int kThreads = 32 * (kWarpSoftmax + kSoftmaxWarps);
+constexpr int kSmemQ = 0;                                   // [item parity][row block][hi, lo]
+constexpr int kSmemK = 8 * kTileQ;
+constexpr int kSmemV8 = kSmemK + kKStages * kTile8;
+constexpr int kSmemV = kSmemV8 + kVStages * kTile8;         // fp16 V of tile t at kSmemV + (t & 1) * kTileV
+constexpr int kSmemFac = kSmemV + 2 * kTileV;               // [item parity][256] row factors
+constexpr int kSmemMask = kSmemFac + 2 * 2 * kBM * 4;       // [item parity][256][W] mask words
+constexpr int kTmemCols = 512;  // S of row block g, buffer b at 64 (2g + b) (P over it), O of block g at 256 + 128 g
 
 // kind::f8f6f4, both operands e4m3 (type 0), fp32 accumulate; kind::f16 with both fp16 (type 0).
 __host__ __device__ constexpr uint32_t idesc_type0(int M, int N, int b_mn_major) {
@@ -70,13 +74,11 @@ __device__ __forceinline__ void mma_f8(uint32_t tmem_d, uint64_t a, uint64_t b, 
         : "memory");
 }
 
-__device__ __forceinline__ void named_sync_softmax() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory"); }
-__device__ __forceinline__ void named_sync_pair(int q4) { asm volatile("bar.sync %0, 64;" ::"r"(2 + q4) : "memory"); }
-
-__device__ __forceinline__ float max16(const float* v) {
-    const float a = fmax3(v[0], v[1], v[2]), b = fmax3(v[3], v[4], v[5]), c = fmax3(v[6], v[7], v[8]);
-    const float d = fmax3(v[9], v[10], v[11]), e = fmax3(v[12], v[13], v[14]);
-    return fmaxf(fmax3(a, b, c), fmax3(d, e, v[15]));
+__device__ __forceinline__ float max16(const uint32_t* v) {
+    auto f = [&](int i) { return __uint_as_float(v[i]); };
+    const float a = fmax3(f(0), f(1), f(2)), b = fmax3(f(3), f(4), f(5)), c = fmax3(f(6), f(7), f(8));
+    const float d = fmax3(f(9), f(10), f(11)), e = fmax3(f(12), f(13), f(14));
+    return fmaxf(fmax3(a, b, c), fmax3(d, e, f(15)));
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low byte
@@ -85,31 +87,60 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low 
     return d;
 }
 
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+// A wait of a whole warp: every lane polls; after a first timeout later waits
+// are short, so that a failed launch still ends promptly (its results are
+// meaningless then and the status says so; every role keeps its own order of
+// arrivals, so nobody waits without bound).
+struct Waiter {
+    bool ok = true;
+    __device__ __forceinline__ void operator()(uint64_t* bar, int phase) {
+        if (!mbar_wait(bar, phase & 1, ok ? (1u << 21) : 64u)) ok = false;
+    }
+};
+
+// What the softmax needs of a tile's scales, per 16-key group.
+struct alignas(16) TileScales {
+    float k[kSub];   // K's scale
+    float lv[kSub];  // log2 of V's scale over the reference (at least 2^-24)
+    float iv[kSub];  // the reverse of that ratio
+    float alpha;     // O's factor when the reference was raised for this tile, else 1
+    float sref;      // the reference scale
+    float pad[2];
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
     kvq_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, KvqAttnParams p) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t bar_q, bar_k_full[kStages], bar_k_empty[kStages], bar_v_full[kStages], bar_v_empty[kStages],
-        bar_s_full[2], bar_p_full[2], bar_pv_done[2];
+    __shared__ uint64_t bar_q_full[2], bar_q_empty[2], bar_k_full[kKStages], bar_k_empty[kKStages],
+        bar_v8_full[kVStages], bar_v8_empty[kVStages], bar_v_full[2], bar_v_empty[2], bar_sc[2], bar_s_full[2][2],
+        bar_p_full[2][2], bar_pv_done[2][2];
     __shared__ uint32_t tmem_holder;
-    __shared__ float xch[2][2][kBM];  // [tile parity][column half][row]: per-tile row maxima
-    __shared__ float lsum[2][kBM];    // [column half][row]: row sums of a piece
+    __shared__ TileScales ts[2];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int worker = blockIdx.x;
     if (threadIdx.x == 0) {
-        mbar_init(&bar_q, kSoftmaxThreads);
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < kKStages; ++s) {
             mbar_init(&bar_k_full[s], 1);
             mbar_init(&bar_k_empty[s], 1);
-            mbar_init(&bar_v_full[s], 1);
-            mbar_init(&bar_v_empty[s], kSoftmaxWarps);
+        }
+        for (int s = 0; s < kVStages; ++s) {
+            mbar_init(&bar_v8_full[s], 1);
+            mbar_init(&bar_v8_empty[s], kConvWarps);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&bar_s_full[s], 1);
-            mbar_init(&bar_p_full[s], kSoftmaxThreads);
-            mbar_init(&bar_pv_done[s], 1);
+            mbar_init(&bar_q_full[s], kConvWarps);
+            mbar_init(&bar_q_empty[s], 1 + kSoftmaxWarps);
+            mbar_init(&bar_v_full[s], kConvWarps);
+            mbar_init(&bar_v_empty[s], 2);
+            mbar_init(&bar_sc[s], 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&bar_pv_done[s][b], 1);
+                mbar_init(&bar_s_full[s][b], 1);
+                mbar_init(&bar_p_full[s][b], 4);
+            }
         }
         fence_mbar_init();
     }
@@ -120,17 +151,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     pdl_wait_prior();
-    pdl_launch_dependents();  // after the wait: the merge reads the lengths before its own
+    pdl_launch_dependents();
     KvqCursor cur;
     cur.init(p.s, worker);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_holder;
-    const uint32_t tmem_s = tmem;           // S(t) at tmem_s + 64 (t & 1); P(t) over its first 32 columns
-    const uint32_t tmem_o = tmem + kTmemO;  // O
-    uint32_t* mask_sm = reinterpret_cast<uint32_t*>(smem + kSmemBytes);  // [row][W]: mask words of each row's slot
+    const int rows = p.G * p.s.T;
+    float* fac_sm = reinterpret_cast<float*>(smem + kSmemFac);
+    uint32_t* mask_sm = reinterpret_cast<uint32_t*>(smem + kSmemMask);
     KvqPiece it;
+    Waiter wait;
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producers ---
@@ -138,120 +170,139 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // done), lane 1 the V tiles (free once converted).
         if (lane < 2) {
             const bool is_k = lane == 0;
-            uint64_t* full = is_k ? bar_k_full : bar_v_full;
-            uint64_t* empty = is_k ? bar_k_empty : bar_v_empty;
+            uint64_t* full = is_k ? bar_k_full : bar_v8_full;
+            uint64_t* empty = is_k ? bar_k_empty : bar_v8_empty;
             const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+            const int ns = is_k ? kKStages : kVStages;
             int t = 0;
-            bool ok = true;
-            while (ok && cur.next(p.s, it)) {
-                const int hk = it.sub / p.n_rb;
+            while (wait.ok && cur.next(p.s, it)) {
+                const int hk = it.sub / p.n_items;
                 for (int j = it.t0; j < it.t1; ++j, ++t) {
-                    const int st = t % kStages;
-                    if (t >= kStages && !mbar_wait_sleep(&empty[st], ((t / kStages) - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
+                    const int st = t % ns;
+                    if (t >= ns) wait(&empty[st], t / ns - 1);
+                    if (!wait.ok) break;
                     mbar_arrive_expect_tx(&full[st], kTile8);
                     tma_load_4d(smem + (is_k ? kSmemK : kSmemV8) + st * kTile8, map, 0, hk, j * kBN, it.b, &full[st]);
                 }
             }
-            // the copies in flight land before the CTA's shared memory goes away
-            if (!ok) {
+            if (!wait.ok) {  // the copies in flight land before the CTA's shared memory goes away
                 raise_status(p.status, kDevTimeout);
-                for (int f = t > kStages ? t - kStages : 0; f < t; ++f)
-                    mbar_wait_sleep(&full[f % kStages], (f / kStages) & 1, 1u << 10);
+                for (int f = max(0, t - ns); f < t; ++f) wait(&full[f % ns], f / ns);
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issuer ---
-        // Tiles are numbered t over all of the worker's pieces. QK(t) goes
-        // into S buffer t & 1, whose previous content P(t-2) was read by
-        // PV(t-2), issued earlier (tcgen05.mma of one thread execute in issue
-        // order). Issue order QK(0) QK(1) PV(0) QK(2) PV(1) ... A piece's
-        // first PV overwrites O: the softmax threads have read the previous
-        // piece's O before they arrive for it.
+        // Tiles are numbered t over all of the worker's pieces, and tg per row
+        // block over those in which the block has rows. QK_g goes into S
+        // buffer tg & 1 of block g, over the P that PV_g(tg - 2) reads; the two
+        // are of different kinds and accumulators, which the pipe does not
+        // promise to run in order, so QK waits for that PV's completion. Issue
+        // order QK0(t) QK1(t) PV0(t-1) PV1(t-1) QK0(t+1) ...: the other block's
+        // MMA is in flight during the wait. A piece's first PV overwrites O: the
+        // softmax threads have read the previous piece's O before they arrive
+        // for it. A PV's completion is told on one of two barriers in turn: when
+        // the softmax waits for PV(tg) the one before may still be running,
+        // and a single barrier's parity would be taken for the phase before.
         if (lane == 0) {
             constexpr uint32_t id_qk = idesc_type0(kBM, kBN, 0);
             constexpr uint32_t id_pv = idesc_type0(kBM, kHD, 1);
-            const uint32_t aQ = smem_u32(smem + kSmemQ);
-            int t = 0, qi = 0;
-            bool ok = true;
-            auto issue_pv = [&](int tp, bool first) -> bool {
-                const int sb = tp & 1;
-                if (!mbar_wait_sleep(&bar_p_full[sb], (tp >> 1) & 1)) return false;  // P written, V converted
-                tc_fence_after();
-                const uint32_t aV = smem_u32(smem + kSmemV + sb * kTileV);
+            int t = 0, qi = 0, tg[2] = {0, 0};
+            while (cur.next(p.s, it)) {
+                const int nb = (it.sub % p.n_items) * 2 + 1 < (rows + kBM - 1) / kBM ? 2 : 1;  // row blocks of the item
+                const uint32_t aQ = smem_u32(smem + kSmemQ + (qi & 1) * 4 * kTileQ);
+                auto pv = [&](int tp, bool first) {  // tile tp; of each block its tile tg - 1
+                    wait(&bar_v_full[tp & 1], tp >> 1);
+                    const uint32_t aV = smem_u32(smem + kSmemV + (tp & 1) * kTileV);
 #pragma unroll
-                for (int kk = 0; kk < kBN / 16; ++kk)  // A = P from TMEM: 16 keys = 8 columns per MMA
-                    mma_bf16_ts(tmem_o, tmem_s + sb * kBN + kk * 8, smem_desc(aV + kk * 2048, kHalfV, 1024), id_pv,
-                                (!first || kk > 0) ? 1 : 0);
-                mma_commit(&bar_pv_done[sb]);
-                return true;
-            };
-            while (ok && cur.next(p.s, it)) {
-                if (!mbar_wait_sleep(&bar_q, qi & 1)) {
-                    ok = false;
-                    break;
-                }
-                ++qi;
-                for (int j = it.t0; ok && j < it.t1; ++j, ++t) {
-                    const int sb = t & 1, sk = t % kStages;
-                    ok = mbar_wait_sleep(&bar_k_full[sk], (t / kStages) & 1);
-                    if (!ok) break;
+                    for (int g = 0; g < 2; ++g) {
+                        if (g < nb) {
+                            const int u = tg[g] - 1;
+                            wait(&bar_p_full[g][u & 1], u >> 1);
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = 0; kk < kBN / 16; ++kk)  // A = P from TMEM: 16 keys = 8 columns per MMA
+                                mma_bf16_ts(tmem + 256 + 128 * g, tmem + 64 * (2 * g + (u & 1)) + kk * 8,
+                                            smem_desc(aV + kk * 2048, kHalfV, 1024), id_pv, (!first || kk > 0) ? 1 : 0);
+                            mma_commit(&bar_pv_done[g][u & 1]);
+                        }
+                        mma_commit(&bar_v_empty[tp & 1]);
+                    }
+                };
+                wait(&bar_q_full[qi & 1], qi >> 1);
+                for (int j = it.t0; j < it.t1; ++j, ++t) {
+                    const int sk = t % kKStages;
+                    wait(&bar_k_full[sk], t / kKStages);
                     tc_fence_after();
                     const uint32_t aK = smem_u32(smem + kSmemK + sk * kTile8);
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)  // hi (0..3), lo (4..7); 32 elements of the head dimension each
-                        mma_f8(tmem_s + sb * kBN, smem_desc(aQ + (kk >> 2) * kTileQ + (kk & 3) * 32, 16, 1024),
-                               smem_desc(aK + (kk & 3) * 32, 16, 1024), id_qk, kk > 0);
+                    for (int g = 0; g < 2; ++g) {
+                        if (g >= nb) break;
+                        if (tg[g] >= 2) wait(&bar_pv_done[g][tg[g] & 1], (tg[g] >> 1) - 1);
+                        const uint32_t d = tmem + 64 * (2 * g + (tg[g] & 1));
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)  // hi (0..3), lo (4..7); 32 elements of the head dimension each
+                            mma_f8(d, smem_desc(aQ + (2 * g + (kk >> 2)) * kTileQ + (kk & 3) * 32, 16, 1024),
+                                   smem_desc(aK + (kk & 3) * 32, 16, 1024), id_qk, kk > 0);
+                        mma_commit(&bar_s_full[g][tg[g] & 1]);
+                    }
                     mma_commit(&bar_k_empty[sk]);
-                    mma_commit(&bar_s_full[sb]);
-                    if (j > it.t0) ok = issue_pv(t - 1, j == it.t0 + 1);
+                    if (j == it.t1 - 1) mma_commit(&bar_q_empty[qi & 1]);
+                    if (j > it.t0) pv(t - 1, j == it.t0 + 1);
+                    tg[0] += 1;
+                    tg[1] += nb - 1;
                 }
-                if (ok) ok = issue_pv(t - 1, it.t1 - it.t0 == 1);
+                pv(t - 1, it.t1 - it.t0 == 1);
+                ++qi;
             }
-            if (!ok) raise_status(p.status, kDevTimeout);
+            if (!wait.ok) raise_status(p.status, kDevTimeout);
         }
-    } else {
-        // ------------------------------------------------------ softmax ---
-        // Warp w serves TMEM lane quarter w % 4 (rows 32 q4 ..) and key
-        // columns 32 h .. 32 h + 31 of each tile, h the warp's column half;
-        // the two threads of a row exchange row maxima through shared memory.
-        const int sw = warp - 2;
-        const int h = sw >> 2;            // column half
-        const int q4 = warp & 3;
-        const int r = (q4 << 5) | lane;   // row of the block = TMEM lane
-        const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
-        int t = 0;                        // tiles so far
-        bool ok = true;
-        kvq_zero_bad(p.s, p.Hq, p.out, p.status, worker, threadIdx.x - 64, kSoftmaxThreads);
-        while (cur.next(p.s, it)) {
-            const int hk = it.sub / p.n_rb, rb = it.sub - hk * p.n_rb;
-            const int row = rb * kBM + r;  // row of the (sequence, KV head)
-            const int i = row / p.G;       // its tree slot
-            const bool row_live = i < p.s.T;
-            // a lane quarter whose 32 rows are all past the problem's rows does no
-            // arithmetic on S (it still takes part in every barrier and conversion)
-            const bool quarter_live = rb * kBM + q4 * 32 < p.G * p.s.T;
-            const size_t qrow = ((static_cast<size_t>(it.b) * p.s.T + i) * p.Hq + static_cast<size_t>(hk) * p.G +
-                                 (row - i * p.G)) * kHD;
-            // ---- q: this thread's 64 elements as two e4m3 parts ----
-            float fac;  // a score in the log2 domain, without K's scale
-            {
-                const uint4* src = reinterpret_cast<const uint4*>(p.q + qrow + 64 * h);
+        __syncwarp();
+    } else if (warp < kWarpSoftmax) {
+        // ----------------------------------------------------- converters ---
+        // V codes to fp16, the tile's scales for the softmax, and q, row
+        // factors and mask words of the next item while the current one runs.
+        const int cw = warp - kWarpConv;
+        const int i = threadIdx.x - kWarpConv * 32;
+        float next = 0.0f;  // lanes 0..3 of the first warp: K's scales of the next tile's groups; 4..7: V's
+        auto read_scale = [&](const KvqPiece& a, int j) {
+            if (cw == 0 && lane < 2 * kSub) {
+                const int last = (a.nkeys - 1) >> p.blk_shift;
+                next = __ldg((lane < kSub ? p.k_scale : p.v_scale) + a.b * p.s_seq + a.sub / p.n_items +
+                             min((j * kBN + 16 * (lane & 3)) >> p.blk_shift, last) * p.s_blk);
+            }
+        };
+        auto convert_q = [&](const KvqPiece& a, int qi) {
+            if (qi >= 2) wait(&bar_q_empty[qi & 1], (qi >> 1) - 1);
+            const int hk = a.sub / p.n_items, row0 = (a.sub - hk * p.n_items) * 2 * kBM;
+            unsigned char* sq = smem + kSmemQ + (qi & 1) * 4 * kTileQ;
+            const int h = i & 1;
+            for (int r = i >> 1; r < 2 * kBM && row0 + (r & kBM) < rows; r += kConvWarps * 16) {  // half a row per thread
+                const int slot = (row0 + r) / p.G;
+                const bool live = slot < p.s.T;
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    p.q + ((static_cast<size_t>(a.b) * p.s.T + slot) * p.Hq + static_cast<size_t>(hk) * p.G +
+                           (row0 + r - slot * p.G)) * kHD + 64 * h);
                 uint4 u[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] = live ? __ldg(src + e) : make_uint4(0u, 0u, 0u, 0u);
+                for (int w = h; w < p.W; w += 2) {  // the row's mask words
+                    uint32_t m = 0u;
+                    if (live) {
+                        if (p.mask) m = __ldg(&p.mask[(static_cast<size_t>(a.b) * p.s.T + slot) * p.W + w]);
+                        else m = slot >= 32 * w + 31 ? ~0u : slot < 32 * w ? 0u : (2u << (slot - 32 * w)) - 1u;
+                    }
+                    mask_sm[((qi & 1) * 2 * kBM + r) * p.W + w] = m;
+                }
                 uint32_t mx = 0u;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    u[e] = row_live ? __ldg(src + e) : make_uint4(0u, 0u, 0u, 0u);
+                for (int e = 0; e < 8; ++e)
                     mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(u[e].x & 0x7fff7fffu, u[e].y & 0x7fff7fffu),
                                                __vmaxu2(u[e].z & 0x7fff7fffu, u[e].w & 0x7fff7fffu)));
-                }
-                xch[t & 1][h][r] = __uint_as_float(max(mx & 0xffffu, mx >> 16) << 16);
-                named_sync_pair(q4);
-                const float s = pow2_to(fmaxf(xch[t & 1][0][r], xch[t & 1][1][r]), 7);
-                fac = p.scale_log2 / s;
+                mx = max(mx & 0xffffu, mx >> 16);
+                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                const float s = pow2_to(__uint_as_float(mx << 16), 7);
+                if (h == 0) fac_sm[(qi & 1) * 2 * kBM + r] = p.scale_log2 / s;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {  // 16 elements: one 16-byte chunk of each part
                     uint32_t hi[4], lo[4];
@@ -268,232 +319,256 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         hi[e] = h0 | (h1 << 16);
                         lo[e] = e4m3x2(x[0] - b0.x, x[1] - b0.y) | (e4m3x2(x[2] - b1.x, x[3] - b1.y) << 16);
                     }
-                    unsigned char* dst = smem + kSmemQ + r * kHD + (((4 * h + c) ^ (r & 7)) << 4);
+                    unsigned char* dst = sq + (r >> 7) * 2 * kTileQ + (r & 127) * kHD + (((4 * h + c) ^ (r & 7)) << 4);
                     *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4*>(dst + kTileQ) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
-                fence_proxy_async_smem();  // the MMA reads q through the async proxy
-                mbar_arrive(&bar_q);
             }
-            if (h == 0) {  // the row's mask words
-#pragma unroll
-                for (int w = 0; w < kMaxW; ++w) {
-                    if (w >= p.W) break;
-                    uint32_t m = 0u;
-                    if (row_live) {
-                        if (p.mask) m = __ldg(&p.mask[(static_cast<size_t>(it.b) * p.s.T + i) * p.W + w]);
-                        else m = i >= 32 * w + 31 ? ~0u : i < 32 * w ? 0u : (2u << (i - 32 * w)) - 1u;
-                    }
-                    mask_sm[r * p.W + w] = m;
-                }
-            }
-            named_sync_softmax();
-            const uint32_t* mrow = mask_sm + r * p.W;
-            const int L = it.L, n = it.n;
-            const float* ks = p.k_scale + it.b * p.s_seq + hk;
-            const float* vs = p.v_scale + it.b * p.s_seq + hk;
-            const int last = (it.nkeys - 1) >> p.blk_shift;
-            // K's scales of this thread's two 16-key groups, V's of the tile's four: read a
-            // tile ahead and used only then (their latency is that of a miss)
-            float kc[2], vc[4];
-            auto scales = [&](int j) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    vc[e] = __ldg(vs + min((j * kBN + 16 * e) >> p.blk_shift, last) * p.s_blk);
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    kc[e] = __ldg(ks + min((j * kBN + 32 * h + 16 * e) >> p.blk_shift, last) * p.s_blk);
-            };
-            scales(it.t0);
-            float m_use = 0.0f, lh = 0.0f, sref = 0.0f;  // lh: this half's share of the row sum
-            bool seen = false;
+            fence_proxy_async_smem();  // the MMA reads q through the async proxy
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_q_full[qi & 1]);
+        };
+        int t = 0, qi = 0;
+        KvqPiece ahead;
+        bool more = cur.next(p.s, ahead);
+        if (more) {
+            read_scale(ahead, ahead.t0);
+            convert_q(ahead, 0);
+        }
+        while (more) {
+            it = ahead;
+            more = cur.next(p.s, ahead);
+            float sref = 0.0f;
             for (int j = it.t0; j < it.t1; ++j, ++t) {
-                const int sb = t & 1;
+                const int b = t & 1;
+                if (t >= 2) wait(&bar_v_empty[b], (t >> 1) - 1);
+                if (cw == 0) {
+                    // V's reference scale: the first tile's largest, raised by more than 2^4 only
+                    const float own = next;
+                    float vm = lane >= kSub && lane < 2 * kSub ? own : 0.0f;
+                    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+                    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+                    vm = __shfl_sync(0xffffffffu, vm, kSub);
+                    float alpha = 1.0f;
+                    if (vm > 16.0f * sref) {
+                        if (sref > 0.0f) alpha = sref / vm;
+                        sref = vm;
+                    }
+                    if (lane < kSub) ts[b].k[lane] = own;
+                    if (lane >= kSub && lane < 2 * kSub) {
+                        const float ratio = fmaxf(own / sref, 0x1p-24f);
+                        ts[b].lv[lane - kSub] = log2f(ratio);
+                        ts[b].iv[lane - kSub] = 1.0f / ratio;
+                    }
+                    if (lane == 0) {
+                        ts[b].alpha = alpha;
+                        ts[b].sref = sref;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar_sc[b]);
+                    if (j + 1 < it.t1) read_scale(it, j + 1);
+                    else if (more) read_scale(ahead, ahead.t0);
+                }
+                const int st = t % kVStages;
+                wait(&bar_v8_full[st], t / kVStages);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = lane + 32 * (e & 1), c16 = 2 * cw + (e >> 1);
+                    uint4 u = *reinterpret_cast<const uint4*>(smem + kSmemV8 + st * kTile8 + key * kHD + ((c16 ^ (key & 7)) << 4));
+                    // keys that no row can see may hold anything (even NaN): 0 * V has to stay 0
+                    if (j * kBN + key >= it.nkeys) u = make_uint4(0u, 0u, 0u, 0u);
+                    unsigned char* dst = smem + kSmemV + b * kTileV + (c16 >> 2) * kHalfV + key * 128;
+                    const int c = 2 * (c16 & 3);
+                    *reinterpret_cast<uint4*>(dst + ((c ^ (key & 7)) << 4)) =
+                        make_uint4(e4m3_to_f16x2(u.x), e4m3_to_f16x2(u.x >> 16), e4m3_to_f16x2(u.y), e4m3_to_f16x2(u.y >> 16));
+                    *reinterpret_cast<uint4*>(dst + (((c + 1) ^ (key & 7)) << 4)) =
+                        make_uint4(e4m3_to_f16x2(u.z), e4m3_to_f16x2(u.z >> 16), e4m3_to_f16x2(u.w), e4m3_to_f16x2(u.w >> 16));
+                }
+                fence_proxy_async_smem();  // the MMA reads V through the async proxy
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bar_v8_empty[st]);
+                    mbar_arrive(&bar_v_full[b]);
+                }
+                if (more && j == min(it.t0 + 1, it.t1 - 1)) convert_q(ahead, qi + 1);
+            }
+            ++qi;
+        }
+        if (!wait.ok) raise_status(p.status, kDevTimeout);
+    } else {
+        // ------------------------------------------------------ softmax ---
+        // Four warps per row block; warp w serves TMEM lane quarter w % 4, one
+        // thread per row.
+        const int g = (warp - kWarpSoftmax) >> 2;
+        const int q4 = warp & 3;
+        const int r = (q4 << 5) | lane;   // row of the block = TMEM lane
+        const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+        const uint32_t o_cols = tmem + 256 + 128 * g + lane_off;
+        int t = 0, tg = 0, qi = 0;
+        int4 cut = make_int4(0, 0, 0, 0);
+        kvq_zero_bad(p.s, p.Hq, p.out, p.status, worker, threadIdx.x - kWarpSoftmax * 32, kSoftmaxWarps * 32);
+        for (; cur.next(p.s, it); ++qi) {
+            if (it.np) cut = kvq_cut(it);
+            const int hk = it.sub / p.n_items, row0 = ((it.sub - hk * p.n_items) * 2 + g) * kBM;
+            const int nt = it.t1 - it.t0;
+            wait(&bar_q_full[qi & 1], qi >> 1);  // also keeps an idle block from arriving for a later item
+            __syncwarp();
+            if (row0 >= rows) {  // the last pair of an odd number of row blocks: nothing to do for this one
+                t += nt;
+                if (lane == 0) mbar_arrive(&bar_q_empty[qi & 1]);
+                continue;
+            }
+            const int row = row0 + r;      // row of the (sequence, KV head)
+            const int slot = row / p.G;    // its tree slot
+            const bool row_live = slot < p.s.T;
+            // a quarter whose 32 rows are all past the problem's rows does no arithmetic
+            const bool quarter_live = row0 + q4 * 32 < rows;
+            const float fac = fac_sm[(qi & 1) * 2 * kBM + g * kBM + r];
+            const uint32_t* mrow = mask_sm + ((qi & 1) * 2 * kBM + g * kBM + r) * p.W;
+            const int L = it.L, n = it.n;
+            float m_use = 0.0f, l = 0.0f, sref = 0.0f;
+            bool seen = false;
+            for (int j = it.t0; j < it.t1; ++j, ++t, ++tg) {
                 const int key0 = j * kBN;
-                const uint32_t s_cols = tmem_s + sb * kBN;
-                const float k0 = kc[0] * fac, k1 = kc[1] * fac, v0 = h ? vc[2] : vc[0], v1 = h ? vc[3] : vc[1];
-                const float vmax = fmaxf(fmaxf(vc[0], vc[1]), fmaxf(vc[2], vc[3]));
-                if (j + 1 < it.t1) scales(j + 1);
-                // ---- V of this tile: 16 columns of two keys per thread, codes to fp16 ----
-                {
-                    const int st = t % kStages;
-                    if (ok && (!__all_sync(0xffffffffu, mbar_wait_sleep(&bar_v_full[st], (t / kStages) & 1)) ||
-                               (t >= 2 && !__all_sync(0xffffffffu, mbar_wait_sleep(&bar_pv_done[sb], ((t >> 1) - 1) & 1)))))
-                        ok = false;
-                    if (ok) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int key = lane + 32 * e;
-                            uint4 u = *reinterpret_cast<const uint4*>(smem + kSmemV8 + st * kTile8 + key * kHD +
-                                                                      ((sw ^ (key & 7)) << 4));
-                            // keys that no row can see may hold anything (even NaN): 0 * V has to stay 0
-                            if (key0 + key >= it.nkeys) u = make_uint4(0u, 0u, 0u, 0u);
-                            unsigned char* dst = smem + kSmemV + sb * kTileV + (sw >> 2) * kHalfV + key * 128;
-                            const int c = 2 * (sw & 3);
-                            *reinterpret_cast<uint4*>(dst + ((c ^ (key & 7)) << 4)) =
-                                make_uint4(e4m3_to_f16x2(u.x & 0xffffu), e4m3_to_f16x2(u.x >> 16),
-                                           e4m3_to_f16x2(u.y & 0xffffu), e4m3_to_f16x2(u.y >> 16));
-                            *reinterpret_cast<uint4*>(dst + (((c + 1) ^ (key & 7)) << 4)) =
-                                make_uint4(e4m3_to_f16x2(u.z & 0xffffu), e4m3_to_f16x2(u.z >> 16),
-                                           e4m3_to_f16x2(u.w & 0xffffu), e4m3_to_f16x2(u.w >> 16));
-                        }
-                        fence_proxy_async_smem();  // the MMA reads V through the async proxy
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar_v_empty[st]);
-                    }
-                }
-                // After a timed-out wait a warp skips the work of the remaining tiles
-                // but still takes every named barrier, so the others never wait for
-                // it without bound.
-                if (ok && !__all_sync(0xffffffffu, mbar_wait_sleep(&bar_s_full[sb], (t >> 1) & 1))) ok = false;
+                const uint32_t s_cols = tmem + 64 * (2 * g + (tg & 1)) + lane_off;
+                wait(&bar_sc[t & 1], t >> 1);
+                wait(&bar_s_full[g][tg & 1], tg >> 1);
+                __syncwarp();
                 tc_fence_after();
-                float sv[32];
-                if (ok && quarter_live) {
-                    tmem_ld32(s_cols + lane_off + 32 * h, sv);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) sv[e] = -INFINITY;
-                }
-                // visibility of the half's 32 keys: prefix keys, then tree slots in mask row i
-                {
-                    const int kb = key0 + 32 * h;
-                    const int npre = L - kb;  // keys of the 32 inside the prefix
-                    if (npre < 32) {
-                        const uint32_t pre = npre > 0 ? (1u << npre) - 1u : 0u;
-                        const int j0 = kb - L;  // slot of the first key (may be negative)
-                        const int lo = j0 < 0 ? 0 : j0;
-                        const int w0 = lo >> 5, sh = lo & 31;
-                        uint32_t win = w0 < p.W ? mrow[w0] >> sh : 0u;
-                        if (sh && w0 + 1 < p.W) win |= mrow[w0 + 1] << (32 - sh);
-                        const int limit = n - lo;  // slots j >= n are never visible
-                        if (limit <= 0) win = 0u;
-                        else if (limit < 32) win &= (1u << limit) - 1u;
-                        uint32_t tree = j0 < 0 ? (win << (-j0 & 31)) : win;
-                        if (j0 <= -32) tree = 0u;
-                        const uint32_t vis = pre | tree;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) sv[e] = ((vis >> e) & 1u) ? sv[e] : -INFINITY;
-                    }
-                }
-                float mx = fmaxf(max16(sv) * k0, max16(sv + 16) * k1);  // the scales are positive
                 if (quarter_live) {
-                    xch[t & 1][h][r] = mx;
-                    tc_fence_before();
-                    named_sync_pair(q4);  // also: both halves have read S, so P may overwrite it
-                    tc_fence_after();
-                    mx = fmaxf(xch[t & 1][0][r], xch[t & 1][1][r]);
-                }
-                bool rescale = false;
-                float alpha = 1.0f;
-                if (mx > -INFINITY) {
-                    if (!seen) {
-                        m_use = mx;  // O and l are still zero for this piece
-                        seen = true;
-                    } else if (mx > m_use + 8.0f) {
-                        alpha = ex2_approx(m_use - mx);
-                        m_use = mx;
-                        rescale = true;
-                        lh *= alpha;
-                    }
-                }
-                if (vmax > 16.0f * sref) {  // uniform: the tile's largest V scale
-                    alpha *= sref / vmax;
-                    rescale = sref > 0.0f;
-                    sref = vmax;
-                }
-                if (!ok) continue;
-                if (quarter_live) {
-                    // p = 2^(s k - m_use), two per packed multiply-add; packed partial sums.
-                    // P(t) as fp16 pairs over S columns 16 h .. 16 h + 15 of this buffer.
-                    const uint64_t nm2 = f2_pack(-m_use, -m_use);
-                    const float rs = 1.0f / sref;
-                    uint64_t acc[2] = {0ull, 0ull};
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float kk = e < 16 ? k0 : k1, vv = (e < 16 ? v0 : v1) * rs;
-                        const uint64_t z = f2_fma(f2_pack(sv[e], sv[e + 1]), f2_pack(kk, kk), nm2);
-                        const uint64_t w = f2_pack(ex2_approx(f2_lo(z)), ex2_approx(f2_hi(z)));
-                        acc[(e >> 1) & 1] = f2_add(acc[(e >> 1) & 1], w);
-                        const uint64_t x = f2_mul(w, f2_pack(vv, vv));
-                        pk[e >> 1] = pack_f16(f2_lo(x), f2_hi(x));
-                    }
-                    tmem_st16(s_cols + lane_off + 16 * h, pk);
-                    const uint64_t s2 = f2_add(acc[0], acc[1]);
-                    lh += f2_lo(s2) + f2_hi(s2);
-                }
-                // Rescaling O needs PV(t-1) done (PV(t) waits for this thread's
-                // arrival below). tcgen05.ld/st are warp-collective: rescale if any
-                // row of the warp needs it (alpha = 1 for the others).
-                if (quarter_live && j > it.t0 && __any_sync(0xffffffffu, rescale)) {
-                    if (!__all_sync(0xffffffffu, mbar_wait_sleep(&bar_pv_done[sb ^ 1], ((t - 1) >> 1) & 1))) {
-                        ok = false;
-                    } else {
-                        tc_fence_after();
+                    const TileScales& sc = ts[t & 1];
+                    const float4 k4 = *reinterpret_cast<const float4*>(sc.k), lv4 = *reinterpret_cast<const float4*>(sc.lv);
+                    const float4 iv4 = *reinterpret_cast<const float4*>(sc.iv);
+                    const float k[kSub] = {k4.x * fac, k4.y * fac, k4.z * fac, k4.w * fac};
+                    const float lv[kSub] = {lv4.x, lv4.y, lv4.z, lv4.w}, iv[kSub] = {iv4.x, iv4.y, iv4.z, iv4.w};
+                    float alpha = sc.alpha;
+                    sref = sc.sref;
+                    uint32_t s[kBN];
+                    tmem_ld64(s_cols, s);
+                    // visibility of 32 keys at a time: prefix keys, then tree slots in the row's mask
+                    if (key0 + kBN > L) {
 #pragma unroll
                         for (int hq = 0; hq < 2; ++hq) {
+                            const int kb = key0 + 32 * hq;
+                            const int npre = min(32, L - kb);  // keys of the 32 inside the prefix
+                            const uint32_t pre = npre > 0 ? 0xffffffffu >> (32 - npre) : 0u;
+                            const int j0 = kb - L;  // slot of the first key (may be negative)
+                            const int lo = j0 < 0 ? 0 : j0;
+                            const int w0 = lo >> 5, sh = lo & 31;
+                            uint32_t win = w0 < p.W ? mrow[w0] >> sh : 0u;
+                            if (sh && w0 + 1 < p.W) win |= mrow[w0 + 1] << (32 - sh);
+                            const int limit = n - lo;  // slots j >= n are never visible
+                            if (limit <= 0) win = 0u;
+                            else if (limit < 32) win &= (1u << limit) - 1u;
+                            uint32_t tree = j0 < 0 ? (win << (-j0 & 31)) : win;
+                            if (j0 <= -32) tree = 0u;
+                            const uint32_t vis = pre | tree;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                s[32 * hq + e] = ((vis >> e) & 1u) ? s[32 * hq + e] : 0xff800000u;
+                        }
+                    }
+                    const float mx = fmaxf(fmaxf(max16(s) * k[0], max16(s + 16) * k[1]),
+                                           fmaxf(max16(s + 32) * k[2], max16(s + 48) * k[3]));  // the scales are positive
+                    bool rescale = alpha != 1.0f;
+                    if (mx > -INFINITY) {
+                        if (!seen) {
+                            m_use = mx;  // l is still zero (and so is the row of O)
+                            seen = true;
+                        } else if (mx > m_use + 8.0f) {
+                            const float a = ex2_approx(m_use - mx);
+                            m_use = mx;
+                            l *= a;
+                            alpha *= a;
+                            rescale = true;
+                        }
+                    }
+                    // P = 2^(s k - m_use + lv), two per packed multiply-add; the row sum takes the
+                    // reverse of V's ratio. P as fp16 pairs over the first 32 columns of S.
+#pragma unroll
+                    for (int q = 0; q < kSub; ++q) {
+                        const float c = lv[q] - m_use;
+                        const uint64_t k2 = f2_pack(k[q], k[q]), c2 = f2_pack(c, c);
+                        uint64_t acc = 0ull;
+                        uint32_t pk[8];
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const uint64_t sp = (static_cast<uint64_t>(s[16 * q + e + 1]) << 32) | s[16 * q + e];
+                            const uint64_t z = f2_fma(sp, k2, c2);
+                            const float w0 = ex2_approx(f2_lo(z)), w1 = ex2_approx(f2_hi(z));
+                            acc = e == 0 ? f2_pack(w0, w1) : f2_add(acc, f2_pack(w0, w1));
+                            pk[e >> 1] = pack_f16(w0, w1);
+                        }
+                        l = fmaf(f2_lo(acc) + f2_hi(acc), iv[q], l);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) s[8 * q + e] = pk[e];
+                    }
+                    tmem_st16(s_cols, s);
+                    tmem_st16(s_cols + 16, s + 16);
+                    // Rescaling O needs PV of the previous tile done (this tile's PV waits for
+                    // this warp's arrival below). tcgen05.ld/st are warp-collective: rescale if
+                    // any row of the warp needs it (alpha = 1 for the others).
+                    if (j > it.t0 && __any_sync(0xffffffffu, rescale)) {
+                        wait(&bar_pv_done[g][(tg - 1) & 1], (tg - 1) >> 1);
+                        __syncwarp();
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
                             float o[32];
-                            tmem_ld32(tmem_o + lane_off + 64 * h + 32 * hq, o);
+                            tmem_ld32(o_cols + 32 * c, o);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                            tmem_st32(tmem_o + lane_off + 64 * h + 32 * hq, o);
+                            tmem_st32(o_cols + 32 * c, o);
                         }
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(&bar_p_full[sb]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_p_full[g][tg & 1]);
             }
-            // the piece's last PV done: O final, q and the V buffers free
-            if (ok && !__all_sync(0xffffffffu, mbar_wait_sleep(&bar_pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1))) ok = false;
-            if (!ok) raise_status(p.status, kDevTimeout);
+            if (lane == 0) mbar_arrive(&bar_q_empty[qi & 1]);  // factors and masks read
             // ----------------------------------------------------- epilogue ---
-            // Thread (row r, half h) owns output columns 64 h .. 64 h + 63 of its row.
-            lsum[h][r] = lh;
-            named_sync_softmax();  // row sums of both halves; every mask row has been read
+            wait(&bar_pv_done[g][(tg - 1) & 1], (tg - 1) >> 1);
+            __syncwarp();
             tc_fence_after();
-            const float l = lsum[0][r] + lsum[1][r];
-            const bool any = row_live && quarter_live && seen && l > 0.0f && ok;
-            if (it.whole()) {
-                const bool live = any && i < n;  // unused slots: zeros
-                const float inv = live ? sref / l : 0.0f;
-                __nv_bfloat16* orow = p.out + qrow + 64 * h;
+            if (!quarter_live) continue;
+            const bool any = row_live && seen && l > 0.0f && wait.ok;
+            const bool whole = it.whole();
+            const bool live = any && (!whole || slot < n);  // unused slots: zeros
+            const float f = !live ? 0.0f : whole ? sref / l : sref;
+            const size_t at = static_cast<size_t>(it.slot(worker)) * p.part.rows + g * kBM + r;
+            __nv_bfloat16* orow = p.out + ((static_cast<size_t>(it.b) * p.s.T + slot) * p.Hq +
+                                           static_cast<size_t>(hk) * p.G + (row - slot * p.G)) * kHD;
+            float* prow = p.part.o + at * kHD;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                float o[32];
+                __syncwarp();
+                tmem_ld32(o_cols + 32 * c, o);
 #pragma unroll
-                for (int hq = 0; hq < 2; ++hq) {
-                    float o[32];
-                    tmem_ld32(tmem_o + lane_off + 64 * h + 32 * hq, o);
-                    if (!row_live) continue;
+                for (int e = 0; e < 32; ++e) o[e] = live ? o[e] * f : 0.0f;
+                if (!row_live) {  // past the (sequence, KV head)'s rows
+                } else if (whole) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint4 uo = make_uint4(0u, 0u, 0u, 0u);
-                        if (live)
-                            uo = make_uint4(pack_bf16(o[8 * q] * inv, o[8 * q + 1] * inv),
-                                            pack_bf16(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
-                                            pack_bf16(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
-                                            pack_bf16(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
-                        *reinterpret_cast<uint4*>(orow + 32 * hq + 8 * q) = uo;
-                    }
-                }
-            } else {
-                const size_t at = static_cast<size_t>(it.slot(worker)) * kBM + r;
-                float* po = p.part.o + at * kHD + 64 * h;
-#pragma unroll
-                for (int hq = 0; hq < 2; ++hq) {
-                    float o[32];
-                    tmem_ld32(tmem_o + lane_off + 64 * h + 32 * hq, o);
-                    if (!row_live) continue;
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint4*>(orow + 32 * c + 8 * q) =
+                            make_uint4(pack_bf16(o[8 * q], o[8 * q + 1]), pack_bf16(o[8 * q + 2], o[8 * q + 3]),
+                                       pack_bf16(o[8 * q + 4], o[8 * q + 5]), pack_bf16(o[8 * q + 6], o[8 * q + 7]));
+                } else {
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        *reinterpret_cast<float4*>(po + 32 * hq + 4 * q) =
-                            any ? make_float4(o[4 * q] * sref, o[4 * q + 1] * sref, o[4 * q + 2] * sref, o[4 * q + 3] * sref)
-                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        *reinterpret_cast<float4*>(prow + 32 * c + 4 * q) =
+                            make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
                 }
-                if (row_live && h == 0) {
-                    p.part.ml[2 * at] = any ? m_use : -INFINITY;
-                    p.part.ml[2 * at + 1] = any ? l : 0.0f;
-                }
+            }
+            if (!whole && row_live) {
+                p.part.ml[2 * at] = any ? m_use : -INFINITY;
+                p.part.ml[2 * at + 1] = any ? l : 0.0f;
             }
             tc_fence_before();
         }
+        if (!wait.ok) raise_status(p.status, kDevTimeout);
+        if (threadIdx.x == kWarpSoftmax * 32) p.part.cut[worker] = cut;
     }
     tc_fence_before();
     __syncthreads();
@@ -506,9 +581,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
 struct Plan {
     KvqSched s;
-    int G, n_rb, rows;
+    int G, n_items, rows;
     bool decode;
-    size_t off_ml, off_o, bytes;
+    size_t off_cut, off_ml, off_o, bytes;
 };
 
 // Up to 16 query rows per KV head: the decode kernel, a worker per warp;
@@ -517,18 +592,20 @@ struct Plan {
 Plan make_plan(const KvqDims& kv, int T) {
     Plan pl{};
     pl.G = kv.Hq / kv.Hkv;
-    pl.decode = static_cast<long>(pl.G) * T <= kKvqDecodeRows;
+    const int rows = pl.G * T;
+    pl.decode = rows <= kKvqDecodeRows;
     if (pl.decode) {
-        pl.n_rb = 1;
-        pl.rows = pl.G * T;
-        pl.s = kvq_decode_sched(kv.B, T, kv.max_len, kv.Hkv);
+        pl.n_items = 1;
+        pl.rows = rows;
+        pl.s = kvq_decode_sched(kv.B, T, kv.max_len, kv.Hkv, rows);
     } else {
-        pl.n_rb = (pl.G * T + kBM - 1) / kBM;
-        pl.rows = kBM;
-        pl.s = KvqSched{nullptr, nullptr, kv.B, T, kv.max_len, kv.Hkv * pl.n_rb, kBN, 3, kKvqSms * kCtasPerSm, 6};
+        pl.n_items = (rows + 2 * kBM - 1) / (2 * kBM);
+        pl.rows = 2 * kBM;
+        pl.s = KvqSched{nullptr, nullptr, kv.B, T, kv.max_len, kv.Hkv * pl.n_items, kBN, 3, kKvqSms, 5};
     }
     const size_t slots = 2 * static_cast<size_t>(pl.s.workers) * pl.rows;
-    pl.off_ml = 256;
+    pl.off_cut = 256;
+    pl.off_ml = align_up(pl.off_cut + pl.s.workers * sizeof(int4), 256);
     pl.off_o = align_up(pl.off_ml + slots * 2 * sizeof(float), 256);
     pl.bytes = align_up(pl.off_o + slots * kHD * sizeof(float), 256);
     return pl;
@@ -547,11 +624,12 @@ cudaError_t launch_kvq_attention(const KvqDims& kv, int T, const void* q, const 
     char* w = static_cast<char*>(ws);
     KvqAttnParams p{};
     p.s = pl.s;
-    p.part = KvqPartials{reinterpret_cast<float*>(w + pl.off_o), reinterpret_cast<float*>(w + pl.off_ml), pl.rows};
+    p.part = KvqPartials{reinterpret_cast<float*>(w + pl.off_o), reinterpret_cast<float*>(w + pl.off_ml),
+                         reinterpret_cast<int4*>(w + pl.off_cut), pl.rows};
     p.Hq = kv.Hq;
     p.Hkv = kv.Hkv;
     p.G = pl.G;
-    p.n_rb = pl.n_rb;
+    p.n_items = pl.n_items;
     p.W = (T + 31) / 32;
     p.blk_shift = kv.block == 16 ? 4 : kv.block == 32 ? 5 : kv.block == 64 ? 6 : 7;
     p.s_seq = kv.s_seq;
@@ -571,18 +649,13 @@ cudaError_t launch_kvq_attention(const KvqDims& kv, int T, const void* q, const 
     } else {
         CUtensorMap tk, tv;
         if (!make_map_codes(&tk, kbase, kv, kBN) || !make_map_codes(&tv, vbase, kv, kBN)) return cudaErrorInvalidValue;
-        const int dyn = kSmemBytes + kBM * p.W * 4 + 1024;  // stages, mask rows, alignment slack
+        const int dyn = kSmemMask + 2 * 2 * kBM * p.W * 4 + 1024;  // mask rows, alignment slack
         e = ensure_dyn_smem(reinterpret_cast<const void*>(kvq_attn_kernel), dyn);
         if (e != cudaSuccess) return e;
-        static std::once_flag carve;  // two CTAs per SM need the largest shared-memory carveout
-        std::call_once(carve, [] {
-            cudaFuncSetAttribute(reinterpret_cast<const void*>(kvq_attn_kernel),
-                                 cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-        });
         e = launch_pdl(kvq_attn_kernel, dim3(pl.s.workers), dim3(kThreads), dyn, stream, tk, tv, p);
     }
     if (e != cudaSuccess) return e;
-    return launch_kvq_merge(KvqMergeParams{pl.s, p.part, p.G, T, p.Hq, p.n_rb, p.out}, stream);
+    return launch_kvq_merge(KvqMergeParams{p.part, pl.s.workers, p.G, T, p.Hq, p.n_items, p.out}, stream);
 }
 
 }  // namespace eagle

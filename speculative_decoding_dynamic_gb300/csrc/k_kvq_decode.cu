@@ -8,11 +8,15 @@
 //   - a warp is a worker of the split (kvq_sched.cuh) and works alone: it
 //     streams its keys 32 at a time through its own ring of TMA tiles
 //     (4 KB of K, 4 KB of V a stage) and keeps the running maximum, sum and
-//     the 16 x 128 accumulator in registers. No barrier between warps.
+//     accumulator in registers. No barrier between warps.
+//   - the products run transposed, S^T = K q^T and O^T = V^T P^T, on mma.sync
+//     m16n8k16 with the cache as the 16-row operand: eight query rows are one
+//     n-tile (with q as the 16-row operand half of the products of a group of
+//     four heads would be empty rows: 42 against .. us, see below). tcgen05's
+//     128-row tile would need the operands as fp16 in shared memory, twice
+//     their bytes written and read again.
 //   - codes go from shared memory to fp16 fragments by one conversion per two
-//     elements (exact), and the products run on mma.sync m16n8k16: with at most
-//     16 rows the tcgen05 tile (128 rows) would be seven eighths empty, and the
-//     operands would have to be written back to shared memory as fp16.
+//     elements (exact); P^T is turned around in registers (movmatrix).
 //   - q is scaled per row by a power of two into fp16's range (exact but for
 //     elements below 2^-28 of the row's largest).
 //   - K's scale multiplies the scores; V's multiplies the softmax weights,
@@ -28,18 +32,27 @@ namespace eagle {
 namespace {
 
 constexpr int kStep = 32;                      // keys per stage
-constexpr int kStages = 3;
-constexpr int kWarps = 8;                      // workers per CTA, one CTA per SM
 constexpr int kTile = kStep * kKvqHeadDim;     // 4 KB
 constexpr int kStageBytes = 2 * kTile;
-constexpr int kSmem = kWarps * kStages * kStageBytes + 1024;
+// Up to eight rows: twelve warps of two stages; up to sixteen (twice the
+// accumulators): eight of three. 192 KB of ring either way.
+constexpr int warps_of(int NT) { return NT == 1 ? 12 : 8; }
+constexpr int stages_of(int NT) { return NT == 1 ? 2 : 3; }
+constexpr int kSmem = 192 * 1024 + 1024;
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
         "%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transpose of an 8 x 8 matrix of 16-bit elements held two per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
 }
 
 // 16 bf16 as fp16, scaled by a power of two.
@@ -55,13 +68,15 @@ __device__ __forceinline__ float absmax8(const uint4& u) {
     return __uint_as_float(max(m & 0xffffu, m >> 16) << 16);
 }
 
-__global__ void __launch_bounds__(kWarps * 32, 1)
+template <int NT>
+__global__ void __launch_bounds__(warps_of(NT) * 32, 1)
     kvq_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       KvqAttnParams p) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t bar[kWarps][kStages];
+    constexpr int kStages = stages_of(NT);
+    __shared__ uint64_t bar[warps_of(NT)][kStages];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int worker = warp * gridDim.x + blockIdx.x;  // neighbouring workers on different SMs
     const int g = lane >> 2, t = lane & 3;
@@ -72,7 +87,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
     __syncwarp();
     pdl_wait_prior();
-    pdl_launch_dependents();  // after the wait: the merge reads the lengths before its own
+    pdl_launch_dependents();
     kvq_zero_bad(p.s, p.Hq, p.out, p.status, worker, lane, 32);
 
     KvqCursor cur, ahead;
@@ -102,19 +117,22 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
     const int rows = p.G * p.s.T;
     bool ok = true;
+    int4 cut = make_int4(0, 0, 0, 0);
     KvqPiece it;
     while (cur.next(p.s, it)) {
+        if (it.np) cut = kvq_cut(it);
         const int hk = it.sub;
-        // q of rows g and g + 8 as A fragments, and the factor that takes a score to the log2 domain
-        uint32_t qa[8][4];
-        float fac[2];
-        uint32_t see[2];  // visible tree slots of the row's slot (T <= 16: one mask word)
+        // q rows 8 nt + g as B fragments; a score of row 8 nt + 2t + e to the log2 domain; that row's
+        // visible tree slots (T <= 16: one mask word)
+        uint32_t qb[NT][8][2];
+        float fac[NT][2];
+        uint32_t see[NT][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = g + 8 * e;
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = 8 * nt + g;
             const int slot = r / p.G;
             uint4 u[4] = {};
-            see[e] = 0u;
+            uint32_t vis = 0u;
             if (r < rows) {
                 const uint4* src = reinterpret_cast<const uint4*>(
                     p.q + ((static_cast<size_t>(it.b) * p.s.T + slot) * p.Hq + hk * p.G + (r - slot * p.G)) * kKvqHeadDim);
@@ -122,27 +140,38 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 u[1] = __ldg(src + 2 * t + 1);
                 u[2] = __ldg(src + 8 + 2 * t);
                 u[3] = __ldg(src + 8 + 2 * t + 1);
-                see[e] = p.mask ? __ldg(&p.mask[static_cast<size_t>(it.b) * p.s.T + slot]) : (2u << slot) - 1u;
-                see[e] &= (1u << it.n) - 1u;  // n <= 16
+                vis = p.mask ? __ldg(&p.mask[static_cast<size_t>(it.b) * p.s.T + slot]) : (2u << slot) - 1u;
+                vis &= (1u << it.n) - 1u;  // n <= 16
             }
             float am = fmaxf(fmaxf(absmax8(u[0]), absmax8(u[1])), fmaxf(absmax8(u[2]), absmax8(u[3])));
             am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
             am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
             const float s = pow2_to(am, 14);
-            fac[e] = p.scale_log2 / s;
             uint32_t d[16];
 #pragma unroll
             for (int i = 0; i < 4; ++i) q_to_f16(u[i], s, d + 4 * i);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {  // MMA i sums over bytes 4i..4i+3 of the lane's 32
-                qa[i][e] = d[2 * i];
-                qa[i][2 + e] = d[2 * i + 1];
+                qb[nt][i][0] = d[2 * i];
+                qb[nt][i][1] = d[2 * i + 1];
+            }
+            const float f = p.scale_log2 / s;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {  // row 2t + e is held by the lanes 4 (2t + e) ..
+                fac[nt][e] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + e));
+                see[nt][e] = __shfl_sync(0xffffffffu, vis, 4 * (2 * t + e));
             }
         }
-        float o[16][4];
+        float o[NT][8][4];  // columns 16 g + 2j (+ 1: [2], [3]) of rows 8 nt + 2t ([0], [2]) and 2t + 1
+        float m[NT][2], l[NT][2];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, sref = 0.0f;
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.0f;
+        }
+        float sref = 0.0f, inv_sref = 0.0f;
         // scales of a step's two 16-key halves, read a step ahead
         const float* ks = p.k_scale + it.b * p.s_seq + hk;
         const float* vs = p.v_scale + it.b * p.s_seq + hk;
@@ -162,91 +191,115 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             const unsigned char* sk = ring + st * kStageBytes;
             const unsigned char* sv = sk + kTile;
             const int key0 = step * kStep;
-            const float k0 = kc[0], k1 = kc[1], v0 = vc[0], v1 = vc[1];
+            const float kk[2] = {kc[0], kc[1]}, vv[2] = {vc[0], vc[1]};
             if (step + 1 < it.t1) scales(step + 1);
-            if (ok && !__all_sync(0xffffffffu, mbar_wait_sleep(&bar[warp][st], (used / kStages) & 1))) {
+            if (ok && !__all_sync(0xffffffffu, mbar_wait(&bar[warp][st], (used / kStages) & 1))) {
                 // a copy that never landed: no more reading, nothing is refilled,
                 // and the other copies land before shared memory goes away
                 ok = false;
                 if (lane == 0) raise_status(p.status, kDevTimeout);
-                for (int f = used + 1; f < filled; ++f) mbar_wait_sleep(&bar[warp][f % kStages], (f / kStages) & 1);
+                for (int f = used + 1; f < filled; ++f) mbar_wait(&bar[warp][f % kStages], (f / kStages) & 1);
             }
             ++used;
             if (!ok) continue;
-            // ---- scores: rows g, g + 8; keys 8 nt + 2t, + 1 ----
-            float s[4][4];
+            // ---- scores: keys 16 hf + g ([0], [1]) and + 8; rows 8 nt + 2t, + 1 ----
+            float s[2][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
-                const unsigned char* row = sk + (nt * 8 + g) * kKvqHeadDim;
+            for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) s[hf][nt][0] = s[hf][nt][1] = s[hf][nt][2] = s[hf][nt][3] = 0.0f;
+                const unsigned char* row = sk + (hf * 16 + g) * kKvqHeadDim;  // the swizzle of keys g and g + 8 is the same
                 const uint4 a = *reinterpret_cast<const uint4*>(row + ((t ^ g) << 4));
                 const uint4 b = *reinterpret_cast<const uint4*>(row + (((t + 4) ^ g) << 4));
+                const uint4 c = *reinterpret_cast<const uint4*>(row + 8 * kKvqHeadDim + ((t ^ g) << 4));
+                const uint4 d = *reinterpret_cast<const uint4*>(row + 8 * kKvqHeadDim + (((t + 4) ^ g) << 4));
                 const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                const uint32_t x[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    mma_f16(s[nt], qa[i], e4m3_to_f16x2(w[i] & 0xffffu), e4m3_to_f16x2(w[i] >> 16));
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t a0 = e4m3_to_f16x2(w[i]), a1 = e4m3_to_f16x2(x[i]);
+                    const uint32_t a2 = e4m3_to_f16x2(w[i] >> 16), a3 = e4m3_to_f16x2(x[i] >> 16);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(s[hf][nt], a0, a1, a2, a3, qb[nt][i][0], qb[nt][i][1]);
+                }
             }
-            const bool edge = key0 + kStep > it.L;
-            float mx[2] = {-INFINITY, -INFINITY};
+            // ---- log2 domain, tree mask, maxima ----
+            float mx[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                const float kk = nt < 2 ? k0 : k1;
+            for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = s[nt][e] * (kk * fac[e >> 1]);
-                    if (edge) {
-                        const int j = key0 + nt * 8 + 2 * t + (e & 1) - it.L;  // tree slot (< 0: prefix)
-                        if (j >= 0 && !(j < 32 && ((see[e >> 1] >> j) & 1u))) x = -INFINITY;
-                    }
-                    s[nt][e] = x;
-                    mx[e >> 1] = fmaxf(mx[e >> 1], x);
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[hf][nt][e] *= kk[hf] * fac[nt][e & 1];
+                if (key0 + kStep > it.L) {
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = key0 + hf * 16 + g + 8 * (e >> 1) - it.L;  // tree slot (< 0: prefix)
+                            if (j >= 0 && !(j < 32 && ((see[nt][e & 1] >> j) & 1u))) s[hf][nt][e] = -INFINITY;
+                        }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    mx[nt][e] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                 }
             }
             // ---- running maximum and reference V scale, raised only by more than 2^8 (2^4): weights stay below 2^12 ----
-            float al[2] = {1.0f, 1.0f};
+            float al[NT][2];
             bool raise = false;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-                mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-                if (mx[e] > m[e] + 8.0f || (m[e] == -INFINITY && mx[e] > -INFINITY)) {
-                    al[e] = m[e] == -INFINITY ? 0.0f : ex2_approx(m[e] - mx[e]);
-                    m[e] = mx[e];
-                    l[e] *= al[e];
-                    raise = true;
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    al[nt][e] = 1.0f;
+                    if (mx[nt][e] > m[nt][e] + 8.0f) {  // -inf at first
+                        al[nt][e] = m[nt][e] == -INFINITY ? 0.0f : ex2_approx(m[nt][e] - mx[nt][e]);
+                        m[nt][e] = mx[nt][e];
+                        l[nt][e] *= al[nt][e];
+                        raise = true;
+                    }
                 }
-            }
-            const float vm = fmaxf(v0, v1);
+            const float vm = fmaxf(vv[0], vv[1]);
             if (vm > 16.0f * sref) {  // uniform over the warp
                 const float r = sref / vm;
-                al[0] *= r;
-                al[1] *= r;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    al[nt][0] *= r;
+                    al[nt][1] *= r;
+                }
                 sref = vm;
+                inv_sref = 1.0f / vm;
                 raise = true;
             }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    o[j][0] *= al[0];
-                    o[j][1] *= al[0];
-                    o[j][2] *= al[1];
-                    o[j][3] *= al[1];
-                }
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[nt][j][e] *= al[nt][e & 1];
             }
-            const float rv[2] = {v0 / sref, v1 / sref};
-            const float mu[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
-            uint32_t pa[2][4];  // weights as A fragments, 16 keys each
+            // ---- weights, transposed into B fragments ----
+            uint32_t pb[2][NT][2];
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                float w[4];
+            for (int nt = 0; nt < NT; ++nt) {
+                const float mu[2] = {m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m[nt][1] == -INFINITY ? 0.0f : m[nt][1]};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    w[e] = ex2_approx(s[nt][e] - mu[e >> 1]);
-                    l[e >> 1] += w[e];
-                    w[e] *= rv[nt >> 1];
+                for (int hf = 0; hf < 2; ++hf) {
+                    const float rv = vv[hf] * inv_sref;
+                    float w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        w[e] = ex2_approx(s[hf][nt][e] - mu[e & 1]);
+                        l[nt][e & 1] += w[e];
+                    }
+                    pb[hf][nt][0] = transpose8(pack_f16(w[0] * rv, w[1] * rv));
+                    pb[hf][nt][1] = transpose8(pack_f16(w[2] * rv, w[3] * rv));
                 }
-                pa[nt >> 1][(nt & 1) * 2] = pack_f16(w[0], w[1]);
-                pa[nt >> 1][(nt & 1) * 2 + 1] = pack_f16(w[2], w[3]);
             }
             // ---- O += P V: keys 16 hf + {2t, 2t+1, 8+2t, 8+2t+1}, columns 16 g .. 16 g + 15 ----
             const bool tail = key0 + kStep > it.nkeys;
@@ -267,87 +320,67 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t a = __byte_perm(w[0][i], w[1][i], 0x5140), b = __byte_perm(w[2][i], w[3][i], 0x5140);
                     const uint32_t c = __byte_perm(w[0][i], w[1][i], 0x7362), d = __byte_perm(w[2][i], w[3][i], 0x7362);
-                    mma_f16(o[4 * i], pa[hf], e4m3_to_f16x2(a & 0xffffu), e4m3_to_f16x2(b & 0xffffu));
-                    mma_f16(o[4 * i + 1], pa[hf], e4m3_to_f16x2(a >> 16), e4m3_to_f16x2(b >> 16));
-                    mma_f16(o[4 * i + 2], pa[hf], e4m3_to_f16x2(c & 0xffffu), e4m3_to_f16x2(d & 0xffffu));
-                    mma_f16(o[4 * i + 3], pa[hf], e4m3_to_f16x2(c >> 16), e4m3_to_f16x2(d >> 16));
+                    const uint32_t a0 = e4m3_to_f16x2(a), a1 = e4m3_to_f16x2(a >> 16), a2 = e4m3_to_f16x2(b), a3 = e4m3_to_f16x2(b >> 16);
+                    const uint32_t c0 = e4m3_to_f16x2(c), c1 = e4m3_to_f16x2(c >> 16), c2 = e4m3_to_f16x2(d), c3 = e4m3_to_f16x2(d >> 16);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(o[nt][2 * i], a0, a1, a2, a3, pb[hf][nt][0], pb[hf][nt][1]);
+                        mma_f16(o[nt][2 * i + 1], c0, c1, c2, c3, pb[hf][nt][0], pb[hf][nt][1]);
+                    }
                 }
             }
             __syncwarp();  // every lane has read the stage
             fill();
         }
-        // ---- the piece's rows: columns 32t .. 32t+31 of rows g, g + 8 ----
+        // ---- the piece's rows: columns 16g .. 16g+15 of rows 8 nt + 2t, + 1 ----
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-            const int r = g + 8 * e;
-            if (r >= rows) continue;
-            if (it.whole()) {
-                const int slot = r / p.G;
-                const bool live = ok && slot < it.n && l[e] > 0.0f;
-                const float inv = live ? sref / l[e] : 0.0f;
-                uint4* dst = reinterpret_cast<uint4*>(
-                    p.out + ((static_cast<size_t>(it.b) * p.s.T + slot) * p.Hq + hk * p.G + (r - slot * p.G)) * kKvqHeadDim +
-                    32 * t);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t w[4];
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[nt][e];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                const int r = 8 * nt + 2 * t + e;
+                if (r >= rows) continue;
+                float x[16];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int j = (c & 1) * 8 + 2 * i;
-                        w[i] = live ? pack_bf16(o[j][2 * e + (c >> 1)] * inv, o[j + 1][2 * e + (c >> 1)] * inv) : 0u;
+                for (int j = 0; j < 8; ++j) {
+                    x[2 * j] = o[nt][j][e];
+                    x[2 * j + 1] = o[nt][j][2 + e];
+                }
+                if (it.whole()) {
+                    const int slot = r / p.G;
+                    const bool live = ok && slot < it.n && sum > 0.0f;
+                    const float inv = live ? sref / sum : 0.0f;
+                    uint32_t w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = live ? pack_bf16(x[2 * i] * inv, x[2 * i + 1] * inv) : 0u;
+                    uint4* dst = reinterpret_cast<uint4*>(
+                        p.out + ((static_cast<size_t>(it.b) * p.s.T + slot) * p.Hq + hk * p.G + (r - slot * p.G)) * kKvqHeadDim +
+                        16 * g);
+                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                } else {
+                    const size_t row = static_cast<size_t>(it.slot(worker)) * p.part.rows + r;
+                    float4* dst = reinterpret_cast<float4*>(p.part.o + row * kKvqHeadDim + 16 * g);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        dst[c] = make_float4(x[4 * c] * sref, x[4 * c + 1] * sref, x[4 * c + 2] * sref, x[4 * c + 3] * sref);
+                    if (g == 0) {
+                        p.part.ml[2 * row] = ok ? m[nt][e] : -INFINITY;
+                        p.part.ml[2 * row + 1] = ok ? sum : 0.0f;
                     }
-                    dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            } else {
-                const size_t row = static_cast<size_t>(it.slot(worker)) * p.part.rows + r;
-                float4* dst = reinterpret_cast<float4*>(p.part.o + row * kKvqHeadDim + 32 * t);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const int j = (c & 3) * 4, x = 2 * e + (c >> 2);
-                    dst[c] = make_float4(o[j][x] * sref, o[j + 1][x] * sref, o[j + 2][x] * sref, o[j + 3][x] * sref);
-                }
-                if (t == 0) {
-                    p.part.ml[2 * row] = ok ? m[e] : -INFINITY;
-                    p.part.ml[2 * row + 1] = ok ? l[e] : 0.0f;
                 }
             }
-        }
     }
+    if (lane == 0) p.part.cut[worker] = cut;
 }
 
 // ------------------------------------------------------------------ merge ---
 
 constexpr int kMergeWarps = 8;
 constexpr int kMergeAlone = 4;  // most pieces that one warp combines by itself
-
-// The cut item that worker w began: O = sum_i 2^(m_i - M) O_i over
-// sum_i 2^(m_i - M) l_i of its pieces i (worker w's in slot 2w + 1, w + i's in
-// slot 2 (w + i)).
-struct CutItem {
-    int np;  // pieces; 0: worker w began none that was cut
-    int b, sub, n;
-};
-
-__device__ __forceinline__ CutItem cut_item(const KvqSched& s, int w) {  // whole warp
-    CutItem c{0, 0, 0, 0};
-    const long long total = kvq_total(s), chunk = kvq_chunk(s, total);
-    const long long end = (w + 1) * chunk;
-    if (w * chunk >= total || end >= total) return c;  // the last worker's items end with it
-    long long base;
-    const int b = kvq_find(s, end - 1, &base);
-    const KvqSeq q = kvq_seq(s, b);
-    const int sub = static_cast<int>((end - 1 - base) / q.len);
-    const long long g0 = base + static_cast<long long>(sub) * q.len;
-    const long long t1 = end - g0 - s.ov, t0 = w * chunk - g0 - s.ov;
-    if (t1 <= 0 || t1 >= q.nt || t0 > 0) return c;  // not cut, or begun by an earlier worker
-    c.np = static_cast<int>((g0 + s.ov + q.nt - 1) / chunk) - w + 1;
-    c.b = b;
-    c.sub = sub;
-    c.n = q.n;
-    return c;
-}
 
 // Running combination of a row's pieces, four columns per lane.
 struct RowSum {
@@ -363,37 +396,35 @@ struct RowSum {
     }
 };
 
-__device__ __forceinline__ void merge_store(const KvqMergeParams& p, const CutItem& c, int r, const RowSum& s, int lane) {
-    const int hk = c.sub / p.n_rb, row = (c.sub - hk * p.n_rb) * p.part.rows + r;
+// c: (pieces, sequence, item, tree size) of a cut item.
+__device__ __forceinline__ void merge_store(const KvqMergeParams& p, const int4& c, int r, const RowSum& s, int lane) {
+    const int hk = c.z / p.n_items, row = (c.z - hk * p.n_items) * p.part.rows + r;
     const int slot = row / p.G;
     if (slot >= p.T) return;  // past the (sequence, KV head)'s rows
-    const bool live = slot < c.n && s.l > 0.0f;
+    const bool live = slot < c.w && s.l > 0.0f;
     const float inv = live ? 1.0f / s.l : 0.0f;
     uint2* dst = reinterpret_cast<uint2*>(
-        p.out + ((static_cast<size_t>(c.b) * p.T + slot) * p.Hq + static_cast<size_t>(hk) * p.G + (row - slot * p.G)) * kKvqHeadDim);
+        p.out + ((static_cast<size_t>(c.y) * p.T + slot) * p.Hq + static_cast<size_t>(hk) * p.G + (row - slot * p.G)) * kKvqHeadDim);
     dst[lane] = live ? make_uint2(pack_bf16(s.o.x * inv, s.o.y * inv), pack_bf16(s.o.z * inv, s.o.w * inv))
                      : make_uint2(0u, 0u);
 }
 
-// A CTA serves the items that eight neighbouring workers began (decode: few
-// rows) or one worker's (128 rows, blockIdx.y taking some of them). Which those are
-// comes from the lengths alone and is found while the attention kernel still
-// runs. With 128 rows a warp takes whole rows. Decode items of up to four pieces go
-// to one warp each; those of many (few long sequences) are shared by all
-// eight warps, row by row.
+// The cut item that worker w began: O = sum_i 2^(m_i - M) O_i over
+// sum_i 2^(m_i - M) l_i of its pieces i (worker w's in slot 2w + 1, w + i's in
+// slot 2 (w + i)). A CTA serves the items that eight neighbouring workers
+// began (decode: few rows) or one worker's (256 rows, blockIdx.y taking some of
+// them). With many rows a warp takes whole rows. Decode items of up to four
+// pieces go to one warp each; those of many (few long sequences) are shared
+// by all eight warps, row by row.
 __global__ void __launch_bounds__(kMergeWarps * 32) kvq_merge_kernel(KvqMergeParams p, int per_cta, int rows_per_cta) {
-    __shared__ CutItem items[kMergeWarps];
     __shared__ float4 so[kMergeWarps][32];
     __shared__ float2 sml[kMergeWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w0 = blockIdx.x * per_cta;
-    if (warp < per_cta) {
-        const CutItem c = w0 + warp < p.s.workers ? cut_item(p.s, w0 + warp) : CutItem{0, 0, 0, 0};
-        if (lane == 0) items[warp] = c;
-    }
-    __syncthreads();
     pdl_wait_prior();
     pdl_launch_dependents();
+    const int4* items = p.part.cut + w0;
+    const int n_here = min(per_cta, p.workers - w0);
     const int r0 = blockIdx.y * rows_per_cta, r1 = min(p.part.rows, r0 + rows_per_cta);
     const float2* ml = reinterpret_cast<const float2*>(p.part.ml);
     const float4* po = reinterpret_cast<const float4*>(p.part.o);
@@ -401,36 +432,36 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kvq_merge_kernel(KvqMergePar
         return static_cast<size_t>(i == 0 ? 2 * w + 1 : 2 * (w + i)) * p.part.rows + r;
     };
     const bool decode = per_cta > 1;
-    for (int e = 0; e < per_cta; ++e) {
-        const CutItem c = items[e];
-        if (c.np == 0 || (decode && (c.np > kMergeAlone || e != warp))) continue;
+    for (int e = 0; e < n_here; ++e) {
+        const int4 c = __ldcg(items + e);
+        if (c.x == 0 || (decode && (c.x > kMergeAlone || e != warp))) continue;
         // decode: item e belongs to warp e; else its rows are dealt over the warps
         for (int r = decode ? r0 : r0 + warp; r < r1; r += decode ? 1 : kMergeWarps) {
             RowSum s;
-            for (int i0 = 0; i0 < c.np; i0 += kMergeAlone) {
+            for (int i0 = 0; i0 < c.x; i0 += kMergeAlone) {
                 float2 a[kMergeAlone];
                 float4 x[kMergeAlone];
 #pragma unroll
                 for (int i = 0; i < kMergeAlone; ++i) {
-                    if (i0 + i >= c.np) break;
+                    if (i0 + i >= c.x) break;
                     const size_t at = slot_row(w0 + e, i0 + i, r);
                     a[i] = __ldcg(ml + at);
                     x[i] = __ldcg(po + at * 32 + lane);
                 }
 #pragma unroll
                 for (int i = 0; i < kMergeAlone; ++i)
-                    if (i0 + i < c.np) s.add(a[i].x, a[i].y, x[i]);
+                    if (i0 + i < c.x) s.add(a[i].x, a[i].y, x[i]);
             }
             merge_store(p, c, r, s, lane);
         }
     }
-    for (int e = 0; e < per_cta; ++e) {
-        const CutItem c = items[e];
-        if (!decode || c.np <= kMergeAlone) continue;  // uniform over the CTA
+    for (int e = 0; e < n_here; ++e) {
+        const int4 c = __ldcg(items + e);
+        if (!decode || c.x <= kMergeAlone) continue;  // uniform over the CTA
         for (int r = r0; r < r1; ++r) {
             RowSum s;
 #pragma unroll 4
-            for (int i = warp; i < c.np; i += kMergeWarps) {
+            for (int i = warp; i < c.x; i += kMergeWarps) {
                 const size_t at = slot_row(w0 + e, i, r);
                 const float2 a = __ldcg(ml + at);
                 const float4 x = __ldcg(po + at * 32 + lane);
@@ -454,21 +485,26 @@ cudaError_t launch_kvq_merge(const KvqMergeParams& p, cudaStream_t stream) {
     const bool decode = p.part.rows <= kKvqDecodeRows;
     const int per_cta = decode ? kMergeWarps : 1, rows_per_cta = decode ? p.part.rows : 32;
     return launch_pdl(kvq_merge_kernel,
-                      dim3((p.s.workers + per_cta - 1) / per_cta, (p.part.rows + rows_per_cta - 1) / rows_per_cta),
+                      dim3((p.workers + per_cta - 1) / per_cta, (p.part.rows + rows_per_cta - 1) / rows_per_cta),
                       dim3(kMergeWarps * 32), 0, stream, p, per_cta, rows_per_cta);
 }
 
-KvqSched kvq_decode_sched(int B, int T, int max_len, int Hkv) {
-    return KvqSched{nullptr, nullptr, B, T, max_len, Hkv, kStep, 2, kKvqSms * kWarps, 4};
+KvqSched kvq_decode_sched(int B, int T, int max_len, int Hkv, int rows) {
+    return KvqSched{nullptr, nullptr, B, T, max_len, Hkv, kStep, 2, kKvqSms * warps_of(rows <= 8 ? 1 : 2), 4};
+}
+
+template <int NT>
+static cudaError_t launch_decode(const KvqAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kvq_decode_kernel<NT>), kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kvq_decode_kernel<NT>, dim3(kKvqSms), dim3(warps_of(NT) * 32), kSmem, stream, tk, tv, p);
 }
 
 cudaError_t launch_kvq_decode(const KvqDims& kv, const KvqAttnParams& p, const void* kbase, const void* vbase,
                               cudaStream_t stream) {
     CUtensorMap tk, tv;
     if (!make_map_codes(&tk, kbase, kv, kStep) || !make_map_codes(&tv, vbase, kv, kStep)) return cudaErrorInvalidValue;
-    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kvq_decode_kernel), kSmem);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kvq_decode_kernel, dim3(kKvqSms), dim3(kWarps * 32), kSmem, stream, tk, tv, p);
+    return p.G * p.s.T <= 8 ? launch_decode<1>(p, tk, tv, stream) : launch_decode<2>(p, tk, tv, stream);
 }
 
 }  // namespace eagle

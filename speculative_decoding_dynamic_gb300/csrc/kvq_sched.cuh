@@ -81,20 +81,23 @@ __device__ __forceinline__ int kvq_find(const KvqSched& s, long long pos, long l
     return s.B;  // not reached for pos < total
 }
 
-// One piece: steps [t0, t1) of item `sub` of sequence b.
+// One piece: steps [t0, t1) of item `sub` of sequence b; np: pieces of the
+// item if this is its first and it is cut, else 0.
 struct KvqPiece {
-    int b, sub, L, n, nkeys, nt, t0, t1;
+    int b, sub, L, n, nkeys, nt, t0, t1, np;
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
     __device__ __forceinline__ int slot(int worker) const { return 2 * worker + (t0 == 0 ? 1 : 0); }
 };
 
 // A worker's pieces in order. init by a whole warp; next by any thread.
 struct KvqCursor {
-    long long pos, end, base;
-    int b;
+    long long pos, end, base, chunk;
+    int b, worker;
     KvqSeq q;
-    __device__ __forceinline__ void init(const KvqSched& s, int worker) {
-        const long long total = kvq_total(s), chunk = kvq_chunk(s, total);
+    __device__ __forceinline__ void init(const KvqSched& s, int w) {
+        const long long total = kvq_total(s);
+        worker = w;
+        chunk = kvq_chunk(s, total);
         pos = min(total, worker * chunk);
         end = min(total, (worker + 1) * chunk);
         base = 0;
@@ -126,6 +129,7 @@ struct KvqCursor {
             p.nt = q.nt;
             p.t0 = max(0, from - s.ov);
             p.t1 = max(0, to - s.ov);
+            p.np = p.t0 == 0 && p.t1 < p.nt ? static_cast<int>((g0 + s.ov + p.nt - 1) / chunk) - worker + 1 : 0;
             if (p.t1 > p.t0) return true;
         }
         return false;
@@ -133,17 +137,19 @@ struct KvqCursor {
 };
 
 // Partial results of cut items: O [slot][row][128] (in units where O / sum is
-// the output), and (max in the log2 domain, sum) [slot][row][2].
+// the output), (max in the log2 domain, sum) [slot][row][2], and which cut
+// item each worker began: (pieces or 0, sequence, item, tree size) [worker].
 struct KvqPartials {
     float* o;
     float* ml;
+    int4* cut;
     int rows;  // rows of a piece
 };
+__device__ __forceinline__ int4 kvq_cut(const KvqPiece& p) { return make_int4(p.np, p.b, p.sub, p.n); }
 
 struct KvqMergeParams {
-    KvqSched s;
     KvqPartials part;
-    int G, T, Hq, n_rb;
+    int workers, G, T, Hq, n_items;  // n_items: items of a KV head
     __nv_bfloat16* out;
 };
 cudaError_t launch_kvq_merge(const KvqMergeParams& p, cudaStream_t stream);
@@ -202,7 +208,8 @@ constexpr int kKvqSms = 152;
 struct KvqAttnParams {
     KvqSched s;
     KvqPartials part;
-    int Hq, Hkv, G, n_rb, W;
+    int Hq, Hkv, G, W;
+    int n_items;    // items of a KV head (pairs of row blocks; 1 in the decode kernel)
     int blk_shift;  // log2 of the positions of a scale block
     int64_t s_seq, s_blk;
     const float *k_scale, *v_scale;  // of this layer
@@ -214,6 +221,6 @@ struct KvqAttnParams {
 };
 cudaError_t launch_kvq_decode(const KvqDims& kv, const KvqAttnParams& p, const void* kbase, const void* vbase,
                               cudaStream_t stream);
-KvqSched kvq_decode_sched(int B, int T, int max_len, int Hkv);
+KvqSched kvq_decode_sched(int B, int T, int max_len, int Hkv, int rows);
 
 }  // namespace eagle
