@@ -228,6 +228,18 @@ __device__ __forceinline__ void prefetch_l2_segment(const char* src, int bytes) 
     for (int off = 0; off < bytes; off += 16384) prefetch_l2(src + off, static_cast<uint32_t>(min(16384, bytes - off)));
 }
 
+// 16 bytes from / to shared memory by its 32-bit address (a pointer into
+// dynamic shared memory that was aligned by hand is a generic one to the
+// compiler, and generic loads are tracked like global ones).
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // Global loads that bypass L1 (data written by other CTAs of the same launch).
 __device__ __forceinline__ int ld_cg_i32(const int* p) { return __ldcg(p); }
 __device__ __forceinline__ float ld_cg_f32(const float* p) { return __ldcg(p); }

@@ -51,8 +51,10 @@ constexpr int kTileV = kBN * kHD * 2;    // 16 KB: V as fp16, two halves of 64 c
 constexpr int kHalfV = kTileV / 2;
 constexpr int kKStages = 3, kVStages = 2;  // code tiles in flight
 constexpr int kConvWarps = 4, kSoftmaxWarps = 8;
-constexpr int kWarpConv = 2, kWarpSoftmax = kWarpConv + kConvWarps;  // warp 0 TMA, warp 1 MMA
-constexpr int kThreads = 32 * (kWarpSoftmax + kSoftmaxWarps);
+constexpr int kWarpConv = 2, kWarpSoftmax = kWarpConv + kConvWarps;  // warp 0 TMA, warp 1 MMA of block 0
+constexpr int kWarpScale = kWarpSoftmax + kSoftmaxWarps;
+constexpr int kWarpMma1 = kWarpScale + 1;
+constexpr int kThreads = 32 * (kWarpMma1 + 1);
 constexpr int kSmemQ = 0;                                   // [item parity][row block][hi, lo]
 constexpr int kSmemK = 8 * kTileQ;
 constexpr int kSmemV8 = kSmemK + kKStages * kTile8;
@@ -66,13 +68,39 @@ __host__ __device__ constexpr uint32_t idesc_type0(int M, int N, int b_mn_major)
     return (1u << 4) | (static_cast<uint32_t>(b_mn_major) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
            (static_cast<uint32_t>(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_f8(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, int accum) {
+// An MMA warp runs as one: every lane computes the same descriptors (in
+// uniform registers) and one elected lane issues, by a predicate inside the
+// instruction. Issued from a branch that one lane takes, each MMA moves its six
+// operands into uniform registers first: about 110 cycles per instruction, three
+// times what it computes (70B 32K: 1329 us).
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void mma_f8(uint32_t lead, uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, int accum) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(tmem_d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accum)
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(tmem_d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accum), "r"(lead)
         : "memory");
 }
+__device__ __forceinline__ void mma_f16_ts(uint32_t lead, uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc,
+                                           int accum) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(b), "r"(idesc), "r"(accum), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __device__ __forceinline__ float max16(const uint32_t* v) {
     auto f = [&](int i) { return __uint_as_float(v[i]); };
@@ -87,14 +115,27 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low 
     return d;
 }
 
-// A wait of a whole warp: every lane polls; after a first timeout later waits
-// are short, so that a failed launch still ends promptly (its results are
-// meaningless then and the status says so; every role keeps its own order of
-// arrivals, so nobody waits without bound).
+// Bounded waits of a whole warp. Every lane polls: tensor-memory instructions
+// want the warp converged, which one lane's polls and a warp barrier do not
+// promise. SLEEP: a short nap between polls, for the waits that are long
+// anyway, so that idle warps leave issue slots and the barrier unit to the
+// others. After a first timeout later waits are short, so that a failed launch
+// still ends promptly (its results are meaningless then and the status says
+// so; every role keeps its own order of arrivals, so nobody waits without bound).
 struct Waiter {
     bool ok = true;
+    template <bool SLEEP = true>
+    __device__ __forceinline__ void poll(uint64_t* bar, int phase) {
+        const uint32_t limit = ok ? (1u << 21) : 64u;
+        for (uint32_t i = 0; i < limit; ++i) {
+            if (mbar_try_wait(bar, phase & 1)) return;
+            if (SLEEP) __nanosleep(32);
+        }
+        ok = false;
+    }
     __device__ __forceinline__ void operator()(uint64_t* bar, int phase) {
-        if (!mbar_wait(bar, phase & 1, ok ? (1u << 21) : 64u)) ok = false;
+        poll(bar, phase);
+        __syncwarp();
     }
 };
 
@@ -124,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kKStages; ++s) {
             mbar_init(&bar_k_full[s], 1);
-            mbar_init(&bar_k_empty[s], 1);
+            mbar_init(&bar_k_empty[s], 2);
         }
         for (int s = 0; s < kVStages; ++s) {
             mbar_init(&bar_v8_full[s], 1);
@@ -132,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bar_q_full[s], kConvWarps);
-            mbar_init(&bar_q_empty[s], 1 + kSoftmaxWarps);
+            mbar_init(&bar_q_empty[s], 2 + kSoftmaxWarps);
             mbar_init(&bar_v_full[s], kConvWarps);
             mbar_init(&bar_v_empty[s], 2);
             mbar_init(&bar_sc[s], 1);
@@ -166,112 +207,117 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producers ---
-        // Lane 0 loads the K tiles (a stage is free once QK^T of its tile is
-        // done), lane 1 the V tiles (free once converted).
-        if (lane < 2) {
-            const bool is_k = lane == 0;
-            uint64_t* full = is_k ? bar_k_full : bar_v8_full;
-            uint64_t* empty = is_k ? bar_k_empty : bar_v8_empty;
-            const CUtensorMap* map = is_k ? &tm_k : &tm_v;
-            const int ns = is_k ? kKStages : kVStages;
+        // One lane: K tiles (a stage is free once both blocks' QK^T of its
+        // tile are done) and V tiles (free once converted) in turn.
+        if (lane == 0) {
             int t = 0;
             while (wait.ok && cur.next(p.s, it)) {
                 const int hk = it.sub / p.n_items;
                 for (int j = it.t0; j < it.t1; ++j, ++t) {
-                    const int st = t % ns;
-                    if (t >= ns) wait(&empty[st], t / ns - 1);
+                    const int sk = t % kKStages, sv = t % kVStages;
+                    if (t >= kKStages) wait.poll(&bar_k_empty[sk], t / kKStages - 1);
                     if (!wait.ok) break;
-                    mbar_arrive_expect_tx(&full[st], kTile8);
-                    tma_load_4d(smem + (is_k ? kSmemK : kSmemV8) + st * kTile8, map, 0, hk, j * kBN, it.b, &full[st]);
+                    mbar_arrive_expect_tx(&bar_k_full[sk], kTile8);
+                    tma_load_4d(smem + kSmemK + sk * kTile8, &tm_k, 0, hk, j * kBN, it.b, &bar_k_full[sk]);
+                    if (t >= kVStages) wait.poll(&bar_v8_empty[sv], t / kVStages - 1);
+                    if (!wait.ok) {
+                        mbar_wait(&bar_k_full[sk], (t / kKStages) & 1);
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&bar_v8_full[sv], kTile8);
+                    tma_load_4d(smem + kSmemV8 + sv * kTile8, &tm_v, 0, hk, j * kBN, it.b, &bar_v8_full[sv]);
                 }
             }
             if (!wait.ok) {  // the copies in flight land before the CTA's shared memory goes away
                 raise_status(p.status, kDevTimeout);
-                for (int f = max(0, t - ns); f < t; ++f) wait(&full[f % ns], f / ns);
+                for (int f = max(0, t - kKStages); f < t; ++f) mbar_wait(&bar_k_full[f % kKStages], (f / kKStages) & 1);
+                for (int f = max(0, t - kVStages); f < t; ++f) mbar_wait(&bar_v8_full[f % kVStages], (f / kVStages) & 1);
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ---------------------------------------------------- MMA issuer ---
-        // Tiles are numbered t over all of the worker's pieces, and tg per row
-        // block over those in which the block has rows. QK_g goes into S
-        // buffer tg & 1 of block g, over the P that PV_g(tg - 2) reads; the two
-        // are of different kinds and accumulators, which the pipe does not
-        // promise to run in order, so QK waits for that PV's completion. Issue
-        // order QK0(t) QK1(t) PV0(t-1) PV1(t-1) QK0(t+1) ...: the other block's
-        // MMA is in flight during the wait. A piece's first PV overwrites O: the
-        // softmax threads have read the previous piece's O before they arrive
-        // for it. A PV's completion is told on one of two barriers in turn: when
-        // the softmax waits for PV(tg) the one before may still be running,
-        // and a single barrier's parity would be taken for the phase before.
-        if (lane == 0) {
-            constexpr uint32_t id_qk = idesc_type0(kBM, kBN, 0);
-            constexpr uint32_t id_pv = idesc_type0(kBM, kHD, 1);
-            int t = 0, qi = 0, tg[2] = {0, 0};
-            while (cur.next(p.s, it)) {
-                const int nb = (it.sub % p.n_items) * 2 + 1 < (rows + kBM - 1) / kBM ? 2 : 1;  // row blocks of the item
-                const uint32_t aQ = smem_u32(smem + kSmemQ + (qi & 1) * 4 * kTileQ);
-                auto pv = [&](int tp, bool first) {  // tile tp; of each block its tile tg - 1
-                    wait(&bar_v_full[tp & 1], tp >> 1);
-                    const uint32_t aV = smem_u32(smem + kSmemV + (tp & 1) * kTileV);
+    } else if (warp == 1 || warp == kWarpMma1) {
+        // --------------------------------------------------- MMA issuers ---
+        // One warp per row block g: its waits (four a tile) overlap the other's.
+        // Tiles are numbered t over all of
+        // the worker's pieces, and u over those in which the block has rows. QK(u)
+        // goes into S buffer u & 1, over the P that PV(u - 2) reads; the two are
+        // of different kinds and accumulators, which the pipe does not promise to
+        // run in order, so QK waits for that PV's completion. Issue order QK(0)
+        // QK(1) PV(0) QK(2) PV(1) ... A piece's first PV overwrites O: the softmax
+        // threads have read the previous piece's O before they arrive for it. A
+        // PV's completion is told on one of two barriers in turn: when the softmax
+        // waits for PV(u) the one before may still be running, and a single
+        // barrier's parity would be taken for the phase before.
+        constexpr uint32_t id_qk = idesc_type0(kBM, kBN, 0);
+        constexpr uint32_t id_pv = idesc_type0(kBM, kHD, 1);
+        const uint32_t lead = elect_one();
+        const uint32_t base = smem_u32(smem), tm = uniform(tmem);
+        const int g = uniform(warp == 1 ? 0 : 1);
+        const int blocks = (rows + kBM - 1) / kBM;
+        const uint32_t tS = tm + 128 * g, tO = tm + 256 + 128 * g;
+        int t = 0, qi = 0, u = 0;
+        auto spin = [&](uint64_t* bar, int phase) {
+            wait.poll<false>(bar, phase);
+            __syncwarp();
+        };
+        auto pv = [&](int tp, int up, bool first) {
+            spin(&bar_v_full[tp & 1], tp >> 1);
+            spin(&bar_p_full[g][up & 1], up >> 1);
+            tc_fence_after();
+            const uint32_t aV = base + kSmemV + (tp & 1) * kTileV;
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        if (g < nb) {
-                            const int u = tg[g] - 1;
-                            wait(&bar_p_full[g][u & 1], u >> 1);
-                            tc_fence_after();
-#pragma unroll
-                            for (int kk = 0; kk < kBN / 16; ++kk)  // A = P from TMEM: 16 keys = 8 columns per MMA
-                                mma_bf16_ts(tmem + 256 + 128 * g, tmem + 64 * (2 * g + (u & 1)) + kk * 8,
-                                            smem_desc(aV + kk * 2048, kHalfV, 1024), id_pv, (!first || kk > 0) ? 1 : 0);
-                            mma_commit(&bar_pv_done[g][u & 1]);
-                        }
-                        mma_commit(&bar_v_empty[tp & 1]);
-                    }
-                };
-                wait(&bar_q_full[qi & 1], qi >> 1);
-                for (int j = it.t0; j < it.t1; ++j, ++t) {
-                    const int sk = t % kKStages;
-                    wait(&bar_k_full[sk], t / kKStages);
-                    tc_fence_after();
-                    const uint32_t aK = smem_u32(smem + kSmemK + sk * kTile8);
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        if (g >= nb) break;
-                        if (tg[g] >= 2) wait(&bar_pv_done[g][tg[g] & 1], (tg[g] >> 1) - 1);
-                        const uint32_t d = tmem + 64 * (2 * g + (tg[g] & 1));
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)  // hi (0..3), lo (4..7); 32 elements of the head dimension each
-                            mma_f8(d, smem_desc(aQ + (2 * g + (kk >> 2)) * kTileQ + (kk & 3) * 32, 16, 1024),
-                                   smem_desc(aK + (kk & 3) * 32, 16, 1024), id_qk, kk > 0);
-                        mma_commit(&bar_s_full[g][tg[g] & 1]);
-                    }
-                    mma_commit(&bar_k_empty[sk]);
-                    if (j == it.t1 - 1) mma_commit(&bar_q_empty[qi & 1]);
-                    if (j > it.t0) pv(t - 1, j == it.t0 + 1);
-                    tg[0] += 1;
-                    tg[1] += nb - 1;
+            for (int kk = 0; kk < kBN / 16; ++kk)  // A = P from TMEM: 16 keys = 8 columns per MMA
+                mma_f16_ts(lead, tO, tS + 64 * (up & 1) + kk * 8, smem_desc(aV + kk * 2048, kHalfV, 1024), id_pv,
+                           (!first || kk > 0) ? 1 : 0);
+            commit(lead, &bar_pv_done[g][up & 1]);
+            commit(lead, &bar_v_empty[tp & 1]);
+        };
+        for (;;) {
+            const bool more = cur.next(p.s, it);
+            if (!uniform(more)) break;
+            const int n_tiles = uniform(it.t1 - it.t0);
+            const bool live = uniform((it.sub % p.n_items) * 2 + g) < blocks;
+            const uint32_t aQ = base + kSmemQ + ((qi & 1) * 4 + 2 * g) * kTileQ;
+            spin(&bar_q_full[qi & 1], qi >> 1);
+            if (!live) {  // a block without rows: keep the shared barriers' counts, in step
+                for (int j = 0; j < n_tiles; ++j, ++t) {
+                    spin(&bar_k_full[t % kKStages], t / kKStages);
+                    if (lane == 0) mbar_arrive(&bar_k_empty[t % kKStages]);
+                    spin(&bar_v_full[t & 1], t >> 1);
+                    if (lane == 0) mbar_arrive(&bar_v_empty[t & 1]);
                 }
-                pv(t - 1, it.t1 - it.t0 == 1);
+                if (lane == 0) mbar_arrive(&bar_q_empty[qi & 1]);
                 ++qi;
+                continue;
             }
-            if (!wait.ok) raise_status(p.status, kDevTimeout);
+            for (int j = 0; j < n_tiles; ++j, ++t, ++u) {
+                const int sk = t % kKStages;
+                spin(&bar_k_full[sk], t / kKStages);
+                if (u >= 2) spin(&bar_pv_done[g][u & 1], (u >> 1) - 1);
+                tc_fence_after();
+                const uint32_t aK = base + kSmemK + sk * kTile8;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)  // hi (0..3), lo (4..7); 32 elements of the head dimension each
+                    mma_f8(lead, tS + 64 * (u & 1), smem_desc(aQ + (kk >> 2) * kTileQ + (kk & 3) * 32, 16, 1024),
+                           smem_desc(aK + (kk & 3) * 32, 16, 1024), id_qk, kk > 0);
+                commit(lead, &bar_s_full[g][u & 1]);
+                commit(lead, &bar_k_empty[sk]);
+                if (j == n_tiles - 1) commit(lead, &bar_q_empty[qi & 1]);
+                if (j > 0) pv(t - 1, u - 1, j == 1);
+            }
+            pv(t - 1, u - 1, n_tiles == 1);
+            ++qi;
         }
-        __syncwarp();
+        // the last commits' arrivals come before the CTA's shared memory goes away
+        if (t > 0) spin(&bar_v_empty[(t - 1) & 1], (t - 1) >> 1);
+        if (!wait.ok) raise_status(p.status, kDevTimeout);
     } else if (warp < kWarpSoftmax) {
         // ----------------------------------------------------- converters ---
-        // V codes to fp16, the tile's scales for the softmax, and q, row
-        // factors and mask words of the next item while the current one runs.
+        // V codes to fp16, and q, row factors and mask words of the next item
+        // while the current one runs.
         const int cw = warp - kWarpConv;
+        const uint32_t base = smem_u32(smem);
         const int i = threadIdx.x - kWarpConv * 32;
-        float next = 0.0f;  // lanes 0..3 of the first warp: K's scales of the next tile's groups; 4..7: V's
-        auto read_scale = [&](const KvqPiece& a, int j) {
-            if (cw == 0 && lane < 2 * kSub) {
-                const int last = (a.nkeys - 1) >> p.blk_shift;
-                next = __ldg((lane < kSub ? p.k_scale : p.v_scale) + a.b * p.s_seq + a.sub / p.n_items +
-                             min((j * kBN + 16 * (lane & 3)) >> p.blk_shift, last) * p.s_blk);
-            }
-        };
         auto convert_q = [&](const KvqPiece& a, int qi) {
             if (qi >= 2) wait(&bar_q_empty[qi & 1], (qi >> 1) - 1);
             const int hk = a.sub / p.n_items, row0 = (a.sub - hk * p.n_items) * 2 * kBM;
@@ -331,58 +377,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         int t = 0, qi = 0;
         KvqPiece ahead;
         bool more = cur.next(p.s, ahead);
-        if (more) {
-            read_scale(ahead, ahead.t0);
-            convert_q(ahead, 0);
-        }
+        if (more) convert_q(ahead, 0);
         while (more) {
             it = ahead;
             more = cur.next(p.s, ahead);
-            float sref = 0.0f;
             for (int j = it.t0; j < it.t1; ++j, ++t) {
                 const int b = t & 1;
                 if (t >= 2) wait(&bar_v_empty[b], (t >> 1) - 1);
-                if (cw == 0) {
-                    // V's reference scale: the first tile's largest, raised by more than 2^4 only
-                    const float own = next;
-                    float vm = lane >= kSub && lane < 2 * kSub ? own : 0.0f;
-                    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
-                    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
-                    vm = __shfl_sync(0xffffffffu, vm, kSub);
-                    float alpha = 1.0f;
-                    if (vm > 16.0f * sref) {
-                        if (sref > 0.0f) alpha = sref / vm;
-                        sref = vm;
-                    }
-                    if (lane < kSub) ts[b].k[lane] = own;
-                    if (lane >= kSub && lane < 2 * kSub) {
-                        const float ratio = fmaxf(own / sref, 0x1p-24f);
-                        ts[b].lv[lane - kSub] = log2f(ratio);
-                        ts[b].iv[lane - kSub] = 1.0f / ratio;
-                    }
-                    if (lane == 0) {
-                        ts[b].alpha = alpha;
-                        ts[b].sref = sref;
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar_sc[b]);
-                    if (j + 1 < it.t1) read_scale(it, j + 1);
-                    else if (more) read_scale(ahead, ahead.t0);
-                }
                 const int st = t % kVStages;
                 wait(&bar_v8_full[st], t / kVStages);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int key = lane + 32 * (e & 1), c16 = 2 * cw + (e >> 1);
-                    uint4 u = *reinterpret_cast<const uint4*>(smem + kSmemV8 + st * kTile8 + key * kHD + ((c16 ^ (key & 7)) << 4));
+                    uint4 u = lds128(base + kSmemV8 + st * kTile8 + key * kHD + ((c16 ^ (key & 7)) << 4));
                     // keys that no row can see may hold anything (even NaN): 0 * V has to stay 0
                     if (j * kBN + key >= it.nkeys) u = make_uint4(0u, 0u, 0u, 0u);
-                    unsigned char* dst = smem + kSmemV + b * kTileV + (c16 >> 2) * kHalfV + key * 128;
+                    const uint32_t dst = base + kSmemV + b * kTileV + (c16 >> 2) * kHalfV + key * 128;
                     const int c = 2 * (c16 & 3);
-                    *reinterpret_cast<uint4*>(dst + ((c ^ (key & 7)) << 4)) =
-                        make_uint4(e4m3_to_f16x2(u.x), e4m3_to_f16x2(u.x >> 16), e4m3_to_f16x2(u.y), e4m3_to_f16x2(u.y >> 16));
-                    *reinterpret_cast<uint4*>(dst + (((c + 1) ^ (key & 7)) << 4)) =
-                        make_uint4(e4m3_to_f16x2(u.z), e4m3_to_f16x2(u.z >> 16), e4m3_to_f16x2(u.w), e4m3_to_f16x2(u.w >> 16));
+                    sts128(dst + ((c ^ (key & 7)) << 4),
+                           make_uint4(e4m3_to_f16x2(u.x), e4m3_to_f16x2(u.x >> 16), e4m3_to_f16x2(u.y), e4m3_to_f16x2(u.y >> 16)));
+                    sts128(dst + (((c + 1) ^ (key & 7)) << 4),
+                           make_uint4(e4m3_to_f16x2(u.z), e4m3_to_f16x2(u.z >> 16), e4m3_to_f16x2(u.w), e4m3_to_f16x2(u.w >> 16)));
                 }
                 fence_proxy_async_smem();  // the MMA reads V through the async proxy
                 __syncwarp();
@@ -393,6 +408,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (more && j == min(it.t0 + 1, it.t1 - 1)) convert_q(ahead, qi + 1);
             }
             ++qi;
+        }
+        if (!wait.ok) raise_status(p.status, kDevTimeout);
+    } else if (warp == kWarpScale) {
+        // --------------------------------------------------------- scales ---
+        // What the softmax needs of the tiles' scales, read a tile ahead. A warp
+        // of its own: in a converter the fence behind each tile would wait for
+        // the scales in flight (8B b64: 211 us instead of the figure above).
+        int t = 0;
+        float next = 0.0f;  // lanes 0..3: K's scales of the next tile's groups; 4..7: V's
+        auto read_scale = [&](const KvqPiece& a, int j) {
+            if (lane < 2 * kSub) {
+                const int last = (a.nkeys - 1) >> p.blk_shift;
+                next = __ldg((lane < kSub ? p.k_scale : p.v_scale) + a.b * p.s_seq + a.sub / p.n_items +
+                             min((j * kBN + 16 * (lane & 3)) >> p.blk_shift, last) * p.s_blk);
+            }
+        };
+        KvqPiece ahead;
+        bool more = cur.next(p.s, ahead);
+        if (more) read_scale(ahead, ahead.t0);
+        while (more) {
+            it = ahead;
+            more = cur.next(p.s, ahead);
+            float sref = 0.0f;
+            for (int j = it.t0; j < it.t1; ++j, ++t) {
+                const int b = t & 1;
+                const float own = next;
+                if (j + 1 < it.t1) read_scale(it, j + 1);
+                else if (more) read_scale(ahead, ahead.t0);
+                // V's reference scale: the first tile's largest, raised by more than 2^4 only
+                float vm = lane >= kSub && lane < 2 * kSub ? own : 0.0f;
+                vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+                vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+                vm = __shfl_sync(0xffffffffu, vm, kSub);
+                float alpha = 1.0f;
+                if (vm > 16.0f * sref) {
+                    if (sref > 0.0f) alpha = sref / vm;
+                    sref = vm;
+                }
+                const float ratio = fmaxf(own / sref, 0x1p-24f), lv = log2f(ratio), iv = 1.0f / ratio;
+                if (t >= 2) wait(&bar_v_empty[b], (t >> 1) - 1);  // tile t - 2's softmax has read the slot
+                __syncwarp();
+                if (lane < kSub) ts[b].k[lane] = own;
+                if (lane >= kSub && lane < 2 * kSub) {
+                    ts[b].lv[lane - kSub] = lv;
+                    ts[b].iv[lane - kSub] = iv;
+                }
+                if (lane == 0) {
+                    ts[b].alpha = alpha;
+                    ts[b].sref = sref;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_sc[b]);
+            }
         }
         if (!wait.ok) raise_status(p.status, kDevTimeout);
     } else {
@@ -412,7 +480,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int hk = it.sub / p.n_items, row0 = ((it.sub - hk * p.n_items) * 2 + g) * kBM;
             const int nt = it.t1 - it.t0;
             wait(&bar_q_full[qi & 1], qi >> 1);  // also keeps an idle block from arriving for a later item
-            __syncwarp();
             if (row0 >= rows) {  // the last pair of an odd number of row blocks: nothing to do for this one
                 t += nt;
                 if (lane == 0) mbar_arrive(&bar_q_empty[qi & 1]);
@@ -433,7 +500,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t s_cols = tmem + 64 * (2 * g + (tg & 1)) + lane_off;
                 wait(&bar_sc[t & 1], t >> 1);
                 wait(&bar_s_full[g][tg & 1], tg >> 1);
-                __syncwarp();
                 tc_fence_after();
                 if (quarter_live) {
                     const TileScales& sc = ts[t & 1];
@@ -503,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 8; ++e) s[8 * q + e] = pk[e];
                     }
+                    __syncwarp();  // the rows took different branches; tensor-memory accesses are the whole warp's
                     tmem_st16(s_cols, s);
                     tmem_st16(s_cols + 16, s + 16);
                     // Rescaling O needs PV of the previous tile done (this tile's PV waits for
@@ -510,7 +577,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // any row of the warp needs it (alpha = 1 for the others).
                     if (j > it.t0 && __any_sync(0xffffffffu, rescale)) {
                         wait(&bar_pv_done[g][(tg - 1) & 1], (tg - 1) >> 1);
-                        __syncwarp();
                         tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
@@ -529,7 +595,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&bar_q_empty[qi & 1]);  // factors and masks read
             // ----------------------------------------------------- epilogue ---
             wait(&bar_pv_done[g][(tg - 1) & 1], (tg - 1) >> 1);
-            __syncwarp();
             tc_fence_after();
             if (!quarter_live) continue;
             const bool any = row_live && seen && l > 0.0f && wait.ok;

@@ -188,8 +188,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1)
         scales(it.t0);
         for (int step = it.t0; step < it.t1; ++step) {
             const int st = used % kStages;
-            const unsigned char* sk = ring + st * kStageBytes;
-            const unsigned char* sv = sk + kTile;
+            const uint32_t sk = smem_u32(ring) + st * kStageBytes, sv = sk + kTile;
             const int key0 = step * kStep;
             const float kk[2] = {kc[0], kc[1]}, vv[2] = {vc[0], vc[1]};
             if (step + 1 < it.t1) scales(step + 1);
@@ -208,11 +207,10 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1)
             for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) s[hf][nt][0] = s[hf][nt][1] = s[hf][nt][2] = s[hf][nt][3] = 0.0f;
-                const unsigned char* row = sk + (hf * 16 + g) * kKvqHeadDim;  // the swizzle of keys g and g + 8 is the same
-                const uint4 a = *reinterpret_cast<const uint4*>(row + ((t ^ g) << 4));
-                const uint4 b = *reinterpret_cast<const uint4*>(row + (((t + 4) ^ g) << 4));
-                const uint4 c = *reinterpret_cast<const uint4*>(row + 8 * kKvqHeadDim + ((t ^ g) << 4));
-                const uint4 d = *reinterpret_cast<const uint4*>(row + 8 * kKvqHeadDim + (((t + 4) ^ g) << 4));
+                const uint32_t row = sk + (hf * 16 + g) * kKvqHeadDim;  // the swizzle of keys g and g + 8 is the same
+                const uint4 a = lds128(row + ((t ^ g) << 4)), b = lds128(row + (((t + 4) ^ g) << 4));
+                const uint4 c = lds128(row + 8 * kKvqHeadDim + ((t ^ g) << 4));
+                const uint4 d = lds128(row + 8 * kKvqHeadDim + (((t + 4) ^ g) << 4));
                 const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
                 const uint32_t x[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
 #pragma unroll
@@ -309,7 +307,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int key = hf * 16 + (e >> 1) * 8 + 2 * t + (e & 1);
-                    u[e] = *reinterpret_cast<const uint4*>(sv + key * kKvqHeadDim + ((g ^ (key & 7)) << 4));
+                    u[e] = lds128(sv + key * kKvqHeadDim + ((g ^ (key & 7)) << 4));
                     if (tail && key0 + key >= it.nkeys) u[e] = make_uint4(0u, 0u, 0u, 0u);  // unwritten: may be NaN
                 }
                 const uint32_t w[4][4] = {{u[0].x, u[0].y, u[0].z, u[0].w},

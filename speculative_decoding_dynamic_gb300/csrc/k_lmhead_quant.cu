@@ -68,12 +68,28 @@ __device__ __forceinline__ void mma_bf16_16816(float (&c)[4], uint32_t a0, uint3
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 // Codes at bits S and 16 + S of w as bf16 pairs c - 8.
 template <int S>
 __device__ __forceinline__ uint32_t pair(uint32_t w) {
     const uint32_t x = ((w >> S) & 0x000f000fu) | 0x43004300u;  // 128 + c
     const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), __float2bfloat162_rn(136.0f));
     return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// A warp's bounded wait.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 
 // First hidden entry (within a slice) of the eight that lane t of a quad
@@ -211,31 +227,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 2 * MT; ++i) sc[i] = next[i];
                 read_scales(min(slice + kMmaWarps, p.n_slice - 1));
-                if (ok && !__all_sync(0xffffffffu, mbar_wait_sleep(&bar_full[warp][st], (used / p.stages) & 1))) {
+                if (ok && !warp_wait(&bar_full[warp][st], (used / p.stages) & 1)) {
                     ok = false;
                     if (lane == 0) raise_status(p.status, kDevTimeout);
                     for (int f = used + 1; f < filled; ++f)  // copies land before shared memory goes away
-                        mbar_wait_sleep(&bar_full[warp][f % p.stages], (f / p.stages) & 1);
+                        warp_wait(&bar_full[warp][f % p.stages], (f / p.stages) & 1);
                 }
                 ++used;
                 if (!ok) continue;
-                const unsigned char* src = ring + st * kStage;
+                const uint32_t src = smem_u32(ring) + st * kStage;
                 uint32_t w[MT][2][4];
 #pragma unroll
                 for (int a = 0; a < MT; ++a)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const unsigned char* row = src + (a * 16 + g + 8 * e) * kSliceBytes;
+                        const uint32_t row = src + (a * 16 + g + 8 * e) * kSliceBytes;
                         if (GROUP == 128) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(row + t * 16);
+                            const uint4 x = lds128(row + t * 16);
                             w[a][e][0] = x.x, w[a][e][1] = x.y, w[a][e][2] = x.z, w[a][e][3] = x.w;
                         } else if (GROUP == 64) {
-                            const uint2 x = *reinterpret_cast<const uint2*>(row + t * 8);
-                            const uint2 y = *reinterpret_cast<const uint2*>(row + 32 + t * 8);
+                            const uint2 x = lds64(row + t * 8), y = lds64(row + 32 + t * 8);
                             w[a][e][0] = x.x, w[a][e][1] = x.y, w[a][e][2] = y.x, w[a][e][3] = y.y;
                         } else {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) w[a][e][q] = *reinterpret_cast<const uint32_t*>(row + q * 16 + t * 4);
+                            for (int q = 0; q < 4; ++q) w[a][e][q] = lds32(row + q * 16 + t * 4);
                         }
                     }
                 __syncwarp();  // every lane has read the stage
@@ -253,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int b = 0; b < NT; ++b) {
                         const int m = b * 8 + g;
-                        hb[b] = m < rows ? *reinterpret_cast<const uint4*>(hid + m * p.hid_stride + (slice * 16 + q * 4 + t) * 16)
+                        hb[b] = m < rows ? lds128(smem_u32(hid) + m * p.hid_stride + (slice * 16 + q * 4 + t) * 16)
                                          : make_uint4(0u, 0u, 0u, 0u);
                     }
 #pragma unroll
@@ -280,10 +295,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // the tile's partial sums to the adding warps
             const int buf = tile % p.bufs, turn = tile / p.bufs;
-            if (ok && turn > 0 && !__all_sync(0xffffffffu, mbar_wait_sleep(&bar_red_empty[buf], (turn - 1) & 1))) {
+            if (ok && turn > 0 && !warp_wait(&bar_red_empty[buf], (turn - 1) & 1)) {
                 ok = false;
                 if (lane == 0) raise_status(p.status, kDevTimeout);
-                for (int f = used; f < filled; ++f) mbar_wait_sleep(&bar_full[warp][f % p.stages], (f / p.stages) & 1);
+                for (int f = used; f < filled; ++f) warp_wait(&bar_full[warp][f % p.stages], (f / p.stages) & 1);
             }
             float* dst = red + (buf * kMmaWarps + warp) * p.rows * CS + g;
             if (ok) {
@@ -308,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int buf = tile % p.bufs, turn = tile / p.bufs;
             const int v = v0 + tile * RT;
             const int nv = min(RT, min(v1, p.V) - v);  // rows of the tile inside the vocabulary (a multiple of 8)
-            if (!__all_sync(0xffffffffu, mbar_wait_sleep(&bar_red_full[buf], turn & 1))) {
+            if (!warp_wait(&bar_red_full[buf], turn & 1)) {
                 if (lane == 0) raise_status(p.status, kDevTimeout);
                 break;
             }
