@@ -20,7 +20,7 @@
 //   O += P V         tcgen05.mma kind::f16, A = P from tensor memory, B = V as
 //                    fp16 in shared memory (MN-major), converted from the
 //                    tile's codes (exact, one conversion per two elements) by
-//                    four warps of their own, once for both row blocks. P in
+//                    three warps of their own, once for both row blocks. P in
 //                    e4m3 would spare that, at 2^-4 per weight instead of 2^-11.
 // The reference maximum (scale) is raised, and O and the row sum rescaled in
 // place, only when a tile's exceeds it by more than 2^8 (2^4), so the weights
@@ -30,9 +30,9 @@
 // arrive by TMA (128-byte swizzle) in rings of their own; mbarriers order
 // everything and every wait is bounded.
 //
-// Bound by the tensor pipe: 2 x 64 x 128 x 128 multiply-adds per tile and row
-// block, about 630 cycles at the measured bf16 rate, against 256 for the
-// exponentials and about 300 of issue.
+// Bound by the tensor pipe where all overlaps: 2 x 64 x 128 x 128 multiply-adds
+// per tile and row block, about 630 cycles at the measured bf16 rate, against
+// 256 for the exponentials and about 300 of issue.
 
 #include "kvq_sched.cuh"
 
@@ -50,11 +50,12 @@ constexpr int kTile8 = kBN * kHD;        // 8 KB: a K or V tile of codes
 constexpr int kTileV = kBN * kHD * 2;    // 16 KB: V as fp16, two halves of 64 columns
 constexpr int kHalfV = kTileV / 2;
 constexpr int kKStages = 3, kVStages = 2;  // code tiles in flight
-constexpr int kConvWarps = 4, kSoftmaxWarps = 8;
-constexpr int kWarpConv = 2, kWarpSoftmax = kWarpConv + kConvWarps;  // warp 0 TMA, warp 1 MMA of block 0
-constexpr int kWarpScale = kWarpSoftmax + kSoftmaxWarps;
-constexpr int kWarpMma1 = kWarpScale + 1;
-constexpr int kThreads = 32 * (kWarpMma1 + 1);
+constexpr int kScaleSlots = 8;
+// Sixteen warps: 0 copies and scales; 1, 2 QK^T of block 0, 1; 3, 4 PV of block 0, 1;
+// 5..7 converters; 8..11 and 12..15 softmax of block 0 and 1.
+constexpr int kWarpMma = 1, kWarpConv = 5, kWarpSoftmax = 8;
+constexpr int kConvWarps = 3, kSoftmaxWarps = 8;
+constexpr int kThreads = 32 * (kWarpSoftmax + kSoftmaxWarps);
 constexpr int kSmemQ = 0;                                   // [item parity][row block][hi, lo]
 constexpr int kSmemK = 8 * kTileQ;
 constexpr int kSmemV8 = kSmemK + kKStages * kTile8;
@@ -137,6 +138,14 @@ struct Waiter {
         poll(bar, phase);
         __syncwarp();
     }
+    // Two barriers: both first polls in flight together (each answer takes over 100 cycles).
+    template <bool SLEEP = true>
+    __device__ __forceinline__ void both(uint64_t* a, int pa, uint64_t* b, int pb) {
+        const bool ra = mbar_try_wait(a, pa & 1), rb = mbar_try_wait(b, pb & 1);
+        if (!ra) poll<SLEEP>(a, pa);
+        if (!rb) poll<SLEEP>(b, pb);
+        __syncwarp();
+    }
 };
 
 // What the softmax needs of a tile's scales, per 16-key group.
@@ -155,10 +164,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t bar_q_full[2], bar_q_empty[2], bar_k_full[kKStages], bar_k_empty[kKStages],
-        bar_v8_full[kVStages], bar_v8_empty[kVStages], bar_v_full[2], bar_v_empty[2], bar_sc[2], bar_s_full[2][2],
+        bar_v8_full[kVStages], bar_v8_empty[kVStages], bar_v_full[2], bar_v_empty[2], bar_sc[kScaleSlots], bar_s_full[2][2],
         bar_p_full[2][2], bar_pv_done[2][2];
     __shared__ uint32_t tmem_holder;
-    __shared__ TileScales ts[2];
+    __shared__ TileScales ts[kScaleSlots];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int worker = blockIdx.x;
@@ -176,13 +185,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar_q_empty[s], 2 + kSoftmaxWarps);
             mbar_init(&bar_v_full[s], kConvWarps);
             mbar_init(&bar_v_empty[s], 2);
-            mbar_init(&bar_sc[s], 1);
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&bar_pv_done[s][b], 1);
                 mbar_init(&bar_s_full[s][b], 1);
                 mbar_init(&bar_p_full[s][b], 4);
             }
         }
+        for (int s = 0; s < kScaleSlots; ++s) mbar_init(&bar_sc[s], 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -206,110 +215,168 @@ __global__ void __launch_bounds__(kThreads, 1)
     Waiter wait;
 
     if (warp == 0) {
-        // ------------------------------------------------ TMA producers ---
-        // One lane: K tiles (a stage is free once both blocks' QK^T of its
-        // tile are done) and V tiles (free once converted) in turn.
-        if (lane == 0) {
-            int t = 0;
-            while (wait.ok && cur.next(p.s, it)) {
-                const int hk = it.sub / p.n_items;
-                for (int j = it.t0; j < it.t1; ++j, ++t) {
-                    const int sk = t % kKStages, sv = t % kVStages;
-                    if (t >= kKStages) wait.poll(&bar_k_empty[sk], t / kKStages - 1);
-                    if (!wait.ok) break;
+        // --------------------------------------------- copies and scales ---
+        // Step t: once the K stage of tile t is free (both blocks' QK^T of tile
+        // t - 3 done), give the softmax the scales of tile t - 1, read a step ago;
+        // then K of tile t, and V once its stage is free (converted). The free
+        // stage also says that QK(t - 3) had waited for PV(t - 5), so slot
+        // (t - 1) & 7 of the scales is free. (Not a converter's work: the fence
+        // behind each of its tiles would wait for the scales in flight; nor a QK
+        // warp's: it was late for its next tile, 767 against .. us at 70B 32K.)
+        // Lanes 0..3 hold K's scales of a tile's 16-key groups, 4..7 V's.
+        int t = 0, sk = 0, pk = 0;
+        float last_scale = 0.0f, sref = 0.0f, inv_sref = 0.0f;
+        auto give = [&](int tile) {
+            // V's reference scale: the piece's first tile's largest, raised by more than 2^4 only
+            float vm = lane >= kSub && lane < 2 * kSub ? last_scale : 0.0f;
+            vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+            vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+            vm = __shfl_sync(0xffffffffu, vm, kSub);
+            float alpha = 1.0f;
+            if (vm > 16.0f * sref) {
+                if (sref > 0.0f) alpha = sref / vm;
+                sref = vm;
+                inv_sref = 1.0f / vm;
+            }
+            const float ratio = fmaxf(last_scale * inv_sref, 0x1p-24f);
+            TileScales& o = ts[tile & (kScaleSlots - 1)];
+            if (lane < 2 * kSub) (&o.k[0])[lane] = lane < kSub ? last_scale : __log2f(ratio);  // k, then lv
+            if (lane >= kSub && lane < 2 * kSub) o.iv[lane - kSub] = __frcp_rn(ratio);
+            if (lane == 0) o.alpha = alpha;
+            if (lane == 1) o.sref = sref;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_sc[tile & (kScaleSlots - 1)]);
+            __syncwarp();
+        };
+        while (cur.next(p.s, it)) {
+            const int hk = it.sub / p.n_items;
+            const float* src = (lane < kSub ? p.k_scale : p.v_scale) + it.b * p.s_seq + hk;
+            const int last = (it.nkeys - 1) >> p.blk_shift;
+            for (int j = it.t0; j < it.t1; ++j, ++t) {
+                float own = 0.0f;
+                if (lane < 2 * kSub) own = __ldg(src + min((j * kBN + 16 * (lane & 3)) >> p.blk_shift, last) * p.s_blk);
+                if (t >= kKStages) wait(&bar_k_empty[sk], pk ^ 1);
+                if (t > 0) give(t - 1);
+                if (j == it.t0) sref = 0.0f;  // the tile just given was the last piece's
+                last_scale = own;
+                if (lane == 0 && wait.ok) {
                     mbar_arrive_expect_tx(&bar_k_full[sk], kTile8);
                     tma_load_4d(smem + kSmemK + sk * kTile8, &tm_k, 0, hk, j * kBN, it.b, &bar_k_full[sk]);
-                    if (t >= kVStages) wait.poll(&bar_v8_empty[sv], t / kVStages - 1);
-                    if (!wait.ok) {
-                        mbar_wait(&bar_k_full[sk], (t / kKStages) & 1);
-                        break;
-                    }
-                    mbar_arrive_expect_tx(&bar_v8_full[sv], kTile8);
-                    tma_load_4d(smem + kSmemV8 + sv * kTile8, &tm_v, 0, hk, j * kBN, it.b, &bar_v8_full[sv]);
+                }
+                __syncwarp();
+                if (t >= kVStages) wait(&bar_v8_empty[t & 1], (t >> 1) - 1);
+                if (lane == 0 && wait.ok) {
+                    mbar_arrive_expect_tx(&bar_v8_full[t & 1], kTile8);
+                    tma_load_4d(smem + kSmemV8 + (t & 1) * kTile8, &tm_v, 0, hk, j * kBN, it.b, &bar_v8_full[t & 1]);
+                }
+                __syncwarp();
+                if (++sk == kKStages) {
+                    sk = 0;
+                    pk ^= 1;
                 }
             }
-            if (!wait.ok) {  // the copies in flight land before the CTA's shared memory goes away
-                raise_status(p.status, kDevTimeout);
-                for (int f = max(0, t - kKStages); f < t; ++f) mbar_wait(&bar_k_full[f % kKStages], (f / kKStages) & 1);
-                for (int f = max(0, t - kVStages); f < t; ++f) mbar_wait(&bar_v8_full[f % kVStages], (f / kVStages) & 1);
-            }
+        }
+        if (t > 0) give(t - 1);
+        if (!wait.ok) {  // the copies in flight land before the CTA's shared memory goes away
+            if (lane == 0) raise_status(p.status, kDevTimeout);
+            for (int s = 0; s < kKStages; ++s)
+                for (int ph = 0; ph < 2; ++ph) mbar_wait(&bar_k_full[s], ph, 1u << 16);
+            for (int s = 0; s < kVStages; ++s)
+                for (int ph = 0; ph < 2; ++ph) mbar_wait(&bar_v8_full[s], ph, 1u << 16);
         }
         __syncwarp();
-    } else if (warp == 1 || warp == kWarpMma1) {
+    } else if (warp < kWarpConv) {
         // --------------------------------------------------- MMA issuers ---
-        // One warp per row block g: its waits (four a tile) overlap the other's.
-        // Tiles are numbered t over all of
-        // the worker's pieces, and u over those in which the block has rows. QK(u)
-        // goes into S buffer u & 1, over the P that PV(u - 2) reads; the two are
-        // of different kinds and accumulators, which the pipe does not promise to
-        // run in order, so QK waits for that PV's completion. Issue order QK(0)
-        // QK(1) PV(0) QK(2) PV(1) ... A piece's first PV overwrites O: the softmax
-        // threads have read the previous piece's O before they arrive for it. A
-        // PV's completion is told on one of two barriers in turn: when the softmax
-        // waits for PV(u) the one before may still be running, and a single
-        // barrier's parity would be taken for the phase before.
-        constexpr uint32_t id_qk = idesc_type0(kBM, kBN, 0);
-        constexpr uint32_t id_pv = idesc_type0(kBM, kHD, 1);
+        // Per row block g one warp issues QK^T and one PV: a wait for a phase long
+        // complete takes over 100 cycles, an MMA's issue about 20, and one warp
+        // for both kinds took 2000 cycles a tile (for both blocks as well, 2660).
+        // Tiles are numbered t over all of the worker's pieces, and u over those
+        // in which the block has rows. QK(u) goes into S buffer u & 1, over the P
+        // that PV(u - 2) reads, so it waits for that PV's completion. A piece's
+        // first PV overwrites O: the softmax threads have read the previous piece's
+        // O before they arrive for it. A PV's completion is told on one of two
+        // barriers in turn: when the softmax waits for PV(u) the one before may
+        // still be running, and a single barrier's parity would be taken for the
+        // phase before.
         const uint32_t lead = elect_one();
         const uint32_t base = smem_u32(smem), tm = uniform(tmem);
-        const int g = uniform(warp == 1 ? 0 : 1);
+        const int role = uniform(warp - kWarpMma);  // QK of block 0, 1, PV of block 0, 1
+        const int g = role & 1;
         const int blocks = (rows + kBM - 1) / kBM;
         const uint32_t tS = tm + 128 * g, tO = tm + 256 + 128 * g;
-        int t = 0, qi = 0, u = 0;
+        int t = 0, u = 0;
+        int sk = 0, pk = 0;  // K stage of tile t and its phase
+        auto next_k = [&]() {
+            if (++sk == kKStages) {
+                sk = 0;
+                pk ^= 1;
+            }
+        };
         auto spin = [&](uint64_t* bar, int phase) {
             wait.poll<false>(bar, phase);
             __syncwarp();
         };
-        auto pv = [&](int tp, int up, bool first) {
-            spin(&bar_v_full[tp & 1], tp >> 1);
-            spin(&bar_p_full[g][up & 1], up >> 1);
-            tc_fence_after();
-            const uint32_t aV = base + kSmemV + (tp & 1) * kTileV;
-#pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk)  // A = P from TMEM: 16 keys = 8 columns per MMA
-                mma_f16_ts(lead, tO, tS + 64 * (up & 1) + kk * 8, smem_desc(aV + kk * 2048, kHalfV, 1024), id_pv,
-                           (!first || kk > 0) ? 1 : 0);
-            commit(lead, &bar_pv_done[g][up & 1]);
-            commit(lead, &bar_v_empty[tp & 1]);
-        };
-        for (;;) {
-            const bool more = cur.next(p.s, it);
-            if (!uniform(more)) break;
-            const int n_tiles = uniform(it.t1 - it.t0);
-            const bool live = uniform((it.sub % p.n_items) * 2 + g) < blocks;
-            const uint32_t aQ = base + kSmemQ + ((qi & 1) * 4 + 2 * g) * kTileQ;
-            spin(&bar_q_full[qi & 1], qi >> 1);
-            if (!live) {  // a block without rows: keep the shared barriers' counts, in step
-                for (int j = 0; j < n_tiles; ++j, ++t) {
-                    spin(&bar_k_full[t % kKStages], t / kKStages);
-                    if (lane == 0) mbar_arrive(&bar_k_empty[t % kKStages]);
-                    spin(&bar_v_full[t & 1], t >> 1);
-                    if (lane == 0) mbar_arrive(&bar_v_empty[t & 1]);
+        if (role < 2) {
+            constexpr uint32_t id_qk = idesc_type0(kBM, kBN, 0);
+            for (int qi = 0;; ++qi) {
+                const bool more = cur.next(p.s, it);
+                if (!uniform(more)) break;
+                const int n_tiles = uniform(it.t1 - it.t0);
+                const bool live = uniform((it.sub % p.n_items) * 2 + g) < blocks;
+                const uint32_t aQ = base + kSmemQ + ((qi & 1) * 4 + 2 * g) * kTileQ;
+                spin(&bar_q_full[qi & 1], qi >> 1);
+                if (!live) {  // a block without rows: keep the shared barriers' counts, in step
+                    for (int j = 0; j < n_tiles; ++j, ++t, next_k()) {
+                        wait(&bar_k_full[sk], pk);
+                        if (lane == 0) mbar_arrive(&bar_k_empty[sk]);
+                    }
+                    if (lane == 0) mbar_arrive(&bar_q_empty[qi & 1]);
+                    continue;
                 }
-                if (lane == 0) mbar_arrive(&bar_q_empty[qi & 1]);
-                ++qi;
-                continue;
-            }
-            for (int j = 0; j < n_tiles; ++j, ++t, ++u) {
-                const int sk = t % kKStages;
-                spin(&bar_k_full[sk], t / kKStages);
-                if (u >= 2) spin(&bar_pv_done[g][u & 1], (u >> 1) - 1);
-                tc_fence_after();
-                const uint32_t aK = base + kSmemK + sk * kTile8;
+                for (int j = 0; j < n_tiles; ++j, ++t, ++u, next_k()) {
+                    if (u >= 2) wait.both<false>(&bar_k_full[sk], pk, &bar_pv_done[g][u & 1], (u >> 1) - 1);
+                    else spin(&bar_k_full[sk], pk);
+                    tc_fence_after();
+                    const uint32_t aK = base + kSmemK + sk * kTile8;
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)  // hi (0..3), lo (4..7); 32 elements of the head dimension each
-                    mma_f8(lead, tS + 64 * (u & 1), smem_desc(aQ + (kk >> 2) * kTileQ + (kk & 3) * 32, 16, 1024),
-                           smem_desc(aK + (kk & 3) * 32, 16, 1024), id_qk, kk > 0);
-                commit(lead, &bar_s_full[g][u & 1]);
-                commit(lead, &bar_k_empty[sk]);
-                if (j == n_tiles - 1) commit(lead, &bar_q_empty[qi & 1]);
-                if (j > 0) pv(t - 1, u - 1, j == 1);
+                    for (int kk = 0; kk < 8; ++kk)  // hi (0..3), lo (4..7); 32 elements of the head dimension each
+                        mma_f8(lead, tS + 64 * (u & 1), smem_desc(aQ + (kk >> 2) * kTileQ + (kk & 3) * 32, 16, 1024),
+                               smem_desc(aK + (kk & 3) * 32, 16, 1024), id_qk, kk > 0);
+                    commit(lead, &bar_s_full[g][u & 1]);
+                    commit(lead, &bar_k_empty[sk]);
+                    if (j == n_tiles - 1) commit(lead, &bar_q_empty[qi & 1]);
+                }
             }
-            pv(t - 1, u - 1, n_tiles == 1);
-            ++qi;
+            // the last commits' arrivals come before the CTA's shared memory goes away
+            if (t > 0) wait(&bar_k_empty[(t - 1) % kKStages], (t - 1) / kKStages);
+        } else {
+            constexpr uint32_t id_pv = idesc_type0(kBM, kHD, 1);
+            for (;;) {
+                const bool more = cur.next(p.s, it);
+                if (!uniform(more)) break;
+                const int n_tiles = uniform(it.t1 - it.t0);
+                const bool live = uniform((it.sub % p.n_items) * 2 + g) < blocks;
+                if (!live) {
+                    for (int j = 0; j < n_tiles; ++j, ++t) {
+                        wait(&bar_v_full[t & 1], t >> 1);
+                        if (lane == 0) mbar_arrive(&bar_v_empty[t & 1]);
+                    }
+                    continue;
+                }
+                for (int j = 0; j < n_tiles; ++j, ++t, ++u) {
+                    wait.both<false>(&bar_v_full[t & 1], t >> 1, &bar_p_full[g][u & 1], u >> 1);
+                    tc_fence_after();
+                    const uint32_t aV = base + kSmemV + (t & 1) * kTileV;
+#pragma unroll
+                    for (int kk = 0; kk < kBN / 16; ++kk)  // A = P from TMEM: 16 keys = 8 columns per MMA
+                        mma_f16_ts(lead, tO, tS + 64 * (u & 1) + kk * 8, smem_desc(aV + kk * 2048, kHalfV, 1024), id_pv,
+                                   (j > 0 || kk > 0) ? 1 : 0);
+                    commit(lead, &bar_pv_done[g][u & 1]);
+                    commit(lead, &bar_v_empty[t & 1]);
+                }
+            }
+            if (t > 0) wait(&bar_v_empty[(t - 1) & 1], (t - 1) >> 1);
         }
-        // the last commits' arrivals come before the CTA's shared memory goes away
-        if (t > 0) spin(&bar_v_empty[(t - 1) & 1], (t - 1) >> 1);
         if (!wait.ok) raise_status(p.status, kDevTimeout);
     } else if (warp < kWarpSoftmax) {
         // ----------------------------------------------------- converters ---
@@ -385,10 +452,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int b = t & 1;
                 if (t >= 2) wait(&bar_v_empty[b], (t >> 1) - 1);
                 const int st = t % kVStages;
+                static_assert(kVStages == 2, "stage of V tile t: t & 1");
                 wait(&bar_v8_full[st], t / kVStages);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int key = lane + 32 * (e & 1), c16 = 2 * cw + (e >> 1);
+                for (int e = 0; e < 6; ++e) {  // chunks cw, cw + 3, cw + 6 of 16 columns, two keys each
+                    const int key = lane + 32 * (e & 1), c16 = cw + kConvWarps * (e >> 1);
+                    if (c16 >= 8) break;
                     uint4 u = lds128(base + kSmemV8 + st * kTile8 + key * kHD + ((c16 ^ (key & 7)) << 4));
                     // keys that no row can see may hold anything (even NaN): 0 * V has to stay 0
                     if (j * kBN + key >= it.nkeys) u = make_uint4(0u, 0u, 0u, 0u);
@@ -408,59 +477,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (more && j == min(it.t0 + 1, it.t1 - 1)) convert_q(ahead, qi + 1);
             }
             ++qi;
-        }
-        if (!wait.ok) raise_status(p.status, kDevTimeout);
-    } else if (warp == kWarpScale) {
-        // --------------------------------------------------------- scales ---
-        // What the softmax needs of the tiles' scales, read a tile ahead. A warp
-        // of its own: in a converter the fence behind each tile would wait for
-        // the scales in flight (8B b64: 211 us instead of the figure above).
-        int t = 0;
-        float next = 0.0f;  // lanes 0..3: K's scales of the next tile's groups; 4..7: V's
-        auto read_scale = [&](const KvqPiece& a, int j) {
-            if (lane < 2 * kSub) {
-                const int last = (a.nkeys - 1) >> p.blk_shift;
-                next = __ldg((lane < kSub ? p.k_scale : p.v_scale) + a.b * p.s_seq + a.sub / p.n_items +
-                             min((j * kBN + 16 * (lane & 3)) >> p.blk_shift, last) * p.s_blk);
-            }
-        };
-        KvqPiece ahead;
-        bool more = cur.next(p.s, ahead);
-        if (more) read_scale(ahead, ahead.t0);
-        while (more) {
-            it = ahead;
-            more = cur.next(p.s, ahead);
-            float sref = 0.0f;
-            for (int j = it.t0; j < it.t1; ++j, ++t) {
-                const int b = t & 1;
-                const float own = next;
-                if (j + 1 < it.t1) read_scale(it, j + 1);
-                else if (more) read_scale(ahead, ahead.t0);
-                // V's reference scale: the first tile's largest, raised by more than 2^4 only
-                float vm = lane >= kSub && lane < 2 * kSub ? own : 0.0f;
-                vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
-                vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
-                vm = __shfl_sync(0xffffffffu, vm, kSub);
-                float alpha = 1.0f;
-                if (vm > 16.0f * sref) {
-                    if (sref > 0.0f) alpha = sref / vm;
-                    sref = vm;
-                }
-                const float ratio = fmaxf(own / sref, 0x1p-24f), lv = log2f(ratio), iv = 1.0f / ratio;
-                if (t >= 2) wait(&bar_v_empty[b], (t >> 1) - 1);  // tile t - 2's softmax has read the slot
-                __syncwarp();
-                if (lane < kSub) ts[b].k[lane] = own;
-                if (lane >= kSub && lane < 2 * kSub) {
-                    ts[b].lv[lane - kSub] = lv;
-                    ts[b].iv[lane - kSub] = iv;
-                }
-                if (lane == 0) {
-                    ts[b].alpha = alpha;
-                    ts[b].sref = sref;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar_sc[b]);
-            }
         }
         if (!wait.ok) raise_status(p.status, kDevTimeout);
     } else {
@@ -498,11 +514,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = it.t0; j < it.t1; ++j, ++t, ++tg) {
                 const int key0 = j * kBN;
                 const uint32_t s_cols = tmem + 64 * (2 * g + (tg & 1)) + lane_off;
-                wait(&bar_sc[t & 1], t >> 1);
-                wait(&bar_s_full[g][tg & 1], tg >> 1);
+                wait.both(&bar_sc[t & (kScaleSlots - 1)], t / kScaleSlots, &bar_s_full[g][tg & 1], tg >> 1);
                 tc_fence_after();
                 if (quarter_live) {
-                    const TileScales& sc = ts[t & 1];
+                    const TileScales& sc = ts[t & (kScaleSlots - 1)];
                     const float4 k4 = *reinterpret_cast<const float4*>(sc.k), lv4 = *reinterpret_cast<const float4*>(sc.lv);
                     const float4 iv4 = *reinterpret_cast<const float4*>(sc.iv);
                     const float k[kSub] = {k4.x * fac, k4.y * fac, k4.z * fac, k4.w * fac};
@@ -570,8 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 8; ++e) s[8 * q + e] = pk[e];
                     }
                     __syncwarp();  // the rows took different branches; tensor-memory accesses are the whole warp's
-                    tmem_st16(s_cols, s);
-                    tmem_st16(s_cols + 16, s + 16);
+                    tmem_st32(s_cols, reinterpret_cast<const float*>(s));
                     // Rescaling O needs PV of the previous tile done (this tile's PV waits for
                     // this warp's arrival below). tcgen05.ld/st are warp-collective: rescale if
                     // any row of the warp needs it (alpha = 1 for the others).
