@@ -56,6 +56,7 @@ constexpr int kScaleSlots = 8;
 constexpr int kWarpMma = 1, kWarpConv = 5, kWarpSoftmax = 8;
 constexpr int kConvWarps = 3, kSoftmaxWarps = 8;
 constexpr int kThreads = 32 * (kWarpSoftmax + kSoftmaxWarps);
+constexpr int kPassRows = kConvWarps * 16;  // rows of q that the converters take at once
 constexpr int kSmemQ = 0;                                   // [item parity][row block][hi, lo]
 constexpr int kSmemK = 8 * kTileQ;
 constexpr int kSmemV8 = kSmemK + kKStages * kTile8;
@@ -148,6 +149,70 @@ struct Waiter {
     }
 };
 
+// Half a row of q (64 elements; two neighbouring lanes hold a row): load, then
+// store as two e4m3 parts with the row's factor and mask words.
+struct HalfRow {
+    uint4 u[8];
+    int r, h, slot;
+    bool in, live;  // in: a row of a block that has rows; live: a row of the problem
+    const uint32_t* mask;
+    // row r (0..255) of the pair of row blocks of piece a
+    __device__ __forceinline__ void load(const KvqAttnParams& p, const KvqPiece& a, int row, int half, int rows) {
+        r = row;
+        h = half;
+        const int hk = a.sub / p.n_items, row0 = (a.sub - hk * p.n_items) * 2 * kBM;
+        in = r < 2 * kBM && row0 + (r & kBM) < rows;
+        slot = (row0 + r) / p.G;
+        live = in && slot < p.s.T;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + ((static_cast<size_t>(a.b) * p.s.T + slot) * p.Hq + static_cast<size_t>(hk) * p.G + (row0 + r - slot * p.G)) * kHD +
+            64 * h);
+        mask = p.mask ? p.mask + (static_cast<size_t>(a.b) * p.s.T + slot) * p.W : nullptr;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = live ? __ldg(src + e) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void store(const KvqAttnParams& p, unsigned char* sq, float* fac, uint32_t* mask_sm) {
+        uint32_t mx = 0u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(u[e].x & 0x7fff7fffu, u[e].y & 0x7fff7fffu),
+                                       __vmaxu2(u[e].z & 0x7fff7fffu, u[e].w & 0x7fff7fffu)));
+        mx = max(mx & 0xffffu, mx >> 16);
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        if (!in) return;
+        for (int w = h; w < p.W; w += 2) {  // the row's mask words
+            uint32_t m = 0u;
+            if (live) {
+                if (mask) m = __ldg(mask + w);
+                else m = slot >= 32 * w + 31 ? ~0u : slot < 32 * w ? 0u : (2u << (slot - 32 * w)) - 1u;
+            }
+            mask_sm[r * p.W + w] = m;
+        }
+        const float s = pow2_to(__uint_as_float(mx << 16), 7);
+        if (h == 0) fac[r] = p.scale_log2 / s;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {  // 16 elements: one 16-byte chunk of each part
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint4& v = u[2 * c + (e >> 1)];
+                const uint32_t w0 = (e & 1) ? v.z : v.x, w1 = (e & 1) ? v.w : v.y;
+                const float x[4] = {__uint_as_float(w0 << 16) * s, __uint_as_float(w0 & 0xffff0000u) * s,
+                                    __uint_as_float(w1 << 16) * s, __uint_as_float(w1 & 0xffff0000u) * s};
+                const uint32_t h0 = e4m3x2(x[0], x[1]), h1 = e4m3x2(x[2], x[3]);
+                const uint32_t f0 = e4m3_to_f16x2(h0), f1 = e4m3_to_f16x2(h1);
+                const float2 b0 = __half22float2(*reinterpret_cast<const __half2*>(&f0));
+                const float2 b1 = __half22float2(*reinterpret_cast<const __half2*>(&f1));
+                hi[e] = h0 | (h1 << 16);
+                lo[e] = e4m3x2(x[0] - b0.x, x[1] - b0.y) | (e4m3x2(x[2] - b1.x, x[3] - b1.y) << 16);
+            }
+            unsigned char* dst = sq + (r >> 7) * 2 * kTileQ + (r & 127) * kHD + (((4 * h + c) ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(dst + kTileQ) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
+};
+
 // What the softmax needs of a tile's scales, per 16-key group.
 struct alignas(16) TileScales {
     float k[kSub];   // K's scale
@@ -204,15 +269,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     KvqCursor cur;
     cur.init(p.s, worker);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_holder;
     const int rows = p.G * p.s.T;
     float* fac_sm = reinterpret_cast<float*>(smem + kSmemFac);
     uint32_t* mask_sm = reinterpret_cast<uint32_t*>(smem + kSmemMask);
     KvqPiece it;
     Waiter wait;
+    {  // the first item's q: half a row per thread
+        KvqCursor c = cur;
+        if (c.next(p.s, it)) {
+            static_assert(kThreads == 4 * kBM, "two threads per row of both blocks");
+            HalfRow hr;
+            hr.load(p, it, threadIdx.x >> 1, threadIdx.x & 1, rows);
+            hr.store(p, smem + kSmemQ, fac_sm, mask_sm);
+            fence_proxy_async_smem();  // the MMA reads q through the async proxy
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_holder;
 
     if (warp == 0) {
         // --------------------------------------------- copies and scales ---
@@ -380,77 +455,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait.ok) raise_status(p.status, kDevTimeout);
     } else if (warp < kWarpSoftmax) {
         // ----------------------------------------------------- converters ---
-        // V codes to fp16, and q, row factors and mask words of the next item
-        // while the current one runs.
+        // V codes to fp16, and q of the next item while the current one runs.
         const int cw = warp - kWarpConv;
         const uint32_t base = smem_u32(smem);
         const int i = threadIdx.x - kWarpConv * 32;
-        auto convert_q = [&](const KvqPiece& a, int qi) {
-            if (qi >= 2) wait(&bar_q_empty[qi & 1], (qi >> 1) - 1);
-            const int hk = a.sub / p.n_items, row0 = (a.sub - hk * p.n_items) * 2 * kBM;
-            unsigned char* sq = smem + kSmemQ + (qi & 1) * 4 * kTileQ;
-            const int h = i & 1;
-            for (int r = i >> 1; r < 2 * kBM && row0 + (r & kBM) < rows; r += kConvWarps * 16) {  // half a row per thread
-                const int slot = (row0 + r) / p.G;
-                const bool live = slot < p.s.T;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    p.q + ((static_cast<size_t>(a.b) * p.s.T + slot) * p.Hq + static_cast<size_t>(hk) * p.G +
-                           (row0 + r - slot * p.G)) * kHD + 64 * h);
-                uint4 u[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = live ? __ldg(src + e) : make_uint4(0u, 0u, 0u, 0u);
-                for (int w = h; w < p.W; w += 2) {  // the row's mask words
-                    uint32_t m = 0u;
-                    if (live) {
-                        if (p.mask) m = __ldg(&p.mask[(static_cast<size_t>(a.b) * p.s.T + slot) * p.W + w]);
-                        else m = slot >= 32 * w + 31 ? ~0u : slot < 32 * w ? 0u : (2u << (slot - 32 * w)) - 1u;
-                    }
-                    mask_sm[((qi & 1) * 2 * kBM + r) * p.W + w] = m;
-                }
-                uint32_t mx = 0u;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(u[e].x & 0x7fff7fffu, u[e].y & 0x7fff7fffu),
-                                               __vmaxu2(u[e].z & 0x7fff7fffu, u[e].w & 0x7fff7fffu)));
-                mx = max(mx & 0xffffu, mx >> 16);
-                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                const float s = pow2_to(__uint_as_float(mx << 16), 7);
-                if (h == 0) fac_sm[(qi & 1) * 2 * kBM + r] = p.scale_log2 / s;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {  // 16 elements: one 16-byte chunk of each part
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint4& v = u[2 * c + (e >> 1)];
-                        const uint32_t w0 = (e & 1) ? v.z : v.x, w1 = (e & 1) ? v.w : v.y;
-                        const float x[4] = {__uint_as_float(w0 << 16) * s, __uint_as_float(w0 & 0xffff0000u) * s,
-                                            __uint_as_float(w1 << 16) * s, __uint_as_float(w1 & 0xffff0000u) * s};
-                        const uint32_t h0 = e4m3x2(x[0], x[1]), h1 = e4m3x2(x[2], x[3]);
-                        const uint32_t f0 = e4m3_to_f16x2(h0), f1 = e4m3_to_f16x2(h1);
-                        const float2 b0 = __half22float2(*reinterpret_cast<const __half2*>(&f0));
-                        const float2 b1 = __half22float2(*reinterpret_cast<const __half2*>(&f1));
-                        hi[e] = h0 | (h1 << 16);
-                        lo[e] = e4m3x2(x[0] - b0.x, x[1] - b0.y) | (e4m3x2(x[2] - b1.x, x[3] - b1.y) << 16);
-                    }
-                    unsigned char* dst = sq + (r >> 7) * 2 * kTileQ + (r & 127) * kHD + (((4 * h + c) ^ (r & 7)) << 4);
-                    *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(dst + kTileQ) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
-            }
-            fence_proxy_async_smem();  // the MMA reads q through the async proxy
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_q_full[qi & 1]);
-        };
         int t = 0, qi = 0;
         KvqPiece ahead;
         bool more = cur.next(p.s, ahead);
-        if (more) convert_q(ahead, 0);
+        if (more && lane == 0) mbar_arrive(&bar_q_full[0]);  // converted by the whole CTA
         while (more) {
             it = ahead;
             more = cur.next(p.s, ahead);
+            // The next item's q in passes of 48 rows, one behind each tile: its loads
+            // are in flight while the warp waits for the next tile. (All at once they
+            // held up V for 11,000 cycles per item.)
+            int pass = 0;
+            const int passes = !more ? 0 : (min(2 * kBM, rows - (ahead.sub % p.n_items) * 2 * kBM + kBM - 1) / kBM * kBM + kPassRows - 1) / kPassRows;
+            bool loaded = false;
+            HalfRow hr;
+            auto load_pass = [&]() {
+                if (pass == passes) return;
+                if (pass == 0 && qi >= 1) wait(&bar_q_empty[(qi + 1) & 1], ((qi + 1) >> 1) - 1);
+                hr.load(p, ahead, pass * kPassRows + (i >> 1), i & 1, rows);
+                loaded = true;
+            };
+            auto store_pass = [&]() {
+                if (!loaded) return;
+                hr.store(p, smem + kSmemQ + ((qi + 1) & 1) * 4 * kTileQ, fac_sm + ((qi + 1) & 1) * 2 * kBM,
+                         mask_sm + ((qi + 1) & 1) * 2 * kBM * p.W);
+                loaded = false;
+                if (++pass == passes) {
+                    fence_proxy_async_smem();  // the MMA reads q through the async proxy
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar_q_full[(qi + 1) & 1]);
+                }
+            };
             for (int j = it.t0; j < it.t1; ++j, ++t) {
                 const int b = t & 1;
                 if (t >= 2) wait(&bar_v_empty[b], (t >> 1) - 1);
+                store_pass();
                 const int st = t % kVStages;
                 static_assert(kVStages == 2, "stage of V tile t: t & 1");
                 wait(&bar_v8_full[st], t / kVStages);
@@ -474,7 +517,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&bar_v8_empty[st]);
                     mbar_arrive(&bar_v_full[b]);
                 }
-                if (more && j == min(it.t0 + 1, it.t1 - 1)) convert_q(ahead, qi + 1);
+                load_pass();
+            }
+            store_pass();
+            while (pass < passes) {  // fewer tiles than passes
+                load_pass();
+                store_pass();
             }
             ++qi;
         }
@@ -566,24 +614,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     // P = 2^(s k - m_use + lv), two per packed multiply-add; the row sum takes the
                     // reverse of V's ratio. P as fp16 pairs over the first 32 columns of S.
-#pragma unroll
-                    for (int q = 0; q < kSub; ++q) {
+                    // (A group's arguments, then its exponentials, then the last group's sums and
+                    // pairs, in place: taken pair by pair every step waited for the one before.)
+                    auto arguments = [&](int q) {
                         const float c = lv[q] - m_use;
                         const uint64_t k2 = f2_pack(k[q], k[q]), c2 = f2_pack(c, c);
-                        uint64_t acc = 0ull;
-                        uint32_t pk[8];
+#pragma unroll
+                        for (int e = 16 * q; e < 16 * q + 16; e += 2) {
+                            const uint64_t z = f2_fma((static_cast<uint64_t>(s[e + 1]) << 32) | s[e], k2, c2);
+                            s[e] = __float_as_uint(f2_lo(z));
+                            s[e + 1] = __float_as_uint(f2_hi(z));
+                        }
+                    };
+                    auto exponentials = [&](int q) {
+#pragma unroll
+                        for (int e = 16 * q; e < 16 * q + 16; ++e) s[e] = __float_as_uint(ex2_approx(__uint_as_float(s[e])));
+                    };
+                    auto sum_and_pack = [&](int q) {
+                        uint64_t a[2];
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
-                            const uint64_t sp = (static_cast<uint64_t>(s[16 * q + e + 1]) << 32) | s[16 * q + e];
-                            const uint64_t z = f2_fma(sp, k2, c2);
-                            const float w0 = ex2_approx(f2_lo(z)), w1 = ex2_approx(f2_hi(z));
-                            acc = e == 0 ? f2_pack(w0, w1) : f2_add(acc, f2_pack(w0, w1));
-                            pk[e >> 1] = pack_f16(w0, w1);
+                            const uint64_t w = (static_cast<uint64_t>(s[16 * q + e + 1]) << 32) | s[16 * q + e];
+                            a[(e >> 1) & 1] = e < 4 ? w : f2_add(a[(e >> 1) & 1], w);
                         }
-                        l = fmaf(f2_lo(acc) + f2_hi(acc), iv[q], l);
+                        const uint64_t a2 = f2_add(a[0], a[1]);
+                        l = fmaf(f2_lo(a2) + f2_hi(a2), iv[q], l);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) s[8 * q + e] = pk[e];
+                        for (int e = 0; e < 8; ++e)
+                            s[8 * q + e] = pack_f16(__uint_as_float(s[16 * q + 2 * e]), __uint_as_float(s[16 * q + 2 * e + 1]));
+                    };
+                    arguments(0);
+#pragma unroll
+                    for (int q = 0; q < kSub; ++q) {
+                        if (q + 1 < kSub) arguments(q + 1);
+                        exponentials(q);
+                        if (q > 0) sum_and_pack(q - 1);
                     }
+                    sum_and_pack(kSub - 1);
                     __syncwarp();  // the rows took different branches; tensor-memory accesses are the whole warp's
                     tmem_st32(s_cols, reinterpret_cast<const float*>(s));
                     // Rescaling O needs PV of the previous tile done (this tile's PV waits for
