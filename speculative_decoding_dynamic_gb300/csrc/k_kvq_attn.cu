@@ -2,8 +2,7 @@
 // GQA attention for more than 16 query rows per KV head.
 //
 // For sequence b and KV head hk the G = Hq/Hkv query heads of every tree slot
-// form G*T query rows (row r <-> slot r / G, head hk*G + r % G), in row blocks
-// of 128. An item is a pair of row blocks with all keys; a worker (one CTA per
+// form G*T query rows, in row blocks of 128. An item is a pair of row blocks with all keys; a worker (one CTA per
 // SM) walks its pieces of items (kvq_sched.cuh) in key tiles of 64. Per tile t
 // and row block g of the pair:
 //   S = q K^T        tcgen05.mma kind::f8f6f4 straight from the codes: a row
@@ -11,7 +10,9 @@
 //                    into two e4m3 operands q = hi + lo (eight significant
 //                    bits in all, those of bf16; elements below 2^-9 of the
 //                    row's largest lose some), two MMAs at twice the fp16
-//                    rate. K needs no conversion and its tile is half the size.
+//                    rate, by a small kernel before this one. (K to bf16 and q
+//                    as it is: 945 us at 70B 32K, for the conversion of K and the
+//                    larger tiles' traffic through shared memory.)
 //   P = softmax part four warps, one thread per row (TMEM lane = row, 64 key
 //                    columns): K's block scale and q's row scale, tree mask,
 //                    exponentials in the log2 domain against a reference
@@ -26,7 +27,7 @@
 // place, only when a tile's exceeds it by more than 2^8 (2^4), so the weights
 // stay below 2^12. S is double buffered per row block: while one block's
 // softmax works, the tensor pipe serves the other and the next tile. q of the
-// next item is converted while the current one runs (double buffered). Codes
+// next item arrives while the current one runs (double buffered). Codes
 // arrive by TMA (128-byte swizzle) in rings of their own; mbarriers order
 // everything and every wait is bounded.
 //
@@ -49,20 +50,18 @@ constexpr int kTileQ = kBM * kHD;        // 16 KB: one e4m3 part of a row block'
 constexpr int kTile8 = kBN * kHD;        // 8 KB: a K or V tile of codes
 constexpr int kTileV = kBN * kHD * 2;    // 16 KB: V as fp16, two halves of 64 columns
 constexpr int kHalfV = kTileV / 2;
-constexpr int kKStages = 3, kVStages = 2;  // code tiles in flight
+constexpr int kKStages = 3;              // K tiles in flight (V tiles: 2)
 constexpr int kScaleSlots = 8;
 // Sixteen warps: 0 copies and scales; 1, 2 QK^T of block 0, 1; 3, 4 PV of block 0, 1;
 // 5..7 converters; 8..11 and 12..15 softmax of block 0 and 1.
 constexpr int kWarpMma = 1, kWarpConv = 5, kWarpSoftmax = 8;
 constexpr int kConvWarps = 3, kSoftmaxWarps = 8;
 constexpr int kThreads = 32 * (kWarpSoftmax + kSoftmaxWarps);
-constexpr int kPassRows = kConvWarps * 16;  // rows of q that the converters take at once
-constexpr int kSmemQ = 0;                                   // [item parity][row block][hi, lo]
+constexpr int kSmemQ = 0;  // [item parity][row block][hi, lo]
 constexpr int kSmemK = 8 * kTileQ;
 constexpr int kSmemV8 = kSmemK + kKStages * kTile8;
-constexpr int kSmemV = kSmemV8 + kVStages * kTile8;         // fp16 V of tile t at kSmemV + (t & 1) * kTileV
-constexpr int kSmemFac = kSmemV + 2 * kTileV;               // [item parity][256] row factors
-constexpr int kSmemMask = kSmemFac + 2 * 2 * kBM * 4;       // [item parity][256][W] mask words
+constexpr int kSmemV = kSmemV8 + 2 * kTile8;        // [tile parity]
+constexpr int kSmem = kSmemV + 2 * kTileV + 1024;   // and alignment slack
 constexpr int kTmemCols = 512;  // S of row block g, buffer b at 64 (2g + b) (P over it), O of block g at 256 + 128 g
 
 // kind::f8f6f4, both operands e4m3 (type 0), fp32 accumulate; kind::f16 with both fp16 (type 0).
@@ -111,12 +110,6 @@ __device__ __forceinline__ float max16(const uint32_t* v) {
     return fmaxf(fmax3(a, b, c), fmax3(d, e, f(15)));
 }
 
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low byte
-    uint16_t d;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(b), "f"(a));
-    return d;
-}
-
 // Bounded waits of a whole warp. Every lane polls: tensor-memory instructions
 // want the warp converged, which one lane's polls and a warp barrier do not
 // promise. SLEEP: a short nap between polls, for the waits that are long
@@ -149,69 +142,63 @@ struct Waiter {
     }
 };
 
-// Half a row of q (64 elements; two neighbouring lanes hold a row): load, then
-// store as two e4m3 parts with the row's factor and mask words.
-struct HalfRow {
-    uint4 u[8];
-    int r, h, slot;
-    bool in, live;  // in: a row of a block that has rows; live: a row of the problem
-    const uint32_t* mask;
-    // row r (0..255) of the pair of row blocks of piece a
-    __device__ __forceinline__ void load(const KvqAttnParams& p, const KvqPiece& a, int row, int half, int rows) {
-        r = row;
-        h = half;
-        const int hk = a.sub / p.n_items, row0 = (a.sub - hk * p.n_items) * 2 * kBM;
-        in = r < 2 * kBM && row0 + (r & kBM) < rows;
-        slot = (row0 + r) / p.G;
-        live = in && slot < p.s.T;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + ((static_cast<size_t>(a.b) * p.s.T + slot) * p.Hq + static_cast<size_t>(hk) * p.G + (row0 + r - slot * p.G)) * kHD +
-            64 * h);
-        mask = p.mask ? p.mask + (static_cast<size_t>(a.b) * p.s.T + slot) * p.W : nullptr;
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low byte
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(b), "f"(a));
+    return d;
+}
+
+// q as two e4m3 parts: s x = hi + lo for a row x, s the power of two that
+// brings its largest element into [128, 256); the softmax's factor log2(e) /
+// (s sqrt(128)). From [B][T][Hq][128] to [B][Hkv][hi, lo][G*T][128] and
+// [B][Hkv][G*T]. Sixteen lanes take a row, two rows each (both loads first).
+// Moves 4 bytes per element; at 8B b64, 31 MB each way.
+// (In the attention kernel, by its converters behind their tiles, it held up
+// each item by 11,000 cycles: the fence behind a converted tile waits for the
+// loads of q in flight.)
+constexpr int kSplitThreads = 256, kSplitRows = 2 * kSplitThreads / 16;
+__global__ void __launch_bounds__(kSplitThreads)
+    kvq_split_q_kernel(const __nv_bfloat16* __restrict__ q, uint2* __restrict__ dst, float* __restrict__ fac, KvqRows rows,
+                       int Hkv, int64_t n, float scale_log2) {
+    pdl_wait_prior();
+    pdl_launch_dependents();
+    const int l16 = threadIdx.x & 15;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSplitRows + (threadIdx.x >> 4);
+    uint4 u[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] = live ? __ldg(src + e) : make_uint4(0u, 0u, 0u, 0u);
+    for (int e = 0; e < 2; ++e) {
+        const int64_t i = i0 + e * (kSplitRows / 2);
+        u[e] = i < n ? __ldg(reinterpret_cast<const uint4*>(q + i * kHD) + l16) : make_uint4(0u, 0u, 0u, 0u);
     }
-    __device__ __forceinline__ void store(const KvqAttnParams& p, unsigned char* sq, float* fac, uint32_t* mask_sm) {
-        uint32_t mx = 0u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(u[e].x & 0x7fff7fffu, u[e].y & 0x7fff7fffu),
-                                       __vmaxu2(u[e].z & 0x7fff7fffu, u[e].w & 0x7fff7fffu)));
+    for (int e = 0; e < 2; ++e) {
+        uint32_t mx = __vmaxu2(__vmaxu2(u[e].x & 0x7fff7fffu, u[e].y & 0x7fff7fffu),
+                               __vmaxu2(u[e].z & 0x7fff7fffu, u[e].w & 0x7fff7fffu));
+#pragma unroll
+        for (int m = 1; m < 16; m <<= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, m));
         mx = max(mx & 0xffffu, mx >> 16);
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        if (!in) return;
-        for (int w = h; w < p.W; w += 2) {  // the row's mask words
-            uint32_t m = 0u;
-            if (live) {
-                if (mask) m = __ldg(mask + w);
-                else m = slot >= 32 * w + 31 ? ~0u : slot < 32 * w ? 0u : (2u << (slot - 32 * w)) - 1u;
-            }
-            mask_sm[r * p.W + w] = m;
-        }
         const float s = pow2_to(__uint_as_float(mx << 16), 7);
-        if (h == 0) fac[r] = p.scale_log2 / s;
+        const uint32_t w[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // 16 elements: one 16-byte chunk of each part
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint4& v = u[2 * c + (e >> 1)];
-                const uint32_t w0 = (e & 1) ? v.z : v.x, w1 = (e & 1) ? v.w : v.y;
-                const float x[4] = {__uint_as_float(w0 << 16) * s, __uint_as_float(w0 & 0xffff0000u) * s,
-                                    __uint_as_float(w1 << 16) * s, __uint_as_float(w1 & 0xffff0000u) * s};
-                const uint32_t h0 = e4m3x2(x[0], x[1]), h1 = e4m3x2(x[2], x[3]);
-                const uint32_t f0 = e4m3_to_f16x2(h0), f1 = e4m3_to_f16x2(h1);
-                const float2 b0 = __half22float2(*reinterpret_cast<const __half2*>(&f0));
-                const float2 b1 = __half22float2(*reinterpret_cast<const __half2*>(&f1));
-                hi[e] = h0 | (h1 << 16);
-                lo[e] = e4m3x2(x[0] - b0.x, x[1] - b0.y) | (e4m3x2(x[2] - b1.x, x[3] - b1.y) << 16);
-            }
-            unsigned char* dst = sq + (r >> 7) * 2 * kTileQ + (r & 127) * kHD + (((4 * h + c) ^ (r & 7)) << 4);
-            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(dst + kTileQ) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        for (int c = 0; c < 4; ++c) {
+            const float x = __uint_as_float(w[c] << 16) * s, y = __uint_as_float(w[c] & 0xffff0000u) * s;
+            hi[c] = e4m3x2(x, y);
+            const uint32_t h = e4m3_to_f16x2(hi[c]);
+            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            lo[c] = e4m3x2(x - b.x, y - b.y);
         }
+        const int64_t i = i0 + e * (kSplitRows / 2);
+        if (i >= n) continue;
+        const int64_t bt = i / rows.Hq;
+        const int h = static_cast<int>(i - bt * rows.Hq), hk = h / rows.G;
+        const int64_t b = bt / rows.T;
+        const int64_t bk = b * Hkv + hk, r = (bt - b * rows.T) * rows.G + (h - hk * rows.G), RT = static_cast<int64_t>(rows.G) * rows.T;
+        dst[(2 * bk * RT + r) * 16 + l16] = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+        dst[((2 * bk + 1) * RT + r) * 16 + l16] = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+        if (l16 == 0) fac[bk * RT + r] = scale_log2 / s;
     }
-};
+}
 
 // What the softmax needs of a tile's scales, per 16-key group.
 struct alignas(16) TileScales {
@@ -224,12 +211,13 @@ struct alignas(16) TileScales {
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
-    kvq_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, KvqAttnParams p) {
+    kvq_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, KvqAttnParams p) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t bar_q_full[2], bar_q_empty[2], bar_k_full[kKStages], bar_k_empty[kKStages],
-        bar_v8_full[kVStages], bar_v8_empty[kVStages], bar_v_full[2], bar_v_empty[2], bar_sc[kScaleSlots], bar_s_full[2][2],
+    __shared__ uint64_t bar_q_full[2], bar_q_empty[2], bar_k_full[kKStages], bar_k_empty[kKStages], bar_v8_full[2],
+        bar_v8_empty[2], bar_v_full[2], bar_v_empty[2], bar_sc[kScaleSlots], bar_s_full[2][2],
         bar_p_full[2][2], bar_pv_done[2][2];
     __shared__ uint32_t tmem_holder;
     __shared__ TileScales ts[kScaleSlots];
@@ -237,17 +225,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int worker = blockIdx.x;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kKStages; ++s) {
-            mbar_init(&bar_k_full[s], 1);
-            mbar_init(&bar_k_empty[s], 2);
-        }
-        for (int s = 0; s < kVStages; ++s) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bar_q_full[s], 1);
+            mbar_init(&bar_q_empty[s], 2);
             mbar_init(&bar_v8_full[s], 1);
             mbar_init(&bar_v8_empty[s], kConvWarps);
-        }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&bar_q_full[s], kConvWarps);
-            mbar_init(&bar_q_empty[s], 2 + kSoftmaxWarps);
             mbar_init(&bar_v_full[s], kConvWarps);
             mbar_init(&bar_v_empty[s], 2);
             for (int b = 0; b < 2; ++b) {
@@ -255,6 +237,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&bar_s_full[s][b], 1);
                 mbar_init(&bar_p_full[s][b], 4);
             }
+        }
+        for (int s = 0; s < kKStages; ++s) {
+            mbar_init(&bar_k_full[s], 1);
+            mbar_init(&bar_k_empty[s], 2);
         }
         for (int s = 0; s < kScaleSlots; ++s) mbar_init(&bar_sc[s], 1);
         fence_mbar_init();
@@ -269,21 +255,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     KvqCursor cur;
     cur.init(p.s, worker);
-    const int rows = p.G * p.s.T;
-    float* fac_sm = reinterpret_cast<float*>(smem + kSmemFac);
-    uint32_t* mask_sm = reinterpret_cast<uint32_t*>(smem + kSmemMask);
     KvqPiece it;
     Waiter wait;
-    {  // the first item's q: half a row per thread
-        KvqCursor c = cur;
-        if (c.next(p.s, it)) {
-            static_assert(kThreads == 4 * kBM, "two threads per row of both blocks");
-            HalfRow hr;
-            hr.load(p, it, threadIdx.x >> 1, threadIdx.x & 1, rows);
-            hr.store(p, smem + kSmemQ, fac_sm, mask_sm);
-            fence_proxy_async_smem();  // the MMA reads q through the async proxy
-        }
-    }
+    const int rows = p.G * p.s.T, n_blocks = (rows + kBM - 1) / kBM;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -292,15 +266,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // --------------------------------------------- copies and scales ---
         // Step t: once the K stage of tile t is free (both blocks' QK^T of tile
-        // t - 3 done), give the softmax the scales of tile t - 1, read a step ago;
-        // then K of tile t, and V once its stage is free (converted). The free
-        // stage also says that QK(t - 3) had waited for PV(t - 5), so slot
-        // (t - 1) & 7 of the scales is free. (Not a converter's work: the fence
+        // t - 3 done), give the softmax the scales of tile t - 1, read a step ago; then
+        // copy K of tile t, and V once its stage is free. The slot of the scales, tile
+        // t - 9's, is free: the copy of V(t - 1) waited for the conversion of V(t - 3),
+        // that for both blocks' PV of tile t - 5. (Not a converter's work: the fence
         // behind each of its tiles would wait for the scales in flight; nor a QK
-        // warp's: it was late for its next tile, 767 against .. us at 70B 32K.)
+        // warp's: it was late for its next tile.) The next item's q is asked for once
+        // this item's fourth tile starts: the last item's QK^T are done by then.
         // Lanes 0..3 hold K's scales of a tile's 16-key groups, 4..7 V's.
-        int t = 0, sk = 0, pk = 0;
+        int t = 0, qi = 0, sk = 0, pk = 0;  // K stage of tile t and its phase
         float last_scale = 0.0f, sref = 0.0f, inv_sref = 0.0f;
+        auto copy_q = [&](const KvqPiece& a, int i) {  // q of the i-th item
+            if (i >= 2) wait(&bar_q_empty[i & 1], (i >> 1) - 1);
+            if (lane == 0 && wait.ok) {
+                const int hk = a.sub / p.n_items, block = (a.sub - hk * p.n_items) * 2;
+                const int n = min(2, n_blocks - block);
+                mbar_arrive_expect_tx(&bar_q_full[i & 1], n * 2 * kTileQ);
+                for (int h = 0; h < 2 * n; ++h)  // (row block, part); rows past the last are zeros
+                    tma_load_4d(smem + kSmemQ + ((i & 1) * 4 + h) * kTileQ, &tm_q, 0, (block + (h >> 1)) * kBM, h & 1,
+                                a.b * p.Hkv + hk, &bar_q_full[i & 1]);
+            }
+            __syncwarp();
+        };
         auto give = [&](int tile) {
             // V's reference scale: the piece's first tile's largest, raised by more than 2^4 only
             float vm = lane >= kSub && lane < 2 * kSub ? last_scale : 0.0f;
@@ -323,11 +310,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&bar_sc[tile & (kScaleSlots - 1)]);
             __syncwarp();
         };
-        while (cur.next(p.s, it)) {
+        KvqPiece ahead;
+        bool more = cur.next(p.s, ahead);
+        if (more) copy_q(ahead, 0);
+        for (; more; ++qi) {
+            it = ahead;
+            more = cur.next(p.s, ahead);
             const int hk = it.sub / p.n_items;
             const float* src = (lane < kSub ? p.k_scale : p.v_scale) + it.b * p.s_seq + hk;
             const int last = (it.nkeys - 1) >> p.blk_shift;
             for (int j = it.t0; j < it.t1; ++j, ++t) {
+                const int b = t & 1;
                 float own = 0.0f;
                 if (lane < 2 * kSub) own = __ldg(src + min((j * kBN + 16 * (lane & 3)) >> p.blk_shift, last) * p.s_blk);
                 if (t >= kKStages) wait(&bar_k_empty[sk], pk ^ 1);
@@ -339,25 +332,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_4d(smem + kSmemK + sk * kTile8, &tm_k, 0, hk, j * kBN, it.b, &bar_k_full[sk]);
                 }
                 __syncwarp();
-                if (t >= kVStages) wait(&bar_v8_empty[t & 1], (t >> 1) - 1);
-                if (lane == 0 && wait.ok) {
-                    mbar_arrive_expect_tx(&bar_v8_full[t & 1], kTile8);
-                    tma_load_4d(smem + kSmemV8 + (t & 1) * kTile8, &tm_v, 0, hk, j * kBN, it.b, &bar_v8_full[t & 1]);
-                }
-                __syncwarp();
                 if (++sk == kKStages) {
                     sk = 0;
                     pk ^= 1;
                 }
+                if (t >= 2) wait(&bar_v8_empty[b], (t >> 1) - 1);
+                if (lane == 0 && wait.ok) {
+                    mbar_arrive_expect_tx(&bar_v8_full[b], kTile8);
+                    tma_load_4d(smem + kSmemV8 + b * kTile8, &tm_v, 0, hk, j * kBN, it.b, &bar_v8_full[b]);
+                }
+                __syncwarp();
+                if (more && j == min(it.t0 + 3, it.t1 - 1)) copy_q(ahead, qi + 1);
             }
         }
         if (t > 0) give(t - 1);
         if (!wait.ok) {  // the copies in flight land before the CTA's shared memory goes away
             if (lane == 0) raise_status(p.status, kDevTimeout);
+            for (int s = 0; s < 2; ++s)
+                for (int ph = 0; ph < 2; ++ph) {
+                    mbar_wait(&bar_q_full[s], ph, 1u << 16);
+                    mbar_wait(&bar_v8_full[s], ph, 1u << 16);
+                }
             for (int s = 0; s < kKStages; ++s)
                 for (int ph = 0; ph < 2; ++ph) mbar_wait(&bar_k_full[s], ph, 1u << 16);
-            for (int s = 0; s < kVStages; ++s)
-                for (int ph = 0; ph < 2; ++ph) mbar_wait(&bar_v8_full[s], ph, 1u << 16);
         }
         __syncwarp();
     } else if (warp < kWarpConv) {
@@ -377,7 +374,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t base = smem_u32(smem), tm = uniform(tmem);
         const int role = uniform(warp - kWarpMma);  // QK of block 0, 1, PV of block 0, 1
         const int g = role & 1;
-        const int blocks = (rows + kBM - 1) / kBM;
         const uint32_t tS = tm + 128 * g, tO = tm + 256 + 128 * g;
         int t = 0, u = 0;
         int sk = 0, pk = 0;  // K stage of tile t and its phase
@@ -397,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool more = cur.next(p.s, it);
                 if (!uniform(more)) break;
                 const int n_tiles = uniform(it.t1 - it.t0);
-                const bool live = uniform((it.sub % p.n_items) * 2 + g) < blocks;
+                const bool live = uniform((it.sub % p.n_items) * 2 + g) < n_blocks;
                 const uint32_t aQ = base + kSmemQ + ((qi & 1) * 4 + 2 * g) * kTileQ;
                 spin(&bar_q_full[qi & 1], qi >> 1);
                 if (!live) {  // a block without rows: keep the shared barriers' counts, in step
@@ -430,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool more = cur.next(p.s, it);
                 if (!uniform(more)) break;
                 const int n_tiles = uniform(it.t1 - it.t0);
-                const bool live = uniform((it.sub % p.n_items) * 2 + g) < blocks;
+                const bool live = uniform((it.sub % p.n_items) * 2 + g) < n_blocks;
                 if (!live) {
                     for (int j = 0; j < n_tiles; ++j, ++t) {
                         wait(&bar_v_full[t & 1], t >> 1);
@@ -455,53 +451,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait.ok) raise_status(p.status, kDevTimeout);
     } else if (warp < kWarpSoftmax) {
         // ----------------------------------------------------- converters ---
-        // V codes to fp16, and q of the next item while the current one runs.
         const int cw = warp - kWarpConv;
         const uint32_t base = smem_u32(smem);
-        const int i = threadIdx.x - kWarpConv * 32;
-        int t = 0, qi = 0;
-        KvqPiece ahead;
-        bool more = cur.next(p.s, ahead);
-        if (more && lane == 0) mbar_arrive(&bar_q_full[0]);  // converted by the whole CTA
-        while (more) {
-            it = ahead;
-            more = cur.next(p.s, ahead);
-            // The next item's q in passes of 48 rows, one behind each tile: its loads
-            // are in flight while the warp waits for the next tile. (All at once they
-            // held up V for 11,000 cycles per item.)
-            int pass = 0;
-            const int passes = !more ? 0 : (min(2 * kBM, rows - (ahead.sub % p.n_items) * 2 * kBM + kBM - 1) / kBM * kBM + kPassRows - 1) / kPassRows;
-            bool loaded = false;
-            HalfRow hr;
-            auto load_pass = [&]() {
-                if (pass == passes) return;
-                if (pass == 0 && qi >= 1) wait(&bar_q_empty[(qi + 1) & 1], ((qi + 1) >> 1) - 1);
-                hr.load(p, ahead, pass * kPassRows + (i >> 1), i & 1, rows);
-                loaded = true;
-            };
-            auto store_pass = [&]() {
-                if (!loaded) return;
-                hr.store(p, smem + kSmemQ + ((qi + 1) & 1) * 4 * kTileQ, fac_sm + ((qi + 1) & 1) * 2 * kBM,
-                         mask_sm + ((qi + 1) & 1) * 2 * kBM * p.W);
-                loaded = false;
-                if (++pass == passes) {
-                    fence_proxy_async_smem();  // the MMA reads q through the async proxy
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar_q_full[(qi + 1) & 1]);
-                }
-            };
+        int t = 0;
+        while (cur.next(p.s, it))
             for (int j = it.t0; j < it.t1; ++j, ++t) {
                 const int b = t & 1;
-                if (t >= 2) wait(&bar_v_empty[b], (t >> 1) - 1);
-                store_pass();
-                const int st = t % kVStages;
-                static_assert(kVStages == 2, "stage of V tile t: t & 1");
-                wait(&bar_v8_full[st], t / kVStages);
+                if (t >= 2) wait.both(&bar_v_empty[b], (t >> 1) - 1, &bar_v8_full[b], t >> 1);
+                else wait(&bar_v8_full[b], t >> 1);
 #pragma unroll
                 for (int e = 0; e < 6; ++e) {  // chunks cw, cw + 3, cw + 6 of 16 columns, two keys each
                     const int key = lane + 32 * (e & 1), c16 = cw + kConvWarps * (e >> 1);
                     if (c16 >= 8) break;
-                    uint4 u = lds128(base + kSmemV8 + st * kTile8 + key * kHD + ((c16 ^ (key & 7)) << 4));
+                    uint4 u = lds128(base + kSmemV8 + b * kTile8 + key * kHD + ((c16 ^ (key & 7)) << 4));
                     // keys that no row can see may hold anything (even NaN): 0 * V has to stay 0
                     if (j * kBN + key >= it.nkeys) u = make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t dst = base + kSmemV + b * kTileV + (c16 >> 2) * kHalfV + key * 128;
@@ -514,18 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();  // the MMA reads V through the async proxy
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&bar_v8_empty[st]);
+                    mbar_arrive(&bar_v8_empty[b]);
                     mbar_arrive(&bar_v_full[b]);
                 }
-                load_pass();
             }
-            store_pass();
-            while (pass < passes) {  // fewer tiles than passes
-                load_pass();
-                store_pass();
-            }
-            ++qi;
-        }
         if (!wait.ok) raise_status(p.status, kDevTimeout);
     } else {
         // ------------------------------------------------------ softmax ---
@@ -536,32 +490,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = (q4 << 5) | lane;   // row of the block = TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
         const uint32_t o_cols = tmem + 256 + 128 * g + lane_off;
-        int t = 0, tg = 0, qi = 0;
+        int t = 0, tg = 0;
         int4 cut = make_int4(0, 0, 0, 0);
         kvq_zero_bad(p.s, p.Hq, p.out, p.status, worker, threadIdx.x - kWarpSoftmax * 32, kSoftmaxWarps * 32);
-        for (; cur.next(p.s, it); ++qi) {
+        while (cur.next(p.s, it)) {
             if (it.np) cut = kvq_cut(it);
-            const int hk = it.sub / p.n_items, row0 = ((it.sub - hk * p.n_items) * 2 + g) * kBM;
+            const int hk = it.sub / p.n_items, block = (it.sub - hk * p.n_items) * 2 + g;
             const int nt = it.t1 - it.t0;
-            wait(&bar_q_full[qi & 1], qi >> 1);  // also keeps an idle block from arriving for a later item
-            if (row0 >= rows) {  // the last pair of an odd number of row blocks: nothing to do for this one
+            if (block >= n_blocks) {  // the last pair of an odd number of row blocks: nothing to do for this one
                 t += nt;
-                if (lane == 0) mbar_arrive(&bar_q_empty[qi & 1]);
                 continue;
             }
-            const int row = row0 + r;      // row of the (sequence, KV head)
-            const int slot = row / p.G;    // its tree slot
-            const bool row_live = slot < p.s.T;
-            // a quarter whose 32 rows are all past the problem's rows does no arithmetic
-            const bool quarter_live = row0 + q4 * 32 < rows;
-            const float fac = fac_sm[(qi & 1) * 2 * kBM + g * kBM + r];
-            const uint32_t* mrow = mask_sm + ((qi & 1) * 2 * kBM + g * kBM + r) * p.W;
+            int slot;
+            const int64_t row = p.rows.row(it.b, hk, block * kBM + r, &slot);
+            const bool row_live = row >= 0;
+            // a quarter without rows of the problem does no arithmetic
+            const bool quarter_live = __any_sync(0xffffffffu, row_live);
+            const uint32_t* mrow =
+                p.mask ? p.mask + (static_cast<size_t>(it.b) * p.s.T + (row_live ? slot : 0)) * p.W : nullptr;
             const int L = it.L, n = it.n;
+            const float fac =
+                row_live ? __ldg(p.q_fac + (static_cast<size_t>(it.b) * p.Hkv + hk) * rows + block * kBM + r) : 0.0f;
+            // word w of the row's mask
+            auto word = [&](int w) {
+                if (w >= p.W) return 0u;
+                if (mrow) return __ldg(mrow + w);
+                return slot >= 32 * w + 31 ? ~0u : slot < 32 * w ? 0u : (2u << (slot - 32 * w)) - 1u;
+            };
             float m_use = 0.0f, l = 0.0f, sref = 0.0f;
             bool seen = false;
             for (int j = it.t0; j < it.t1; ++j, ++t, ++tg) {
                 const int key0 = j * kBN;
                 const uint32_t s_cols = tmem + 64 * (2 * g + (tg & 1)) + lane_off;
+                // visibility of 32 keys at a time: prefix keys, then tree slots in the row's mask
+                uint32_t vis[2] = {~0u, ~0u};
+                if (key0 + kBN > L) {
+#pragma unroll
+                    for (int hq = 0; hq < 2; ++hq) {
+                        const int kb = key0 + 32 * hq;
+                        const int npre = min(32, L - kb);  // keys of the 32 inside the prefix
+                        const uint32_t pre = npre > 0 ? 0xffffffffu >> (32 - npre) : 0u;
+                        const int j0 = kb - L;  // slot of the first key (may be negative)
+                        const int lo = j0 < 0 ? 0 : j0;
+                        const int w0 = lo >> 5, sh = lo & 31;
+                        uint32_t win = word(w0) >> sh;
+                        if (sh) win |= word(w0 + 1) << (32 - sh);
+                        const int limit = n - lo;  // slots j >= n are never visible
+                        if (limit <= 0) win = 0u;
+                        else if (limit < 32) win &= (1u << limit) - 1u;
+                        uint32_t tree = j0 < 0 ? (win << (-j0 & 31)) : win;
+                        if (j0 <= -32) tree = 0u;
+                        vis[hq] = pre | tree;
+                    }
+                }
                 wait.both(&bar_sc[t & (kScaleSlots - 1)], t / kScaleSlots, &bar_s_full[g][tg & 1], tg >> 1);
                 tc_fence_after();
                 if (quarter_live) {
@@ -574,28 +555,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sref = sc.sref;
                     uint32_t s[kBN];
                     tmem_ld64(s_cols, s);
-                    // visibility of 32 keys at a time: prefix keys, then tree slots in the row's mask
                     if (key0 + kBN > L) {
 #pragma unroll
-                        for (int hq = 0; hq < 2; ++hq) {
-                            const int kb = key0 + 32 * hq;
-                            const int npre = min(32, L - kb);  // keys of the 32 inside the prefix
-                            const uint32_t pre = npre > 0 ? 0xffffffffu >> (32 - npre) : 0u;
-                            const int j0 = kb - L;  // slot of the first key (may be negative)
-                            const int lo = j0 < 0 ? 0 : j0;
-                            const int w0 = lo >> 5, sh = lo & 31;
-                            uint32_t win = w0 < p.W ? mrow[w0] >> sh : 0u;
-                            if (sh && w0 + 1 < p.W) win |= mrow[w0 + 1] << (32 - sh);
-                            const int limit = n - lo;  // slots j >= n are never visible
-                            if (limit <= 0) win = 0u;
-                            else if (limit < 32) win &= (1u << limit) - 1u;
-                            uint32_t tree = j0 < 0 ? (win << (-j0 & 31)) : win;
-                            if (j0 <= -32) tree = 0u;
-                            const uint32_t vis = pre | tree;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                s[32 * hq + e] = ((vis >> e) & 1u) ? s[32 * hq + e] : 0xff800000u;
-                        }
+                        for (int e = 0; e < kBN; ++e)
+                            s[e] = ((vis[e >> 5] >> (e & 31)) & 1u) ? s[e] : 0xff800000u;
                     }
                     const float mx = fmaxf(fmaxf(max16(s) * k[0], max16(s + 16) * k[1]),
                                            fmaxf(max16(s + 32) * k[2], max16(s + 48) * k[3]));  // the scales are positive
@@ -612,6 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             rescale = true;
                         }
                     }
+                    // (the vote here: its answer is not needed before P is written)
+                    const bool any_rescale = __any_sync(0xffffffffu, rescale);
                     // P = 2^(s k - m_use + lv), two per packed multiply-add; the row sum takes the
                     // reverse of V's ratio. P as fp16 pairs over the first 32 columns of S.
                     // (A group's arguments, then its exponentials, then the last group's sums and
@@ -656,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // Rescaling O needs PV of the previous tile done (this tile's PV waits for
                     // this warp's arrival below). tcgen05.ld/st are warp-collective: rescale if
                     // any row of the warp needs it (alpha = 1 for the others).
-                    if (j > it.t0 && __any_sync(0xffffffffu, rescale)) {
+                    if (j > it.t0 && any_rescale) {
                         wait(&bar_pv_done[g][(tg - 1) & 1], (tg - 1) >> 1);
                         tc_fence_after();
 #pragma unroll 1
@@ -673,7 +638,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar_p_full[g][tg & 1]);
             }
-            if (lane == 0) mbar_arrive(&bar_q_empty[qi & 1]);  // factors and masks read
             // ----------------------------------------------------- epilogue ---
             wait(&bar_pv_done[g][(tg - 1) & 1], (tg - 1) >> 1);
             tc_fence_after();
@@ -682,10 +646,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool whole = it.whole();
             const bool live = any && (!whole || slot < n);  // unused slots: zeros
             const float f = !live ? 0.0f : whole ? sref / l : sref;
-            const size_t at = static_cast<size_t>(it.slot(worker)) * p.part.rows + g * kBM + r;
-            __nv_bfloat16* orow = p.out + ((static_cast<size_t>(it.b) * p.s.T + slot) * p.Hq +
-                                           static_cast<size_t>(hk) * p.G + (row - slot * p.G)) * kHD;
-            float* prow = p.part.o + at * kHD;
+            const size_t part_slot = it.slot(worker);
+            const int prow = g * kBM + r;
+            float4* part = reinterpret_cast<float4*>(p.part.o) + part_slot * (kHD / 4) * p.part.rows + prow;
+            // whole: neighbouring lanes store 32 bytes of one row together (full sectors)
+            const int64_t other = static_cast<int64_t>(shfl_xor_u64(static_cast<uint64_t>(row), 1));
+            const bool odd = lane & 1;
+            const int64_t row_a = odd ? other : row, row_b = odd ? row : other;  // the even lane's row, the odd one's
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 float o[32];
@@ -693,24 +660,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(o_cols + 32 * c, o);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = live ? o[e] * f : 0.0f;
-                if (!row_live) {  // past the (sequence, KV head)'s rows
-                } else if (whole) {
+                if (whole) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<uint4*>(orow + 32 * c + 8 * q) =
-                            make_uint4(pack_bf16(o[8 * q], o[8 * q + 1]), pack_bf16(o[8 * q + 2], o[8 * q + 3]),
-                                       pack_bf16(o[8 * q + 4], o[8 * q + 5]), pack_bf16(o[8 * q + 6], o[8 * q + 7]));
-                } else {
+                    for (int h = 0; h < 2; ++h) {  // 16 columns: chunks of 8 columns, this lane's x and y
+                        uint4 x = make_uint4(pack_bf16(o[16 * h], o[16 * h + 1]), pack_bf16(o[16 * h + 2], o[16 * h + 3]),
+                                             pack_bf16(o[16 * h + 4], o[16 * h + 5]), pack_bf16(o[16 * h + 6], o[16 * h + 7]));
+                        uint4 y = make_uint4(pack_bf16(o[16 * h + 8], o[16 * h + 9]), pack_bf16(o[16 * h + 10], o[16 * h + 11]),
+                                             pack_bf16(o[16 * h + 12], o[16 * h + 13]),
+                                             pack_bf16(o[16 * h + 14], o[16 * h + 15]));
+                        uint4 give = odd ? x : y, got;  // the even lane keeps x of its row and gets x of the odd one's
+                        got.x = __shfl_xor_sync(0xffffffffu, give.x, 1);
+                        got.y = __shfl_xor_sync(0xffffffffu, give.y, 1);
+                        got.z = __shfl_xor_sync(0xffffffffu, give.z, 1);
+                        got.w = __shfl_xor_sync(0xffffffffu, give.w, 1);
+                        const int col = 32 * c + 16 * h + (odd ? 8 : 0);
+                        if (row_a >= 0) *reinterpret_cast<uint4*>(p.out + row_a * kHD + col) = odd ? got : x;
+                        if (row_b >= 0) *reinterpret_cast<uint4*>(p.out + row_b * kHD + col) = odd ? y : got;
+                    }
+                } else if (row_live) {
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        *reinterpret_cast<float4*>(prow + 32 * c + 4 * q) =
+                        part[static_cast<size_t>(8 * c + q) * p.part.rows] =
                             make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
                 }
             }
-            if (!whole && row_live) {
-                p.part.ml[2 * at] = any ? m_use : -INFINITY;
-                p.part.ml[2 * at + 1] = any ? l : 0.0f;
-            }
+            if (!whole && row_live)
+                reinterpret_cast<float2*>(p.part.ml)[part_slot * p.part.rows + prow] =
+                    make_float2(any ? m_use : -INFINITY, any ? l : 0.0f);
             tc_fence_before();
         }
         if (!wait.ok) raise_status(p.status, kDevTimeout);
@@ -723,13 +699,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
+// The cut item that worker w began (blockIdx.x), from its pieces i: worker w's
+// in slot 2w + 1, w + i's in slot 2 (w + i). A warp takes eight rows; a lane
+// one row and every fourth column group, so that the reads of the pieces are
+// 128 bytes wide and the row's stores 32.
+constexpr int kMergeWarps = 4;
+__global__ void __launch_bounds__(kMergeWarps * 32) kvq_merge_rows_kernel(KvqMergeParams p) {
+    const int lane = threadIdx.x & 31;
+    const int r = (blockIdx.y * kMergeWarps + (threadIdx.x >> 5)) * 8 + (lane & 7), cg = lane >> 3;
+    const int w = blockIdx.x;
+    pdl_wait_prior();
+    pdl_launch_dependents();
+    const int4 c = __ldcg(p.part.cut + w);
+    if (c.x == 0) return;
+    const int hk = c.z / p.n_items;
+    int slot;
+    const int64_t row = p.rows.row(c.y, hk, (c.z - hk * p.n_items) * 2 * kBM + r, &slot);
+    if (row < 0) return;
+    const float2* ml = reinterpret_cast<const float2*>(p.part.ml);
+    const float4* po = reinterpret_cast<const float4*>(p.part.o);
+    RowSum<8> s;
+#pragma unroll 2
+    for (int i = 0; i < c.x; ++i) {
+        const size_t at = i == 0 ? 2 * w + 1 : 2 * (w + i);
+        const float2 a = __ldcg(ml + at * p.part.rows + r);
+        float4 x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __ldcg(po + (at * (kHD / 4) + cg + 4 * e) * p.part.rows + r);
+        s.add(a.x, a.y, x);
+    }
+    const bool live = slot < c.w && s.l > 0.0f;
+    const float inv = live ? 1.0f / s.l : 0.0f;
+    uint2* dst = reinterpret_cast<uint2*>(p.out + row * kHD);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        dst[cg + 4 * e] = live ? make_uint2(pack_bf16(s.o[e].x * inv, s.o[e].y * inv), pack_bf16(s.o[e].z * inv, s.o[e].w * inv))
+                               : make_uint2(0u, 0u);
+}
+
 // ------------------------------------------------------------- host side ---
 
 struct Plan {
     KvqSched s;
     int G, n_items, rows;
     bool decode;
-    size_t off_cut, off_ml, off_o, bytes;
+    size_t off_cut, off_ml, off_o, off_q, off_fac, bytes;
 };
 
 // Up to 16 query rows per KV head: the decode kernel, a worker per warp;
@@ -753,7 +767,10 @@ Plan make_plan(const KvqDims& kv, int T) {
     pl.off_cut = 256;
     pl.off_ml = align_up(pl.off_cut + pl.s.workers * sizeof(int4), 256);
     pl.off_o = align_up(pl.off_ml + slots * 2 * sizeof(float), 256);
-    pl.bytes = align_up(pl.off_o + slots * kHD * sizeof(float), 256);
+    pl.off_q = align_up(pl.off_o + slots * kHD * sizeof(float), 256);
+    const size_t q_rows = pl.decode ? 0 : static_cast<size_t>(kv.B) * kv.Hkv * rows;
+    pl.off_fac = pl.off_q + q_rows * 2 * kHD;
+    pl.bytes = align_up(pl.off_fac + q_rows * sizeof(float), 256);
     return pl;
 }
 
@@ -772,6 +789,8 @@ cudaError_t launch_kvq_attention(const KvqDims& kv, int T, const void* q, const 
     p.s = pl.s;
     p.part = KvqPartials{reinterpret_cast<float*>(w + pl.off_o), reinterpret_cast<float*>(w + pl.off_ml),
                          reinterpret_cast<int4*>(w + pl.off_cut), pl.rows};
+    p.rows = KvqRows{pl.G, T, kv.Hq};
+    p.q_fac = reinterpret_cast<const float*>(w + pl.off_fac);
     p.Hq = kv.Hq;
     p.Hkv = kv.Hkv;
     p.G = pl.G;
@@ -789,19 +808,36 @@ cudaError_t launch_kvq_attention(const KvqDims& kv, int T, const void* q, const 
     p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kHD)));
     const char* kbase = static_cast<const char*>(codes) + static_cast<int64_t>(layer) * kv.layer_stride;
     const char* vbase = kbase + kv.kv_stride;
-    cudaError_t e;
+    const KvqMergeParams mp{p.part, p.rows, pl.s.workers, p.n_items, p.out};
     if (pl.decode) {
-        e = launch_kvq_decode(kv, p, kbase, vbase, stream);
-    } else {
-        CUtensorMap tk, tv;
-        if (!make_map_codes(&tk, kbase, kv, kBN) || !make_map_codes(&tv, vbase, kv, kBN)) return cudaErrorInvalidValue;
-        const int dyn = kSmemMask + 2 * 2 * kBM * p.W * 4 + 1024;  // mask rows, alignment slack
-        e = ensure_dyn_smem(reinterpret_cast<const void*>(kvq_attn_kernel), dyn);
-        if (e != cudaSuccess) return e;
-        e = launch_pdl(kvq_attn_kernel, dim3(pl.s.workers), dim3(kThreads), dyn, stream, tk, tv, p);
+        cudaError_t e = launch_kvq_decode(kv, p, kbase, vbase, stream);
+        return e != cudaSuccess ? e : launch_kvq_merge_decode(mp, stream);
     }
+    CUtensorMap tq, tk, tv;
+    const int rows = pl.G * T;
+    {  // (128 bytes, row, part, (sequence, KV head))
+        auto fn = tensor_map_encode_fn();
+        if (!fn) return cudaErrorInvalidValue;
+        const cuuint64_t dims[4] = {kHD, static_cast<cuuint64_t>(rows), 2, static_cast<cuuint64_t>(kv.B) * kv.Hkv};
+        const cuuint64_t strides[3] = {kHD, static_cast<cuuint64_t>(kHD) * rows, static_cast<cuuint64_t>(kHD) * rows * 2};
+        const cuuint32_t box[4] = {kHD, kBM, 1, 1}, estride[4] = {1, 1, 1, 1};
+        if (fn(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, w + pl.off_q, dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    if (!make_map_codes(&tk, kbase, kv, kBN) || !make_map_codes(&tv, vbase, kv, kBN)) return cudaErrorInvalidValue;
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kvq_attn_kernel), kSmem);
     if (e != cudaSuccess) return e;
-    return launch_kvq_merge(KvqMergeParams{p.part, pl.s.workers, p.G, T, p.Hq, p.n_items, p.out}, stream);
+    const int64_t q_rows = static_cast<int64_t>(kv.B) * T * kv.Hq;
+    e = launch_pdl(kvq_split_q_kernel, dim3(static_cast<unsigned>((q_rows + kSplitRows - 1) / kSplitRows)), dim3(kSplitThreads), 0,
+                   stream, p.q, reinterpret_cast<uint2*>(w + pl.off_q), reinterpret_cast<float*>(w + pl.off_fac), p.rows,
+                   kv.Hkv, q_rows, p.scale_log2);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kvq_attn_kernel, dim3(pl.s.workers), dim3(kThreads), kSmem, stream, tq, tk, tv, p);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kvq_merge_rows_kernel, dim3(pl.s.workers, pl.rows / (8 * kMergeWarps)), dim3(kMergeWarps * 32), 0, stream,
+                      mp);
 }
 
 }  // namespace eagle

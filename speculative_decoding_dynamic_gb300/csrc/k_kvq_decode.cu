@@ -381,95 +381,75 @@ constexpr int kMergeWarps = 8;
 constexpr int kMergeAlone = 4;  // most pieces that one warp combines by itself
 
 // Running combination of a row's pieces, four columns per lane.
-struct RowSum {
-    float m = -INFINITY, l = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    __device__ __forceinline__ void add(float pm, float pl, const float4& x) {
-        // a piece in which the row saw nothing: maximum -inf, O 0
-        const float M = fmaxf(m, pm);
-        const float a = m == -INFINITY ? 0.0f : ex2_approx(m - M), c = pm == -INFINITY ? 0.0f : ex2_approx(pm - M);
-        m = M;
-        l = l * a + pl * c;
-        o = make_float4(o.x * a + x.x * c, o.y * a + x.y * c, o.z * a + x.z * c, o.w * a + x.w * c);
-    }
-};
-
 // c: (pieces, sequence, item, tree size) of a cut item.
-__device__ __forceinline__ void merge_store(const KvqMergeParams& p, const int4& c, int r, const RowSum& s, int lane) {
-    const int hk = c.z / p.n_items, row = (c.z - hk * p.n_items) * p.part.rows + r;
-    const int slot = row / p.G;
-    if (slot >= p.T) return;  // past the (sequence, KV head)'s rows
+__device__ __forceinline__ void merge_store(const KvqMergeParams& p, const int4& c, int r, const RowSum<1>& s, int lane) {
+    int slot;
+    const int64_t row = p.rows.row(c.y, c.z, r, &slot);  // an item is a KV head
+    if (row < 0) return;
     const bool live = slot < c.w && s.l > 0.0f;
     const float inv = live ? 1.0f / s.l : 0.0f;
-    uint2* dst = reinterpret_cast<uint2*>(
-        p.out + ((static_cast<size_t>(c.y) * p.T + slot) * p.Hq + static_cast<size_t>(hk) * p.G + (row - slot * p.G)) * kKvqHeadDim);
-    dst[lane] = live ? make_uint2(pack_bf16(s.o.x * inv, s.o.y * inv), pack_bf16(s.o.z * inv, s.o.w * inv))
+    uint2* dst = reinterpret_cast<uint2*>(p.out + row * kKvqHeadDim);
+    dst[lane] = live ? make_uint2(pack_bf16(s.o[0].x * inv, s.o[0].y * inv), pack_bf16(s.o[0].z * inv, s.o[0].w * inv))
                      : make_uint2(0u, 0u);
 }
 
 // The cut item that worker w began: O = sum_i 2^(m_i - M) O_i over
 // sum_i 2^(m_i - M) l_i of its pieces i (worker w's in slot 2w + 1, w + i's in
 // slot 2 (w + i)). A CTA serves the items that eight neighbouring workers
-// began (decode: few rows) or one worker's (256 rows, blockIdx.y taking some of
-// them). With many rows a warp takes whole rows. Decode items of up to four
-// pieces go to one warp each; those of many (few long sequences) are shared
-// by all eight warps, row by row.
-__global__ void __launch_bounds__(kMergeWarps * 32) kvq_merge_kernel(KvqMergeParams p, int per_cta, int rows_per_cta) {
+// began: those of up to four pieces go to one warp each, those of many (few
+// long sequences) are shared by all eight warps, row by row.
+__global__ void __launch_bounds__(kMergeWarps * 32) kvq_merge_decode_kernel(KvqMergeParams p) {
     __shared__ float4 so[kMergeWarps][32];
     __shared__ float2 sml[kMergeWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int w0 = blockIdx.x * per_cta;
+    const int w0 = blockIdx.x * kMergeWarps;
     pdl_wait_prior();
     pdl_launch_dependents();
     const int4* items = p.part.cut + w0;
-    const int n_here = min(per_cta, p.workers - w0);
-    const int r0 = blockIdx.y * rows_per_cta, r1 = min(p.part.rows, r0 + rows_per_cta);
+    const int n_here = min(kMergeWarps, p.workers - w0);
     const float2* ml = reinterpret_cast<const float2*>(p.part.ml);
     const float4* po = reinterpret_cast<const float4*>(p.part.o);
     auto slot_row = [&](int w, int i, int r) {
         return static_cast<size_t>(i == 0 ? 2 * w + 1 : 2 * (w + i)) * p.part.rows + r;
     };
-    const bool decode = per_cta > 1;
-    for (int e = 0; e < n_here; ++e) {
-        const int4 c = __ldcg(items + e);
-        if (c.x == 0 || (decode && (c.x > kMergeAlone || e != warp))) continue;
-        // decode: item e belongs to warp e; else its rows are dealt over the warps
-        for (int r = decode ? r0 : r0 + warp; r < r1; r += decode ? 1 : kMergeWarps) {
-            RowSum s;
-            for (int i0 = 0; i0 < c.x; i0 += kMergeAlone) {
-                float2 a[kMergeAlone];
-                float4 x[kMergeAlone];
+    const int4 own = __ldcg(items + min(warp, n_here - 1));
+    if (warp < n_here && own.x > 0 && own.x <= kMergeAlone)
+        for (int r = 0; r < p.part.rows; ++r) {
+            RowSum<1> s;
+            float2 a[kMergeAlone];
+            float4 x[kMergeAlone][1];
 #pragma unroll
-                for (int i = 0; i < kMergeAlone; ++i) {
-                    if (i0 + i >= c.x) break;
-                    const size_t at = slot_row(w0 + e, i0 + i, r);
-                    a[i] = __ldcg(ml + at);
-                    x[i] = __ldcg(po + at * 32 + lane);
-                }
-#pragma unroll
-                for (int i = 0; i < kMergeAlone; ++i)
-                    if (i0 + i < c.x) s.add(a[i].x, a[i].y, x[i]);
+            for (int i = 0; i < kMergeAlone; ++i) {
+                if (i >= own.x) break;
+                const size_t at = slot_row(w0 + warp, i, r);
+                a[i] = __ldcg(ml + at);
+                x[i][0] = __ldcg(po + at * 32 + lane);
             }
-            merge_store(p, c, r, s, lane);
+#pragma unroll
+            for (int i = 0; i < kMergeAlone; ++i)
+                if (i < own.x) s.add(a[i].x, a[i].y, x[i]);
+            merge_store(p, own, r, s, lane);
         }
-    }
     for (int e = 0; e < n_here; ++e) {
         const int4 c = __ldcg(items + e);
-        if (!decode || c.x <= kMergeAlone) continue;  // uniform over the CTA
-        for (int r = r0; r < r1; ++r) {
-            RowSum s;
+        if (c.x <= kMergeAlone) continue;  // uniform over the CTA
+        for (int r = 0; r < p.part.rows; ++r) {
+            RowSum<1> s;
 #pragma unroll 4
             for (int i = warp; i < c.x; i += kMergeWarps) {
                 const size_t at = slot_row(w0 + e, i, r);
                 const float2 a = __ldcg(ml + at);
-                const float4 x = __ldcg(po + at * 32 + lane);
+                const float4 x[1] = {__ldcg(po + at * 32 + lane)};
                 s.add(a.x, a.y, x);
             }
-            so[warp][lane] = s.o;
+            so[warp][lane] = s.o[0];
             if (lane == 0) sml[warp] = make_float2(s.m, s.l);
             __syncthreads();
             if (warp == 0) {
-                for (int i = 1; i < kMergeWarps; ++i) s.add(sml[i].x, sml[i].y, so[i][lane]);
+                for (int i = 1; i < kMergeWarps; ++i) {
+                    const float4 x[1] = {so[i][lane]};
+                    s.add(sml[i].x, sml[i].y, x);
+                }
                 merge_store(p, c, r, s, lane);
             }
             __syncthreads();
@@ -479,12 +459,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kvq_merge_kernel(KvqMergePar
 
 }  // namespace
 
-cudaError_t launch_kvq_merge(const KvqMergeParams& p, cudaStream_t stream) {
-    const bool decode = p.part.rows <= kKvqDecodeRows;
-    const int per_cta = decode ? kMergeWarps : 1, rows_per_cta = decode ? p.part.rows : 32;
-    return launch_pdl(kvq_merge_kernel,
-                      dim3((p.workers + per_cta - 1) / per_cta, (p.part.rows + rows_per_cta - 1) / rows_per_cta),
-                      dim3(kMergeWarps * 32), 0, stream, p, per_cta, rows_per_cta);
+cudaError_t launch_kvq_merge_decode(const KvqMergeParams& p, cudaStream_t stream) {
+    return launch_pdl(kvq_merge_decode_kernel, dim3((p.workers + kMergeWarps - 1) / kMergeWarps), dim3(kMergeWarps * 32), 0,
+                      stream, p);
 }
 
 KvqSched kvq_decode_sched(int B, int T, int max_len, int Hkv, int rows) {

@@ -14,6 +14,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "attn_common.cuh"
 #include "eagle_internal.cuh"
@@ -43,43 +44,69 @@ __device__ __forceinline__ KvqSeq kvq_seq(const KvqSched& s, int b) {
     return q;
 }
 
-// Total length of the line (whole warp).
-__device__ __forceinline__ long long kvq_total(const KvqSched& s) {
-    const int lane = threadIdx.x & 31;
-    long long t = 0;
-    for (int b = lane; b < s.B; b += 32) t += kvq_seq(s, b).len;
-    return static_cast<long long>(warp_sum_u64(static_cast<uint64_t>(t))) * s.per_seq;
+// a / b for a >= 0, b > 0: a 64-bit division takes some 150 cycles, and hardly ever is one needed.
+__device__ __forceinline__ long long kvq_div(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
 }
 
 __device__ __forceinline__ long long kvq_chunk(const KvqSched& s, long long total) {
-    const long long c = (total + s.workers - 1) / s.workers;
+    const long long c = kvq_div(total + s.workers - 1, s.workers);
     return c < s.min_chunk ? s.min_chunk : c;
 }
 
-// The sequence that holds unit pos < total, and the line's length before it (whole warp).
-__device__ __forceinline__ int kvq_find(const KvqSched& s, long long pos, long long* base) {
-    const int lane = threadIdx.x & 31;
-    long long before = 0;
-    for (int b0 = 0; b0 < s.B; b0 += 32) {
-        const int b = b0 + lane;
-        const long long own = b < s.B ? static_cast<long long>(kvq_seq(s, b).len) * s.per_seq : 0;
-        long long inc = own;
+// The sequences' lengths on the line, 32 at a time over a warp's lanes; the
+// first kHeld groups are read once, all together, and stay in registers.
+struct KvqLens {
+    static constexpr int kHeld = 4;
+    int len[kHeld];
+    long long total;
+    __device__ __forceinline__ int at(const KvqSched& s, int b) const { return b < s.B ? kvq_seq(s, b).len : 0; }
+    __device__ __forceinline__ KvqLens(const KvqSched& s) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) len[i] = at(s, 32 * i + lane);
+        long long t = 0;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) t += len[i];
+        for (int b = 32 * kHeld + lane; b < s.B; b += 32) t += at(s, b);
+        total = static_cast<long long>(warp_sum_u64(static_cast<uint64_t>(t))) * s.per_seq;
+    }
+    // The sequence that holds unit pos < total, and the line's length before it (whole warp).
+    __device__ __forceinline__ int find(const KvqSched& s, long long pos, long long* base) const {
+        const int lane = threadIdx.x & 31;
+        long long before = 0;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int l = step(s, len[i], pos, &before, base);
+            if (l >= 0) return 32 * i + l;
+        }
+        for (int b0 = 32 * kHeld; b0 < s.B; b0 += 32) {
+            const int l = step(s, at(s, b0 + lane), pos, &before, base);
+            if (l >= 0) return b0 + l;
+        }
+        *base = before;
+        return s.B;  // not reached for pos < total
+    }
+
+private:
+    __device__ __forceinline__ int step(const KvqSched& s, int own, long long pos, long long* before, long long* base) const {
+        const int lane = threadIdx.x & 31;
+        uint32_t inc = own;  // 32 lengths of less than 2^26 each
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-            const uint64_t o = shfl_u64(static_cast<uint64_t>(inc), lane >= m ? lane - m : lane);
-            if (lane >= m) inc += static_cast<long long>(o);
+            const uint32_t o = __shfl_up_sync(0xffffffffu, inc, m);
+            if (lane >= m) inc += o;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + inc > pos);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            *base = before + static_cast<long long>(shfl_u64(static_cast<uint64_t>(inc - own), l));
-            return b0 + l;
-        }
-        before += static_cast<long long>(shfl_u64(static_cast<uint64_t>(inc), 31));
+        const long long end = *before + static_cast<long long>(inc) * s.per_seq;
+        const unsigned hit = __ballot_sync(0xffffffffu, end > pos);
+        const int l = hit ? __ffs(hit) - 1 : 31;
+        const uint32_t upto = __shfl_sync(0xffffffffu, inc, l), of_l = __shfl_sync(0xffffffffu, static_cast<uint32_t>(own), l);
+        if (hit) *base = *before + static_cast<long long>(upto - of_l) * s.per_seq;
+        else *before += static_cast<long long>(upto) * s.per_seq;
+        return hit ? l : -1;
     }
-    *base = before;
-    return s.B;  // not reached for pos < total
-}
+};
 
 // One piece: steps [t0, t1) of item `sub` of sequence b; np: pieces of the
 // item if this is its first and it is cut, else 0.
@@ -95,7 +122,8 @@ struct KvqCursor {
     int b, worker;
     KvqSeq q;
     __device__ __forceinline__ void init(const KvqSched& s, int w) {
-        const long long total = kvq_total(s);
+        const KvqLens lens(s);
+        const long long total = lens.total;
         worker = w;
         chunk = kvq_chunk(s, total);
         pos = min(total, worker * chunk);
@@ -103,7 +131,7 @@ struct KvqCursor {
         base = 0;
         b = 0;
         if (pos < end) {
-            b = kvq_find(s, pos, &base);
+            b = lens.find(s, pos, &base);
             q = kvq_seq(s, b);
         }
     }
@@ -116,7 +144,7 @@ struct KvqCursor {
                 while (q.len == 0);
                 continue;
             }
-            const int sub = static_cast<int>((pos - base) / q.len);
+            const int sub = static_cast<int>(kvq_div(pos - base, q.len));
             const long long g0 = base + static_cast<long long>(sub) * q.len;
             const int from = static_cast<int>(pos - g0);
             const int to = static_cast<int>(min(static_cast<long long>(q.len), end - g0));
@@ -129,16 +157,52 @@ struct KvqCursor {
             p.nt = q.nt;
             p.t0 = max(0, from - s.ov);
             p.t1 = max(0, to - s.ov);
-            p.np = p.t0 == 0 && p.t1 < p.nt ? static_cast<int>((g0 + s.ov + p.nt - 1) / chunk) - worker + 1 : 0;
+            p.np = 0;  // pieces: up to the worker that has the item's last unit
+            if (p.t0 == 0 && p.t1 < p.nt)
+                p.np = static_cast<int>(kvq_div(g0 + s.ov + p.nt - 1 - worker * chunk, chunk)) + 1;
             if (p.t1 > p.t0) return true;
         }
         return false;
     }
 };
 
-// Partial results of cut items: O [slot][row][128] (in units where O / sum is
-// the output), (max in the log2 domain, sum) [slot][row][2], and which cut
-// item each worker began: (pieces or 0, sequence, item, tree size) [worker].
+// The G*T query rows of a (sequence, KV head): row r <-> tree slot r / G, head hk*G + r % G.
+struct KvqRows {
+    int G, T, Hq;
+    // Row r's slot and its index in the [B*T*Hq] rows of q and out; -1: not a row.
+    __device__ __forceinline__ int64_t row(int b, int hk, int r, int* slot) const {
+        *slot = r / G;
+        if (*slot >= T) return -1;
+        return (static_cast<int64_t>(b) * T + *slot) * Hq + static_cast<int64_t>(hk) * G + (r - *slot * G);
+    }
+};
+
+// Running sum of pieces: (max in the log2 domain, sum, N x 4 columns of O).
+template <int N>
+struct RowSum {
+    float m = -INFINITY, l = 0.0f;
+    float4 o[N];
+    __device__ __forceinline__ RowSum() {
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    __device__ __forceinline__ void add(float pm, float pl, const float4 (&x)[N]) {
+        // a piece in which the row saw nothing: maximum -inf, O 0
+        const float M = fmaxf(m, pm);
+        const float a = m == -INFINITY ? 0.0f : ex2_approx(m - M), c = pm == -INFINITY ? 0.0f : ex2_approx(pm - M);
+        m = M;
+        l = l * a + pl * c;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            o[i] = make_float4(o[i].x * a + x[i].x * c, o[i].y * a + x[i].y * c, o[i].z * a + x[i].z * c, o[i].w * a + x[i].w * c);
+    }
+};
+
+// Partial results of cut items: O in units where O / sum is the output, (max
+// in the log2 domain, sum) [slot][row][2], and which cut item each worker began:
+// (pieces or 0, sequence, item, tree size) [worker]. O is [slot][row][128] for
+// the decode kernel; the tensor-core kernel, where a thread owns a row, stores
+// [slot][4-column group][row][4] (a row apiece, its stores took 10,000 cycles).
 struct KvqPartials {
     float* o;
     float* ml;
@@ -149,10 +213,11 @@ __device__ __forceinline__ int4 kvq_cut(const KvqPiece& p) { return make_int4(p.
 
 struct KvqMergeParams {
     KvqPartials part;
-    int workers, G, T, Hq, n_items;  // n_items: items of a KV head
+    KvqRows rows;
+    int workers, n_items;  // n_items: items of a KV head
     __nv_bfloat16* out;
 };
-cudaError_t launch_kvq_merge(const KvqMergeParams& p, cudaStream_t stream);
+cudaError_t launch_kvq_merge_decode(const KvqMergeParams& p, cudaStream_t stream);
 
 // Zero rows of the sequences whose lengths are out of range (status 3), dealt
 // over the workers: `n` threads of a worker, this one the i-th.
@@ -208,6 +273,8 @@ constexpr int kKvqSms = 152;
 struct KvqAttnParams {
     KvqSched s;
     KvqPartials part;
+    KvqRows rows;
+    const float* q_fac;  // tensor-core kernel: factors of the rows of q
     int Hq, Hkv, G, W;
     int n_items;    // items of a KV head (pairs of row blocks; 1 in the decode kernel)
     int blk_shift;  // log2 of the positions of a scale block
