@@ -522,27 +522,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = it.t0; j < it.t1; ++j, ++t, ++tg) {
                 const int key0 = j * kBN;
                 const uint32_t s_cols = tmem + 64 * (2 * g + (tg & 1)) + lane_off;
-                // visibility of 32 keys at a time: prefix keys, then tree slots in the row's mask
-                uint32_t vis[2] = {~0u, ~0u};
-                if (key0 + kBN > L) {
-#pragma unroll
-                    for (int hq = 0; hq < 2; ++hq) {
-                        const int kb = key0 + 32 * hq;
-                        const int npre = min(32, L - kb);  // keys of the 32 inside the prefix
-                        const uint32_t pre = npre > 0 ? 0xffffffffu >> (32 - npre) : 0u;
-                        const int j0 = kb - L;  // slot of the first key (may be negative)
-                        const int lo = j0 < 0 ? 0 : j0;
-                        const int w0 = lo >> 5, sh = lo & 31;
-                        uint32_t win = word(w0) >> sh;
-                        if (sh) win |= word(w0 + 1) << (32 - sh);
-                        const int limit = n - lo;  // slots j >= n are never visible
-                        if (limit <= 0) win = 0u;
-                        else if (limit < 32) win &= (1u << limit) - 1u;
-                        uint32_t tree = j0 < 0 ? (win << (-j0 & 31)) : win;
-                        if (j0 <= -32) tree = 0u;
-                        vis[hq] = pre | tree;
-                    }
-                }
                 wait.both(&bar_sc[t & (kScaleSlots - 1)], t / kScaleSlots, &bar_s_full[g][tg & 1], tg >> 1);
                 tc_fence_after();
                 if (quarter_live) {
@@ -555,10 +534,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sref = sc.sref;
                     uint32_t s[kBN];
                     tmem_ld64(s_cols, s);
+                    // visibility of 32 keys at a time: prefix keys, then tree slots in the row's mask
                     if (key0 + kBN > L) {
+                        uint32_t vis[2];
 #pragma unroll
-                        for (int e = 0; e < kBN; ++e)
-                            s[e] = ((vis[e >> 5] >> (e & 31)) & 1u) ? s[e] : 0xff800000u;
+                        for (int hq = 0; hq < 2; ++hq) {
+                            const int kb = key0 + 32 * hq;
+                            const int npre = min(32, L - kb);  // keys of the 32 inside the prefix
+                            const uint32_t pre = npre > 0 ? 0xffffffffu >> (32 - npre) : 0u;
+                            const int j0 = kb - L;  // slot of the first key (may be negative)
+                            const int lo = j0 < 0 ? 0 : j0;
+                            const int w0 = lo >> 5, sh = lo & 31;
+                            uint32_t win = word(w0) >> sh;
+                            if (sh) win |= word(w0 + 1) << (32 - sh);
+                            const int limit = n - lo;  // slots j >= n are never visible
+                            if (limit <= 0) win = 0u;
+                            else if (limit < 32) win &= (1u << limit) - 1u;
+                            uint32_t tree = j0 < 0 ? (win << (-j0 & 31)) : win;
+                            if (j0 <= -32) tree = 0u;
+                            vis[hq] = pre | tree;
+                        }
+#pragma unroll
+                        for (int e = 0; e < kBN; ++e) s[e] = ((vis[e >> 5] >> (e & 31)) & 1u) ? s[e] : 0xff800000u;
                     }
                     const float mx = fmaxf(fmaxf(max16(s) * k[0], max16(s + 16) * k[1]),
                                            fmaxf(max16(s + 32) * k[2], max16(s + 48) * k[3]));  // the scales are positive
@@ -576,7 +573,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     // (the vote here: its answer is not needed before P is written)
-                    const bool any_rescale = __any_sync(0xffffffffu, rescale);
                     // P = 2^(s k - m_use + lv), two per packed multiply-add; the row sum takes the
                     // reverse of V's ratio. P as fp16 pairs over the first 32 columns of S.
                     // (A group's arguments, then its exponentials, then the last group's sums and
@@ -621,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // Rescaling O needs PV of the previous tile done (this tile's PV waits for
                     // this warp's arrival below). tcgen05.ld/st are warp-collective: rescale if
                     // any row of the warp needs it (alpha = 1 for the others).
-                    if (j > it.t0 && any_rescale) {
+                    if (j > it.t0 && __any_sync(0xffffffffu, rescale)) {
                         wait(&bar_pv_done[g][(tg - 1) & 1], (tg - 1) >> 1);
                         tc_fence_after();
 #pragma unroll 1
@@ -761,7 +757,7 @@ Plan make_plan(const KvqDims& kv, int T) {
     } else {
         pl.n_items = (rows + 2 * kBM - 1) / (2 * kBM);
         pl.rows = 2 * kBM;
-        pl.s = KvqSched{nullptr, nullptr, kv.B, T, kv.max_len, kv.Hkv * pl.n_items, kBN, 3, kKvqSms, 5};
+        pl.s = KvqSched{nullptr, nullptr, kv.B, T, kv.max_len, kv.Hkv * pl.n_items, kBN, 4, kKvqSms, 6};
     }
     const size_t slots = 2 * static_cast<size_t>(pl.s.workers) * pl.rows;
     pl.off_cut = 256;
