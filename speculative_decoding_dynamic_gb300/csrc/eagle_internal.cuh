@@ -178,6 +178,13 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// 2^(e) for the power of two that brings a row's largest |q| into [2^to, 2^(to+1)): exponent field of the scale
+__device__ __forceinline__ float pow2_to(float amax, int to) {
+    const int e = static_cast<int>(__float_as_uint(amax) >> 23);  // biased; 0 for zero and subnormals
+    const int f = to + 254 - e;                                   // biased exponent of the scale
+    return __uint_as_float(static_cast<uint32_t>(max(1, min(f, 253))) << 23);
+}
+
 // Bounded wait on an mbarrier phase. Returns false after ~max_iter polls
 // (each poll may suspend the thread for a hardware-chosen time).
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t max_iter = (1u << 21)) {

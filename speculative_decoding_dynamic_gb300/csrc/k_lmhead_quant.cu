@@ -6,14 +6,22 @@
 // With the few rows of a small batch the weight's bytes are the cost (V*H/2,
 // a quarter of the 16-bit head's), 4 M flops a byte. Per byte there is little
 // time: two products per code and row, so the codes are taken from registers:
-//   - mma.sync m16n8k16 with the weight as A (16 vocabulary rows) and the
-//     hidden rows as B (8 per MMA). tcgen05 would need the weight as bf16 in
-//     shared or tensor memory: four times its bytes written and read again
-//     on chip, more than shared memory's bandwidth at HBM's pace.
-//   - a code becomes bf16 in two instructions per pair: (w >> s & 0x000f000f)
-//     | 0x43004300 is 128 + c, minus 136 is c - 8, both exact. The products of a
-//     group are summed by the tensor core in fp32 and multiplied by the
-//     group's scale in fp32: no rounding of a weight at all.
+//   - mma.sync m16n8k16 in fp16 with the weight as A (16 vocabulary rows) and
+//     the hidden rows as B (8 per MMA). tcgen05 would need the weight in shared
+//     or tensor memory: a code as a byte at least, twice its size, written and
+//     read again on chip. (The e4m3 form of this instruction is no shortcut: it
+//     runs as two fp16 ones behind conversions of both operands, 188 us at 8B.)
+//   - the fp16 number with the bits 0000 0000 0000 cccc is c 2^-24, and with
+//     the code four bits higher 16 times that (subnormals, which the tensor core
+//     takes exactly), so a word's eight codes become four operand registers in five
+//     instructions: w & 0x000f000f and w & 0x00f000f0, the same of w >> 8. (To bf16
+//     numbers c - 8 it takes eleven: 112 us at 8B.) The hidden entries of the higher
+//     codes are 16 times smaller, and the 8 that a code is above its weight is
+//     taken off by the accumulator's start: -8 times the group's sum of the hidden row.
+//   - a hidden row is scaled by the power of two that brings its largest element
+//     into [2^14, 2^15): its bf16 entries are fp16 numbers then, exact down to
+//     2^-28 of the largest.
+//   - a group's sum is multiplied by its scale in fp32: no rounding of a weight.
 //   - the hidden dimension is summed over in an order in which a lane holds
 //     32 neighbouring entries of a weight row (one 16-byte load of codes per
 //     128 entries) and the hidden rows are laid out in shared memory in that
@@ -28,6 +36,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 
@@ -53,16 +62,17 @@ struct QuantParams {
     int rows;        // hidden rows of a pass (blockIdx.y takes rows [y * rows, ...))
     int stages, bufs;  // ring stages of an MMA warp; buffers of partial sums
     int hid_stride;  // bytes of a hidden row in shared memory
+    int c_stride;    // floats of a group's corrections
     const __nv_bfloat16* hidden;
     const __nv_bfloat16* scales;
     void* out;
     int* status;
 };
 
-__device__ __forceinline__ void mma_bf16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
         "%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -79,25 +89,20 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
     return v;
 }
 
-// Codes at bits S and 16 + S of w as bf16 pairs c - 8.
-template <int S>
-__device__ __forceinline__ uint32_t pair(uint32_t w) {
-    const uint32_t x = ((w >> S) & 0x000f000fu) | 0x43004300u;  // 128 + c
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), __float2bfloat162_rn(136.0f));
-    return *reinterpret_cast<const uint32_t*>(&d);
-}
-
 // A warp's bounded wait.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 
-// First hidden entry (within a slice) of the eight that lane t of a quad
-// takes in step pair q (0..3): neighbouring words of the lane's codes, for a
-// group that spans the slice; quarters of the slice for the smaller groups.
+// Where the eight entries from `e` (within a slice, a multiple of 8) stand: lane
+// t of a quad takes eight entries in each of the steps q = 0..3, neighbouring words
+// of its codes for a group that spans the slice, quarters of the slice for the
+// smaller groups. Piece (q, t), 16 bytes, is the (4 q + t)-th.
 template <int GROUP>
-__device__ __forceinline__ int entry0(int q, int t) {
-    return GROUP == 128 ? t * 32 + q * 8 : GROUP == 64 ? (q >> 1) * 64 + t * 16 + (q & 1) * 8 : q * 32 + t * 8;
+__device__ __forceinline__ int piece_of(int e) {
+    const int t = GROUP == 128 ? e >> 5 : GROUP == 64 ? (e >> 4) & 3 : (e >> 3) & 3;
+    const int q = GROUP == 128 ? (e >> 3) & 3 : GROUP == 64 ? (e >> 6) * 2 + ((e >> 3) & 1) : e >> 5;
+    return 4 * q + t;
 }
 
 // A row's NG scales of a slice as one load.
@@ -140,10 +145,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = lane >> 2, t = lane & 3;
     const int m0 = blockIdx.y * p.rows;
     const int rows = min(p.rows, p.M - m0);
-    // rings of the MMA warps; hidden rows; partial sums of a tile, [buffer][warp][hidden row][CS]
+    // rings of the MMA warps; hidden rows; corrections [group][c_stride]; the rows' factors;
+    // partial sums of a tile, [buffer][warp][hidden row][CS]
     unsigned char* ring = smem + warp * p.stages * kStage;
     unsigned char* hid = smem + kMmaWarps * p.stages * kStage;
-    float* red = reinterpret_cast<float*>(hid + p.rows * p.hid_stride);
+    float* corr = reinterpret_cast<float*>(hid + p.rows * p.hid_stride);
+    float* fac = corr + p.n_slice * NG * p.c_stride;
+    float* red = fac + 16;
     // this CTA's vocabulary rows, in units of 16
     const int units = (p.V + 15) / 16;
     const int u0 = static_cast<int>(static_cast<long>(units) * blockIdx.x / gridDim.x);
@@ -188,15 +196,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (warp < kMmaWarps)
         for (int s = 0; s < p.stages; ++s) fill();
-    // hidden rows into shared memory: 16-byte pieces of eight entries in MMA order
-    // (0 4, 1 5, 2 6, 3 7), piece (slice, q, t) of a row at (slice * 16 + 4 q + t) * 16
-    for (int i = threadIdx.x; i < rows * p.n_slice * 16; i += kThreads) {
-        const int m = i / (p.n_slice * 16), c = i - m * p.n_slice * 16;
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p.hidden + static_cast<size_t>(m0 + m) * p.H +
-                                                             (c >> 4) * kSlice + entry0<GROUP>((c >> 2) & 3, c & 3)));
-        *reinterpret_cast<uint4*>(hid + m * p.hid_stride + c * 16) =
-            make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632), __byte_perm(u.y, u.w, 0x5410),
-                       __byte_perm(u.y, u.w, 0x7632));
+    // hidden rows into shared memory, a warp per row: its largest element, then pieces of eight
+    // entries as fp16 in MMA order (0 4, 1 5, 2 6, 3 7), and the groups' corrections
+    for (int m = warp; m < p.c_stride; m += kMmaWarps + kAddWarps) {
+        if (m >= rows) {  // columns of the last n-tile without a row
+            for (int i = lane; i < p.n_slice * NG; i += 32) corr[i * p.c_stride + m] = 0.0f;
+            continue;
+        }
+        const uint4* src = reinterpret_cast<const uint4*>(p.hidden + static_cast<size_t>(m0 + m) * p.H);
+        const int pieces = p.H / 8;
+        uint32_t mx = 0u;
+#pragma unroll 8
+        for (int i = lane; i < pieces; i += 32) {
+            const uint4 u = __ldg(src + i);
+            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mx = max(mx & 0xffffu, mx >> 16);
+        const float scale = pow2_to(__uint_as_float(mx << 16), 14);
+        // an infinity or NaN in the row makes its logits NaN
+        if (lane == 0) fac[m] = mx < 0x7f80u ? 1.0f / scale : __uint_as_float(0x7fffffffu);
+        unsigned char* row = hid + m * p.hid_stride;
+#pragma unroll 4
+        for (int i = lane; i < pieces; i += 32) {  // a multiple of 16 pieces: a group's lanes are in range together
+            const uint4 u = __ldg(src + i);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            float x[8], sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[e] = __uint_as_float((e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16)) * scale;
+            uint32_t h[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float f = (c & 1) ? 0x1p-4f : 1.0f;
+                const __half2 y = __floats2half2_rn(x[c] * f, x[c + 4] * f);
+                const float2 b = __half22float2(y);
+                sum += (b.x + b.y) * ((c & 1) ? 16.0f : 1.0f);
+                h[c] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            *reinterpret_cast<uint4*>(row + ((i >> 4) * 16 + piece_of<GROUP>((i & 15) * 8)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+            const unsigned in = i - lane + 32 <= pieces ? 0xffffffffu : 0xffffu;
+#pragma unroll
+            for (int o = 1; o < GROUP / 8; o <<= 1) sum += __shfl_xor_sync(in, sum, o);
+            if (i % (GROUP / 8) == 0) corr[i / (GROUP / 8) * p.c_stride + m] = -0x1p-21f * sum;
+        }
     }
     __syncthreads();
 
@@ -259,10 +303,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     if (q % (4 / NG) == 0) {
+                        const uint32_t c = smem_u32(corr) + ((slice * NG + q / (4 / NG)) * p.c_stride + 2 * t) * 4;
 #pragma unroll
-                        for (int a = 0; a < MT; ++a)
+                        for (int b = 0; b < NT; ++b) {
+                            const uint2 x = lds64(c + b * 32);
 #pragma unroll
-                            for (int b = 0; b < NT; ++b) acc[a][b][0] = acc[a][b][1] = acc[a][b][2] = acc[a][b][3] = 0.0f;
+                            for (int a = 0; a < MT; ++a) {
+                                acc[a][b][0] = acc[a][b][2] = __uint_as_float(x.x);
+                                acc[a][b][1] = acc[a][b][3] = __uint_as_float(x.y);
+                            }
+                        }
                     }
                     uint4 hb[NT];
 #pragma unroll
@@ -273,13 +323,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (int a = 0; a < MT; ++a) {
-                        const uint32_t lo = w[a][0][q], hi = w[a][1][q];
-                        const uint32_t a0 = pair<0>(lo), a1 = pair<0>(hi), a2 = pair<4>(lo), a3 = pair<4>(hi);
-                        const uint32_t a4 = pair<8>(lo), a5 = pair<8>(hi), a6 = pair<12>(lo), a7 = pair<12>(hi);
+                        const uint32_t x = w[a][0][q], y = w[a][1][q], x8 = x >> 8, y8 = y >> 8;
+                        constexpr uint32_t k0 = 0x000f000fu, k4 = 0x00f000f0u;
 #pragma unroll
                         for (int b = 0; b < NT; ++b) {
-                            mma_bf16_16816(acc[a][b], a0, a1, a2, a3, hb[b].x, hb[b].y);
-                            mma_bf16_16816(acc[a][b], a4, a5, a6, a7, hb[b].z, hb[b].w);
+                            mma_f16_16816(acc[a][b], x & k0, y & k0, x & k4, y & k4, hb[b].x, hb[b].y);
+                            mma_f16_16816(acc[a][b], x8 & k0, y8 & k0, x8 & k4, y8 & k4, hb[b].z, hb[b].w);
                         }
                     }
                     if (q % (4 / NG) == 4 / NG - 1) {
@@ -338,6 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     x += s.x;
                     y += s.y;
                 }
+                x = x * 0x1p24f * fac[m];
+                y = y * 0x1p24f * fac[m];
                 const size_t o = static_cast<size_t>(m0 + m) * p.V + v + r;
                 if (BF16) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + o) = pack_bf16(x, y);
                 else *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o) = make_float2(x, y);
@@ -362,8 +413,9 @@ bool make_map(CUtensorMap* m, const void* codes, int V, int H, int rows) {
 }
 
 // Shared memory of a pass of `rows` hidden rows with RT-row tiles, `stages` per ring and `bufs` buffers of partial sums.
-int smem_bytes(int rows, int H, int RT, int stages, int bufs) {
-    return kMmaWarps * stages * RT * kSliceBytes + rows * (2 * H + 64) + bufs * kMmaWarps * rows * (RT + 4) * 4 + 128;
+int smem_bytes(int rows, int H, int group, int RT, int stages, int bufs) {
+    return kMmaWarps * stages * RT * kSliceBytes + rows * (2 * H + 64) + ((H / group) * ((rows + 7) & ~7) + 16) * 4 +
+           bufs * kMmaWarps * rows * (RT + 4) * 4 + 128;
 }
 
 template <int RT, int NT, int GROUP, bool BF16>
@@ -441,13 +493,14 @@ cudaError_t launch_lmhead_quant(int M, int V, int H, int group, const void* hidd
     const bool bf16 = out_dtype == 1;
     auto run = [&](int rows, int RT, auto fn, cudaError_t* e) -> bool {
         int st = 2, nb = 1;
-        if (smem_bytes(rows, H, RT, st, nb) > kMaxSmem) return false;
-        if (smem_bytes(rows, H, RT, st, 2) <= kMaxSmem) nb = 2;
-        while (st < kMaxStages && smem_bytes(rows, H, RT, st + 1, nb) <= kMaxSmem) ++st;
+        if (smem_bytes(rows, H, group, RT, st, nb) > kMaxSmem) return false;
+        if (smem_bytes(rows, H, group, RT, st, 2) <= kMaxSmem) nb = 2;
+        while (st < kMaxStages && smem_bytes(rows, H, group, RT, st + 1, nb) <= kMaxSmem) ++st;
         p.rows = rows;
+        p.c_stride = (rows + 7) & ~7;
         p.stages = st;
         p.bufs = nb;
-        *e = fn(p, group, bf16, codes, smem_bytes(rows, H, RT, st, nb), stream);
+        *e = fn(p, group, bf16, codes, smem_bytes(rows, H, group, RT, st, nb), stream);
         return true;
     };
     cudaError_t e = cudaErrorInvalidValue;

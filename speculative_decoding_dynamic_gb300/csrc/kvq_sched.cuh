@@ -244,13 +244,6 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
     return d;
 }
-// 2^(e) for the power of two that brings a row's largest |q| into [2^to, 2^(to+1)): exponent field of the scale
-__device__ __forceinline__ float pow2_to(float amax, int to) {
-    const int e = static_cast<int>(__float_as_uint(amax) >> 23);  // biased; 0 for zero and subnormals
-    const int f = to + 254 - e;                                   // biased exponent of the scale
-    return __uint_as_float(static_cast<uint32_t>(max(1, min(f, 253))) << 23);
-}
-
 // A 4-D map of codes: (128 bytes of a head, head, position, sequence), 128-byte swizzle.
 inline bool make_map_codes(CUtensorMap* m, const void* base, const KvqDims& kv, int keys) {
     auto fn = tensor_map_encode_fn();
