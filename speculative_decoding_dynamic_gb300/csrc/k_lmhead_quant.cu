@@ -172,11 +172,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait_prior();
     const int my_slices = warp < kMmaWarps ? (p.n_slice - warp + kMmaWarps - 1) / kMmaWarps : 0;
     const int total = my_slices * n_tiles;  // stages this warp consumes
-    int filled = 0, f_tile = 0, f_slice = warp;
+    int filled = 0, f_tile = 0, f_slice = warp, f_stage = 0;
     auto fill = [&]() {
         if (filled >= total) return;
         if (lane == 0) {
-            const int s = filled % p.stages;
+            const int s = f_stage;
             uint64_t* bar = &bar_full[warp][s];
             const int v = v0 + f_tile * RT;
             const int mts = min(MT, (v1 - v) / 16);  // a last tile of fewer rows: 16 at a time
@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_2d(ring + s * kStage + i * 16 * kSliceBytes, &tm16, f_slice * kSliceBytes, v + 16 * i, bar);
         }
         ++filled;
+        f_stage = f_stage + 1 == p.stages ? 0 : f_stage + 1;
         f_slice += kMmaWarps;
         if (f_slice >= p.n_slice) {
             f_slice = warp;
@@ -246,7 +247,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kMmaWarps) {
         bool ok = true;
-        int used = 0;
+        // the lane's hidden row of each n-tile (columns without a row repeat the last one: nobody reads their sums)
+        uint32_t h_at[NT];
+#pragma unroll
+        for (int b = 0; b < NT; ++b) h_at[b] = smem_u32(hid) + min(b * 8 + g, rows - 1) * p.hid_stride + t * 16;
+        int used = 0, st = 0;
+        uint32_t phase = 0;
         for (int tile = 0; tile < n_tiles; ++tile) {
             const int v = v0 + tile * RT;
             const int mts = min(MT, (v1 - v) / 16);
@@ -255,31 +261,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int a = 0; a < MT; ++a)
 #pragma unroll
                 for (int b = 0; b < NT; ++b) sum[a][b][0] = sum[a][b][1] = sum[a][b][2] = sum[a][b][3] = 0.0f;
-            // scales of rows g, g + 8 of every m-tile, a slice's NG together, read a slice ahead
+            // scales of rows g, g + 8 of every m-tile, a slice's NG together, read two slices
+            // ahead (one ahead, the warps waited for them a quarter of their time)
             const int last = (p.V - 1 - v - g) >> 3;  // rows past the vocabulary read its last one's
-            Scales next[2 * MT];
-            auto read_scales = [&](int slice) {
-                const __nv_bfloat16* src = p.scales + (static_cast<size_t>(v + g) * p.n_slice + slice) * NG;
-                const size_t step = static_cast<size_t>(8) * p.n_slice * NG;
+            const __nv_bfloat16* scales = p.scales + static_cast<size_t>(v + g) * p.n_slice * NG;
+            uint32_t off[2 * MT];
 #pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) next[i] = __ldg(reinterpret_cast<const Scales*>(src + min(i, last) * step));
+            for (int i = 0; i < 2 * MT; ++i) off[i] = static_cast<uint32_t>(max(0, min(i, last)) * 8 * p.n_slice * NG);
+            Scales ahead[2][2 * MT];
+            auto read_scales = [&](Scales (&to)[2 * MT], int slice) {
+                const __nv_bfloat16* src = scales + min(slice, p.n_slice - 1) * NG;
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i) to[i] = __ldg(reinterpret_cast<const Scales*>(src + off[i]));
             };
-            read_scales(min(warp, p.n_slice - 1));
+            read_scales(ahead[0], warp);
+            read_scales(ahead[1], warp + kMmaWarps);
             for (int slice = warp; slice < p.n_slice; slice += kMmaWarps) {
-                const int st = used % p.stages;
                 Scales sc[2 * MT];
 #pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) sc[i] = next[i];
-                read_scales(min(slice + kMmaWarps, p.n_slice - 1));
-                if (ok && !warp_wait(&bar_full[warp][st], (used / p.stages) & 1)) {
+                for (int i = 0; i < 2 * MT; ++i) {
+                    sc[i] = ahead[0][i];
+                    ahead[0][i] = ahead[1][i];
+                }
+                read_scales(ahead[1], slice + 2 * kMmaWarps);
+                if (ok && !warp_wait(&bar_full[warp][st], phase)) {
                     ok = false;
                     if (lane == 0) raise_status(p.status, kDevTimeout);
                     for (int f = used + 1; f < filled; ++f)  // copies land before shared memory goes away
                         warp_wait(&bar_full[warp][f % p.stages], (f / p.stages) & 1);
                 }
-                ++used;
-                if (!ok) continue;
                 const uint32_t src = smem_u32(ring) + st * kStage;
+                ++used;
+                if (++st == p.stages) {
+                    st = 0;
+                    phase ^= 1;
+                }
+                if (!ok) continue;
                 uint32_t w[MT][2][4];
 #pragma unroll
                 for (int a = 0; a < MT; ++a)
@@ -316,11 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     uint4 hb[NT];
 #pragma unroll
-                    for (int b = 0; b < NT; ++b) {
-                        const int m = b * 8 + g;
-                        hb[b] = m < rows ? lds128(smem_u32(hid) + m * p.hid_stride + (slice * 16 + q * 4 + t) * 16)
-                                         : make_uint4(0u, 0u, 0u, 0u);
-                    }
+                    for (int b = 0; b < NT; ++b) hb[b] = lds128(h_at[b] + (slice * 16 + q * 4) * 16);
 #pragma unroll
                     for (int a = 0; a < MT; ++a) {
                         const uint32_t x = w[a][0][q], y = w[a][1][q], x8 = x >> 8, y8 = y >> 8;
