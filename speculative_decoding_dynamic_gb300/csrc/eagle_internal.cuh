@@ -185,6 +185,16 @@ __device__ __forceinline__ float pow2_to(float amax, int to) {
     return __uint_as_float(static_cast<uint32_t>(max(1, min(f, 253))) << 23);
 }
 
+// One look at an mbarrier phase, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 // Bounded wait on an mbarrier phase. Returns false after ~max_iter polls
 // (each poll may suspend the thread for a hardware-chosen time).
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t max_iter = (1u << 21)) {

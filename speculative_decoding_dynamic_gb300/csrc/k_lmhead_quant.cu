@@ -30,8 +30,9 @@
 // vocabulary in tiles of 64 rows; its eight MMA warps split the hidden
 // dimension (warp w: the 128-wide slices w, w + 8, ...), so that each works
 // alone, streaming its slices of one tile after the other through its own
-// ring of TMA tiles; two more warps add the eight partial sums of a finished
-// tile and write the logits while the next tile streams.
+// ring of TMA tiles (filled by a warp for all eight rings: a copy's issue takes
+// 400 cycles); three more warps add the eight partial sums of a finished tile
+// and write the logits while the next tile streams.
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -49,8 +50,8 @@ namespace eagle {
 namespace {
 
 constexpr int kMmaWarps = 8;
-constexpr int kAddWarps = 2;
-constexpr int kThreads = (kMmaWarps + kAddWarps) * 32;
+constexpr int kAddWarps = 3;
+constexpr int kThreads = (kMmaWarps + kAddWarps + 1) * 32;  // and the copying warp: three warps per scheduler, 168 registers
 constexpr int kSlice = 128;                // hidden entries of a slice
 constexpr int kSliceBytes = kSlice / 2;    // codes of one row's slice
 constexpr int kMaxStages = 4;
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-    __shared__ uint64_t bar_full[kMmaWarps][kMaxStages], bar_red_full[2], bar_red_empty[2];
+    __shared__ uint64_t bar_full[kMmaWarps][kMaxStages], bar_empty[kMmaWarps][kMaxStages], bar_red_full[2], bar_red_empty[2];
     constexpr int MT = RT / 16;
     constexpr int kStage = RT * kSliceBytes;
     constexpr int NG = kSlice / GROUP;  // groups of a slice
@@ -160,7 +161,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n_tiles = (v1 - v0 + RT - 1) / RT;
     if (threadIdx.x == 0) {
         for (int w = 0; w < kMmaWarps; ++w)
-            for (int s = 0; s < p.stages; ++s) mbar_init(&bar_full[w][s], 1);
+            for (int s = 0; s < p.stages; ++s) {
+                mbar_init(&bar_full[w][s], 1);
+                mbar_init(&bar_empty[w][s], 1);
+            }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bar_red_full[s], kMmaWarps);
             mbar_init(&bar_red_empty[s], kAddWarps);
@@ -170,36 +174,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     pdl_launch_dependents();
     pdl_wait_prior();
-    const int my_slices = warp < kMmaWarps ? (p.n_slice - warp + kMmaWarps - 1) / kMmaWarps : 0;
-    const int total = my_slices * n_tiles;  // stages this warp consumes
-    int filled = 0, f_tile = 0, f_slice = warp, f_stage = 0;
+    // The copying warp: lane w fills the ring of MMA warp w, the first stages before the hidden rows are read.
+    const bool copies = warp == kMmaWarps + kAddWarps;
+    const int total = copies && lane < kMmaWarps ? (p.n_slice - lane + kMmaWarps - 1) / kMmaWarps * n_tiles : 0;
+    int filled = 0, f_tile = 0, f_slice = lane, f_stage = 0;
+    uint32_t f_phase = 1;  // of the stage's release; the first round waits for nothing
     auto fill = [&]() {
-        if (filled >= total) return;
-        if (lane == 0) {
-            const int s = f_stage;
-            uint64_t* bar = &bar_full[warp][s];
-            const int v = v0 + f_tile * RT;
-            const int mts = min(MT, (v1 - v) / 16);  // a last tile of fewer rows: 16 at a time
-            mbar_arrive_expect_tx(bar, mts * 16 * kSliceBytes);
-            if (mts == MT)
-                tma_load_2d(ring + s * kStage, &tm, f_slice * kSliceBytes, v, bar);
-            else
-                for (int i = 0; i < mts; ++i)
-                    tma_load_2d(ring + s * kStage + i * 16 * kSliceBytes, &tm16, f_slice * kSliceBytes, v + 16 * i, bar);
-        }
+        uint64_t* bar = &bar_full[lane][f_stage];
+        unsigned char* dst = smem + (lane * p.stages + f_stage) * kStage;
+        const int v = v0 + f_tile * RT;
+        const int mts = min(MT, (v1 - v) / 16);  // a last tile of fewer rows: 16 at a time
+        mbar_arrive_expect_tx(bar, mts * 16 * kSliceBytes);
+        if (mts == MT)
+            tma_load_2d(dst, &tm, f_slice * kSliceBytes, v, bar);
+        else
+            for (int i = 0; i < mts; ++i) tma_load_2d(dst + i * 16 * kSliceBytes, &tm16, f_slice * kSliceBytes, v + 16 * i, bar);
         ++filled;
-        f_stage = f_stage + 1 == p.stages ? 0 : f_stage + 1;
+        if (++f_stage == p.stages) {
+            f_stage = 0;
+            f_phase ^= 1;
+        }
         f_slice += kMmaWarps;
         if (f_slice >= p.n_slice) {
-            f_slice = warp;
+            f_slice = lane;
             ++f_tile;
         }
     };
-    if (warp < kMmaWarps)
-        for (int s = 0; s < p.stages; ++s) fill();
+    if (copies)
+        while (filled < min(p.stages, total)) fill();
+    __syncwarp();
     // hidden rows into shared memory, a warp per row: its largest element, then pieces of eight
     // entries as fp16 in MMA order (0 4, 1 5, 2 6, 3 7), and the groups' corrections
-    for (int m = warp; m < p.c_stride; m += kMmaWarps + kAddWarps) {
+    for (int m = warp; m < p.c_stride; m += kThreads / 32) {
         if (m >= rows) {  // columns of the last n-tile without a row
             for (int i = lane; i < p.n_slice * NG; i += 32) corr[i * p.c_stride + m] = 0.0f;
             continue;
@@ -216,31 +222,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int o = 16; o > 0; o >>= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         mx = max(mx & 0xffffu, mx >> 16);
         const float scale = pow2_to(__uint_as_float(mx << 16), 14);
+        const float scale16 = scale * 0x1p-4f;
         // an infinity or NaN in the row makes its logits NaN
         if (lane == 0) fac[m] = mx < 0x7f80u ? 1.0f / scale : __uint_as_float(0x7fffffffu);
         unsigned char* row = hid + m * p.hid_stride;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = lane; i < pieces; i += 32) {  // a multiple of 16 pieces: a group's lanes are in range together
             const uint4 u = __ldg(src + i);
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-            float x[8], sum = 0.0f;
+            float x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                x[e] = __uint_as_float((e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16)) * scale;
+            for (int e = 0; e < 8; ++e) x[e] = __uint_as_float((e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16));
+            float sum = ((x[0] + x[4]) + (x[1] + x[5])) + ((x[2] + x[6]) + (x[3] + x[7]));
             uint32_t h[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const float f = (c & 1) ? 0x1p-4f : 1.0f;
+                const float f = (c & 1) ? scale16 : scale;
                 const __half2 y = __floats2half2_rn(x[c] * f, x[c + 4] * f);
-                const float2 b = __half22float2(y);
-                sum += (b.x + b.y) * ((c & 1) ? 16.0f : 1.0f);
                 h[c] = *reinterpret_cast<const uint32_t*>(&y);
             }
             *reinterpret_cast<uint4*>(row + ((i >> 4) * 16 + piece_of<GROUP>((i & 15) * 8)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
             const unsigned in = i - lane + 32 <= pieces ? 0xffffffffu : 0xffffu;
 #pragma unroll
             for (int o = 1; o < GROUP / 8; o <<= 1) sum += __shfl_xor_sync(in, sum, o);
-            if (i % (GROUP / 8) == 0) corr[i / (GROUP / 8) * p.c_stride + m] = -0x1p-21f * sum;
+            if (i % (GROUP / 8) == 0) corr[i / (GROUP / 8) * p.c_stride + m] = sum * scale * -0x1p-21f;
         }
     }
     __syncthreads();
@@ -251,8 +256,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t h_at[NT];
 #pragma unroll
         for (int b = 0; b < NT; ++b) h_at[b] = smem_u32(hid) + min(b * 8 + g, rows - 1) * p.hid_stride + t * 16;
-        int used = 0, st = 0;
+        int st = 0;
         uint32_t phase = 0;
+        // scales of rows g, g + 8 of every m-tile, a slice's NG together, read a slice ahead, also
+        // over the border of a tile; rows past the vocabulary read its last one's
+        Scales next[2 * MT];
+        int r_tile = 0, r_slice = warp;
+        auto read_scales = [&]() {
+            if (r_tile >= n_tiles || warp >= p.n_slice) return;
+            const int v = v0 + r_tile * RT, last = max(0, (p.V - 1 - v - g) >> 3);
+            const __nv_bfloat16* src = p.scales + (static_cast<size_t>(v + g) * p.n_slice + r_slice) * NG;
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) next[i] = __ldg(reinterpret_cast<const Scales*>(src + min(i, last) * 8 * p.n_slice * NG));
+            r_slice += kMmaWarps;
+            if (r_slice >= p.n_slice) {
+                r_slice = warp;
+                ++r_tile;
+            }
+        };
+        read_scales();
         for (int tile = 0; tile < n_tiles; ++tile) {
             const int v = v0 + tile * RT;
             const int mts = min(MT, (v1 - v) / 16);
@@ -261,37 +283,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int a = 0; a < MT; ++a)
 #pragma unroll
                 for (int b = 0; b < NT; ++b) sum[a][b][0] = sum[a][b][1] = sum[a][b][2] = sum[a][b][3] = 0.0f;
-            // scales of rows g, g + 8 of every m-tile, a slice's NG together, read two slices
-            // ahead (one ahead, the warps waited for them a quarter of their time)
-            const int last = (p.V - 1 - v - g) >> 3;  // rows past the vocabulary read its last one's
-            const __nv_bfloat16* scales = p.scales + static_cast<size_t>(v + g) * p.n_slice * NG;
-            uint32_t off[2 * MT];
-#pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) off[i] = static_cast<uint32_t>(max(0, min(i, last)) * 8 * p.n_slice * NG);
-            Scales ahead[2][2 * MT];
-            auto read_scales = [&](Scales (&to)[2 * MT], int slice) {
-                const __nv_bfloat16* src = scales + min(slice, p.n_slice - 1) * NG;
-#pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) to[i] = __ldg(reinterpret_cast<const Scales*>(src + off[i]));
-            };
-            read_scales(ahead[0], warp);
-            read_scales(ahead[1], warp + kMmaWarps);
             for (int slice = warp; slice < p.n_slice; slice += kMmaWarps) {
                 Scales sc[2 * MT];
 #pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) {
-                    sc[i] = ahead[0][i];
-                    ahead[0][i] = ahead[1][i];
-                }
-                read_scales(ahead[1], slice + 2 * kMmaWarps);
+                for (int i = 0; i < 2 * MT; ++i) sc[i] = next[i];
+                read_scales();
                 if (ok && !warp_wait(&bar_full[warp][st], phase)) {
                     ok = false;
                     if (lane == 0) raise_status(p.status, kDevTimeout);
-                    for (int f = used + 1; f < filled; ++f)  // copies land before shared memory goes away
-                        warp_wait(&bar_full[warp][f % p.stages], (f / p.stages) & 1);
                 }
                 const uint32_t src = smem_u32(ring) + st * kStage;
-                ++used;
+                uint64_t* release = &bar_empty[warp][st];
                 if (++st == p.stages) {
                     st = 0;
                     phase ^= 1;
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 __syncwarp();  // every lane has read the stage
-                fill();
+                if (lane == 0) mbar_arrive(release);
                 float acc[MT][NT][4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -360,7 +362,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && turn > 0 && !warp_wait(&bar_red_empty[buf], (turn - 1) & 1)) {
                 ok = false;
                 if (lane == 0) raise_status(p.status, kDevTimeout);
-                for (int f = used; f < filled; ++f) warp_wait(&bar_full[warp][f % p.stages], (f / p.stages) & 1);
             }
             float* dst = red + (buf * kMmaWarps + warp) * p.rows * CS + g;
             if (ok) {
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_red_full[buf]);
         }
-    } else {
+    } else if (!copies) {
         const int at = threadIdx.x - kMmaWarps * 32;
         for (int tile = 0; tile < n_tiles; ++tile) {
             const int buf = tile % p.bufs, turn = tile / p.bufs;
@@ -408,6 +409,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_red_empty[buf]);
+        }
+    } else {
+        uint32_t polls = 0;
+        bool ok = true;
+        while (__any_sync(0xffffffffu, ok && filled < total)) {
+            bool did = false;
+            if (ok && filled < total) {
+                if (mbar_test_wait(&bar_empty[lane][f_stage], f_phase)) {
+                    fill();
+                    did = true;
+                    polls = 0;
+                } else if (++polls > (1u << 21)) {  // that MMA warp gave up: its copies land before shared memory goes away
+                    ok = false;
+                    for (int f = max(0, filled - p.stages); f < filled; ++f)
+                        mbar_wait(&bar_full[lane][f % p.stages], (f / p.stages) & 1, 1u << 16);
+                }
+            }
+            if (!__any_sync(0xffffffffu, did)) __nanosleep(32);
         }
     }
 }
