@@ -70,12 +70,17 @@ struct QuantParams {
     int* status;
 };
 
-__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
-        "%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+// d = A B + (c0, c1, c0, c1): the first MMA of a group; then d += A B.
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1, float c0, float c1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %10, %11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mma_next(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
@@ -211,12 +216,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             continue;
         }
         const uint4* src = reinterpret_cast<const uint4*>(p.hidden + static_cast<size_t>(m0 + m) * p.H);
-        const int pieces = p.H / 8;
+        const int pieces = p.H / 8;  // a multiple of 16: a group's lanes are in range together
+        constexpr int kPer = kLmQuantMaxHidden / 8 / 32;
+        uint4 u[kPer];
         uint32_t mx = 0u;
-#pragma unroll 8
-        for (int i = lane; i < pieces; i += 32) {
-            const uint4 u = __ldg(src + i);
-            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            if (32 * k >= pieces) break;
+            u[k] = 32 * k + lane < pieces ? __ldg(src + 32 * k + lane) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            if (32 * k >= pieces) break;
+            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(u[k].x & 0x7fff7fffu, u[k].y & 0x7fff7fffu),
+                                       __vmaxu2(u[k].z & 0x7fff7fffu, u[k].w & 0x7fff7fffu)));
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -226,10 +239,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // an infinity or NaN in the row makes its logits NaN
         if (lane == 0) fac[m] = mx < 0x7f80u ? 1.0f / scale : __uint_as_float(0x7fffffffu);
         unsigned char* row = hid + m * p.hid_stride;
-#pragma unroll 8
-        for (int i = lane; i < pieces; i += 32) {  // a multiple of 16 pieces: a group's lanes are in range together
-            const uint4 u = __ldg(src + i);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            if (32 * k >= pieces) break;
+            const int i = 32 * k + lane;
+            const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
             float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = __uint_as_float((e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16));
@@ -241,10 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __half2 y = __floats2half2_rn(x[c] * f, x[c + 4] * f);
                 h[c] = *reinterpret_cast<const uint32_t*>(&y);
             }
-            *reinterpret_cast<uint4*>(row + ((i >> 4) * 16 + piece_of<GROUP>((i & 15) * 8)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-            const unsigned in = i - lane + 32 <= pieces ? 0xffffffffu : 0xffffu;
 #pragma unroll
-            for (int o = 1; o < GROUP / 8; o <<= 1) sum += __shfl_xor_sync(in, sum, o);
+            for (int o = 1; o < GROUP / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (i >= pieces) continue;
+            *reinterpret_cast<uint4*>(row + ((i >> 4) * 16 + piece_of<GROUP>((i & 15) * 8)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
             if (i % (GROUP / 8) == 0) corr[i / (GROUP / 8) * p.c_stride + m] = sum * scale * -0x1p-21f;
         }
     }
@@ -287,7 +301,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Scales sc[2 * MT];
 #pragma unroll
                 for (int i = 0; i < 2 * MT; ++i) sc[i] = next[i];
-                read_scales();
                 if (ok && !warp_wait(&bar_full[warp][st], phase)) {
                     ok = false;
                     if (lane == 0) raise_status(p.status, kDevTimeout);
@@ -319,32 +332,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();  // every lane has read the stage
                 if (lane == 0) mbar_arrive(release);
                 float acc[MT][NT][4];
+                float2 c[NT];
+                uint4 hb[2][NT];  // of step q and the next
+                auto read_hidden = [&](int q) {
+#pragma unroll
+                    for (int b = 0; b < NT; ++b) hb[q & 1][b] = lds128(h_at[b] + (slice * 16 + q * 4) * 16);
+                };
+                read_hidden(0);
+                read_scales();
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    if (q % (4 / NG) == 0) {
-                        const uint32_t c = smem_u32(corr) + ((slice * NG + q / (4 / NG)) * p.c_stride + 2 * t) * 4;
+                    const bool first = q % (4 / NG) == 0;  // of a group
+                    if (first) {
 #pragma unroll
                         for (int b = 0; b < NT; ++b) {
-                            const uint2 x = lds64(c + b * 32);
-#pragma unroll
-                            for (int a = 0; a < MT; ++a) {
-                                acc[a][b][0] = acc[a][b][2] = __uint_as_float(x.x);
-                                acc[a][b][1] = acc[a][b][3] = __uint_as_float(x.y);
-                            }
+                            const uint2 x = lds64(smem_u32(corr) + ((slice * NG + q / (4 / NG)) * p.c_stride + b * 8 + 2 * t) * 4);
+                            c[b] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
                         }
                     }
-                    uint4 hb[NT];
-#pragma unroll
-                    for (int b = 0; b < NT; ++b) hb[b] = lds128(h_at[b] + (slice * 16 + q * 4) * 16);
+                    if (q < 3) read_hidden(q + 1);
 #pragma unroll
                     for (int a = 0; a < MT; ++a) {
                         const uint32_t x = w[a][0][q], y = w[a][1][q], x8 = x >> 8, y8 = y >> 8;
                         constexpr uint32_t k0 = 0x000f000fu, k4 = 0x00f000f0u;
 #pragma unroll
                         for (int b = 0; b < NT; ++b) {
-                            mma_f16_16816(acc[a][b], x & k0, y & k0, x & k4, y & k4, hb[b].x, hb[b].y);
-                            mma_f16_16816(acc[a][b], x8 & k0, y8 & k0, x8 & k4, y8 & k4, hb[b].z, hb[b].w);
+                            const uint4& h = hb[q & 1][b];
+                            if (first) mma_first(acc[a][b], x & k0, y & k0, x & k4, y & k4, h.x, h.y, c[b].x, c[b].y);
+                            else mma_next(acc[a][b], x & k0, y & k0, x & k4, y & k4, h.x, h.y);
                         }
+#pragma unroll
+                        for (int b = 0; b < NT; ++b)
+                            mma_next(acc[a][b], x8 & k0, y8 & k0, x8 & k4, y8 & k4, hb[q & 1][b].z, hb[q & 1][b].w);
                     }
                     if (q % (4 / NG) == 4 / NG - 1) {
                         const int gi = q / (4 / NG);
