@@ -5,16 +5,19 @@
 // With c = log2(e) / T, the row's maximum M and y = (x - M) c:
 //   S = sum 2^y, E = sum y 2^y
 //   ln p[t] = (x_t - M) / T - ln S,  entropy = ln S - ln2 E / S
-// S and E are kept together in one pass, like an online softmax: when the
-// running maximum rises by d / c, S <- 2^-d S and E <- 2^-d (E - d S). The
+// M is a reference here, at most 4 / c below the row's maximum: S and E are
+// kept together in one pass, like an online softmax, and when the reference
+// rises by d / c, S <- 2^-d S and E <- 2^-d (E - d S). It rises only when
+// an entry is more than 4 / c above it, so hardly ever after a thread's first
+// group (at every new maximum some lane of a warp had one in most groups). The
 // difference is taken before the product (one packed addition more than a
 // multiply-add of the scaled maximum) so that it is exact next to logits of any
 // size. The rank counts entries above the token's logit, read before the pass.
 // Logits are clamped to -2^100 for the sums only (2^y is 0 there, and y 2^y must
 // not be -inf * 0).
 //
-// Bound by HBM: a row is read once, 16 bytes per lane and load, four loads in
-// flight per thread; about six instructions per element beside
+// Bound by HBM: a row is read once, 16 bytes per lane and load, the next four
+// loads in flight while four are worked on; about six instructions per element beside
 // the one exponential (packed fp32 pairs for the multiply-adds and sums, packed
 // bf16 for clamps, maxima and compares; the compare is skipped for groups
 // whose maximum is below the token's logit). A row is split over a cluster of
@@ -39,6 +42,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kVecs = 4;                             // 16-byte vectors of a group
 constexpr int kChunkBytes = kThreads * kVecs * 16;   // 16 KB
 constexpr int kKeys = 512;                           // candidate keys held at once
+constexpr int kGroups = 512;                         // groups read again at once
 constexpr float kFloor = -0x1p100f;  // a value of both types
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -53,8 +57,9 @@ struct Shared {
     uint64_t ctop[kMaxTopK];
     Part wpart[kWarps];
     float wmax[kWarps];
-    int nkeys;
+    int nkeys, ngroups;
     uint32_t tau;
+    uint32_t groups[kGroups];  // (chunk, thread) of the groups that reach tau
     // filled by every CTA of the cluster in the leader's copy
     uint64_t rtop[kMaxChunks * kMaxTopK];
     Part rpart[kMaxChunks];
@@ -99,7 +104,13 @@ __device__ __forceinline__ int count_above(const uint4& u, float x) {
             __hadd2(__hadd2(__hgt2(bf2(u.x), t), __hgt2(bf2(u.y), t)), __hadd2(__hgt2(bf2(u.z), t), __hgt2(bf2(u.w), t)));
         return static_cast<int>(__low2float(n) + __high2float(n));
     }
-    return (__uint_as_float(u.x) > x) + (__uint_as_float(u.y) > x) + (__uint_as_float(u.z) > x) + (__uint_as_float(u.w) > x);
+    // the signs of x - entry, two per packed instruction (of equal infinities NaN, whose sign is clear)
+    x += 0.0f;  // of -0, 0 - entry would be negative for an entry of 0
+    const uint64_t minus = f2_pack(-1.0f, -1.0f), x2 = f2_pack(x, x);
+    const uint64_t a = f2_fma((static_cast<uint64_t>(u.y) << 32) | u.x, minus, x2);
+    const uint64_t b = f2_fma((static_cast<uint64_t>(u.w) << 32) | u.z, minus, x2);
+    return static_cast<int>((__float_as_uint(f2_lo(a)) >> 31) + (__float_as_uint(f2_hi(a)) >> 31) +
+                            (__float_as_uint(f2_lo(b)) >> 31) + (__float_as_uint(f2_hi(b)) >> 31));
 }
 
 // a <- a and b over the larger maximum.
@@ -112,6 +123,24 @@ __device__ __forceinline__ void join(Part& a, const Part& b, float c) {
     a.s = fa * a.s + fb * b.s;
     a.m = M;
     a.above += b.above;
+}
+
+// The parts of 2^STEPS neighbouring lanes joined in all of them: their common reference, then plain sums.
+template <int STEPS>
+__device__ __forceinline__ void join_lanes(Part& a, float c) {
+    float M = a.m;
+#pragma unroll
+    for (int o = 1; o < 1 << STEPS; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float d = a.m == -INFINITY ? 0.0f : (a.m - M) * c, f = a.m == -INFINITY ? 0.0f : ex2_approx(d);
+    a.e = f > 0.0f ? f * fmaf(d, a.s, a.e) : f * a.s;  // a factor of 0 comes with a difference that may be infinite
+    a.s = f * a.s;
+    a.m = M;
+#pragma unroll
+    for (int o = 1; o < 1 << STEPS; o <<= 1) {
+        a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+        a.e += __shfl_xor_sync(0xffffffffu, a.e, o);
+        a.above += __shfl_xor_sync(0xffffffffu, a.above, o);
+    }
 }
 
 template <int DT>
@@ -156,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
     // x >= xt as x > xt_below, the next value down (both zeros are one value)
     const float xt_below = xt == 0.0f ? __uint_as_float(0x80000001u) : o2f(f2o(xt) - 1u);
     if (tid == 0) {
-        sm.nkeys = 0;
+        sm.nkeys = sm.ngroups = 0;
         sm.tau = 0u;
     }
     if (tid < kMaxTopK) sm.ctop[tid] = 0ull;
@@ -166,17 +195,21 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
     float top = -INFINITY;  // this thread's largest element
     const uint64_t c2 = f2_pack(c, c);
     const int tokv = tok / EPV - first / EPV;  // the token's vector in this CTA's numbering (first is a multiple of EPV)
-    const uint4* in = vec + tid;
-    for (int ch = 0; ch < nch; ++ch, in += kVecs * kThreads) {
-        uint4 u[kVecs];
-        const int v0 = ch * kVecs * kThreads + tid;
+    auto load = [&](int ch, uint4 (&u)[kVecs]) {
+        if (ch >= nch) return;
+        const uint4* in = vec + ch * kVecs * kThreads + tid;
         if ((ch + 1) * kVecs * kThreads <= nvec) {
 #pragma unroll
             for (int q = 0; q < kVecs; ++q) u[q] = __ldg(in + q * kThreads);
         } else {
+            const int v0 = ch * kVecs * kThreads + tid;
 #pragma unroll
             for (int q = 0; q < kVecs; ++q) u[q] = v0 + q * kThreads < nvec ? __ldg(in + q * kThreads) : neg_inf<DT>();
         }
+    };
+    auto group = [&](int ch, const uint4 (&u)[kVecs]) {
+        if (ch >= nch) return;
+        const int v0 = ch * kVecs * kThreads + tid;
         const float gm = fmaxf(fmaxf(vec_max<DT>(u[0]), vec_max<DT>(u[1])), fmaxf(vec_max<DT>(u[2]), vec_max<DT>(u[3])));
         const bool any = v0 < nvec;
         top = fmaxf(top, gm);
@@ -184,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
             if (DT == 1) reinterpret_cast<uint16_t*>(gmax_raw)[ch * kThreads + tid] = any ? f2o(gm) >> 16 : 0;
             else reinterpret_cast<uint32_t*>(gmax_raw)[ch * kThreads + tid] = any ? f2o(gm) : 0u;
         }
-        if (!any) continue;
+        if (!any) return;
         if (gm >= xt) {
             // vectors before the token's: larger or equal; after it: larger
 #pragma unroll
@@ -203,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
                 }
             }
         }
-        if (fmaxf(gm, kFloor) > my.m) {
+        if ((fmaxf(gm, kFloor) - my.m) * c > 4.0f) {
             const Part up{fmaxf(gm, kFloor), 0.0f, 0.0f, 0};
             join(my, up, c);
         }
@@ -244,19 +277,22 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
         if (ge != ge) sums(true);
         my.s += gs;
         my.e += ge;
+    };
+    {
+        uint4 u[kVecs], w[kVecs];
+        load(0, u);
+        for (int ch = 0; ch < nch; ch += 2) {
+            load(ch + 1, w);
+            group(ch, u);
+            load(ch + 2, u);
+            group(ch + 1, w);
+        }
     }
     // ---- this CTA's sums ----
     float wmx = top;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Part x;
-        x.m = __shfl_xor_sync(0xffffffffu, my.m, o);
-        x.s = __shfl_xor_sync(0xffffffffu, my.s, o);
-        x.e = __shfl_xor_sync(0xffffffffu, my.e, o);
-        x.above = __shfl_xor_sync(0xffffffffu, my.above, o);
-        wmx = fmaxf(wmx, __shfl_xor_sync(0xffffffffu, wmx, o));
-        join(my, x, c);
-    }
+    for (int o = 16; o > 0; o >>= 1) wmx = fmaxf(wmx, __shfl_xor_sync(0xffffffffu, wmx, o));
+    join_lanes<5>(my, c);
     if (lane == 0) {
         sm.wpart[warp] = my;
         sm.wmax[warp] = wmx;
@@ -294,28 +330,39 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
                                        : reinterpret_cast<const uint32_t*>(gmax_raw)[ch * kThreads + tid];
             return g != 0u && g >= (DT == 1 ? tau & 0xffff0000u : tau);
         };
+        // The groups are listed first and their vectors then dealt over the threads, so that
+        // all are read at once. (Each thread reading its own groups, one vector after the
+        // other, took a third of the kernel's time.)
         for (int ch = 0; ch < nch; ++ch) {
             if (!hot(ch)) continue;
-            for (int q = 0; q < kVecs; ++q) {
-                const int v = (ch * kVecs + q) * kThreads + tid;
-                if (v >= nvec) break;
+            const int at = atomicAdd(&sm.ngroups, 1);
+            if (at < kGroups) sm.groups[at] = static_cast<uint32_t>(ch * kThreads + tid);
+        }
+        __syncthreads();
+        const int ng = sm.ngroups;
+        if (ng <= kGroups) {
+            for (int i = tid; i < ng * kVecs; i += kThreads) {
+                const int at = static_cast<int>(sm.groups[i / kVecs]);
+                const int v = (at / kThreads * kVecs + i % kVecs) * kThreads + at % kThreads;
+                if (v >= nvec) continue;
                 const uint4 u = __ldg(vec + v);
 #pragma unroll
                 for (int e = 0; e < EPV; ++e) {
                     const float x = element<DT>(u, e);
                     if (x == x && f2o(x) >= tau) {
-                        const int at = atomicAdd(&sm.nkeys, 1);
-                        if (at < kKeys) sm.keys[at] = make_key(x, static_cast<uint32_t>(first + v * EPV + e));
+                        const int key = atomicAdd(&sm.nkeys, 1);
+                        if (key < kKeys) sm.keys[key] = make_key(x, static_cast<uint32_t>(first + v * EPV + e));
                     }
                 }
             }
         }
         __syncthreads();
-        const int nk = sm.nkeys;
+        const int nk = ng <= kGroups ? sm.nkeys : kKeys + 1;
         if (nk <= kKeys) {
             for (int i = tid; i < nk; i += kThreads) {
                 const unsigned long long key = sm.keys[i];
                 int r = 0;
+#pragma unroll 4
                 for (int o = 0; o < nk; ++o) r += sm.keys[o] > key;
                 if (r < k) sm.ctop[r] = key;
             }
@@ -353,15 +400,17 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
     cg::cluster_group cluster = cg::this_cluster();
     Shared* lead = cpr > 1 ? cluster.map_shared_rank(&sm, 0) : &sm;
     if (tid < kMaxTopK) lead->rtop[rank * kMaxTopK + tid] = sm.ctop[tid];
-    if (tid == 0) {
-        Part p = sm.wpart[0];
-        float m = sm.wmax[0];
-        for (int i = 1; i < kWarps; ++i) {
-            join(p, sm.wpart[i], c);
-            m = fmaxf(m, sm.wmax[i]);
+    if (warp == 0) {
+        static_assert(kWarps == 8, "three steps");
+        Part p = sm.wpart[lane & 7];
+        float m = sm.wmax[lane & 7];
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        join_lanes<3>(p, c);
+        if (lane == 0) {
+            lead->rpart[rank] = p;
+            lead->rmax[rank] = m;
         }
-        lead->rpart[rank] = p;
-        lead->rmax[rank] = m;
     }
     if (cpr > 1) {
         cluster.sync();
@@ -396,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
         __syncthreads();
         if (lane == 0) sm.wpart[warp] = Part{0.0f, s, e, 0};
         __syncthreads();
+        p.m = m;
         p.s = p.e = 0.0f;
         for (int i = 0; i < kWarps; ++i) {
             p.s += sm.wpart[i].s;
@@ -403,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
         }
     }
     const float ln2 = 0.693147180559945309417f, lns = logf(p.s);
-    auto ln_p = [&](float x) -> float { return (x - m) / a.temperature - lns; };
+    auto ln_p = [&](float x) -> float { return (x - p.m) / a.temperature - lns; };
     const bool bad = !(p.s > 0.0f) || !isfinite(p.s) || m == -INFINITY;
     if (tid == 0) {
         if (bad) raise_status(a.status, kDevNonFinite);
@@ -413,9 +463,11 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
     }
     if (tid < cpr * kMaxTopK && k > 0) {
         const uint64_t key = sm.rtop[tid];
-        int r = 0;
-        if (key != 0ull)
+        int r = tid;  // a single CTA's are in order
+        if (cpr > 1 && key != 0ull) {
+            r = 0;
             for (int i = 0; i < cpr * kMaxTopK; ++i) r += sm.rtop[i] > key;
+        }
         if (key != 0ull && r < k) {
             a.alt_ids[static_cast<size_t>(entry) * k + r] = static_cast<int32_t>(key_id(key));
             a.alt_logprobs[static_cast<size_t>(entry) * k + r] = bad ? NAN : ln_p(key_val(key));
