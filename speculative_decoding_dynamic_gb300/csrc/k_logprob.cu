@@ -144,7 +144,7 @@ __device__ __forceinline__ void join_lanes(Part& a, float c) {
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs a, int cpr, int seg, float c) {
+__global__ void __launch_bounds__(kThreads, DT == 1 ? 4 : 6) token_logprobs_kernel(LogprobArgs a, int cpr, int seg, float c) {
     extern __shared__ __align__(16) unsigned char gmax_raw[];  // [chunk][thread] group maxima (ordered bits)
     __shared__ Shared sm;
     constexpr int ES = DT == 1 ? 2 : 4;
@@ -279,13 +279,10 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogprobArgs
         my.e += ge;
     };
     {
-        uint4 u[kVecs], w[kVecs];
-        load(0, u);
-        for (int ch = 0; ch < nch; ch += 2) {
-            load(ch + 1, w);
+        for (int ch = 0; ch < nch; ++ch) {
+            uint4 u[kVecs];
+            load(ch, u);
             group(ch, u);
-            load(ch + 2, u);
-            group(ch + 1, w);
         }
     }
     // ---- this CTA's sums ----
