@@ -412,9 +412,12 @@ size_t eagle_kvq_attention_workspace_bytes(const eagle_kvq_cfg* kv, int T);
 /*
  * Stage 5 over the 8-bit cache: eagle_tree_attention's definition with K and V
  * the values code * scale. Sums, row maxima and the softmax are fp32; K takes
- * part exactly and q within 2^-18 of its row's largest element; the softmax
- * weights are rounded to fp16 (relative 2^-11) for the product with V. Output
- * bf16, rounded to nearest even.
+ * part exactly and q within 2^-17 of its row's largest element; the softmax
+ * weights are rounded to fp16 (relative 2^-11, and 2^-25 of the row's largest
+ * weight) for the product with V. V's scales enter relative to the largest of
+ * the tiles so far (a smaller one counts as 2^-24 of it at least). Output bf16,
+ * rounded to nearest even. A NaN among the codes or in q makes the rows that
+ * see it zero or NaN.
  *   q, out   [B, T, Hq, 128] bf16, contiguous, 16-byte aligned; T = 1..256.
  *   mask     [B, T, W] as eagle_build_tree writes it, or NULL: slot i sees the
  *            slots 0..i (a chain; with T = 1 the plain decode step).
@@ -447,7 +450,9 @@ int eagle_kvq_compact(const eagle_kvq_cfg* kv, void* codes, float* scales, const
  * eagle_lmhead with 4-bit weights [notes EAGLE 方法: the draft model reuses the
  * target model's LM head, which every draft step reads whole].
  *   group    32, 64 or 128: entries of a weight row that share a scale.
- *   hidden   [B*k, H] bf16 in, H a multiple of 128.
+ *   hidden   [B*k, H] bf16 in, H a multiple of 128 up to 8192. Elements below
+ *            2^-28 of their row's largest are rounded to 2^-36 of it; a row
+ *            with an infinity or NaN gives NaN logits.
  *   codes    [V, H/2] in: byte i of a row holds entry 2i in its low and entry
  *            2i + 1 in its high four bits, code c = 0..15.
  *   scales   [V, H/group] bf16 in: weight[v, h] = (c - 8) * scales[v, h / group].

@@ -2,8 +2,11 @@
 
 Allocation of the caller-owned workspaces and outputs, then the sequence
 tree_init -> expand x D -> rerank -> build_tree -> tree_attention -> verify ->
-kv_compact. Every step runs in libeagle's kernels; this module only holds
-buffers and passes pointers.
+kv_compact. With a KvqCfg the cache is the 8-bit one (the tree's K and V are
+stored, attended to and compacted in it), a head given as (codes, scales, group)
+is the 4-bit one, and with n_alt the accepted tokens come with their
+log-probabilities. Every step runs in libeagle's kernels; this module only
+holds buffers and passes pointers.
 """
 from __future__ import annotations
 
@@ -17,16 +20,22 @@ def torch_dtype(code: int) -> torch.dtype:
 
 
 class DeviceCycle:
-    """Buffers for one cycle of a (TreeCfg, KvCfg) problem on one device."""
+    """Buffers for one cycle of a (TreeCfg, KvCfg or KvqCfg) problem on one device.
 
-    def __init__(self, cfg: E.TreeCfg, kv: E.KvCfg, device="cuda", fused_head: bool = False):
+    n_alt: None, or how many alternatives `logprobs` reports per accepted token (0..16)."""
+
+    def __init__(self, cfg: E.TreeCfg, kv: E.KvCfg | E.KvqCfg, device="cuda", fused_head: bool = False,
+                 n_alt: int | None = None):
         self.cfg, self.kv = cfg, kv
         self.fused_head = fused_head
+        self.quant_kv = isinstance(kv, E.KvqCfg)
+        self.n_alt = n_alt
         dev = torch.device(device)
         B, D, k, T, W = cfg.batch, cfg.depth, cfg.top_k, cfg.T, cfg.W
         i32 = dict(dtype=torch.int32, device=dev)
         self.ws = E.alloc_workspace(E.eagle_workspace_bytes(cfg), dev)
-        self.attn_ws = E.alloc_workspace(E.eagle_attention_workspace_bytes(kv, T), dev)
+        attn_bytes = E.eagle_kvq_attention_workspace_bytes if self.quant_kv else E.eagle_attention_workspace_bytes
+        self.attn_ws = E.alloc_workspace(attn_bytes(kv, T), dev)
         self.row_lse = torch.empty(B, D, k, dtype=torch.float32, device=dev)
         self.ftok = torch.empty(B, k, **i32)
         self.fcount = torch.empty(B, **i32)
@@ -46,6 +55,13 @@ class DeviceCycle:
             self.lm_lse = torch.empty(B * k, dtype=torch.float32, device=dev)
             self.lm_ids = torch.empty(B * k, k, **i32)
             self.lm_vals = torch.empty(B * k, k, dtype=torch.float32, device=dev)
+        if n_alt is not None:
+            f32 = dict(dtype=torch.float32, device=dev)
+            self.logprob = torch.empty(B, D + 1, **f32)
+            self.rank = torch.empty(B, D + 1, **i32)
+            self.entropy = torch.empty(B, D + 1, **f32)
+            self.alt_ids = torch.empty(B, D + 1, n_alt, **i32)
+            self.alt_logprobs = torch.empty(B, D + 1, n_alt, **f32)
 
     # ---- stages -----------------------------------------------------------
     def draft(self, draft_logits: torch.Tensor, stream=None, steps=None, lse_in=None, head=None):
@@ -54,8 +70,11 @@ class DeviceCycle:
         head: optional (weight [V, H], hidden [D, B*k, H]), both bf16: each
         step's rows are then first written into draft_logits[s] by the LM head,
         or, with fused_head, reduced to their lse and top-k in the LM head's
-        epilogue and expanded from those (draft_logits unused)."""
+        epilogue and expanded from those (draft_logits unused). A weight given
+        as (codes, scales, group) is the 4-bit head of eagle_lmhead_quant."""
         cfg = self.cfg
+        if self.fused_head and head is not None and isinstance(head[0], tuple):
+            raise ValueError("DeviceCycle.draft: the 4-bit head has no form with stage 1 in its epilogue (fused_head)")
         E.eagle_tree_init(cfg, self.ws, stream)
         for s in range(cfg.depth if steps is None else steps):
             if head is not None and self.fused_head:
@@ -66,7 +85,12 @@ class DeviceCycle:
                 continue
             if head is not None:
                 weight, hidden = head
-                E.eagle_lmhead(cfg, self.ws, hidden.shape[-1], hidden[s], weight, draft_logits[s], stream)
+                if isinstance(weight, tuple):
+                    codes, scales, group = weight
+                    E.eagle_lmhead_quant(cfg, self.ws, hidden.shape[-1], group, hidden[s], codes, scales,
+                                         draft_logits[s], stream)
+                else:
+                    E.eagle_lmhead(cfg, self.ws, hidden.shape[-1], hidden[s], weight, draft_logits[s], stream)
             E.eagle_expand(cfg, self.ws, s, draft_logits[s], None if lse_in is None else lse_in[s], self.row_lse,
                            self.ftok, self.fcount, stream)
         if steps is None:
@@ -81,7 +105,20 @@ class DeviceCycle:
         E.eagle_build_tree(self.cfg, self.ws, prefix_len, root_token, self.tokens, self.parent, self.depth, self.pos,
                            self.mask, self.n_tree, stream)
 
+    def store(self, k, v, cache, layer, prefix_len, stream=None):
+        """The tree's K and V of a layer into the 8-bit cache: k, v [B, T, Hkv, 128] bf16, tree slot j
+        of a sequence at position prefix_len + j (slots past n_tree are not written)."""
+        kv = self.kv
+        E.eagle_kvq_store(kv, layer, self.cfg.T, k, v, kv.n_kv_heads * kv.head_dim, None, prefix_len, self.n_tree,
+                          *cache, ws=self.ws, stream=stream)
+
     def attention(self, q, cache, layer, prefix_len, stream=None):
+        """cache: the 16-bit cache's tensor, or the 8-bit cache's (codes, scales)."""
+        if self.quant_kv:
+            codes, scales = cache
+            E.eagle_kvq_tree_attention(self.kv, self.cfg.T, q, codes, scales, layer, prefix_len, self.mask,
+                                       self.n_tree, self.attn_out, self.attn_ws, stream)
+            return
         E.eagle_tree_attention(self.kv, self.cfg.T, q, cache, layer, prefix_len, self.mask, self.n_tree,
                                self.attn_out, self.attn_ws, stream)
 
@@ -90,17 +127,34 @@ class DeviceCycle:
         E.eagle_verify(self.cfg, self.ws, mode, temperature, seed, cycle, target, self.tokens, self.parent,
                        self.n_tree, self.accept_len, self.slots, self.out_tokens, stream=stream)
 
+    def logprobs(self, target, temperature=1.0, stream=None):
+        """Log-probability, rank, entropy and n_alt alternatives of the accepted tokens and the bonus (after verify)."""
+        cfg = self.cfg
+        E.eagle_token_logprobs(cfg, self.ws, cfg.batch, cfg.depth + 1, cfg.T, target, temperature, self.slots,
+                               self.out_tokens, self.n_alt, self.logprob, self.rank, self.entropy,
+                               self.alt_ids if self.n_alt else None, self.alt_logprobs if self.n_alt else None, stream)
+
     def compact(self, cache, prefix_len, stream=None):
+        if self.quant_kv:
+            codes, scales = cache
+            E.eagle_kvq_compact(self.kv, codes, scales, prefix_len, self.accept_len, self.slots, self.cfg.depth + 1,
+                                self.new_len, self.ws, stream)
+            return
         E.eagle_kv_compact(self.kv, cache, prefix_len, self.accept_len, self.slots, self.cfg.depth + 1, self.new_len,
                            self.ws, stream)
 
     def run(self, draft_logits, prefix_len, root_token, q, cache, layer, target, seed, cycle, mode, temperature=1.0,
-            compact=True, stream=None, head=None):
-        """The whole cycle (all stages) enqueued on `stream`."""
+            compact=True, stream=None, head=None, new_kv=None):
+        """The whole cycle (all stages) enqueued on `stream`. new_kv: optional (k, v) of the tree's
+        slots, stored in the 8-bit cache first."""
         self.draft(draft_logits, stream, head=head)
         self.build(prefix_len, root_token, stream)
+        if new_kv is not None:
+            self.store(*new_kv, cache, layer, prefix_len, stream)
         self.attention(q, cache, layer, prefix_len, stream)
         self.verify(mode, temperature, target, seed, cycle, stream)
+        if self.n_alt is not None:
+            self.logprobs(target, temperature, stream)
         if compact:
             self.compact(cache, prefix_len, stream)
 
