@@ -50,7 +50,7 @@ constexpr int kTileQ = kBM * kHD;        // 16 KB: one e4m3 part of a row block'
 constexpr int kTile8 = kBN * kHD;        // 8 KB: a K or V tile of codes
 constexpr int kTileV = kBN * kHD * 2;    // 16 KB: V as fp16, two halves of 64 columns
 constexpr int kHalfV = kTileV / 2;
-constexpr int kKStages = 3;              // K tiles in flight (V tiles: 2)
+constexpr int kKStages = 4, kVStages = 3;  // tiles of codes in flight
 constexpr int kScaleSlots = 8;
 // Sixteen warps: 0 copies and scales; 1, 2 QK^T of block 0, 1; 3, 4 PV of block 0, 1;
 // 5..7 converters; 8..11 and 12..15 softmax of block 0 and 1.
@@ -60,7 +60,7 @@ constexpr int kThreads = 32 * (kWarpSoftmax + kSoftmaxWarps);
 constexpr int kSmemQ = 0;  // [item parity][row block][hi, lo]
 constexpr int kSmemK = 8 * kTileQ;
 constexpr int kSmemV8 = kSmemK + kKStages * kTile8;
-constexpr int kSmemV = kSmemV8 + 2 * kTile8;        // [tile parity]
+constexpr int kSmemV = kSmemV8 + kVStages * kTile8;  // [tile parity]
 constexpr int kSmem = kSmemV + 2 * kTileV + 1024;   // and alignment slack
 constexpr int kTmemCols = 512;  // S of row block g, buffer b at 64 (2g + b) (P over it), O of block g at 256 + 128 g
 
@@ -68,6 +68,9 @@ constexpr int kTmemCols = 512;  // S of row block g, buffer b at 64 (2g + b) (P 
 __host__ __device__ constexpr uint32_t idesc_type0(int M, int N, int b_mn_major) {
     return (1u << 4) | (static_cast<uint32_t>(b_mn_major) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
            (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
 // An MMA warp runs as one: every lane computes the same descriptors (in
 // uniform registers) and one elected lane issues, by a predicate inside the
@@ -152,26 +155,35 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low 
 // brings its largest element into [128, 256); the softmax's factor log2(e) /
 // (s sqrt(128)). From [B][T][Hq][128] to [B][Hkv][hi, lo][G*T][128] and
 // [B][Hkv][G*T]. Sixteen lanes take a row, two rows each (both loads first).
-// Moves 4 bytes per element; at 8B b64, 31 MB each way.
-// (In the attention kernel, by its converters behind their tiles, it held up
-// each item by 11,000 cycles: the fence behind a converted tile waits for the
-// loads of q in flight.)
-constexpr int kSplitThreads = 256, kSplitRows = 2 * kSplitThreads / 16;
+// Moves 4 bytes per element; at 8B b64, 31 MB each way. (In the attention
+// kernel, by its converters behind their tiles, it held up each item by
+// 11,000 cycles: the fence behind a converted tile waits for the loads of q
+// in flight.) The first CTAs find where the attention's workers start.
+constexpr int kSplitThreads = 256, kSplitPer = 2, kSplitRows = kSplitPer * kSplitThreads / 16;
 __global__ void __launch_bounds__(kSplitThreads)
     kvq_split_q_kernel(const __nv_bfloat16* __restrict__ q, uint2* __restrict__ dst, float* __restrict__ fac, KvqRows rows,
-                       int Hkv, int64_t n, float scale_log2) {
+                       int Hkv, int64_t n, float scale_log2, KvqSched sched, KvqCursor* __restrict__ cursors) {
     pdl_wait_prior();
     pdl_launch_dependents();
+    constexpr int kStarts = kSplitThreads / 32;
+    const int starts = (sched.workers + kStarts - 1) / kStarts;
+    if (static_cast<int>(blockIdx.x) < starts) {
+        const int w = blockIdx.x * kStarts + (threadIdx.x >> 5);
+        KvqCursor c;
+        c.init(sched, w);
+        if (w < sched.workers && (threadIdx.x & 31) == 0) cursors[w] = c;
+        return;
+    }
     const int l16 = threadIdx.x & 15;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSplitRows + (threadIdx.x >> 4);
-    uint4 u[2];
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x - starts) * kSplitRows + (threadIdx.x >> 4);
+    uint4 u[kSplitPer];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int64_t i = i0 + e * (kSplitRows / 2);
+    for (int e = 0; e < kSplitPer; ++e) {
+        const int64_t i = i0 + e * (kSplitThreads / 16);
         u[e] = i < n ? __ldg(reinterpret_cast<const uint4*>(q + i * kHD) + l16) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < kSplitPer; ++e) {
         uint32_t mx = __vmaxu2(__vmaxu2(u[e].x & 0x7fff7fffu, u[e].y & 0x7fff7fffu),
                                __vmaxu2(u[e].z & 0x7fff7fffu, u[e].w & 0x7fff7fffu));
 #pragma unroll
@@ -188,12 +200,11 @@ __global__ void __launch_bounds__(kSplitThreads)
             const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h));
             lo[c] = e4m3x2(x - b.x, y - b.y);
         }
-        const int64_t i = i0 + e * (kSplitRows / 2);
+        const int64_t i = i0 + e * (kSplitThreads / 16);
         if (i >= n) continue;
-        const int64_t bt = i / rows.Hq;
-        const int h = static_cast<int>(i - bt * rows.Hq), hk = h / rows.G;
-        const int64_t b = bt / rows.T;
-        const int64_t bk = b * Hkv + hk, r = (bt - b * rows.T) * rows.G + (h - hk * rows.G), RT = static_cast<int64_t>(rows.G) * rows.T;
+        const int64_t bt = kvq_div(i, rows.Hq), b = kvq_div(bt, rows.T);
+        const int h = static_cast<int>(i - bt * rows.Hq), t = static_cast<int>(bt - b * rows.T), hk = h / rows.G;
+        const int64_t bk = b * Hkv + hk, r = t * rows.G + (h - hk * rows.G), RT = rows.G * rows.T;
         dst[(2 * bk * RT + r) * 16 + l16] = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
         dst[((2 * bk + 1) * RT + r) * 16 + l16] = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
         if (l16 == 0) fac[bk * RT + r] = scale_log2 / s;
@@ -216,8 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t bar_q_full[2], bar_q_empty[2], bar_k_full[kKStages], bar_k_empty[kKStages], bar_v8_full[2],
-        bar_v8_empty[2], bar_v_full[2], bar_v_empty[2], bar_sc[kScaleSlots], bar_s_full[2][2],
+    __shared__ uint64_t bar_q_full[2], bar_q_empty[2], bar_k_full[kKStages], bar_k_empty[kKStages], bar_v8_full[kVStages],
+        bar_v8_empty[kVStages], bar_v_full[2], bar_v_empty[2], bar_sc[kScaleSlots], bar_s_full[2][2],
         bar_p_full[2][2], bar_pv_done[2][2];
     __shared__ uint32_t tmem_holder;
     __shared__ TileScales ts[kScaleSlots];
@@ -228,8 +239,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bar_q_full[s], 1);
             mbar_init(&bar_q_empty[s], 2);
-            mbar_init(&bar_v8_full[s], 1);
-            mbar_init(&bar_v8_empty[s], kConvWarps);
             mbar_init(&bar_v_full[s], kConvWarps);
             mbar_init(&bar_v_empty[s], 2);
             for (int b = 0; b < 2; ++b) {
@@ -242,8 +251,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar_k_full[s], 1);
             mbar_init(&bar_k_empty[s], 2);
         }
+        for (int s = 0; s < kVStages; ++s) {
+            mbar_init(&bar_v8_full[s], 1);
+            mbar_init(&bar_v8_empty[s], kConvWarps);
+        }
         for (int s = 0; s < kScaleSlots; ++s) mbar_init(&bar_sc[s], 1);
         fence_mbar_init();
+    }
+    if (threadIdx.x == 32 * kWarpConv) {  // the maps are parameters: no need to wait for the kernels before
+        prefetch_map(&tm_q);
+        prefetch_map(&tm_k);
+        prefetch_map(&tm_v);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_holder)),
@@ -254,7 +272,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait_prior();
     pdl_launch_dependents();
     KvqCursor cur;
-    cur.init(p.s, worker);
+    {
+        static_assert(sizeof(KvqCursor) % 16 == 0, "whole 16-byte pieces");
+        const int4* src = reinterpret_cast<const int4*>(p.cursors + worker);
+        int4* dst = reinterpret_cast<int4*>(&cur);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(KvqCursor) / 16); ++i) dst[i] = __ldcg(src + i);
+    }
     KvqPiece it;
     Waiter wait;
     const int rows = p.G * p.s.T, n_blocks = (rows + kBM - 1) / kBM;
@@ -266,15 +290,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // --------------------------------------------- copies and scales ---
         // Step t: once the K stage of tile t is free (both blocks' QK^T of tile
-        // t - 3 done), give the softmax the scales of tile t - 1, read a step ago; then
+        // t - 4 done), give the softmax the scales of tile t - 1, read a step ago; then
         // copy K of tile t, and V once its stage is free. The slot of the scales, tile
-        // t - 9's, is free: the copy of V(t - 1) waited for the conversion of V(t - 3),
-        // that for both blocks' PV of tile t - 5. (Not a converter's work: the fence
+        // t - 9's, is free: the copy of V(t - 1) waited for the conversion of V(t - 4),
+        // that for both blocks' PV of tile t - 6. (Not a converter's work: the fence
         // behind each of its tiles would wait for the scales in flight; nor a QK
         // warp's: it was late for its next tile.) The next item's q is asked for once
-        // this item's fourth tile starts: the last item's QK^T are done by then.
+        // this item's fifth tile starts: the last item's QK^T are done by then.
         // Lanes 0..3 hold K's scales of a tile's 16-key groups, 4..7 V's.
-        int t = 0, qi = 0, sk = 0, pk = 0;  // K stage of tile t and its phase
+        int t = 0, qi = 0, sk = 0, pk = 0, sv = 0, pv = 0;  // stages of tile t and their phases
         float last_scale = 0.0f, sref = 0.0f, inv_sref = 0.0f;
         auto copy_q = [&](const KvqPiece& a, int i) {  // q of the i-th item
             if (i >= 2) wait(&bar_q_empty[i & 1], (i >> 1) - 1);
@@ -320,7 +344,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float* src = (lane < kSub ? p.k_scale : p.v_scale) + it.b * p.s_seq + hk;
             const int last = (it.nkeys - 1) >> p.blk_shift;
             for (int j = it.t0; j < it.t1; ++j, ++t) {
-                const int b = t & 1;
                 float own = 0.0f;
                 if (lane < 2 * kSub) own = __ldg(src + min((j * kBN + 16 * (lane & 3)) >> p.blk_shift, last) * p.s_blk);
                 if (t >= kKStages) wait(&bar_k_empty[sk], pk ^ 1);
@@ -336,23 +359,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sk = 0;
                     pk ^= 1;
                 }
-                if (t >= 2) wait(&bar_v8_empty[b], (t >> 1) - 1);
+                if (t >= kVStages) wait(&bar_v8_empty[sv], pv ^ 1);
                 if (lane == 0 && wait.ok) {
-                    mbar_arrive_expect_tx(&bar_v8_full[b], kTile8);
-                    tma_load_4d(smem + kSmemV8 + b * kTile8, &tm_v, 0, hk, j * kBN, it.b, &bar_v8_full[b]);
+                    mbar_arrive_expect_tx(&bar_v8_full[sv], kTile8);
+                    tma_load_4d(smem + kSmemV8 + sv * kTile8, &tm_v, 0, hk, j * kBN, it.b, &bar_v8_full[sv]);
                 }
                 __syncwarp();
-                if (more && j == min(it.t0 + 3, it.t1 - 1)) copy_q(ahead, qi + 1);
+                if (++sv == kVStages) {
+                    sv = 0;
+                    pv ^= 1;
+                }
+                if (more && j == min(it.t0 + 4, it.t1 - 1)) copy_q(ahead, qi + 1);
             }
         }
         if (t > 0) give(t - 1);
         if (!wait.ok) {  // the copies in flight land before the CTA's shared memory goes away
             if (lane == 0) raise_status(p.status, kDevTimeout);
             for (int s = 0; s < 2; ++s)
-                for (int ph = 0; ph < 2; ++ph) {
-                    mbar_wait(&bar_q_full[s], ph, 1u << 16);
-                    mbar_wait(&bar_v8_full[s], ph, 1u << 16);
-                }
+                for (int ph = 0; ph < 2; ++ph) mbar_wait(&bar_q_full[s], ph, 1u << 16);
+            for (int s = 0; s < kVStages; ++s)
+                for (int ph = 0; ph < 2; ++ph) mbar_wait(&bar_v8_full[s], ph, 1u << 16);
             for (int s = 0; s < kKStages; ++s)
                 for (int ph = 0; ph < 2; ++ph) mbar_wait(&bar_k_full[s], ph, 1u << 16);
         }
@@ -453,17 +479,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ----------------------------------------------------- converters ---
         const int cw = warp - kWarpConv;
         const uint32_t base = smem_u32(smem);
-        int t = 0;
+        int t = 0, st = 0, ph = 0;  // the stage of codes and its phase
         while (cur.next(p.s, it))
             for (int j = it.t0; j < it.t1; ++j, ++t) {
                 const int b = t & 1;
-                if (t >= 2) wait.both(&bar_v_empty[b], (t >> 1) - 1, &bar_v8_full[b], t >> 1);
-                else wait(&bar_v8_full[b], t >> 1);
+                if (t >= 2) wait.both(&bar_v_empty[b], (t >> 1) - 1, &bar_v8_full[st], ph);
+                else wait(&bar_v8_full[st], ph);
 #pragma unroll
                 for (int e = 0; e < 6; ++e) {  // chunks cw, cw + 3, cw + 6 of 16 columns, two keys each
                     const int key = lane + 32 * (e & 1), c16 = cw + kConvWarps * (e >> 1);
                     if (c16 >= 8) break;
-                    uint4 u = lds128(base + kSmemV8 + b * kTile8 + key * kHD + ((c16 ^ (key & 7)) << 4));
+                    uint4 u = lds128(base + kSmemV8 + st * kTile8 + key * kHD + ((c16 ^ (key & 7)) << 4));
                     // keys that no row can see may hold anything (even NaN): 0 * V has to stay 0
                     if (j * kBN + key >= it.nkeys) u = make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t dst = base + kSmemV + b * kTileV + (c16 >> 2) * kHalfV + key * 128;
@@ -476,8 +502,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();  // the MMA reads V through the async proxy
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&bar_v8_empty[b]);
+                    mbar_arrive(&bar_v8_empty[st]);
                     mbar_arrive(&bar_v_full[b]);
+                }
+                if (++st == kVStages) {
+                    st = 0;
+                    ph ^= 1;
                 }
             }
         if (!wait.ok) raise_status(p.status, kDevTimeout);
@@ -648,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // whole: neighbouring lanes store 32 bytes of one row together (full sectors)
             const int64_t other = static_cast<int64_t>(shfl_xor_u64(static_cast<uint64_t>(row), 1));
             const bool odd = lane & 1;
-            const int64_t row_a = odd ? other : row, row_b = odd ? row : other;  // the even lane's row, the odd one's
+            const int64_t row_e = odd ? other : row, row_o = odd ? row : other;  // the even lane's row, the odd one's
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 float o[32];
@@ -670,8 +700,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         got.z = __shfl_xor_sync(0xffffffffu, give.z, 1);
                         got.w = __shfl_xor_sync(0xffffffffu, give.w, 1);
                         const int col = 32 * c + 16 * h + (odd ? 8 : 0);
-                        if (row_a >= 0) *reinterpret_cast<uint4*>(p.out + row_a * kHD + col) = odd ? got : x;
-                        if (row_b >= 0) *reinterpret_cast<uint4*>(p.out + row_b * kHD + col) = odd ? y : got;
+                        if (row_e >= 0) *reinterpret_cast<uint4*>(p.out + row_e * kHD + col) = odd ? got : x;
+                        if (row_o >= 0) *reinterpret_cast<uint4*>(p.out + row_o * kHD + col) = odd ? y : got;
                     }
                 } else if (row_live) {
 #pragma unroll
@@ -739,7 +769,7 @@ struct Plan {
     KvqSched s;
     int G, n_items, rows;
     bool decode;
-    size_t off_cut, off_ml, off_o, off_q, off_fac, bytes;
+    size_t off_cut, off_cur, off_ml, off_o, off_q, off_fac, bytes;
 };
 
 // Up to 16 query rows per KV head: the decode kernel, a worker per warp;
@@ -761,7 +791,8 @@ Plan make_plan(const KvqDims& kv, int T) {
     }
     const size_t slots = 2 * static_cast<size_t>(pl.s.workers) * pl.rows;
     pl.off_cut = 256;
-    pl.off_ml = align_up(pl.off_cut + pl.s.workers * sizeof(int4), 256);
+    pl.off_cur = align_up(pl.off_cut + pl.s.workers * sizeof(int4), 256);
+    pl.off_ml = align_up(pl.off_cur + (pl.decode ? 0 : pl.s.workers * sizeof(KvqCursor)), 256);
     pl.off_o = align_up(pl.off_ml + slots * 2 * sizeof(float), 256);
     pl.off_q = align_up(pl.off_o + slots * kHD * sizeof(float), 256);
     const size_t q_rows = pl.decode ? 0 : static_cast<size_t>(kv.B) * kv.Hkv * rows;
@@ -787,6 +818,7 @@ cudaError_t launch_kvq_attention(const KvqDims& kv, int T, const void* q, const 
                          reinterpret_cast<int4*>(w + pl.off_cut), pl.rows};
     p.rows = KvqRows{pl.G, T, kv.Hq};
     p.q_fac = reinterpret_cast<const float*>(w + pl.off_fac);
+    p.cursors = reinterpret_cast<const KvqCursor*>(w + pl.off_cur);
     p.Hq = kv.Hq;
     p.Hkv = kv.Hkv;
     p.G = pl.G;
@@ -826,9 +858,9 @@ cudaError_t launch_kvq_attention(const KvqDims& kv, int T, const void* q, const 
     cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kvq_attn_kernel), kSmem);
     if (e != cudaSuccess) return e;
     const int64_t q_rows = static_cast<int64_t>(kv.B) * T * kv.Hq;
-    e = launch_pdl(kvq_split_q_kernel, dim3(static_cast<unsigned>((q_rows + kSplitRows - 1) / kSplitRows)), dim3(kSplitThreads), 0,
+    e = launch_pdl(kvq_split_q_kernel, dim3(static_cast<unsigned>((q_rows + kSplitRows - 1) / kSplitRows + (pl.s.workers + kSplitThreads / 32 - 1) / (kSplitThreads / 32))), dim3(kSplitThreads), 0,
                    stream, p.q, reinterpret_cast<uint2*>(w + pl.off_q), reinterpret_cast<float*>(w + pl.off_fac), p.rows,
-                   kv.Hkv, q_rows, p.scale_log2);
+                   kv.Hkv, q_rows, p.scale_log2, p.s, reinterpret_cast<KvqCursor*>(w + pl.off_cur));
     if (e != cudaSuccess) return e;
     e = launch_pdl(kvq_attn_kernel, dim3(pl.s.workers), dim3(kThreads), kSmem, stream, tq, tk, tv, p);
     if (e != cudaSuccess) return e;

@@ -117,10 +117,10 @@ struct KvqPiece {
 };
 
 // A worker's pieces in order. init by a whole warp; next by any thread.
-struct KvqCursor {
+struct alignas(16) KvqCursor {
     long long pos, end, base, chunk;
-    int b, worker;
     KvqSeq q;
+    int b, worker, pad;
     __device__ __forceinline__ void init(const KvqSched& s, int w) {
         const KvqLens lens(s);
         const long long total = lens.total;
@@ -267,7 +267,8 @@ struct KvqAttnParams {
     KvqSched s;
     KvqPartials part;
     KvqRows rows;
-    const float* q_fac;  // tensor-core kernel: factors of the rows of q
+    const float* q_fac;         // tensor-core kernel: factors of the rows of q,
+    const KvqCursor* cursors;  // and where its workers start
     int Hq, Hkv, G, W;
     int n_items;    // items of a KV head (pairs of row blocks; 1 in the decode kernel)
     int blk_shift;  // log2 of the positions of a scale block
