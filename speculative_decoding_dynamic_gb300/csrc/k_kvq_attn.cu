@@ -787,7 +787,7 @@ Plan make_plan(const KvqDims& kv, int T) {
     } else {
         pl.n_items = (rows + 2 * kBM - 1) / (2 * kBM);
         pl.rows = 2 * kBM;
-        pl.s = KvqSched{nullptr, nullptr, kv.B, T, kv.max_len, kv.Hkv * pl.n_items, kBN, 4, kKvqSms, 6};
+        pl.s = KvqSched{nullptr, nullptr, kv.B, T, kv.max_len, kv.Hkv * pl.n_items, kBN, 6, kKvqSms, 8};
     }
     const size_t slots = 2 * static_cast<size_t>(pl.s.workers) * pl.rows;
     pl.off_cut = 256;

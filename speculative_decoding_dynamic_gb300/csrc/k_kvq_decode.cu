@@ -11,8 +11,8 @@
 //     accumulator in registers. No barrier between warps.
 //   - the products run transposed, S^T = K q^T and O^T = V^T P^T, on mma.sync
 //     m16n8k16 with the cache as the 16-row operand: eight query rows are one
-//     n-tile (with q as the 16-row operand half of the products of a group of
-//     four heads would be empty rows: 42 against .. us, see below). tcgen05's
+//     n-tile (with q as the 16-row operand twelve of its rows would be empty
+//     for a group of four heads). tcgen05's
 //     128-row tile would need the operands as fp16 in shared memory, twice
 //     their bytes written and read again.
 //   - codes go from shared memory to fp16 fragments by one conversion per two
@@ -396,13 +396,13 @@ __device__ __forceinline__ void merge_store(const KvqMergeParams& p, const int4&
 // The cut item that worker w began: O = sum_i 2^(m_i - M) O_i over
 // sum_i 2^(m_i - M) l_i of its pieces i (worker w's in slot 2w + 1, w + i's in
 // slot 2 (w + i)). A CTA serves the items that eight neighbouring workers
-// began: those of up to four pieces go to one warp each, those of many (few
-// long sequences) are shared by all eight warps, row by row.
+// began, one row of them (blockIdx.y): those of up to four pieces go to one
+// warp each, those of many (few long sequences) are shared by all eight warps.
 __global__ void __launch_bounds__(kMergeWarps * 32) kvq_merge_decode_kernel(KvqMergeParams p) {
     __shared__ float4 so[kMergeWarps][32];
     __shared__ float2 sml[kMergeWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int w0 = blockIdx.x * kMergeWarps;
+    const int w0 = blockIdx.x * kMergeWarps, r = blockIdx.y;
     pdl_wait_prior();
     pdl_launch_dependents();
     const int4* items = p.part.cut + w0;
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kvq_merge_decode_kernel(KvqM
     };
     const int4 own = __ldcg(items + min(warp, n_here - 1));
     if (warp < n_here && own.x > 0 && own.x <= kMergeAlone)
-        for (int r = 0; r < p.part.rows; ++r) {
+        {
             RowSum<1> s;
             float2 a[kMergeAlone];
             float4 x[kMergeAlone][1];
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kvq_merge_decode_kernel(KvqM
     for (int e = 0; e < n_here; ++e) {
         const int4 c = __ldcg(items + e);
         if (c.x <= kMergeAlone) continue;  // uniform over the CTA
-        for (int r = 0; r < p.part.rows; ++r) {
+        {
             RowSum<1> s;
 #pragma unroll 4
             for (int i = warp; i < c.x; i += kMergeWarps) {
@@ -460,8 +460,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kvq_merge_decode_kernel(KvqM
 }  // namespace
 
 cudaError_t launch_kvq_merge_decode(const KvqMergeParams& p, cudaStream_t stream) {
-    return launch_pdl(kvq_merge_decode_kernel, dim3((p.workers + kMergeWarps - 1) / kMergeWarps), dim3(kMergeWarps * 32), 0,
-                      stream, p);
+    return launch_pdl(kvq_merge_decode_kernel, dim3((p.workers + kMergeWarps - 1) / kMergeWarps, p.part.rows), dim3(kMergeWarps * 32),
+                      0, stream, p);
 }
 
 KvqSched kvq_decode_sched(int B, int T, int max_len, int Hkv, int rows) {
