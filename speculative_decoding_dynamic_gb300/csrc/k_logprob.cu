@@ -93,24 +93,38 @@ __device__ __forceinline__ uint4 neg_inf() {
     return make_uint4(w, w, w, w);
 }
 
-// Entries of a vector above x.
-template <int DT>
-__device__ __forceinline__ int count_above(const uint4& u, float x) {
+// Entries of N vectors above x.
+template <int DT, int N>
+__device__ __forceinline__ int count_above(const uint4* u, float x) {
     if (DT == 1) {
         // x is a bf16 value, or the fp32 value below one: rounding it down to bf16 keeps the order of bf16 entries
         const __nv_bfloat16 h = __float2bfloat16_rd(x);
         const __nv_bfloat162 t = __halves2bfloat162(h, h);
-        const __nv_bfloat162 n =
-            __hadd2(__hadd2(__hgt2(bf2(u.x), t), __hgt2(bf2(u.y), t)), __hadd2(__hgt2(bf2(u.z), t), __hgt2(bf2(u.w), t)));
-        return static_cast<int>(__low2float(n) + __high2float(n));
+        __nv_bfloat162 n[2];  // at most 8 N a half: exact
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+            const __nv_bfloat162 a = __hadd2(__hgt2(bf2(u[q].x), t), __hgt2(bf2(u[q].y), t));
+            const __nv_bfloat162 b = __hadd2(__hgt2(bf2(u[q].z), t), __hgt2(bf2(u[q].w), t));
+            n[0] = q ? __hadd2(n[0], a) : a;
+            n[1] = q ? __hadd2(n[1], b) : b;
+        }
+        const __nv_bfloat162 all = __hadd2(n[0], n[1]);
+        return static_cast<int>(__low2float(all) + __high2float(all));
     }
     // the signs of x - entry, two per packed instruction (of equal infinities NaN, whose sign is clear)
     x += 0.0f;  // of -0, 0 - entry would be negative for an entry of 0
     const uint64_t minus = f2_pack(-1.0f, -1.0f), x2 = f2_pack(x, x);
-    const uint64_t a = f2_fma((static_cast<uint64_t>(u.y) << 32) | u.x, minus, x2);
-    const uint64_t b = f2_fma((static_cast<uint64_t>(u.w) << 32) | u.z, minus, x2);
-    return static_cast<int>((__float_as_uint(f2_lo(a)) >> 31) + (__float_as_uint(f2_hi(a)) >> 31) +
-                            (__float_as_uint(f2_lo(b)) >> 31) + (__float_as_uint(f2_hi(b)) >> 31));
+    uint32_t n = 0u;
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+        const uint64_t a = f2_fma((static_cast<uint64_t>(u[q].y) << 32) | u[q].x, minus, x2);
+        const uint64_t b = f2_fma((static_cast<uint64_t>(u[q].w) << 32) | u[q].z, minus, x2);
+        n += __float_as_uint(f2_lo(a)) >> 31;
+        n += __float_as_uint(f2_hi(a)) >> 31;
+        n += __float_as_uint(f2_lo(b)) >> 31;
+        n += __float_as_uint(f2_hi(b)) >> 31;
+    }
+    return static_cast<int>(n);
 }
 
 // a <- a and b over the larger maximum.
@@ -218,8 +232,10 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 4 : 6) token_logprobs_kern
             else reinterpret_cast<uint32_t*>(gmax_raw)[ch * kThreads + tid] = any ? f2o(gm) : 0u;
         }
         if (!any) return;
-        if (gm >= xt) {
-            // vectors before the token's: larger or equal; after it: larger
+        if (gm >= xt && xt > -INFINITY && (v0 > tokv || v0 + (kVecs - 1) * kThreads < tokv)) {
+            // vectors before the token's: larger or equal; after it: larger (the filling of a short group never is)
+            my.above += count_above<DT, kVecs>(u, v0 > tokv ? xt : xt_below);
+        } else if (gm >= xt) {
 #pragma unroll
             for (int q = 0; q < kVecs; ++q) {
                 const int v = v0 + q * kThreads;
@@ -232,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 4 : 6) token_logprobs_kern
                     }
                 } else {
                     // nothing is below -inf: every entry before such a token is above it
-                    my.above += v < tokv && xt == -INFINITY ? EPV : count_above<DT>(u[q], v < tokv ? xt_below : xt);
+                    my.above += v < tokv && xt == -INFINITY ? EPV : count_above<DT, 1>(u + q, v < tokv ? xt_below : xt);
                 }
             }
         }
