@@ -21,7 +21,7 @@
 //   O += P V         tcgen05.mma kind::f16, A = P from tensor memory, B = V as
 //                    fp16 in shared memory (MN-major), converted from the
 //                    tile's codes (exact, one conversion per two elements) by
-//                    three warps of their own, once for both row blocks. P in
+//                    two warps of their own, once for both row blocks. P in
 //                    e4m3 would spare that, at 2^-4 per weight instead of 2^-11.
 // The reference maximum (scale) is raised, and O and the row sum rescaled in
 // place, only when a tile's exceeds it by more than 2^8 (2^4), so the weights
@@ -52,10 +52,11 @@ constexpr int kTileV = kBN * kHD * 2;    // 16 KB: V as fp16, two halves of 64 c
 constexpr int kHalfV = kTileV / 2;
 constexpr int kKStages = 4, kVStages = 3;  // tiles of codes in flight
 constexpr int kScaleSlots = 8;
-// Sixteen warps: 0 copies and scales; 1, 2 QK^T of block 0, 1; 3, 4 PV of block 0, 1;
-// 5..7 converters; 8..11 and 12..15 softmax of block 0 and 1.
-constexpr int kWarpMma = 1, kWarpConv = 5, kWarpSoftmax = 8;
-constexpr int kConvWarps = 3, kSoftmaxWarps = 8;
+// Sixteen warps: 0 copies; 1, 2 QK^T of block 0, 1; 3, 4 PV of block 0, 1; 5, 6 converters; 7 scales;
+// 8..11 and 12..15 softmax of block 0 and 1. (The scales as the copying warp's work made it the
+// slowest of all: 1750 cycles a tile.)
+constexpr int kWarpMma = 1, kWarpConv = 5, kWarpScale = 7, kWarpSoftmax = 8;
+constexpr int kConvWarps = 2, kSoftmaxWarps = 8;
 constexpr int kThreads = 32 * (kWarpSoftmax + kSoftmaxWarps);
 constexpr int kSmemQ = 0;  // [item parity][row block][hi, lo]
 constexpr int kSmemK = 8 * kTileQ;
@@ -102,6 +103,23 @@ __device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
         "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
         " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)),
         "r"(lead)
+        : "memory");
+}
+// One lane's copy, issued like an MMA by the whole warp.
+__device__ __forceinline__ void expect_tx(uint32_t lead, uint64_t* bar, uint32_t bytes) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
+        " @q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(smem_u32(bar)),
+        "r"(bytes), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void copy_4d(uint32_t lead, uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                        uint64_t* bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %7, 0;\n"
+        " @q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];\n}" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)), "r"(lead)
         : "memory");
 }
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
@@ -228,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t bar_q_full[2], bar_q_empty[2], bar_k_full[kKStages], bar_k_empty[kKStages], bar_v8_full[kVStages],
-        bar_v8_empty[kVStages], bar_v_full[2], bar_v_empty[2], bar_sc[kScaleSlots], bar_s_full[2][2],
+        bar_v8_empty[kVStages], bar_v_full[2], bar_v_empty[2], bar_sc[kScaleSlots], bar_go[kScaleSlots], bar_s_full[2][2],
         bar_p_full[2][2], bar_pv_done[2][2];
     __shared__ uint32_t tmem_holder;
     __shared__ TileScales ts[kScaleSlots];
@@ -255,7 +273,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar_v8_full[s], 1);
             mbar_init(&bar_v8_empty[s], kConvWarps);
         }
-        for (int s = 0; s < kScaleSlots; ++s) mbar_init(&bar_sc[s], 1);
+        for (int s = 0; s < kScaleSlots; ++s) {
+            mbar_init(&bar_sc[s], 1);
+            mbar_init(&bar_go[s], 1);
+        }
         fence_mbar_init();
     }
     if (threadIdx.x == 32 * kWarpConv) {  // the maps are parameters: no need to wait for the kernels before
@@ -288,91 +309,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = tmem_holder;
 
     if (warp == 0) {
-        // --------------------------------------------- copies and scales ---
-        // Step t: once the K stage of tile t is free (both blocks' QK^T of tile
-        // t - 4 done), give the softmax the scales of tile t - 1, read a step ago; then
-        // copy K of tile t, and V once its stage is free. The slot of the scales, tile
-        // t - 9's, is free: the copy of V(t - 1) waited for the conversion of V(t - 4),
-        // that for both blocks' PV of tile t - 6. (Not a converter's work: the fence
-        // behind each of its tiles would wait for the scales in flight; nor a QK
-        // warp's: it was late for its next tile.) The next item's q is asked for once
-        // this item's fifth tile starts: the last item's QK^T are done by then.
-        // Lanes 0..3 hold K's scales of a tile's 16-key groups, 4..7 V's.
+        // -------------------------------------------------------- copies ---
+        // Step t: once the stages of tile t are free (both blocks' QK^T of tile t - 4
+        // done, V of tile t - 3 converted), say that the slot of the scales of tile
+        // t - 1 is free, and copy K and V of tile t. (The slot held tile t - 9's: V(t - 4)
+        // was converted after both blocks' PV of tile t - 6.) The next item's q is
+        // asked for once this item's fifth tile starts: the last item's QK^T are done by then.
+        const uint32_t lead = elect_one(), base = smem_u32(smem);
         int t = 0, qi = 0, sk = 0, pk = 0, sv = 0, pv = 0;  // stages of tile t and their phases
-        float last_scale = 0.0f, sref = 0.0f, inv_sref = 0.0f;
         auto copy_q = [&](const KvqPiece& a, int i) {  // q of the i-th item
             if (i >= 2) wait(&bar_q_empty[i & 1], (i >> 1) - 1);
-            if (lane == 0 && wait.ok) {
-                const int hk = a.sub / p.n_items, block = (a.sub - hk * p.n_items) * 2;
-                const int n = min(2, n_blocks - block);
-                mbar_arrive_expect_tx(&bar_q_full[i & 1], n * 2 * kTileQ);
+            if (wait.ok) {
+                const int hk = uniform(a.sub / p.n_items), block = uniform((a.sub - hk * p.n_items) * 2);
+                const int n = min(2, n_blocks - block), w = uniform(a.b) * p.Hkv + hk;
+                expect_tx(lead, &bar_q_full[i & 1], n * 2 * kTileQ);
                 for (int h = 0; h < 2 * n; ++h)  // (row block, part); rows past the last are zeros
-                    tma_load_4d(smem + kSmemQ + ((i & 1) * 4 + h) * kTileQ, &tm_q, 0, (block + (h >> 1)) * kBM, h & 1,
-                                a.b * p.Hkv + hk, &bar_q_full[i & 1]);
+                    copy_4d(lead, base + kSmemQ + ((i & 1) * 4 + h) * kTileQ, &tm_q, 0, (block + (h >> 1)) * kBM, h & 1, w,
+                            &bar_q_full[i & 1]);
             }
-            __syncwarp();
-        };
-        auto give = [&](int tile) {
-            // V's reference scale: the piece's first tile's largest, raised by more than 2^4 only
-            float vm = lane >= kSub && lane < 2 * kSub ? last_scale : 0.0f;
-            vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
-            vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
-            vm = __shfl_sync(0xffffffffu, vm, kSub);
-            float alpha = 1.0f;
-            if (vm > 16.0f * sref) {
-                if (sref > 0.0f) alpha = sref / vm;
-                sref = vm;
-                inv_sref = 1.0f / vm;
-            }
-            const float ratio = fmaxf(last_scale * inv_sref, 0x1p-24f);
-            TileScales& o = ts[tile & (kScaleSlots - 1)];
-            if (lane < 2 * kSub) (&o.k[0])[lane] = lane < kSub ? last_scale : __log2f(ratio);  // k, then lv
-            if (lane >= kSub && lane < 2 * kSub) o.iv[lane - kSub] = __frcp_rn(ratio);
-            if (lane == 0) o.alpha = alpha;
-            if (lane == 1) o.sref = sref;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_sc[tile & (kScaleSlots - 1)]);
-            __syncwarp();
         };
         KvqPiece ahead;
         bool more = cur.next(p.s, ahead);
         if (more) copy_q(ahead, 0);
-        for (; more; ++qi) {
+        for (; uniform(more); ++qi) {
             it = ahead;
             more = cur.next(p.s, ahead);
-            const int hk = it.sub / p.n_items;
-            const float* src = (lane < kSub ? p.k_scale : p.v_scale) + it.b * p.s_seq + hk;
-            const int last = (it.nkeys - 1) >> p.blk_shift;
-            for (int j = it.t0; j < it.t1; ++j, ++t) {
-                float own = 0.0f;
-                if (lane < 2 * kSub) own = __ldg(src + min((j * kBN + 16 * (lane & 3)) >> p.blk_shift, last) * p.s_blk);
-                if (t >= kKStages) wait(&bar_k_empty[sk], pk ^ 1);
-                if (t > 0) give(t - 1);
-                if (j == it.t0) sref = 0.0f;  // the tile just given was the last piece's
-                last_scale = own;
-                if (lane == 0 && wait.ok) {
-                    mbar_arrive_expect_tx(&bar_k_full[sk], kTile8);
-                    tma_load_4d(smem + kSmemK + sk * kTile8, &tm_k, 0, hk, j * kBN, it.b, &bar_k_full[sk]);
-                }
+            const int hk = uniform(it.sub / p.n_items), b = uniform(it.b), j1 = uniform(it.t1), j0 = uniform(it.t0);
+            for (int j = j0; j < j1; ++j, ++t) {
+                if (t >= kKStages) wait.both(&bar_k_empty[sk], pk ^ 1, &bar_v8_empty[sv], pv ^ 1);
+                else if (t >= kVStages) wait(&bar_v8_empty[sv], pv ^ 1);
+                if (t > 0 && lane == 0) mbar_arrive(&bar_go[(t - 1) & (kScaleSlots - 1)]);
                 __syncwarp();
+                if (wait.ok) {
+                    expect_tx(lead, &bar_k_full[sk], kTile8);
+                    copy_4d(lead, base + kSmemK + sk * kTile8, &tm_k, 0, hk, j * kBN, b, &bar_k_full[sk]);
+                    expect_tx(lead, &bar_v8_full[sv], kTile8);
+                    copy_4d(lead, base + kSmemV8 + sv * kTile8, &tm_v, 0, hk, j * kBN, b, &bar_v8_full[sv]);
+                }
                 if (++sk == kKStages) {
                     sk = 0;
                     pk ^= 1;
                 }
-                if (t >= kVStages) wait(&bar_v8_empty[sv], pv ^ 1);
-                if (lane == 0 && wait.ok) {
-                    mbar_arrive_expect_tx(&bar_v8_full[sv], kTile8);
-                    tma_load_4d(smem + kSmemV8 + sv * kTile8, &tm_v, 0, hk, j * kBN, it.b, &bar_v8_full[sv]);
-                }
-                __syncwarp();
                 if (++sv == kVStages) {
                     sv = 0;
                     pv ^= 1;
                 }
-                if (more && j == min(it.t0 + 4, it.t1 - 1)) copy_q(ahead, qi + 1);
+                if (more && j == min(j0 + 4, j1 - 1)) copy_q(ahead, qi + 1);
             }
         }
-        if (t > 0) give(t - 1);
+        if (t > 0 && lane == 0) mbar_arrive(&bar_go[(t - 1) & (kScaleSlots - 1)]);
+        __syncwarp();
         if (!wait.ok) {  // the copies in flight land before the CTA's shared memory goes away
             if (lane == 0) raise_status(p.status, kDevTimeout);
             for (int s = 0; s < 2; ++s)
@@ -475,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t > 0) wait(&bar_v_empty[(t - 1) & 1], (t - 1) >> 1);
         }
         if (!wait.ok) raise_status(p.status, kDevTimeout);
-    } else if (warp < kWarpSoftmax) {
+    } else if (warp < kWarpScale) {
         // ----------------------------------------------------- converters ---
         const int cw = warp - kWarpConv;
         const uint32_t base = smem_u32(smem);
@@ -485,19 +471,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int b = t & 1;
                 if (t >= 2) wait.both(&bar_v_empty[b], (t >> 1) - 1, &bar_v8_full[st], ph);
                 else wait(&bar_v8_full[st], ph);
+                uint4 u[8];  // chunks cw, cw + 2, .. of 16 columns, two keys each
 #pragma unroll
-                for (int e = 0; e < 6; ++e) {  // chunks cw, cw + 3, cw + 6 of 16 columns, two keys each
+                for (int e = 0; e < 8; ++e) {
                     const int key = lane + 32 * (e & 1), c16 = cw + kConvWarps * (e >> 1);
-                    if (c16 >= 8) break;
-                    uint4 u = lds128(base + kSmemV8 + st * kTile8 + key * kHD + ((c16 ^ (key & 7)) << 4));
+                    u[e] = lds128(base + kSmemV8 + st * kTile8 + key * kHD + ((c16 ^ (key & 7)) << 4));
                     // keys that no row can see may hold anything (even NaN): 0 * V has to stay 0
-                    if (j * kBN + key >= it.nkeys) u = make_uint4(0u, 0u, 0u, 0u);
+                    if (j * kBN + key >= it.nkeys) u[e] = make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int key = lane + 32 * (e & 1), c16 = cw + kConvWarps * (e >> 1);
                     const uint32_t dst = base + kSmemV + b * kTileV + (c16 >> 2) * kHalfV + key * 128;
                     const int c = 2 * (c16 & 3);
-                    sts128(dst + ((c ^ (key & 7)) << 4),
-                           make_uint4(e4m3_to_f16x2(u.x), e4m3_to_f16x2(u.x >> 16), e4m3_to_f16x2(u.y), e4m3_to_f16x2(u.y >> 16)));
-                    sts128(dst + (((c + 1) ^ (key & 7)) << 4),
-                           make_uint4(e4m3_to_f16x2(u.z), e4m3_to_f16x2(u.z >> 16), e4m3_to_f16x2(u.w), e4m3_to_f16x2(u.w >> 16)));
+                    sts128(dst + ((c ^ (key & 7)) << 4), make_uint4(e4m3_to_f16x2(u[e].x), e4m3_to_f16x2(u[e].x >> 16),
+                                                                    e4m3_to_f16x2(u[e].y), e4m3_to_f16x2(u[e].y >> 16)));
+                    sts128(dst + (((c + 1) ^ (key & 7)) << 4), make_uint4(e4m3_to_f16x2(u[e].z), e4m3_to_f16x2(u[e].z >> 16),
+                                                                          e4m3_to_f16x2(u[e].w), e4m3_to_f16x2(u[e].w >> 16)));
                 }
                 fence_proxy_async_smem();  // the MMA reads V through the async proxy
                 __syncwarp();
@@ -511,6 +501,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         if (!wait.ok) raise_status(p.status, kDevTimeout);
+    } else if (warp == kWarpScale) {
+        // -------------------------------------------------------- scales ---
+        // The softmax's scales of a tile, read a tile ahead (the fence behind a
+        // converter's tile would wait for them; a QK warp was late for its next tile).
+        // Lanes 0..3 hold K's scales of a tile's 16-key groups, 4..7 V's.
+        int t = 0;
+        float last_scale = 0.0f, sref = 0.0f, inv_sref = 0.0f;
+        auto give = [&](int tile) {
+            // V's reference scale: the piece's first tile's largest, raised by more than 2^4 only
+            float vm = lane >= kSub && lane < 2 * kSub ? last_scale : 0.0f;
+            vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+            vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+            vm = __shfl_sync(0xffffffffu, vm, kSub);
+            float alpha = 1.0f;
+            if (vm > 16.0f * sref) {
+                if (sref > 0.0f) alpha = sref / vm;
+                sref = vm;
+                inv_sref = 1.0f / vm;
+            }
+            const float ratio = fmaxf(last_scale * inv_sref, 0x1p-24f);
+            const float lv = __log2f(ratio), iv = __frcp_rn(ratio);
+            const int slot = tile & (kScaleSlots - 1);
+            wait(&bar_go[slot], tile / kScaleSlots);
+            TileScales& o = ts[slot];
+            if (lane < 2 * kSub) (&o.k[0])[lane] = lane < kSub ? last_scale : lv;  // k, then lv
+            if (lane >= kSub && lane < 2 * kSub) o.iv[lane - kSub] = iv;
+            if (lane == 0) o.alpha = alpha;
+            if (lane == 1) o.sref = sref;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_sc[slot]);
+            __syncwarp();
+        };
+        while (cur.next(p.s, it)) {
+            const int hk = it.sub / p.n_items;
+            const float* src = (lane < kSub ? p.k_scale : p.v_scale) + it.b * p.s_seq + hk;
+            const int last = (it.nkeys - 1) >> p.blk_shift;
+            for (int j = it.t0; j < it.t1; ++j, ++t) {
+                float own = 0.0f;
+                if (lane < 2 * kSub) own = __ldg(src + min((j * kBN + 16 * (lane & 3)) >> p.blk_shift, last) * p.s_blk);
+                if (t > 0) give(t - 1);
+                if (j == it.t0) sref = 0.0f;  // the tile just given was the last piece's
+                last_scale = own;
+            }
+        }
+        if (t > 0) give(t - 1);
+        if (!wait.ok && lane == 0) raise_status(p.status, kDevTimeout);
     } else {
         // ------------------------------------------------------ softmax ---
         // Four warps per row block; warp w serves TMEM lane quarter w % 4, one
