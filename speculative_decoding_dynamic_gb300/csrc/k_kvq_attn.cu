@@ -31,9 +31,17 @@
 // arrive by TMA (128-byte swizzle) in rings of their own; mbarriers order
 // everything and every wait is bounded.
 //
-// Bound by the tensor pipe where all overlaps: 2 x 64 x 128 x 128 multiply-adds
-// per tile and row block, about 630 cycles at the measured bf16 rate, against
-// 256 for the exponentials and about 300 of issue.
+// Bound by the tensor pipe: per tile and row block eight QK^T MMAs of 48
+// cycles (N = 64 is bound by reading the operands from shared memory) and four
+// PV MMAs of 64, so 1280 cycles for both blocks of a tile, of 1590 measured
+// (8 sequences of 32K, 70B heads: 613 us, the pipe 72% busy; 64 sequences
+// of 8B: 121 us; one: 23.5 us). What was tried against it: QK^T over 128 keys
+// at once (N = 128, two thirds of the cycles) leaves no second buffer of S, and
+// waits for PV (857 us); S freed as soon as it is read, with P beside it, puts
+// the copy's, QK^T's and softmax's latencies in one chain (678 us); half a row
+// per softmax thread (24 warps of 80 registers, 730 against 701 us then);
+// exponentials as polynomials on the FMA pipe (753 us); the weights against
+// the last tile's maximum while this tile's is found (733 against 690 us).
 
 #include "kvq_sched.cuh"
 
@@ -121,6 +129,11 @@ __device__ __forceinline__ void copy_4d(uint32_t lead, uint32_t dst, const CUten
         "[%6];\n}" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)), "r"(lead)
         : "memory");
+}
+__device__ __forceinline__ void arrive(uint32_t lead, uint64_t* bar) {
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(smem_u32(bar)),
+                 "r"(lead)
+                 : "memory");
 }
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
@@ -556,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = (q4 << 5) | lane;   // row of the block = TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
         const uint32_t o_cols = tmem + 256 + 128 * g + lane_off;
+        const uint32_t lead = elect_one();
         int t = 0, tg = 0;
         int4 cut = make_int4(0, 0, 0, 0);
         kvq_zero_bad(p.s, p.Hq, p.out, p.status, worker, threadIdx.x - kWarpSoftmax * 32, kSoftmaxWarps * 32);
@@ -698,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar_p_full[g][tg & 1]);
+                arrive(lead, &bar_p_full[g][tg & 1]);
             }
             // ----------------------------------------------------- epilogue ---
             wait(&bar_pv_done[g][(tg - 1) & 1], (tg - 1) >> 1);
