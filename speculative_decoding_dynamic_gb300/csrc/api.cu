@@ -10,6 +10,7 @@
 
 #include "../../include/eagle.h"
 #include "eagle_ws.h"
+#include "quant_ws.h"
 
 namespace eagle {
 

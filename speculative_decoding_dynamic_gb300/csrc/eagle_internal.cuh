@@ -178,23 +178,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// 2^(e) for the power of two that brings a row's largest |q| into [2^to, 2^(to+1)): exponent field of the scale
-__device__ __forceinline__ float pow2_to(float amax, int to) {
-    const int e = static_cast<int>(__float_as_uint(amax) >> 23);  // biased; 0 for zero and subnormals
-    const int f = to + 254 - e;                                   // biased exponent of the scale
-    return __uint_as_float(static_cast<uint32_t>(max(1, min(f, 253))) << 23);
-}
-
-// One look at an mbarrier phase, without waiting.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 // Bounded wait on an mbarrier phase. Returns false after ~max_iter polls
 // (each poll may suspend the thread for a hardware-chosen time).
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t max_iter = (1u << 21)) {
@@ -243,18 +226,6 @@ __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
 __device__ __forceinline__ void prefetch_l2_segment(const char* src, int bytes) {
     bytes = min(bytes, 2 * 16384);
     for (int off = 0; off < bytes; off += 16384) prefetch_l2(src + off, static_cast<uint32_t>(min(16384, bytes - off)));
-}
-
-// 16 bytes from / to shared memory by its 32-bit address (a pointer into
-// dynamic shared memory that was aligned by hand is a generic one to the
-// compiler, and generic loads are tracked like global ones).
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // Global loads that bypass L1 (data written by other CTAs of the same launch).

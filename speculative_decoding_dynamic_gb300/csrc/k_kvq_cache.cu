@@ -15,7 +15,7 @@
 #include <algorithm>
 
 #include "eagle_internal.cuh"
-#include "eagle_ws.h"
+#include "quant_ws.h"
 
 namespace eagle {
 namespace {

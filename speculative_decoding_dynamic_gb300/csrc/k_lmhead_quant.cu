@@ -43,7 +43,8 @@
 
 #include "attn_common.cuh"
 #include "eagle_internal.cuh"
-#include "eagle_ws.h"
+#include "quant_ptx.cuh"
+#include "quant_ws.h"
 #include "tc_ptx.cuh"
 
 namespace eagle {

@@ -32,7 +32,7 @@
 #include <cmath>
 
 #include "eagle_internal.cuh"
-#include "eagle_ws.h"
+#include "quant_ws.h"
 
 namespace eagle {
 namespace {
