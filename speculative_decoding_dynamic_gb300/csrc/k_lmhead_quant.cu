@@ -27,12 +27,19 @@
 //     128 entries) and the hidden rows are laid out in shared memory in that
 //     order once per CTA.
 // One persistent CTA per SM takes an equal, contiguous range of the
-// vocabulary in tiles of 64 rows; its eight MMA warps split the hidden
+// vocabulary in tiles of 64 or 32 rows; its eight MMA warps split the hidden
 // dimension (warp w: the 128-wide slices w, w + 8, ...), so that each works
 // alone, streaming its slices of one tile after the other through its own
 // ring of TMA tiles (filled by a warp for all eight rings: a copy's issue takes
-// 400 cycles); three more warps add the eight partial sums of a finished tile
-// and write the logits while the next tile streams.
+// 400 cycles) and reading a slice's codes while the one before is multiplied;
+// three more warps add the eight partial sums of a finished tile and write the
+// logits while the next tile streams.
+//
+// Measured: 8 rows, H = 8192, V = 128256 (525 MB of codes): 107 us, 4.9 TB/s;
+// 10 rows, H = 4096 (263 MB): 77 us, 3.4 TB/s. Bound by latency with two MMA
+// warps per scheduler (their 168 registers allow no third beside the others):
+// ten rows are two n-tiles of which the tensor pipe alone takes 28 us (8 cycles
+// an MMA). Sixteen MMA warps of 96 registers: 119 and 128 us. More stages: no change.
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -290,94 +297,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         read_scales();
-        for (int tile = 0; tile < n_tiles; ++tile) {
-            const int v = v0 + tile * RT;
-            const int mts = min(MT, (v1 - v) / 16);
-            float sum[MT][NT][4];
+        // codes of the warp's next slice, from its ring
+        using Codes = uint32_t[MT][2][4];
+        int left = warp < p.n_slice ? (p.n_slice - warp + kMmaWarps - 1) / kMmaWarps * n_tiles : 0;  // slices not read yet
+        auto read_codes = [&](Codes& w) {
+            if (left == 0 || !ok) return;
+            --left;
+            if (!warp_wait(&bar_full[warp][st], phase)) {
+                ok = false;
+                if (lane == 0) raise_status(p.status, kDevTimeout);
+                return;
+            }
+            const uint32_t src = smem_u32(ring) + st * kStage;
+#pragma unroll
+            for (int a = 0; a < MT; ++a)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t row = src + (a * 16 + g + 8 * e) * kSliceBytes;
+                    if (GROUP == 128) {
+                        const uint4 x = lds128(row + t * 16);
+                        w[a][e][0] = x.x, w[a][e][1] = x.y, w[a][e][2] = x.z, w[a][e][3] = x.w;
+                    } else if (GROUP == 64) {
+                        const uint2 x = lds64(row + t * 8), y = lds64(row + 32 + t * 8);
+                        w[a][e][0] = x.x, w[a][e][1] = x.y, w[a][e][2] = y.x, w[a][e][3] = y.y;
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) w[a][e][q] = lds32(row + q * 16 + t * 4);
+                    }
+                }
+            __syncwarp();  // every lane has read the stage
+            if (lane == 0) mbar_arrive(&bar_empty[warp][st]);
+            if (++st == p.stages) {
+                st = 0;
+                phase ^= 1;
+            }
+        };
+        float sum[MT][NT][4];
+        auto clear = [&]() {
 #pragma unroll
             for (int a = 0; a < MT; ++a)
 #pragma unroll
                 for (int b = 0; b < NT; ++b) sum[a][b][0] = sum[a][b][1] = sum[a][b][2] = sum[a][b][3] = 0.0f;
-            for (int slice = warp; slice < p.n_slice; slice += kMmaWarps) {
-                Scales sc[2 * MT];
-#pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) sc[i] = next[i];
-                if (ok && !warp_wait(&bar_full[warp][st], phase)) {
-                    ok = false;
-                    if (lane == 0) raise_status(p.status, kDevTimeout);
-                }
-                const uint32_t src = smem_u32(ring) + st * kStage;
-                uint64_t* release = &bar_empty[warp][st];
-                if (++st == p.stages) {
-                    st = 0;
-                    phase ^= 1;
-                }
-                if (!ok) continue;
-                uint32_t w[MT][2][4];
-#pragma unroll
-                for (int a = 0; a < MT; ++a)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t row = src + (a * 16 + g + 8 * e) * kSliceBytes;
-                        if (GROUP == 128) {
-                            const uint4 x = lds128(row + t * 16);
-                            w[a][e][0] = x.x, w[a][e][1] = x.y, w[a][e][2] = x.z, w[a][e][3] = x.w;
-                        } else if (GROUP == 64) {
-                            const uint2 x = lds64(row + t * 8), y = lds64(row + 32 + t * 8);
-                            w[a][e][0] = x.x, w[a][e][1] = x.y, w[a][e][2] = y.x, w[a][e][3] = y.y;
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) w[a][e][q] = lds32(row + q * 16 + t * 4);
-                        }
-                    }
-                __syncwarp();  // every lane has read the stage
-                if (lane == 0) mbar_arrive(release);
-                float acc[MT][NT][4];
-                float2 c[NT];
-                uint4 hb[2][NT];  // of step q and the next
-                auto read_hidden = [&](int q) {
-#pragma unroll
-                    for (int b = 0; b < NT; ++b) hb[q & 1][b] = lds128(h_at[b] + (slice * 16 + q * 4) * 16);
-                };
-                read_hidden(0);
-                read_scales();
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const bool first = q % (4 / NG) == 0;  // of a group
-                    if (first) {
-#pragma unroll
-                        for (int b = 0; b < NT; ++b) {
-                            const uint2 x = lds64(smem_u32(corr) + ((slice * NG + q / (4 / NG)) * p.c_stride + b * 8 + 2 * t) * 4);
-                            c[b] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
-                        }
-                    }
-                    if (q < 3) read_hidden(q + 1);
-#pragma unroll
-                    for (int a = 0; a < MT; ++a) {
-                        const uint32_t x = w[a][0][q], y = w[a][1][q], x8 = x >> 8, y8 = y >> 8;
-                        constexpr uint32_t k0 = 0x000f000fu, k4 = 0x00f000f0u;
-#pragma unroll
-                        for (int b = 0; b < NT; ++b) {
-                            const uint4& h = hb[q & 1][b];
-                            if (first) mma_first(acc[a][b], x & k0, y & k0, x & k4, y & k4, h.x, h.y, c[b].x, c[b].y);
-                            else mma_next(acc[a][b], x & k0, y & k0, x & k4, y & k4, h.x, h.y);
-                        }
-#pragma unroll
-                        for (int b = 0; b < NT; ++b)
-                            mma_next(acc[a][b], x8 & k0, y8 & k0, x8 & k4, y8 & k4, hb[q & 1][b].z, hb[q & 1][b].w);
-                    }
-                    if (q % (4 / NG) == 4 / NG - 1) {
-                        const int gi = q / (4 / NG);
-#pragma unroll
-                        for (int a = 0; a < MT; ++a)
-#pragma unroll
-                            for (int b = 0; b < NT; ++b)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) sum[a][b][e] = fmaf(acc[a][b][e], scale_of<NG>(sc[2 * a + (e >> 1)], gi), sum[a][b][e]);
-                    }
-                }
-            }
-            // the tile's partial sums to the adding warps
+        };
+        // a tile's partial sums to the adding warps
+        auto hand_over = [&](int tile) {
             const int buf = tile % p.bufs, turn = tile / p.bufs;
             if (ok && turn > 0 && !warp_wait(&bar_red_empty[buf], (turn - 1) & 1)) {
                 ok = false;
@@ -399,6 +362,79 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_red_full[buf]);
+        };
+        // a slice's products with the codes w; the next slice's go into `ahead` meanwhile
+        auto slice_of = [&](int slice, const Codes& w, Codes& ahead) {
+            Scales sc[2 * MT];
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) sc[i] = next[i];
+            float acc[MT][NT][4];
+            float2 c[NT];
+            uint4 hb[2][NT];  // of step q and the next
+            auto read_hidden = [&](int q) {
+#pragma unroll
+                for (int b = 0; b < NT; ++b) hb[q & 1][b] = lds128(h_at[b] + (slice * 16 + q * 4) * 16);
+            };
+            read_hidden(0);
+            read_scales();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const bool first = q % (4 / NG) == 0;  // of a group
+                if (first) {
+#pragma unroll
+                    for (int b = 0; b < NT; ++b) {
+                        const uint2 x = lds64(smem_u32(corr) + ((slice * NG + q / (4 / NG)) * p.c_stride + b * 8 + 2 * t) * 4);
+                        c[b] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
+                    }
+                }
+                if (q < 3) read_hidden(q + 1);
+                if (q == 2) read_codes(ahead);
+#pragma unroll
+                for (int a = 0; a < MT; ++a) {
+                    const uint32_t x = w[a][0][q], y = w[a][1][q], x8 = x >> 8, y8 = y >> 8;
+                    constexpr uint32_t k0 = 0x000f000fu, k4 = 0x00f000f0u;
+#pragma unroll
+                    for (int b = 0; b < NT; ++b) {
+                        const uint4& h = hb[q & 1][b];
+                        if (first) mma_first(acc[a][b], x & k0, y & k0, x & k4, y & k4, h.x, h.y, c[b].x, c[b].y);
+                        else mma_next(acc[a][b], x & k0, y & k0, x & k4, y & k4, h.x, h.y);
+                    }
+#pragma unroll
+                    for (int b = 0; b < NT; ++b)
+                        mma_next(acc[a][b], x8 & k0, y8 & k0, x8 & k4, y8 & k4, hb[q & 1][b].z, hb[q & 1][b].w);
+                }
+                if (q % (4 / NG) == 4 / NG - 1) {
+                    const int gi = q / (4 / NG);
+#pragma unroll
+                    for (int a = 0; a < MT; ++a)
+#pragma unroll
+                        for (int b = 0; b < NT; ++b)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                sum[a][b][e] = fmaf(acc[a][b][e], scale_of<NG>(sc[2 * a + (e >> 1)], gi), sum[a][b][e]);
+                }
+            }
+        };
+        clear();
+        if (left == 0) {  // fewer slices than warps: nothing to add
+            for (int tile = 0; tile < n_tiles; ++tile) hand_over(tile);
+        } else {
+            Codes w0, w1;
+            read_codes(w0);
+            int tile = 0, slice = warp;
+            auto step = [&](const Codes& w, Codes& ahead) {
+                slice_of(slice, w, ahead);
+                slice += kMmaWarps;
+                if (slice < p.n_slice) return;
+                hand_over(tile);
+                clear();
+                slice = warp;
+                ++tile;
+            };
+            while (tile < n_tiles) {
+                step(w0, w1);
+                if (tile < n_tiles) step(w1, w0);
+            }
         }
     } else if (!copies) {
         const int at = threadIdx.x - kMmaWarps * 32;
@@ -540,8 +576,10 @@ cudaError_t launch_lmhead_quant(int M, int V, int H, int group, const void* hidd
     p.out = out;
     p.status = status;
     // Up to 16 hidden rows per pass, 8 when 16 (or all, if fewer) do not fit beside two stages
-    // of the rings; tiles of 64 vocabulary rows (a load of a hidden piece serves four MMAs), 32
-    // when 64 do not fit; a second buffer of partial sums and more stages where there is room.
+    // of the rings. Tiles of 64 vocabulary rows (a load of a hidden piece serves four MMAs), 32
+    // when 64 do not fit, or with two n-tiles, whose sums leave no registers for the next slice's
+    // codes of 64 rows (103 against 77 us at 8B); a second buffer of partial sums and more stages
+    // where there is room.
     const bool bf16 = out_dtype == 1;
     auto run = [&](int rows, int RT, auto fn, cudaError_t* e) -> bool {
         int st = 2, nb = 1;
@@ -558,7 +596,7 @@ cudaError_t launch_lmhead_quant(int M, int V, int H, int group, const void* hidd
     cudaError_t e = cudaErrorInvalidValue;
     if (M > 8) {
         const int rows = std::min(M, 16);
-        if (run(rows, 64, launch_group<64, 2>, &e) || run(rows, 32, launch_group<32, 2>, &e)) return e;
+        if (run(rows, 32, launch_group<32, 2>, &e)) return e;
     }
     const int rows = std::min(M, 8);
     if (run(rows, 64, launch_group<64, 1>, &e) || run(rows, 32, launch_group<32, 1>, &e)) return e;
