@@ -486,7 +486,8 @@ int eagle_lmhead_quant_pack(int vocab, int hidden_dim, int group, const void* we
  *                    [n_seq, rows_per_seq, V], in cfg->logit_dtype. After
  *                    eagle_verify: tokens = out_tokens, slots =
  *                    accepted_slots, per_seq = D + 1, rows_per_seq = T.
- *   temperature      > 0, finite: probabilities are softmax(row / temperature).
+ *   temperature      a positive normal number: probabilities are
+ *                    softmax(row / temperature).
  *   n_alt            alternatives per entry, 0..16.
  *   logprob  fp32 out: ln p[token].   rank  int32 out, or NULL: entries of the
  *            row above the token (larger logit, or equal and lower id).

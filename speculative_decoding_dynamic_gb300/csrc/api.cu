@@ -534,7 +534,7 @@ int eagle_token_logprobs(const eagle_tree_cfg* cfg, void* ws, size_t ws_bytes, i
     if (rc == EAGLE_OK) rc = bind_ws(d, ws, ws_bytes, &w);
     if (rc != EAGLE_OK) return rc;
     if (n_seq < 1 || per_seq < 1 || rows_per_seq < 1 || n_alt < 0 || n_alt > kMaxTopK || !logits || !tokens ||
-        !logprob || (n_alt > 0 && (!alt_ids || !alt_logprobs)) || !(temperature > 0.0f) || !std::isfinite(temperature))
+        !logprob || (n_alt > 0 && (!alt_ids || !alt_logprobs)) || !(temperature >= 0x1p-126f) || !std::isfinite(temperature))
         return EAGLE_ERR_INVALID_ARG;
     if (slots == nullptr && per_seq > rows_per_seq) return EAGLE_ERR_INVALID_ARG;
     if (!aligned16(logits) || static_cast<int64_t>(n_seq) * per_seq > (1 << 24)) return EAGLE_ERR_UNSUPPORTED;

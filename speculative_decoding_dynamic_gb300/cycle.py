@@ -146,7 +146,7 @@ class DeviceCycle:
     def run(self, draft_logits, prefix_len, root_token, q, cache, layer, target, seed, cycle, mode, temperature=1.0,
             compact=True, stream=None, head=None, new_kv=None):
         """The whole cycle (all stages) enqueued on `stream`. new_kv: optional (k, v) of the tree's
-        slots, stored in the 8-bit cache first."""
+        slots, stored in the 8-bit cache first. Log-probabilities are at the verification's temperature (greedy: 1)."""
         self.draft(draft_logits, stream, head=head)
         self.build(prefix_len, root_token, stream)
         if new_kv is not None:
@@ -154,7 +154,7 @@ class DeviceCycle:
         self.attention(q, cache, layer, prefix_len, stream)
         self.verify(mode, temperature, target, seed, cycle, stream)
         if self.n_alt is not None:
-            self.logprobs(target, temperature, stream)
+            self.logprobs(target, 1.0 if mode == E.GREEDY else temperature, stream)
         if compact:
             self.compact(cache, prefix_len, stream)
 

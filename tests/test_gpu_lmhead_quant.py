@@ -138,3 +138,27 @@ def test_draft_step_on_the_packed_head():
     assert (fcount.cpu().numpy() == k).all()
     for b in range(B):
         assert (ftok[b].cpu().numpy() == np.lexsort((np.arange(V), -x[b]))[:k]).all()
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_a_non_finite_row_is_nan_and_the_others_unharmed(value):
+    import torch
+    E = _E()
+    rng = np.random.default_rng(21)
+    M, V, H, group = 10, 640, 512, 64
+    h = P.bf16_round(rng.standard_normal((M, H)))
+    h[1] *= 2.0 ** 100
+    h[2] *= 2.0 ** -120
+    h[3, ::2] *= 2.0 ** -20  # entries far below their row's largest stay exact
+    h[4] = 0.0
+    h[5, 17] = value
+    codes = rng.integers(0, 256, (V, H // 2)).astype(np.uint8)
+    scales = P.bf16_round(rng.uniform(0.01, 1.0, (V, H // group)))
+    w = P.unpack_w4(codes, scales, group)
+    got = _head(E, h, codes, scales, group, torch.float32)
+    assert np.isnan(got[5]).all()
+    keep = [m for m in range(M) if m != 5]
+    x = h[keep].astype(np.float64)
+    tol = H * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T)
+    assert (np.abs(got[keep] - x @ w.T) <= tol).all()
+    assert (got[4] == 0).all()

@@ -179,3 +179,22 @@ def test_optional_outputs_and_capture():
     g.replay()
     torch.cuda.synchronize()
     assert (out.cpu().numpy() == want).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("temperature", [2.0 ** -126, 1e-20, 1e-3, 1e30])
+def test_extreme_temperatures(dtype, temperature):
+    """Differences over the temperature past fp32's range: probability 0 for all but the largest, entropy 0."""
+    import torch
+    rng = np.random.default_rng(11)
+    x = torch.from_numpy(rng.permutation(4096).astype(np.float32)[None, None] / 8 - 100).cuda()
+    x[0, 0, 7] = 3e38
+    x[0, 0, 9] = -3e38
+    x = x.to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    E = _E()
+    (lp, rank, ent, _, _), status = _run(E, x, None, np.array([[7]]), 2, temperature)
+    assert status == 0 and rank[0, 0] == 0
+    if temperature < 1e10:
+        assert lp[0, 0] == 0 and ent[0, 0] == 0
+    else:  # 3e38 / 1e30 = 3e8 over the others
+        assert lp[0, 0] == 0 and abs(ent[0, 0]) <= 2.0 ** -16

@@ -124,6 +124,14 @@ def test_token_logprobs_refusals(E):
     assert E.raw_call("eagle_token_logprobs", *args) == -1
 
 
+def test_token_logprobs_refuses_a_temperature_whose_reverse_overflows(E):
+    cfg = _cfg(E)
+    for t in (1e-39, 2.0 ** -127):
+        args = [ctypes.byref(cfg), PTR, E.eagle_workspace_bytes(cfg), 3, 7, 61, PTR, ctypes.c_float(t), PTR, PTR, 5, PTR, PTR,
+                PTR, PTR, PTR, None]
+        assert E.raw_call("eagle_token_logprobs", *args) == -1, t
+
+
 def test_binding_refuses_tensors_that_do_not_fit(E):
     import torch
     kv = E.kvq_contiguous(1, 2, 2, 128, 1, 64, 32)
