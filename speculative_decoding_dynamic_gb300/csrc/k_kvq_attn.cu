@@ -599,6 +599,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             float m_use = 0.0f, l = 0.0f, sref = 0.0f;
             bool seen = false;
+            // S of the piece's first tile before its scales are looked at: behind a piece without rows for
+            // this block the scales' barrier may be phases back, and its parity be taken for this
+            // tile's; S of a tile says that the tiles up to the sixth before it have theirs.
+            wait(&bar_s_full[g][tg & 1], tg >> 1);
             for (int j = it.t0; j < it.t1; ++j, ++t, ++tg) {
                 const int key0 = j * kBN;
                 const uint32_t s_cols = tmem + 64 * (2 * g + (tg & 1)) + lane_off;

@@ -512,3 +512,28 @@ def test_two_calls_at_once_on_their_own_workspaces():
     for *_, out, ws, want, tol in cases:
         assert E.eagle_status_fetch(ws) == 0
         assert (np.abs(out.float().cpu().numpy() - want) <= tol).all()
+
+
+def test_row_blocks_without_rows_between_items_of_a_worker():
+    """320 query rows per KV head: the second pair of row blocks has one block without rows, and workers pass from
+    such items to full ones. Scales far apart, so that another tile's would show; repeated, bit for bit."""
+    import torch
+    E = _E()
+    rng = np.random.default_rng(31)
+    B, Hq, H, T = 24, 64, 8, 40
+    kv = E.kvq_contiguous(B, Hq, H, D, 1, 1600, 16)
+    codes, scales = _buffers(kv, rng, lo=-9, hi=-3)
+    L = rng.integers(900, 1500, B)
+    q = _bf16(rng, (B, T, Hq, D), 0.2)
+    ws = E.alloc_workspace(E.eagle_kvq_attention_workspace_bytes(kv, T))
+    dc, ds, dq, dl = _dev(codes), _dev(scales), _dev_bf16(q), _dev(L.astype(np.int32))
+    runs = []
+    for _ in range(30):
+        out = torch.empty(B, T, Hq, D, dtype=torch.bfloat16, device="cuda")
+        E.eagle_kvq_tree_attention(kv, T, dq, dc, ds, 0, dl, None, None, out, ws)
+        runs.append(out)
+    torch.cuda.synchronize()
+    assert E.eagle_status_fetch(ws) == 0
+    want, tol = P.attention(kv, T, q, *P.views(kv, codes, scales), 0, L, None, None)
+    assert (np.abs(runs[0].float().cpu().numpy() - want) <= tol).all()
+    assert all((r == runs[0]).all() for r in runs)
