@@ -33,10 +33,13 @@
 //
 // Bound by the tensor pipe: per tile and row block eight QK^T MMAs of 48
 // cycles (N = 64 is bound by reading the operands from shared memory) and four
-// PV MMAs of 64, so 1280 cycles for both blocks of a tile, of 1590 measured
-// (8 sequences of 32K, 70B heads: 613 us, the pipe 72% busy; 64 sequences
-// of 8B: 121 us; one: 23.5 us). What was tried against it: QK^T over 128 keys
-// at once (N = 128, two thirds of the cycles) leaves no second buffer of S, and
+// PV MMAs of 64, so 1280 cycles for both blocks of a tile of some 1500 measured
+// (8 sequences of 32K, 70B heads: 543 us; 64 sequences of 8B: 123 us; one of
+// 2048: 25 us). That holds while the two blocks' softmaxes run half a tile apart,
+// as they do in this build; builds of the same loop in which they ran together
+// took 1900 (710 us), and letting PV of one block wait for the other's QK^T did
+// not part them (807 us). What was tried against the bound: QK^T over 128 keys at
+// once (N = 128, two thirds of the cycles) leaves no second buffer of S, and
 // waits for PV (857 us); S freed as soon as it is read, with P beside it, puts
 // the copy's, QK^T's and softmax's latencies in one chain (678 us); half a row
 // per softmax thread (24 warps of 80 registers, 730 against 701 us then);
@@ -263,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_p_full[2][2], bar_pv_done[2][2];
     __shared__ uint32_t tmem_holder;
     __shared__ TileScales ts[kScaleSlots];
+    __shared__ KvqCursor softmax_cur[kSoftmaxWarps];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int worker = blockIdx.x;
@@ -572,8 +576,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lead = elect_one();
         int t = 0, tg = 0;
         int4 cut = make_int4(0, 0, 0, 0);
+        // The cursor waits in shared memory while a piece is worked on: a tile needs the registers.
+        KvqCursor& own = softmax_cur[warp - kWarpSoftmax];
+        if (lane == 0) own = cur;
+        __syncwarp();
+        auto next_piece = [&]() {
+            KvqCursor c = own;
+            __syncwarp();
+            const bool more = c.next(p.s, it);
+            if (lane == 0) own = c;
+            __syncwarp();
+            return more;
+        };
         kvq_zero_bad(p.s, p.Hq, p.out, p.status, worker, threadIdx.x - kWarpSoftmax * 32, kSoftmaxWarps * 32);
-        while (cur.next(p.s, it)) {
+        while (next_piece()) {
             if (it.np) cut = kvq_cut(it);
             const int hk = it.sub / p.n_items, block = (it.sub - hk * p.n_items) * 2 + g;
             const int nt = it.t1 - it.t0;
@@ -657,6 +673,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     // (the vote here: its answer is not needed before P is written)
+                    // (the vote here: its answer is not needed before P is written)
+                    const bool any_rescale = __any_sync(0xffffffffu, rescale);
                     // P = 2^(s k - m_use + lv), two per packed multiply-add; the row sum takes the
                     // reverse of V's ratio. P as fp16 pairs over the first 32 columns of S.
                     // (A group's arguments, then its exponentials, then the last group's sums and
@@ -701,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // Rescaling O needs PV of the previous tile done (this tile's PV waits for
                     // this warp's arrival below). tcgen05.ld/st are warp-collective: rescale if
                     // any row of the warp needs it (alpha = 1 for the others).
-                    if (j > it.t0 && __any_sync(0xffffffffu, rescale)) {
+                    if (j > it.t0 && any_rescale) {
                         wait(&bar_pv_done[g][(tg - 1) & 1], (tg - 1) >> 1);
                         tc_fence_after();
 #pragma unroll 1
@@ -841,7 +859,9 @@ Plan make_plan(const KvqDims& kv, int T) {
     } else {
         pl.n_items = (rows + 2 * kBM - 1) / (2 * kBM);
         pl.rows = 2 * kBM;
-        pl.s = KvqSched{nullptr, nullptr, kv.B, T, kv.max_len, kv.Hkv * pl.n_items, kBN, 6, kKvqSms, 8};
+        // a tile with one block costs three quarters of one with two; a start and an end six tiles
+        const int blocks = (rows + kBM - 1) / kBM;
+        pl.s = KvqSched{nullptr, nullptr, kv.B, T, kv.max_len, kv.Hkv, pl.n_items, kBN, 24, 4, blocks % 2 ? 3 : 4, kKvqSms, 32};
     }
     const size_t slots = 2 * static_cast<size_t>(pl.s.workers) * pl.rows;
     pl.off_cut = 256;

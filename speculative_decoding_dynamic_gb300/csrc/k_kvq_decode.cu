@@ -465,7 +465,7 @@ cudaError_t launch_kvq_merge_decode(const KvqMergeParams& p, cudaStream_t stream
 }
 
 KvqSched kvq_decode_sched(int B, int T, int max_len, int Hkv, int rows) {
-    return KvqSched{nullptr, nullptr, B, T, max_len, Hkv, kStep, 2, kKvqSms * warps_of(rows <= 8 ? 1 : 2), 4};
+    return KvqSched{nullptr, nullptr, B, T, max_len, Hkv, 1, kStep, 2, 1, 1, kKvqSms * warps_of(rows <= 8 ? 1 : 2), 4};
 }
 
 template <int NT>

@@ -4,8 +4,9 @@
 // An item is one (sequence, KV head, row block) with all of the sequence's
 // keys in steps of `step` keys. The items of all sequences, laid end to end,
 // are one line of cost units: `ov` units for an item's start and end, then
-// one per step. Worker w takes the units [w chunk, (w+1) chunk), whatever the
-// lengths are, so ragged batches, single sequences and long contexts all fill
+// `cost` per step (`cost_last` in a KV head's last item, which may have fewer
+// rows). Worker w takes the steps that begin in the units [w chunk, (w+1) chunk),
+// whatever the lengths are, so ragged batches, single sequences and long contexts all fill
 // the machine; an item that a boundary cuts is finished from its pieces'
 // partial results (O, max, sum) by the merge kernel. A worker holds at most
 // two pieces of cut items: of the one it continues (slot 2w) and of the one
@@ -26,13 +27,19 @@ namespace eagle {
 struct KvqSched {
     const int32_t *prefix_len, *n_tree;  // n_tree may be NULL: T each
     int B, T, max_len;
-    int per_seq;  // items of a sequence
-    int step, ov, workers, min_chunk;
+    int heads, n_items;  // KV heads; items of one
+    int step, ov, cost, cost_last, workers, min_chunk;
 };
 
 struct KvqSeq {
-    int L, n, nkeys, nt, len;  // nkeys = nt = len = 0: lengths out of range
+    int L, n, nkeys, nt;  // nkeys = nt = 0: lengths out of range
+    long long len;        // units of a KV head
 };
+
+// Units of an item of nt steps.
+__device__ __forceinline__ int kvq_units(const KvqSched& s, int nt, bool last) {
+    return s.ov + nt * (last ? s.cost_last : s.cost);
+}
 
 __device__ __forceinline__ KvqSeq kvq_seq(const KvqSched& s, int b) {
     KvqSeq q;
@@ -41,7 +48,7 @@ __device__ __forceinline__ KvqSeq kvq_seq(const KvqSched& s, int b) {
     const bool bad = q.L < 0 || q.L > s.max_len - s.T || q.n < 1 || q.n > s.T;
     q.nkeys = bad ? 0 : q.L + q.n;
     q.nt = (q.nkeys + s.step - 1) / s.step;
-    q.len = bad ? 0 : q.nt + s.ov;
+    q.len = bad ? 0 : (s.n_items - 1) * static_cast<long long>(kvq_units(s, q.nt, false)) + kvq_units(s, q.nt, true);
     return q;
 }
 
@@ -60,9 +67,9 @@ __device__ __forceinline__ long long kvq_chunk(const KvqSched& s, long long tota
 // first kHeld groups are read once, all together, and stay in registers.
 struct KvqLens {
     static constexpr int kHeld = 4;
-    int len[kHeld];
+    long long len[kHeld];
     long long total;
-    __device__ __forceinline__ int at(const KvqSched& s, int b) const { return b < s.B ? kvq_seq(s, b).len : 0; }
+    __device__ __forceinline__ long long at(const KvqSched& s, int b) const { return b < s.B ? kvq_seq(s, b).len : 0; }
     __device__ __forceinline__ KvqLens(const KvqSched& s) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -71,7 +78,7 @@ struct KvqLens {
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) t += len[i];
         for (int b = 32 * kHeld + lane; b < s.B; b += 32) t += at(s, b);
-        total = static_cast<long long>(warp_sum_u64(static_cast<uint64_t>(t))) * s.per_seq;
+        total = static_cast<long long>(warp_sum_u64(static_cast<uint64_t>(t))) * s.heads;
     }
     // The sequence that holds unit pos < total, and the line's length before it (whole warp).
     __device__ __forceinline__ int find(const KvqSched& s, long long pos, long long* base) const {
@@ -91,20 +98,21 @@ struct KvqLens {
     }
 
 private:
-    __device__ __forceinline__ int step(const KvqSched& s, int own, long long pos, long long* before, long long* base) const {
+    __device__ __forceinline__ int step(const KvqSched& s, long long own, long long pos, long long* before,
+                                        long long* base) const {
         const int lane = threadIdx.x & 31;
-        uint32_t inc = own;  // 32 lengths of less than 2^26 each
+        own *= s.heads;
+        long long inc = own;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-            const uint32_t o = __shfl_up_sync(0xffffffffu, inc, m);
+            const long long o = __shfl_up_sync(0xffffffffu, inc, m);
             if (lane >= m) inc += o;
         }
-        const long long end = *before + static_cast<long long>(inc) * s.per_seq;
-        const unsigned hit = __ballot_sync(0xffffffffu, end > pos);
+        const unsigned hit = __ballot_sync(0xffffffffu, *before + inc > pos);
         const int l = hit ? __ffs(hit) - 1 : 31;
-        const uint32_t upto = __shfl_sync(0xffffffffu, inc, l), of_l = __shfl_sync(0xffffffffu, static_cast<uint32_t>(own), l);
-        if (hit) *base = *before + static_cast<long long>(upto - of_l) * s.per_seq;
-        else *before += static_cast<long long>(upto) * s.per_seq;
+        const long long upto = __shfl_sync(0xffffffffu, inc, l), of_l = __shfl_sync(0xffffffffu, own, l);
+        if (hit) *base = *before + upto - of_l;
+        else *before += upto;
         return hit ? l : -1;
     }
 };
@@ -121,7 +129,7 @@ struct KvqPiece {
 struct alignas(16) KvqCursor {
     long long pos, end, base, chunk;
     KvqSeq q;
-    int b, worker, pad;
+    int b, worker;
     __device__ __forceinline__ void init(const KvqSched& s, int w) {
         const KvqLens lens(s);
         const long long total = lens.total;
@@ -138,29 +146,35 @@ struct alignas(16) KvqCursor {
     }
     __device__ __forceinline__ bool next(const KvqSched& s, KvqPiece& p) {
         while (pos < end) {
-            const long long seq_end = base + static_cast<long long>(q.len) * s.per_seq;
+            const long long seq_end = base + q.len * s.heads;
             if (pos >= seq_end) {  // the next sequence with keys (one exists: pos < end <= total)
                 base = seq_end;
                 do q = kvq_seq(s, ++b);
-                while (q.len == 0);
+                while (q.nt == 0);
                 continue;
             }
-            const int sub = static_cast<int>(kvq_div(pos - base, q.len));
-            const long long g0 = base + static_cast<long long>(sub) * q.len;
-            const int from = static_cast<int>(pos - g0);
-            const int to = static_cast<int>(min(static_cast<long long>(q.len), end - g0));
-            pos = g0 + q.len;
+            const int hk = static_cast<int>(kvq_div(pos - base, q.len));
+            const long long head = base + hk * q.len;
+            const int full = kvq_units(s, q.nt, false);
+            const int i = min(s.n_items - 1, static_cast<int>(kvq_div(pos - head, full)));
+            const bool last = i == s.n_items - 1;
+            const int cost = last ? s.cost_last : s.cost, units = kvq_units(s, q.nt, last);
+            const long long g0 = head + static_cast<long long>(i) * full;
+            const int from = static_cast<int>(pos - g0) - s.ov;
+            const int to = static_cast<int>(min(static_cast<long long>(units), end - g0)) - s.ov;
+            pos = g0 + units;
             p.b = b;
-            p.sub = sub;
+            p.sub = hk * s.n_items + i;
             p.L = q.L;
             p.n = q.n;
             p.nkeys = q.nkeys;
             p.nt = q.nt;
-            p.t0 = max(0, from - s.ov);
-            p.t1 = max(0, to - s.ov);
-            p.np = 0;  // pieces: up to the worker that has the item's last unit
+            // the steps that begin in [from, to)
+            p.t0 = from <= 0 ? 0 : (from + cost - 1) / cost;
+            p.t1 = to <= 0 ? 0 : (to + cost - 1) / cost;
+            p.np = 0;  // pieces: up to the worker that has the item's last step
             if (p.t0 == 0 && p.t1 < p.nt)
-                p.np = static_cast<int>(kvq_div(g0 + s.ov + p.nt - 1 - worker * chunk, chunk)) + 1;
+                p.np = static_cast<int>(kvq_div(g0 + s.ov + static_cast<long long>(p.nt - 1) * cost - worker * chunk, chunk)) + 1;
             if (p.t1 > p.t0) return true;
         }
         return false;
@@ -225,7 +239,7 @@ cudaError_t launch_kvq_merge_decode(const KvqMergeParams& p, cudaStream_t stream
 __device__ __forceinline__ void kvq_zero_bad(const KvqSched& s, int Hq, __nv_bfloat16* out, int* status, int worker,
                                              int i, int n) {
     for (int b = worker; b < s.B; b += s.workers) {
-        if (kvq_seq(s, b).len != 0) continue;
+        if (kvq_seq(s, b).nt != 0) continue;
         if (i == 0) raise_status(status, kDevBadIndex);
         uint4* o = reinterpret_cast<uint4*>(out + static_cast<size_t>(b) * s.T * Hq * kKvqHeadDim);
         const int nv = s.T * Hq * kKvqHeadDim / 8;
