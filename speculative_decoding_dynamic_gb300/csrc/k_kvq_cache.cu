@@ -257,11 +257,20 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kvq_compact_kernel(
     for (int i = 0; i < 2; ++i) {
         if (!live || grown[i] == 1.0f) continue;  // uniform over a head's lanes
         const int hi = min((blk0 + i + 1) * kv.block, L + a + 1);
-        for (int pos = (blk0 + i) * kv.block; pos < hi; ++pos) {  // the block's other rows move to its grown scale
-            const int j = pos - L;
-            if (j >= 1 && ((moving >> j) & 1u)) continue;
-            uint4* w = reinterpret_cast<uint4*>(col + pos * kv.pos_stride);
-            *w = rescale16(*w, grown[i]);
+        // the block's other rows move to its grown scale, four read at once (one after the other, each
+        // waited for the one before: 44 us for 64 cold sequences of 8B against 30; eight: 32)
+        for (int pos = (blk0 + i) * kv.block; pos < hi; pos += 4) {
+            uint4 w[4];
+            bool stays[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = pos + e - L;
+                stays[e] = pos + e < hi && !(j >= 1 && ((moving >> j) & 1u));
+                if (stays[e]) w[e] = *reinterpret_cast<const uint4*>(col + (pos + e) * kv.pos_stride);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (stays[e]) *reinterpret_cast<uint4*>(col + (pos + e) * kv.pos_stride) = rescale16(w[e], grown[i]);
         }
     }
     const float ratio[2] = {blk_of[0] >= 0 ? __fdiv_rn(s_src[0], s_new[0]) : 1.0f,
