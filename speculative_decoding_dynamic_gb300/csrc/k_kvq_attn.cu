@@ -193,10 +193,20 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low 
 // kernel, by its converters behind their tiles, it held up each item by
 // 11,000 cycles: the fence behind a converted tile waits for the loads of q
 // in flight.) The first CTAs find where the attention's workers start.
+// n / d by the reciprocal 2^63 / d, rounded up: exact for all 32-bit n and d.
+// (Three divisions a row took half of the kernel's instructions.)
+struct Divisor {
+    uint64_t m;
+    explicit Divisor(int d) : m((uint64_t{1} << 63) / static_cast<uint64_t>(d) + 1) {}
+    __device__ __forceinline__ uint32_t of(uint32_t n) const {
+        return static_cast<uint32_t>(__umul64hi(m, static_cast<uint64_t>(n) << 1));
+    }
+};
 constexpr int kSplitThreads = 256, kSplitPer = 2, kSplitRows = kSplitPer * kSplitThreads / 16;
 __global__ void __launch_bounds__(kSplitThreads)
     kvq_split_q_kernel(const __nv_bfloat16* __restrict__ q, uint2* __restrict__ dst, float* __restrict__ fac, KvqRows rows,
-                       int Hkv, int64_t n, float scale_log2, KvqSched sched, KvqCursor* __restrict__ cursors) {
+                       Divisor by_Hq, Divisor by_T, Divisor by_G, int Hkv, uint32_t n, float scale_log2, KvqSched sched,
+                       KvqCursor* __restrict__ cursors) {
     pdl_wait_prior();
     pdl_launch_dependents();
     constexpr int kStarts = kSplitThreads / 32;
@@ -209,12 +219,12 @@ __global__ void __launch_bounds__(kSplitThreads)
         return;
     }
     const int l16 = threadIdx.x & 15;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x - starts) * kSplitRows + (threadIdx.x >> 4);
+    const uint32_t i0 = (blockIdx.x - starts) * kSplitRows + (threadIdx.x >> 4);
     uint4 u[kSplitPer];
 #pragma unroll
     for (int e = 0; e < kSplitPer; ++e) {
-        const int64_t i = i0 + e * (kSplitThreads / 16);
-        u[e] = i < n ? __ldg(reinterpret_cast<const uint4*>(q + i * kHD) + l16) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t i = i0 + e * (kSplitThreads / 16);
+        u[e] = i < n ? __ldg(reinterpret_cast<const uint4*>(q) + static_cast<size_t>(i) * (kHD / 8) + l16) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int e = 0; e < kSplitPer; ++e) {
@@ -234,11 +244,12 @@ __global__ void __launch_bounds__(kSplitThreads)
             const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h));
             lo[c] = e4m3x2(x - b.x, y - b.y);
         }
-        const int64_t i = i0 + e * (kSplitThreads / 16);
+        const uint32_t i = i0 + e * (kSplitThreads / 16);
         if (i >= n) continue;
-        const int64_t bt = kvq_div(i, rows.Hq), b = kvq_div(bt, rows.T);
-        const int h = static_cast<int>(i - bt * rows.Hq), t = static_cast<int>(bt - b * rows.T), hk = h / rows.G;
-        const int64_t bk = b * Hkv + hk, r = t * rows.G + (h - hk * rows.G), RT = rows.G * rows.T;
+        const uint32_t bt = by_Hq.of(i), b = by_T.of(bt);
+        const uint32_t h = i - bt * rows.Hq, t = bt - b * rows.T, hk = by_G.of(h);
+        const uint32_t RT = rows.G * rows.T, r = t * rows.G + (h - hk * rows.G);
+        const size_t bk = static_cast<size_t>(b) * Hkv + hk;
         dst[(2 * bk * RT + r) * 16 + l16] = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
         dst[((2 * bk + 1) * RT + r) * 16 + l16] = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
         if (l16 == 0) fac[bk * RT + r] = scale_log2 / s;
@@ -932,9 +943,10 @@ cudaError_t launch_kvq_attention(const KvqDims& kv, int T, const void* q, const 
     cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kvq_attn_kernel), kSmem);
     if (e != cudaSuccess) return e;
     const int64_t q_rows = static_cast<int64_t>(kv.B) * T * kv.Hq;
+    if (q_rows > INT32_MAX) return cudaErrorInvalidValue;  // half a terabyte of q
     e = launch_pdl(kvq_split_q_kernel, dim3(static_cast<unsigned>((q_rows + kSplitRows - 1) / kSplitRows + (pl.s.workers + kSplitThreads / 32 - 1) / (kSplitThreads / 32))), dim3(kSplitThreads), 0,
                    stream, p.q, reinterpret_cast<uint2*>(w + pl.off_q), reinterpret_cast<float*>(w + pl.off_fac), p.rows,
-                   kv.Hkv, q_rows, p.scale_log2, p.s, reinterpret_cast<KvqCursor*>(w + pl.off_cur));
+                   Divisor(kv.Hq), Divisor(T), Divisor(pl.G), kv.Hkv, static_cast<uint32_t>(q_rows), p.scale_log2, p.s, reinterpret_cast<KvqCursor*>(w + pl.off_cur));
     if (e != cudaSuccess) return e;
     e = launch_pdl(kvq_attn_kernel, dim3(pl.s.workers), dim3(kThreads), kSmem, stream, tq, tk, tv, p);
     if (e != cudaSuccess) return e;
