@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int t = 0, qi = 0, sk = 0, pk = 0, sv = 0, pv = 0;  // stages of tile t and their phases
         auto copy_q = [&](const KvqPiece& a, int i) {  // q of the i-th item
             if (i >= 2) wait(&bar_q_empty[i & 1], (i >> 1) - 1);
-            if (wait.ok) {
+            if (__all_sync(0xffffffffu, wait.ok)) {
                 const int hk = uniform(a.sub / p.n_items), block = uniform((a.sub - hk * p.n_items) * 2);
                 const int n = min(2, n_blocks - block), w = uniform(a.b) * p.Hkv + hk;
                 expect_tx(lead, &bar_q_full[i & 1], n * 2 * kTileQ);
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else if (t >= kVStages) wait(&bar_v8_empty[sv], pv ^ 1);
                 if (t > 0 && lane == 0) mbar_arrive(&bar_go[(t - 1) & (kScaleSlots - 1)]);
                 __syncwarp();
-                if (wait.ok) {
+                if (__all_sync(0xffffffffu, wait.ok)) {
                     expect_tx(lead, &bar_k_full[sk], kTile8);
                     copy_4d(lead, base + kSmemK + sk * kTile8, &tm_k, 0, hk, j * kBN, b, &bar_k_full[sk]);
                     expect_tx(lead, &bar_v8_full[sv], kTile8);

@@ -58,7 +58,8 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
 //
 // Bound by HBM: two bytes read and one written per element. Holding the block
 // in registers instead of reading it a second time for the codes is why the
-// group grows with the block.
+// group grows with the block. Measured: 20,000 prompt tokens of 40 heads (461 MB)
+// 71.4 us, 6.5 TB/s; 64 trees of 61 slots of 8 heads (24 MB) 5.6 us.
 template <int BLK>
 __global__ void __launch_bounds__(kStoreThreads) kvq_store_kernel(
     KvqDims kv, int layer, int T, int nhg, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
@@ -188,8 +189,8 @@ __device__ __forceinline__ uint4 rescale16(const uint4& u, float ratio) {
 // rewrites only bytes that it alone reads, so no barrier is needed. The cost
 // is a chain of small loads (lengths and slots, then rows and scales) and
 // the number of warps that go through it: four heads per warp bring a batch
-// of 64 with 32 layers into one wave (one head per warp: 16.8 us; 4: see the
-// launch's note).
+// of 64 with 32 layers into one wave (one head per warp: 16.8 us; four: 9.1, and
+// 2.8 us for one sequence).
 __global__ void __launch_bounds__(kMoveWarps * 32) kvq_compact_kernel(
     KvqDims kv, unsigned char* __restrict__ codes, float* __restrict__ scales, const int32_t* __restrict__ prefix_len,
     const int32_t* __restrict__ accept_len, const int32_t* __restrict__ slots, int slots_stride,
