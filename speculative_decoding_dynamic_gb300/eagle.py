@@ -82,11 +82,11 @@ class KvqCfg(ctypes.Structure):
 
     def extent(self, layers: int) -> tuple[int, int]:
         """Bytes of codes and elements of scales that `layers` layers of the cache span."""
-        row = self.n_kv_heads * self.head_dim
-        return ((self.batch - 1) * self.seq_stride + (layers - 1) * self.layer_stride + self.kv_stride +
-                (self.max_len - 1) * self.pos_stride + row,
-                (self.batch - 1) * self.scale_seq_stride + (layers - 1) * self.scale_layer_stride +
-                self.scale_kv_stride + (self.n_blocks - 1) * self.scale_block_stride + self.n_kv_heads)
+        heads, max_len, b, k = self.n_kv_heads, self.max_len, self.batch - 1, layers - 1
+        return (b * self.seq_stride + k * self.layer_stride + self.kv_stride + (max_len - 1) * self.pos_stride +
+                heads * self.head_dim,
+                b * self.scale_seq_stride + k * self.scale_layer_stride + self.scale_kv_stride +
+                (-(-max_len // self.block) - 1) * self.scale_block_stride + heads)
 
 
 _p = ctypes.c_void_p
@@ -165,13 +165,13 @@ def _ws(ws) -> tuple[int, int]:
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _need(fn: str, name: str, t, dtypes, n: int, dev: int) -> None:
-    """A tensor argument of `fn`: contiguous, on device `dev` (the current one), of one of `dtypes`, with at least n
-    elements (None and raw addresses pass: the library checks what it can of those)."""
+def _need(fn: str, name: str, t, dtypes, n: int, dev: int) -> int | None:
+    """The address of a tensor argument of `fn`: contiguous, on device `dev` (the current one), of one of `dtypes`, with
+    at least n elements (None and raw addresses pass: the library checks what it can of those)."""
     if t is None or type(t) is int:
-        return
+        return t
     if t.dtype in dtypes and t.get_device() == dev and t.is_contiguous() and t.numel() >= n:
-        return
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise ValueError(f"{fn}: {name} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
     if t.get_device() != dev:
@@ -181,8 +181,14 @@ def _need(fn: str, name: str, t, dtypes, n: int, dev: int) -> None:
     raise ValueError(f"{fn}: {name} has {t.numel()} elements, needs {n}")
 
 
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _device() -> int:
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    """The current device's index; -2 (no tensor's) before CUDA is initialised."""
+    if not torch.cuda.is_initialized():
+        return -2
+    return _get_device() if _get_device is not None else torch.cuda.current_device()
 
 
 # the current stream's handle without a stream object around it: a third of a small call's time on the host
@@ -349,40 +355,37 @@ def alloc_kvq(kv: KvqCfg, device="cuda") -> tuple[torch.Tensor, torch.Tensor]:
             torch.zeros(*shape, kv.n_blocks, kv.n_kv_heads, dtype=torch.float32, device=device))
 
 
-def _need_kvq(fn: str, kv: KvqCfg, layers: int, codes, scales, dev: int) -> None:
-    c, s = kv.extent(layers)
-    _need(fn, "codes", codes, _CODES, c, dev)
-    _need(fn, "scales", scales, _F32, s, dev)
+def _behind(t):
+    """A slice of fused rows as all that lies behind its start in its storage."""
+    if not isinstance(t, torch.Tensor) or t.is_contiguous():
+        return t
+    return t.as_strided((t.untyped_storage().nbytes() // t.element_size() - t.storage_offset(),), (1,))
 
 
 def eagle_kvq_store(kv, layer, T, k, v, row_stride, row_start, start, count, codes, scales, ws=None, stream=None):
     fn, dev, B = "eagle_kvq_store", _device(), kv.batch
     # dense rows: the last one reaches its heads' end (packed rows: the caller's row_start says how far)
     rows = 0 if row_start is not None else (B * T - 1) * row_stride + kv.n_kv_heads * kv.head_dim
-    for name, t in (("k", k), ("v", v)):
-        if isinstance(t, torch.Tensor) and not t.is_contiguous():  # a slice of fused rows: what lies behind its start
-            t = t.as_strided((t.untyped_storage().nbytes() // t.element_size() - t.storage_offset(),), (1,))
-        _need(fn, name, t, _BF16, rows, dev)
-    _need(fn, "row_start", row_start, _I32, B, dev)
-    _need(fn, "start", start, _I32, B, dev)
-    _need(fn, "count", count, _I32, B, dev)
-    _need_kvq(fn, kv, layer + 1, codes, scales, dev)
-    _check(fn, _lib.eagle_kvq_store(ctypes.byref(kv), layer, T, _ptr(k), _ptr(v), row_stride, _ptr(row_start),
-                                    _ptr(start), _ptr(count), _ptr(codes), _ptr(scales), _ptr(ws),
+    n_codes, n_scales = kv.extent(layer + 1)
+    _check(fn, _lib.eagle_kvq_store(ctypes.byref(kv), layer, T, _need(fn, "k", _behind(k), _BF16, rows, dev),
+                                    _need(fn, "v", _behind(v), _BF16, rows, dev), row_stride,
+                                    _need(fn, "row_start", row_start, _I32, B, dev),
+                                    _need(fn, "start", start, _I32, B, dev), _need(fn, "count", count, _I32, B, dev),
+                                    _need(fn, "codes", codes, _CODES, n_codes, dev),
+                                    _need(fn, "scales", scales, _F32, n_scales, dev), _ptr(ws),
                                     _stream_on(stream, dev)))
 
 
 def eagle_kvq_compact(kv, codes, scales, prefix_len, accept_len, accepted_slots, slots_stride, new_len, ws=None,
                       stream=None):
     fn, dev, B = "eagle_kvq_compact", _device(), kv.batch
-    _need(fn, "prefix_len", prefix_len, _I32, B, dev)
-    _need(fn, "accept_len", accept_len, _I32, B, dev)
-    _need(fn, "new_len", new_len, _I32, B, dev)
-    _need(fn, "accepted_slots", accepted_slots, _I32, B * slots_stride, dev)
-    if kv.layers > 0:
-        _need_kvq(fn, kv, kv.layers, codes, scales, dev)
-    _check(fn, _lib.eagle_kvq_compact(ctypes.byref(kv), _ptr(codes), _ptr(scales), _ptr(prefix_len),
-                                      _ptr(accept_len), _ptr(accepted_slots), slots_stride, _ptr(new_len), _ptr(ws),
+    n_codes, n_scales = kv.extent(kv.layers) if kv.layers > 0 else (0, 0)
+    _check(fn, _lib.eagle_kvq_compact(ctypes.byref(kv), _need(fn, "codes", codes, _CODES, n_codes, dev),
+                                      _need(fn, "scales", scales, _F32, n_scales, dev),
+                                      _need(fn, "prefix_len", prefix_len, _I32, B, dev),
+                                      _need(fn, "accept_len", accept_len, _I32, B, dev),
+                                      _need(fn, "accepted_slots", accepted_slots, _I32, B * slots_stride, dev),
+                                      slots_stride, _need(fn, "new_len", new_len, _I32, B, dev), _ptr(ws),
                                       _stream_on(stream, dev)))
 
 
@@ -394,15 +397,14 @@ def eagle_kvq_tree_attention(kv, T, q, codes, scales, layer, prefix_len, mask, n
     """Tree attention over the 8-bit cache; mask None: slot i sees slots 0..i (T = 1: a decode step)."""
     fn, dev, B = "eagle_kvq_tree_attention", _device(), kv.batch
     n = B * T * kv.n_q_heads * kv.head_dim
-    _need(fn, "q", q, _BF16, n, dev)
-    _need(fn, "out", out, _BF16, n, dev)
-    _need(fn, "prefix_len", prefix_len, _I32, B, dev)
-    _need(fn, "n_tree", n_tree, _I32, B, dev)
-    _need(fn, "mask", mask, _W32, B * T * ((T + 31) // 32), dev)
-    _need_kvq(fn, kv, layer + 1, codes, scales, dev)
-    _check(fn, _lib.eagle_kvq_tree_attention(ctypes.byref(kv), T, _ptr(q), _ptr(codes), _ptr(scales), layer,
-                                             _ptr(prefix_len), _ptr(mask), _ptr(n_tree), _ptr(out), *_ws(ws),
-                                             _stream_on(stream, dev)))
+    n_codes, n_scales = kv.extent(layer + 1)
+    _check(fn, _lib.eagle_kvq_tree_attention(ctypes.byref(kv), T, _need(fn, "q", q, _BF16, n, dev),
+                                             _need(fn, "codes", codes, _CODES, n_codes, dev),
+                                             _need(fn, "scales", scales, _F32, n_scales, dev), layer,
+                                             _need(fn, "prefix_len", prefix_len, _I32, B, dev),
+                                             _need(fn, "mask", mask, _W32, B * T * ((T + 31) // 32), dev),
+                                             _need(fn, "n_tree", n_tree, _I32, B, dev),
+                                             _need(fn, "out", out, _BF16, n, dev), *_ws(ws), _stream_on(stream, dev)))
 
 
 def _logit_dtypes(cfg):
@@ -412,20 +414,20 @@ def _logit_dtypes(cfg):
 def eagle_lmhead_quant(cfg, ws, hidden_dim, group, hidden, codes, scales, draft_logits, stream=None):
     """LM-head logits from 4-bit weights with group scales (eagle_lmhead_quant_pack)."""
     fn, dev, M = "eagle_lmhead_quant", _device(), cfg.batch * cfg.top_k
-    _need(fn, "hidden", hidden, _BF16, M * hidden_dim, dev)
-    _need(fn, "codes", codes, _U8, cfg.vocab * hidden_dim // 2, dev)
-    _need(fn, "scales", scales, _BF16, cfg.vocab * hidden_dim // max(1, group), dev)
-    _need(fn, "draft_logits", draft_logits, _logit_dtypes(cfg), M * cfg.vocab, dev)
-    _check(fn, _lib.eagle_lmhead_quant(ctypes.byref(cfg), *_ws(ws), hidden_dim, group, _ptr(hidden), _ptr(codes),
-                                       _ptr(scales), _ptr(draft_logits), _stream_on(stream, dev)))
+    n = cfg.vocab * hidden_dim
+    _check(fn, _lib.eagle_lmhead_quant(ctypes.byref(cfg), *_ws(ws), hidden_dim, group,
+                                       _need(fn, "hidden", hidden, _BF16, M * hidden_dim, dev),
+                                       _need(fn, "codes", codes, _U8, n // 2, dev),
+                                       _need(fn, "scales", scales, _BF16, n // max(1, group), dev),
+                                       _need(fn, "draft_logits", draft_logits, _logit_dtypes(cfg), M * cfg.vocab, dev),
+                                       _stream_on(stream, dev)))
 
 
 def eagle_lmhead_quant_pack(vocab, hidden_dim, group, weight, codes, scales, stream=None):
-    fn, dev = "eagle_lmhead_quant_pack", _device()
-    _need(fn, "weight", weight, _BF16, vocab * hidden_dim, dev)
-    _need(fn, "codes", codes, _U8, vocab * hidden_dim // 2, dev)
-    _need(fn, "scales", scales, _BF16, vocab * hidden_dim // max(1, group), dev)
-    _check(fn, _lib.eagle_lmhead_quant_pack(vocab, hidden_dim, group, _ptr(weight), _ptr(codes), _ptr(scales),
+    fn, dev, n = "eagle_lmhead_quant_pack", _device(), vocab * hidden_dim
+    _check(fn, _lib.eagle_lmhead_quant_pack(vocab, hidden_dim, group, _need(fn, "weight", weight, _BF16, n, dev),
+                                            _need(fn, "codes", codes, _U8, n // 2, dev),
+                                            _need(fn, "scales", scales, _BF16, n // max(1, group), dev),
                                             _stream_on(stream, dev)))
 
 
@@ -433,17 +435,14 @@ def eagle_token_logprobs(cfg, ws, n_seq, per_seq, rows_per_seq, logits, temperat
                          rank=None, entropy=None, alt_ids=None, alt_logprobs=None, stream=None):
     """Log-probability, rank, entropy and top alternatives of given tokens (slots None: entry j reads row j)."""
     fn, dev, n = "eagle_token_logprobs", _device(), n_seq * per_seq
-    _need(fn, "logits", logits, _logit_dtypes(cfg), n_seq * rows_per_seq * cfg.vocab, dev)
-    _need(fn, "slots", slots, _I32, n, dev)
-    _need(fn, "tokens", tokens, _I32, n, dev)
-    _need(fn, "logprob", logprob, _F32, n, dev)
-    _need(fn, "rank", rank, _I32, n, dev)
-    _need(fn, "entropy", entropy, _F32, n, dev)
-    _need(fn, "alt_ids", alt_ids, _I32, n * n_alt, dev)
-    _need(fn, "alt_logprobs", alt_logprobs, _F32, n * n_alt, dev)
-    _check(fn, _lib.eagle_token_logprobs(ctypes.byref(cfg), *_ws(ws), n_seq, per_seq, rows_per_seq, _ptr(logits),
-                                         float(temperature), _ptr(slots), _ptr(tokens), n_alt, _ptr(logprob),
-                                         _ptr(rank), _ptr(entropy), _ptr(alt_ids), _ptr(alt_logprobs),
+    rows = n_seq * rows_per_seq * cfg.vocab
+    _check(fn, _lib.eagle_token_logprobs(ctypes.byref(cfg), *_ws(ws), n_seq, per_seq, rows_per_seq,
+                                         _need(fn, "logits", logits, _logit_dtypes(cfg), rows, dev), float(temperature),
+                                         _need(fn, "slots", slots, _I32, n, dev), _need(fn, "tokens", tokens, _I32, n, dev),
+                                         n_alt, _need(fn, "logprob", logprob, _F32, n, dev),
+                                         _need(fn, "rank", rank, _I32, n, dev), _need(fn, "entropy", entropy, _F32, n, dev),
+                                         _need(fn, "alt_ids", alt_ids, _I32, n * n_alt, dev),
+                                         _need(fn, "alt_logprobs", alt_logprobs, _F32, n * n_alt, dev),
                                          _stream_on(stream, dev)))
 
 
