@@ -2,17 +2,17 @@
 // GQA attention for more than 16 query rows per KV head.
 //
 // For sequence b and KV head hk the G = Hq/Hkv query heads of every tree slot
-// form G*T query rows, in row blocks of 128. An item is a pair of row blocks with all keys; a worker (one CTA per
-// SM) walks its pieces of items (kvq_sched.cuh) in key tiles of 64. Per tile t
-// and row block g of the pair:
+// form G*T query rows, in row blocks of 128. An item is a pair of row blocks
+// with all keys; a worker (one CTA per SM) walks its pieces of items
+// (kvq_sched.cuh) in key tiles of 64. Per tile t and row block g of the pair:
 //   S = q K^T        tcgen05.mma kind::f8f6f4 straight from the codes: a row
 //                    of q, scaled by a power of two to at most 256, is split
 //                    into two e4m3 operands q = hi + lo (eight significant
 //                    bits in all, those of bf16; elements below 2^-9 of the
 //                    row's largest lose some), two MMAs at twice the fp16
 //                    rate, by a small kernel before this one. (K to bf16 and q
-//                    as it is: 945 us at 70B 32K, for the conversion of K and the
-//                    larger tiles' traffic through shared memory.)
+//                    as it is: 945 against 703 us at 70B 32K then, for the
+//                    conversion of K and the larger tiles in shared memory.)
 //   P = softmax part four warps, one thread per row (TMEM lane = row, 64 key
 //                    columns): K's block scale and q's row scale, tree mask,
 //                    exponentials in the log2 domain against a reference
