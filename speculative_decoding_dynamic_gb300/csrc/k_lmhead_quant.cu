@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     pdl_launch_dependents();
     pdl_wait_prior();
-    // The copying warp: lane w fills the ring of MMA warp w, the first stages before the hidden rows are read.
+    // The copying warp: lane w fills the ring of MMA warp w.
     const bool copies = warp == kMmaWarps + kAddWarps;
     const int total = copies && lane < kMmaWarps ? (p.n_slice - lane + kMmaWarps - 1) / kMmaWarps * n_tiles : 0;
     int filled = 0, f_tile = 0, f_slice = lane, f_stage = 0;
@@ -213,9 +213,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++f_tile;
         }
     };
-    if (copies)
-        while (filled < min(p.stages, total)) fill();
-    __syncwarp();
     // hidden rows into shared memory, a warp per row: its largest element, then pieces of eight
     // entries as fp16 in MMA order (0 4, 1 5, 2 6, 3 7), and the groups' corrections
     for (int m = warp; m < p.c_stride; m += kThreads / 32) {
@@ -243,7 +240,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int o = 16; o > 0; o >>= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         mx = max(mx & 0xffffu, mx >> 16);
         const float scale = pow2_to(__uint_as_float(mx << 16), 14);
-        const float scale16 = scale * 0x1p-4f;
         // an infinity or NaN in the row makes its logits NaN
         if (lane == 0) fac[m] = mx < 0x7f80u ? 1.0f / scale : __uint_as_float(0x7fffffffu);
         unsigned char* row = hid + m * p.hid_stride;
@@ -254,12 +250,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
             float x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = __uint_as_float((e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16));
+            for (int e = 0; e < 8; ++e)
+                x[e] = __uint_as_float((e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16)) * scale;
             float sum = ((x[0] + x[4]) + (x[1] + x[5])) + ((x[2] + x[6]) + (x[3] + x[7]));
             uint32_t h[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const float f = (c & 1) ? scale16 : scale;
+                const float f = (c & 1) ? 0x1p-4f : 1.0f;
                 const __half2 y = __floats2half2_rn(x[c] * f, x[c + 4] * f);
                 h[c] = *reinterpret_cast<const uint32_t*>(&y);
             }
@@ -267,9 +264,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int o = 1; o < GROUP / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             if (i >= pieces) continue;
             *reinterpret_cast<uint4*>(row + ((i >> 4) * 16 + piece_of<GROUP>((i & 15) * 8)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-            if (i % (GROUP / 8) == 0) corr[i / (GROUP / 8) * p.c_stride + m] = sum * scale * -0x1p-21f;
+            if (i % (GROUP / 8) == 0) corr[i / (GROUP / 8) * p.c_stride + m] = sum * -0x1p-21f;
         }
     }
+    // the first copies behind the hidden rows: before them the rows' loads waited in their queue (1.5 us at 8B)
+    if (copies)
+        while (filled < min(p.stages, total)) fill();
+    __syncwarp();
     __syncthreads();
 
     if (warp < kMmaWarps) {

@@ -162,3 +162,18 @@ def test_a_non_finite_row_is_nan_and_the_others_unharmed(value):
     tol = H * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T)
     assert (np.abs(got[keep] - x @ w.T) <= tol).all()
     assert (got[4] == 0).all()
+
+
+def test_rows_whose_plain_sums_overflow():
+    """Entries near the largest bf16 number and scales as small: the logits are ordinary, a group's sum of entries is not."""
+    import torch
+    E = _E()
+    rng = np.random.default_rng(22)
+    M, V, H, group = 3, 128, 256, 64
+    h = P.bf16_round(np.full((M, H), 2.0 ** 127) * rng.choice([1.0, 1.5, -1.0], (M, H), p=[0.6, 0.3, 0.1]))
+    codes = rng.integers(0, 256, (V, H // 2)).astype(np.uint8)
+    scales = P.bf16_round(2.0 ** -125 * rng.uniform(1.0, 2.0, (V, H // group)))
+    w = P.unpack_w4(codes, scales, group)
+    got = _head(E, h, codes, scales, group, torch.float32)
+    x = h.astype(np.float64)
+    assert (np.abs(got - x @ w.T) <= H * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T)).all()
