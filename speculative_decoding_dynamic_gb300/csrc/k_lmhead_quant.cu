@@ -36,7 +36,7 @@
 // logits while the next tile streams.
 //
 // Measured: 8 rows, H = 8192, V = 128256 (525 MB of codes): 107 us, 4.9 TB/s;
-// 10 rows, H = 4096 (263 MB): 77 us, 3.4 TB/s. Bound by latency with two MMA
+// 10 rows, H = 4096 (263 MB): 75.5 us, 3.5 TB/s. Bound by latency with two MMA
 // warps per scheduler (their 168 registers allow no third beside the others):
 // ten rows are two n-tiles of which the tensor pipe alone takes 28 us (8 cycles
 // an MMA). Sixteen MMA warps of 96 registers: 119 and 128 us. More stages: no change.
