@@ -109,6 +109,8 @@ class DeviceCycle:
         """The tree's K and V of a layer into the 8-bit cache: k, v [B, T, Hkv, 128] bf16, tree slot j
         of a sequence at position prefix_len + j (slots past n_tree are not written)."""
         kv = self.kv
+        if not self.quant_kv:
+            raise ValueError("DeviceCycle.store: only the 8-bit cache (a KvqCfg) is written here")
         E.eagle_kvq_store(kv, layer, self.cfg.T, k, v, kv.n_kv_heads * kv.head_dim, None, prefix_len, self.n_tree,
                           *cache, ws=self.ws, stream=stream)
 

@@ -162,3 +162,14 @@ def test_the_fused_head_refuses_the_4_bit_weight():
     z = torch.zeros(8, device="cuda")
     with pytest.raises(ValueError, match="4-bit head"):
         dc.draft(None, head=((z, z, 32), z))
+
+
+def test_store_refuses_the_16_bit_cache():
+    import torch
+    from speculative_decoding_dynamic_gb300 import cycle as C, eagle as E
+    cfg = E.TreeCfg(1, 128, 2, 1, 2, 0.0, E.EAGLE_BF16)
+    row = 2 * D
+    dc = C.DeviceCycle(cfg, E.KvCfg(1, 2, 2, D, 1, 16, E.EAGLE_BF16, 2 * 16 * row, 2 * 16 * row, 16 * row, row))
+    z = torch.zeros(8, device="cuda")
+    with pytest.raises(ValueError, match="8-bit cache"):
+        dc.store(z, z, z, 0, z)
