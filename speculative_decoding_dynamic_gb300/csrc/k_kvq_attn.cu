@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const TileScales& sc = ts[t & (kScaleSlots - 1)];
                     const float4 k4 = *reinterpret_cast<const float4*>(sc.k), lv4 = *reinterpret_cast<const float4*>(sc.lv);
                     const float4 iv4 = *reinterpret_cast<const float4*>(sc.iv);
-                    const float k[kSub] = {k4.x * fac, k4.y * fac, k4.z * fac, k4.w * fac};
+                    float k[kSub] = {k4.x * fac, k4.y * fac, k4.z * fac, k4.w * fac};
                     const float lv[kSub] = {lv4.x, lv4.y, lv4.z, lv4.w}, iv[kSub] = {iv4.x, iv4.y, iv4.z, iv4.w};
                     float alpha = sc.alpha;
                     sref = sc.sref;
@@ -667,6 +667,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
 #pragma unroll
                         for (int e = 0; e < kBN; ++e) s[e] = ((vis[e >> 5] >> (e & 31)) & 1u) ? s[e] : 0xff800000u;
+                        // -inf times a product that underflowed to 0 would be NaN (a row of zeros has the factor
+                        // 2^-129, a block of zeros the scale 2^-126): above 0, a score changes by less than 2^-125
+#pragma unroll
+                        for (int e = 0; e < kSub; ++e) k[e] = fmaxf(k[e], 0x1p-149f);
                     }
                     const float mx = fmaxf(fmaxf(max16(s) * k[0], max16(s + 16) * k[1]),
                                            fmaxf(max16(s + 32) * k[2], max16(s + 48) * k[3]));  // the scales are positive

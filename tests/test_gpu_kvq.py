@@ -537,3 +537,32 @@ def test_row_blocks_without_rows_between_items_of_a_worker():
     want, tol = P.attention(kv, T, q, *P.views(kv, codes, scales), 0, L, None, None)
     assert (np.abs(runs[0].float().cpu().numpy() - want) <= tol).all()
     assert all((r == runs[0]).all() for r in runs)
+
+
+# ------------------------------------------- small products, NaN, limits ---
+
+@pytest.mark.parametrize("T,L", [(1, [20, 333]), (61, [20, 333]), (1, [3000]), (61, [3000])])
+def test_attention_zero_and_tiny_rows_over_small_scales(T, L):
+    """Rows of q that are zero or tiny over blocks of zero K (scale 2^-126, as the store writes it) and over small
+    scales: the factor of a score underflows, and the row is the mean of the V rows that it sees. Whole items, and
+    one of 3000 positions that many workers share."""
+    E = _E()
+    rng = np.random.default_rng(40 + T)
+    B, Hq, H = len(L), 8, 2
+    kv = E.kvq_contiguous(B, Hq, H, D, 1, max(L) + T, 16)
+    codes, scales = _buffers(kv, rng)
+    vc, vs = P.views(kv, codes, scales)
+    vs[:, 0, 0] = 2.0 ** rng.choice([-126.0, -60.0, -24.0, -9.0], vs[:, 0, 0].shape)
+    vs[:, 0, 0, -5:] = 2.0 ** -126 if T > 1 else 2.0 ** -24
+    zero = np.repeat(vs[:, 0, 0] == 2.0 ** -126, 16, 1)[:, :kv.max_len]
+    vc[:, 0, 0][zero] = 0
+    q = _bf16(rng, (B, T, Hq, D), 2.0)
+    size = 2.0 ** np.array([-200.0, -130.0, -100.0, -40.0, -20.0, -15.0, -14.0, 0.0])
+    q = P.bf16_round(q * size[rng.permutation(B * T * Hq) % 8].reshape(B, T, Hq, 1))
+    q[:, 0, ::2] = 0.0
+    see = _tree(rng, B, T, [T] * B) if T > 1 else None
+    want, tol = P.attention(kv, T, q, vc, vs, 0, L, see, None)
+    got, status = _attend(E, kv, T, L, None, see, codes, scales, q, 0)
+    assert status == 0
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4])
