@@ -798,8 +798,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!whole && row_live)
+                // (a sum that is NaN goes into the merge as it is: the whole row is zero then, not this piece left out)
                 reinterpret_cast<float2*>(p.part.ml)[part_slot * p.part.rows + prow] =
-                    make_float2(any ? m_use : -INFINITY, any ? l : 0.0f);
+                    make_float2(seen ? m_use : -INFINITY, wait.ok ? l : 0.0f);
             tc_fence_before();
         }
         if (!wait.ok) raise_status(p.status, kDevTimeout);

@@ -566,3 +566,35 @@ def test_attention_zero_and_tiny_rows_over_small_scales(T, L):
     assert status == 0
     bad = ~(np.abs(got - want) <= tol)
     assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4])
+
+
+@pytest.mark.parametrize("T,L", [(1, 40), (12, 40), (61, 40), (1, 5000), (61, 5000)])
+@pytest.mark.parametrize("where", ["prefix", "slot", "q"])
+def test_attention_nan_in_k_or_q_reaches_the_rows_that_see_it_only(T, L, where):
+    """A NaN among K's codes or in q: the rows that see it are zero or NaN, all others as without it, whether an
+    item is one worker's or shared by many."""
+    if where == "slot" and T == 1:
+        pytest.skip("a decode step's only slot is seen by its row")
+    E = _E()
+    rng = np.random.default_rng(50 + T)
+    Hq, H = 2 if T == 12 else 8, 2
+    G = Hq // H
+    kv = E.kvq_contiguous(1, Hq, H, D, 1, L + T, 32)
+    codes, scales = _buffers(kv, rng)
+    vc, vs = P.views(kv, codes, scales)
+    q = _bf16(rng, (1, T, Hq, D), 2.0)
+    see = _tree(rng, 1, T, [T]) if T > 1 else None
+    want, tol = P.attention(kv, T, q, vc, vs, 0, [L], see, None)
+    hit = np.zeros((T, Hq), bool)
+    if where == "q":
+        q[0, T - 1, Hq - 1, 5] = np.nan
+        hit[T - 1, Hq - 1] = True
+    else:
+        at = 3 if where == "prefix" else T // 2
+        vc[0, 0, 0, at if where == "prefix" else L + at, 1, 77] = 0x7F
+        hit[:, G:] = (np.ones(T, bool) if where == "prefix" else see[0, :, at])[:, None]
+    got, status = _attend(E, kv, T, [L], None, see, codes, scales, q, 0)
+    assert status == 0
+    got, want, tol = got[0], want[0], tol[0]
+    assert ((got[hit] == 0) | np.isnan(got[hit])).all()
+    assert (np.abs(got - want) <= tol)[~hit].all()
