@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 4 : 6) token_logprobs_kern
         }
         return;
     }
+    if (cpr > 1) cluster_started_arrive();
     const char* row = static_cast<const char*>(a.logits) +
                       (static_cast<size_t>(b) * a.rows_per_seq + slot) * static_cast<size_t>(a.V) * ES;
     const int first = rank * seg;                       // this CTA's elements [first, first + n)
@@ -411,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 4 : 6) token_logprobs_kern
     __syncthreads();
     // ---- the row's results in the cluster's leader ----
     cg::cluster_group cluster = cg::this_cluster();
+    if (cpr > 1) cluster_started_wait();
     Shared* lead = cpr > 1 ? cluster.map_shared_rank(&sm, 0) : &sm;
     if (tid < kMaxTopK) lead->rtop[rank * kMaxTopK + tid] = sm.ctop[tid];
     if (warp == 0) {

@@ -198,3 +198,15 @@ def test_extreme_temperatures(dtype, temperature):
         assert lp[0, 0] == 0 and ent[0, 0] == 0
     else:  # 3e38 / 1e30 = 3e8 over the others
         assert lp[0, 0] == 0 and abs(ent[0, 0]) <= 2.0 ** -16
+
+
+def test_rows_over_clusters_of_every_size_again_and_again():
+    """Rows split over 2, 4 and 8 CTAs, as short as they are split at all, so that the shares meet with little
+    work before; other values in every run."""
+    import torch
+    E = _E()
+    rng = np.random.default_rng(13)
+    for V in (8192, 16384, 32768):  # fp32: two, four and eight pieces of 16 KB
+        for run in range(40):
+            x = torch.from_numpy(rng.standard_normal((1, 5, V)).astype(np.float32) * 2.5).cuda()
+            _check(E, x, None, rng.integers(0, V, (1, 5)), 4, 1.0)
