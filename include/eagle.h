@@ -499,7 +499,7 @@ int eagle_lmhead_quant_pack(int vocab, int hidden_dim, int group, const void* we
  * alt_logprobs NaN, rank and alt_ids -1, no row read. A token >= V or a slot
  * >= rows_per_seq raises status 3 and gives padding values. Logits of -inf
  * have probability 0; a row with a NaN, a +inf or no finite logit raises
- * status 1. Of `cfg` only vocab and logit_dtype matter here, of `ws` the
+ * status 1 and gives padding values. Of `cfg` only vocab and logit_dtype matter here, of `ws` the
  * status word.
  */
 int eagle_token_logprobs(const eagle_tree_cfg* cfg, void* ws, size_t ws_bytes, int n_seq, int per_seq,

@@ -474,7 +474,14 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 4 : 6) token_logprobs_kern
         if (bad) raise_status(a.status, kDevNonFinite);
         a.logprob[entry] = bad ? NAN : ln_p(xt);
         if (a.entropy) a.entropy[entry] = bad ? NAN : lns - ln2 * (p.e / p.s);
-        if (a.rank) a.rank[entry] = p.above;
+        if (a.rank) a.rank[entry] = bad ? -1 : p.above;
+    }
+    if (bad) {  // NaN entries have no key: the alternatives of padding instead of what was there
+        if (tid < k) {
+            a.alt_ids[static_cast<size_t>(entry) * k + tid] = -1;
+            a.alt_logprobs[static_cast<size_t>(entry) * k + tid] = NAN;
+        }
+        return;
     }
     if (tid < cpr * kMaxTopK && k > 0) {
         const uint64_t key = sm.rtop[tid];
@@ -485,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 4 : 6) token_logprobs_kern
         }
         if (key != 0ull && r < k) {
             a.alt_ids[static_cast<size_t>(entry) * k + r] = static_cast<int32_t>(key_id(key));
-            a.alt_logprobs[static_cast<size_t>(entry) * k + r] = bad ? NAN : ln_p(key_val(key));
+            a.alt_logprobs[static_cast<size_t>(entry) * k + r] = ln_p(key_val(key));
         }
     }
     if (tid < k && tid >= a.V) {  // alternatives past the row's entries

@@ -210,3 +210,24 @@ def test_rows_over_clusters_of_every_size_again_and_again():
         for run in range(40):
             x = torch.from_numpy(rng.standard_normal((1, 5, V)).astype(np.float32) * 2.5).cuda()
             _check(E, x, None, rng.integers(0, V, (1, 5)), 4, 1.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("V", [64, 128256])
+def test_rows_without_a_distribution_give_status_1_and_padding_values(dtype, value, V):
+    """A row with one NaN or +inf, or with nothing but NaN, +inf or -inf: the status is 1, the row's outputs are
+    those of padding, none is left as it was, and the other row is unharmed."""
+    import torch
+    E = _E()
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    for everywhere in (False, True):
+        if value == float("-inf") and not everywhere:
+            continue  # a masked entry
+        x = torch.zeros(1, 2, V, device="cuda", dtype=dt)
+        x[0, 1, slice(None) if everywhere else V - 3] = value
+        (lp, rank, ent, ids, alts), status = _run(E, x, None, np.array([[1, 2]]), 4, 1.0)
+        assert status == 1
+        assert abs(lp[0, 0] + math.log(V)) < 2.0 ** -16 and rank[0, 0] == 1 and (ids[0, 0] == np.arange(4)).all()
+        assert math.isnan(lp[0, 1]) and math.isnan(ent[0, 1]) and rank[0, 1] == -1
+        assert (ids[0, 1] == -1).all() and np.isnan(alts[0, 1]).all()
