@@ -458,8 +458,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     x += s.x;
                     y += s.y;
                 }
-                x = x * 0x1p24f * fac[m];
-                y = y * 0x1p24f * fac[m];
+                // 2^24 / scale in two powers of two, of which neither leaves fp32's range before the logit does
+                const float f = fac[m], f0 = f < 1.0f ? f * 0x1p24f : 0x1p24f, f1 = f < 1.0f ? 1.0f : f;
+                x = x * f0 * f1;
+                y = y * f0 * f1;
                 const size_t o = static_cast<size_t>(m0 + m) * p.V + v + r;
                 if (BF16) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + o) = pack_bf16(x, y);
                 else *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o) = make_float2(x, y);

@@ -177,3 +177,23 @@ def test_rows_whose_plain_sums_overflow():
     got = _head(E, h, codes, scales, group, torch.float32)
     x = h.astype(np.float64)
     assert (np.abs(got - x @ w.T) <= H * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T)).all()
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_tiny_rows_under_huge_scales_and_the_reverse(out):
+    """Ordinary logits from hidden entries and scales far from 1, in either direction: nothing on the way overflows."""
+    import torch
+    E = _E()
+    rng = np.random.default_rng(23)
+    M, V, H, group = 5, 256, 512, 64
+    for e in (-110, -90, -60, 60, 90, 110):
+        h = P.bf16_round(rng.standard_normal((M, H)) * 2.0 ** e)
+        codes = rng.integers(0, 256, (V, H // 2)).astype(np.uint8)
+        scales = P.bf16_round(rng.uniform(1.0, 2.0, (V, H // group)) * 2.0 ** -e)
+        w = P.unpack_w4(codes, scales, group)
+        got = _head(E, h, codes, scales, group, torch.bfloat16 if out == "bf16" else torch.float32)
+        x = h.astype(np.float64)
+        tol = H * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T)
+        if out == "bf16":
+            tol = tol + 2.0 ** -8 * (np.abs(x @ w.T) + tol)
+        assert (np.abs(got - x @ w.T) <= tol).all(), e
