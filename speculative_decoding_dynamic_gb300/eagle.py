@@ -78,7 +78,7 @@ class KvqCfg(ctypes.Structure):
 
     @property
     def n_blocks(self) -> int:
-        return -(-self.max_len // self.block)
+        return -(-self.max_len // max(1, self.block))  # a block of 0 is the library's to refuse
 
     def extent(self, layers: int) -> tuple[int, int]:
         """Bytes of codes and elements of scales that `layers` layers of the cache span."""
@@ -86,7 +86,7 @@ class KvqCfg(ctypes.Structure):
         return (b * self.seq_stride + k * self.layer_stride + self.kv_stride + (max_len - 1) * self.pos_stride +
                 heads * self.head_dim,
                 b * self.scale_seq_stride + k * self.scale_layer_stride + self.scale_kv_stride +
-                (-(-max_len // self.block) - 1) * self.scale_block_stride + heads)
+                (self.n_blocks - 1) * self.scale_block_stride + heads)
 
 
 _p = ctypes.c_void_p
@@ -342,7 +342,7 @@ def eagle_kv_compact(kv, kv_cache, prefix_len, accept_len, accepted_slots, slots
 def kvq_contiguous(batch, n_q_heads, n_kv_heads, head_dim, layers, max_len, block) -> KvqCfg:
     """The 8-bit cache with codes [batch, layers, 2, max_len, n_kv_heads, head_dim] and scales
     [batch, layers, 2, ceil(max_len / block), n_kv_heads], both contiguous."""
-    row, nb = n_kv_heads * head_dim, -(-max_len // block)
+    row, nb = n_kv_heads * head_dim, -(-max_len // max(1, block))
     return KvqCfg(batch, n_q_heads, n_kv_heads, head_dim, layers, max_len, block, EAGLE_BF16,
                   layers * 2 * max_len * row, 2 * max_len * row, max_len * row, row,
                   layers * 2 * nb * n_kv_heads, 2 * nb * n_kv_heads, nb * n_kv_heads, n_kv_heads)

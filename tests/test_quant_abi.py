@@ -162,3 +162,22 @@ def test_plain_e4m3_rounding():
         assert P.block_scale(448.0 * 2.0 ** e) == 2.0 ** e
         assert P.block_scale(np.nextafter(448.0, 500) * 2.0 ** e) == 2.0 ** (e + 1)
     assert P.block_scale(0.0) == 2.0 ** -126
+
+
+@pytest.mark.parametrize("kw,code", BAD_CFG)
+def test_binding_leaves_a_bad_cache_description_to_the_library(E, kw, code):
+    kv = _kv(E, **kw)
+
+    class Ws:  # a workspace's address and size
+        def data_ptr(self): return PTR
+        def numel(self): return 1 << 40
+        def element_size(self): return 1
+
+    for call in (lambda: E.eagle_kvq_store(kv, 0, 4, PTR, PTR, 256, None, PTR, None, PTR, PTR, None, 0),
+                 lambda: E.eagle_kvq_compact(kv, PTR, PTR, PTR, PTR, PTR, 7, PTR, None, 0),
+                 lambda: E.eagle_kvq_tree_attention(kv, 4, PTR, PTR, PTR, 0, PTR, None, None, PTR, Ws(), 0)):
+        with pytest.raises(E.EagleError) as e:
+            call()
+        assert e.value.code == code
+    empty = E.kvq_contiguous(2, 8, 2, 128, 3, 256, 0)
+    assert E.eagle_kvq_attention_workspace_bytes(empty, 4) == 0
