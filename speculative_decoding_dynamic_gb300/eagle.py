@@ -181,6 +181,15 @@ def _need(fn: str, name: str, t, dtypes, n: int, dev: int) -> int | None:
     raise ValueError(f"{fn}: {name} has {t.numel()} elements, needs {n}")
 
 
+def _ws_on(fn: str, ws, dev: int) -> tuple[int | None, int]:
+    """Address and bytes of a workspace argument of `fn`, checked like its other tensors (kernels write its status
+    word); None and a raw address, as a call that needs the status word alone takes it, have no bytes."""
+    if isinstance(ws, torch.Tensor):
+        size = ws.element_size()
+        return _need(fn, "ws", ws, (ws.dtype,), -(-4 // size), dev), ws.numel() * size
+    return (ws, 0) if ws is None or isinstance(ws, int) else _ws(ws)
+
+
 _get_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
@@ -372,7 +381,7 @@ def eagle_kvq_store(kv, layer, T, k, v, row_stride, row_start, start, count, cod
                                     _need(fn, "row_start", row_start, _I32, B, dev),
                                     _need(fn, "start", start, _I32, B, dev), _need(fn, "count", count, _I32, B, dev),
                                     _need(fn, "codes", codes, _CODES, n_codes, dev),
-                                    _need(fn, "scales", scales, _F32, n_scales, dev), _ptr(ws),
+                                    _need(fn, "scales", scales, _F32, n_scales, dev), _ws_on(fn, ws, dev)[0],
                                     _stream_on(stream, dev)))
 
 
@@ -385,7 +394,7 @@ def eagle_kvq_compact(kv, codes, scales, prefix_len, accept_len, accepted_slots,
                                       _need(fn, "prefix_len", prefix_len, _I32, B, dev),
                                       _need(fn, "accept_len", accept_len, _I32, B, dev),
                                       _need(fn, "accepted_slots", accepted_slots, _I32, B * slots_stride, dev),
-                                      slots_stride, _need(fn, "new_len", new_len, _I32, B, dev), _ptr(ws),
+                                      slots_stride, _need(fn, "new_len", new_len, _I32, B, dev), _ws_on(fn, ws, dev)[0],
                                       _stream_on(stream, dev)))
 
 
@@ -404,7 +413,7 @@ def eagle_kvq_tree_attention(kv, T, q, codes, scales, layer, prefix_len, mask, n
                                              _need(fn, "prefix_len", prefix_len, _I32, B, dev),
                                              _need(fn, "mask", mask, _W32, B * T * ((T + 31) // 32), dev),
                                              _need(fn, "n_tree", n_tree, _I32, B, dev),
-                                             _need(fn, "out", out, _BF16, n, dev), *_ws(ws), _stream_on(stream, dev)))
+                                             _need(fn, "out", out, _BF16, n, dev), *_ws_on(fn, ws, dev), _stream_on(stream, dev)))
 
 
 def _logit_dtypes(cfg):
@@ -415,7 +424,7 @@ def eagle_lmhead_quant(cfg, ws, hidden_dim, group, hidden, codes, scales, draft_
     """LM-head logits from 4-bit weights with group scales (eagle_lmhead_quant_pack)."""
     fn, dev, M = "eagle_lmhead_quant", _device(), cfg.batch * cfg.top_k
     n = cfg.vocab * hidden_dim
-    _check(fn, _lib.eagle_lmhead_quant(ctypes.byref(cfg), *_ws(ws), hidden_dim, group,
+    _check(fn, _lib.eagle_lmhead_quant(ctypes.byref(cfg), *_ws_on(fn, ws, dev), hidden_dim, group,
                                        _need(fn, "hidden", hidden, _BF16, M * hidden_dim, dev),
                                        _need(fn, "codes", codes, _U8, n // 2, dev),
                                        _need(fn, "scales", scales, _BF16, n // max(1, group), dev),
@@ -436,7 +445,7 @@ def eagle_token_logprobs(cfg, ws, n_seq, per_seq, rows_per_seq, logits, temperat
     """Log-probability, rank, entropy and top alternatives of given tokens (slots None: entry j reads row j)."""
     fn, dev, n = "eagle_token_logprobs", _device(), n_seq * per_seq
     rows = n_seq * rows_per_seq * cfg.vocab
-    _check(fn, _lib.eagle_token_logprobs(ctypes.byref(cfg), *_ws(ws), n_seq, per_seq, rows_per_seq,
+    _check(fn, _lib.eagle_token_logprobs(ctypes.byref(cfg), *_ws_on(fn, ws, dev), n_seq, per_seq, rows_per_seq,
                                          _need(fn, "logits", logits, _logit_dtypes(cfg), rows, dev), float(temperature),
                                          _need(fn, "slots", slots, _I32, n, dev), _need(fn, "tokens", tokens, _I32, n, dev),
                                          n_alt, _need(fn, "logprob", logprob, _F32, n, dev),

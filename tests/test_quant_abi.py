@@ -181,3 +181,20 @@ def test_binding_leaves_a_bad_cache_description_to_the_library(E, kw, code):
         assert e.value.code == code
     empty = E.kvq_contiguous(2, 8, 2, 128, 3, 256, 0)
     assert E.eagle_kvq_attention_workspace_bytes(empty, 4) == 0
+
+
+def test_binding_refuses_a_workspace_that_is_not_on_the_current_device(E):
+    """Kernels write the status word: a workspace in host memory (or on another GPU) is refused like any other tensor."""
+    import torch
+    kv, cfg = _kv(E), _cfg(E)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    for call in (lambda: E.eagle_kvq_store(kv, 0, 4, PTR, PTR, 256, None, PTR, None, PTR, PTR, ws, 0),
+                 lambda: E.eagle_kvq_compact(kv, PTR, PTR, PTR, PTR, PTR, 7, PTR, ws, 0),
+                 lambda: E.eagle_kvq_tree_attention(kv, 4, PTR, PTR, PTR, 0, PTR, None, None, PTR, ws, 0),
+                 lambda: E.eagle_lmhead_quant(cfg, ws, 256, 128, PTR, PTR, PTR, PTR, 0),
+                 lambda: E.eagle_token_logprobs(cfg, ws, 3, 7, 61, PTR, 1.0, PTR, PTR, 0, PTR, stream=0)):
+        with pytest.raises(ValueError, match="ws is on cpu"):
+            call()
+    with pytest.raises(E.EagleError) as e:
+        E.eagle_lmhead_quant(cfg, None, 256, 128, PTR, PTR, PTR, PTR, 0)
+    assert e.value.code == -4
