@@ -26,6 +26,8 @@ class DeviceCycle:
 
     def __init__(self, cfg: E.TreeCfg, kv: E.KvCfg | E.KvqCfg, device="cuda", fused_head: bool = False,
                  n_alt: int | None = None):
+        if n_alt is not None and not 0 <= n_alt <= E.MAX_TOPK:
+            raise ValueError(f"DeviceCycle: n_alt {n_alt} is not 0..{E.MAX_TOPK}")
         self.cfg, self.kv = cfg, kv
         self.fused_head = fused_head
         self.quant_kv = isinstance(kv, E.KvqCfg)
@@ -131,6 +133,8 @@ class DeviceCycle:
 
     def logprobs(self, target, temperature=1.0, stream=None):
         """Log-probability, rank, entropy and n_alt alternatives of the accepted tokens and the bonus (after verify)."""
+        if self.n_alt is None:
+            raise ValueError("DeviceCycle.logprobs: the cycle was made without log-probabilities (n_alt)")
         cfg = self.cfg
         E.eagle_token_logprobs(cfg, self.ws, cfg.batch, cfg.depth + 1, cfg.T, target, temperature, self.slots,
                                self.out_tokens, self.n_alt, self.logprob, self.rank, self.entropy,

@@ -198,3 +198,14 @@ def test_binding_refuses_a_workspace_that_is_not_on_the_current_device(E):
     with pytest.raises(E.EagleError) as e:
         E.eagle_lmhead_quant(cfg, None, 256, 128, PTR, PTR, PTR, PTR, 0)
     assert e.value.code == -4
+
+
+def test_cycle_refuses_log_probabilities_it_has_no_buffers_for(E):
+    from speculative_decoding_dynamic_gb300 import cycle as C
+    cfg, kv = _cfg(E), E.kvq_contiguous(2, 2, 2, 128, 1, 16, 16)
+    with pytest.raises(ValueError, match="n_alt"):
+        C.DeviceCycle(cfg, kv, device="cpu").logprobs(None)
+    for n_alt in (-1, 17):
+        with pytest.raises(ValueError, match="n_alt"):
+            C.DeviceCycle(cfg, kv, device="cpu", n_alt=n_alt)
+    assert C.DeviceCycle(cfg, kv, device="cpu", n_alt=16).alt_ids.shape == (2, 2, 16)
