@@ -107,12 +107,15 @@ class DeviceCycle:
         E.eagle_build_tree(self.cfg, self.ws, prefix_len, root_token, self.tokens, self.parent, self.depth, self.pos,
                            self.mask, self.n_tree, stream)
 
+    def _need_quant_kv(self):
+        if not self.quant_kv:
+            raise ValueError("DeviceCycle.store: only the 8-bit cache (a KvqCfg) is written here")
+
     def store(self, k, v, cache, layer, prefix_len, stream=None):
         """The tree's K and V of a layer into the 8-bit cache: k, v [B, T, Hkv, 128] bf16, tree slot j
         of a sequence at position prefix_len + j (slots past n_tree are not written)."""
         kv = self.kv
-        if not self.quant_kv:
-            raise ValueError("DeviceCycle.store: only the 8-bit cache (a KvqCfg) is written here")
+        self._need_quant_kv()
         E.eagle_kvq_store(kv, layer, self.cfg.T, k, v, kv.n_kv_heads * kv.head_dim, None, prefix_len, self.n_tree,
                           *cache, ws=self.ws, stream=stream)
 
@@ -153,6 +156,8 @@ class DeviceCycle:
             compact=True, stream=None, head=None, new_kv=None):
         """The whole cycle (all stages) enqueued on `stream`. new_kv: optional (k, v) of the tree's
         slots, stored in the 8-bit cache first. Log-probabilities are at the verification's temperature (greedy: 1)."""
+        if new_kv is not None:
+            self._need_quant_kv()  # before the first launch
         self.draft(draft_logits, stream, head=head)
         self.build(prefix_len, root_token, stream)
         if new_kv is not None:

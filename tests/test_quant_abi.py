@@ -209,3 +209,14 @@ def test_cycle_refuses_log_probabilities_it_has_no_buffers_for(E):
         with pytest.raises(ValueError, match="n_alt"):
             C.DeviceCycle(cfg, kv, device="cpu", n_alt=n_alt)
     assert C.DeviceCycle(cfg, kv, device="cpu", n_alt=16).alt_ids.shape == (2, 2, 16)
+
+
+def test_cycle_refuses_new_rows_for_the_16_bit_cache_before_its_first_launch(E):
+    from speculative_decoding_dynamic_gb300 import cycle as C
+    row = 2 * 128
+    kv = E.KvCfg(2, 2, 2, 128, 1, 16, E.EAGLE_BF16, 2 * 16 * row, 2 * 16 * row, 16 * row, row)
+    dc = C.DeviceCycle(_cfg(E), kv, device="cpu")
+    n = E.eagle_kernel_launches()
+    with pytest.raises(ValueError, match="8-bit cache"):
+        dc.run(PTR, PTR, PTR, PTR, PTR, 0, PTR, 0, 0, E.GREEDY, stream=0, new_kv=(PTR, PTR))
+    assert E.eagle_kernel_launches() == n
