@@ -204,7 +204,7 @@ struct Divisor {
 };
 constexpr int kSplitThreads = 256, kSplitPer = 2, kSplitRows = kSplitPer * kSplitThreads / 16;
 __global__ void __launch_bounds__(kSplitThreads)
-    kvq_split_q_kernel(const __nv_bfloat16* __restrict__ q, uint2* __restrict__ dst, float* __restrict__ fac, KvqRows rows,
+    kvq_split_q_kernel(const __nv_bfloat16* q, uint2* __restrict__ dst, float* __restrict__ fac, KvqRows rows,
                        Divisor by_Hq, Divisor by_T, Divisor by_G, int Hkv, uint32_t n, float scale_log2, KvqSched sched,
                        KvqCursor* __restrict__ cursors) {
     pdl_wait_prior();
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kSplitThreads)
 #pragma unroll
     for (int e = 0; e < kSplitPer; ++e) {
         const uint32_t i = i0 + e * (kSplitThreads / 16);
-        u[e] = i < n ? __ldg(reinterpret_cast<const uint4*>(q) + static_cast<size_t>(i) * (kHD / 8) + l16) : make_uint4(0u, 0u, 0u, 0u);
+        u[e] = i < n ? ld_prior(reinterpret_cast<const uint4*>(q) + static_cast<size_t>(i) * (kHD / 8) + l16) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int e = 0; e < kSplitPer; ++e) {
@@ -318,6 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    // Of what this kernel reads, only the split of q's results (q's parts and factors, the cursors) were written
+    // since its launch: the split lets it start behind its own wait. The rest may be read by __ldg.
     pdl_wait_prior();
     pdl_launch_dependents();
     KvqCursor cur;
@@ -357,11 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         KvqPiece ahead;
-        bool more = cur.next(p.s, ahead);
+        bool more = cur.next<true>(p.s, ahead);
         if (more) copy_q(ahead, 0);
         for (; uniform(more); ++qi) {
             it = ahead;
-            more = cur.next(p.s, ahead);
+            more = cur.next<true>(p.s, ahead);
             const int hk = uniform(it.sub / p.n_items), b = uniform(it.b), j1 = uniform(it.t1), j0 = uniform(it.t0);
             for (int j = j0; j < j1; ++j, ++t) {
                 if (t >= kKStages) wait.both(&bar_k_empty[sk], pk ^ 1, &bar_v8_empty[sv], pv ^ 1);
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (role < 2) {
             constexpr uint32_t id_qk = idesc_type0(kBM, kBN, 0);
             for (int qi = 0;; ++qi) {
-                const bool more = cur.next(p.s, it);
+                const bool more = cur.next<true>(p.s, it);
                 if (!uniform(more)) break;
                 const int n_tiles = uniform(it.t1 - it.t0);
                 const bool live = uniform((it.sub % p.n_items) * 2 + g) < n_blocks;
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
             constexpr uint32_t id_pv = idesc_type0(kBM, kHD, 1);
             for (;;) {
-                const bool more = cur.next(p.s, it);
+                const bool more = cur.next<true>(p.s, it);
                 if (!uniform(more)) break;
                 const int n_tiles = uniform(it.t1 - it.t0);
                 const bool live = uniform((it.sub % p.n_items) * 2 + g) < n_blocks;
@@ -494,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int cw = warp - kWarpConv;
         const uint32_t base = smem_u32(smem);
         int t = 0, st = 0, ph = 0;  // the stage of codes and its phase
-        while (cur.next(p.s, it))
+        while (cur.next<true>(p.s, it))
             for (int j = it.t0; j < it.t1; ++j, ++t) {
                 const int b = t & 1;
                 if (t >= 2) wait.both(&bar_v_empty[b], (t >> 1) - 1, &bar_v8_full[st], ph);
@@ -561,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&bar_sc[slot]);
             __syncwarp();
         };
-        while (cur.next(p.s, it)) {
+        while (cur.next<true>(p.s, it)) {
             const int hk = it.sub / p.n_items;
             const float* src = (lane < kSub ? p.k_scale : p.v_scale) + it.b * p.s_seq + hk;
             const int last = (it.nkeys - 1) >> p.blk_shift;
@@ -594,12 +596,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto next_piece = [&]() {
             KvqCursor c = own;
             __syncwarp();
-            const bool more = c.next(p.s, it);
+            const bool more = c.next<true>(p.s, it);
             if (lane == 0) own = c;
             __syncwarp();
             return more;
         };
-        kvq_zero_bad(p.s, p.Hq, p.out, p.status, worker, threadIdx.x - kWarpSoftmax * 32, kSoftmaxWarps * 32);
+        kvq_zero_bad<true>(p.s, p.Hq, p.out, p.status, worker, threadIdx.x - kWarpSoftmax * 32, kSoftmaxWarps * 32);
         while (next_piece()) {
             if (it.np) cut = kvq_cut(it);
             const int hk = it.sub / p.n_items, block = (it.sub - hk * p.n_items) * 2 + g;
@@ -617,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 p.mask ? p.mask + (static_cast<size_t>(it.b) * p.s.T + (row_live ? slot : 0)) * p.W : nullptr;
             const int L = it.L, n = it.n;
             const float fac =
-                row_live ? __ldg(p.q_fac + (static_cast<size_t>(it.b) * p.Hkv + hk) * rows + block * kBM + r) : 0.0f;
+                row_live ? ld_prior(p.q_fac + (static_cast<size_t>(it.b) * p.Hkv + hk) * rows + block * kBM + r) : 0.0f;
             // word w of the row's mask
             auto word = [&](int w) {
                 if (w >= p.W) return 0u;

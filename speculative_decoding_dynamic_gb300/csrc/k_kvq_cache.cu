@@ -23,6 +23,10 @@ namespace {
 constexpr int kD = kKvqHeadDim;
 constexpr int kStoreThreads = 256;
 
+// The kernels' inputs are not __restrict__: a const __restrict__ input may be
+// read like one by __ldg, which wants data that nothing writes while the grid
+// runs, and under programmatic launch the kernel that writes it may still run.
+
 // The smallest power of two s >= 2^-126 with amax <= 448 s, amax finite.
 // 448 = 1.75 * 2^8: the exponent of amax less 8, one more when its fraction
 // is above 1.75.
@@ -62,9 +66,9 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
 // 71.4 us, 6.5 TB/s; 64 trees of 61 slots of 8 heads (24 MB) 5.6 us.
 template <int BLK>
 __global__ void __launch_bounds__(kStoreThreads) kvq_store_kernel(
-    KvqDims kv, int layer, int T, int nhg, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
-    int64_t row_stride, const int32_t* __restrict__ row_start, const int32_t* __restrict__ start,
-    const int32_t* __restrict__ count, unsigned char* __restrict__ codes, float* __restrict__ scales, int* status) {
+    KvqDims kv, int layer, int T, int nhg, const __nv_bfloat16* k, const __nv_bfloat16* v,
+    int64_t row_stride, const int32_t* row_start, const int32_t* start,
+    const int32_t* count, unsigned char* __restrict__ codes, float* __restrict__ scales, int* status) {
     constexpr int GT = 2 * BLK;                 // threads of a group
     constexpr int GROUPS = kStoreThreads / GT;  // groups (heads) per CTA
     constexpr int ROWS = BLK / 8;               // rows per pass
@@ -192,8 +196,8 @@ __device__ __forceinline__ uint4 rescale16(const uint4& u, float ratio) {
 // of 64 with 32 layers into one wave (one head per warp: 16.8 us; four: 9.1, and
 // 2.8 us for one sequence).
 __global__ void __launch_bounds__(kMoveWarps * 32) kvq_compact_kernel(
-    KvqDims kv, unsigned char* __restrict__ codes, float* __restrict__ scales, const int32_t* __restrict__ prefix_len,
-    const int32_t* __restrict__ accept_len, const int32_t* __restrict__ slots, int slots_stride,
+    KvqDims kv, unsigned char* __restrict__ codes, float* __restrict__ scales, const int32_t* prefix_len,
+    const int32_t* accept_len, const int32_t* slots, int slots_stride,
     int32_t* __restrict__ new_len, int* status) {
     const int b = blockIdx.z;
     const int layer = blockIdx.y >> 1, which = blockIdx.y & 1;

@@ -138,11 +138,11 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1)
             if (r < rows) {
                 const uint4* src = reinterpret_cast<const uint4*>(
                     p.q + ((static_cast<size_t>(it.b) * p.s.T + slot) * p.Hq + hk * p.G + (r - slot * p.G)) * kKvqHeadDim);
-                u[0] = __ldg(src + 2 * t);
-                u[1] = __ldg(src + 2 * t + 1);
-                u[2] = __ldg(src + 8 + 2 * t);
-                u[3] = __ldg(src + 8 + 2 * t + 1);
-                vis = p.mask ? __ldg(&p.mask[static_cast<size_t>(it.b) * p.s.T + slot]) : (2u << slot) - 1u;
+                u[0] = ld_prior(src + 2 * t);
+                u[1] = ld_prior(src + 2 * t + 1);
+                u[2] = ld_prior(src + 8 + 2 * t);
+                u[3] = ld_prior(src + 8 + 2 * t + 1);
+                vis = p.mask ? ld_prior(&p.mask[static_cast<size_t>(it.b) * p.s.T + slot]) : (2u << slot) - 1u;
                 vis &= (1u << it.n) - 1u;  // n <= 16
             }
             float am = fmaxf(fmaxf(absmax8(u[0]), absmax8(u[1])), fmaxf(absmax8(u[2]), absmax8(u[3])));
@@ -183,8 +183,8 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int64_t at = min((step * kStep + 16 * e) >> p.blk_shift, last) * p.s_blk;
-                kc[e] = __ldg(ks + at);
-                vc[e] = __ldg(vs + at);
+                kc[e] = ld_prior(ks + at);
+                vc[e] = ld_prior(vs + at);
             }
         };
         scales(it.t0);

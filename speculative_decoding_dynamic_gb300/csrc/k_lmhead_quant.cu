@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
             if (32 * k >= pieces) break;
-            u[k] = 32 * k + lane < pieces ? __ldg(src + 32 * k + lane) : make_uint4(0u, 0u, 0u, 0u);
+            u[k] = 32 * k + lane < pieces ? ld_prior(src + 32 * k + lane) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int v = v0 + r_tile * RT, last = max(0, (p.V - 1 - v - g) >> 3);
             const __nv_bfloat16* src = p.scales + (static_cast<size_t>(v + g) * p.n_slice + r_slice) * NG;
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) next[i] = __ldg(reinterpret_cast<const Scales*>(src + min(i, last) * 8 * p.n_slice * NG));
+            for (int i = 0; i < 2 * MT; ++i) next[i] = ld_prior(reinterpret_cast<const Scales*>(src + min(i, last) * 8 * p.n_slice * NG));
             r_slice += kMmaWarps;
             if (r_slice >= p.n_slice) {
                 r_slice = warp;
@@ -531,7 +531,7 @@ cudaError_t launch_group(const QuantParams& p, int group, bool bf16, const void*
 // ------------------------------------------------------------------- pack ---
 
 // One lane per eight entries; group / 8 neighbouring lanes share a scale.
-__global__ void __launch_bounds__(256) lmhead_quant_pack_kernel(long pieces, int group, const uint4* __restrict__ weight,
+__global__ void __launch_bounds__(256) lmhead_quant_pack_kernel(long pieces, int group, const uint4* weight,
                                                                 uint32_t* __restrict__ codes,
                                                                 __nv_bfloat16* __restrict__ scales) {
     pdl_launch_dependents();

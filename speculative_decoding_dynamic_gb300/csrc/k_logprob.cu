@@ -35,6 +35,7 @@
 #include <cmath>
 
 #include "eagle_internal.cuh"
+#include "quant_ptx.cuh"
 #include "quant_ws.h"
 
 namespace eagle {
@@ -198,8 +199,8 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 4 : 6) token_logprobs_kern
     const int nch = (n + CE - 1) / CE;
     const uint4* vec = reinterpret_cast<const uint4*>(row + static_cast<size_t>(first) * ES);
     const int nvec = n / EPV;
-    const float xt = DT == 1 ? __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(row) + tok)) << 16)
-                             : __ldg(reinterpret_cast<const float*>(row) + tok);
+    const float xt = DT == 1 ? __uint_as_float(static_cast<uint32_t>(ld_prior(reinterpret_cast<const unsigned short*>(row) + tok)) << 16)
+                             : ld_prior(reinterpret_cast<const float*>(row) + tok);
     // x >= xt as x > xt_below, the next value down (both zeros are one value)
     const float xt_below = xt == 0.0f ? __uint_as_float(0x80000001u) : o2f(f2o(xt) - 1u);
     if (tid == 0) {
@@ -218,11 +219,11 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 4 : 6) token_logprobs_kern
         const uint4* in = vec + ch * kVecs * kThreads + tid;
         if ((ch + 1) * kVecs * kThreads <= nvec) {
 #pragma unroll
-            for (int q = 0; q < kVecs; ++q) u[q] = __ldg(in + q * kThreads);
+            for (int q = 0; q < kVecs; ++q) u[q] = ld_prior(in + q * kThreads);
         } else {
             const int v0 = ch * kVecs * kThreads + tid;
 #pragma unroll
-            for (int q = 0; q < kVecs; ++q) u[q] = v0 + q * kThreads < nvec ? __ldg(in + q * kThreads) : neg_inf<DT>();
+            for (int q = 0; q < kVecs; ++q) u[q] = v0 + q * kThreads < nvec ? ld_prior(in + q * kThreads) : neg_inf<DT>();
         }
     };
     auto group = [&](int ch, const uint4 (&u)[kVecs]) {
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 4 : 6) token_logprobs_kern
                 const int at = static_cast<int>(sm.groups[i / kVecs]);
                 const int v = (at / kThreads * kVecs + i % kVecs) * kThreads + at % kThreads;
                 if (v >= nvec) continue;
-                const uint4 u = __ldg(vec + v);
+                const uint4 u = ld_prior(vec + v);
 #pragma unroll
                 for (int e = 0; e < EPV; ++e) {
                     const float x = element<DT>(u, e);
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 4 : 6) token_logprobs_kern
                     for (int q = 0; q < kVecs; ++q) {
                         const int v = (ch * kVecs + q) * kThreads + tid;
                         if (v >= nvec) break;
-                        const uint4 u = __ldg(vec + v);
+                        const uint4 u = ld_prior(vec + v);
 #pragma unroll
                         for (int e = 0; e < EPV; ++e) {
                             const float x = element<DT>(u, e);
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 4 : 6) token_logprobs_kern
         // the clamp hides its differences, so the leader sums it again as it is.
         float s = 0.0f, e = 0.0f;
         for (int v = tid; v < a.V / EPV; v += kThreads) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(row) + v);
+            const uint4 u = ld_prior(reinterpret_cast<const uint4*>(row) + v);
 #pragma unroll
             for (int i = 0; i < EPV; ++i) {
                 const float y = (element<DT>(u, i) - m) * c, w = ex2_approx(y);

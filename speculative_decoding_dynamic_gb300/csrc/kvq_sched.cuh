@@ -41,10 +41,15 @@ __device__ __forceinline__ int kvq_units(const KvqSched& s, int nt, bool last) {
     return s.ov + nt * (last ? s.cost_last : s.cost);
 }
 
+// SETTLED: the lengths were written before this grid was launched (the
+// tensor-core kernel's, behind the split of q, which lets it start only once its
+// own wait is over), so that __ldg may read them.
+template <bool SETTLED = false>
 __device__ __forceinline__ KvqSeq kvq_seq(const KvqSched& s, int b) {
+    auto load = [](const int32_t* p) { return SETTLED ? __ldg(p) : ld_prior(p); };
     KvqSeq q;
-    q.L = __ldg(&s.prefix_len[b]);
-    q.n = s.n_tree ? __ldg(&s.n_tree[b]) : s.T;
+    q.L = load(&s.prefix_len[b]);
+    q.n = s.n_tree ? load(&s.n_tree[b]) : s.T;
     const bool bad = q.L < 0 || q.L > s.max_len - s.T || q.n < 1 || q.n > s.T;
     q.nkeys = bad ? 0 : q.L + q.n;
     q.nt = (q.nkeys + s.step - 1) / s.step;
@@ -144,12 +149,13 @@ struct alignas(16) KvqCursor {
             q = kvq_seq(s, b);
         }
     }
+    template <bool SETTLED = false>
     __device__ __forceinline__ bool next(const KvqSched& s, KvqPiece& p) {
         while (pos < end) {
             const long long seq_end = base + q.len * s.heads;
             if (pos >= seq_end) {  // the next sequence with keys (one exists: pos < end <= total)
                 base = seq_end;
-                do q = kvq_seq(s, ++b);
+                do q = kvq_seq<SETTLED>(s, ++b);
                 while (q.nt == 0);
                 continue;
             }
@@ -236,10 +242,11 @@ cudaError_t launch_kvq_merge_decode(const KvqMergeParams& p, cudaStream_t stream
 
 // Zero rows of the sequences whose lengths are out of range (status 3), dealt
 // over the workers: `n` threads of a worker, this one the i-th.
+template <bool SETTLED = false>
 __device__ __forceinline__ void kvq_zero_bad(const KvqSched& s, int Hq, __nv_bfloat16* out, int* status, int worker,
                                              int i, int n) {
     for (int b = worker; b < s.B; b += s.workers) {
-        if (kvq_seq(s, b).nt != 0) continue;
+        if (kvq_seq<SETTLED>(s, b).nt != 0) continue;
         if (i == 0) raise_status(status, kDevBadIndex);
         uint4* o = reinterpret_cast<uint4*>(out + static_cast<size_t>(b) * s.T * Hq * kKvqHeadDim);
         const int nv = s.T * Hq * kKvqHeadDim / 8;

@@ -5,6 +5,16 @@
 
 namespace eagle {
 
+// An ordinary load of data that an earlier kernel of the stream may have
+// written. Not __ldg: that promises that nothing writes the data while this
+// grid runs, and a grid launched with programmatic serialisation runs before
+// the earlier kernel has ended (pdl_wait_prior), so its loads could be taken
+// from before the wait.
+template <typename V>
+__device__ __forceinline__ V ld_prior(const V* p) {
+    return *p;
+}
+
 // The power of two that brings a row's largest element amax into [2^to, 2^(to + 1)).
 __device__ __forceinline__ float pow2_to(float amax, int to) {
     const int e = static_cast<int>(__float_as_uint(amax) >> 23);  // biased; 0 for zero and subnormals

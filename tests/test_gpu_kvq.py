@@ -598,3 +598,37 @@ def test_attention_nan_in_k_or_q_reaches_the_rows_that_see_it_only(T, L, where):
     got, want, tol = got[0], want[0], tol[0]
     assert ((got[hit] == 0) | np.isnan(got[hit])).all()
     assert (np.abs(got - want) <= tol)[~hit].all()
+
+
+def test_decode_steps_issued_back_to_back():
+    """Sixty decode steps, store then attention, with nothing in between that waits: each attention reads the codes,
+    the scales (which grow in most steps) and the lengths as the calls just before it left them."""
+    import torch
+    E = _E()
+    rng = np.random.default_rng(70)
+    B, Hq, H, steps = 3, 8, 2, 60
+    kv = E.kvq_contiguous(B, Hq, H, D, 1, 700, 32)
+    codes, scales = _buffers(kv, rng)
+    vc, vs = P.views(kv, codes, scales)
+    dc, ds = _dev(codes), _dev(scales)
+    start = np.array([0, 30, 600])
+    grow = (1.12 ** np.arange(steps))[:, None, None, None, None]
+    rows, q = _bf16(rng, (steps, 2, B, H, D), 0.1) * grow, _bf16(rng, (steps, B, 1, Hq, D))
+    rows = P.bf16_round(rows)
+    d_rows, d_q = _dev_bf16(rows), _dev_bf16(q)
+    out = torch.full((steps, B, 1, Hq, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    d_start, one = _dev(start.astype(np.int32)), torch.ones(B, dtype=torch.int32, device="cuda")
+    ws = E.alloc_workspace(E.eagle_kvq_attention_workspace_bytes(kv, 1))
+    torch.cuda.synchronize()
+    for s in range(steps):
+        E.eagle_kvq_store(kv, 0, 1, d_rows[s, 0], d_rows[s, 1], H * D, None, d_start, None, dc, ds, ws)
+        E.eagle_kvq_tree_attention(kv, 1, d_q[s], dc, ds, 0, d_start, None, None, out[s], ws)
+        d_start.add_(one)
+    torch.cuda.synchronize()
+    assert E.eagle_status_fetch(ws) == 0
+    got = out.float().cpu().numpy()
+    for s in range(steps):
+        P.store(kv, 0, 1, rows[s, 0], rows[s, 1], None, start + s, None, vc, vs)
+        want, tol = P.attention(kv, 1, q[s], vc, vs, 0, start + s, None, None)
+        assert (np.abs(got[s] - want) <= tol).all(), s
+    assert (ds.cpu().numpy() == scales).all() and (dc.cpu().numpy() == codes).all()
