@@ -78,7 +78,7 @@ class KvqCfg(ctypes.Structure):
 
     @property
     def n_blocks(self) -> int:
-        return -(-self.max_len // max(1, self.block))  # a block of 0 is the library's to refuse
+        return -(-self.max_len // (self.block or 1))  # a block of 0 is the library's to refuse
 
     def extent(self, layers: int) -> tuple[int, int]:
         """Bytes of codes and elements of scales that `layers` layers of the cache span."""
@@ -86,7 +86,7 @@ class KvqCfg(ctypes.Structure):
         return (b * self.seq_stride + k * self.layer_stride + self.kv_stride + (max_len - 1) * self.pos_stride +
                 heads * self.head_dim,
                 b * self.scale_seq_stride + k * self.scale_layer_stride + self.scale_kv_stride +
-                (self.n_blocks - 1) * self.scale_block_stride + heads)
+                (-(-max_len // (self.block or 1)) - 1) * self.scale_block_stride + heads)
 
 
 _p = ctypes.c_void_p
@@ -381,8 +381,8 @@ def eagle_kvq_store(kv, layer, T, k, v, row_stride, row_start, start, count, cod
                                     _need(fn, "row_start", row_start, _I32, B, dev),
                                     _need(fn, "start", start, _I32, B, dev), _need(fn, "count", count, _I32, B, dev),
                                     _need(fn, "codes", codes, _CODES, n_codes, dev),
-                                    _need(fn, "scales", scales, _F32, n_scales, dev), _ws_on(fn, ws, dev)[0],
-                                    _stream_on(stream, dev)))
+                                    _need(fn, "scales", scales, _F32, n_scales, dev),
+                                    None if ws is None else _ws_on(fn, ws, dev)[0], _stream_on(stream, dev)))
 
 
 def eagle_kvq_compact(kv, codes, scales, prefix_len, accept_len, accepted_slots, slots_stride, new_len, ws=None,
@@ -394,8 +394,8 @@ def eagle_kvq_compact(kv, codes, scales, prefix_len, accept_len, accepted_slots,
                                       _need(fn, "prefix_len", prefix_len, _I32, B, dev),
                                       _need(fn, "accept_len", accept_len, _I32, B, dev),
                                       _need(fn, "accepted_slots", accepted_slots, _I32, B * slots_stride, dev),
-                                      slots_stride, _need(fn, "new_len", new_len, _I32, B, dev), _ws_on(fn, ws, dev)[0],
-                                      _stream_on(stream, dev)))
+                                      slots_stride, _need(fn, "new_len", new_len, _I32, B, dev),
+                                      None if ws is None else _ws_on(fn, ws, dev)[0], _stream_on(stream, dev)))
 
 
 def eagle_kvq_attention_workspace_bytes(kv: KvqCfg, T: int) -> int:
@@ -413,7 +413,8 @@ def eagle_kvq_tree_attention(kv, T, q, codes, scales, layer, prefix_len, mask, n
                                              _need(fn, "prefix_len", prefix_len, _I32, B, dev),
                                              _need(fn, "mask", mask, _W32, B * T * ((T + 31) // 32), dev),
                                              _need(fn, "n_tree", n_tree, _I32, B, dev),
-                                             _need(fn, "out", out, _BF16, n, dev), *_ws_on(fn, ws, dev), _stream_on(stream, dev)))
+                                             _need(fn, "out", out, _BF16, n, dev), *_ws_on(fn, ws, dev),
+                                             _stream_on(stream, dev)))
 
 
 def _logit_dtypes(cfg):
