@@ -632,3 +632,24 @@ def test_decode_steps_issued_back_to_back():
         want, tol = P.attention(kv, 1, q[s], vc, vs, 0, start + s, None, None)
         assert (np.abs(got[s] - want) <= tol).all(), s
     assert (ds.cpu().numpy() == scales).all() and (dc.cpu().numpy() == codes).all()
+
+
+@pytest.mark.parametrize("T,L", [(1, 40), (12, 40), (61, 40), (61, 5000)])
+def test_attention_nan_in_v_stays_in_its_column_and_head(T, L):
+    E = _E()
+    rng = np.random.default_rng(60 + T)
+    Hq, H = 2 if T == 12 else 8, 2
+    G = Hq // H
+    kv = E.kvq_contiguous(1, Hq, H, D, 1, L + T, 32)
+    codes, scales = _buffers(kv, rng)
+    vc, vs = P.views(kv, codes, scales)
+    q = _bf16(rng, (1, T, Hq, D), 2.0)
+    see = _tree(rng, 1, T, [T]) if T > 1 else None
+    want, tol = P.attention(kv, T, q, vc, vs, 0, [L], see, None)
+    vc[0, 0, 1, L + T // 2, 1, 77] = 0xFF
+    got, status = _attend(E, kv, T, [L], None, see, codes, scales, q, 0)
+    assert status == 0
+    ok = np.abs(got[0] - want[0]) <= tol[0]
+    assert np.isnan(got[0][:, G:, 77]).all()
+    ok[:, G:, 77] = True
+    assert ok.all()
