@@ -462,7 +462,11 @@ int eagle_kvq_compact(const eagle_kvq_cfg* kv, void* codes, float* scales, const
  *   scales   [V, H/group] bf16 in: weight[v, h] = (c - 8) * scales[v, h / group].
  *   draft_logits [B*k, V] out in cfg->logit_dtype: the sums of hidden * weight,
  *            fp32 (products of a group on the tensor cores, exact operands;
- *            groups scaled and added in fp32), rounded once.
+ *            groups scaled and added in fp32), rounded once. A group is summed
+ *            as codes c, from -8 times the sum of its hidden entries on, so
+ *            the bound of the fp32 sums is H * 2^-23 * sum_h |hidden[r, h]| *
+ *            (|c - 8| + 8) * |scale|: weights of 0 give logits that are 0
+ *            within it only.
  * Reads the weight once per 16 rows of hidden (once per 8 when the rows of 16
  * do not fit in shared memory: H > 5120): meant for the few rows of a
  * small batch, where reading the weight is the cost; V a multiple of 8.

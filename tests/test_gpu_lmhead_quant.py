@@ -197,3 +197,23 @@ def test_tiny_rows_under_huge_scales_and_the_reverse(out):
         if out == "bf16":
             tol = tol + 2.0 ** -8 * (np.abs(x @ w.T) + tol)
         assert (np.abs(got - x @ w.T) <= tol).all(), e
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_weights_of_zero_within_the_documented_bound(group):
+    """Codes of 8 (weight 0) and next to it under scales that are not 0. A group's products are summed as codes from
+    -8 times the sum of its hidden entries on, so the bound counts |c - 8| + 8: every one of the H products and of
+    the group's 4 + group / 16 other additions rounds a sum of at most sum |h| (|c - 8| + 8) scale by 2^-23."""
+    import torch
+    E = _E()
+    rng = np.random.default_rng(24)
+    M, V, H = 10, 256, 1024
+    h = P.bf16_round(rng.standard_normal((M, H)) * 3)
+    codes = np.full((V, H // 2), 0x88, np.uint8)
+    codes[V // 2:] = rng.choice([0x88, 0x89, 0x78, 0x98], (V - V // 2, H // 2))
+    scales = P.bf16_round(rng.uniform(0.01, 1.0, (V, H // group)))
+    w = P.unpack_w4(codes, scales, group)
+    got = _head(E, h, codes, scales, group, torch.float32)
+    x = h.astype(np.float64)
+    tol = H * 2.0 ** -23 * (np.abs(x) @ (np.abs(w) + 8 * np.repeat(scales.astype(np.float64), group, 1)).T)
+    assert (np.abs(got - x @ w.T) <= tol).all()
