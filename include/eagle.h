@@ -467,9 +467,12 @@ int eagle_kvq_compact(const eagle_kvq_cfg* kv, void* codes, float* scales, const
  *            the bound of the fp32 sums is H * 2^-23 * sum_h |hidden[r, h]| *
  *            (|c - 8| + 8) * |scale|: weights of 0 give logits that are 0
  *            within it only.
- * Reads the weight once per 16 rows of hidden (once per 8 when the rows of 16
- * do not fit in shared memory: H > 5120): meant for the few rows of a
- * small batch, where reading the weight is the cost; V a multiple of 8.
+ * Reads the weight once per 16 rows of hidden where min(B*k, 16) rows fit in
+ * shared memory (16 rows: H up to 5248, 5376, 5504 for groups of 32, 64, 128;
+ * 12 rows: 7040, 7296, 7424; 10 rows: any H), else once per 8. Meant for the
+ * few rows of a small batch, where reading the weight is the cost: from three
+ * passes on at H = 4096 (33 rows), four at H = 8192 (25 rows), eagle_lmhead on
+ * the 16-bit weight takes less time. V a multiple of 8.
  */
 int eagle_lmhead_quant(const eagle_tree_cfg* cfg, void* ws, size_t ws_bytes, int hidden_dim, int group,
                        const void* hidden, const void* codes, const void* scales, void* draft_logits, void* stream);

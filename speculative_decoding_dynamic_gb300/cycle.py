@@ -73,7 +73,8 @@ class DeviceCycle:
         step's rows are then first written into draft_logits[s] by the LM head,
         or, with fused_head, reduced to their lse and top-k in the LM head's
         epilogue and expanded from those (draft_logits unused). A weight given
-        as (codes, scales, group) is the 4-bit head of eagle_lmhead_quant."""
+        as (codes, scales, group) is the 4-bit head of eagle_lmhead_quant: for
+        up to 32 rows (24 at H = 8192); past them the 16-bit head takes less time."""
         cfg = self.cfg
         if self.fused_head and head is not None and isinstance(head[0], tuple):
             raise ValueError("DeviceCycle.draft: the 4-bit head has no form with stage 1 in its epilogue (fused_head)")

@@ -217,3 +217,21 @@ def test_weights_of_zero_within_the_documented_bound(group):
     x = h.astype(np.float64)
     tol = H * 2.0 ** -23 * (np.abs(x) @ (np.abs(w) + 8 * np.repeat(scales.astype(np.float64), group, 1)).T)
     assert (np.abs(got - x @ w.T) <= tol).all()
+
+
+@pytest.mark.parametrize("M,H,group", [(16, 5504, 128), (16, 5248, 32), (16, 5376, 64), (16, 5632, 128), (12, 7296, 128),
+                                       (9, 8192, 64), (17, 5504, 128)])
+def test_passes_at_the_limits_of_shared_memory(M, H, group):
+    """The widest hidden states of a pass of nine to sixteen rows, and those beyond it."""
+    import torch
+    E = _E()
+    rng = np.random.default_rng(M + H)
+    V = 152 * 16 + 40
+    h = P.bf16_round(rng.standard_normal((M, H)))
+    codes = rng.integers(0, 256, (V, H // 2)).astype(np.uint8)
+    scales = P.bf16_round(rng.uniform(1e-3, 5e-2, (V, H // group)))
+    w = P.unpack_w4(codes, scales, group)
+    got = _head(E, h, codes, scales, group, torch.float32, extra=1)
+    x = h.astype(np.float64)
+    tol = H * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T)
+    assert (np.abs(got[:M] - x @ w.T) <= tol).all() and (got[M] == 7.0).all()
