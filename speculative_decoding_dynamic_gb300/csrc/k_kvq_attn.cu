@@ -389,6 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (t > 0 && lane == 0) mbar_arrive(&bar_go[(t - 1) & (kScaleSlots - 1)]);
         __syncwarp();
+        // the QK warps' commits on the last item's q, which nobody else waits for, arrive before the CTA's shared
+        // memory goes away
+        if (qi > 0) wait(&bar_q_empty[(qi - 1) & 1], (qi - 1) >> 1);
         if (!wait.ok) {  // the copies in flight land before the CTA's shared memory goes away
             if (lane == 0) raise_status(p.status, kDevTimeout);
             for (int s = 0; s < 2; ++s)

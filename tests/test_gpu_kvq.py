@@ -653,3 +653,26 @@ def test_attention_nan_in_v_stays_in_its_column_and_head(T, L):
     assert np.isnan(got[0][:, G:, 77]).all()
     ok[:, G:, 77] = True
     assert ok.all()
+
+
+def test_short_items_launched_again_and_again():
+    """Workers with one tile or two, which leave right behind their last product, in launches that follow one another at
+    once: every run is the first, bit for bit."""
+    import torch
+    E = _E()
+    rng = np.random.default_rng(80)
+    B, Hq, H, T = 5, 32, 8, 61
+    L = np.array([0, 1, 3, 64, 130])
+    kv = E.kvq_contiguous(B, Hq, H, D, 1, 256, 16)
+    codes, scales = _buffers(kv, rng)
+    q = _bf16(rng, (B, T, Hq, D), 2.0)
+    want, tol = P.attention(kv, T, q, *P.views(kv, codes, scales), 0, L, None, None)
+    ws = E.alloc_workspace(E.eagle_kvq_attention_workspace_bytes(kv, T))
+    dc, ds, dq, dl = _dev(codes), _dev(scales), _dev_bf16(q), _dev(L.astype(np.int32))
+    runs = torch.empty(200, B, T, Hq, D, dtype=torch.bfloat16, device="cuda")
+    for out in runs:
+        E.eagle_kvq_tree_attention(kv, T, dq, dc, ds, 0, dl, None, None, out, ws)
+    torch.cuda.synchronize()
+    assert E.eagle_status_fetch(ws) == 0
+    assert (np.abs(runs[0].float().cpu().numpy() - want) <= tol).all()
+    assert (runs == runs[0]).all()
