@@ -418,12 +418,13 @@ size_t eagle_kvq_attention_workspace_bytes(const eagle_kvq_cfg* kv, int T);
  * weights are rounded to fp16 (relative 2^-11, and 2^-25 of the row's largest
  * weight) for the product with V. V's scales enter relative to the largest of
  * the tiles so far (a smaller one counts as 2^-24 of it at least). Output bf16,
- * rounded to nearest even. A NaN among K's codes or in q makes the rows that
- * see it zero or NaN and leaves the others alone; a NaN among V's codes at a
- * position below prefix_len[b] + n_tree[b] makes its element of the output NaN
- * (or the row zero) in every row of that sequence and KV head, also where the
- * mask leaves the position out (0 * NaN in the product with V). Sums of |v|
- * times up to 2^8 over a row's keys have to stay in fp32's range.
+ * rounded to nearest even. A NaN among K's codes or a NaN or infinity in q
+ * makes the rows that see it zero or NaN and leaves the others alone; a NaN
+ * among V's codes at a position below prefix_len[b] + n_tree[b] makes its
+ * element of the output NaN (or the row zero) in every row of that sequence and
+ * KV head, also where the mask leaves the position out (0 * NaN in the product
+ * with V). Sums of |v| times up to 2^8 over a row's keys have to stay in fp32's
+ * range.
  *   q, out   [B, T, Hq, 128] bf16, contiguous, 16-byte aligned; T = 1..256.
  *   mask     [B, T, W] as eagle_build_tree writes it, or NULL: slot i sees the
  *            slots 0..i (a chain; with T = 1 the plain decode step).

@@ -234,11 +234,13 @@ __global__ void __launch_bounds__(kSplitThreads)
         for (int m = 1; m < 16; m <<= 1) mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, m));
         mx = max(mx & 0xffffu, mx >> 16);
         const float s = pow2_to(__uint_as_float(mx << 16), 7);
+        // a row with an infinity becomes NaN as a whole: as e4m3 an infinity would be 448
+        const float sx = mx < 0x7f80u ? s : NAN;
         const uint32_t w[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const float x = __uint_as_float(w[c] << 16) * s, y = __uint_as_float(w[c] & 0xffff0000u) * s;
+            const float x = __uint_as_float(w[c] << 16) * sx, y = __uint_as_float(w[c] & 0xffff0000u) * sx;
             hi[c] = e4m3x2(x, y);
             const uint32_t h = e4m3_to_f16x2(hi[c]);
             const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h));

@@ -676,3 +676,26 @@ def test_short_items_launched_again_and_again():
     assert E.eagle_status_fetch(ws) == 0
     assert (np.abs(runs[0].float().cpu().numpy() - want) <= tol).all()
     assert (runs == runs[0]).all()
+
+
+@pytest.mark.parametrize("T,L", [(1, 40), (12, 40), (61, 40), (1, 5000), (61, 5000)])
+@pytest.mark.parametrize("value", [np.inf, -np.inf])
+def test_attention_infinities_in_q_do_not_pass_for_numbers(T, L, value):
+    """A row of q with an infinity is zero or NaN, as one with a NaN; the others are as without it."""
+    E = _E()
+    rng = np.random.default_rng(90 + T)
+    Hq, H = 2 if T == 12 else 8, 2
+    kv = E.kvq_contiguous(1, Hq, H, D, 1, L + T, 32)
+    codes, scales = _buffers(kv, rng, lo=-30, hi=-4)
+    vc, vs = P.views(kv, codes, scales)
+    vs[:, :, 0] = 2.0 ** -30 / np.float32(1.4426950408889634 / np.sqrt(128.0))  # factors of the scores: powers of two
+    q = _bf16(rng, (1, T, Hq, D), 2.0)
+    want, tol = P.attention(kv, T, q, vc, vs, 0, [L], None, None)
+    q[0, T // 2, Hq - 1, 77] = value
+    got, status = _attend(E, kv, T, [L], None, None, codes, scales, q, 0)
+    assert status == 0
+    ok = np.abs(got[0] - want[0]) <= tol[0]
+    row = got[0, T // 2, Hq - 1]
+    assert ((row == 0) | np.isnan(row)).all()
+    ok[T // 2, Hq - 1] = True
+    assert ok.all()
