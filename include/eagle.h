@@ -417,7 +417,8 @@ size_t eagle_kvq_attention_workspace_bytes(const eagle_kvq_cfg* kv, int T);
  * part exactly and q within 2^-17 of its row's largest element; the softmax
  * weights are rounded to fp16 (relative 2^-11, and 2^-25 of the row's largest
  * weight) for the product with V. V's scales enter relative to the largest of
- * the tiles so far (a smaller one counts as 2^-24 of it at least). Output bf16,
+ * the tiles so far, 2^-126 at least (a smaller one counts as 2^-24 of it at
+ * least). Output bf16,
  * rounded to nearest even. A NaN among K's codes or a NaN or infinity in q
  * makes the rows that see it zero or NaN and leaves the others alone; a NaN
  * among V's codes at a position below prefix_len[b] + n_tree[b] makes its

@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float vm = lane >= kSub && lane < 2 * kSub ? last_scale : 0.0f;
             vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
             vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
-            vm = __shfl_sync(0xffffffffu, vm, kSub);
+            vm = fmaxf(__shfl_sync(0xffffffffu, vm, kSub), kKvqMinRef);
             float alpha = 1.0f;
             if (vm > 16.0f * sref) {
                 if (sref > 0.0f) alpha = sref / vm;

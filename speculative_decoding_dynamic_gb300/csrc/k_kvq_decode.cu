@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1)
                         raise = true;
                     }
                 }
-            const float vm = fmaxf(vv[0], vv[1]);
+            const float vm = fmaxf(fmaxf(vv[0], vv[1]), kKvqMinRef);
             if (vm > 16.0f * sref) {  // uniform over the warp
                 const float r = sref / vm;
 #pragma unroll

@@ -282,6 +282,9 @@ inline bool make_map_codes(CUtensorMap* m, const void* base, const KvqDims& kv, 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The least reference of V's scales: its reverse is finite (a subnormal scale's need not be).
+constexpr float kKvqMinRef = 0x1p-126f;
+
 // Few query rows per KV head: k_kvq_decode.cu.
 constexpr int kKvqDecodeRows = 16;
 constexpr int kKvqSms = 152;

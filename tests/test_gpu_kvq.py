@@ -699,3 +699,26 @@ def test_attention_infinities_in_q_do_not_pass_for_numbers(T, L, value):
     assert ((row == 0) | np.isnan(row)).all()
     ok[T // 2, Hq - 1] = True
     assert ok.all()
+
+
+@pytest.mark.parametrize("T,L", [(1, 200), (12, 200), (61, 200), (1, 5000), (61, 5000)])
+def test_attention_subnormal_and_huge_v_scales(T, L):
+    """V scales from fp32's subnormal numbers to 2^100, whole sequences of one size and blocks of both."""
+    E = _E()
+    rng = np.random.default_rng(95 + T)
+    B, Hq, H = 5, 2 if T == 12 else 8, 2
+    kv = E.kvq_contiguous(B, Hq, H, D, 1, L + T, 32)
+    codes, scales = _buffers(kv, rng)
+    vc, vs = P.views(kv, codes, scales)
+    sizes = (-149.0, -140.0, -127.0, 100.0)
+    for b, e in enumerate(sizes):
+        vs[b, :, 1] = 2.0 ** e
+    vs[4, :, 1] = 2.0 ** rng.choice(np.array([-149.0, -130.0, -126.0, -120.0]), vs[4, :, 1].shape)
+    q = _bf16(rng, (B, T, Hq, D), 1.0)
+    want, tol = P.attention(kv, T, q, vc, vs, 0, [L] * B, None, None)
+    got, status = _attend(E, kv, T, [L] * B, None, None, codes, scales, q, 0)
+    assert status == 0
+    # beside tol (without its 1e-30): half of bf16's subnormal step, half of fp32's in the partial results, the
+    # normalisation and the products, and the weights' 2^-25 under the least reference of V's scales, 2^-126
+    more = 2.0 ** -134 + 8 * 2.0 ** -150 + (L + T) * 2.0 ** -25 * 448 * 2.0 ** -126
+    assert (np.abs(got - want) <= tol - 1e-30 + more).all()
