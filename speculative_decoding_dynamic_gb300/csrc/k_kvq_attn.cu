@@ -185,14 +185,6 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low 
     return d;
 }
 
-// q as two e4m3 parts: s x = hi + lo for a row x, s the power of two that
-// brings its largest element into [128, 256); the softmax's factor log2(e) /
-// (s sqrt(128)). From [B][T][Hq][128] to [B][Hkv][hi, lo][G*T][128] and
-// [B][Hkv][G*T]. Sixteen lanes take a row, two rows each (both loads first).
-// Moves 4 bytes per element; at 8B b64, 31 MB each way. (In the attention
-// kernel, by its converters behind their tiles, it held up each item by
-// 11,000 cycles: the fence behind a converted tile waits for the loads of q
-// in flight.) The first CTAs find where the attention's workers start.
 // n / d by the reciprocal 2^63 / d, rounded up: exact for all 32-bit n and d.
 // (Three divisions a row took half of the kernel's instructions.)
 struct Divisor {
@@ -202,6 +194,15 @@ struct Divisor {
         return static_cast<uint32_t>(__umul64hi(m, static_cast<uint64_t>(n) << 1));
     }
 };
+
+// q as two e4m3 parts: s x = hi + lo for a row x, s the power of two that
+// brings its largest element into [128, 256); the softmax's factor log2(e) /
+// (s sqrt(128)). From [B][T][Hq][128] to [B][Hkv][hi, lo][G*T][128] and
+// [B][Hkv][G*T]. Sixteen lanes take a row, two rows each (both loads first).
+// Moves 4 bytes per element; at 8B b64, 31 MB each way. (In the attention
+// kernel, by its converters behind their tiles, it held up each item by
+// 11,000 cycles: the fence behind a converted tile waits for the loads of q
+// in flight.) The first CTAs find where the attention's workers start.
 constexpr int kSplitThreads = 256, kSplitPer = 2, kSplitRows = kSplitPer * kSplitThreads / 16;
 __global__ void __launch_bounds__(kSplitThreads)
     kvq_split_q_kernel(const __nv_bfloat16* q, uint2* __restrict__ dst, float* __restrict__ fac, KvqRows rows,
@@ -694,7 +695,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             rescale = true;
                         }
                     }
-                    // (the vote here: its answer is not needed before P is written)
                     // (the vote here: its answer is not needed before P is written)
                     const bool any_rescale = __any_sync(0xffffffffu, rescale);
                     // P = 2^(s k - m_use + lv), two per packed multiply-add; the row sum takes the

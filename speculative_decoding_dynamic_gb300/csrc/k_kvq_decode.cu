@@ -415,47 +415,44 @@ __global__ void __launch_bounds__(kMergeWarps * 32) kvq_merge_decode_kernel(KvqM
         return static_cast<size_t>(i == 0 ? 2 * w + 1 : 2 * (w + i)) * p.part.rows + r;
     };
     const int4 own = __ldcg(items + min(warp, n_here - 1));
-    if (warp < n_here && own.x > 0 && own.x <= kMergeAlone)
-        {
-            RowSum<1> s;
-            float2 a[kMergeAlone];
-            float4 x[kMergeAlone][1];
+    if (warp < n_here && own.x > 0 && own.x <= kMergeAlone) {
+        RowSum<1> s;
+        float2 a[kMergeAlone];
+        float4 x[kMergeAlone][1];
 #pragma unroll
-            for (int i = 0; i < kMergeAlone; ++i) {
-                if (i >= own.x) break;
-                const size_t at = slot_row(w0 + warp, i, r);
-                a[i] = __ldcg(ml + at);
-                x[i][0] = __ldcg(po + at * 32 + lane);
-            }
-#pragma unroll
-            for (int i = 0; i < kMergeAlone; ++i)
-                if (i < own.x) s.add(a[i].x, a[i].y, x[i]);
-            merge_store(p, own, r, s, lane);
+        for (int i = 0; i < kMergeAlone; ++i) {
+            if (i >= own.x) break;
+            const size_t at = slot_row(w0 + warp, i, r);
+            a[i] = __ldcg(ml + at);
+            x[i][0] = __ldcg(po + at * 32 + lane);
         }
+#pragma unroll
+        for (int i = 0; i < kMergeAlone; ++i)
+            if (i < own.x) s.add(a[i].x, a[i].y, x[i]);
+        merge_store(p, own, r, s, lane);
+    }
     for (int e = 0; e < n_here; ++e) {
         const int4 c = __ldcg(items + e);
         if (c.x <= kMergeAlone) continue;  // uniform over the CTA
-        {
-            RowSum<1> s;
+        RowSum<1> s;
 #pragma unroll 4
-            for (int i = warp; i < c.x; i += kMergeWarps) {
-                const size_t at = slot_row(w0 + e, i, r);
-                const float2 a = __ldcg(ml + at);
-                const float4 x[1] = {__ldcg(po + at * 32 + lane)};
-                s.add(a.x, a.y, x);
-            }
-            so[warp][lane] = s.o[0];
-            if (lane == 0) sml[warp] = make_float2(s.m, s.l);
-            __syncthreads();
-            if (warp == 0) {
-                for (int i = 1; i < kMergeWarps; ++i) {
-                    const float4 x[1] = {so[i][lane]};
-                    s.add(sml[i].x, sml[i].y, x);
-                }
-                merge_store(p, c, r, s, lane);
-            }
-            __syncthreads();
+        for (int i = warp; i < c.x; i += kMergeWarps) {
+            const size_t at = slot_row(w0 + e, i, r);
+            const float2 a = __ldcg(ml + at);
+            const float4 x[1] = {__ldcg(po + at * 32 + lane)};
+            s.add(a.x, a.y, x);
         }
+        so[warp][lane] = s.o[0];
+        if (lane == 0) sml[warp] = make_float2(s.m, s.l);
+        __syncthreads();
+        if (warp == 0) {
+            for (int i = 1; i < kMergeWarps; ++i) {
+                const float4 x[1] = {so[i][lane]};
+                s.add(sml[i].x, sml[i].y, x);
+            }
+            merge_store(p, c, r, s, lane);
+        }
+        __syncthreads();
     }
 }
 

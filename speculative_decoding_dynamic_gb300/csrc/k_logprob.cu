@@ -296,12 +296,10 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 4 : 6) token_logprobs_kern
         my.s += gs;
         my.e += ge;
     };
-    {
-        for (int ch = 0; ch < nch; ++ch) {
-            uint4 u[kVecs];
-            load(ch, u);
-            group(ch, u);
-        }
+    for (int ch = 0; ch < nch; ++ch) {
+        uint4 u[kVecs];
+        load(ch, u);
+        group(ch, u);
     }
     // ---- this CTA's sums ----
     float wmx = top;
