@@ -34,11 +34,14 @@
 // Bound by the tensor pipe: per tile and row block eight QK^T MMAs of 48
 // cycles (N = 64 is bound by reading the operands from shared memory) and four
 // PV MMAs of 64, so 1280 cycles for both blocks of a tile of some 1500 measured
-// (8 sequences of 32K, 70B heads: 543 us; 64 sequences of 8B: 123 us; one of
-// 2048: 25 us). That holds while the two blocks' softmaxes run half a tile apart,
-// as they do in this build; builds of the same loop in which they ran together
-// took 1900 (710 us), and letting PV of one block wait for the other's QK^T did
-// not part them (807 us). What was tried against the bound: QK^T over 128 keys at
+// (8 sequences of 32K, 70B heads: 561 us in a captured graph, 562 to 580 call
+// after call, by the card; 64 sequences of 8B: 122 us; one of 2048: 25 us). That
+// holds while the two blocks' softmaxes run half a tile apart, as they do in this
+// build: nothing here orders them. Builds of the same loop in which they ran
+// together took 1900 (710 us; 743 us and 149 us at 8B with nothing changed but
+// the kind of load of the sequences' lengths, so time this kernel after any
+// change), and letting PV of one block wait for the other's QK^T did not part
+// them (807 us). What was tried against the bound: QK^T over 128 keys at
 // once (N = 128, two thirds of the cycles) leaves no second buffer of S, and
 // waits for PV (857 us); S freed as soon as it is read, with P beside it, puts
 // the copy's, QK^T's and softmax's latencies in one chain (678 us); half a row

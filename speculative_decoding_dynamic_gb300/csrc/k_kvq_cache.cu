@@ -63,7 +63,7 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
 // Bound by HBM: two bytes read and one written per element. Holding the block
 // in registers instead of reading it a second time for the codes is why the
 // group grows with the block. Measured: 20,000 prompt tokens of 40 heads (461 MB)
-// 71.4 us, 6.5 TB/s; 64 trees of 61 slots of 8 heads (24 MB) 5.6 us.
+// 71.4 us, 6.5 TB/s; 64 trees of 61 slots of 8 heads (24 MB) 5.5 us in a captured graph.
 template <int BLK>
 __global__ void __launch_bounds__(kStoreThreads) kvq_store_kernel(
     KvqDims kv, int layer, int T, int nhg, const __nv_bfloat16* k, const __nv_bfloat16* v,
@@ -194,7 +194,8 @@ __device__ __forceinline__ uint4 rescale16(const uint4& u, float ratio) {
 // is a chain of small loads (lengths and slots, then rows and scales) and
 // the number of warps that go through it: four heads per warp bring a batch
 // of 64 with 32 layers into one wave (one head per warp: 16.8 us; four: 9.1, and
-// 2.8 us for one sequence).
+// 2.8 us for one sequence, in a captured graph on a cache that it has compacted before;
+// 27 and 5 us on a fresh one, where the scales of destination blocks grow).
 __global__ void __launch_bounds__(kMoveWarps * 32) kvq_compact_kernel(
     KvqDims kv, unsigned char* __restrict__ codes, float* __restrict__ scales, const int32_t* prefix_len,
     const int32_t* accept_len, const int32_t* slots, int slots_stride,

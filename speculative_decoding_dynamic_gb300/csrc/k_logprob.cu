@@ -22,8 +22,8 @@
 // tail. About six instructions per element beside the one exponential
 // (packed fp32 pairs for the multiply-adds and sums, packed bf16 for maxima and
 // compares; the compare is skipped for groups whose maximum is below the
-// token's logit). Measured: 4096 fp32 rows of 32000 (524 MB) 100 us, 78% of HBM;
-// some 250 bf16 rows of 128256 (65 MB) 22.5 us, a wave of CTAs. A row is split over a cluster of
+// token's logit). Measured: 4096 fp32 rows of 32000 (524 MB) 99 us, 79% of HBM;
+// some 250 bf16 rows of 128256 (65 MB) 22.2 us, a wave of CTAs. A row is split over a cluster of
 // 1..8 CTAs when there are few rows. The alternatives need no second pass
 // over the row: the k-th largest of the threads' maxima bounds the k-th
 // largest entry from below, and only the groups (four vectors of a thread)
