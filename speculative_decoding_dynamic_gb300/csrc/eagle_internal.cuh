@@ -247,8 +247,8 @@ __device__ __forceinline__ int ticket_add(int* p) {
 // CTA runs: every thread arrives when it has started and waits right before
 // its CTA's first remote access, with the work in between. (Threads that have
 // left are not waited for.) A cluster.sync() afterwards is a barrier of its own.
-__device__ __forceinline__ void cluster_started_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
-__device__ __forceinline__ void cluster_started_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
+__device__ __forceinline__ void cluster_started_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_started_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
 // ------------------------------------------------------------- host side ---
 // Dynamic shared memory opt-in and launch helpers live in the launcher files.

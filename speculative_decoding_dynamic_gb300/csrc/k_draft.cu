@@ -196,9 +196,11 @@ __global__ void __launch_bounds__(kDraftThreads) verify_draft_kernel(TreeDims d,
     uint64_t* A = w.resid + static_cast<size_t>(b) * V;
     ClusterReduce red{cluster, &sm, rank, 0};
     pdl_launch_dependents();
+    cluster_started_arrive();
     pdl_wait_prior();
 
     const int n = n_tree[b];
+    cluster_started_wait();  // behind the load
     if (tid == 0) {
         sm.bad = (n < 1 || n > T) ? 1 : 0;
         sm.bonus = -1;
@@ -478,9 +480,11 @@ __global__ void __launch_bounds__(kWalkThreads) verify_lossless_walk_kernel(Tree
     // rounds of kWalkVec vectors per thread, the same in every CTA (their control flow must agree)
     const int rounds = (seg / EPV + kWalkThreads * kWalkVec - 1) / (kWalkThreads * kWalkVec);
     pdl_launch_dependents();
+    cluster_started_arrive();
     pdl_wait_prior();
 
     const int n = n_tree[b];
+    cluster_started_wait();  // behind the load
     const size_t tb = static_cast<size_t>(b) * T;
     if (tid == 0) {
         sm.bad = (n < 1 || n > T || rounds > kWalkMaxRounds) ? 1 : 0;

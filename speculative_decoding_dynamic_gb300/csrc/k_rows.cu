@@ -593,7 +593,8 @@ __device__ __forceinline__ void segment_consume(ExpandSmem& sm, unsigned char* d
 // Merge of the CTAs of one row's cluster: every CTA pushes its top-k keys and
 // (max, sum) into the leader's shared memory, then the leader (rank 0) ranks
 // the keys into sm.top and combines (max, sum) into (sm.wm[0], sm.ws[0]).
-// Returns true in the leader, after a block barrier.
+// Returns true in the leader, after a block barrier. Every thread has waited
+// (cluster_started_wait) for the other CTAs' start, while the row streamed.
 __device__ __forceinline__ bool cluster_row_merge(ExpandSmem& sm, cg::cluster_group& cluster, int rank, int cpr, int k) {
     const int tid = threadIdx.x;
     ExpandSmem* leader = cluster.map_shared_rank(&sm, 0);
@@ -655,6 +656,7 @@ __global__ void __launch_bounds__(kRowThreads, SAMP ? 3 : 5) expand_kernel(TreeD
     const int nch = min(max_seg_chunks<DT>(), (n * ES + kRowChunkBytes - 1) / kRowChunkBytes);  // the launcher keeps within
     const char* row_base = static_cast<const char*>(logits) + static_cast<size_t>(b * d.k + f) * d.V * ES;
     pdl_launch_dependents();
+    cluster_started_arrive();
     // Before the dependency wait: the head of the segment into L2 (a hint; a
     // later write by the previous kernel still lands first), and every piece
     // of state that does not depend on the previous kernel.
@@ -694,7 +696,9 @@ __global__ void __launch_bounds__(kRowThreads, SAMP ? 3 : 5) expand_kernel(TreeD
             sm.plogv = plogv;
         }
         __syncwarp();
+        cluster_started_wait();
     } else {
+        cluster_started_wait();  // the first chunk is on its way
         segment_consume<DT, SAMP>(sm, dyn_smem, smem_bytes, ns, row_base, c0, n, nch, k, lse_in == nullptr, 0, w.status,
                                   static_cast<uint32_t>(b * d.k + f), grng);
     }
@@ -848,6 +852,7 @@ __global__ void __launch_bounds__(kRowThreads) verify_kernel(TreeDims d, TreeWs 
     constexpr int EPV = 16 / ES;
     constexpr int CE = kRowChunkBytes / ES;
     pdl_launch_dependents();
+    cluster_started_arrive();
     if (tid == kProducerWarp * 32) {  // the segment's head into L2 while the previous kernel finishes
         const int cp = rank * seg;
         const int np = max(0, min(seg, d.V - cp));
@@ -891,7 +896,9 @@ __global__ void __launch_bounds__(kRowThreads) verify_kernel(TreeDims d, TreeWs 
             }
         }
         __syncwarp();
+        cluster_started_wait();
     } else {
+        cluster_started_wait();
         // ---- pass 1: maximum, lowest id among equal values ----
         float lm = -INFINITY;
         int larg = -1;
@@ -1054,6 +1061,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) shard_partial_kernel(int Vs, i
     const int nch = min(max_seg_chunks<DT>(), (n * ES + kRowChunkBytes - 1) / kRowChunkBytes);
     const char* row_base = static_cast<const char*>(logits) + static_cast<size_t>(row) * Vs * ES;
     pdl_launch_dependents();
+    cluster_started_arrive();
     if (tid == kProducerWarp * 32) prefetch_l2_segment(row_base + static_cast<size_t>(c0) * ES, n * ES);
     if (tid == 0) {
         ring_init(sm.ring, ns);
@@ -1071,7 +1079,9 @@ __global__ void __launch_bounds__(kRowThreads, 5) shard_partial_kernel(int Vs, i
         if (lane == 0 && nch > 0)
             ring_produce(sm.ring, dyn_smem, row_base + static_cast<size_t>(c0) * ES, n * ES, nch, ns, status);
         __syncwarp();
+        cluster_started_wait();
     } else {
+        cluster_started_wait();
         segment_consume<DT, false>(sm, dyn_smem, smem_bytes, ns, row_base, c0, n, nch, k, true, id_base, status, 0u,
                                    GumbelRng{});
     }

@@ -344,3 +344,38 @@ def test_status_ring_wait_timeout_then_recovers():
     assert E.eagle_status_fetch(ws) == 2
     assert E.eagle_status_fetch(ws) == 0
     _run_tree(logits, B, V, k, D, N, 0.0, synth.BF16)
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2])
+@pytest.mark.parametrize("V", [16384, 40000])
+def test_short_rows_over_clusters_again_and_again(V, mode):
+    """Draft and verification on rows that clusters of CTAs share and that leave little work before the shares
+    meet, a hundred cycles one behind the other: every one is the first, bit for bit."""
+    import torch
+    from speculative_decoding_dynamic_gb300 import cycle as C
+    E = _E()
+    B, k, D, N = 2, 4, 3, 12
+    cfg = E.TreeCfg(B, V, k, D, N, 0.0, synth.BF16, 3 if mode == E.DRAFT else 0)
+    kv = E.KvCfg(B, 1, 1, 128, 1, 32, synth.BF16, 2 * 32 * 128, 2 * 32 * 128, 32 * 128, 128)
+    dc = C.DeviceCycle(cfg, kv)
+    draft = H.to_dev(synth.normal4((D, B, k, V), synth.BF16, 2.5, seed=V, stream=synth.STREAM_DRAFT))
+    target = H.to_dev(synth.normal4((B, cfg.T, V), synth.BF16, 2.5, seed=V, stream=synth.STREAM_TARGET))
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    runs = []
+    for _ in range(100):
+        if mode == E.DRAFT:
+            E.eagle_tree_init(cfg, dc.ws)
+            for s in range(D):
+                E.eagle_expand_sampled(cfg, dc.ws, s, draft[s], None, 5, 0, dc.row_lse, dc.ftok, dc.fcount)
+            E.eagle_rerank(cfg, dc.ws)
+        else:
+            dc.draft(draft)
+        dc.build(zero, zero)
+        E.eagle_verify(cfg, dc.ws, mode, 1.0, 5, 0, target, dc.tokens, dc.parent, dc.n_tree, dc.accept_len, dc.slots,
+                       dc.out_tokens, draft_logits=draft if mode == E.DRAFT else None)
+        runs.append([x.clone() for x in (dc.row_lse, dc.tokens, dc.parent, dc.accept_len, dc.slots, dc.out_tokens)])
+    torch.cuda.synchronize()
+    assert dc.status() == 0
+    for r in runs:
+        for a, b in zip(r, runs[0]):
+            assert torch.equal(a.view(torch.int32), b.view(torch.int32))
