@@ -418,14 +418,13 @@ size_t eagle_kvq_attention_workspace_bytes(const eagle_kvq_cfg* kv, int T);
  * weights are rounded to fp16 (relative 2^-11, and 2^-25 of the row's largest
  * weight) for the product with V. V's scales enter relative to the largest of
  * the tiles so far, 2^-126 at least (a smaller one counts as 2^-24 of it at
- * least). Output bf16,
- * rounded to nearest even. A NaN among K's codes or a NaN or infinity in q
- * makes the rows that see it zero or NaN and leaves the others alone; a NaN
- * among V's codes at a position below prefix_len[b] + n_tree[b] makes its
- * element of the output NaN (or the row zero) in every row of that sequence and
- * KV head, also where the mask leaves the position out (0 * NaN in the product
- * with V). Sums of |v| times up to 2^8 over a row's keys have to stay in fp32's
- * range.
+ * least). Output bf16, rounded to nearest even. A NaN among K's codes or a NaN
+ * or infinity in q makes the rows that see it zero or NaN and leaves the others
+ * alone; a NaN among V's codes at a position below prefix_len[b] + n_tree[b]
+ * makes its element of the output NaN (or the row zero) in every row of that
+ * sequence and KV head, also where the mask leaves the position out (0 * NaN in
+ * the product with V). Sums of |v| times up to 2^8 over a row's keys have to
+ * stay in fp32's range.
  *   q, out   [B, T, Hq, 128] bf16, contiguous, 16-byte aligned; T = 1..256.
  *   mask     [B, T, W] as eagle_build_tree writes it, or NULL: slot i sees the
  *            slots 0..i (a chain; with T = 1 the plain decode step).
@@ -516,8 +515,8 @@ int eagle_lmhead_quant_pack(int vocab, int hidden_dim, int group, const void* we
  * alt_logprobs NaN, rank and alt_ids -1, no row read. A token >= V or a slot
  * >= rows_per_seq raises status 3 and gives padding values. Logits of -inf
  * have probability 0; a row with a NaN, a +inf or no finite logit raises
- * status 1 and gives padding values. Of `cfg` only vocab and logit_dtype matter here, of `ws` the
- * status word.
+ * status 1 and gives padding values. Of `cfg` only vocab and logit_dtype
+ * matter here, of `ws` the status word.
  */
 int eagle_token_logprobs(const eagle_tree_cfg* cfg, void* ws, size_t ws_bytes, int n_seq, int per_seq,
                          int rows_per_seq, const void* logits, float temperature, const int32_t* slots,

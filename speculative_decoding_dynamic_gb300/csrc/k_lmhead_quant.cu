@@ -531,8 +531,8 @@ cudaError_t launch_group(const QuantParams& p, int group, bool bf16, const void*
 // ------------------------------------------------------------------- pack ---
 
 // One lane per eight entries; group / 8 neighbouring lanes share a scale. Run once
-// per model: V = 128256, H = 4096 637 us (1.3 GB moved, 198 us at the copy's rate;
-// a division per entry and one 16-byte load in flight per thread bound it).
+// per model and not made fast: 637 us at V = 128256, H = 4096 (1.3 GB moved, 198 us
+// at the copy's rate).
 __global__ void __launch_bounds__(256) lmhead_quant_pack_kernel(long pieces, int group, const uint4* weight,
                                                                 uint32_t* __restrict__ codes,
                                                                 __nv_bfloat16* __restrict__ scales) {
