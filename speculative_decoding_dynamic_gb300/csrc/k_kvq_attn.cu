@@ -395,9 +395,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (t > 0 && lane == 0) mbar_arrive(&bar_go[(t - 1) & (kScaleSlots - 1)]);
         __syncwarp();
-        // the QK warps' commits on the last item's q, which nobody else waits for, arrive before the CTA's shared
-        // memory goes away
-        if (qi > 0) wait(&bar_q_empty[(qi - 1) & 1], (qi - 1) >> 1);
         if (!wait.ok) {  // the copies in flight land before the CTA's shared memory goes away
             if (lane == 0) raise_status(p.status, kDevTimeout);
             for (int s = 0; s < 2; ++s)
@@ -572,7 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&bar_sc[slot]);
             __syncwarp();
         };
-        while (cur.next<true>(p.s, it)) {
+        int qi = 0;
+        for (; cur.next<true>(p.s, it); ++qi) {
             const int hk = it.sub / p.n_items;
             const float* src = (lane < kSub ? p.k_scale : p.v_scale) + it.b * p.s_seq + hk;
             const int last = (it.nkeys - 1) >> p.blk_shift;
@@ -585,6 +583,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (t > 0) give(t - 1);
+        // The QK warps' commits on the last item's q, which nobody else waits for, arrive before the CTA's shared
+        // memory goes away. (Its q was copied, so the barrier's phase before is over.)
+        if (qi > 0) wait(&bar_q_empty[(qi - 1) & 1], (qi - 1) >> 1);
         if (!wait.ok && lane == 0) raise_status(p.status, kDevTimeout);
     } else {
         // ------------------------------------------------------ softmax ---
