@@ -433,7 +433,7 @@ size_t eagle_kvq_attention_workspace_bytes(const eagle_kvq_cfg* kv, int T);
  * zero rows otherwise). A row that sees no key is zero. Any number of query
  * heads per KV head. On half the cache of eagle_tree_attention it takes less
  * time where the contexts are long; trees of many short ones take more (8B
- * heads, 64 sequences of 256..2048: 122 against 95 us a layer).
+ * heads, 64 sequences of 256..2048: 121 against 95 us a layer).
  */
 int eagle_kvq_tree_attention(const eagle_kvq_cfg* kv, int T, const void* q, const void* codes, const float* scales,
                              int layer, const int32_t* prefix_len, const uint32_t* mask, const int32_t* n_tree,

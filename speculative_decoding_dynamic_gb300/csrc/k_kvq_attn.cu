@@ -34,8 +34,8 @@
 // Bound by the tensor pipe: per tile and row block eight QK^T MMAs of 48
 // cycles (N = 64 is bound by reading the operands from shared memory) and four
 // PV MMAs of 64, so 1280 cycles for both blocks of a tile of some 1500 measured
-// (8 sequences of 32K, 70B heads: 561 us in a captured graph, 562 to 580 call
-// after call, by the card; 64 sequences of 8B: 122 us; one of 2048: 25 us). That
+// (8 sequences of 32K, 70B heads: 557 us in a captured graph, 560 to 580 call
+// after call, by the card; 64 sequences of 8B: 121 us; one of 2048: 25 us). That
 // holds while the two blocks' softmaxes run half a tile apart, as they do in this
 // build: nothing here orders them. Builds of the same loop in which they ran
 // together took 1900 (710 us; 743 us and 149 us at 8B with nothing changed but
