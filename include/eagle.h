@@ -523,6 +523,103 @@ int eagle_token_logprobs(const eagle_tree_cfg* cfg, void* ws, size_t ws_bytes, i
                          const int32_t* tokens, int n_alt, float* logprob, int32_t* rank, float* entropy,
                          int32_t* alt_ids, float* alt_logprobs, void* stream);
 
+/* ------------------------------------------- 8-bit rows and products --- */
+/*
+ * Rows and weights in 8 bits: e4m3 codes with a power-of-two scale for each 128
+ * entries of a row, or each block of 128 x 128 entries of a weight, held as the
+ * byte e of 2^(e - 127) (E8M0, 255 is NaN): the form that the block-scaled
+ * tensor instructions read. A row of `dim` entries has its codes one after the
+ * other and its scales in eagle_fp8_scale_stride(dim) bytes: one for each block,
+ * the last of them partial, filled up to a multiple of four. Not on the pages:
+ * every draft step reads the LM head whole [notes EAGLE 方法: the draft model
+ * reuses the target model's LM head], and these are half its bytes at twice its
+ * rate.
+ */
+/* Scale bytes of a row of `dim` entries: ceil(dim / 128) rounded up to a multiple of four (0: dim < 1). */
+int eagle_fp8_scale_stride(int dim);
+
+/*
+ * Rows to codes and scales: with the residual's addition and the
+ * root-mean-square norm before it (the last norm before an LM head, or before a
+ * projection), or the rows as they are.
+ *   dtype       eagle_dtype of x, residual, sum and weight.
+ *   x           [rows, dim], row r at r * row_stride elements (row_stride >=
+ *               dim, a multiple of 16 bytes).
+ *   residual    [rows, dim] with the same row_stride, or NULL.
+ *   sum         out, the same layout, or NULL (it needs a residual): x +
+ *               residual, rounded once. May be x or residual itself.
+ *   weight      [dim], or NULL: no norm, the rows (or sums) are coded as they are.
+ *   eps         added to the mean square, a positive normal number (weight NULL: unused).
+ *   codes       [rows, dim] out. scales [rows, eagle_fp8_scale_stride(dim)] out,
+ *               the bytes past the last block 0.
+ * With s the row (x, or x + residual rounded to dtype), y = s / sqrt(mean(s^2) +
+ * eps) * weight in fp32. Per block of 128: the scale is the smallest power of
+ * two, at least 2^-126, with max |y| <= 448 scale, and a code y / scale rounded
+ * to the nearest e4m3 value (ties to even). A block with a NaN or an infinity
+ * in y (each block of a row whose s has one, with a norm) gets NaN codes, scale
+ * 1 and raises status 1.
+ *   ws          any eagle workspace whose status word receives device faults, or NULL.
+ * dim a multiple of 16 up to 16384; pointers but scales' 16-byte aligned.
+ */
+int eagle_rmsnorm_fp8(int rows, int dim, int dtype, const void* x, int64_t row_stride, const void* residual, void* sum,
+                      const void* weight, float eps, void* codes, uint8_t* scales, void* ws, void* stream);
+
+/*
+ * out[m, n] = sum_k x[m, k] w[n, k]: an LM head, or a projection of a draft
+ * layer, on rows and weights of codes and scales.
+ *   x_codes   [rows, in_dim], x_scales [rows, eagle_fp8_scale_stride(in_dim)] in.
+ *   w_codes   [out_dim, in_dim], w_scales [ceil(out_dim / 128),
+ *             eagle_fp8_scale_stride(in_dim)] in: one scale for 128 rows and 128 entries.
+ *   out       [rows, out_dim] out in out_dtype: fp32 sums of the products on the
+ *             tensor cores (order unspecified), rounded once for bf16. NaN codes
+ *             or scales make the outputs that read them NaN.
+ *   ws        any eagle workspace whose status word receives device faults (2: a
+ *             wait gave up), or NULL.
+ * in_dim a multiple of 16; code pointers and out 16-byte aligned, scales 4-byte aligned.
+ */
+int eagle_linear_fp8(int rows, int out_dim, int in_dim, const void* x_codes, const uint8_t* x_scales,
+                     const void* w_codes, const uint8_t* w_scales, int out_dtype, void* out, void* ws, void* stream);
+
+/* The 8-bit form of a bf16 weight [out_dim, in_dim], in_dim a multiple of 16: scales and codes of
+ * eagle_rmsnorm_fp8's rule over blocks of 128 x 128 (a block with a NaN or infinity: NaN codes, scale 1). */
+int eagle_linear_fp8_pack(int out_dim, int in_dim, const void* weight, void* codes, uint8_t* scales, void* stream);
+
+/* ------------------------------------------------- training the draft --- */
+/*
+ * The loss that trains a draft on its target's top logits, and its gradient, in
+ * one pass (not on the pages: the draft's rows are those of eagle_lmhead or
+ * eagle_linear_fp8, the target's lists those of eagle_lmhead_topk and
+ * eagle_shard_merge).
+ *   logits           [rows, V] in cfg->logit_dtype: the draft's.
+ *   n_top            entries of the target's list, 1..256.
+ *   teacher_ids      [rows, n_top] int32 in, no id twice; a negative one is padding.
+ *   teacher_logits   [rows, n_top] fp32 in.
+ *   teacher_lse      [rows] fp32 in, or NULL: log-sum-exp of the target's whole
+ *                    row divided by the temperature (at temperature 1 the
+ *                    row_lse that comes with the list).
+ *   temperature      T, a positive normal number; both rows are divided by it.
+ *   row_weight       [rows] fp32 in, or NULL (1 each): a row of weight 0 is not
+ *                    read, its loss and gradient are 0.
+ *   loss             [rows] fp32 out. dlogits [rows, V] out in cfg->logit_dtype,
+ *                    or NULL (the loss alone); may be `logits` itself.
+ * With q the draft's softmax(logits / T) and p the target's probabilities of its
+ * list, exp(t / T - teacher_lse), or, without teacher_lse, normalised over the
+ * list (the list taken for the whole distribution; a row with padding alone has
+ * loss and gradient 0):
+ *   loss = weight * (sum p (ln p - ln q) + r (ln r - ln q_R)),
+ * r = max(0, 1 - sum p) what the list leaves and q_R the draft's probability of
+ * everything else (the r term only with teacher_lse, and where r and q_R are
+ * above 0); dlogits = d loss / d logits, fp32 rounded once. Multiply the weights
+ * by T^2 for the usual scale at other temperatures.
+ * A row with a NaN or +inf logit or no finite one, a NaN or infinite weight or
+ * lse, or a list with a NaN, a +inf or no finite logit raises status 1; an id >=
+ * V or twice in a list status 3: its loss is NaN, its gradient 0. Of `cfg` only
+ * vocab and logit_dtype matter here, of `ws` the status word.
+ */
+int eagle_distill_loss(const eagle_tree_cfg* cfg, void* ws, size_t ws_bytes, int rows, int n_top, const void* logits,
+                       const int32_t* teacher_ids, const float* teacher_logits, const float* teacher_lse,
+                       float temperature, const float* row_weight, float* loss, void* dlogits, void* stream);
+
 /* ------------------------------------------------- vocabulary shards --- */
 /*
  * When the LM head is split over several GPUs by vocabulary rows, each GPU

@@ -543,6 +543,65 @@ int eagle_token_logprobs(const eagle_tree_cfg* cfg, void* ws, size_t ws_bytes, i
     return launch_result(launch_token_logprobs(a, d.dtype, static_cast<cudaStream_t>(stream)));
 }
 
+int eagle_fp8_scale_stride(int dim) { return dim < 1 ? 0 : fp8_scale_stride(dim); }
+
+int eagle_rmsnorm_fp8(int rows, int dim, int dtype, const void* x, int64_t row_stride, const void* residual, void* sum,
+                      const void* weight, float eps, void* codes, uint8_t* scales, void* ws, void* stream) {
+    EAGLE_CALL(stream, ws);
+    if (rows < 1 || dim < 1 || (dtype != EAGLE_F32 && dtype != EAGLE_BF16) || !x || !codes || !scales ||
+        row_stride < dim || (sum && !residual) || (weight && (!(eps >= 0x1p-126f) || !std::isfinite(eps))))
+        return EAGLE_ERR_INVALID_ARG;
+    if (dim % 16 != 0 || dim > kFp8MaxNormDim || rows > (1 << 24) || row_stride >= (int64_t{1} << 32) ||
+        row_stride % (dtype == EAGLE_BF16 ? 8 : 4) != 0 || !aligned16(x) || !aligned16(residual) || !aligned16(sum) ||
+        !aligned16(weight) || !aligned16(codes))
+        return EAGLE_ERR_UNSUPPORTED;
+    const RmsnormFp8Args a{rows, dim, fp8_scale_stride(dim), row_stride, x,     residual, weight,
+                           sum,  eps, codes,                 scales,     static_cast<int*>(ws)};
+    return launch_result(launch_rmsnorm_fp8(a, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int eagle_linear_fp8(int rows, int out_dim, int in_dim, const void* x_codes, const uint8_t* x_scales,
+                     const void* w_codes, const uint8_t* w_scales, int out_dtype, void* out, void* ws, void* stream) {
+    EAGLE_CALL(stream, ws);
+    if (rows < 1 || out_dim < 1 || in_dim < 1 || !x_codes || !x_scales || !w_codes || !w_scales || !out ||
+        (out_dtype != EAGLE_F32 && out_dtype != EAGLE_BF16))
+        return EAGLE_ERR_INVALID_ARG;
+    if (in_dim % 16 != 0 || rows > (1 << 20) || out_dim > (1 << 24) || in_dim > (1 << 20) || !aligned16(x_codes) ||
+        !aligned16(w_codes) || !aligned16(out) || (reinterpret_cast<uintptr_t>(x_scales) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(w_scales) & 3u) != 0)
+        return EAGLE_ERR_UNSUPPORTED;
+    return launch_result(launch_linear_fp8(rows, out_dim, in_dim, x_codes, x_scales, w_codes, w_scales, out_dtype, out,
+                                           static_cast<int*>(ws), static_cast<cudaStream_t>(stream)));
+}
+
+int eagle_linear_fp8_pack(int out_dim, int in_dim, const void* weight, void* codes, uint8_t* scales, void* stream) {
+    EAGLE_CALL(stream, nullptr);
+    if (out_dim < 1 || in_dim < 1 || !weight || !codes || !scales) return EAGLE_ERR_INVALID_ARG;
+    if (in_dim % 16 != 0 || out_dim > 65535 * kFp8Block || in_dim > (1 << 20) || !aligned16(weight) || !aligned16(codes))
+        return EAGLE_ERR_UNSUPPORTED;
+    return launch_result(launch_fp8_pack(out_dim, in_dim, fp8_scale_stride(in_dim), weight, codes, scales,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+int eagle_distill_loss(const eagle_tree_cfg* cfg, void* ws, size_t ws_bytes, int rows, int n_top, const void* logits,
+                       const int32_t* teacher_ids, const float* teacher_logits, const float* teacher_lse,
+                       float temperature, const float* row_weight, float* loss, void* dlogits, void* stream) {
+    EAGLE_CALL(stream, ws);
+    TreeDims d;
+    TreeWs w;
+    int rc = resolve(cfg, &d);
+    if (rc == EAGLE_OK) rc = bind_ws(d, ws, ws_bytes, &w);
+    if (rc != EAGLE_OK) return rc;
+    if (rows < 1 || n_top < 1 || !logits || !teacher_ids || !teacher_logits || !loss || !(temperature >= 0x1p-126f) ||
+        !std::isfinite(temperature))
+        return EAGLE_ERR_INVALID_ARG;
+    if (n_top > kDistillMaxTop || rows > (1 << 24) || !aligned16(logits) || !aligned16(dlogits))
+        return EAGLE_ERR_UNSUPPORTED;
+    const DistillArgs a{rows,        d.V,        n_top, temperature, logits, teacher_ids, teacher_logits,
+                        teacher_lse, row_weight, loss,  dlogits,     w.status};
+    return launch_result(launch_distill(a, d.dtype, static_cast<cudaStream_t>(stream)));
+}
+
 int eagle_status_fetch(void* ws, int* device_status, void* stream) {
     if (ws == nullptr || device_status == nullptr) return EAGLE_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -1,5 +1,6 @@
-// Launchers of the 8-bit KV cache, the 4-bit LM head and the token
-// log-probabilities. Not part of the public ABI.
+// Launchers of the 8-bit KV cache, the 4-bit LM head, the 8-bit product and
+// norm, the token log-probabilities and the distillation loss. Not part of the
+// public ABI.
 #pragma once
 
 #include "eagle_ws.h"
@@ -42,5 +43,39 @@ struct LogprobArgs {
     int* status;
 };
 cudaError_t launch_token_logprobs(const LogprobArgs& a, int dtype, cudaStream_t stream);
+
+// Rows of e4m3 codes with a power-of-two scale (a byte, E8M0) for each 128 entries.
+constexpr int kFp8Block = 128;
+constexpr int kFp8MaxNormDim = 16384;  // a row's entries in the registers of 1024 threads
+inline int fp8_scale_stride(int dim) { return (dim + 4 * kFp8Block - 1) / (4 * kFp8Block) * 4; }
+struct RmsnormFp8Args {
+    int rows, dim, scale_stride;
+    int64_t row_stride;  // elements
+    const void *x, *residual, *weight;
+    void* sum;
+    float eps;
+    void* codes;
+    uint8_t* scales;
+    int* status;
+};
+cudaError_t launch_rmsnorm_fp8(const RmsnormFp8Args& a, int dtype, cudaStream_t stream);
+cudaError_t launch_fp8_pack(int N, int K, int scale_stride, const void* weight, void* codes, uint8_t* scales,
+                            cudaStream_t stream);
+// out [M, N] = x [M, K] w [N, K]^T, both of codes and scales.
+cudaError_t launch_linear_fp8(int M, int N, int K, const void* x, const uint8_t* x_scales, const void* w,
+                              const uint8_t* w_scales, int out_dtype, void* out, int* status, cudaStream_t stream);
+
+constexpr int kDistillMaxTop = 256;  // a teacher's list: one thread of a CTA for each entry
+struct DistillArgs {
+    int rows, V, n_top;
+    float temperature;
+    const void* logits;
+    const int32_t* ids;
+    const float *teacher, *teacher_lse, *row_weight;
+    float* loss;
+    void* grad;
+    int* status;
+};
+cudaError_t launch_distill(const DistillArgs& a, int dtype, cudaStream_t stream);
 
 }  // namespace eagle

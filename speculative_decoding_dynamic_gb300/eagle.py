@@ -133,6 +133,11 @@ _lib.eagle_kvq_tree_attention.argtypes = [_QP, _i, _p, _p, _p, _i, _p, _p, _p, _
 _lib.eagle_lmhead_quant.argtypes = [_TP, _p, _sz, _i, _i, _p, _p, _p, _p, _p]
 _lib.eagle_lmhead_quant_pack.argtypes = [_i, _i, _i, _p, _p, _p, _p]
 _lib.eagle_token_logprobs.argtypes = [_TP, _p, _sz, _i, _i, _i, _p, ctypes.c_float, _p, _p, _i, _p, _p, _p, _p, _p, _p]
+_lib.eagle_fp8_scale_stride.argtypes = [_i]
+_lib.eagle_rmsnorm_fp8.argtypes = [_i, _i, _i, _p, _i64, _p, _p, _p, ctypes.c_float, _p, _p, _p, _p]
+_lib.eagle_linear_fp8.argtypes = [_i, _i, _i, _p, _p, _p, _p, _i, _p, _p, _p]
+_lib.eagle_linear_fp8_pack.argtypes = [_i, _i, _p, _p, _p, _p]
+_lib.eagle_distill_loss.argtypes = [_TP, _p, _sz, _i, _i, _p, _p, _p, _p, ctypes.c_float, _p, _p, _p, _p]
 _lib.eagle_kernel_launches.restype = ctypes.c_uint64
 _lib.eagle_last_cuda_error.argtypes = [ctypes.POINTER(ctypes.c_char_p)]
 _lib.eagle_last_cuda_error.restype = _i
@@ -454,6 +459,70 @@ def eagle_token_logprobs(cfg, ws, n_seq, per_seq, rows_per_seq, logits, temperat
                                          _need(fn, "alt_ids", alt_ids, _I32, n * n_alt, dev),
                                          _need(fn, "alt_logprobs", alt_logprobs, _F32, n * n_alt, dev),
                                          _stream_on(stream, dev)))
+
+
+def eagle_fp8_scale_stride(dim: int) -> int:
+    return int(_lib.eagle_fp8_scale_stride(dim))
+
+
+def _dtypes(code):
+    return _BF16 if code == EAGLE_BF16 else _F32
+
+
+_EXP = tuple(t for t in (torch.uint8, getattr(torch, "float8_e8m0fnu", None)) if t is not None)
+
+
+def alloc_fp8(rows: int, dim: int, scale_rows: int | None = None, device="cuda") -> tuple[torch.Tensor, torch.Tensor]:
+    """Codes [rows, dim] and scale bytes of 8-bit rows (a weight's, one scale row for 128 rows: scale_rows)."""
+    n = rows if scale_rows is None else scale_rows
+    return (torch.zeros(rows, dim, dtype=torch.uint8, device=device),
+            torch.zeros(n, eagle_fp8_scale_stride(dim), dtype=torch.uint8, device=device))
+
+
+def eagle_rmsnorm_fp8(rows, dim, dtype, x, row_stride, residual, sum, weight, eps, codes, scales, ws=None, stream=None):
+    """Residual, root-mean-square norm and 8-bit codes with a scale for each 128 entries (weight None: no norm)."""
+    fn, dev, dt = "eagle_rmsnorm_fp8", _device(), _dtypes(dtype)
+    n = (rows - 1) * row_stride + dim
+    _check(fn, _lib.eagle_rmsnorm_fp8(rows, dim, dtype, _need(fn, "x", _behind(x), dt, n, dev), row_stride,
+                                      _need(fn, "residual", _behind(residual), dt, n, dev),
+                                      _need(fn, "sum", _behind(sum), dt, n, dev), _need(fn, "weight", weight, dt, dim, dev),
+                                      float(eps), _need(fn, "codes", codes, _CODES, rows * dim, dev),
+                                      _need(fn, "scales", scales, _EXP, rows * eagle_fp8_scale_stride(dim), dev),
+                                      None if ws is None else _ws_on(fn, ws, dev)[0], _stream_on(stream, dev)))
+
+
+def eagle_linear_fp8(rows, out_dim, in_dim, x_codes, x_scales, w_codes, w_scales, out_dtype, out, ws=None, stream=None):
+    """out [rows, out_dim] = x w^T on 8-bit codes with power-of-two scales."""
+    fn, dev, stride = "eagle_linear_fp8", _device(), eagle_fp8_scale_stride(in_dim)
+    _check(fn, _lib.eagle_linear_fp8(rows, out_dim, in_dim, _need(fn, "x_codes", x_codes, _CODES, rows * in_dim, dev),
+                                     _need(fn, "x_scales", x_scales, _EXP, rows * stride, dev),
+                                     _need(fn, "w_codes", w_codes, _CODES, out_dim * in_dim, dev),
+                                     _need(fn, "w_scales", w_scales, _EXP, -(-out_dim // 128) * stride, dev), out_dtype,
+                                     _need(fn, "out", out, _dtypes(out_dtype), rows * out_dim, dev),
+                                     None if ws is None else _ws_on(fn, ws, dev)[0], _stream_on(stream, dev)))
+
+
+def eagle_linear_fp8_pack(out_dim, in_dim, weight, codes, scales, stream=None):
+    fn, dev, n = "eagle_linear_fp8_pack", _device(), out_dim * in_dim
+    _check(fn, _lib.eagle_linear_fp8_pack(out_dim, in_dim, _need(fn, "weight", weight, _BF16, n, dev),
+                                          _need(fn, "codes", codes, _CODES, n, dev),
+                                          _need(fn, "scales", scales, _EXP,
+                                                -(-out_dim // 128) * eagle_fp8_scale_stride(in_dim), dev),
+                                          _stream_on(stream, dev)))
+
+
+def eagle_distill_loss(cfg, ws, rows, n_top, logits, teacher_ids, teacher_logits, teacher_lse, temperature, row_weight,
+                       loss, dlogits=None, stream=None):
+    """Loss of a draft's rows against its target's top logits, and (dlogits) its gradient."""
+    fn, dev, n, dt = "eagle_distill_loss", _device(), rows * n_top, _logit_dtypes(cfg)
+    _check(fn, _lib.eagle_distill_loss(ctypes.byref(cfg), *_ws_on(fn, ws, dev), rows, n_top,
+                                       _need(fn, "logits", logits, dt, rows * cfg.vocab, dev),
+                                       _need(fn, "teacher_ids", teacher_ids, _I32, n, dev),
+                                       _need(fn, "teacher_logits", teacher_logits, _F32, n, dev),
+                                       _need(fn, "teacher_lse", teacher_lse, _F32, rows, dev), float(temperature),
+                                       _need(fn, "row_weight", row_weight, _F32, rows, dev),
+                                       _need(fn, "loss", loss, _F32, rows, dev),
+                                       _need(fn, "dlogits", dlogits, dt, rows * cfg.vocab, dev), _stream_on(stream, dev)))
 
 
 def eagle_status_fetch(ws, stream=None) -> int:
