@@ -11,23 +11,32 @@
 // As in the 16-bit LM head the product is computed as w x^T: 128 weight rows
 // fill the MMA's 128 lanes, Nr rows of x its columns, so few rows cost few
 // columns.
-//   tile (vt, rc)   weight rows 128 vt .. against rows Nr rc .. of x, summed
-//                   over K in stages of 128 codes (128-byte rows, 128B swizzle)
-//   warp 0          one lane streams the boxes of w and x into a ring (TMA)
-//   warp 1          one lane issues the MMAs into an fp32 accumulator in tensor
-//                   memory, double buffered across tiles, and the copies of the
-//                   scale words into tensor memory (tcgen05.cp)
+//   tile            weight rows 128 vt .. against a chunk of x rows, summed over
+//                   K in stages of 128 codes (128-byte rows, 128B swizzle)
+//   warp 0          streams the boxes of w and x into a ring (TMA)
+//   warp 1          issues the MMAs into fp32 accumulators in tensor memory and
+//                   the copies of the scale words into it (tcgen05.cp)
 //   warp 2          lays the scale words out for those copies, one group of
 //                   K = 512 after the other
-//   warps 4..7      read the accumulator and store the outputs
+//   warps 4..11     read the accumulators and store the outputs
 // Rows and columns past the operands' ends arrive as zeros and are not stored.
+//
+// Many rows (CG = 2): two CTAs share an MMA of 256 weight rows (cta_group::2),
+// each holding its 128 of them and half of the rows of x; the first of the pair
+// issues. A stage's weights meet two accumulators of Nr <= 224 rows each, so a
+// tile is 256 x 448.
+// Few rows (CG = 1): one accumulator per tile, two tiles deep; where there are
+// fewer tiles than SMs a cluster's CTAs each take a part of a tile's K and
+// their sums meet in distributed shared memory, added in the CTAs' order.
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
+#include "eagle_internal.cuh"
 #include "eagle_ws.h"
 #include "quant_ptx.cuh"
 #include "quant_ws.h"
@@ -36,26 +45,41 @@
 namespace eagle {
 namespace {
 
-constexpr int kTileN = 128;   // weight rows of a tile (MMA M)
+constexpr int kTileN = 128;   // weight rows of a CTA's tile (the MMA's M is 128 a CTA)
 constexpr int kStageK = 128;  // codes of K of a stage
-constexpr int kMaxNr = 224;   // rows of x of a tile (MMA N): two accumulators and the scales fit in 512 columns
-constexpr int kMaxStages = 12;
-constexpr int kSfSlots = 4;   // groups of scale words (K = 512) on their way
+constexpr int kGroup = 4;     // stages of a word of scales, K = 512: the ring holds one or two groups
+constexpr int kMaxNr = 224;   // rows of x of an accumulator (MMA N): two accumulators and the scales fit in 512 columns
+constexpr int kMaxNr1 = 64;   // (CG = 1)
+constexpr int kMaxStages = 2 * kGroup;
+constexpr int kSfSlots = 3;   // groups of scale words on their way
 constexpr int kSfBytes = 512; // scale words of 128 rows and K = 512
-constexpr int kLinThreads = 256;
+constexpr int kEpiWarps = 8;
+constexpr int kLinThreads = 128 + 32 * kEpiWarps;
 constexpr int kWBytes = kTileN * kStageK;
-constexpr int kSmemBudget = 224 * 1024;
+constexpr int kOutBytes = 32768;  // (CG = 2) outputs on their way to memory: four boxes (fp32: two) a warp
+constexpr int kSmemBudget = 226 * 1024;
+constexpr int kMaxSplit = 8;
+constexpr int kMaxDevices = 64;
+// An MMA cuts what it adds to a sum to fp32's last place, so long sums come out smaller (K = 8192: 1.3e-6 of the
+// outputs' norm): fp32 outputs are summed in tensor memory over K = 2048 (CG = 1) or 4096, and those sums in fp32.
+constexpr int kF32Chunk1 = 16, kF32Chunk2 = 32;
 
 struct LinParams {
     int M, N, K;
-    int Nr, nrc;      // rows of x of a tile, row chunks
+    int Nr;           // rows of x of an accumulator
+    int nrc;          // row chunks (of a tile's accumulators)
     int ntiles;
-    int nk, ngroups;  // stages and groups of scale words of a tile
-    int stages, stage_bytes;
-    int sf_blocks;    // 128-row blocks of x scale words of a tile
+    int nwt;          // 128-row tiles of the weight
+    int split;        // CTAs of a cluster that share a tile's K (CG = 1)
+    int nk;           // stages of a tile
+    int per;          // stages of a CTA (whole groups)
+    int chunk;        // stages summed in tensor memory (whole groups)
+    int ring;         // groups of the ring
+    int stage_bytes;
+    int sf_blocks;    // 128-row blocks of scale words of an accumulator's rows
     int sf_row_words; // scale words of a row
     uint32_t acc_stride, sf_col, sf_cols, tmem_cols;
-    int out_bf16;
+    int bulk_out;     // the output's rows allow bulk stores (16-byte rows)
     const uint32_t *x_scales, *w_scales;
     void* out;
     int* status;
@@ -66,27 +90,152 @@ struct LinParams {
 __host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N) {
     return (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_mxf8(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+// Operands by the low words of their descriptors (address and leading offset); the high word is the same for all.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+template <int CG>
+__device__ __forceinline__ void mma_mxf8(uint32_t tmem_d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sfa,
                                          uint32_t sfb, int accum) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(tmem_d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accum)
-        : "memory");
+    if (CG == 1)
+        asm volatile(
+            "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %6, 0;\n mov.b64 da, {%1, %7};\n mov.b64 db, {%2, %7};\n"
+            " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], da, db, %3, [%4], [%5], p;\n}" ::"r"(tmem_d),
+            "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accum), "r"(kDescHi)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %6, 0;\n mov.b64 da, {%1, %7};\n mov.b64 db, {%2, %7};\n"
+            " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], da, db, %3, [%4], [%5], p;\n}" ::"r"(tmem_d),
+            "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accum), "r"(kDescHi)
+            : "memory");
 }
 // Descriptor of 32 rows of 16 bytes, one after the other (no swizzle): 8-row groups 128 bytes apart.
 __device__ __forceinline__ uint64_t sf_desc(uint32_t saddr) {
     return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 16) |
            (static_cast<uint64_t>(128 >> 4) << 32) | (1ull << 46);
 }
-// Those 512 bytes into four columns of tensor memory, the same in each quarter of its lanes.
+// Those 512 bytes into four columns of tensor memory, the same in each quarter of its lanes (of a
+// pair: each CTA's bytes into its own).
+template <int CG>
 __device__ __forceinline__ void copy_sf(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    if (CG == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// An arrival on `bar` (of a pair: on both CTAs' barriers) when the MMAs and copies so far have ended.
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if (CG == 1)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// A bounded wait by a whole warp, whose lanes leave it together, for arrivals from the other CTA of a pair as
+// well. Without the hint of how long to sleep: that cost some 30 clocks a stage.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+    for (uint32_t i = 0; i < (1u << 21); ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (__all_sync(0xffffffffu, ok)) return true;
+    }
+    return false;
+}
+// The same for warps that wait long.
+__device__ __forceinline__ bool wait_warp_sleep(uint32_t bar, uint32_t parity) {
+    for (uint32_t i = 0; i < (1u << 16); ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(20000u)
+            : "memory");
+        if (__all_sync(0xffffffffu, ok)) return true;
+    }
+    return false;
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
+template <int CG>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
+    else  // into this CTA's memory, counted on the barrier of the pair's first
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
+}
+__device__ __forceinline__ void store_remote(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// 16 rows of the output from `o` on, rows n elements apart, `live` of them.
+template <typename T>
+__device__ __forceinline__ void store_rows(T* o, int64_t n, int live, const float* x) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        if (j < live) {
+            if (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat16*>(o) = __float2bfloat16_rn(x[j]);
+            else *reinterpret_cast<float*>(o) = x[j];
+        }
+        o += n;
+    }
+}
+// A box of the output from shared memory, stored or (fp32) added to what is there.
+__device__ __forceinline__ void store_block(const CUtensorMap* map, uint32_t src, int c0, int c1, bool add) {
+    if (add)
+        asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                         reinterpret_cast<uint64_t>(map)),
+                     "r"(c0), "r"(c1), "r"(src)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                         reinterpret_cast<uint64_t>(map)),
+                     "r"(c0), "r"(c1), "r"(src)
+                     : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// Blocks of 16 columns of an accumulator that the warps of one half read.
+constexpr int kHalfBlocks = kMaxNr / 32, kHalfBlocks1 = kMaxNr1 / 32;
+__device__ __forceinline__ int half_first(int Nr, int half) { return half ? (Nr / 16 + 1) / 2 : 0; }
+__device__ __forceinline__ int half_count(int Nr, int half) { return half ? Nr / 32 : (Nr / 16 + 1) / 2; }
+
+// CG: CTAs that share an MMA. NSUB: accumulators of a tile.
+template <int CG, int NSUB, bool BF16>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_fp8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-                      const LinParams p) {
+                      const __grid_constant__ CUtensorMap tm_out, const LinParams p) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -94,204 +243,476 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         bar_sf_empty[kSfSlots], bar_acc_full[2], bar_acc_empty[2];
     __shared__ uint32_t tmem_holder;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    unsigned char* sf_smem = smem + p.stages * p.stage_bytes;
-    const int sf_slot_bytes = kSfBytes * (1 + p.sf_blocks);
+    const int ncta = CG == 2 ? 2 : p.split;  // CTAs of the cluster
+    const int rank = blockIdx.x % ncta;
+    const int lead = CG == 2 ? 0 : rank;     // who issues this CTA's MMAs
+    const int unit = blockIdx.x / ncta, nunits = gridDim.x / ncta;
+    const int k0 = CG == 2 ? 0 : rank * p.per, k1 = min(p.nk, k0 + p.per);
+    unsigned char* out_smem = smem + kGroup * p.ring * p.stage_bytes;
+    unsigned char* sf_smem = out_smem + (CG == 2 ? kOutBytes : 0);
+    const int sf_slot_bytes = kSfBytes * (1 + NSUB * p.sf_blocks);
 
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < p.stages; ++s) {
+        for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(&bar_full[s], 1);
             mbar_init(&bar_empty[s], 1);
         }
         for (int s = 0; s < kSfSlots; ++s) {
-            mbar_init(&bar_sf_full[s], 32);
+            mbar_init(&bar_sf_full[s], 32 * CG);
             mbar_init(&bar_sf_empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bar_acc_full[s], 1);
-            mbar_init(&bar_acc_empty[s], 128);
+            mbar_init(&bar_acc_empty[s], kEpiWarps * CG);
         }
         fence_mbar_init();
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_holder)),
-                     "r"(p.tmem_cols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if (CG == 1) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_holder)),
+                         "r"(p.tmem_cols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_holder)),
+                         "r"(p.tmem_cols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if (ncta > 1) cg::this_cluster().sync();  // the other CTAs' barriers are there
     tc_fence_after();
     const uint32_t tmem = tmem_holder;
     pdl_wait_prior();
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; ok && t < p.ntiles; t += gridDim.x) {
-                const int rc = t % p.nrc, vt = t / p.nrc;
-                for (int kc = 0; kc < p.nk; ++kc, ++it) {
-                    const uint32_t st = it % p.stages;
-                    if (it >= static_cast<uint32_t>(p.stages) &&
-                        !mbar_wait_sleep(&bar_empty[st], ((it / p.stages) - 1) & 1)) {
+        // ------------------------------------------------------- loads ---
+        const bool issue = elect_one();  // the warp goes through its loops together, one lane issues (see warp 1)
+        const uint32_t full = smem_u32(bar_full), empty = smem_u32(bar_empty), smem0 = smem_u32(smem);
+        const uint32_t full_at = CG == 2 ? cluster_addr(bar_full, 0) : full;
+        const uint32_t bytes = static_cast<uint32_t>(p.stage_bytes) * CG;
+        const int xbox = p.Nr / CG;  // rows of x in a box
+        uint32_t half = 0, phase = 1;  // group of the ring and the parity of its last use (none yet: passes)
+        bool ok = true;
+        for (int t = unit; ok && t < p.ntiles; t += nunits) {
+            const int rc = t % p.nrc, vt = t / p.nrc;
+            const int w0 = (CG * vt + (CG == 2 ? rank : 0)) * kTileN;
+            const int x0 = rc * NSUB * p.Nr + (CG == 2 ? rank * xbox : 0);
+            for (int kg = k0; kg < k1; kg += kGroup) {
+#pragma unroll
+                for (int i = 0; i < kGroup; ++i) {
+                    const uint32_t st = half * kGroup + i;
+                    if (!wait_warp(empty + st * 8, phase)) {
                         ok = false;
                         break;
                     }
-                    unsigned char* dst = smem + st * p.stage_bytes;
-                    mbar_arrive_expect_tx(&bar_full[st], p.stage_bytes);
-                    tma_load_2d(dst, &tm_w, kc * kStageK, vt * kTileN, &bar_full[st]);
-                    tma_load_2d(dst + kWBytes, &tm_x, kc * kStageK, rc * p.Nr, &bar_full[st]);
+                    if (issue) {
+                        if (kg + i < k1) {
+                            const uint32_t dst = smem0 + st * p.stage_bytes, bar = full_at + st * 8;
+                            const int k = (kg + i) * kStageK;
+                            if (rank == lead) mbar_arrive_expect_tx(&bar_full[st], bytes);
+                            load_box<CG>(dst, &tm_w, k, w0, bar);
+#pragma unroll
+                            for (int a = 0; a < NSUB; ++a)
+                                load_box<CG>(dst + kWBytes + a * xbox * kStageK, &tm_x, k, x0 + a * p.Nr, bar);
+                        } else if (rank == lead) {  // a group's stages past K: nothing to load
+                            mbar_arrive(&bar_full[st]);
+                        }
+                    }
+                }
+                if (!ok) break;
+                if (++half == static_cast<uint32_t>(p.ring)) {
+                    half = 0;
+                    phase ^= 1;
                 }
             }
-            if (!ok) raise_status(p.status, kDevTimeout);
-            // the CTA does not end before its copies have arrived
-            for (uint32_t i = it > static_cast<uint32_t>(p.stages) ? it - p.stages : 0u; i < it; ++i)
-                if (!mbar_wait_sleep(&bar_full[i % p.stages], (i / p.stages) & 1)) break;
         }
-        __syncwarp();
+        if (!ok && issue) raise_status(p.status, kDevTimeout);
+        // The CTA does not end before the MMAs that read its last stages, and their arrivals, are done. (Where a
+        // wait has given up, the copies have had its limit, far more than they take.)
+        for (int s = 0; ok && s < kGroup * p.ring; ++s) {
+            ok = wait_warp(empty + (half * kGroup + s % kGroup) * 8, phase);
+            if (s % kGroup == kGroup - 1 && ++half == static_cast<uint32_t>(p.ring)) {
+                half = 0;
+                phase ^= 1;
+            }
+        }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_mxf8(kTileN, p.Nr);
-            uint32_t it = 0, gr = 0;
+        // -------------------------------------------------------- MMAs ---
+        if (rank == lead) {
+            // The warp goes through the loops together and one lane issues, so that descriptors, addresses and
+            // the loops' conditions stay in uniform registers: a lane on its own took 720 clocks a stage, whatever
+            // its MMAs' size, and 1050 with divisions for stage and parity (four MMAs of 224 rows take 448). A
+            // group's four stages are unrolled, their places in the ring fixed.
+            const uint32_t idesc = idesc_mxf8(kTileN * CG, p.Nr);
+            const bool issue = elect_one();
+            const uint32_t full = smem_u32(bar_full), empty = smem_u32(bar_empty);
+            const uint32_t sf_full = smem_u32(bar_sf_full), sf_empty = smem_u32(bar_sf_empty);
+            const uint32_t acc_full = smem_u32(bar_acc_full), acc_empty = smem_u32(bar_acc_empty);
+            uint32_t half = 0, phase = 0, slot = 0, sf_phase = 0;
+            uint32_t buf = 0, acc_phase = 1;  // (NSUB = 1) the accumulator; the parity of its last reading (none yet: passes)
+            const uint32_t base = ((smem_u32(smem) & 0x3FFFFu) >> 4) | (1u << 16);
+            const uint64_t sf_base = sf_desc(smem_u32(sf_smem));
+            const uint32_t step = static_cast<uint32_t>(p.stage_bytes) >> 4;
+            const uint32_t x_step = static_cast<uint32_t>(p.Nr / CG * kStageK) >> 4;
+            const uint32_t sfb_step = 4u * p.sf_blocks;
             bool ok = true;
-            int lt = 0;
-            for (int t = blockIdx.x; ok && t < p.ntiles; t += gridDim.x, ++lt) {
-                const int buf = lt & 1;
-                if (lt >= 2 && !mbar_wait_sleep(&bar_acc_empty[buf], ((lt >> 1) - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t d = tmem + buf * p.acc_stride;
-                uint32_t sfa = 0, sfb = 0;
-                for (int kc = 0; kc < p.nk; ++kc, ++it) {
-                    if ((kc & 3) == 0) {
+            for (int t = unit; ok && t < p.ntiles; t += nunits) {
+                for (int kb = k0; ok && kb < k1; kb += p.chunk) {
+                    const int ke = min(k1, kb + p.chunk);
+                    for (int kg = kb; kg < ke; kg += kGroup) {
                         // The next group's scale words into this slot's columns. The slot was filled
                         // after the MMAs that read these columns last had ended.
-                        const uint32_t slot = gr % kSfSlots;
-                        if (!mbar_wait_sleep(&bar_sf_full[slot], (gr / kSfSlots) & 1)) {
+                        if (!wait_warp(sf_full + slot * 8, sf_phase) ||
+                            (kg == kb && !wait_warp(acc_empty + buf * 8, acc_phase))) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t src = smem_u32(sf_smem + slot * sf_slot_bytes);
-                        sfa = tmem + p.sf_col + slot * p.sf_cols;
-                        sfb = sfa + 4;
-                        for (int b = 0; b <= p.sf_blocks; ++b) copy_sf(sfa + 4 * b, sf_desc(src + b * kSfBytes));
-                    }
-                    const uint32_t st = it % p.stages;
-                    if (!mbar_wait_sleep(&bar_full[st], (it / p.stages) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t aW = smem_u32(smem + st * p.stage_bytes);
-                    const uint32_t aX = aW + kWBytes;
-                    const uint32_t id = idesc | (static_cast<uint32_t>(kc & 3) << 4) | (static_cast<uint32_t>(kc & 3) << 29);
+                        const uint32_t sfa = tmem + p.sf_col + slot * p.sf_cols;
+                        const uint64_t sd = sf_base + static_cast<uint32_t>(slot * sf_slot_bytes >> 4);
+                        if (issue)
+                            for (int b = 0; b <= NSUB * p.sf_blocks; ++b) copy_sf<CG>(sfa + 4 * b, sd + b * (kSfBytes >> 4));
+                        const uint32_t first = base + half * kGroup * step;
+                        const uint32_t d = tmem + buf * p.acc_stride;
+                        const bool fresh = kg == kb;
 #pragma unroll
-                    for (int kk = 0; kk < kStageK / 32; ++kk)  // K = 32 per MMA: 32 bytes along the swizzled row
-                        mma_mxf8(d, smem_desc(aW + kk * 32, 16, 1024), smem_desc(aX + kk * 32, 16, 1024), id, sfa, sfb,
-                                 (kc > 0 || kk > 0) ? 1 : 0);
-                    mma_commit(&bar_empty[st]);
-                    if ((kc & 3) == 3 || kc == p.nk - 1) {
-                        mma_commit(&bar_sf_empty[gr % kSfSlots]);
-                        ++gr;
+                        for (int i = 0; i < kGroup; ++i) {
+                            const uint32_t st = half * kGroup + i;
+                            if (!wait_warp(full + st * 8, phase)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const uint32_t id = idesc | (static_cast<uint32_t>(i) << 4) | (static_cast<uint32_t>(i) << 29);
+                            const uint32_t aw = first + i * step;
+#pragma unroll
+                            for (int a = 0; a < NSUB; ++a) {
+                                if (a == 1 && i == 0 && fresh) {  // the second accumulator's last sums have been read
+                                    if (!wait_warp(acc_empty + 8, acc_phase)) {
+                                        ok = false;
+                                        break;
+                                    }
+                                    tc_fence_after();
+                                }
+                                if (issue) {
+                                    if (kg + i < k1) {
+                                        const uint32_t ax = aw + (kWBytes >> 4) + a * x_step;
+#pragma unroll
+                                        for (int kk = 0; kk < kStageK / 32; ++kk)  // K = 32: 32 bytes along the swizzled row
+                                            mma_mxf8<CG>(d + a * p.acc_stride, aw + 2 * kk, ax + 2 * kk, id, sfa,
+                                                         sfa + 4 + a * sfb_step, i > 0 || kk > 0 ? 1 : !fresh);
+                                    }
+                                    if (i == kGroup - 1 && kg + kGroup >= ke) commit<CG>(acc_full + (buf + a) * 8);
+                                }
+                            }
+                            if (!ok) break;
+                            if (issue) commit<CG>(empty + st * 8);
+                        }
+                        if (!ok) break;
+                        if (issue) commit<CG>(sf_empty + slot * 8);
+                        if (++half == static_cast<uint32_t>(p.ring)) {
+                            half = 0;
+                            phase ^= 1;
+                        }
+                        if (++slot == kSfSlots) {
+                            slot = 0;
+                            sf_phase ^= 1;
+                        }
+                    }
+                    if (NSUB == 2) {
+                        acc_phase ^= 1;
+                    } else {
+                        buf ^= 1;
+                        if (buf == 0) acc_phase ^= 1;
                     }
                 }
-                if (ok) mma_commit(&bar_acc_full[buf]);
             }
-            if (!ok) raise_status(p.status, kDevTimeout);
+            if (!ok && issue) raise_status(p.status, kDevTimeout);
         }
-        __syncwarp();
     } else if (warp == 2) {
-        uint32_t gr = 0;
+        // ------------------------------------------------------ scales ---
+        const uint32_t sf_empty = smem_u32(bar_sf_empty), sf_full = cluster_addr(bar_sf_full, lead);
+        uint32_t slot = 0, sf_phase = 1;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < p.ntiles; t += gridDim.x) {
-            const int rc = t % p.nrc, vt = t / p.nrc;
-            const int m0 = rc * p.Nr, mn = min(p.Nr, p.M - m0);
-            for (int g = 0; g < p.ngroups; ++g, ++gr) {
-                const uint32_t slot = gr % kSfSlots;
-                const uint32_t ww = ld_prior(p.w_scales + static_cast<size_t>(vt) * p.sf_row_words + g);
-                uint32_t xw[2][4];
+        constexpr int kBlocks = CG == 1 ? 1 : 2 * NSUB;  // 128-row blocks of x at most
+        for (int t = unit; ok && t < p.ntiles; t += nunits) {
+            const int rc = t % p.nrc, vt = min(CG * (t / p.nrc) + (CG == 2 ? rank : 0), p.nwt - 1);
+            const int m0 = rc * NSUB * p.Nr;
+            const uint32_t* wrow = p.w_scales + static_cast<size_t>(vt) * p.sf_row_words;
+            uint32_t ww = 0u, xw[kBlocks][4];
+            auto fetch = [&](int g) {
+                ww = ld_prior(wrow + g);
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int r = b * 128 + i * 32 + lane;
-                        xw[b][i] = r < mn ? ld_prior(p.x_scales + static_cast<size_t>(m0 + r) * p.sf_row_words + g) : 0u;
+                        const int a = NSUB == 2 && b >= p.sf_blocks ? 1 : 0;  // the block's accumulator
+                        const int r = (b - a * p.sf_blocks) * 128 + i * 32 + lane, m = m0 + a * p.Nr + r;
+                        xw[b][i] = r < p.Nr && m < p.M && b < NSUB * p.sf_blocks
+                                       ? ld_prior(p.x_scales + static_cast<size_t>(m) * p.sf_row_words + g)
+                                       : 0u;
                     }
-                if (gr >= kSfSlots && !__all_sync(0xffffffffu, mbar_wait_sleep(&bar_sf_empty[slot], ((gr / kSfSlots) - 1) & 1))) {
+            };
+            const int g1 = (k1 + kGroup - 1) / kGroup;
+            if (k0 < k1) fetch(k0 / kGroup);
+            for (int g = k0 / kGroup; g < g1; ++g) {
+                if (!wait_warp_sleep(sf_empty + slot * 8, sf_phase)) {
                     ok = false;
                     break;
                 }
                 const uint32_t dst = smem_u32(sf_smem + slot * sf_slot_bytes) + lane * 16;
                 sts128(dst, make_uint4(ww, ww, ww, ww));
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    if (b < p.sf_blocks) sts128(dst + (1 + b) * kSfBytes, make_uint4(xw[b][0], xw[b][1], xw[b][2], xw[b][3]));
+                for (int b = 0; b < kBlocks; ++b)
+                    if (b < NSUB * p.sf_blocks) sts128(dst + (1 + b) * kSfBytes, make_uint4(xw[b][0], xw[b][1], xw[b][2], xw[b][3]));
                 fence_proxy_async_smem();
-                mbar_arrive(&bar_sf_full[slot]);
+                arrive_at(sf_full + slot * 8);
+                if (++slot == kSfSlots) {
+                    slot = 0;
+                    sf_phase ^= 1;
+                }
+                if (g + 1 < g1) fetch(g + 1);  // on its way while the slots are full
             }
         }
         if (!ok) raise_status(p.status, kDevTimeout);
-    } else if (warp >= 4) {
-        const int q4 = warp & 3;
-        const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
-        int lt = 0;
-        for (int t = blockIdx.x; t < p.ntiles; t += gridDim.x, ++lt) {
-            const int rc = t % p.nrc, vt = t / p.nrc;
-            const int buf = lt & 1;
-            if (!__all_sync(0xffffffffu, mbar_wait_sleep(&bar_acc_full[buf], (lt >> 1) & 1))) {
-                raise_status(p.status, kDevTimeout);
-                break;
+        for (int s = 0; ok && s < kSfSlots; ++s) {
+            ok = wait_warp_sleep(sf_empty + slot * 8, sf_phase);
+            if (++slot == kSfSlots) {
+                slot = 0;
+                sf_phase ^= 1;
             }
-            tc_fence_after();
-            const int v = vt * kTileN + q4 * 32 + lane;
-            const int m0 = rc * p.Nr;
-            const int mn = min(p.Nr, p.M - m0);  // live rows of the chunk (uniform)
-            const uint32_t cols = tmem + lane_off + buf * p.acc_stride;
-            for (int c = 0; c < mn; c += 16) {
-                float x[16];
-                tmem_ld16(cols + c, x);
-                if (v < p.N) {
-                    const int jn = min(16, mn - c);
-                    const size_t at = static_cast<size_t>(m0 + c) * p.N + v;
-                    if (p.out_bf16) {
-                        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (j < jn) o[static_cast<size_t>(j) * p.N] = __float2bfloat16_rn(x[j]);
-                    } else {
-                        float* o = static_cast<float*>(p.out) + at;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (j < jn) o[static_cast<size_t>(j) * p.N] = x[j];
+        }
+    } else if (warp >= 4) {
+        // ---------------------------------------------------- epilogue ---
+        // Lane quarter warp % 4; warps 4..7 read the first half of the columns, 8..11 the second
+        const int q4 = warp & 3, half = (warp - 4) >> 2;
+        const int b0 = half_first(p.Nr, half), nb = half_count(p.Nr, half);
+        const uint32_t from = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + b0 * 16;
+        const uint32_t freed = cluster_addr(bar_acc_empty, lead), acc_full = smem_u32(bar_acc_full);
+        uint32_t buf = 0, acc_phase = 0;
+        bool ok = true;
+        auto wait_full = [&](uint32_t b) -> bool {
+            if (wait_warp_sleep(acc_full + b * 8, acc_phase)) {
+                tc_fence_after();
+                return true;
+            }
+            raise_status(p.status, kDevTimeout);
+            return ok = false;
+        };
+        auto release = [&](uint32_t b) {  // the accumulator may take its next sums
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(freed + b * 8);
+        };
+        auto next = [&]() {
+            if (NSUB == 2) {
+                acc_phase ^= 1;
+            } else {
+                buf ^= 1;
+                if (buf == 0) acc_phase ^= 1;
+            }
+        };
+        // (CG = 2) The way out, by each warp for its 32 columns: 16 rows at a time through one of its boxes in shared
+        // memory, stored from there in bulk where the output's rows allow it
+        constexpr int kBoxes = BF16 ? 4 : 2, kBoxBytes = kOutBytes / kEpiWarps / kBoxes;
+        static_assert(kBoxBytes == 16 * 32 * (BF16 ? 2 : 4), "16 rows of 32 columns");
+        const uint32_t box0 = smem_u32(out_smem) + (warp - 4) * (kOutBytes / kEpiWarps);
+        uint32_t box = 0;
+        auto box_free = [&]() {  // the box's last store has been read
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBoxes - 1) : "memory");
+            __syncwarp();
+        };
+        auto box_out = [&](int v0, int m, bool add) {
+            const uint32_t at = box0 + box * kBoxBytes;
+            if (p.bulk_out) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) store_block(&tm_out, at, v0, m, add);
+                __syncwarp();
+            } else if (v0 + lane < p.N) {
+                // this lane's own column
+                const int live = min(16, p.M - m);
+                if (BF16) {
+                    unsigned short* o = static_cast<unsigned short*>(p.out) + static_cast<size_t>(m) * p.N + v0 + lane;
+                    for (int j = 0; j < live; ++j, o += p.N) {
+                        unsigned short x;
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + j * 64 + lane * 2) : "memory");
+                        *o = x;
+                    }
+                } else {
+                    float* o = static_cast<float*>(p.out) + static_cast<size_t>(m) * p.N + v0 + lane;
+                    for (int j = 0; j < live; ++j, o += p.N) {
+                        float x;
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at + j * 128 + lane * 4) : "memory");
+                        *o = add ? *o + x : x;
                     }
                 }
             }
-            // the accumulator may take the tile after next
-            tc_fence_before();
-            mbar_arrive(&bar_acc_empty[buf]);
+            box = (box + 1) % kBoxes;
+        };
+        for (int t = unit; ok && t < p.ntiles; t += nunits) {
+            const int rc = t % p.nrc, vt = CG * (t / p.nrc) + (CG == 2 ? rank : 0);
+            const int v0 = vt * kTileN + q4 * 32, v = v0 + lane;
+            const int row = rc * NSUB * p.Nr + b0 * 16;
+            if (CG == 2 && BF16) {
+                // All accumulators are read, rounded and freed before the first store. (What does not fit in
+                // registers here goes to L2, the shared memory leaves no L1: spills took as long as the MMAs.)
+                uint32_t pk[NSUB][kHalfBlocks][8];
+#pragma unroll
+                for (int a = 0; a < NSUB; ++a) {
+                    if (!ok || !wait_full(buf + a)) break;
+#pragma unroll
+                    for (int b = 0; b < kHalfBlocks; ++b) {
+                        if (b < nb) {
+                            float x[16];
+                            tmem_ld16(from + (buf + a) * p.acc_stride + b * 16, x);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) pk[a][b][j] = pack2(x[2 * j], x[2 * j + 1]);
+                        }
+                    }
+                    release(buf + a);
+                }
+                next();
+                if (!ok) break;
+#pragma unroll
+                for (int a = 0; a < NSUB; ++a) {
+#pragma unroll
+                    for (int b = 0; b < kHalfBlocks; ++b) {
+                        const int m = row + a * p.Nr + b * 16;
+                        if (b < nb && m < p.M) {
+                            box_free();
+                            const uint32_t to = box0 + box * kBoxBytes + lane * 2;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + j * 64),
+                                             "h"(static_cast<unsigned short>((j & 1) ? pk[a][b][j >> 1] >> 16 : pk[a][b][j >> 1]))
+                                             : "memory");
+                            box_out(v0, m, false);
+                        }
+                    }
+                }
+            } else if (CG == 2) {
+                for (int kb = k0; ok && kb < k1; kb += p.chunk, next()) {
+                    // a later chunk's sums are added to the outputs, once their stores are there
+                    const bool add = kb > k0;
+                    if (add && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+#pragma unroll 1
+                    for (int a = 0; a < NSUB; ++a) {
+                        if (!wait_full(buf + a)) break;
+                        float x[kHalfBlocks][16];
+#pragma unroll
+                        for (int b = 0; b < kHalfBlocks; ++b)
+                            if (b < nb) tmem_ld16(from + (buf + a) * p.acc_stride + b * 16, x[b]);
+                        release(buf + a);
+#pragma unroll
+                        for (int b = 0; b < kHalfBlocks; ++b) {
+                            const int m = row + a * p.Nr + b * 16;
+                            if (b < nb && m < p.M) {
+                                box_free();
+                                const uint32_t to = box0 + box * kBoxBytes + lane * 4;
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + j * 128), "f"(x[b][j]) : "memory");
+                                box_out(v0, m, add);
+                            }
+                        }
+                    }
+                }
+            } else {
+                float acc[kHalfBlocks1][16];
+#pragma unroll
+                for (int b = 0; b < kHalfBlocks1; ++b)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[b][j] = 0.0f;
+                for (int kb = k0; ok && kb < k1; kb += p.chunk, next()) {
+                    if (!wait_full(buf)) break;
+#pragma unroll
+                    for (int b = 0; b < kHalfBlocks1; ++b) {
+                        if (b >= nb) continue;
+                        float x[16];
+                        tmem_ld16(from + buf * p.acc_stride + b * 16, x);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[b][j] += x[j];
+                    }
+                    release(buf);
+                }
+                if (!ok) break;
+                const int live = min(nb * 16, p.M - row);  // rows of this warp (uniform, may be negative)
+                if (p.split > 1) {
+                    // Column j's partial sums of all ranks meet in CTA j % split: slot [j / split][rank][lane].
+                    const uint32_t red = smem_u32(sf_smem + kSfSlots * sf_slot_bytes);
+                    int slot = b0 * 16 / p.split, owner = b0 * 16 % p.split;
+#pragma unroll
+                    for (int b = 0; b < kHalfBlocks1; ++b)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if (b * 16 + j < live) {
+                                const uint32_t at = red + ((slot * p.split + rank) * kTileN + q4 * 32 + lane) * 4;
+                                uint32_t to;
+                                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(owner));
+                                store_remote(to, acc[b][j]);
+                            }
+                            if (++owner == p.split) {
+                                owner = 0;
+                                ++slot;
+                            }
+                        }
+                } else if (v < p.N) {
+                    const size_t at = static_cast<size_t>(row) * p.N + v;
+#pragma unroll
+                    for (int b = 0; b < kHalfBlocks1; ++b) {
+                        if (b * 16 >= live) continue;
+                        const int64_t off = static_cast<int64_t>(b) * 16 * p.N;
+                        if (BF16) store_rows(static_cast<__nv_bfloat16*>(p.out) + at + off, p.N, live - b * 16, acc[b]);
+                        else store_rows(static_cast<float*>(p.out) + at + off, p.N, live - b * 16, acc[b]);
+                    }
+                }
+            }
         }
+        if (CG == 2 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
+    if (ncta > 1) cg::this_cluster().sync();
     tc_fence_after();
-    if (warp == 1)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols) : "memory");
+    if (CG == 1 && p.split > 1 && threadIdx.x < kTileN) {  // one tile a cluster: the ranks' sums, in their order
+        const int rc = unit % p.nrc, v = (unit / p.nrc) * kTileN + static_cast<int>(threadIdx.x);
+        const float* red = reinterpret_cast<const float*>(sf_smem + kSfSlots * sf_slot_bytes);
+        const int mn = min(p.Nr, p.M - rc * p.Nr);
+        for (int col = rank; col < mn && v < p.N; col += p.split) {
+            float s = 0.0f;
+            for (int r = 0; r < p.split; ++r) s += red[((col / p.split) * p.split + r) * kTileN + threadIdx.x];
+            const size_t at = static_cast<size_t>(rc * p.Nr + col) * p.N + v;
+            if (BF16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(s);
+            else static_cast<float*>(p.out)[at] = s;
+        }
+    }
+    if (warp == 1) {
+        if (CG == 1)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols) : "memory");
+    }
 }
 
-bool make_map_codes(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_outer) {
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
+              uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle) {
     auto fn = tensor_map_encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {inner, outer};
-    const cuuint64_t strides[1] = {inner};
-    const cuuint32_t box[2] = {kStageK, box_outer};
+    const cuuint64_t strides[1] = {row_bytes};
+    const cuuint32_t box[2] = {box_inner, box_outer};
     const cuuint32_t estride[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estride,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool make_map_codes(CUtensorMap* m, const void* base, int inner, int outer, int box_outer) {
+    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, static_cast<uint64_t>(inner), static_cast<uint64_t>(outer),
+                    static_cast<uint64_t>(inner), kStageK, static_cast<uint32_t>(box_outer), CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 int sm_count() {
@@ -305,44 +726,141 @@ int sm_count() {
     return n;
 }
 
-}  // namespace
+// How many clusters of ncta CTAs run at once (GPCs hold no whole number of them), asked once for each size and
+// device. A CTA has an SM for itself, whatever its share of the shared memory.
+template <int CG, int NSUB, bool BF16>
+cudaError_t clusters_at_once(int ncta, int* n) {
+    *n = sm_count();
+    if (ncta == 1) return cudaSuccess;
+    static std::atomic<int> known[kMaxDevices][kMaxSplit + 1];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::atomic<int>& slot = known[dev % kMaxDevices][ncta];
+    if ((*n = slot.load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    e = ensure_dyn_smem(reinterpret_cast<const void*>(linear_fp8_kernel<CG, NSUB, BF16>), kSmemBudget);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ncta);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ncta));
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = kSmemBudget;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(n, linear_fp8_kernel<CG, NSUB, BF16>, &cfg);
+    if (e == cudaSuccess && *n > 0) slot.store(*n, std::memory_order_relaxed);
+    return e;
+}
 
-cudaError_t launch_linear_fp8(int M, int N, int K, const void* x, const uint8_t* x_scales, const void* w,
-                              const uint8_t* w_scales, int out_dtype, void* out, int* status, cudaStream_t stream) {
+int round_up(int x, int to) { return (x + to - 1) / to * to; }
+
+template <int CG, int NSUB, bool BF16>
+cudaError_t launch(LinParams& p, const void* x, const void* w, cudaStream_t stream) {
+    const int ncta = CG == 2 ? 2 : p.split;
+    p.nrc = (p.M + p.Nr * NSUB - 1) / (p.Nr * NSUB);
+    p.ntiles = p.nrc * ((p.nwt + CG - 1) / CG);
+    p.stage_bytes = kWBytes + NSUB * (p.Nr / CG) * kStageK;
+    p.sf_blocks = (p.Nr + 127) / 128;
+    const int red_bytes = p.split > 1 ? (p.Nr + p.split) * kTileN * 4 : 0;
+    const int sf_bytes = kSfSlots * kSfBytes * (1 + NSUB * p.sf_blocks);
+    const int rest = 1024 + sf_bytes + red_bytes + (CG == 2 ? kOutBytes : 0);
+    p.ring = rest + 2 * kGroup * p.stage_bytes <= kSmemBudget ? 2 : 1;
+    p.sf_row_words = fp8_scale_stride(p.K) / 4;
+    p.acc_stride = static_cast<uint32_t>(round_up(p.Nr, 32));
+    p.sf_col = 2 * p.acc_stride;
+    p.sf_cols = 4u * (1 + NSUB * p.sf_blocks);
+    p.tmem_cols = 32;
+    while (p.tmem_cols < p.sf_col + kSfSlots * p.sf_cols) p.tmem_cols <<= 1;
+    CUtensorMap tw, tx, to;
+    if (!make_map_codes(&tw, w, p.K, p.N, kTileN) || !make_map_codes(&tx, x, p.K, p.M, p.Nr / CG)) return cudaErrorInvalidValue;
+    constexpr int es = BF16 ? 2 : 4;
+    p.bulk_out = CG == 2 && static_cast<int64_t>(p.N) * es % 16 == 0;
+    if (p.bulk_out) {
+        if (!make_map(&to, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.out,
+                      static_cast<uint64_t>(p.N), static_cast<uint64_t>(p.M), static_cast<uint64_t>(p.N) * es, 32, 16,
+                      CU_TENSOR_MAP_SWIZZLE_NONE))
+            return cudaErrorInvalidValue;
+    } else {
+        to = tx;  // (not used)
+    }
+    const int smem = rest + kGroup * p.ring * p.stage_bytes;
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(linear_fp8_kernel<CG, NSUB, BF16>), smem);
+    if (e != cudaSuccess) return e;
+    int fit = 0;
+    e = clusters_at_once<CG, NSUB, BF16>(ncta, &fit);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    // (a cluster that splits K has one tile)
+    cfg.gridDim = dim3(static_cast<unsigned>((p.split > 1 ? p.ntiles : std::min(p.ntiles, std::max(1, fit))) * ncta));
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(ncta);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    count_launch();
+    return cudaLaunchKernelEx(&cfg, linear_fp8_kernel<CG, NSUB, BF16>, tw, tx, to, p);
+}
+
+template <bool BF16>
+cudaError_t launch_dtype(int M, int N, int K, const void* x, const uint8_t* x_scales, const void* w,
+                         const uint8_t* w_scales, void* out, int* status, cudaStream_t stream) {
     LinParams p{};
     p.M = M;
     p.N = N;
     p.K = K;
-    p.nrc = (M + kMaxNr - 1) / kMaxNr;
-    const int per = (M + p.nrc - 1) / p.nrc;
-    p.Nr = (per + 15) & ~15;
-    p.ntiles = p.nrc * ((N + kTileN - 1) / kTileN);
+    p.nwt = (N + kTileN - 1) / kTileN;
     p.nk = (K + kStageK - 1) / kStageK;
-    p.ngroups = (p.nk + 3) / 4;
-    p.stage_bytes = kWBytes + (p.Nr * kStageK + 1023) / 1024 * 1024;
-    p.sf_blocks = (p.Nr + 127) / 128;
-    const int sf_bytes = kSfSlots * kSfBytes * (1 + p.sf_blocks);
-    p.stages = std::min(kMaxStages, (kSmemBudget - 1024 - sf_bytes) / p.stage_bytes);
-    p.sf_row_words = fp8_scale_stride(K) / 4;
-    p.acc_stride = (static_cast<uint32_t>(p.Nr) + 31u) & ~31u;
-    p.sf_col = 2 * p.acc_stride;
-    p.sf_cols = 4u * (1 + p.sf_blocks);
-    p.tmem_cols = 32;
-    while (p.tmem_cols < p.sf_col + kSfSlots * p.sf_cols) p.tmem_cols <<= 1;
-    p.out_bf16 = out_dtype == 1;
+    p.split = 1;
+    p.per = round_up(p.nk, kGroup);
     p.x_scales = reinterpret_cast<const uint32_t*>(x_scales);
     p.w_scales = reinterpret_cast<const uint32_t*>(w_scales);
     p.out = out;
     p.status = status;
-    CUtensorMap tw, tx;
-    if (!make_map_codes(&tw, w, static_cast<uint64_t>(K), static_cast<uint64_t>(N), kTileN) ||
-        !make_map_codes(&tx, x, static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint32_t>(p.Nr)))
-        return cudaErrorInvalidValue;
-    const int smem = p.stages * p.stage_bytes + sf_bytes + 1024;
-    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(linear_fp8_kernel), smem);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(linear_fp8_kernel, dim3(std::min(p.ntiles, sm_count())), dim3(kLinThreads),
-                      static_cast<size_t>(smem), stream, tw, tx, p);
+    const int sms = sm_count();
+    const int subs = (M + kMaxNr - 1) / kMaxNr;
+    const bool few = static_cast<long>(subs) * p.nwt * 2 <= sms;
+    if (M > kMaxNr1 && !few) {
+        // Pairs: the fewest accumulators of up to 224 rows, evenly, two of them to a tile
+        const int per_row = round_up(subs, subs > 1 ? 2 : 1);
+        p.Nr = round_up((M + per_row - 1) / per_row, 16);
+        p.chunk = BF16 ? p.per : kF32Chunk2;
+        return subs > 1 ? launch<2, 2, BF16>(p, x, w, stream) : launch<2, 1, BF16>(p, x, w, stream);
+    }
+    p.Nr = std::min(kMaxNr1, round_up(M, 16));
+    if (few) {
+        // Few tiles: K split over clusters, one tile a cluster
+        const int tiles = (M + p.Nr - 1) / p.Nr * p.nwt;
+        const int groups = p.per / kGroup;
+        int want = std::max(1, std::min({kMaxSplit, sms / tiles, groups}));
+        for (int fit = 0; want > 1; --want) {
+            const cudaError_t e = clusters_at_once<1, 1, BF16>(want, &fit);
+            if (e != cudaSuccess) return e;
+            if (fit >= tiles) break;
+        }
+        p.per = (groups + want - 1) / want * kGroup;
+        p.split = (groups * kGroup + p.per - 1) / p.per;
+    }
+    p.chunk = BF16 ? p.per : kF32Chunk1;
+    return launch<1, 1, BF16>(p, x, w, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_fp8(int M, int N, int K, const void* x, const uint8_t* x_scales, const void* w,
+                              const uint8_t* w_scales, int out_dtype, void* out, int* status, cudaStream_t stream) {
+    return out_dtype == 1 ? launch_dtype<true>(M, N, K, x, x_scales, w, w_scales, out, status, stream)
+                          : launch_dtype<false>(M, N, K, x, x_scales, w, w_scales, out, status, stream);
 }
 
 }  // namespace eagle

@@ -203,7 +203,8 @@ def _check_linear(out, x, xs, w, wsc, dt):
 @pytest.mark.parametrize("rows,out_dim,in_dim", [
     (1, 8, 16), (1, 128, 128), (3, 129, 144), (16, 256, 512), (17, 300, 528), (10, 1000, 1040), (1, 4096, 4096),
     (33, 640, 2048), (100, 520, 640), (129, 384, 656), (224, 130, 512), (225, 257, 1152), (300, 1024, 384),
-    (448, 300, 256), (700, 777, 912), (1000, 129, 2064), (2, 20000, 256), (513, 5000, 128)])
+    (448, 300, 256), (700, 777, 912), (1000, 129, 2064), (2, 20000, 256), (513, 5000, 128),
+    (65, 10100, 2512), (230, 10001, 1040), (449, 4000, 4224), (40, 20001, 2064), (20, 700, 8192), (672, 2500, 640)])
 def test_linear(E, dt, rows, out_dim, in_dim):
     rng = np.random.default_rng(rows * 1009 + out_dim * 31 + in_dim)
     ops = _operands(rng, rows, out_dim, in_dim)
