@@ -47,10 +47,11 @@ namespace {
 
 constexpr int kTileN = 128;   // weight rows of a CTA's tile (the MMA's M is 128 a CTA)
 constexpr int kStageK = 128;  // codes of K of a stage
-constexpr int kGroup = 4;     // stages of a word of scales, K = 512: the ring holds one or two groups
+constexpr int kGroup = 4;     // stages of a word of scales, K = 512
 constexpr int kMaxNr = 224;   // rows of x of an accumulator (MMA N): two accumulators and the scales fit in 512 columns
 constexpr int kMaxNr1 = 64;   // (CG = 1)
-constexpr int kMaxStages = 2 * kGroup;
+constexpr int kPartRows = 16; // (CG = 1) weight rows in which they are dealt to the CTAs
+constexpr int kMaxStages = 8;
 constexpr int kSfSlots = 3;   // groups of scale words on their way
 constexpr int kSfBytes = 512; // scale words of 128 rows and K = 512
 constexpr int kEpiWarps = 8;
@@ -74,7 +75,7 @@ struct LinParams {
     int nk;           // stages of a tile
     int per;          // stages of a CTA (whole groups)
     int chunk;        // stages summed in tensor memory (whole groups)
-    int ring;         // groups of the ring
+    int stages;       // of the ring
     int stage_bytes;
     int sf_blocks;    // 128-row blocks of scale words of an accumulator's rows
     int sf_row_words; // scale words of a row
@@ -191,6 +192,11 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
             "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
             : "memory");
 }
+__device__ __forceinline__ void prefetch_box(const CUtensorMap* map, int c0, int c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0),
+                 "r"(c1)
+                 : "memory");
+}
 __device__ __forceinline__ void store_remote(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -231,11 +237,12 @@ constexpr int kHalfBlocks = kMaxNr / 32, kHalfBlocks1 = kMaxNr1 / 32;
 __device__ __forceinline__ int half_first(int Nr, int half) { return half ? (Nr / 16 + 1) / 2 : 0; }
 __device__ __forceinline__ int half_count(int Nr, int half) { return half ? Nr / 32 : (Nr / 16 + 1) / 2; }
 
-// CG: CTAs that share an MMA. NSUB: accumulators of a tile.
+// CG: CTAs that share an MMA. NSUB: accumulators of a tile. tm_more: the output's map (CG = 2), or the weight's with
+// boxes of kPartRows rows (CG = 1).
 template <int CG, int NSUB, bool BF16>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_fp8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-                      const __grid_constant__ CUtensorMap tm_out, const LinParams p) {
+                      const __grid_constant__ CUtensorMap tm_more, const LinParams p) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -248,13 +255,28 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const int lead = CG == 2 ? 0 : rank;     // who issues this CTA's MMAs
     const int unit = blockIdx.x / ncta, nunits = gridDim.x / ncta;
     const int k0 = CG == 2 ? 0 : rank * p.per, k1 = min(p.nk, k0 + p.per);
-    unsigned char* out_smem = smem + kGroup * p.ring * p.stage_bytes;
+    unsigned char* out_smem = smem + p.stages * p.stage_bytes;
     unsigned char* sf_smem = out_smem + (CG == 2 ? kOutBytes : 0);
     const int sf_slot_bytes = kSfBytes * (1 + NSUB * p.sf_blocks);
+    // This cluster's tiles. Weight rows n0 .. n0 + rows - 1 of a CTA against row chunk rc of x. With one row chunk the
+    // CTAs (CG = 1) share the weight rows evenly in units of 16 and end with a part of a tile: whole tiles would leave
+    // SMs idle in the last round (128256 rows on 152 SMs: 7 rounds for 6.6 rounds' work).
+    const bool even = CG == 1 && p.split == 1 && p.nrc == 1;
+    const int parts = (p.N + kPartRows - 1) / kPartRows;
+    const int r0 = even ? static_cast<int>(static_cast<int64_t>(parts) * unit / nunits) * kPartRows : 0;
+    const int r1 = even ? static_cast<int>(static_cast<int64_t>(parts) * (unit + 1) / nunits) * kPartRows : 0;
+    const int t0 = even ? 0 : unit, t1 = even ? (r1 - r0 + kTileN - 1) / kTileN : p.ntiles, dt = even ? 1 : nunits;
+    struct Tile {
+        int rc, n0, rows;
+    };
+    auto tile = [&](int t) -> Tile {
+        if (even) return Tile{0, r0 + t * kTileN, min(kTileN, r1 - r0 - t * kTileN)};
+        return Tile{t % p.nrc, (CG * (t / p.nrc) + (CG == 2 ? rank : 0)) * kTileN, kTileN};
+    };
 
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kMaxStages; ++s) {
+        for (int s = 0; s < p.stages; ++s) {
             mbar_init(&bar_full[s], 1);
             mbar_init(&bar_empty[s], 1);
         }
@@ -286,6 +308,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (ncta > 1) cg::this_cluster().sync();  // the other CTAs' barriers are there
     tc_fence_after();
     const uint32_t tmem = tmem_holder;
+    if (warp == 0 && lane == 0) {
+        // The first boxes of the weight on their way to L2 while an earlier kernel ends (a hint: what that kernel
+        // writes to them still arrives)
+        const Tile tl = tile(t0);
+        for (int kc = k0; t0 < t1 && kc < min(k1, k0 + p.stages); ++kc) prefetch_box(&tm_w, kc * kStageK, tl.n0);
+    }
     pdl_wait_prior();
 
     if (warp == 0) {
@@ -293,39 +321,33 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const bool issue = elect_one();  // the warp goes through its loops together, one lane issues (see warp 1)
         const uint32_t full = smem_u32(bar_full), empty = smem_u32(bar_empty), smem0 = smem_u32(smem);
         const uint32_t full_at = CG == 2 ? cluster_addr(bar_full, 0) : full;
-        const uint32_t bytes = static_cast<uint32_t>(p.stage_bytes) * CG;
         const int xbox = p.Nr / CG;  // rows of x in a box
-        uint32_t half = 0, phase = 1;  // group of the ring and the parity of its last use (none yet: passes)
+        uint32_t st = 0, phase = 1;  // stage and the parity of its last use (none yet: passes)
         bool ok = true;
-        for (int t = unit; ok && t < p.ntiles; t += nunits) {
-            const int rc = t % p.nrc, vt = t / p.nrc;
-            const int w0 = (CG * vt + (CG == 2 ? rank : 0)) * kTileN;
-            const int x0 = rc * NSUB * p.Nr + (CG == 2 ? rank * xbox : 0);
-            for (int kg = k0; kg < k1; kg += kGroup) {
-#pragma unroll
-                for (int i = 0; i < kGroup; ++i) {
-                    const uint32_t st = half * kGroup + i;
-                    if (!wait_warp(empty + st * 8, phase)) {
-                        ok = false;
-                        break;
-                    }
-                    if (issue) {
-                        if (kg + i < k1) {
-                            const uint32_t dst = smem0 + st * p.stage_bytes, bar = full_at + st * 8;
-                            const int k = (kg + i) * kStageK;
-                            if (rank == lead) mbar_arrive_expect_tx(&bar_full[st], bytes);
-                            load_box<CG>(dst, &tm_w, k, w0, bar);
-#pragma unroll
-                            for (int a = 0; a < NSUB; ++a)
-                                load_box<CG>(dst + kWBytes + a * xbox * kStageK, &tm_x, k, x0 + a * p.Nr, bar);
-                        } else if (rank == lead) {  // a group's stages past K: nothing to load
-                            mbar_arrive(&bar_full[st]);
-                        }
-                    }
+        for (int t = t0; ok && t < t1; t += dt) {
+            const Tile tl = tile(t);
+            const int x0 = tl.rc * NSUB * p.Nr + (CG == 2 ? rank * xbox : 0);
+            const uint32_t bytes = CG == 2 ? 2u * p.stage_bytes : static_cast<uint32_t>((tl.rows + p.Nr) * kStageK);
+            for (int kc = k0; kc < k1; ++kc) {
+                if (!wait_warp(empty + st * 8, phase)) {
+                    ok = false;
+                    break;
                 }
-                if (!ok) break;
-                if (++half == static_cast<uint32_t>(p.ring)) {
-                    half = 0;
+                if (issue) {
+                    const uint32_t dst = smem0 + st * p.stage_bytes, bar = full_at + st * 8;
+                    if (rank == lead) mbar_arrive_expect_tx(&bar_full[st], bytes);
+                    if (CG == 2 || tl.rows == kTileN) {
+                        load_box<CG>(dst, &tm_w, kc * kStageK, tl.n0, bar);
+                    } else {
+                        for (int r = 0; r < tl.rows; r += kPartRows)
+                            load_box<CG>(dst + r * kStageK, &tm_more, kc * kStageK, tl.n0 + r, bar);
+                    }
+#pragma unroll
+                    for (int a = 0; a < NSUB; ++a)
+                        load_box<CG>(dst + kWBytes + a * xbox * kStageK, &tm_x, kc * kStageK, x0 + a * p.Nr, bar);
+                }
+                if (++st == static_cast<uint32_t>(p.stages)) {
+                    st = 0;
                     phase ^= 1;
                 }
             }
@@ -333,10 +355,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (!ok && issue) raise_status(p.status, kDevTimeout);
         // The CTA does not end before the MMAs that read its last stages, and their arrivals, are done. (Where a
         // wait has given up, the copies have had its limit, far more than they take.)
-        for (int s = 0; ok && s < kGroup * p.ring; ++s) {
-            ok = wait_warp(empty + (half * kGroup + s % kGroup) * 8, phase);
-            if (s % kGroup == kGroup - 1 && ++half == static_cast<uint32_t>(p.ring)) {
-                half = 0;
+        for (int s = 0; ok && s < p.stages; ++s) {
+            ok = wait_warp(empty + st * 8, phase);
+            if (++st == static_cast<uint32_t>(p.stages)) {
+                st = 0;
                 phase ^= 1;
             }
         }
@@ -345,29 +367,30 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (rank == lead) {
             // The warp goes through the loops together and one lane issues, so that descriptors, addresses and
             // the loops' conditions stay in uniform registers: a lane on its own took 720 clocks a stage, whatever
-            // its MMAs' size, and 1050 with divisions for stage and parity (four MMAs of 224 rows take 448). A
-            // group's four stages are unrolled, their places in the ring fixed.
+            // its MMAs' size, and 1050 with divisions for stage and parity (four MMAs of 224 rows take 448).
             const uint32_t idesc = idesc_mxf8(kTileN * CG, p.Nr);
             const bool issue = elect_one();
             const uint32_t full = smem_u32(bar_full), empty = smem_u32(bar_empty);
             const uint32_t sf_full = smem_u32(bar_sf_full), sf_empty = smem_u32(bar_sf_empty);
             const uint32_t acc_full = smem_u32(bar_acc_full), acc_empty = smem_u32(bar_acc_empty);
-            uint32_t half = 0, phase = 0, slot = 0, sf_phase = 0;
+            uint32_t st = 0, phase = 0, slot = 0, sf_phase = 0;
             uint32_t buf = 0, acc_phase = 1;  // (NSUB = 1) the accumulator; the parity of its last reading (none yet: passes)
             const uint32_t base = ((smem_u32(smem) & 0x3FFFFu) >> 4) | (1u << 16);
             const uint64_t sf_base = sf_desc(smem_u32(sf_smem));
             const uint32_t step = static_cast<uint32_t>(p.stage_bytes) >> 4;
             const uint32_t x_step = static_cast<uint32_t>(p.Nr / CG * kStageK) >> 4;
             const uint32_t sfb_step = 4u * p.sf_blocks;
+            uint32_t desc = base;
             bool ok = true;
-            for (int t = unit; ok && t < p.ntiles; t += nunits) {
+            for (int t = t0; ok && t < t1; t += dt) {
                 for (int kb = k0; ok && kb < k1; kb += p.chunk) {
                     const int ke = min(k1, kb + p.chunk);
                     for (int kg = kb; kg < ke; kg += kGroup) {
                         // The next group's scale words into this slot's columns. The slot was filled
                         // after the MMAs that read these columns last had ended.
+                        const bool first = kg == kb, last = kg + kGroup >= ke;
                         if (!wait_warp(sf_full + slot * 8, sf_phase) ||
-                            (kg == kb && !wait_warp(acc_empty + buf * 8, acc_phase))) {
+                            (first && !wait_warp(acc_empty + buf * 8, acc_phase))) {
                             ok = false;
                             break;
                         }
@@ -376,48 +399,76 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         const uint64_t sd = sf_base + static_cast<uint32_t>(slot * sf_slot_bytes >> 4);
                         if (issue)
                             for (int b = 0; b <= NSUB * p.sf_blocks; ++b) copy_sf<CG>(sfa + 4 * b, sd + b * (kSfBytes >> 4));
-                        const uint32_t first = base + half * kGroup * step;
                         const uint32_t d = tmem + buf * p.acc_stride;
-                        const bool fresh = kg == kb;
+                        // A stage's MMAs of accumulator a (K = 32 each: 32 bytes along the swizzled row)
+                        auto mmas = [&](int i, int a, uint32_t aw) {
+                            const uint32_t id = idesc | (static_cast<uint32_t>(i) << 4) | (static_cast<uint32_t>(i) << 29);
+                            const uint32_t ax = aw + (kWBytes >> 4) + a * x_step;
+#pragma unroll
+                            for (int kk = 0; kk < kStageK / 32; ++kk)
+                                mma_mxf8<CG>(d + a * p.acc_stride, aw + 2 * kk, ax + 2 * kk, id, sfa, sfa + 4 + a * sfb_step,
+                                             i > 0 || kk > 0 ? 1 : !first);
+                        };
+                        // Two accumulators take turns stage by stage; at a sum's ends the group goes through
+                        // the first and then the second, so that each is read while the other is summed (a
+                        // group of 2 x 224 rows: 1800 clocks each).
+                        const bool apart = NSUB == 2 && (first || last) && kg + kGroup <= ke;
+                        const uint32_t desc0 = desc, st0 = st;
 #pragma unroll
                         for (int i = 0; i < kGroup; ++i) {
-                            const uint32_t st = half * kGroup + i;
+                            if (kg + i >= ke) break;
                             if (!wait_warp(full + st * 8, phase)) {
                                 ok = false;
                                 break;
                             }
                             tc_fence_after();
-                            const uint32_t id = idesc | (static_cast<uint32_t>(i) << 4) | (static_cast<uint32_t>(i) << 29);
-                            const uint32_t aw = first + i * step;
-#pragma unroll
-                            for (int a = 0; a < NSUB; ++a) {
-                                if (a == 1 && i == 0 && fresh) {  // the second accumulator's last sums have been read
-                                    if (!wait_warp(acc_empty + 8, acc_phase)) {
-                                        ok = false;
-                                        break;
+                            if (issue) mmas(i, 0, desc);
+                            if (!apart) {
+                                if (NSUB == 2) {
+                                    if (i == 0 && first) {  // the second accumulator's last sums have been read
+                                        if (!wait_warp(acc_empty + 8, acc_phase)) {
+                                            ok = false;
+                                            break;
+                                        }
+                                        tc_fence_after();
                                     }
-                                    tc_fence_after();
+                                    if (issue) mmas(i, 1, desc);
                                 }
-                                if (issue) {
-                                    if (kg + i < k1) {
-                                        const uint32_t ax = aw + (kWBytes >> 4) + a * x_step;
-#pragma unroll
-                                        for (int kk = 0; kk < kStageK / 32; ++kk)  // K = 32: 32 bytes along the swizzled row
-                                            mma_mxf8<CG>(d + a * p.acc_stride, aw + 2 * kk, ax + 2 * kk, id, sfa,
-                                                         sfa + 4 + a * sfb_step, i > 0 || kk > 0 ? 1 : !fresh);
-                                    }
-                                    if (i == kGroup - 1 && kg + kGroup >= ke) commit<CG>(acc_full + (buf + a) * 8);
-                                }
+                                if (issue) commit<CG>(empty + st * 8);
                             }
-                            if (!ok) break;
-                            if (issue) commit<CG>(empty + st * 8);
+                            desc += step;
+                            if (++st == static_cast<uint32_t>(p.stages)) {
+                                st = 0;
+                                phase ^= 1;
+                                desc = base;
+                            }
                         }
                         if (!ok) break;
-                        if (issue) commit<CG>(sf_empty + slot * 8);
-                        if (++half == static_cast<uint32_t>(p.ring)) {
-                            half = 0;
-                            phase ^= 1;
+                        if (last && issue) commit<CG>(acc_full + buf * 8);
+                        if (NSUB == 2) {
+                            if (apart) {
+                                if (first && !wait_warp(acc_empty + 8, acc_phase)) {
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after();
+                                uint32_t da = desc0, sa = st0;
+#pragma unroll
+                                for (int i = 0; i < kGroup; ++i) {
+                                    if (issue) {
+                                        mmas(i, 1, da);
+                                        commit<CG>(empty + sa * 8);
+                                    }
+                                    da += step;
+                                    if (++sa == static_cast<uint32_t>(p.stages)) {
+                                        sa = 0;
+                                        da = base;
+                                    }
+                                }
+                            }
+                            if (last && issue) commit<CG>(acc_full + 8);
                         }
+                        if (issue) commit<CG>(sf_empty + slot * 8);
                         if (++slot == kSfSlots) {
                             slot = 0;
                             sf_phase ^= 1;
@@ -439,13 +490,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         uint32_t slot = 0, sf_phase = 1;
         bool ok = true;
         constexpr int kBlocks = CG == 1 ? 1 : 2 * NSUB;  // 128-row blocks of x at most
-        for (int t = unit; ok && t < p.ntiles; t += nunits) {
-            const int rc = t % p.nrc, vt = min(CG * (t / p.nrc) + (CG == 2 ? rank : 0), p.nwt - 1);
-            const int m0 = rc * NSUB * p.Nr;
-            const uint32_t* wrow = p.w_scales + static_cast<size_t>(vt) * p.sf_row_words;
-            uint32_t ww = 0u, xw[kBlocks][4];
+        for (int t = t0; ok && t < t1; t += dt) {
+            const Tile tl = tile(t);
+            const int m0 = tl.rc * NSUB * p.Nr;
+            const uint32_t* wrow[CG == 1 ? 4 : 1];  // (a part's rows may lie in two of the weight's blocks)
+#pragma unroll
+            for (int i = 0; i < (CG == 1 ? 4 : 1); ++i)
+                wrow[i] = p.w_scales + static_cast<size_t>(min((tl.n0 + (CG == 1 ? i * 32 + lane : 0)) / kTileN, p.nwt - 1)) * p.sf_row_words;
+            uint32_t ww[CG == 1 ? 4 : 1], xw[kBlocks][4];
             auto fetch = [&](int g) {
-                ww = ld_prior(wrow + g);
+#pragma unroll
+                for (int i = 0; i < (CG == 1 ? 4 : 1); ++i) ww[i] = ld_prior(wrow[i] + g);
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
@@ -465,7 +520,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     break;
                 }
                 const uint32_t dst = smem_u32(sf_smem + slot * sf_slot_bytes) + lane * 16;
-                sts128(dst, make_uint4(ww, ww, ww, ww));
+                sts128(dst, CG == 1 ? make_uint4(ww[0], ww[CG == 1 ? 1 : 0], ww[CG == 1 ? 2 : 0], ww[CG == 1 ? 3 : 0]) : make_uint4(ww[0], ww[0], ww[0], ww[0]));
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b)
                     if (b < NSUB * p.sf_blocks) sts128(dst + (1 + b) * kSfBytes, make_uint4(xw[b][0], xw[b][1], xw[b][2], xw[b][3]));
@@ -531,7 +586,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             if (p.bulk_out) {
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) store_block(&tm_out, at, v0, m, add);
+                if (lane == 0) store_block(&tm_more, at, v0, m, add);
                 __syncwarp();
             } else if (v0 + lane < p.N) {
                 // this lane's own column
@@ -554,10 +609,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
             box = (box + 1) % kBoxes;
         };
-        for (int t = unit; ok && t < p.ntiles; t += nunits) {
-            const int rc = t % p.nrc, vt = CG * (t / p.nrc) + (CG == 2 ? rank : 0);
-            const int v0 = vt * kTileN + q4 * 32, v = v0 + lane;
-            const int row = rc * NSUB * p.Nr + b0 * 16;
+        for (int t = t0; ok && t < t1; t += dt) {
+            const Tile tl = tile(t);
+            const int v0 = tl.n0 + q4 * 32, v = v0 + lane;
+            const int row = tl.rc * NSUB * p.Nr + b0 * 16;
             if (CG == 2 && BF16) {
                 // All accumulators are read, rounded and freed before the first store. (What does not fit in
                 // registers here goes to L2, the shared memory leaves no L1: spills took as long as the MMAs.)
@@ -661,7 +716,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                                 ++slot;
                             }
                         }
-                } else if (v < p.N) {
+                } else if (v < min(p.N, tl.n0 + tl.rows)) {
                     const size_t at = static_cast<size_t>(row) * p.N + v;
 #pragma unroll
                     for (int b = 0; b < kHalfBlocks1; ++b) {
@@ -768,7 +823,7 @@ cudaError_t launch(LinParams& p, const void* x, const void* w, cudaStream_t stre
     const int red_bytes = p.split > 1 ? (p.Nr + p.split) * kTileN * 4 : 0;
     const int sf_bytes = kSfSlots * kSfBytes * (1 + NSUB * p.sf_blocks);
     const int rest = 1024 + sf_bytes + red_bytes + (CG == 2 ? kOutBytes : 0);
-    p.ring = rest + 2 * kGroup * p.stage_bytes <= kSmemBudget ? 2 : 1;
+    p.stages = std::min(kMaxStages, (kSmemBudget - rest) / p.stage_bytes);
     p.sf_row_words = fp8_scale_stride(p.K) / 4;
     p.acc_stride = static_cast<uint32_t>(round_up(p.Nr, 32));
     p.sf_col = 2 * p.acc_stride;
@@ -784,17 +839,17 @@ cudaError_t launch(LinParams& p, const void* x, const void* w, cudaStream_t stre
                       static_cast<uint64_t>(p.N), static_cast<uint64_t>(p.M), static_cast<uint64_t>(p.N) * es, 32, 16,
                       CU_TENSOR_MAP_SWIZZLE_NONE))
             return cudaErrorInvalidValue;
-    } else {
-        to = tx;  // (not used)
+    } else if (!make_map_codes(&to, w, p.K, p.N, kPartRows)) {
+        return cudaErrorInvalidValue;
     }
-    const int smem = rest + kGroup * p.ring * p.stage_bytes;
+    const int smem = rest + p.stages * p.stage_bytes;
     cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(linear_fp8_kernel<CG, NSUB, BF16>), smem);
     if (e != cudaSuccess) return e;
     int fit = 0;
     e = clusters_at_once<CG, NSUB, BF16>(ncta, &fit);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    // (a cluster that splits K has one tile)
+    // (a cluster that splits K has one tile; CTAs that share the weight's rows evenly have one at least)
     cfg.gridDim = dim3(static_cast<unsigned>((p.split > 1 ? p.ntiles : std::min(p.ntiles, std::max(1, fit))) * ncta));
     cfg.blockDim = dim3(kLinThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
