@@ -13,11 +13,11 @@
 // Bound by HBM: a row is read once and its gradient written once. A row lies in
 // the shared memory of a cluster of 1..8 CTAs (bulk copies, at most 64 KB a
 // CTA, so that three CTAs share an SM and one's copies run behind another's
-// arithmetic); the listed entries are taken out of it, each CTA sums
-// exp((z - m) / T) over the rest of its segment, and one exchange of (m, sum)
-// through distributed shared memory gives every CTA the row's sums. The rest is
-// summed by itself, so that a draft that is sure of the listed ids loses
-// nothing of q_R to cancellation.
+// arithmetic). The first warp takes the listed entries out of the row and then
+// works out the target's side while the others sum exp((z - m) / T) over the
+// rest, and one exchange of (m, sum) through distributed shared memory gives
+// every CTA the row's sums. The rest is summed by itself, so that a draft that
+// is sure of the listed ids loses nothing of q_R to cancellation.
 
 #include <cuda_bf16.h>
 
@@ -32,24 +32,20 @@
 namespace eagle {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxWarps = 8;
 constexpr int kMaxSegBytes = 65536;  // of a row in a CTA's shared memory
 constexpr int kCopyBytes = 16384;
 constexpr float kLog2e = 1.4426950408889634f;
-static_assert(kDistillMaxTop <= kThreads, "a thread for each listed id");
 
-struct Part {  // a CTA's share of the row outside the list
-    float m, s;
-    int bad;  // a DeviceError, 0 = none
-};
 struct Shared {
     alignas(8) uint64_t bar;
-    float redf[kWarps];
-    double redd[kWarps];
-    float wm[kWarps], ws[kWarps];
-    int bad;
-    Part part[kMaxChunks];  // of all CTAs of the cluster
+    float2 part[kMaxChunks * (kMaxWarps - 1)];  // (m, sum) of the rest, of each warp but the first of each CTA of the cluster
+    int bad[kMaxChunks];                  // a DeviceError of each CTA, 0 = none
+    float2 list;                          // (m, sum) of the listed entries
+    float r, mass;                        // what the list leaves; sum p + r
+    int nothing;                          // a list of padding alone that is the whole distribution
+    int id[kDistillMaxTop];               // -1: padding, or no entry of the row
+    float z[kDistillMaxTop], lnp[kDistillMaxTop];
 };
 
 template <int DT>
@@ -58,51 +54,38 @@ __device__ __forceinline__ float load1(const void* row, int i) {
         return __uint_as_float(static_cast<uint32_t>(ld_prior(static_cast<const unsigned short*>(row) + i)) << 16);
     return ld_prior(static_cast<const float*>(row) + i);
 }
+__device__ __forceinline__ __nv_bfloat162 bf2(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+// The entries of 16 bytes as packed pairs.
 template <int DT>
-__device__ __forceinline__ void unpack(const uint4& u, float (&x)[DT == 1 ? 8 : 4]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void unpack(const uint4& u, uint64_t (&x)[DT == 1 ? 4 : 2]) {
+    if (DT == 1) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (DT == 1) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        } else {
-            x[i] = __uint_as_float(w[i]);
-        }
+        for (int i = 0; i < 4; ++i) x[i % (DT == 1 ? 4 : 2)] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    } else {
+        x[0] = f2_pack(__uint_as_float(u.x), __uint_as_float(u.y));
+        x[1] = f2_pack(__uint_as_float(u.z), __uint_as_float(u.w));
     }
 }
 
-__device__ __forceinline__ float block_max(float v, float* red) {
+__device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int i = 1; i < kWarps; ++i) v = fmaxf(v, red[i]);
     return v;
 }
 template <typename T>
-__device__ __forceinline__ T block_sum(T v, T* red) {
+__device__ __forceinline__ T warp_sum(T v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int i = 1; i < kWarps; ++i) v += red[i];
     return v;
 }
-
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 3) distill_kernel(DistillArgs a, int cpr, int seg, float c) {
+__global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs a, int cpr, int seg, int ahead, float c) {
     extern __shared__ __align__(128) unsigned char row_smem[];
     __shared__ Shared sm;
     constexpr int ES = DT == 1 ? 2 : 4;
     constexpr int EPV = 16 / ES;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
     const int row = blockIdx.x / cpr, rank = blockIdx.x % cpr;  // a cluster is cpr neighbouring CTAs
     pdl_launch_dependents();
     pdl_wait_prior();
@@ -114,19 +97,24 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(DistillArgs a, int
     uint4* grad = a.grad ? reinterpret_cast<uint4*>(static_cast<char*>(a.grad) + static_cast<size_t>(row) * row_bytes +
                                                     static_cast<size_t>(first) * ES)
                          : nullptr;
-    const float w = a.row_weight ? ld_prior(a.row_weight + row) : 1.0f;
-    // ---- the target's list: thread t holds entry t ----
-    int id = -1;
-    float t = -INFINITY;
-    if (tid < a.n_top) {
-        id = ld_prior(a.ids + static_cast<size_t>(row) * a.n_top + tid);
-        t = ld_prior(a.teacher + static_cast<size_t>(row) * a.n_top + tid);
+    // The first warp's lanes hold the target's list, 32 apart (all loads of a kind go out together)
+    constexpr int kSlots = kDistillMaxTop / 32;
+    int id[kSlots];
+    float t[kSlots], lse = 0.0f;
+    if (warp == 0) {
+        const size_t at = static_cast<size_t>(row) * a.n_top;
+#pragma unroll
+        for (int k = 0; k < kSlots; ++k) {
+            const int i = k * 32 + lane;
+            id[k] = i < a.n_top ? ld_prior(a.ids + at + i) : -1;
+            t[k] = i < a.n_top ? ld_prior(a.teacher + at + i) : -INFINITY;
+        }
+        if (a.teacher_lse) lse = ld_prior(a.teacher_lse + row);
     }
-    const bool whole = a.teacher_lse == nullptr;  // the list is the whole distribution
-    const bool listed = __syncthreads_or(id >= 0);
-    if (w == 0.0f || (whole && !listed)) {  // no weight, or nothing to learn: uniform over the cluster
+    const float w = a.row_weight ? ld_prior(a.row_weight + row) : 1.0f;
+    if (w == 0.0f) {  // uniform over the cluster
         if (grad)
-            for (int v = tid; v < nvec; v += kThreads) grad[v] = make_uint4(0u, 0u, 0u, 0u);
+            for (int v = tid; v < nvec; v += threads) grad[v] = make_uint4(0u, 0u, 0u, 0u);
         if (rank == 0 && tid == 0) a.loss[row] = 0.0f;
         return;
     }
@@ -134,164 +122,250 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(DistillArgs a, int
     if (tid == 0) {
         mbar_init(&sm.bar, 1);
         fence_mbar_init();
-        sm.bad = isfinite(w) ? 0 : kDevNonFinite;
-    }
-    __syncthreads();
-    if (tid == 0) {
         mbar_arrive_expect_tx(&sm.bar, static_cast<uint32_t>(n) * ES);
         for (int off = 0; off < n * ES; off += kCopyBytes)
             bulk_g2s(row_smem + off, in + static_cast<size_t>(first) * ES + off,
                      static_cast<uint32_t>(min(kCopyBytes, n * ES - off)), &sm.bar);
     }
     int bad = 0;
-    if (id >= a.V) {
-        bad = kDevBadIndex;
-        id = -1;
+    float z[kSlots];
+    if (warp == 0) {
+        // ---- the list's entries leave the row ----
+        __syncwarp();
+        bad = isfinite(w) ? 0 : kDevNonFinite;
+#pragma unroll
+        for (int k = 0; k < kSlots; ++k) {
+            z[k] = -INFINITY;
+            if (k * 32 >= a.n_top) continue;
+            if (id[k] >= a.V) {
+                bad = kDevBadIndex;
+                id[k] = -1;
+            }
+            if (id[k] >= 0) z[k] = load1<DT>(in, id[k]);  // the draft's logit there
+        }
+        if (mbar_wait_sleep(&sm.bar, 0)) {
+            // An id listed twice: the last of its entries to write its number there finds another one
+            auto slot = [&](int k) -> int {  // where entry k lies in this CTA's segment, -1: not there
+                const int at = id[k] - first;
+                return k * 32 < a.n_top && id[k] >= 0 && at >= 0 && at < n ? at : -1;
+            };
+            volatile uint16_t* row16 = reinterpret_cast<volatile uint16_t*>(row_smem);
+            volatile uint32_t* row32 = reinterpret_cast<volatile uint32_t*>(row_smem);
+#pragma unroll
+            for (int k = 0; k < kSlots; ++k) {
+                const int at = slot(k);
+                if (at < 0) continue;
+                if (DT == 1) row16[at] = static_cast<uint16_t>(k * 32 + lane);
+                else row32[at] = static_cast<uint32_t>(k * 32 + lane);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < kSlots; ++k) {
+                const int at = slot(k);
+                if (at < 0) continue;
+                if ((DT == 1 ? static_cast<uint32_t>(row16[at]) : row32[at]) != static_cast<uint32_t>(k * 32 + lane)) bad = kDevBadIndex;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < kSlots; ++k) {
+                const int at = slot(k);
+                if (at < 0) continue;
+                if (DT == 1) row16[at] = 0xff80u;
+                else row32[at] = 0xff800000u;
+            }
+        } else {
+            bad = kDevTimeout;
+        }
     }
-    const bool on = id >= 0;
-    const float z = on ? load1<DT>(in, id) : -INFINITY;  // the draft's logit there
-    // the target's log-probabilities
-    float lnp = -INFINITY, p = 0.0f;
-    if (whole) {
-        const float top = block_max(on ? t : -INFINITY, sm.redf);
-        const float y = on ? (t - top) / a.temperature : -INFINITY;
-        const float e = on ? expf(y) : 0.0f;
-        const float total = block_sum(e, sm.redf);
-        lnp = y - logf(total);
-        if (!(total > 0.0f) || !isfinite(total)) bad = kDevNonFinite;
-    } else {
-        const float lse = ld_prior(a.teacher_lse + row);
-        lnp = t / a.temperature - lse;
-        if (!isfinite(lse)) bad = kDevNonFinite;
-    }
-    if (on) p = expf(lnp);
-    if (on && !(p < INFINITY)) bad = kDevNonFinite;
-    const double psum = block_sum(static_cast<double>(p), sm.redd);
-    const float r = whole ? 0.0f : static_cast<float>(fmax(0.0, 1.0 - psum));
-    const float mass = whole ? 1.0f : static_cast<float>(psum) + r;
-    // ---- the segment ----
-    const bool arrived = mbar_wait_sleep(&sm.bar, 0);
-    if (!arrived) bad = kDevTimeout;
-    // An id listed twice: the last of its entries to write its number there finds another one.
-    const bool mine = on && id >= first && id < first + n;
-    if (arrived && mine) {
-        if (DT == 1) reinterpret_cast<volatile uint16_t*>(row_smem)[id - first] = static_cast<uint16_t>(tid);
-        else reinterpret_cast<volatile uint32_t*>(row_smem)[id - first] = static_cast<uint32_t>(tid);
-    }
+    // A CTA that starts when this one ends finds its row on its way or in L2: HBM reads go on while the CTAs of an SM,
+    // which run much in step, add up and store.
+    if (tid == 32 && row + ahead < a.rows && (a.row_weight == nullptr || ld_prior(a.row_weight + row + ahead) != 0.0f))
+        for (int off = 0; off < n * ES; off += kCopyBytes)
+            prefetch_l2(in + static_cast<size_t>(ahead) * row_bytes + static_cast<size_t>(first) * ES + off,
+                        static_cast<uint32_t>(min(kCopyBytes, n * ES - off)));
     __syncthreads();
-    if (arrived && mine) {
-        const uint32_t who = DT == 1 ? reinterpret_cast<volatile uint16_t*>(row_smem)[id - first]
-                                     : reinterpret_cast<volatile uint32_t*>(row_smem)[id - first];
-        if (who != static_cast<uint32_t>(tid)) bad = kDevBadIndex;
-    }
-    __syncthreads();
-    if (arrived && mine) {  // the list's entries leave the segment
-        if (DT == 1) reinterpret_cast<uint16_t*>(row_smem)[id - first] = 0xff80u;
-        else reinterpret_cast<uint32_t*>(row_smem)[id - first] = 0xff800000u;
-    }
-    if (bad) atomicMax(&sm.bad, bad);
-    __syncthreads();
+    mbar_try_wait(&sm.bar, 0);  // done: every thread that reads what was copied has seen it
+    // ---- the rest: this thread's largest entry, then its sum relative to it (no reference to agree on first) ----
     const uint4* vec = reinterpret_cast<const uint4*>(row_smem);
-    float m = -INFINITY;
-    for (int v = tid; v < nvec; v += kThreads) {
-        float x[EPV];
-        unpack<DT>(vec[v], x);
+    const uint64_t c2 = f2_pack(c, c);
+    float m = -INFINITY, s = 0.0f;
+    if (warp == 0) {
+        // ---- the target's side ----
+        const bool whole = a.teacher_lse == nullptr;  // the list is the whole distribution
+        bool any = false;
+        float top = -INFINITY, ztop = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < EPV; ++i) m = fmaxf(m, x[i]);
-    }
-    float s = 0.0f;
-    const float m0 = m == -INFINITY ? 0.0f : m;  // nothing but -inf: every term is 0
-    for (int v = tid; v < nvec; v += kThreads) {
-        float x[EPV];
-        unpack<DT>(vec[v], x);
-        float part = 0.0f;
+        for (int k = 0; k < kSlots; ++k) {
+            any = any || id[k] >= 0;
+            if (id[k] >= 0) top = fmaxf(top, t[k]);
+            ztop = fmaxf(ztop, z[k]);
+        }
+        any = __any_sync(0xffffffffu, any);
+        ztop = warp_max(ztop);
+        const float z0 = ztop == -INFINITY ? 0.0f : ztop;
+        float shift = lse;
+        if (whole) {
+            top = warp_max(top);
+            float total = 0.0f;
 #pragma unroll
-        for (int i = 0; i < EPV; ++i) part += ex2_approx((x[i] - m0) * c);
-        s += part;
-    }
-    // joined over the CTA
-    auto join = [&](float& am, float& as, float bm, float bs) {
-        const float M = fmaxf(am, bm), M0 = M == -INFINITY ? 0.0f : M;
-        as = as * ex2_approx((am - M0) * c) + bs * ex2_approx((bm - M0) * c);
-        am = M;
-    };
+            for (int k = 0; k < kSlots; ++k) {
+                if (k * 32 >= a.n_top) continue;
+                t[k] = (t[k] - top) / a.temperature;
+                if (id[k] >= 0) total += expf(t[k]);
+            }
+            total = warp_sum(total);
+            shift = logf(total);
+            if (!(total > 0.0f)) bad = max(bad, static_cast<int>(kDevNonFinite));
+        } else {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s, o);
-        join(m, s, om, os);
+            for (int k = 0; k < kSlots; ++k)
+                if (k * 32 < a.n_top) t[k] /= a.temperature;
+        }
+        if (!isfinite(shift)) bad = max(bad, static_cast<int>(kDevNonFinite));
+        float zsum = 0.0f, psum = 0.0f, low = 0.0f;  // (sum p and what its roundings lost: 1 - sum p is of that size)
+        auto add = [&](float p) {
+            const float u = psum + p, q = u - psum;
+            low += (psum - (u - q)) + (p - q);
+            psum = u;
+        };
+#pragma unroll
+        for (int k = 0; k < kSlots; ++k) {
+            const int i = k * 32 + lane;
+            if (k * 32 >= a.n_top) continue;
+            const bool on = id[k] >= 0;
+            const float lnp = on ? t[k] - shift : -INFINITY, p = on ? expf(lnp) : 0.0f;
+            if (!(p < INFINITY)) bad = max(bad, static_cast<int>(kDevNonFinite));
+            add(p);
+            if (on) zsum += ex2_approx((z[k] - z0) * c);  // a NaN or +inf logit makes it NaN
+            if (i < a.n_top) {
+                sm.id[i] = id[k];
+                sm.z[i] = z[k];
+                sm.lnp[i] = lnp;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            low += __shfl_xor_sync(0xffffffffu, low, o);
+            add(__shfl_xor_sync(0xffffffffu, psum, o));
+            zsum += __shfl_xor_sync(0xffffffffu, zsum, o);
+        }
+        bad = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(bad)));
+        if (lane == 0) {
+            // (lanes differ in `low` by what their own last sums lost: far below what matters)
+            const float r = whole ? 0.0f : fmaxf(0.0f, (1.0f - psum) - low);
+            sm.r = r;
+            sm.mass = whole ? 1.0f : psum + r;
+            sm.list = make_float2(ztop, zsum);
+            sm.nothing = whole && !any;
+            sm.bad[rank] = bad;
+        }
+        __syncwarp();
+    } else {
+        // ---- the rest: this warp's largest entry, then its sum relative to it (no reference to agree on first) ----
+        const int t0 = tid - 32, step = threads - 32;
+        if (DT == 1) {
+            __nv_bfloat162 top = __floats2bfloat162_rn(-INFINITY, -INFINITY);
+            for (int v = t0; v < nvec; v += step) {
+                const uint4 u = vec[v];
+                top = __hmax2(top, __hmax2(__hmax2(bf2(u.x), bf2(u.y)), __hmax2(bf2(u.z), bf2(u.w))));
+            }
+            m = fmaxf(__low2float(top), __high2float(top));
+        } else {
+            for (int v = t0; v < nvec; v += step) {
+                const uint4 u = vec[v];
+                m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w))));
+            }
+        }
+        m = warp_max(m);
+        const float m0 = m == -INFINITY ? 0.0f : m;  // nothing but -inf: every term is 0
+        const uint64_t minus = f2_pack(-m0, -m0);
+        uint64_t s2[2] = {0ull, 0ull};
+        for (int v = t0; v < nvec; v += step) {
+            uint64_t x[EPV / 2];
+            unpack<DT>(vec[v], x);
+#pragma unroll
+            for (int i = 0; i < EPV / 2; ++i) {
+                const uint64_t y = f2_mul(f2_add(x[i], minus), c2);
+                s2[i & 1] = f2_add(s2[i & 1], f2_pack(ex2_approx(f2_lo(y)), ex2_approx(f2_hi(y))));
+            }
+        }
+        const uint64_t u = f2_add(s2[0], s2[1]);
+        s = warp_sum(f2_lo(u) + f2_hi(u));
     }
-    if (lane == 0) {
-        sm.wm[warp] = m;
-        sm.ws[warp] = s;
-    }
-    __syncthreads();
-    m = sm.wm[0];
-    s = sm.ws[0];
-    for (int i = 1; i < kWarps; ++i) join(m, s, sm.wm[i], sm.ws[i]);
-    // ---- joined over the cluster ----
+    // ---- over the cluster ----
+    const int nparts = warps - 1;  // of a CTA
     cg::cluster_group cluster = cg::this_cluster();
-    if (cpr > 1) cluster_started_wait();
-    if (tid < cpr) {
-        Part* to = cpr > 1 ? cluster.map_shared_rank(&sm.part[rank], tid) : &sm.part[rank];
-        *to = Part{m, s, sm.bad};
+    if (cpr > 1) {
+        cluster_started_wait();
+        if (warp > 0 && lane < cpr) *cluster.map_shared_rank(&sm.part[rank * nparts + warp - 1], lane) = make_float2(m, s);
+        if (warp == 0 && lane < cpr) *cluster.map_shared_rank(&sm.bad[rank], lane) = bad;
+        cluster.sync();
+    } else {
+        if (warp > 0 && lane == 0) sm.part[warp - 1] = make_float2(m, s);
+        __syncthreads();
     }
-    if (cpr > 1) cluster.sync();
-    else __syncthreads();
-    int fault = sm.part[0].bad;
-    m = sm.part[0].m;
-    float sr = sm.part[0].s;
-    for (int i = 1; i < cpr; ++i) {
-        join(m, sr, sm.part[i].m, sm.part[i].s);
-        fault = max(fault, sm.part[i].bad);
-    }
-    const float ztop = block_max(z, sm.redf);
-    const float M = fmaxf(m, ztop), M0 = M == -INFINITY ? 0.0f : M;
-    sr *= ex2_approx((m - M0) * c);
-    const float e = on ? ex2_approx((z - M0) * c) : 0.0f;
-    const float total = sr + block_sum(e, sm.redf);
-    const float lns = logf(total);
-    // a NaN among the list's logits is in e, one of the rest in sr; a maximum of +inf makes them NaN
-    if (fault == 0 && (!(total > 0.0f) || !isfinite(total))) fault = kDevNonFinite;
-    const bool rest = r > 0.0f && sr > 0.0f;
-    if (rank == 0) {
-        // p ln p is 0 where p is; a listed id that the draft rules out makes the loss infinite
-        float term = on && p > 0.0f ? p * (lnp - ((z - M0) / a.temperature - lns)) : 0.0f;
-        term = block_sum(term, sm.redf);
-        if (tid == 0) {
-            if (rest) term += r * (logf(r) - (logf(sr) - lns));
-            if (fault) raise_status(a.status, fault);
-            a.loss[row] = fault ? NAN : w * term;
+    // the parts over their largest m, two a lane at most
+    static_assert(kMaxChunks * (kMaxWarps - 1) <= 64, "two parts a lane");
+    const float2 none = make_float2(-INFINITY, 0.0f);
+    const float2 p0 = lane < cpr * nparts ? sm.part[lane] : none, p1 = lane + 32 < cpr * nparts ? sm.part[lane + 32] : none;
+    const float M = fmaxf(warp_max(fmaxf(p0.x, p1.x)), sm.list.x), M0 = M == -INFINITY ? 0.0f : M;
+    const float sr = warp_sum(p0.y * ex2_approx((p0.x - M0) * c) + p1.y * ex2_approx((p1.x - M0) * c));
+    const float total = sr + sm.list.y * ex2_approx((sm.list.x - M0) * c), r = sm.r;
+    int fault = lane < cpr ? sm.bad[lane] : 0;
+    fault = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(fault)));
+    // a NaN is in one of the sums, a maximum of +inf makes them NaN
+    if (!(total > 0.0f) || !isfinite(total)) fault = max(fault, static_cast<int>(kDevNonFinite));
+    const bool nothing = sm.nothing != 0, leaves = r > 0.0f && sr > 0.0f;
+    const float wt = w / a.temperature;
+    if (rank == 0 && warp == 0) {
+        const float lns = logf(total);
+        float term = 0.0f;
+        for (int i = lane; i < a.n_top; i += 32) {
+            // p ln p is 0 where p is; a listed id that the draft rules out makes the loss infinite
+            const float lnp = sm.lnp[i], p = expf(lnp);
+            if (sm.id[i] >= 0 && p > 0.0f) term += p * (lnp - ((sm.z[i] - M0) / a.temperature - lns));
+        }
+        term = warp_sum(term);
+        if (lane == 0) {
+            if (leaves) term += r * (logf(r) - (logf(sr) - lns));
+            if (fault && !nothing) raise_status(a.status, fault);
+            a.loss[row] = nothing ? 0.0f : fault ? NAN : w * term;
         }
     }
     if (grad == nullptr) return;
-    if (fault) {
-        for (int v = tid; v < nvec; v += kThreads) grad[v] = make_uint4(0u, 0u, 0u, 0u);
+    if (fault || nothing) {
+        for (int v = tid; v < nvec; v += threads) grad[v] = make_uint4(0u, 0u, 0u, 0u);
         return;
     }
-    const float wt = w / a.temperature;
-    const float factor = wt * (mass / total - (rest ? r / sr : 0.0f));
-    for (int v = tid; v < nvec; v += kThreads) {
-        float x[EPV];
+    const float factor = wt * (sm.mass / total - (leaves ? r / sr : 0.0f));
+    const uint64_t minus = f2_pack(-M0, -M0), f2 = f2_pack(factor, factor);
+    for (int v = tid; v < nvec; v += threads) {
+        uint64_t x[EPV / 2];
         unpack<DT>(vec[v], x);
-#pragma unroll
-        for (int i = 0; i < EPV; ++i) x[i] = ex2_approx((x[i] - M0) * c) * factor;
         uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < EPV / 2; ++i) {
+            const uint64_t y = f2_mul(f2_add(x[i], minus), c2);
+            const uint64_t g = f2_mul(f2_pack(ex2_approx(f2_lo(y)), ex2_approx(f2_hi(y))), f2);
             if (DT == 1) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(x[(2 * i) % EPV], x[(2 * i + 1) % EPV]);
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f2_lo(g), f2_hi(g));
                 o[i] = *reinterpret_cast<const uint32_t*>(&h);
             } else {
-                o[i] = __float_as_uint(x[i]);
+                o[2 * (i & 1)] = __float_as_uint(f2_lo(g));
+                o[2 * (i & 1) + 1] = __float_as_uint(f2_hi(g));
             }
         }
         grad[v] = make_uint4(o[0], o[1], o[2], o[3]);
     }
     __syncthreads();  // the list's entries after the vectors that hold them
-    if (mine) {
-        const float g = wt * (mass * (e / total) - p);
-        if (DT == 1) reinterpret_cast<__nv_bfloat16*>(grad)[id - first] = __float2bfloat16_rn(g);
-        else reinterpret_cast<float*>(grad)[id - first] = g;
+    if (warp == 0) {
+        for (int i = lane; i < a.n_top; i += 32) {
+            const int at = sm.id[i] - first;
+            if (sm.id[i] < 0 || at < 0 || at >= n) continue;
+            const float g = wt * (sm.mass * (ex2_approx((sm.z[i] - M0) * c) / total) - expf(sm.lnp[i]));
+            if (DT == 1) reinterpret_cast<__nv_bfloat16*>(grad)[at] = __float2bfloat16_rn(g);
+            else reinterpret_cast<float*>(grad)[at] = g;
+        }
     }
 }
 
@@ -304,12 +378,16 @@ cudaError_t launch(const DistillArgs& a, cudaStream_t stream) {
     while (cpr < kMaxChunks && static_cast<long>(a.rows) * cpr < 152 * 3 && row_seg_elems(a.V, ES, cpr * 2) * ES >= kCopyBytes) cpr *= 2;
     const int seg = row_seg_elems(a.V, ES, cpr);
     const int smem = seg * ES;
+    const int warps = smem > 16384 ? kMaxWarps : smem > 4096 ? 4 : 2;  // of short rows more share an SM
+    // rows at once, as far as shared memory, threads and registers decide it
+    const int at_once = std::min({(226 * 1024) / (smem + static_cast<int>(sizeof(Shared)) + 1024), 2048 / (warps * 32), 24, 24 / warps});
+    const int ahead = std::max(1, 76 * std::max(1, at_once) / cpr);  // half of them: as many rows are still to be read
     auto kernel = distill_kernel<DT>;
     cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * cpr);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(warps * 32));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -322,7 +400,7 @@ cudaError_t launch(const DistillArgs& a, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     count_launch();
-    return cudaLaunchKernelEx(&cfg, kernel, a, cpr, seg, kLog2e / a.temperature);
+    return cudaLaunchKernelEx(&cfg, kernel, a, cpr, seg, ahead, kLog2e / a.temperature);
 }
 
 }  // namespace

@@ -3,13 +3,18 @@
 // codes in one pass) and eagle_linear_fp8_pack (a weight's codes, one scale for
 // each block of 128 x 128).
 //
-// A thread holds 16 neighbouring entries of a row in registers from the load to
-// the codes, so a row is read once: the sum of squares goes over the row's
-// threads (shuffles, then shared memory where a row has several warps), the
-// largest |y| of a block of 128 over eight neighbouring lanes. A scale is the
-// smallest power of two 2^k with amax <= 448 2^k, taken from amax's bits, and
-// stored as the byte k + 127 that the block-scaled tensor instructions read.
-// Sums are fp32: a thread's 16 squares in pairs, then a tree.
+// A thread holds 16 entries of a block of 128 (eight neighbouring lanes hold
+// the block, each 16 bytes of 128 bytes that a load or store covers) in
+// registers from the load to the codes, so a row is read once: the sum of
+// squares goes over the row's threads (shuffles, then shared memory where a row
+// has several warps, one barrier a row), the largest |y| of a block over its
+// eight lanes. A scale is the smallest power of two 2^k with amax <= 448 2^k,
+// taken from amax's bits, and stored as the byte k + 127 that the block-scaled
+// tensor instructions read. Sums are fp32: a thread's 16 squares in four parts,
+// then a tree.
+//
+// Bound by HBM. CTAs stay for several rows, so that the weight comes from L1, and load the next rows before they
+// reduce one where registers allow it.
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -26,46 +31,59 @@ namespace {
 constexpr int kPer = 16;           // entries of a thread
 constexpr int kNormThreads = 256;  // of a CTA, more where a row needs them
 
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[kPer]) {
+// The 16 entries of a thread as loaded: V vectors of 16 bytes.
+template <typename T>
+struct Raw {
+    static constexpr int V = kPer * static_cast<int>(sizeof(T)) / 16, N = 16 / static_cast<int>(sizeof(T));
+    uint4 u[V];
+};
+// Vector q of lane l (0..7) of a block: entries q * 8 N + l N ..
+template <typename T>
+__device__ __forceinline__ int vec_at(int q, int l) { return (q * 8 + l) * Raw<T>::N; }
+
+template <typename T>
+__device__ __forceinline__ void load16(const T* block, int l, int left, Raw<T>& r) {
+#pragma unroll
+    for (int q = 0; q < Raw<T>::V; ++q)
+        r.u[q] = vec_at<T>(q, l) < left ? ld_prior(reinterpret_cast<const uint4*>(block + vec_at<T>(q, l))) : make_uint4(0u, 0u, 0u, 0u);
+}
+// The 16 entries as eight packed pairs (two results an instruction).
+__device__ __forceinline__ void unpack16(const Raw<__nv_bfloat16>& r, uint64_t (&v)[kPer / 2]) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        const uint4 u = ld_prior(reinterpret_cast<const uint4*>(p) + q);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        const uint32_t w[4] = {r.u[q].x, r.u[q].y, r.u[q].z, r.u[q].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[q * 8 + 2 * i] = __uint_as_float(w[i] << 16);
-            v[q * 8 + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        for (int i = 0; i < 4; ++i) v[q * 4 + i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
 }
-__device__ __forceinline__ void load16(const float* p, float (&v)[kPer]) {
+__device__ __forceinline__ void unpack16(const Raw<float>& r, uint64_t (&v)[kPer / 2]) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const uint4 u = ld_prior(reinterpret_cast<const uint4*>(p) + q);
-        v[4 * q] = __uint_as_float(u.x);
-        v[4 * q + 1] = __uint_as_float(u.y);
-        v[4 * q + 2] = __uint_as_float(u.z);
-        v[4 * q + 3] = __uint_as_float(u.w);
+        v[2 * q] = f2_pack(__uint_as_float(r.u[q].x), __uint_as_float(r.u[q].y));
+        v[2 * q + 1] = f2_pack(__uint_as_float(r.u[q].z), __uint_as_float(r.u[q].w));
     }
 }
-// v rounded to the rows' type, stored, and kept as rounded.
-__device__ __forceinline__ void store16(__nv_bfloat16* p, float (&v)[kPer]) {
+// v rounded to the rows' type, kept as rounded, and stored.
+__device__ __forceinline__ void store16(__nv_bfloat16* block, int l, int left, uint64_t (&v)[kPer / 2]) {
     uint32_t w[kPer / 2];
 #pragma unroll
     for (int i = 0; i < kPer / 2; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f2_lo(v[i]), f2_hi(v[i]));
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        v[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
-    if (p == nullptr) return;
+    if (block == nullptr) return;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) reinterpret_cast<uint4*>(p)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    for (int q = 0; q < 2; ++q)
+        if (vec_at<__nv_bfloat16>(q, l) < left)
+            *reinterpret_cast<uint4*>(block + vec_at<__nv_bfloat16>(q, l)) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
 }
-__device__ __forceinline__ void store16(float* p, float (&v)[kPer]) {
-    if (p == nullptr) return;
+__device__ __forceinline__ void store16(float* block, int l, int left, uint64_t (&v)[kPer / 2]) {
+    if (block == nullptr) return;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) reinterpret_cast<float4*>(p)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    for (int q = 0; q < 4; ++q)
+        if (vec_at<float>(q, l) < left)
+            *reinterpret_cast<float4*>(block + vec_at<float>(q, l)) = make_float4(f2_lo(v[2 * q]), f2_hi(v[2 * q]), f2_lo(v[2 * q + 1]), f2_hi(v[2 * q + 1]));
 }
 
 // Scale byte of a block whose largest |y| has these bits; 0 where it is an infinity or NaN.
@@ -74,33 +92,43 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
     if (e == 255) return 0u;
     return static_cast<uint32_t>(max(1, e - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0)));
 }
-// 16 codes of y under a scale byte (0: the block has no scale, its codes are NaN).
-__device__ __forceinline__ uint4 codes16(const float (&y)[kPer], uint32_t byte) {
-    if (byte == 0u) return make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
-    const float inv = __uint_as_float((254u - byte) << 23);
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * i] * inv, y[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * i + 2] * inv, y[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-        w[i] = lo | (hi << 16);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+// Four codes of y * inv; NaN for those of a block without a scale.
+__device__ __forceinline__ uint32_t codes4(const uint64_t* y, float inv, bool none) {
+    const uint64_t i2 = f2_pack(inv, inv), a = f2_mul(y[0], i2), b = f2_mul(y[1], i2);
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f2_lo(a), f2_hi(a)), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f2_lo(b), f2_hi(b)), __NV_SATFINITE, __NV_E4M3);
+    return none ? 0x7f7f7f7fu : lo | (hi << 16);
 }
-__device__ __forceinline__ uint32_t amax_bits(const float (&y)[kPer]) {
-    uint32_t a = 0u;
+// The codes of a thread's 16 entries under a scale byte (0: none).
+template <typename T>
+__device__ __forceinline__ void store_codes(uint8_t* block, int l, int left, const uint64_t (&y)[kPer / 2], uint32_t byte) {
+    const float inv = __uint_as_float((254u - byte) << 23);
+    constexpr int P = Raw<T>::N / 2;  // pairs of a vector
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) a = max(a, __float_as_uint(y[i]) & 0x7fffffffu);
-    return a;
+    for (int q = 0; q < Raw<T>::V; ++q) {
+        if (vec_at<T>(q, l) >= left) continue;
+        uint8_t* to = block + vec_at<T>(q, l);
+        const uint32_t w = codes4(y + q * P, inv, byte == 0u);
+        if (P == 4) *reinterpret_cast<uint2*>(to) = make_uint2(w, codes4(y + q * P + (P == 4 ? 2 : 0), inv, byte == 0u));
+        else *reinterpret_cast<uint32_t*>(to) = w;
+    }
+}
+// The bits of the largest |y|, a NaN before everything.
+__device__ __forceinline__ uint32_t amax_bits(const uint64_t (&y)[kPer / 2]) {
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i)
+        asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(a), "f"(f2_lo(y[i])), "f"(f2_hi(y[i])));
+    return __float_as_uint(a) & 0x7fffffffu;
 }
 
-// The sum of a value over the wpr warps of a row; every thread of the CTA takes part.
+// The sum of a value over the wpr warps of a row; every thread of the CTA takes part. `red`: 32 floats that
+// this call has for itself until two barriers later.
 __device__ __forceinline__ float row_sum(float v, int wpr, float* red) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (wpr == 1) return v;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = warp / wpr * wpr;
-    __syncthreads();  // the last use of red is over
     if (lane == 0) red[warp] = v;
     __syncthreads();
     v = lane < wpr ? red[first + lane] : 0.0f;
@@ -108,110 +136,124 @@ __device__ __forceinline__ float row_sum(float v, int wpr, float* red) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+__device__ __forceinline__ float squares(const uint64_t (&s)[kPer / 2]) {
+    uint64_t t[2] = {0ull, 0ull};
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) t[i & 1] = f2_fma(s[i], s[i], t[i & 1]);
+    const uint64_t u = f2_add(t[0], t[1]);
+    return f2_lo(u) + f2_hi(u);
+}
+__device__ __forceinline__ void times(uint64_t (&s)[kPer / 2], float by) {
+    const uint64_t b = f2_pack(by, by);
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) s[i] = f2_mul(s[i], b);
+}
 
-template <typename T>
+// Rows on their way while one is reduced, as registers allow (64 of 1024 threads an SM). Without: 8192 bf16 entries a
+// row and no residual 3.7 TB/s.
+template <typename T, bool RES>
+constexpr int kAheadRows = sizeof(T) == 2 ? (RES ? 1 : 2) : (RES ? 0 : 1);
+
+template <typename T, bool RES>
 __global__ void __launch_bounds__(1024) rmsnorm_fp8_kernel(RmsnormFp8Args a, int wpr) {
-    __shared__ float red[32];
-    __shared__ int odd;
-    const int tid = threadIdx.x, warp = tid >> 5;
-    const int rpc = (blockDim.x >> 5) / wpr;  // rows of a CTA
-    const int row = blockIdx.x * rpc + warp / wpr;
-    const int at = (tid - warp / wpr * wpr * 32) * kPer;  // this thread's first entry
-    const bool live = row < a.rows && at < a.dim;
+    constexpr int A = kAheadRows<T, RES>, R = A > 1 ? A : 1;
+    __shared__ float red[2][32], red_far[32];
+    const int tid = threadIdx.x, warp = tid >> 5, l = tid & 7;
+    const int rpc = (blockDim.x >> 5) / wpr;  // rows of a CTA at a time
+    const int block = (tid - warp / wpr * wpr * 32) / 8;  // this thread's block of 128 entries
+    const int nb = (a.dim + kFp8Block - 1) / kFp8Block;
+    const int left = a.dim - block * kFp8Block;  // entries from the block's first on
+    const int rows_step = gridDim.x * rpc;
     pdl_launch_dependents();
-    if (tid == 0) odd = 0;
-    float w[kPer];
     pdl_wait_prior();
-    float s[kPer];
+    Raw<T> x[R], r;
+    auto load_row = [&](int row, Raw<T>& to) {
+        const int64_t off = static_cast<int64_t>(row) * a.row_stride + block * kFp8Block;
+        const int n = row < a.rows ? left : 0;
+        load16(static_cast<const T*>(a.x) + off, l, n, to);
+        if (RES) load16(static_cast<const T*>(a.residual) + off, l, n, r);
+    };
+    int row = blockIdx.x * rpc + warp / wpr;
+    if (A > 0) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) s[i] = 0.0f;
-    const size_t off = static_cast<size_t>(row) * a.row_stride + at;
-    if (live) {
-        load16(static_cast<const T*>(a.x) + off, s);
-        if (a.residual) {
-            float r[kPer];
-            load16(static_cast<const T*>(a.residual) + off, r);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) s[i] += r[i];
-            store16(a.sum ? static_cast<T*>(a.sum) + off : static_cast<T*>(nullptr), s);
-        }
-        if (a.weight) load16(static_cast<const T*>(a.weight) + at, w);
+        for (int i = 0; i < A; ++i) load_row(row + i * rows_step, x[i]);
     }
-    if (a.weight) {  // uniform
-        float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int turn = 0; blockIdx.x * rpc + static_cast<int64_t>(turn) * rows_step < a.rows; ++turn, row += rows_step) {  // the CTA's warps together
+        if (A == 0) load_row(row, x[0]);
+        const bool live = row < a.rows;
+        uint64_t s[kPer / 2];
+        unpack16(x[0], s);
+        if (RES) {
+            uint64_t t[kPer / 2];
+            unpack16(r, t);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) t[i & 3] = fmaf(s[i], s[i], t[i & 3]);
-        const float n = static_cast<float>(a.dim);
-        const float sq = row_sum((t[0] + t[1]) + (t[2] + t[3]), wpr, red);
-        float rstd = 1.0f / sqrtf(sq / n + a.eps);
-        // A row whose squares leave fp32's range has them summed at 2^-160 (eps does not count
-        // then); one that holds an infinity or NaN has no norm.
-        const bool far = !(sq <= 3.0e38f);
-        if (wpr > 1 || __any_sync(0xffffffffu, far)) {
-            if (wpr > 1) {
-                if (far) odd = 1;
-                __syncthreads();
-            }
-            if (wpr == 1 || odd) {
+            for (int i = 0; i < kPer / 2; ++i) s[i] = f2_add(s[i], t[i]);
+            store16(a.sum ? static_cast<T*>(a.sum) + static_cast<size_t>(row) * a.row_stride + block * kFp8Block : nullptr, l,
+                    live ? left : 0, s);
+        }
+        if (A > 1) x[0] = x[R - 1];
+        if (A > 0) load_row(row + A * rows_step, x[R - 1]);
+        if (a.weight) {  // uniform
+            const float sq = row_sum(squares(s), wpr, red[turn & 1]);
+            float rstd = rsqrtf(fmaf(sq, a.inv_dim, a.eps));
+            // A row whose squares leave fp32's range has them summed at 2^-160 (eps does not count
+            // then); one that holds an infinity or NaN has no norm.
+            const bool far = !(sq <= 3.0e38f);
+            if (wpr == 1 ? __any_sync(0xffffffffu, far) : __syncthreads_or(far)) {
                 constexpr float kDown = 0x1p-80f;
+                uint64_t low[kPer / 2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) t[i] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) t[i & 3] = fmaf(s[i] * kDown, s[i] * kDown, t[i & 3]);
-                const float low = row_sum((t[0] + t[1]) + (t[2] + t[3]), wpr, red);
+                for (int i = 0; i < kPer / 2; ++i) low[i] = f2_mul(s[i], f2_pack(kDown, kDown));
+                const float lsq = row_sum(squares(low), wpr, red_far);
                 if (far) {
-                    rstd = low <= 3.0e38f ? 1.0f / sqrtf(low / n) : NAN;  // of the row at 2^-80
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i) s[i] = s[i] * rstd * kDown;
-                    rstd = 1.0f;
+                    times(s, lsq <= 3.0e38f ? rsqrtf(lsq * a.inv_dim) : NAN);  // of the row at 2^-80
+                    rstd = kDown;
                 }
             }
-        }
-        if (live) {
+            uint64_t t[kPer / 2];
+            Raw<T> w;  // from L1: held in registers it cost the rows on their way more than it saved
+            load16(static_cast<const T*>(a.weight) + block * kFp8Block, l, left, w);
+            unpack16(w, t);
+            times(s, rstd);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) s[i] = s[i] * rstd * w[i];
+            for (int i = 0; i < kPer / 2; ++i) s[i] = f2_mul(s[i], t[i]);
         }
-    }
-    uint32_t amax = live ? amax_bits(s) : 0u;
+        uint32_t amax = amax_bits(s);  // (entries past the row's end are zeros, or NaN in a row without a norm: not its)
+        amax = left > 0 ? amax : 0u;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (row >= a.rows) return;
-    const uint32_t byte = scale_byte(amax);
-    if (live) *reinterpret_cast<uint4*>(static_cast<char*>(a.codes) + static_cast<size_t>(row) * a.dim + at) = codes16(s, byte);
-    if ((tid & 7) == 0) {
-        const int block = at / kFp8Block;
-        // the row's scales are filled up with zeros; where they reach past the row's threads, its last group writes them
-        const int nb = (a.dim + kFp8Block - 1) / kFp8Block;
-        uint8_t* out = a.scales + static_cast<size_t>(row) * a.scale_stride;
-        if (block < nb) {
+        for (int o = 1; o < 8; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (!live) continue;
+        const uint32_t byte = scale_byte(amax);
+        store_codes<T>(static_cast<uint8_t*>(a.codes) + static_cast<size_t>(row) * a.dim + block * kFp8Block, l, left, s, byte);
+        if (l == 0 && block < nb) {
+            uint8_t* out = a.scales + static_cast<size_t>(row) * a.scale_stride;
             out[block] = static_cast<uint8_t>(byte ? byte : 127u);
             if (byte == 0u) raise_status(a.status, kDevNonFinite);
-            if (block == nb - 1)
+            if (block == nb - 1)  // the row's scales are filled up with zeros
                 for (int b = nb; b < a.scale_stride; ++b) out[b] = 0;
         }
     }
 }
 
-// One CTA of 256 threads for each block of 128 x 128: two threads a row, 64 entries each.
+// One CTA of 256 threads for each block of 128 x 128: eight lanes a row, four rows a thread.
 __global__ void __launch_bounds__(256) fp8_pack_kernel(int N, int K, int scale_stride, const __nv_bfloat16* weight,
                                                        uint8_t* codes, uint8_t* scales) {
     __shared__ uint32_t red[8];
     const int tid = threadIdx.x;
-    const int row = blockIdx.y * kFp8Block + tid / 2, col = blockIdx.x * kFp8Block + (tid & 1) * 64;
+    const int row = blockIdx.y * kFp8Block + tid / 8, col = blockIdx.x * kFp8Block;
     pdl_launch_dependents();
     pdl_wait_prior();
-    float y[4][kPer];
+    // thread: lane tid % 8 of the block's row tid / 8 + 32 i
+    const int l = tid & 7, left = K - col;
+    uint64_t y[4][kPer / 2];
     uint32_t amax = 0u;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const bool live = row < N && col + q * kPer < K;
-        if (live) {
-            load16(weight + static_cast<size_t>(row) * K + col + q * kPer, y[q]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) y[q][i] = 0.0f;
-        }
-        amax = max(amax, amax_bits(y[q]));
+    for (int i = 0; i < 4; ++i) {
+        const int n = row + 32 * i;
+        Raw<__nv_bfloat16> r;
+        load16(weight + static_cast<size_t>(n) * K + col, l, n < N ? left : 0, r);
+        unpack16(r, y[i]);
+        amax = max(amax, amax_bits(y[i]));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -221,9 +263,10 @@ __global__ void __launch_bounds__(256) fp8_pack_kernel(int N, int K, int scale_s
     for (int i = 0; i < 8; ++i) amax = max(amax, red[i]);
     const uint32_t byte = scale_byte(amax);
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        if (row < N && col + q * kPer < K)
-            *reinterpret_cast<uint4*>(codes + static_cast<size_t>(row) * K + col + q * kPer) = codes16(y[q], byte);
+    for (int i = 0; i < 4; ++i) {
+        const int n = row + 32 * i;
+        store_codes<__nv_bfloat16>(codes + static_cast<size_t>(n) * K + col, l, n < N ? left : 0, y[i], byte);
+    }
     if (tid == 0) {
         uint8_t* out = scales + static_cast<size_t>(blockIdx.y) * scale_stride;
         out[blockIdx.x] = static_cast<uint8_t>(byte ? byte : 127u);
@@ -235,12 +278,18 @@ __global__ void __launch_bounds__(256) fp8_pack_kernel(int N, int K, int scale_s
 }  // namespace
 
 cudaError_t launch_rmsnorm_fp8(const RmsnormFp8Args& a, int dtype, cudaStream_t stream) {
-    // warps of a row: one for 512 entries, and so many rows that a CTA has kNormThreads
+    // warps of a row: one for 512 entries, and so many rows that a CTA has kNormThreads (bf16 rows of 32 entries
+    // in a warp each: its other lanes idle, which costs nothing at such sizes)
     const int wpr = (a.dim + 32 * kPer - 1) / (32 * kPer);
-    const int rpc = std::max(1, kNormThreads / 32 / wpr);
-    const dim3 grid(static_cast<unsigned>((a.rows + rpc - 1) / rpc)), block(static_cast<unsigned>(wpr * rpc * 32));
-    if (dtype == 1) return launch_pdl(rmsnorm_fp8_kernel<__nv_bfloat16>, grid, block, 0, stream, a, wpr);
-    return launch_pdl(rmsnorm_fp8_kernel<float>, grid, block, 0, stream, a, wpr);
+    const int rpc = std::max(1, kNormThreads / 32 / wpr), threads = wpr * rpc * 32;
+    const int groups = (a.rows + rpc - 1) / rpc;
+    // 1024 threads an SM at 64 registers each
+    const dim3 grid(static_cast<unsigned>(std::min(groups, 152 * std::max(1, 1024 / threads)))), block(static_cast<unsigned>(threads));
+    if (dtype == 1)
+        return launch_pdl(a.residual ? rmsnorm_fp8_kernel<__nv_bfloat16, true> : rmsnorm_fp8_kernel<__nv_bfloat16, false>, grid,
+                          block, 0, stream, a, wpr);
+    return launch_pdl(a.residual ? rmsnorm_fp8_kernel<float, true> : rmsnorm_fp8_kernel<float, false>, grid, block, 0, stream, a,
+                      wpr);
 }
 
 cudaError_t launch_fp8_pack(int N, int K, int scale_stride, const void* weight, void* codes, uint8_t* scales,

@@ -53,7 +53,7 @@ struct RmsnormFp8Args {
     int64_t row_stride;  // elements
     const void *x, *residual, *weight;
     void* sum;
-    float eps;
+    float eps, inv_dim;  // 1 / dim
     void* codes;
     uint8_t* scales;
     int* status;

@@ -465,6 +465,10 @@ def eagle_fp8_scale_stride(dim: int) -> int:
     return int(_lib.eagle_fp8_scale_stride(dim))
 
 
+def _scale_stride(dim):  # the same without a call into the library
+    return (dim + 511) // 512 * 4
+
+
 def _dtypes(code):
     return _BF16 if code == EAGLE_BF16 else _F32
 
@@ -483,17 +487,19 @@ def eagle_rmsnorm_fp8(rows, dim, dtype, x, row_stride, residual, sum, weight, ep
     """Residual, root-mean-square norm and 8-bit codes with a scale for each 128 entries (weight None: no norm)."""
     fn, dev, dt = "eagle_rmsnorm_fp8", _device(), _dtypes(dtype)
     n = (rows - 1) * row_stride + dim
-    _check(fn, _lib.eagle_rmsnorm_fp8(rows, dim, dtype, _need(fn, "x", _behind(x), dt, n, dev), row_stride,
-                                      _need(fn, "residual", _behind(residual), dt, n, dev),
-                                      _need(fn, "sum", _behind(sum), dt, n, dev), _need(fn, "weight", weight, dt, dim, dev),
+    if row_stride != dim:  # rows inside wider ones
+        x, residual, sum = _behind(x), _behind(residual), _behind(sum)
+    _check(fn, _lib.eagle_rmsnorm_fp8(rows, dim, dtype, _need(fn, "x", x, dt, n, dev), row_stride,
+                                      _need(fn, "residual", residual, dt, n, dev),
+                                      _need(fn, "sum", sum, dt, n, dev), _need(fn, "weight", weight, dt, dim, dev),
                                       float(eps), _need(fn, "codes", codes, _CODES, rows * dim, dev),
-                                      _need(fn, "scales", scales, _EXP, rows * eagle_fp8_scale_stride(dim), dev),
+                                      _need(fn, "scales", scales, _EXP, rows * _scale_stride(dim), dev),
                                       None if ws is None else _ws_on(fn, ws, dev)[0], _stream_on(stream, dev)))
 
 
 def eagle_linear_fp8(rows, out_dim, in_dim, x_codes, x_scales, w_codes, w_scales, out_dtype, out, ws=None, stream=None):
     """out [rows, out_dim] = x w^T on 8-bit codes with power-of-two scales."""
-    fn, dev, stride = "eagle_linear_fp8", _device(), eagle_fp8_scale_stride(in_dim)
+    fn, dev, stride = "eagle_linear_fp8", _device(), _scale_stride(in_dim)
     _check(fn, _lib.eagle_linear_fp8(rows, out_dim, in_dim, _need(fn, "x_codes", x_codes, _CODES, rows * in_dim, dev),
                                      _need(fn, "x_scales", x_scales, _EXP, rows * stride, dev),
                                      _need(fn, "w_codes", w_codes, _CODES, out_dim * in_dim, dev),
