@@ -555,8 +555,9 @@ int eagle_rmsnorm_fp8(int rows, int dim, int dtype, const void* x, int64_t row_s
         row_stride % (dtype == EAGLE_BF16 ? 8 : 4) != 0 || !aligned16(x) || !aligned16(residual) || !aligned16(sum) ||
         !aligned16(weight) || !aligned16(codes))
         return EAGLE_ERR_UNSUPPORTED;
-    const RmsnormFp8Args a{rows, dim, fp8_scale_stride(dim),           row_stride, x,      residual, weight,
-                           sum,  eps, 1.0f / static_cast<float>(dim), codes,      scales, static_cast<int*>(ws)};
+    const float inv = static_cast<float>(1.0 / dim);
+    const RmsnormFp8Args a{rows, dim, fp8_scale_stride(dim), row_stride, x, residual, weight, sum, eps, inv,
+                           static_cast<float>(1.0 / dim - inv), codes, scales, static_cast<int*>(ws)};
     return launch_result(launch_rmsnorm_fp8(a, dtype, static_cast<cudaStream_t>(stream)));
 }
 

@@ -80,7 +80,7 @@ __device__ __forceinline__ T warp_sum(T v) {
     return v;
 }
 template <int DT>
-__global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs a, int cpr, int seg, int ahead, float c) {
+__global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs a, int cpr, int seg, int ahead, float c, double inv_t) {
     extern __shared__ __align__(128) unsigned char row_smem[];
     __shared__ Shared sm;
     constexpr int ES = DT == 1 ? 2 : 4;
@@ -210,16 +210,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
 #pragma unroll
             for (int k = 0; k < kSlots; ++k) {
                 if (k * 32 >= a.n_top) continue;
-                t[k] = (t[k] - top) / a.temperature;
-                if (id[k] >= 0) total += expf(t[k]);
+                t[k] = t[k] - top;
+                if (id[k] >= 0) total += expf(t[k] / a.temperature);
             }
             total = warp_sum(total);
             shift = logf(total);
             if (!(total > 0.0f)) bad = max(bad, static_cast<int>(kDevNonFinite));
-        } else {
-#pragma unroll
-            for (int k = 0; k < kSlots; ++k)
-                if (k * 32 < a.n_top) t[k] /= a.temperature;
         }
         if (!isfinite(shift)) bad = max(bad, static_cast<int>(kDevNonFinite));
         float zsum = 0.0f, psum = 0.0f, low = 0.0f;  // (sum p and what its roundings lost: 1 - sum p is of that size)
@@ -233,7 +229,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
             const int i = k * 32 + lane;
             if (k * 32 >= a.n_top) continue;
             const bool on = id[k] >= 0;
-            const float lnp = on ? t[k] - shift : -INFINITY, p = on ? expf(lnp) : 0.0f;
+            // (t / T and the lse nearly cancel: their difference is rounded once)
+            const float lnp = on ? static_cast<float>(fma(static_cast<double>(t[k]), inv_t, -static_cast<double>(shift))) : -INFINITY;
+            const float p = on ? expf(lnp) : 0.0f;
             if (!(p < INFINITY)) bad = max(bad, static_cast<int>(kDevNonFinite));
             add(p);
             if (on) zsum += ex2_approx((z[k] - z0) * c);  // a NaN or +inf logit makes it NaN
@@ -318,16 +316,23 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
     const bool nothing = sm.nothing != 0, leaves = r > 0.0f && sr > 0.0f;
     const float wt = w / a.temperature;
     if (rank == 0 && warp == 0) {
-        const float lns = logf(total);
+        // The loss is a difference of logarithms, often far smaller than they are: these and the differences in 64
+        // bits (three logarithms a row, beside the other warps' gradient)
+        const double ln = log(static_cast<double>(lane == 0 ? total : lane == 1 ? sr : r));
+        const double lns = __shfl_sync(0xffffffffu, ln, 0), lnsr = __shfl_sync(0xffffffffu, ln, 1), lnr = __shfl_sync(0xffffffffu, ln, 2);
         float term = 0.0f;
-        for (int i = lane; i < a.n_top; i += 32) {
+#pragma unroll
+        for (int k = 0; k < kSlots; ++k) {
+            const int i = k * 32 + lane;
+            if (i >= a.n_top) continue;
             // p ln p is 0 where p is; a listed id that the draft rules out makes the loss infinite
             const float lnp = sm.lnp[i], p = expf(lnp);
-            if (sm.id[i] >= 0 && p > 0.0f) term += p * (lnp - ((sm.z[i] - M0) / a.temperature - lns));
+            const double lnq = (static_cast<double>(z[k]) - static_cast<double>(M0)) * inv_t - lns;
+            if (id[k] >= 0 && p > 0.0f) term += p * static_cast<float>(static_cast<double>(lnp) - lnq);
         }
         term = warp_sum(term);
         if (lane == 0) {
-            if (leaves) term += r * (logf(r) - (logf(sr) - lns));
+            if (leaves) term += r * static_cast<float>(lnr - (lnsr - lns));
             if (fault && !nothing) raise_status(a.status, fault);
             a.loss[row] = nothing ? 0.0f : fault ? NAN : w * term;
         }
@@ -339,7 +344,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
     }
     const float factor = wt * (sm.mass / total - (leaves ? r / sr : 0.0f));
     const uint64_t minus = f2_pack(-M0, -M0), f2 = f2_pack(factor, factor);
-    for (int v = tid; v < nvec; v += threads) {
+    if (warp > 0)
+    for (int v = tid - 32; v < nvec; v += threads - 32) {
         uint64_t x[EPV / 2];
         unpack<DT>(vec[v], x);
         uint32_t o[4];
@@ -400,7 +406,7 @@ cudaError_t launch(const DistillArgs& a, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     count_launch();
-    return cudaLaunchKernelEx(&cfg, kernel, a, cpr, seg, ahead, kLog2e / a.temperature);
+    return cudaLaunchKernelEx(&cfg, kernel, a, cpr, seg, ahead, kLog2e / a.temperature, 1.0 / static_cast<double>(a.temperature));
 }
 
 }  // namespace

@@ -53,7 +53,7 @@ struct RmsnormFp8Args {
     int64_t row_stride;  // elements
     const void *x, *residual, *weight;
     void* sum;
-    float eps, inv_dim;  // 1 / dim
+    float eps, inv_dim, inv_dim_lo;  // 1 / dim as a sum of two
     void* codes;
     uint8_t* scales;
     int* status;
