@@ -4,11 +4,13 @@ Allocation of the caller-owned workspaces and outputs, then the sequence
 tree_init -> expand x D -> rerank -> build_tree -> tree_attention -> verify ->
 kv_compact. With a KvqCfg the cache is the 8-bit one (the tree's K and V are
 stored, attended to and compacted in it), a head given as (codes, scales, group)
-is the 4-bit one, and with n_alt the accepted tokens come with their
-log-probabilities. Every step runs in libeagle's kernels; this module only
+is the 4-bit one, an Fp8Head the 8-bit one, and with n_alt the accepted tokens
+come with their log-probabilities. Every step runs in libeagle's kernels; this module only
 holds buffers and passes pointers.
 """
 from __future__ import annotations
+
+from typing import NamedTuple
 
 import torch
 
@@ -19,13 +21,23 @@ def torch_dtype(code: int) -> torch.dtype:
     return torch.float32 if code == E.EAGLE_F32 else torch.bfloat16
 
 
+class Fp8Head(NamedTuple):
+    """An LM head in 8 bits (eagle_linear_fp8_pack), with the weight of the norm before it (bf16 [H]) if the hidden
+    states come without that norm."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    norm: torch.Tensor | None = None
+    eps: float = 1e-5
+
+
 class DeviceCycle:
     """Buffers for one cycle of a (TreeCfg, KvCfg or KvqCfg) problem on one device.
 
-    n_alt: None, or how many alternatives `logprobs` reports per accepted token (0..16)."""
+    n_alt: None, or how many alternatives `logprobs` reports per accepted token (0..16).
+    fp8_head: None, or the hidden dimension of an Fp8Head: `draft` codes a step's hidden rows into buffers of it."""
 
     def __init__(self, cfg: E.TreeCfg, kv: E.KvCfg | E.KvqCfg, device="cuda", fused_head: bool = False,
-                 n_alt: int | None = None):
+                 n_alt: int | None = None, fp8_head: int | None = None):
         if n_alt is not None and not 0 <= n_alt <= E.MAX_TOPK:
             raise ValueError(f"DeviceCycle: n_alt {n_alt} is not 0..{E.MAX_TOPK}")
         self.cfg, self.kv = cfg, kv
@@ -57,6 +69,9 @@ class DeviceCycle:
             self.lm_lse = torch.empty(B * k, dtype=torch.float32, device=dev)
             self.lm_ids = torch.empty(B * k, k, **i32)
             self.lm_vals = torch.empty(B * k, k, dtype=torch.float32, device=dev)
+        self.fp8_head = fp8_head
+        if fp8_head is not None:
+            self.head_codes, self.head_scales = E.alloc_fp8(B * k, fp8_head, device=dev)
         if n_alt is not None:
             f32 = dict(dtype=torch.float32, device=dev)
             self.logprob = torch.empty(B, D + 1, **f32)
@@ -74,10 +89,16 @@ class DeviceCycle:
         or, with fused_head, reduced to their lse and top-k in the LM head's
         epilogue and expanded from those (draft_logits unused). A weight given
         as (codes, scales, group) is the 4-bit head of eagle_lmhead_quant: for
-        up to 32 rows (24 at H = 8192); past them the 16-bit head takes less time."""
+        up to 32 rows (24 at H = 8192); past them the 16-bit head takes less time.
+        An Fp8Head is the 8-bit head of eagle_linear_fp8, for any number of rows:
+        the hidden rows are normed where it has a norm, coded, and multiplied."""
         cfg = self.cfg
-        if self.fused_head and head is not None and isinstance(head[0], tuple):
-            raise ValueError("DeviceCycle.draft: the 4-bit head has no form with stage 1 in its epilogue (fused_head)")
+        if head is not None and isinstance(head[0], tuple):
+            if self.fused_head:
+                raise ValueError("DeviceCycle.draft: the %s head has no form with stage 1 in its epilogue (fused_head)" %
+                                 ("8-bit" if isinstance(head[0], Fp8Head) else "4-bit"))
+            if isinstance(head[0], Fp8Head) and self.fp8_head != head[1].shape[-1]:
+                raise ValueError(f"DeviceCycle.draft: the cycle was made for 8-bit rows of {self.fp8_head}, not {head[1].shape[-1]}")
         E.eagle_tree_init(cfg, self.ws, stream)
         for s in range(cfg.depth if steps is None else steps):
             if head is not None and self.fused_head:
@@ -88,7 +109,9 @@ class DeviceCycle:
                 continue
             if head is not None:
                 weight, hidden = head
-                if isinstance(weight, tuple):
+                if isinstance(weight, Fp8Head):
+                    self.head_fp8(weight, hidden[s], draft_logits[s], stream)
+                elif isinstance(weight, tuple):
                     codes, scales, group = weight
                     E.eagle_lmhead_quant(cfg, self.ws, hidden.shape[-1], group, hidden[s], codes, scales,
                                          draft_logits[s], stream)
@@ -98,6 +121,15 @@ class DeviceCycle:
                            self.ftok, self.fcount, stream)
         if steps is None:
             E.eagle_rerank(cfg, self.ws, stream)
+
+    def head_fp8(self, weight: Fp8Head, hidden_s, logits_s, stream=None):
+        """8-bit LM head of one step's frontier rows, hidden_s [B*k, H] bf16."""
+        cfg, H = self.cfg, hidden_s.shape[-1]
+        rows = cfg.batch * cfg.top_k
+        E.eagle_rmsnorm_fp8(rows, H, E.EAGLE_BF16, hidden_s, H, None, None, weight.norm, weight.eps, self.head_codes,
+                            self.head_scales, self.ws, stream)
+        E.eagle_linear_fp8(rows, cfg.vocab, H, self.head_codes, self.head_scales, weight.codes, weight.scales, cfg.logit_dtype,
+                           logits_s, self.ws, stream)
 
     def head_topk(self, weight, hidden_s, stream=None):
         """LM head of one step with stage 1 in its epilogue (fused_head)."""
