@@ -65,6 +65,10 @@ cudaError_t launch_fp8_pack(int N, int K, int scale_stride, const void* weight, 
 cudaError_t launch_linear_fp8(int M, int N, int K, const void* x, const uint8_t* x_scales, const void* w,
                               const uint8_t* w_scales, int out_dtype, void* out, int* status, cudaStream_t stream);
 
+// The same for one row of x or two, without the tensor cores.
+cudaError_t launch_linear_fp8_rows(int M, int N, int K, const void* x, const uint8_t* x_scales, const void* w,
+                                   const uint8_t* w_scales, int out_dtype, void* out, cudaStream_t stream);
+
 constexpr int kDistillMaxTop = 256;  // a teacher's list: one thread of a CTA for each entry
 struct DistillArgs {
     int rows, V, n_top;
