@@ -42,7 +42,7 @@ struct Shared {
     float2 part[kMaxChunks * (kMaxWarps - 1)];  // (m, sum) of the rest, of each warp but the first of each CTA of the cluster
     int bad[kMaxChunks];                  // a DeviceError of each CTA, 0 = none
     float2 list;                          // (m, sum) of the listed entries
-    float r, mass;                        // what the list leaves; sum p + r
+    float r, mass, psum;                  // what the list leaves; sum p + r; sum p
     int nothing;                          // a list of padding alone that is the whole distribution
     int id[kDistillMaxTop];               // -1: padding, or no entry of the row
     float z[kDistillMaxTop], lnp[kDistillMaxTop];
@@ -79,6 +79,15 @@ __device__ __forceinline__ T warp_sum(T v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+// ln x of a positive x: the exponent's part apart, so that the logarithm's rounding is that of a value below 0.41.
+__device__ __forceinline__ double ln_fine(float x) {
+    const bool small = x < 0x1p-60f;
+    if (small) x *= 0x1p66f;  // (subnormals)
+    const uint32_t b = __float_as_uint(x) - 0x3f3504f3u;  // (bits of sqrt(1/2): the rest is in [0.71, 1.41))
+    const int e = (static_cast<int>(b) >> 23) - (small ? 66 : 0);
+    return fma(static_cast<double>(e), 0.693147180559945309417, static_cast<double>(logf(__uint_as_float((b & 0x7fffffu) + 0x3f3504f3u))));
+}
+
 template <int DT>
 __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs a, int cpr, int seg, int ahead, float c, double inv_t) {
     extern __shared__ __align__(128) unsigned char row_smem[];
@@ -252,6 +261,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
             // (lanes differ in `low` by what their own last sums lost: far below what matters)
             const float r = whole ? 0.0f : fmaxf(0.0f, (1.0f - psum) - low);
             sm.r = r;
+            sm.psum = psum;
             sm.mass = whole ? 1.0f : psum + r;
             sm.list = make_float2(ztop, zsum);
             sm.nothing = whole && !any;
@@ -308,7 +318,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
     const float2 p0 = lane < cpr * nparts ? sm.part[lane] : none, p1 = lane + 32 < cpr * nparts ? sm.part[lane + 32] : none;
     const float M = fmaxf(warp_max(fmaxf(p0.x, p1.x)), sm.list.x), M0 = M == -INFINITY ? 0.0f : M;
     const float sr = warp_sum(p0.y * ex2_approx((p0.x - M0) * c) + p1.y * ex2_approx((p1.x - M0) * c));
-    const float total = sr + sm.list.y * ex2_approx((sm.list.x - M0) * c), r = sm.r;
+    const float listed = sm.list.y * ex2_approx((sm.list.x - M0) * c), total = sr + listed, r = sm.r;
     int fault = lane < cpr ? sm.bad[lane] : 0;
     fault = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(fault)));
     // a NaN is in one of the sums, a maximum of +inf makes them NaN
@@ -316,10 +326,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
     const bool nothing = sm.nothing != 0, leaves = r > 0.0f && sr > 0.0f;
     const float wt = w / a.temperature;
     if (rank == 0 && warp == 0) {
-        // The loss is a difference of logarithms, often far smaller than they are: these and the differences in 64
-        // bits (three logarithms a row, beside the other warps' gradient)
-        const double ln = log(static_cast<double>(lane == 0 ? total : lane == 1 ? sr : r));
-        const double lns = __shfl_sync(0xffffffffu, ln, 0), lnsr = __shfl_sync(0xffffffffu, ln, 1), lnr = __shfl_sync(0xffffffffu, ln, 2);
+        // The loss is a difference of logarithms, often far smaller than they are: differences in 64 bits, of logarithms
+        // that are within 2^-25 (beside the other warps' gradient)
+        const double lns = ln_fine(total);
         float term = 0.0f;
 #pragma unroll
         for (int k = 0; k < kSlots; ++k) {
@@ -332,7 +341,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
         }
         term = warp_sum(term);
         if (lane == 0) {
-            if (leaves) term += r * static_cast<float>(lnr - (lnsr - lns));
+            if (leaves) {
+                // ln r and ln q_R from the list's side where that is the smaller part
+                const float ps = sm.psum;
+                const double lnr = ps < 0.5f ? static_cast<double>(log1pf(-ps)) : ln_fine(r);
+                const double lnqr = listed < sr ? static_cast<double>(log1pf(-listed / total)) : ln_fine(sr) - lns;
+                term += r * static_cast<float>(lnr - lnqr);
+            }
             if (fault && !nothing) raise_status(a.status, fault);
             a.loss[row] = nothing ? 0.0f : fault ? NAN : w * term;
         }
@@ -342,7 +357,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
         for (int v = tid; v < nvec; v += threads) grad[v] = make_uint4(0u, 0u, 0u, 0u);
         return;
     }
-    const float factor = wt * (sm.mass / total - (leaves ? r / sr : 0.0f));
+    // (sum p + r) / total - r / sr, with sum p + r - r total / sr = sum p - r listed / sr where the list is the smaller part
+    const float factor = wt * (!leaves ? sm.mass / total : listed < sr ? (sm.psum - r * (listed / sr)) / total : sm.mass / total - r / sr);
     const uint64_t minus = f2_pack(-M0, -M0), f2 = f2_pack(factor, factor);
     if (warp > 0)
     for (int v = tid - 32; v < nvec; v += threads - 32) {

@@ -214,6 +214,28 @@ def test_linear(E, dt, rows, out_dim, in_dim):
     _check_linear(out, *ops, dt)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,out_dim,in_dim", [(1, 1, 32), (2, 5, 496), (1, 1003, 5120), (2, 1003, 4608), (1, 70, 16384),
+                                                 (2, 333, 3600), (1, 11000, 4096), (2, 130, 16384), (1, 130000, 128)])
+def test_linear_single_rows(E, dt, rows, out_dim, in_dim):
+    """A row or two: K in chunks of 512 shared by one to eight warps, ends inside a chunk, weights across the rule's limit."""
+    rng = np.random.default_rng(rows * 1013 + out_dim * 37 + in_dim)
+    ops = _operands(rng, rows, out_dim, in_dim)
+    _check_linear(_linear(E, dt, *ops), *ops, dt)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 17, 130, 300])
+def test_linear_scales_of_every_size(E, rows):
+    """Scales from 2^-120 to 2^120 whose products are ordinary: each block's two exponents nearly cancel."""
+    rng = np.random.default_rng(rows)
+    out_dim, in_dim = 9000, 1040
+    x, xs, w, wsc = _operands(rng, rows, out_dim, in_dim)
+    nb = -(-in_dim // 128)
+    xs[:, :nb] = np.array([7, 247, 127, 200, 50, 240, 14, 100, 180])[None]
+    wsc[:, :nb] = 254 - xs[:1, :nb] + rng.integers(-3, 4, (wsc.shape[0], nb))
+    _check_linear(_linear(E, "fp32", x, xs, w, wsc), x, xs, w, wsc, "fp32")
+
+
 @pytest.mark.parametrize("rows", [1, 40, 300])
 def test_linear_one_hot(E, rows):
     """A single code in each row of x picks a weight column under both scales: exact, so no scale is another's."""
@@ -228,17 +250,25 @@ def test_linear_one_hot(E, rows):
     assert np.array_equal(_np(out), want)
 
 
-def test_linear_nan_reaches_its_own_outputs(E):
+@pytest.mark.parametrize("rows", [1, 2, 20, 300])
+def test_linear_nan_reaches_its_own_outputs(E, rows):
     rng = np.random.default_rng(8)
-    x, xs, w, wsc = _operands(rng, 20, 300, 512)
-    x[3, 100] = 0x7F
-    w[200, 7] = 0xFF
-    xs[11, 2] = 255
-    out = _np(_linear(E, "fp32", x, xs, w, wsc))
-    nan = np.isnan(out)
-    want = np.zeros_like(nan)
-    want[3], want[11], want[:, 200] = True, True, True
-    assert np.array_equal(nan, want)
+    for kind in ("x code", "x scale", "w code", "w scale"):
+        x, xs, w, wsc = _operands(rng, rows, 10300, 512)
+        want = np.zeros((rows, 10300), bool)
+        if kind == "x code":
+            x[rows - 1, 100] = 0x7F
+            want[rows - 1] = True
+        elif kind == "x scale":
+            xs[rows - 1, 2] = 255
+            want[rows - 1] = True
+        elif kind == "w code":
+            w[200, 7] = 0xFF
+            want[:, 200] = True
+        else:
+            wsc[1, 3] = 255
+            want[:, 128:256] = True
+        assert np.array_equal(np.isnan(_np(_linear(E, "fp32", x, xs, w, wsc))), want), kind
 
 
 def test_linear_captured_and_other_stream(E):
@@ -269,7 +299,7 @@ def test_linear_captured_and_other_stream(E):
 
 def test_linear_same_result_every_time(E):
     rng = np.random.default_rng(10)
-    for shape in ((2, 4096, 4096), (300, 1300, 1024)):
+    for shape in ((2, 4096, 4096), (5, 4096, 4096), (300, 1300, 1024), (300, 11000, 640)):
         ops = _operands(rng, *shape)
         first = _linear(E, "fp32", *ops)
         for _ in range(3):
