@@ -22,9 +22,11 @@
  *   eagle_tree_attention                  stage 5 (one layer per call)
  *   eagle_verify                          stage 6
  *   eagle_kv_compact                      stage 6b
- * The same cycle over a KV cache of 8-bit codes (eagle_kvq_*) and with 4-bit
- * LM-head weights (eagle_lmhead_quant), and the log-probabilities of a cycle's
- * tokens (eagle_token_logprobs), are further down.
+ * The same cycle over a KV cache of 8-bit codes (eagle_kvq_*), with 4-bit
+ * (eagle_lmhead_quant) or 8-bit LM-head weights (eagle_rmsnorm_fp8,
+ * eagle_linear_fp8), the log-probabilities of a cycle's tokens
+ * (eagle_token_logprobs) and the loss that trains a draft on its target's top
+ * logits (eagle_distill_loss) are further down.
  *
  * Conventions for every call:
  *   - Pointers named in the signatures are device pointers owned by the
@@ -570,12 +572,17 @@ int eagle_rmsnorm_fp8(int rows, int dim, int dtype, const void* x, int64_t row_s
  *   x_codes   [rows, in_dim], x_scales [rows, eagle_fp8_scale_stride(in_dim)] in.
  *   w_codes   [out_dim, in_dim], w_scales [ceil(out_dim / 128),
  *             eagle_fp8_scale_stride(in_dim)] in: one scale for 128 rows and 128 entries.
- *   out       [rows, out_dim] out in out_dtype: fp32 sums of the products on the
- *             tensor cores (order unspecified), rounded once for bf16. NaN codes
- *             or scales make the outputs that read them NaN.
+ *   out       [rows, out_dim] out in out_dtype: fp32 sums of the products (order
+ *             and rounding of the sums unspecified but the same for the same
+ *             arguments; within in_dim * 2^-23 * sum_k |x w| of the exact sum),
+ *             rounded to nearest even for bf16. NaN codes or scales make the
+ *             outputs that read them NaN.
  *   ws        any eagle workspace whose status word receives device faults (2: a
  *             wait gave up), or NULL.
- * in_dim a multiple of 16; code pointers and out 16-byte aligned, scales 4-byte aligned.
+ * in_dim a multiple of 16; code pointers and out 16-byte aligned, scales 4-byte
+ * aligned; out overlaps no operand. Any number of rows: one or two of a small
+ * weight take a path without the tensor cores, many the one whose rate is twice
+ * that of 16-bit operands.
  */
 int eagle_linear_fp8(int rows, int out_dim, int in_dim, const void* x_codes, const uint8_t* x_scales,
                      const void* w_codes, const uint8_t* w_scales, int out_dtype, void* out, void* ws, void* stream);

@@ -18,6 +18,9 @@
 // rest, and one exchange of (m, sum) through distributed shared memory gives
 // every CTA the row's sums. The rest is summed by itself, so that a draft that
 // is sure of the listed ids loses nothing of q_R to cancellation.
+//
+// Measured: 4096 fp32 rows of 32000 (985 MB) 160 us, 91% of HBM; 640 bf16 rows of
+// 128256 (308 MB) 60 us, 76%: six waves of CTAs that run much in step; 10 rows 5.8 us.
 
 #include <cuda_bf16.h>
 
@@ -394,16 +397,17 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
 template <int DT>
 cudaError_t launch(const DistillArgs& a, cudaStream_t stream) {
     constexpr int ES = DT == 1 ? 2 : 4;
-    // CTAs of a row: as many as hold it, more where there are few rows
+    // CTAs of a row: as many as hold it, more where there are fewer than SMs (100 rows of 128256 bf16 entries: four a row
+    // 14.6 us, eight 17.2)
     int cpr = 1;
     while (cpr < kMaxChunks && row_seg_elems(a.V, ES, cpr) * ES > kMaxSegBytes) cpr *= 2;
-    while (cpr < kMaxChunks && static_cast<long>(a.rows) * cpr < 152 * 3 && row_seg_elems(a.V, ES, cpr * 2) * ES >= kCopyBytes) cpr *= 2;
+    while (cpr < kMaxChunks && static_cast<long>(a.rows) * cpr < 152 && row_seg_elems(a.V, ES, cpr * 2) * ES >= kCopyBytes) cpr *= 2;
     const int seg = row_seg_elems(a.V, ES, cpr);
     const int smem = seg * ES;
     const int warps = smem > 16384 ? kMaxWarps : smem > 4096 ? 4 : 2;  // of short rows more share an SM
     // rows at once, as far as shared memory, threads and registers decide it
     const int at_once = std::min({(226 * 1024) / (smem + static_cast<int>(sizeof(Shared)) + 1024), 2048 / (warps * 32), 24, 24 / warps});
-    const int ahead = std::max(1, 76 * std::max(1, at_once) / cpr);  // half of them: as many rows are still to be read
+    const int ahead = std::max(1, 38 * std::max(1, at_once) / cpr);  // a quarter of them: half and all were slower
     auto kernel = distill_kernel<DT>;
     cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
