@@ -25,9 +25,10 @@
 // each holding its 128 of them and half of the rows of x; the first of the pair
 // issues. A stage's weights meet two accumulators of Nr <= 224 rows each, so a
 // tile is 256 x 448.
-// Few rows (CG = 1): one accumulator per tile, two tiles deep; where there are
-// fewer tiles than SMs a cluster's CTAs each take a part of a tile's K and
-// their sums meet in distributed shared memory, added in the CTAs' order.
+// Few rows (CG = 1, up to 128): one accumulator per tile, two tiles deep; the CTAs
+// share the weight's rows evenly. Where there are at most half as many tiles as
+// SMs a cluster's CTAs each take a part of a tile's K and their sums meet in
+// distributed shared memory, added in the CTAs' order.
 //
 // What bounds it. Few rows: HBM and some 4.5 us that a launch costs (10 rows
 // against 128256 x 4096: 93 us, 83% of HBM). Many: the weight comes from L2 once
@@ -60,7 +61,7 @@ constexpr int kTileN = 128;   // weight rows of a CTA's tile (the MMA's M is 128
 constexpr int kStageK = 128;  // codes of K of a stage
 constexpr int kGroup = 4;     // stages of a word of scales, K = 512
 constexpr int kMaxNr = 224;   // rows of x of an accumulator (MMA N): two accumulators and the scales fit in 512 columns
-constexpr int kMaxNr1 = 64;   // (CG = 1)
+constexpr int kMaxNr1 = 128;  // (CG = 1)
 constexpr int kPartRows = 16; // (CG = 1) weight rows in which they are dealt to the CTAs
 constexpr int kMaxStages = 8;
 constexpr int kSfSlots = 3;   // groups of scale words on their way
@@ -713,7 +714,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     const uint32_t red = smem_u32(sf_smem + kSfSlots * sf_slot_bytes);
                     int slot = b0 * 16 / p.split, owner = b0 * 16 % p.split;
 #pragma unroll
-                    for (int b = 0; b < kHalfBlocks1; ++b)
+                    for (int b = 0; b < kHalfBlocks1; ++b) {
+                        if (b * 16 >= live) break;
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             if (b * 16 + j < live) {
@@ -727,6 +729,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                                 ++slot;
                             }
                         }
+                    }
                 } else if (v < min(p.N, tl.n0 + tl.rows)) {
                     const size_t at = static_cast<size_t>(row) * p.N + v;
 #pragma unroll
@@ -745,17 +748,32 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     __syncthreads();
     if (ncta > 1) cg::this_cluster().sync();
     tc_fence_after();
-    if (CG == 1 && p.split > 1 && threadIdx.x < kTileN) {  // one tile a cluster: the ranks' sums, in their order
-        const int rc = unit % p.nrc, v = (unit / p.nrc) * kTileN + static_cast<int>(threadIdx.x);
-        const float* red = reinterpret_cast<const float*>(sf_smem + kSfSlots * sf_slot_bytes);
+    if (CG == 1 && p.split > 1) {
+        // One tile a cluster: the ranks' sums, in their order. A warp to a column, its loads side by side (128 threads
+        // through the columns one after the other: 64 rows against 4096 x 4096 10.1 us, 3 of them here).
+        const int rc = unit % p.nrc, v0 = (unit / p.nrc) * kTileN + lane;
+        const float* red = reinterpret_cast<const float*>(sf_smem + kSfSlots * sf_slot_bytes) + lane;
         const int mn = min(p.Nr, p.M - rc * p.Nr);
-        for (int col = rank; col < mn && v < p.N; col += p.split) {
-            float s = 0.0f;
-            for (int r = 0; r < p.split; ++r) s += red[((col / p.split) * p.split + r) * kTileN + threadIdx.x];
-            const size_t at = static_cast<size_t>(rc * p.Nr + col) * p.N + v;
-            if (BF16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(s);
-            else static_cast<float*>(p.out)[at] = s;
+        for (int s = warp; s * p.split + rank < mn; s += kLinThreads / 32) {
+            const float* from = red + s * p.split * kTileN;
+            float sum[kTileN / 32];
+#pragma unroll
+            for (int i = 0; i < kTileN / 32; ++i) sum[i] = 0.0f;
+#pragma unroll
+            for (int r = 0; r < kMaxSplit; ++r) {
+                if (r >= p.split) break;
+#pragma unroll
+                for (int i = 0; i < kTileN / 32; ++i) sum[i] += from[r * kTileN + i * 32];
+            }
+            const size_t at = static_cast<size_t>(rc * p.Nr + s * p.split + rank) * p.N + v0;
+#pragma unroll
+            for (int i = 0; i < kTileN / 32; ++i) {
+                if (v0 + i * 32 >= p.N) break;
+                if (BF16) static_cast<__nv_bfloat16*>(p.out)[at + i * 32] = __float2bfloat16_rn(sum[i]);
+                else static_cast<float*>(p.out)[at + i * 32] = sum[i];
+            }
         }
+        __syncwarp();
     }
     if (warp == 1) {
         if (CG == 1)
@@ -860,8 +878,11 @@ cudaError_t launch(LinParams& p, const void* x, const void* w, cudaStream_t stre
     e = clusters_at_once<CG, NSUB, BF16>(ncta, &fit);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    // (a cluster that splits K has one tile; CTAs that share the weight's rows evenly have one at least)
-    cfg.gridDim = dim3(static_cast<unsigned>((p.split > 1 ? p.ntiles : std::min(p.ntiles, std::max(1, fit))) * ncta));
+    // A cluster that splits K has one tile. CTAs that share the weight's rows evenly have 16 rows at least, so that
+    // fewer tiles than SMs still keep all of them busy (one tile a CTA / so, us: 10 rows against 10240 x 8192 24.9 /
+    // 23.1, 100 rows against 12288 x 4096 17.1 / 16.0, 3 rows against 14336 x 4096 14.6 / 14.9).
+    const int work = CG == 1 && p.split == 1 && p.nrc == 1 ? (p.N + kPartRows - 1) / kPartRows : p.ntiles;
+    cfg.gridDim = dim3(static_cast<unsigned>((p.split > 1 ? p.ntiles : std::min(work, std::max(1, fit))) * ncta));
     cfg.blockDim = dim3(kLinThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
@@ -897,13 +918,18 @@ cudaError_t launch_dtype(int M, int N, int K, const void* x, const uint8_t* x_sc
     const int subs = (M + kMaxNr - 1) / kMaxNr;
     const bool few = static_cast<long>(subs) * p.nwt * 2 <= sms;
     if (M > kMaxNr1 && !few) {
-        // Pairs: the fewest accumulators of up to 224 rows, evenly, two of them to a tile
+        // Pairs: the fewest accumulators of up to 224 rows, evenly, two of them to a tile. (Up to 128 rows CTAs by
+        // themselves, which share the weight evenly, wait less for memory than pairs: 72 rows against 128256 x 4096
+        // 114 us by pairs, 99; 128 rows 110, 105.)
         const int per_row = round_up(subs, subs > 1 ? 2 : 1);
         p.Nr = round_up((M + per_row - 1) / per_row, 16);
         p.chunk = BF16 ? p.per : kF32Chunk2;
         return subs > 1 ? launch<2, 2, BF16>(p, x, w, stream) : launch<2, 1, BF16>(p, x, w, stream);
     }
-    p.Nr = std::min(kMaxNr1, round_up(M, 16));
+    // 64 rows a tile while there are SMs for more than eight parts of K (500 rows against 512 x 4096: 7.5 us, 8.4 with
+    // 128), 128 else (200 against 2048 x 4096: 9.3 us with 64, 8.6; 90 against 6144 x 4096: 12.9, 10.5)
+    const int max_rows = ((M + kMaxNr1 - 1) / kMaxNr1) * p.nwt * kMaxSplit <= sms ? 64 : kMaxNr1, chunks = (M + max_rows - 1) / max_rows;
+    p.Nr = round_up((M + chunks - 1) / chunks, 16);
     if (few) {
         // Few tiles: K split over clusters, one tile a cluster
         const int tiles = (M + p.Nr - 1) / p.Nr * p.nwt;
@@ -926,8 +952,8 @@ cudaError_t launch_dtype(int M, int N, int K, const void* x, const uint8_t* x_sc
 cudaError_t launch_linear_fp8(int M, int N, int K, const void* x, const uint8_t* x_scales, const void* w,
                               const uint8_t* w_scales, int out_dtype, void* out, int* status, cudaStream_t stream) {
     // One row or two of a small weight: without the tensor cores' fixed cost (us, rows kernel / this one: 1 row 512 x
-    // 2048 2.3 / 5.1, 4096 x 4096 4.5 / 6.7, 6144 x 4096 6.2 / 8.4, 14336 x 4096 14.0 / 14.4, 128256 x 4096 98 / 90;
-    // 2 rows 4096 x 4096 5.7 / 6.8, 6144 x 4096 7.6 / 8.4, 8192 x 3584 11.7 / 8.7, 14336 x 4096 16.6 / 14.4)
+    // 2048 2.3 / 4.8, 4096 x 4096 4.7 / 6.4, 6144 x 4096 6.4 / 8.0, 12288 x 4096 12.9 / 13.9, 128256 x 4096 98 / 90;
+    // 2 rows 4096 x 4096 5.9 / 6.4, 6144 x 4096 7.7 / 8.0, 8192 x 3584 11.7 / 8.4, 14336 x 4096 16.6 / 14.4)
     const int64_t weight = static_cast<int64_t>(N) * K;
     if ((M == 1 && weight <= 48 << 20) || (M == 2 && weight <= 25 << 20)) return launch_linear_fp8_rows(M, N, K, x, x_scales, w, w_scales, out_dtype, out, stream);
     return out_dtype == 1 ? launch_dtype<true>(M, N, K, x, x_scales, w, w_scales, out, status, stream)

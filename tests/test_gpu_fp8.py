@@ -224,6 +224,26 @@ def test_linear_single_rows(E, dt, rows, out_dim, in_dim):
     _check_linear(_linear(E, dt, *ops), *ops, dt)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,out_dim,in_dim", [
+    (66, 9729, 1040), (100, 14336, 528), (128, 20001, 4240), (113, 9800, 16),                # CTAs share the weight's rows
+    (64, 4096, 4096), (90, 6100, 2064), (128, 130, 8192), (128, 8192, 1040), (97, 1000, 3600),  # parts of K
+    (200, 2048, 4096), (257, 515, 5136), (500, 512, 4096),
+    (129, 9729, 2064), (150, 10100, 2512), (224, 12000, 4240)])                              # pairs, one accumulator
+def test_linear_dealt(E, dt, rows, out_dim, in_dim):
+    """On both sides of the rules that deal the weight's rows, K or the rows of x to the CTAs; what lies before and
+    behind the outputs is left."""
+    rng = np.random.default_rng(rows * 1019 + out_dim * 41 + in_dim)
+    ops = _operands(rng, rows, out_dim, in_dim)
+    around = torch.full((rows * out_dim + 128,), 7.0, dtype=DT[dt], device="cuda")
+    out = around[64:-64].view(rows, out_dim)
+    ws = _ws(E)
+    E.eagle_linear_fp8(rows, out_dim, in_dim, *[torch.from_numpy(t).cuda() for t in ops], _code(E, dt), out, ws)
+    assert E.eagle_status_fetch(ws) == 0
+    _check_linear(out, *ops, dt)
+    assert bool((around[:64] == 7).all()) and bool((around[-64:] == 7).all())
+
+
 @pytest.mark.parametrize("rows", [1, 2, 17, 130, 300])
 def test_linear_scales_of_every_size(E, rows):
     """Scales from 2^-120 to 2^120 whose products are ordinary: each block's two exponents nearly cancel."""
