@@ -25,13 +25,13 @@
 // each holding its 128 of them and half of the rows of x; the first of the pair
 // issues. A stage's weights meet two accumulators of Nr <= 224 rows each, so a
 // tile is 256 x 448.
-// Few rows (CG = 1, up to 128): one accumulator per tile, two tiles deep; the CTAs
+// Few rows (CG = 1, up to 224): one accumulator per tile, two tiles deep; the CTAs
 // share the weight's rows evenly. Where there are at most half as many tiles as
 // SMs a cluster's CTAs each take a part of a tile's K and their sums meet in
 // distributed shared memory, added in the CTAs' order.
 //
-// What bounds it. Few rows: HBM and some 4.5 us that a launch costs (10 rows
-// against 128256 x 4096: 93 us, 83% of HBM). Many: the weight comes from L2 once
+// What bounds it. Few rows: HBM and some 4 us that a launch costs (10 rows
+// against 128256 x 4096: 82 us, 95% of HBM). Many: the weight comes from L2 once
 // for each row chunk of a tile, and L2 gives 7.2 TB/s of lines that no two SMs ask
 // for together, hence the two accumulators (with one, 225 us for the next case);
 // then the card's power: 640 rows against 128256 x 4096 222 us at the start of a
@@ -61,7 +61,7 @@ constexpr int kTileN = 128;   // weight rows of a CTA's tile (the MMA's M is 128
 constexpr int kStageK = 128;  // codes of K of a stage
 constexpr int kGroup = 4;     // stages of a word of scales, K = 512
 constexpr int kMaxNr = 224;   // rows of x of an accumulator (MMA N): two accumulators and the scales fit in 512 columns
-constexpr int kMaxNr1 = 128;  // (CG = 1)
+constexpr int kMaxNrFew = 128;  // (CG = 1, few tiles)
 constexpr int kPartRows = 16; // (CG = 1) weight rows in which they are dealt to the CTAs
 constexpr int kMaxStages = 8;
 constexpr int kSfSlots = 3;   // groups of scale words on their way
@@ -151,20 +151,35 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
     return a;
 }
+// On a barrier of the pair's first CTA, for what this thread has written to its own CTA's memory ...
 __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
-// A bounded wait by a whole warp, whose lanes leave it together, for arrivals from the other CTA of a pair as
-// well. Without the hint of how long to sleep: that cost some 30 clocks a stage.
+// ... and without anything written. (That release takes so long that scales came late with it: 10 rows against
+// 128256 x 4096 92 us, 82 with arrivals within the CTA; 640 rows of zeros 193, 181.)
+__device__ __forceinline__ void arrive_at_relaxed(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// A bounded wait by a whole warp, whose lanes leave it together. PEER: for what the other CTA of a pair wrote, too (the
+// wider scope at every wait: 640 rows of zeros against 128256 x 4096 181 us, 177 without). Without the hint of how long
+// to sleep: that cost some 30 clocks a stage.
+template <bool PEER = false>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
     for (uint32_t i = 0; i < (1u << 21); ++i) {
         uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-            " selp.u32 %0, 1, 0, p;\n}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
+        if (PEER)
+            asm volatile(
+                "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+                " selp.u32 %0, 1, 0, p;\n}"
+                : "=r"(ok)
+                : "r"(bar), "r"(parity)
+                : "memory");
+        else
+            asm volatile(
+                "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                : "=r"(ok)
+                : "r"(bar), "r"(parity)
+                : "memory");
         if (__all_sync(0xffffffffu, ok)) return true;
     }
     return false;
@@ -174,8 +189,7 @@ __device__ __forceinline__ bool wait_warp_sleep(uint32_t bar, uint32_t parity) {
     for (uint32_t i = 0; i < (1u << 16); ++i) {
         uint32_t ok;
         asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-            " selp.u32 %0, 1, 0, p;\n}"
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
             : "=r"(ok)
             : "r"(bar), "r"(parity), "r"(20000u)
             : "memory");
@@ -245,16 +259,17 @@ __device__ __forceinline__ void store_block(const CUtensorMap* map, uint32_t src
 }
 
 // Blocks of 16 columns of an accumulator that the warps of one half read.
-constexpr int kHalfBlocks = kMaxNr / 32, kHalfBlocks1 = kMaxNr1 / 32;
+constexpr int kHalfBlocks = kMaxNr / 32;
 __device__ __forceinline__ int half_first(int Nr, int half) { return half ? (Nr / 16 + 1) / 2 : 0; }
 __device__ __forceinline__ int half_count(int Nr, int half) { return half ? Nr / 32 : (Nr / 16 + 1) / 2; }
 
-// CG: CTAs that share an MMA. NSUB: accumulators of a tile. tm_more: the output's map (CG = 2), or the weight's with
+// CG: CTAs that share an MMA, and accumulators of a tile. tm_more: the output's map (CG = 2), or the weight's with
 // boxes of kPartRows rows (CG = 1).
-template <int CG, int NSUB, bool BF16>
+template <int CG, bool BF16>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_fp8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                       const __grid_constant__ CUtensorMap tm_more, const LinParams p) {
+    constexpr int NSUB = CG;  // accumulators of a tile
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -401,7 +416,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         // The next group's scale words into this slot's columns. The slot was filled
                         // after the MMAs that read these columns last had ended.
                         const bool first = kg == kb, last = kg + kGroup >= ke;
-                        if (!wait_warp(sf_full + slot * 8, sf_phase) ||
+                        if (!wait_warp<CG == 2>(sf_full + slot * 8, sf_phase) ||
                             (first && !wait_warp(acc_empty + buf * 8, acc_phase))) {
                             ok = false;
                             break;
@@ -501,7 +516,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const uint32_t sf_empty = smem_u32(bar_sf_empty), sf_full = cluster_addr(bar_sf_full, lead);
         uint32_t slot = 0, sf_phase = 1;
         bool ok = true;
-        constexpr int kBlocks = CG == 1 ? 1 : 2 * NSUB;  // 128-row blocks of x at most
+        constexpr int kBlocks = 2 * NSUB;  // 128-row blocks of x at most
         constexpr int kWRows = CG == 1 ? 4 : 1;  // (a part's rows may lie in two of the weight's blocks)
         const int g0 = k0 / kGroup, g1 = (k1 + kGroup - 1) / kGroup;
         uint32_t ww[kWRows], xw[kBlocks][4];
@@ -552,7 +567,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             for (int b = 0; b < kBlocks; ++b)
                 if (b < NSUB * p.sf_blocks) sts128(dst + (1 + b) * kSfBytes, make_uint4(xw[b][0], xw[b][1], xw[b][2], xw[b][3]));
             fence_proxy_async_smem();
-            arrive_at(sf_full + slot * 8);
+            if (CG == 1 || rank == lead) mbar_arrive(&bar_sf_full[slot]);
+            else arrive_at(sf_full + slot * 8);
             if (++slot == kSfSlots) {
                 slot = 0;
                 sf_phase ^= 1;
@@ -587,7 +603,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         auto release = [&](uint32_t b) {  // the accumulator may take its next sums
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_at(freed + b * 8);
+            if (lane != 0) return;
+            if (CG == 1 || rank == lead) mbar_arrive(&bar_acc_empty[b]);
+            else arrive_at_relaxed(freed + b * 8);  // (its loads have ended, nothing in memory goes with it)
         };
         auto next = [&]() {
             if (NSUB == 2) {
@@ -704,15 +722,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     }
                 }
             } else {
-                float acc[kHalfBlocks1][16];
+                float acc[kHalfBlocks][16];
 #pragma unroll
-                for (int b = 0; b < kHalfBlocks1; ++b)
+                for (int b = 0; b < kHalfBlocks; ++b)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) acc[b][j] = 0.0f;
                 for (int kb = k0; ok && kb < k1; kb += p.chunk, next()) {
                     if (!wait_full(buf)) break;
 #pragma unroll
-                    for (int b = 0; b < kHalfBlocks1; ++b) {
+                    for (int b = 0; b < kHalfBlocks; ++b) {
                         if (b >= nb) continue;
                         float x[16];
                         tmem_ld16(from + buf * p.acc_stride + b * 16, x);
@@ -728,7 +746,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     const uint32_t red = smem_u32(sf_smem + kSfSlots * sf_slot_bytes);
                     int slot = b0 * 16 / p.split, owner = b0 * 16 % p.split;
 #pragma unroll
-                    for (int b = 0; b < kHalfBlocks1; ++b) {
+                    for (int b = 0; b < kHalfBlocks; ++b) {
                         if (b * 16 >= live) break;
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
@@ -747,7 +765,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 } else if (v < min(p.N, tl.n0 + tl.rows)) {
                     const size_t at = static_cast<size_t>(row) * p.N + v;
 #pragma unroll
-                    for (int b = 0; b < kHalfBlocks1; ++b) {
+                    for (int b = 0; b < kHalfBlocks; ++b) {
                         if (b * 16 >= live) continue;
                         const int64_t off = static_cast<int64_t>(b) * 16 * p.N;
                         if (BF16) store_rows(static_cast<__nv_bfloat16*>(p.out) + at + off, p.N, live - b * 16, acc[b]);
@@ -826,7 +844,7 @@ int sm_count() {
 
 // How many clusters of ncta CTAs run at once (GPCs hold no whole number of them), asked once for each size and
 // device. A CTA has an SM for itself, whatever its share of the shared memory.
-template <int CG, int NSUB, bool BF16>
+template <int CG, bool BF16>
 cudaError_t clusters_at_once(int ncta, int* n) {
     *n = sm_count();
     if (ncta == 1) return cudaSuccess;
@@ -836,7 +854,7 @@ cudaError_t clusters_at_once(int ncta, int* n) {
     if (e != cudaSuccess) return e;
     std::atomic<int>& slot = known[dev % kMaxDevices][ncta];
     if ((*n = slot.load(std::memory_order_relaxed)) > 0) return cudaSuccess;
-    e = ensure_dyn_smem(reinterpret_cast<const void*>(linear_fp8_kernel<CG, NSUB, BF16>), kSmemBudget);
+    e = ensure_dyn_smem(reinterpret_cast<const void*>(linear_fp8_kernel<CG, BF16>), kSmemBudget);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -849,15 +867,16 @@ cudaError_t clusters_at_once(int ncta, int* n) {
     cfg.dynamicSmemBytes = kSmemBudget;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(n, linear_fp8_kernel<CG, NSUB, BF16>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(n, linear_fp8_kernel<CG, BF16>, &cfg);
     if (e == cudaSuccess && *n > 0) slot.store(*n, std::memory_order_relaxed);
     return e;
 }
 
 int round_up(int x, int to) { return (x + to - 1) / to * to; }
 
-template <int CG, int NSUB, bool BF16>
+template <int CG, bool BF16>
 cudaError_t launch(LinParams& p, const void* x, const void* w, cudaStream_t stream) {
+    constexpr int NSUB = CG;
     const int ncta = CG == 2 ? 2 : p.split;
     p.nrc = (p.M + p.Nr * NSUB - 1) / (p.Nr * NSUB);
     p.ntiles = p.nrc * ((p.nwt + CG - 1) / CG);
@@ -886,10 +905,10 @@ cudaError_t launch(LinParams& p, const void* x, const void* w, cudaStream_t stre
         return cudaErrorInvalidValue;
     }
     const int smem = rest + p.stages * p.stage_bytes;
-    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(linear_fp8_kernel<CG, NSUB, BF16>), smem);
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(linear_fp8_kernel<CG, BF16>), smem);
     if (e != cudaSuccess) return e;
     int fit = 0;
-    e = clusters_at_once<CG, NSUB, BF16>(ncta, &fit);
+    e = clusters_at_once<CG, BF16>(ncta, &fit);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     // A cluster that splits K has one tile. CTAs that share the weight's rows evenly have 16 rows at least, so that
@@ -910,7 +929,7 @@ cudaError_t launch(LinParams& p, const void* x, const void* w, cudaStream_t stre
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     count_launch();
-    return cudaLaunchKernelEx(&cfg, linear_fp8_kernel<CG, NSUB, BF16>, tw, tx, to, p);
+    return cudaLaunchKernelEx(&cfg, linear_fp8_kernel<CG, BF16>, tw, tx, to, p);
 }
 
 template <bool BF16>
@@ -931,18 +950,19 @@ cudaError_t launch_dtype(int M, int N, int K, const void* x, const uint8_t* x_sc
     const int sms = sm_count();
     const int subs = (M + kMaxNr - 1) / kMaxNr;
     const bool few = static_cast<long>(subs) * p.nwt * 2 <= sms;
-    if (M > kMaxNr1 && !few) {
-        // Pairs: the fewest accumulators of up to 224 rows, evenly, two of them to a tile. (Up to 128 rows CTAs by
-        // themselves, which share the weight evenly, wait less for memory than pairs: 72 rows against 128256 x 4096
-        // 114 us by pairs, 99; 128 rows 110, 105.)
-        const int per_row = round_up(subs, subs > 1 ? 2 : 1);
+    if (M > kMaxNr && !few) {
+        // Pairs: the fewest accumulators of up to 224 rows, evenly, two of them to a tile. (What one accumulator holds is
+        // for CTAs by themselves, which share the weight evenly: 224 rows against 128256 x 4096 110 us by pairs, 99;
+        // 128 rows 109, 88.)
+        const int per_row = round_up(subs, 2);
         p.Nr = round_up((M + per_row - 1) / per_row, 16);
         p.chunk = BF16 ? p.per : kF32Chunk2;
-        return subs > 1 ? launch<2, 2, BF16>(p, x, w, stream) : launch<2, 1, BF16>(p, x, w, stream);
+        return launch<2, BF16>(p, x, w, stream);
     }
-    // 64 rows a tile while there are SMs for more than eight parts of K (500 rows against 512 x 4096: 7.5 us, 8.4 with
-    // 128), 128 else (200 against 2048 x 4096: 9.3 us with 64, 8.6; 90 against 6144 x 4096: 12.9, 10.5)
-    const int max_rows = ((M + kMaxNr1 - 1) / kMaxNr1) * p.nwt * kMaxSplit <= sms ? 64 : kMaxNr1, chunks = (M + max_rows - 1) / max_rows;
+    // Few tiles: 64 rows each while there are SMs for more than eight parts of K (500 rows against 512 x 4096: 7.5 us, 8.4
+    // with 128), 128 else (200 against 2048 x 4096: 9.3 us with 64, 8.6; 90 against 6144 x 4096: 12.9, 10.5)
+    const int max_rows = !few ? kMaxNr : (M + kMaxNrFew - 1) / kMaxNrFew * p.nwt * kMaxSplit <= sms ? 64 : kMaxNrFew;
+    const int chunks = (M + max_rows - 1) / max_rows;
     p.Nr = round_up((M + chunks - 1) / chunks, 16);
     if (few) {
         // Few tiles: K split over clusters, one tile a cluster
@@ -950,7 +970,7 @@ cudaError_t launch_dtype(int M, int N, int K, const void* x, const uint8_t* x_sc
         const int groups = p.per / kGroup;
         int want = std::max(1, std::min({kMaxSplit, sms / tiles, groups}));
         for (int fit = 0; want > 1; --want) {
-            const cudaError_t e = clusters_at_once<1, 1, BF16>(want, &fit);
+            const cudaError_t e = clusters_at_once<1, BF16>(want, &fit);
             if (e != cudaSuccess) return e;
             if (fit >= tiles) break;
         }
@@ -958,7 +978,7 @@ cudaError_t launch_dtype(int M, int N, int K, const void* x, const uint8_t* x_sc
         p.split = (groups * kGroup + p.per - 1) / p.per;
     }
     p.chunk = BF16 ? p.per : kF32Chunk1;
-    return launch<1, 1, BF16>(p, x, w, stream);
+    return launch<1, BF16>(p, x, w, stream);
 }
 
 }  // namespace
@@ -966,10 +986,11 @@ cudaError_t launch_dtype(int M, int N, int K, const void* x, const uint8_t* x_sc
 cudaError_t launch_linear_fp8(int M, int N, int K, const void* x, const uint8_t* x_scales, const void* w,
                               const uint8_t* w_scales, int out_dtype, void* out, int* status, cudaStream_t stream) {
     // One row or two of a small weight: without the tensor cores' fixed cost (us, rows kernel / this one: 1 row 512 x
-    // 2048 2.3 / 4.8, 4096 x 4096 4.7 / 6.4, 6144 x 4096 6.4 / 8.0, 12288 x 4096 12.9 / 13.9, 128256 x 4096 98 / 90;
-    // 2 rows 4096 x 4096 5.9 / 6.4, 6144 x 4096 7.7 / 8.0, 8192 x 3584 11.7 / 8.4, 14336 x 4096 16.6 / 14.4)
+    // 2048 2.3 / 4.0, 4096 x 4096 4.7 / 5.9, 6144 x 4096 6.4 / 7.5, 8192 x 4096 8.9 / 7.9, 12288 x 4096 12.9 / 12.7;
+    // 2 rows 2048 x 4096 3.8 / 5.4, 4096 x 4096 5.9 / 5.9, 6144 x 4096 7.7 / 7.5, 8192 x 3584 11.7 / 7.6)
     const int64_t weight = static_cast<int64_t>(N) * K;
-    if ((M == 1 && weight <= 48 << 20) || (M == 2 && weight <= 25 << 20)) return launch_linear_fp8_rows(M, N, K, x, x_scales, w, w_scales, out_dtype, out, stream);
+    if ((M == 1 && weight <= 28 << 20) || (M == 2 && weight <= 17 << 20))
+        return launch_linear_fp8_rows(M, N, K, x, x_scales, w, w_scales, out_dtype, out, stream);
     return out_dtype == 1 ? launch_dtype<true>(M, N, K, x, x_scales, w, w_scales, out, status, stream)
                           : launch_dtype<false>(M, N, K, x, x_scales, w, w_scales, out, status, stream);
 }

@@ -1,6 +1,6 @@
 // eagle_linear_fp8 for one row of x or two, without the tensor cores (sm_103a).
 //
-// The tensor-core kernel (k_linear_fp8.cu) has a fixed cost of some 4.5 us
+// The tensor-core kernel (k_linear_fp8.cu) has a fixed cost of some 4 us
 // (tensor memory, TMA descriptors, the pipeline's ends, a cluster's exchange);
 // a projection's weight for a single token streams in less. Here a warp holds
 // 512 neighbouring codes of x (16 a lane, as fp32 values) and goes down the
