@@ -34,10 +34,10 @@
 // against 128256 x 4096: 82 us, 95% of HBM). Many: the weight comes from L2 once
 // for each row chunk of a tile, and L2 gives 7.2 TB/s of lines that no two SMs ask
 // for together, hence the two accumulators (with one, 225 us for the next case);
-// then the card's power: 640 rows against 128256 x 4096 222 us at the start of a
-// series (3.0 PFLOP/s at 1.7 GHz), 255 us in a long one (1.5 GHz), 201 us on zeros
-// (1.95 GHz; 164 us without loads and stores); 4001 rows against 14336 x 4096 137
-// us, 157 in a long series, 123 on zeros (3.8 PFLOP/s). Sharing x's boxes over a
+// then the card's power: 640 rows against 128256 x 4096 206 us at the start of a
+// series (3.3 PFLOP/s at 1.7 GHz), 237 us in a long one (1.5 GHz), 177 us on zeros
+// (1.95 GHz; 164 us without loads and stores); 4001 rows against 14336 x 4096 132
+// us, 151 in a long series, 117 on zeros (4.0 PFLOP/s). Sharing x's boxes over a
 // cluster of two pairs (TMA multicast) was slower: 144 SMs, and four CTAs in step
 // (263 us on zeros).
 
