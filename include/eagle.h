@@ -615,9 +615,11 @@ int eagle_linear_fp8_pack(int out_dim, int in_dim, const void* weight, void* cod
  * loss and gradient 0):
  *   loss = weight * (sum p (ln p - ln q) + r (ln r - ln q_R)),
  * r = max(0, 1 - sum p) what the list leaves and q_R the draft's probability of
- * everything else (the r term only with teacher_lse, and where r and q_R are
- * above 0); dlogits = d loss / d logits, fp32 rounded once. Multiply the weights
- * by T^2 for the usual scale at other temperatures.
+ * everything else, however small (the r term only with teacher_lse and r above 0,
+ * and not where everything else is ruled out: its largest logit -inf, or more than
+ * 2^20 max(1, T) under the row's largest, as a mask of the type's lowest value is);
+ * dlogits = d loss / d logits, fp32 rounded once. Multiply the weights by T^2 for
+ * the usual scale at other temperatures.
  * A row with a NaN or +inf logit or no finite one, a NaN or infinite weight or
  * lse, or a list with a NaN, a +inf or no finite logit raises status 1; an id >=
  * V or twice in a list status 3: its loss is NaN, its gradient 0. Of `cfg` only

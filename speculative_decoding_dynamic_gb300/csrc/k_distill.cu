@@ -16,8 +16,12 @@
 // arithmetic). The first warp takes the listed entries out of the row and then
 // works out the target's side while the others sum exp((z - m) / T) over the
 // rest, and one exchange of (m, sum) through distributed shared memory gives
-// every CTA the row's sums. The rest is summed by itself, so that a draft that
-// is sure of the listed ids loses nothing of q_R to cancellation.
+// every CTA the row's sums. The rest is summed by itself and relative to its own
+// largest logit m_R, so that a draft that is sure of the listed ids loses nothing
+// of q_R to cancellation, and however far the rest lies below them nothing of it
+// underflows: with s = sum over the rest of exp((z - m_R) / T), which is at least 1,
+//   ln q_R  = (m_R - M) / T + ln s - ln total
+//   dL/dz_j = (1/T) exp((z_j - m_R) / T) ((sum p + r) exp((m_R - M) / T) / total - r / s)
 //
 // Measured: 4096 fp32 rows of 32000 (985 MB) 160 us, 91% of HBM; 640 bf16 rows of
 // 128256 (308 MB) 60 us, 76%: six waves of CTAs that run much in step; 10 rows 5.8 us.
@@ -39,6 +43,7 @@ constexpr int kMaxWarps = 8;
 constexpr int kMaxSegBytes = 65536;  // of a row in a CTA's shared memory
 constexpr int kCopyBytes = 16384;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRuledOut = 0x1p20f;  // times T if that is above 1: a rest further under the row's top is masked, by -inf or a type's lowest value
 
 struct Shared {
     alignas(8) uint64_t bar;
@@ -319,14 +324,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
     static_assert(kMaxChunks * (kMaxWarps - 1) <= 64, "two parts a lane");
     const float2 none = make_float2(-INFINITY, 0.0f);
     const float2 p0 = lane < cpr * nparts ? sm.part[lane] : none, p1 = lane + 32 < cpr * nparts ? sm.part[lane + 32] : none;
-    const float M = fmaxf(warp_max(fmaxf(p0.x, p1.x)), sm.list.x), M0 = M == -INFINITY ? 0.0f : M;
-    const float sr = warp_sum(p0.y * ex2_approx((p0.x - M0) * c) + p1.y * ex2_approx((p1.x - M0) * c));
-    const float listed = sm.list.y * ex2_approx((sm.list.x - M0) * c), total = sr + listed, r = sm.r;
+    const float mr = warp_max(fmaxf(p0.x, p1.x)), mr0 = mr == -INFINITY ? 0.0f : mr;  // the rest's largest (none: 0)
+    const float M = fmaxf(mr, sm.list.x), M0 = M == -INFINITY ? 0.0f : M;
+    const float sr = warp_sum(p0.y * ex2_approx((p0.x - mr0) * c) + p1.y * ex2_approx((p1.x - mr0) * c));  // relative to it
+    const float down = ex2_approx((mr - M0) * c), rest = sr * down;  // relative to M: 0 where there is none or far below
+    const float listed = sm.list.y * ex2_approx((sm.list.x - M0) * c), total = rest + listed, r = sm.r;
     int fault = lane < cpr ? sm.bad[lane] : 0;
     fault = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(fault)));
     // a NaN is in one of the sums, a maximum of +inf makes them NaN
     if (!(total > 0.0f) || !isfinite(total)) fault = max(fault, static_cast<int>(kDevNonFinite));
-    const bool nothing = sm.nothing != 0, leaves = r > 0.0f && sr > 0.0f;
+    const bool nothing = sm.nothing != 0, leaves = r > 0.0f && mr > -INFINITY && M0 - mr <= kRuledOut * fmaxf(1.0f, a.temperature);
     const float wt = w / a.temperature;
     if (rank == 0 && warp == 0) {
         // The loss is a difference of logarithms, often far smaller than they are: differences in 64 bits, of logarithms
@@ -348,7 +355,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
                 // ln r and ln q_R from the list's side where that is the smaller part
                 const float ps = sm.psum;
                 const double lnr = ps < 0.5f ? static_cast<double>(log1pf(-ps)) : ln_fine(r);
-                const double lnqr = listed < sr ? static_cast<double>(log1pf(-listed / total)) : ln_fine(sr) - lns;
+                const double lnqr = listed < rest ? static_cast<double>(log1pf(-listed / total))
+                                                  : (static_cast<double>(mr) - static_cast<double>(M0)) * inv_t + ln_fine(sr) - lns;
                 term += r * static_cast<float>(lnr - lnqr);
             }
             if (fault && !nothing) raise_status(a.status, fault);
@@ -360,9 +368,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
         for (int v = tid; v < nvec; v += threads) grad[v] = make_uint4(0u, 0u, 0u, 0u);
         return;
     }
-    // (sum p + r) / total - r / sr, with sum p + r - r total / sr = sum p - r listed / sr where the list is the smaller part
-    const float factor = wt * (!leaves ? sm.mass / total : listed < sr ? (sm.psum - r * (listed / sr)) / total : sm.mass / total - r / sr);
-    const uint64_t minus = f2_pack(-M0, -M0), f2 = f2_pack(factor, factor);
+    // Of exp((z - mr) / T): (sum p + r) down / total - r / sr, with sum p + r - r total / rest = sum p - r listed / rest
+    // where the list is the smaller part
+    const float share = down / total;
+    const float factor = wt * (!leaves ? sm.mass * share : listed < rest ? (sm.psum - r * (listed / rest)) * share : sm.mass * share - r / sr);
+    const uint64_t minus = f2_pack(-mr0, -mr0), f2 = f2_pack(factor, factor);
     if (warp > 0)
     for (int v = tid - 32; v < nvec; v += threads - 32) {
         uint64_t x[EPV / 2];
