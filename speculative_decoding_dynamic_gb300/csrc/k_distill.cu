@@ -51,7 +51,7 @@ struct Shared {
     int bad[kMaxChunks];                  // a DeviceError of each CTA, 0 = none
     float2 list;                          // (m, sum) of the listed entries
     float r, mass, psum;                  // what the list leaves; sum p + r; sum p
-    int nothing;                          // a list of padding alone that is the whole distribution
+    int nothing;                          // a list of padding alone that is the whole distribution: no fault by itself
     int id[kDistillMaxTop];               // -1: padding, or no entry of the row
     float z[kDistillMaxTop], lnp[kDistillMaxTop];
 };
@@ -232,9 +232,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
             }
             total = warp_sum(total);
             shift = logf(total);
-            if (!(total > 0.0f)) bad = max(bad, static_cast<int>(kDevNonFinite));
+            if (any && !(total > 0.0f)) bad = max(bad, static_cast<int>(kDevNonFinite));
         }
-        if (!isfinite(shift)) bad = max(bad, static_cast<int>(kDevNonFinite));
+        if ((any || !whole) && !isfinite(shift)) bad = max(bad, static_cast<int>(kDevNonFinite));
         float zsum = 0.0f, psum = 0.0f, low = 0.0f;  // (sum p and what its roundings lost: 1 - sum p is of that size)
         auto add = [&](float p) {
             const float u = psum + p, q = u - psum;
@@ -359,8 +359,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
                                                   : (static_cast<double>(mr) - static_cast<double>(M0)) * inv_t + ln_fine(sr) - lns;
                 term += r * static_cast<float>(lnr - lnqr);
             }
-            if (fault && !nothing) raise_status(a.status, fault);
-            a.loss[row] = nothing ? 0.0f : fault ? NAN : w * term;
+            if (fault) raise_status(a.status, fault);
+            a.loss[row] = fault ? NAN : nothing ? 0.0f : w * term;
         }
     }
     if (grad == nullptr) return;
