@@ -621,7 +621,8 @@ int eagle_linear_fp8_pack(int out_dim, int in_dim, const void* weight, void* cod
  * dlogits = d loss / d logits, fp32 rounded once. Multiply the weights by T^2 for
  * the usual scale at other temperatures.
  * A row with a NaN or +inf logit or no finite one, a NaN or infinite weight or
- * lse, or a list with a NaN, a +inf or no finite logit raises status 1; an id >=
+ * lse, or a list with a NaN, a +inf or no finite logit (padding alone is none of
+ * these: with teacher_lse it leaves everything to r) raises status 1; an id >=
  * V or twice in a list status 3: its loss is NaN, its gradient 0. Of `cfg` only
  * vocab and logit_dtype matter here, of `ws` the status word.
  */

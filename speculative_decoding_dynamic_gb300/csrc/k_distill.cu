@@ -218,6 +218,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
             ztop = fmaxf(ztop, z[k]);
         }
         any = __any_sync(0xffffffffu, any);
+        // a list whose logits are all -inf (or NaN) is no distribution, with an lse neither
+        if (any && !__any_sync(0xffffffffu, top > -INFINITY)) bad = max(bad, static_cast<int>(kDevNonFinite));
         ztop = warp_max(ztop);
         const float z0 = ztop == -INFINITY ? 0.0f : ztop;
         float shift = lse;
@@ -232,7 +234,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
             }
             total = warp_sum(total);
             shift = logf(total);
-            if (any && !(total > 0.0f)) bad = max(bad, static_cast<int>(kDevNonFinite));
         }
         if ((any || !whole) && !isfinite(shift)) bad = max(bad, static_cast<int>(kDevNonFinite));
         float zsum = 0.0f, psum = 0.0f, low = 0.0f;  // (sum p and what its roundings lost: 1 - sum p is of that size)

@@ -45,3 +45,25 @@ def test_padding_alone_hides_no_other_fault(E, V):
         _faulty(E, broken, ids, t, lse, None, 1)
     broken[0] = -float("inf")
     _faulty(E, broken, ids, t, lse, None, 1)
+
+
+@pytest.mark.parametrize("V", [1024, 65536])
+@pytest.mark.parametrize("rest", [True, False])
+def test_list_without_a_finite_logit(E, V, rest):
+    z, ids, t, lse = _case(np.random.default_rng(V + 2), 3, V, 40, "fp32", 1.0, rest)
+    t[0] = -np.inf
+    _faulty(E, z, ids, t, lse, None, 1)
+    ids[0, 1:] = -1  # a single entry, padding's logits finite
+    t[0, 1:] = 1.0
+    _faulty(E, z, ids, t, lse, None, 1)
+    # one finite logit is a list; padding alone with an lse leaves everything to the rest
+    t[0] = -np.inf
+    t[0, 0] = 0.0
+    if rest:
+        lse[0] = 0.5
+        ids[1] = -1
+        t[1] = -np.inf
+    loss, grad, status = _run(E, z, ids, t, lse, 1.0, None)
+    assert status == 0 and np.isfinite(loss).all() and np.isfinite(grad).all()
+    if rest:
+        assert loss[1] == 0 and not grad[1].any()
