@@ -265,9 +265,9 @@ __global__ void __launch_bounds__(E == 1 ? 1024 : 512) rmsnorm_fp8_kernel(Rmsnor
         if (a.weight) {  // uniform
             const Two sq = row_sum(E == 1 ? squares(s[0]) : squares(s[0]) + squares(s[E - 1]), wpr, red[turn & 1]);
             float rstd = rsqrt_of(sq, a.inv_dim, a.inv_dim_lo, a.eps);
-            // A row whose squares leave fp32's range has them summed at 2^-160 (eps does not count
-            // then); one that holds an infinity or NaN has no norm.
-            const bool far = !(sq.hi <= 3.0e38f);
+            // Where the squares, with an eps of their size, leave fp32's range they are summed at 2^-160 and eps is
+            // taken there (one that this rounds to 0 is nothing beside them); a row with an infinity or NaN has no norm.
+            const bool far = !(sq.hi + a.eps <= 3.0e38f);
             // (the CTA's only row: all its threads alike)
             if (rpc == 1 ? far : wpr == 1 ? __any_sync(0xffffffffu, far) != 0 : __syncthreads_or(far) != 0) {
                 constexpr float kDown = 0x1p-80f;
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(E == 1 ? 1024 : 512) rmsnorm_fp8_kernel(Rmsnor
                 const Two lsq = row_sum(part, wpr, red_far);
                 if (far) {
 #pragma unroll
-                    for (int e = 0; e < E; ++e) times(s[e], lsq.hi <= 3.0e38f ? rsqrt_of(lsq, a.inv_dim, a.inv_dim_lo, 0.0f) : NAN);  // of the row at 2^-80
+                    for (int e = 0; e < E; ++e) times(s[e], lsq.hi <= 3.0e38f ? rsqrt_of(lsq, a.inv_dim, a.inv_dim_lo, a.eps * kDown * kDown) : NAN);  // of the row at 2^-80
                     rstd = kDown;
                 }
             }
