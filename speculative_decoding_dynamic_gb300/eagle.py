@@ -376,6 +376,23 @@ def _behind(t):
     return t.as_strided((t.untyped_storage().nbytes() // t.element_size() - t.storage_offset(),), (1,))
 
 
+def _apart(fn, name, t, row_stride, dim):
+    """_behind, of rows of at least `dim` entries that lie row_stride apart."""
+    if not isinstance(t, torch.Tensor) or t.is_contiguous():
+        return t
+    inner, rows = 1, 0  # entries of a row and, past its end, rows so far
+    for size, stride in zip(reversed(t.shape), reversed(t.stride())):
+        if size == 1:
+            continue
+        if inner >= dim and stride == row_stride * max(rows, 1):
+            rows = max(rows, 1) * size
+        elif rows == 0 and stride == inner:
+            inner *= size
+        else:
+            raise ValueError(f"{fn}: {name}'s strides {tuple(t.stride())} are not those of rows of {dim} with row_stride {row_stride}")
+    return _behind(t)
+
+
 def eagle_kvq_store(kv, layer, T, k, v, row_stride, row_start, start, count, codes, scales, ws=None, stream=None):
     fn, dev, B = "eagle_kvq_store", _device(), kv.batch
     # dense rows: the last one reaches its heads' end (packed rows: the caller's row_start says how far)
@@ -488,7 +505,8 @@ def eagle_rmsnorm_fp8(rows, dim, dtype, x, row_stride, residual, sum, weight, ep
     fn, dev, dt = "eagle_rmsnorm_fp8", _device(), _dtypes(dtype)
     n = (rows - 1) * row_stride + dim
     if row_stride != dim:  # rows inside wider ones
-        x, residual, sum = _behind(x), _behind(residual), _behind(sum)
+        x, residual, sum = (_apart(fn, name, t, row_stride, dim)
+                            for name, t in (("x", x), ("residual", residual), ("sum", sum)))
     _check(fn, _lib.eagle_rmsnorm_fp8(rows, dim, dtype, _need(fn, "x", x, dt, n, dev), row_stride,
                                       _need(fn, "residual", residual, dt, n, dev),
                                       _need(fn, "sum", sum, dt, n, dev), _need(fn, "weight", weight, dt, dim, dev),
