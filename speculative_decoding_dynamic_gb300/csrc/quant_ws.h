@@ -47,7 +47,7 @@ cudaError_t launch_token_logprobs(const LogprobArgs& a, int dtype, cudaStream_t 
 // Rows of e4m3 codes with a power-of-two scale (a byte, E8M0) for each 128 entries.
 constexpr int kFp8Block = 128;
 constexpr int kFp8MaxNormDim = 16384;  // a row's entries in the registers of 1024 threads
-inline int fp8_scale_stride(int dim) { return (dim + 4 * kFp8Block - 1) / (4 * kFp8Block) * 4; }
+inline int fp8_scale_stride(int dim) { return ((dim - 1) / (4 * kFp8Block) + 1) * 4; }  // dim >= 1, up to the largest int
 struct RmsnormFp8Args {
     int rows, dim, scale_stride;
     int64_t row_stride;  // elements

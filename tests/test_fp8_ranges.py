@@ -12,6 +12,12 @@ def E():
     return eagle
 
 
+def test_scale_stride_of_the_largest_dims(E):
+    for dim in (2 ** 31 - 1, 2 ** 31 - 511, 2 ** 31 - 512, 2 ** 31 - 513, 1 << 30):
+        assert E.eagle_fp8_scale_stride(dim) == (dim + 511) // 512 * 4
+    assert E.eagle_fp8_scale_stride(-2 ** 31) == 0
+
+
 def test_rows_that_lie_otherwise_than_the_call_says(E):
     """Rows inside wider ones: a tensor's own distance from row to row is the call's row_stride."""
     wide = torch.zeros(8, 1024, dtype=torch.bfloat16)
