@@ -831,13 +831,16 @@ bool make_map_codes(CUtensorMap* m, const void* base, int inner, int outer, int 
                     static_cast<uint64_t>(inner), kStageK, static_cast<uint32_t>(box_outer), CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// SMs of the current device, asked once for each (calls of several threads may meet here).
 int sm_count() {
-    static int n = 0;
+    static std::atomic<int> known[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    std::atomic<int>& slot = known[dev % kMaxDevices];
+    int n = slot.load(std::memory_order_relaxed);
     if (n == 0) {
-        int dev = 0;
-        cudaGetDevice(&dev);
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (n <= 0) n = 1;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 1;
+        slot.store(n, std::memory_order_relaxed);
     }
     return n;
 }
