@@ -561,7 +561,7 @@ int eagle_fp8_scale_stride(int dim);
  * in y (each block of a row whose s has one, with a norm) gets NaN codes, scale
  * 1 and raises status 1.
  *   ws          any eagle workspace whose status word receives device faults, or NULL.
- * dim a multiple of 16 up to 16384; pointers but scales' 16-byte aligned.
+ * dim a multiple of 16 up to 16384; rows up to 2^24; row_stride below 2^32; pointers but scales' 16-byte aligned.
  */
 int eagle_rmsnorm_fp8(int rows, int dim, int dtype, const void* x, int64_t row_stride, const void* residual, void* sum,
                       const void* weight, float eps, void* codes, uint8_t* scales, void* ws, void* stream);
@@ -580,15 +580,16 @@ int eagle_rmsnorm_fp8(int rows, int dim, int dtype, const void* x, int64_t row_s
  *   ws        any eagle workspace whose status word receives device faults (2: a
  *             wait gave up), or NULL.
  * in_dim a multiple of 16; code pointers and out 16-byte aligned, scales 4-byte
- * aligned; out overlaps no operand. Any number of rows: one or two of a small
- * weight take a path without the tensor cores, many the one whose rate is twice
- * that of 16-bit operands.
+ * aligned; out overlaps no operand. rows and in_dim up to 2^20, out_dim up to
+ * 2^24: one row or two of a small weight take a path without the tensor cores,
+ * many rows the one whose rate is twice that of 16-bit operands.
  */
 int eagle_linear_fp8(int rows, int out_dim, int in_dim, const void* x_codes, const uint8_t* x_scales,
                      const void* w_codes, const uint8_t* w_scales, int out_dtype, void* out, void* ws, void* stream);
 
-/* The 8-bit form of a bf16 weight [out_dim, in_dim], in_dim a multiple of 16: scales and codes of
- * eagle_rmsnorm_fp8's rule over blocks of 128 x 128 (a block with a NaN or infinity: NaN codes, scale 1). */
+/* The 8-bit form of a bf16 weight [out_dim, in_dim]: scales and codes of eagle_rmsnorm_fp8's rule over
+ * blocks of 128 x 128 (a block with a NaN or infinity: NaN codes, scale 1). in_dim a multiple of 16 up to
+ * 2^20, out_dim up to 65535 * 128, weight and codes 16-byte aligned. */
 int eagle_linear_fp8_pack(int out_dim, int in_dim, const void* weight, void* codes, uint8_t* scales, void* stream);
 
 /* ------------------------------------------------- training the draft --- */
@@ -617,14 +618,20 @@ int eagle_linear_fp8_pack(int out_dim, int in_dim, const void* weight, void* cod
  * r = max(0, 1 - sum p) what the list leaves and q_R the draft's probability of
  * everything else, however small (the r term only with teacher_lse and r above 0,
  * and not where everything else is ruled out: its largest logit -inf, or more than
- * 2^20 max(1, T) under the row's largest, as a mask of the type's lowest value is);
- * dlogits = d loss / d logits, fp32 rounded once. Multiply the weights by T^2 for
- * the usual scale at other temperatures.
+ * 2^20 max(1, T) under the row's largest, as a mask of the type's lowest value is).
+ * dlogits is its gradient, fp32 rounded once,
+ *   weight / T ((sum p + r) q_j - p_j)            of a listed id j,
+ *   weight / T ((sum p + r) q_j - r q_j / q_R)    elsewhere, 0 where that is ruled
+ * out. (There the listed ids' part is the limit of small q_R and pulls them down by
+ * the r that nothing else can take up; for a draft that has the list alone pass
+ * teacher_lse NULL.) A listed id with p above 0 whose logit is -inf makes the loss
+ * infinite. Multiply the weights by T^2 for the usual scale at other temperatures.
  * A row with a NaN or +inf logit or no finite one, a NaN or infinite weight or
  * lse, or a list with a NaN, a +inf or no finite logit (padding alone is none of
  * these: with teacher_lse it leaves everything to r) raises status 1; an id >=
- * V or twice in a list status 3: its loss is NaN, its gradient 0. Of `cfg` only
- * vocab and logit_dtype matter here, of `ws` the status word.
+ * V or twice in a list status 3: its loss is NaN, its gradient 0. rows up to 2^24;
+ * logits and dlogits 16-byte aligned. Of `cfg` only vocab and logit_dtype matter
+ * here, of `ws` the status word.
  */
 int eagle_distill_loss(const eagle_tree_cfg* cfg, void* ws, size_t ws_bytes, int rows, int n_top, const void* logits,
                        const int32_t* teacher_ids, const float* teacher_logits, const float* teacher_lse,
