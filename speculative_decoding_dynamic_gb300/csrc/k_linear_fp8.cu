@@ -31,15 +31,16 @@
 // distributed shared memory, added in the CTAs' order.
 //
 // What bounds it. Few rows: HBM and some 4 us that a launch costs (10 rows
-// against 128256 x 4096: 82 us, 95% of HBM). Many: the weight comes from L2 once
+// against 128256 x 4096: 82 to 84 us, 93 to 95% of HBM; 64 rows against 4096 x 4096
+// 7.9 us). Many: the weight comes from L2 once
 // for each row chunk of a tile, and L2 gives 7.2 TB/s of lines that no two SMs ask
 // for together, hence the two accumulators (with one, 225 us for the next case);
-// then the card's power: 640 rows against 128256 x 4096 206 us at the start of a
-// series (3.3 PFLOP/s at 1.7 GHz), 237 us in a long one (1.5 GHz), 177 us on zeros
-// (1.95 GHz; 164 us without loads and stores); 4001 rows against 14336 x 4096 132
-// us, 151 in a long series, 117 on zeros (4.0 PFLOP/s). Sharing x's boxes over a
-// cluster of two pairs (TMA multicast) was slower: 144 SMs, and four CTAs in step
-// (263 us on zeros).
+// then the card's power: 640 rows against 128256 x 4096 205 to 213 us at the start
+// of a series (3.2 PFLOP/s at 1.7 GHz), 239 to 246 in a long one (1.5 GHz), 177 us on
+// zeros (1.95 GHz; 164 us without loads and stores); 4001 rows against 14336 x 4096
+// 131 to 134 us, 151 to 154 in a long series, 117 on zeros (4.0 PFLOP/s). Copies of
+// x's boxes shared by a cluster of two pairs were slower: 144 SMs, and four CTAs in
+// step (263 us on zeros).
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -988,9 +989,11 @@ cudaError_t launch_dtype(int M, int N, int K, const void* x, const uint8_t* x_sc
 
 cudaError_t launch_linear_fp8(int M, int N, int K, const void* x, const uint8_t* x_scales, const void* w,
                               const uint8_t* w_scales, int out_dtype, void* out, int* status, cudaStream_t stream) {
-    // One row or two of a small weight: without the tensor cores' fixed cost (us, rows kernel / this one: 1 row 512 x
-    // 2048 2.3 / 4.0, 4096 x 4096 4.7 / 5.9, 6144 x 4096 6.4 / 7.5, 8192 x 4096 8.9 / 7.9, 12288 x 4096 12.9 / 12.7;
-    // 2 rows 2048 x 4096 3.8 / 5.4, 4096 x 4096 5.9 / 5.9, 6144 x 4096 7.7 / 7.5, 8192 x 3584 11.7 / 7.6)
+    // One row or two of a small weight: without the tensor cores' fixed cost. us, rows kernel / this one, on weights
+    // that lie in L2: 1 row 512 x 2048 2.3 / 4.0, 4096 x 4096 4.7 / 5.9, 6144 x 4096 6.4 / 7.5, 8192 x 4096 8.9 / 7.9;
+    // 2 rows 2048 x 4096 3.8 / 5.4, 4096 x 4096 5.9 / 5.9, 6144 x 4096 7.7 / 7.5, 8192 x 3584 11.7 / 7.6; on weights
+    // that come from HBM: 1 row 2.1 / 4.1, 6.2 / 6.8, 8.3 / 8.2, 10.2 / 9.0; 2 rows 4.7 / 5.6, 7.3 / 6.9, 9.6 / 8.3,
+    // 12.5 / 8.8.
     const int64_t weight = static_cast<int64_t>(N) * K;
     if ((M == 1 && weight <= 28 << 20) || (M == 2 && weight <= 17 << 20))
         return launch_linear_fp8_rows(M, N, K, x, x_scales, w, w_scales, out_dtype, out, stream);

@@ -16,8 +16,10 @@
 // Bound by HBM, nearly so by instructions (a thread spends 370 to 480 on its part
 // of a row). CTAs stay for several rows, so that the weight comes from L1, and
 // load the next rows before they reduce one where registers allow it. Measured:
-// 3904 bf16 rows of 5120 with a residual (140 MB) 25 us, 84% of HBM; 8001 fp32
-// rows of 8192 without (328 MB) 55 us, 88%; 10 rows of 4096 2.1 us.
+// 3904 bf16 rows of 5120 with a residual (140 MB) 25 us, 82% of HBM; 8001 fp32
+// rows of 8192 without (328 MB) 55 us, 88%, with one (853 MB) 136 us, 92%; 8001
+// bf16 rows of 8192 without (197 MB) 48 us, 60%, the instructions' time; 640 rows of
+// 4096 5.2 us, 10 rows 2.1.
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
