@@ -626,12 +626,12 @@ int eagle_linear_fp8_pack(int out_dim, int in_dim, const void* weight, void* cod
  * the r that nothing else can take up; for a draft that has the list alone pass
  * teacher_lse NULL.) A listed id with p above 0 whose logit is -inf makes the loss
  * infinite. Multiply the weights by T^2 for the usual scale at other temperatures.
- * A row with a NaN or +inf logit or no finite one, a NaN or infinite weight or
- * lse, or a list with a NaN, a +inf or no finite logit (padding alone is none of
- * these: with teacher_lse it leaves everything to r) raises status 1; an id >=
- * V or twice in a list status 3: its loss is NaN, its gradient 0. rows up to 2^24;
- * logits and dlogits 16-byte aligned. Of `cfg` only vocab and logit_dtype matter
- * here, of `ws` the status word.
+ * A row with a NaN or +inf logit or no finite one, a NaN or infinite weight (with
+ * dlogits: weight / T) or lse, or a list with a NaN, a +inf or no finite logit
+ * (padding alone is none of these: with teacher_lse it leaves everything to r)
+ * raises status 1; an id >= V or twice in a list status 3: its loss is NaN, its
+ * gradient 0. rows up to 2^24; logits and dlogits 16-byte aligned. Of `cfg` only
+ * vocab and logit_dtype matter here, of `ws` the status word.
  */
 int eagle_distill_loss(const eagle_tree_cfg* cfg, void* ws, size_t ws_bytes, int rows, int n_top, const void* logits,
                        const int32_t* teacher_ids, const float* teacher_logits, const float* teacher_lse,

@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 3) distill_kernel(DistillArgs 
     if (warp == 0) {
         // ---- the list's entries leave the row ----
         __syncwarp();
-        bad = isfinite(w) ? 0 : kDevNonFinite;
+        bad = isfinite(grad ? w / a.temperature : w) ? 0 : kDevNonFinite;  // (the gradient's factor)
 #pragma unroll
         for (int k = 0; k < kSlots; ++k) {
             z[k] = -INFINITY;

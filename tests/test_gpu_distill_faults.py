@@ -67,3 +67,21 @@ def test_list_without_a_finite_logit(E, V, rest):
     assert status == 0 and np.isfinite(loss).all() and np.isfinite(grad).all()
     if rest:
         assert loss[1] == 0 and not grad[1].any()
+
+
+@pytest.mark.parametrize("V", [1024, 65536])
+@pytest.mark.parametrize("rest", [True, False])
+def test_weight_over_temperature_past_fp32(E, V, rest):
+    """A finite weight that divided by T is infinite has no gradient in 32 bits: refused where one is asked for."""
+    T = 2.0 ** -126
+    z, ids, t, _ = _case(np.random.default_rng(V + 3), 3, V, 4, "fp32", 1.0, rest)
+    t = np.zeros_like(t)
+    lse = np.full(3, 1.5, np.float32) if rest else None
+    w = np.array([8.0, 1.0, -0.5], np.float32)
+    loss, grad, status = _run(E, z, ids, t, lse, T, w)
+    assert status == 1
+    assert np.isnan(loss[0]) and not grad[0].any()
+    assert not np.isnan(loss[1:]).any() and np.isfinite(grad).all()
+    assert np.all(np.abs(grad[1:]).max(1) <= 2.0 ** 126 * np.abs(w[1:]) * 1.01) and np.all(grad[1:].any(1))
+    alone, _, status = _run(E, z, ids, t, lse, T, w, grad=False)
+    assert status == 0 and not np.isnan(alone).any() and np.array_equal(alone[1:], loss[1:])
